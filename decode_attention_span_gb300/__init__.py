@@ -27,4 +27,14 @@ from .sekv import (  # noqa: F401
     record_size,
     last_launch_count,
     default_scale,
+    SEKV_CALL_KV4,
 )
+from .kv4 import (  # noqa: F401
+    Kv4Cache,
+    alloc_kv4_pages,
+    kv4_append,
+    kv4_attention,
+    kv4_read,
+)
+from .logprobs import TokenLogprobs, surprisal, token_logprobs  # noqa: F401
+from .rotary import RopePlan, rope  # noqa: F401

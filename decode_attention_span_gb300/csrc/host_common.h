@@ -26,5 +26,6 @@ bool encode_rows4d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
                    uint32_t box_rows);
 
 size_t build_workspace_size(const sekv_config* cfg, int64_t ctx_len);
+size_t kv4_workspace_size(const sekv_config* cfg, int64_t n_q);
 
 }  // namespace sekv

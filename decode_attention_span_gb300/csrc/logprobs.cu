@@ -1,0 +1,509 @@
+// sekv_token_logprobs and sekv_surprisal: log-probabilities of given tokens,
+// entropies and the likeliest alternatives, in one pass over the logits.
+//
+// Bound by memory: rows * vocab elements are read once.  A row is cut into
+// 16-byte vectors; a cluster of 1 to 16 CTAs takes one row (as many as it takes
+// to fill the GPU when there are few rows), and each thread keeps a running
+// maximum m, S = sum e^(x-m) and A = sum e^(x-m) (x-m) of its own vectors, joined
+// over the CTA by shuffles and over the cluster through distributed shared
+// memory.  entropy = ln S - A/S has no cancellation (both terms are >= 0).
+//
+// The alternatives need no second pass over the row.  Each thread remembers
+// the group of vectors its maximum came from, and after the pass looks up the
+// maximum's exact key (value, lowest index first) in that group.  The n-th
+// largest of the threads' keys is a bound below which no alternative lies, and
+// exactly n threads have keys at or above it; only those threads' vectors are
+// read again, one warp per thread.  What reaches the bound is sorted.
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "decode_host.h"
+#include "host_common.h"
+
+namespace cg = cooperative_groups;
+using namespace sekv;
+
+namespace {
+
+constexpr int kLpThreads = 512;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpUnroll = 4;      // vectors of a thread in flight
+constexpr int kLpMaxCluster = 16;
+
+struct LpParams {
+  const void* logits;
+  const void* tokens;
+  float *logprob, *lse, *entropy, *top_lp;
+  int32_t* top_ids;
+  int32_t* status;
+  int64_t stride_b, stride_t, token_stride_b;
+  int64_t out_stride_b;    // rows of a sequence in the outputs
+  int64_t n_tokens;        // rows of a sequence that are computed
+  int64_t vocab;
+  float scale;
+  int tokens64, n_top, negate;  // negate: surprisal (and its H[b][0] = 0)
+};
+
+struct Stat {
+  float m, s, a;  // maximum; sums in units of e^(scale (x - m)); a in log2 units
+};
+
+// exponent scale (x - m) in log2 units, finite differences first: with x and m
+// at the type's lowest value the product would overflow, the difference is 0
+__device__ __forceinline__ float exp_arg(float x, float m, float c) {
+  return (x - (m == -INFINITY ? 0.f : m)) * c;
+}
+
+__device__ __forceinline__ Stat join(const Stat& p, const Stat& q, float c) {
+  Stat r;
+  r.m = fmaxf(p.m, q.m);
+  const float dp = fmaxf(exp_arg(p.m, r.m, c), -1e30f), dq = fmaxf(exp_arg(q.m, r.m, c), -1e30f);
+  const float fp = exp2f(dp), fq = exp2f(dq);
+  // a term without weight has no share (0 * finite), whatever its distance
+  r.s = p.s * fp + q.s * fq;
+  r.a = fp * (p.a + p.s * dp) + fq * (q.a + q.s * dq);
+  return r;
+}
+
+__device__ __forceinline__ Stat shfl_xor(const Stat& v, int o) {
+  Stat r;
+  r.m = __shfl_xor_sync(~0u, v.m, o);
+  r.s = __shfl_xor_sync(~0u, v.s, o);
+  r.a = __shfl_xor_sync(~0u, v.a, o);
+  return r;
+}
+
+// Order-preserving key of (value, index): larger value first, then the lower
+// index; -0 counts as 0.  Every key is above 0.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  const uint32_t o = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  return (uint64_t(o) << 32) | uint32_t(~index);
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t o = uint32_t(k >> 32);
+  return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint32_t key_index(uint64_t k) { return ~uint32_t(k); }
+
+__device__ __forceinline__ uint64_t cmp_swap(uint64_t k, int mask, bool keep_max) {
+  const uint64_t o = __shfl_xor_sync(~0u, k, mask);
+  return keep_max ? (k > o ? k : o) : (k < o ? k : o);
+}
+
+// Lane i of the warp gets the i-th largest of its 32 keys.
+__device__ __forceinline__ uint64_t warp_sort(uint64_t k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int m = size >> 1; m > 0; m >>= 1)
+      k = cmp_swap(k, m, ((lane & size) == 0) == ((lane & m) == 0));
+  return k;
+}
+
+// The 32 largest of two descending lists of 32 (q: lane i holds the other
+// list's entry 31 - i): the larger of each pair is a bitonic sequence.
+__device__ __forceinline__ uint64_t warp_merge(uint64_t p, uint64_t q, int lane) {
+  uint64_t k = p > q ? p : q;
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) k = cmp_swap(k, m, (lane & m) == 0);
+  return k;
+}
+
+struct LpShared {
+  Stat stat[kLpWarps];
+  Stat cta[kLpMaxCluster];             // rank 0: the cluster's parts
+  uint64_t lists[kLpWarps][32];
+  uint64_t tops[kLpMaxCluster * 32];   // rank 0: the cluster's lists
+  uint64_t cand[kLpThreads];
+  uint64_t sorted[32];
+  int n_cand;
+};
+
+// The 32 largest of one key per thread, descending, in sh.sorted.
+__device__ __forceinline__ void block_top32(LpShared& sh, uint64_t key) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t k = warp_sort(key, lane);
+  sh.lists[warp][lane] = k;
+  __syncthreads();
+#pragma unroll
+  for (int w = kLpWarps / 2; w > 0; w >>= 1) {
+    if (warp < w) {
+      k = warp_merge(k, sh.lists[warp + w][31 - lane], lane);
+      sh.lists[warp][lane] = k;
+    }
+    __syncthreads();
+  }
+  if (warp == 0) sh.sorted[lane] = k;
+  __syncthreads();
+}
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f(float v) { return v; }
+
+// A row as 16-byte vectors: vector i holds elements i*VE - off .. + VE - 1; the
+// first and the last may be partial (elements outside the row read as -inf).
+template <typename T>
+struct Row {
+  static constexpr int VE = 16 / int(sizeof(T));
+  const T* base;   // 16-byte aligned; element 0 of the row is base[off]
+  int off;
+  int64_t vocab;
+  __device__ __forceinline__ void load(int64_t i, uint4& w) const {
+    const int64_t e0 = i * VE - off;
+    if (e0 >= 0 && e0 + VE <= vocab) {
+      w = __ldcs(reinterpret_cast<const uint4*>(base) + i);
+    } else {
+      T* e = reinterpret_cast<T*>(&w);
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        e[j] = e0 + j >= 0 && e0 + j < vocab ? base[i * VE + j] : T(-INFINITY);
+    }
+  }
+  __device__ __forceinline__ void unpack(const uint4& w, float (&x)[VE]) const {
+    const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int j = 0; j < VE; ++j) x[j] = to_f(e[j]);
+  }
+};
+
+template <typename T, bool FULL>  // FULL: entropy and alternatives may be asked for
+__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
+  constexpr int VE = Row<T>::VE;
+  __shared__ LpShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nc = cluster.num_blocks(), rank = cluster.block_rank();
+  cluster.barrier_arrive();  // waited for before the first remote store: every CTA has started
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t r = blockIdx.x / nc;
+  const int64_t b = r / P.n_tokens, t = r - b * P.n_tokens;
+  const T* first = static_cast<const T*>(P.logits) + b * P.stride_b + t * P.stride_t;
+  Row<T> row;
+  row.off = int((reinterpret_cast<uintptr_t>(first) & 15) / sizeof(T));
+  row.base = first - row.off;
+  row.vocab = P.vocab;
+  const int64_t nv = (row.off + P.vocab + VE - 1) / VE;
+  const int64_t lo = nv * rank / nc, hi = nv * (rank + 1) / nc;
+  const float c = P.scale * kLog2e;
+
+  int64_t tok = -1;
+  float tok_x = 0.f;
+  if (rank == 0 && tid == 0) {
+    const int64_t ti = b * P.token_stride_b + t;
+    tok = P.tokens64 ? static_cast<const int64_t*>(P.tokens)[ti]
+                     : int64_t(static_cast<const int32_t*>(P.tokens)[ti]);
+    if (tok >= 0 && tok < P.vocab) tok_x = to_f(first[tok]);
+  }
+
+  // one pass: m, s, a of this thread's vectors lo + tid + kLpThreads * i
+  Stat st{-INFINITY, 0.f, 0.f};
+  int best_group = 0;
+  int g = 0;
+  for (int64_t i0 = lo + tid; i0 < hi; i0 += int64_t(kLpThreads) * kLpUnroll, ++g) {
+    uint4 w[kLpUnroll];
+#pragma unroll
+    for (int u = 0; u < kLpUnroll; ++u) {
+      const int64_t i = i0 + int64_t(u) * kLpThreads;
+      if (i < hi) row.load(i, w[u]);
+    }
+    float gm = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kLpUnroll; ++u) {
+      if (i0 + int64_t(u) * kLpThreads < hi) {
+        float x[VE];
+        row.unpack(w[u], x);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) gm = fmaxf(gm, x[j]);
+      }
+    }
+    if (gm > st.m) {
+      const float d = fmaxf(exp_arg(st.m, gm, c), -1e30f), f = exp2f(d);
+      if (FULL) st.a = f * (st.a + st.s * d);
+      st.s *= f;
+      st.m = gm;
+      best_group = g;
+    }
+    const float m0 = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+    for (int u = 0; u < kLpUnroll; ++u) {
+      if (i0 + int64_t(u) * kLpThreads < hi) {
+        float x[VE];
+        row.unpack(w[u], x);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float d = (x[j] - m0) * c;
+          const float e = exp2f(d);
+          st.s += e;
+          if (FULL) st.a = fmaf(e, fmaxf(d, -1e30f), st.a);
+        }
+      }
+    }
+  }
+  const float thread_max = st.m;
+
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) st = join(st, shfl_xor(st, o), c);
+  if (lane == 0) sh.stat[warp] = st;
+  if (tid == 0) sh.n_cand = 0;
+  __syncthreads();
+  cluster.barrier_wait();
+  if (warp == 0) {
+    st = lane < kLpWarps ? sh.stat[lane] : Stat{-INFINITY, 0.f, 0.f};
+#pragma unroll
+    for (int o = kLpWarps / 2; o > 0; o >>= 1) st = join(st, shfl_xor(st, o), c);
+    if (lane == 0) cluster.map_shared_rank(&sh, 0)->cta[rank] = st;
+  }
+
+  if (FULL && P.n_top > 0) {
+    // this thread's largest key: the first place of its maximum in its group
+    uint64_t key = 0;
+    if (thread_max > -INFINITY) {
+      for (int u = kLpUnroll - 1; u >= 0; --u) {
+        const int64_t i = lo + tid + (int64_t(best_group) * kLpUnroll + u) * kLpThreads;
+        if (i < hi) {
+          uint4 w;
+          float x[VE];
+          row.load(i, w);
+          row.unpack(w, x);
+#pragma unroll
+          for (int j = VE - 1; j >= 0; --j)
+            if (x[j] == thread_max) key = key_of(x[j], uint32_t(i * VE + j - row.off));
+        }
+      }
+    }
+    block_top32(sh, key);
+    const uint64_t bound = max(sh.sorted[P.n_top - 1], uint64_t(1));
+    uint64_t owner_key = lane < P.n_top ? sh.sorted[lane] : 0;
+    // the threads at or above the bound: warp w takes every kLpWarps-th of them
+    for (int k = warp; k < P.n_top; k += kLpWarps) {
+      const uint64_t ok = __shfl_sync(~0u, owner_key, k);
+      if (ok == 0) break;
+      const int64_t vec = (int64_t(key_index(ok)) + row.off) / VE;
+      const int owner = int((vec - lo) % kLpThreads);
+      for (int64_t i = lo + owner + int64_t(lane) * kLpThreads; i < hi; i += 32 * kLpThreads) {
+        uint4 w;
+        float x[VE];
+        row.load(i, w);
+        row.unpack(w, x);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const uint64_t kk = key_of(x[j], uint32_t(i * VE + j - row.off));
+          if (x[j] > -INFINITY && kk >= bound) {
+            const int at = atomicAdd(&sh.n_cand, 1);
+            if (at < kLpThreads) sh.cand[at] = kk;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const int n = sh.n_cand;
+    if (n <= kLpThreads) {
+      block_top32(sh, tid < n ? sh.cand[tid] : 0);
+    } else {
+      // more candidates than places (the largest logits of a row all in a few
+      // threads' vectors): one alternative per round, the largest key below the last
+      uint64_t last = ~uint64_t(0);
+      for (int k = 0; k < P.n_top; ++k) {
+        uint64_t best = 0;
+        for (int64_t i = lo + tid; i < hi; i += kLpThreads) {
+          uint4 w;
+          float x[VE];
+          row.load(i, w);
+          row.unpack(w, x);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const uint64_t kk = key_of(x[j], uint32_t(i * VE + j - row.off));
+            if (x[j] > -INFINITY && kk < last && kk > best) best = kk;
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t other = __shfl_xor_sync(~0u, best, o);
+          best = best > other ? best : other;
+        }
+        if (lane == 0) sh.lists[warp][0] = best;
+        __syncthreads();
+        for (int w = 0; w < kLpWarps; ++w) best = max(best, sh.lists[w][0]);
+        last = best;
+        if (tid == 0) sh.sorted[k] = best;
+        __syncthreads();
+        if (best == 0) {
+          if (tid > k && tid < 32) sh.sorted[tid] = 0;
+          break;
+        }
+      }
+      __syncthreads();
+    }
+    if (tid < 32) cluster.map_shared_rank(&sh, 0)->tops[rank * 32 + tid] = tid < P.n_top ? sh.sorted[tid] : 0;
+  }
+  cluster.sync();  // the parts of every CTA are in rank 0's shared memory
+  if (rank != 0) return;
+
+  Stat all = sh.cta[0];
+  for (int k = 1; k < nc; ++k) all = join(all, sh.cta[k], c);
+  const bool bad = isnan(all.s) || all.m == INFINITY;
+  const float ln_s = logf(all.s);
+  const float top = all.m == -INFINITY ? all.m : P.scale * all.m;
+  const int64_t o = b * P.out_stride_b + t;
+  if (tid == 0) {
+    float lp;
+    if (tok == -1) {
+      lp = bad ? NAN : 0.f;
+    } else if (tok < 0 || tok >= P.vocab) {
+      lp = NAN;
+      set_device_error(P.status, DEV_BAD_LIST, int32_t(r > INT32_MAX ? INT32_MAX : r));
+    } else if (bad) {
+      lp = NAN;
+    } else if (tok_x == -INFINITY) {
+      lp = -INFINITY;
+    } else {
+      lp = (tok_x - all.m) * P.scale - ln_s;
+    }
+    P.logprob[o] = P.negate && !isnan(lp) ? 0.f - lp : lp;
+    if (P.negate && t == 0) P.logprob[o - 1] = 0.f;
+    if (FULL && P.lse) P.lse[o] = bad ? NAN : all.s > 0.f ? top + ln_s : -INFINITY;
+    if (FULL && P.entropy)
+      P.entropy[o] = bad ? NAN : all.s > 0.f ? ln_s - all.a / all.s * kLn2 : 0.f;
+  }
+  if (FULL && P.n_top > 0) {
+    if (nc > 1) block_top32(sh, tid < nc * 32 ? sh.tops[tid] : 0);
+    if (tid < P.n_top) {
+      const uint64_t k = sh.sorted[tid];
+      const bool none = k == 0 || bad;
+      P.top_ids[o * P.n_top + tid] = none ? -1 : int32_t(key_index(k));
+      P.top_lp[o * P.n_top + tid] =
+          bad ? NAN : k == 0 ? -INFINITY : (key_value(k) - all.m) * P.scale - ln_s;
+    }
+  }
+}
+
+template <typename T, bool FULL>
+sekv_status launch_logprobs(const LpParams& P, int64_t rows, int nc, cudaStream_t stream) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(unsigned(rows * nc));
+  lc.blockDim = dim3(kLpThreads);
+  lc.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = nc;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, logprob_kernel<T, FULL>, P) != cudaSuccess) {
+    cudaGetLastError();
+    return SEKV_ERR_CUDA;
+  }
+  count_launch(1);
+  return SEKV_OK;
+}
+
+sekv_status logprobs_impl(LpParams& P, int32_t dtype, int64_t batch, bool full,
+                          cudaStream_t stream) {
+  const int64_t rows = batch * P.n_tokens;
+  const int sms = device_sm_count();
+  if (sms <= 0) return SEKV_ERR_CUDA;
+  // CTAs per row: doubled while the rows alone leave SMs without a CTA and a
+  // CTA's share is more than one vector per thread
+  const int64_t vecs = P.vocab * (dtype == SEKV_F32 ? 4 : 2) / 16 + 1;
+  int nc = 1;
+  while (nc < 8 && rows * nc < 2 * sms && vecs > int64_t(nc) * kLpThreads) nc *= 2;
+  if (rows * nc > INT32_MAX) return SEKV_ERR_UNSUPPORTED;
+  if (dtype == SEKV_F32)
+    return full ? launch_logprobs<float, true>(P, rows, nc, stream)
+                : launch_logprobs<float, false>(P, rows, nc, stream);
+  if (dtype == SEKV_F16)
+    return full ? launch_logprobs<__half, true>(P, rows, nc, stream)
+                : launch_logprobs<__half, false>(P, rows, nc, stream);
+  return full ? launch_logprobs<__nv_bfloat16, true>(P, rows, nc, stream)
+              : launch_logprobs<__nv_bfloat16, false>(P, rows, nc, stream);
+}
+
+sekv_status check_logits(const void* logits, int32_t dtype, int64_t batch, int64_t n_tokens,
+                         int64_t vocab, const void* tokens, int32_t tokens_64, void* workspace,
+                         size_t workspace_bytes) {
+  if (dtype < SEKV_BF16 || dtype > SEKV_F32 || batch < 0 || n_tokens < 0 || vocab < 1 || !logits ||
+      !tokens || !workspace)
+    return SEKV_ERR_INVALID;
+  const int elem = dtype == SEKV_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % elem ||
+      reinterpret_cast<uintptr_t>(tokens) % (tokens_64 ? 8 : 4) ||
+      reinterpret_cast<uintptr_t>(workspace) % 4)
+    return SEKV_ERR_INVALID;
+  if (workspace_bytes < 64) return SEKV_ERR_CAPACITY;
+  if (vocab > (int64_t(1) << 30) || batch > INT32_MAX || n_tokens > INT32_MAX ||
+      batch * n_tokens > INT32_MAX)
+    return SEKV_ERR_UNSUPPORTED;
+  return SEKV_OK;
+}
+
+}  // namespace
+
+extern "C" sekv_status sekv_token_logprobs(const void* logits, int32_t dtype, int64_t batch,
+                                           int64_t n_tokens, int64_t vocab, int64_t stride_b,
+                                           int64_t stride_t, const void* tokens,
+                                           int32_t tokens_64, int64_t token_stride_b, float scale,
+                                           int32_t n_top, float* logprob, float* lse,
+                                           float* entropy, int32_t* top_ids, float* top_logprobs,
+                                           void* workspace, size_t workspace_bytes,
+                                           cudaStream_t stream) {
+  reset_launches();
+  const sekv_status st = check_logits(logits, dtype, batch, n_tokens, vocab, tokens, tokens_64,
+                                      workspace, workspace_bytes);
+  if (st != SEKV_OK) return st;
+  if (!(scale > 0.f) || !isfinite(scale) || n_top < 0 || !logprob ||
+      (n_top > 0) != (top_ids != nullptr) || (n_top > 0) != (top_logprobs != nullptr))
+    return SEKV_ERR_INVALID;
+  if (n_top > SEKV_MAX_TOP) return SEKV_ERR_UNSUPPORTED;
+  if (batch == 0 || n_tokens == 0) return SEKV_OK;
+  LpParams P{};
+  P.logits = logits;
+  P.tokens = tokens;
+  P.logprob = logprob;
+  P.lse = lse;
+  P.entropy = entropy;
+  P.top_ids = top_ids;
+  P.top_lp = top_logprobs;
+  P.status = static_cast<int32_t*>(workspace);
+  P.stride_b = stride_b;
+  P.stride_t = stride_t;
+  P.token_stride_b = token_stride_b;
+  P.out_stride_b = P.n_tokens = n_tokens;
+  P.vocab = vocab;
+  P.scale = scale;
+  P.tokens64 = tokens_64 != 0;
+  P.n_top = n_top;
+  return logprobs_impl(P, dtype, batch, lse || entropy || n_top > 0, stream);
+}
+
+extern "C" sekv_status sekv_surprisal(const void* logits, int32_t dtype, int64_t batch,
+                                      int64_t ctx_len, int64_t vocab, int64_t stride_b,
+                                      int64_t stride_t, const void* tokens, int32_t tokens_64,
+                                      int64_t token_stride_b, float* H, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+  reset_launches();
+  const sekv_status st = check_logits(logits, dtype, batch, ctx_len, vocab, tokens, tokens_64,
+                                      workspace, workspace_bytes);
+  if (st != SEKV_OK) return st;
+  if (!H) return SEKV_ERR_INVALID;
+  if (batch == 0 || ctx_len == 0) return SEKV_OK;
+  if (ctx_len == 1)  // nothing is predicted: H is all zeros
+    return cudaMemsetAsync(H, 0, size_t(batch) * 4, stream) == cudaSuccess ? SEKV_OK : SEKV_ERR_CUDA;
+  LpParams P{};
+  P.logits = logits;
+  P.tokens = static_cast<const char*>(tokens) + (tokens_64 ? 8 : 4);  // row t: token t + 1
+  P.logprob = H + 1;
+  P.status = static_cast<int32_t*>(workspace);
+  P.stride_b = stride_b;
+  P.stride_t = stride_t;
+  P.token_stride_b = token_stride_b;
+  P.out_stride_b = ctx_len;
+  P.n_tokens = ctx_len - 1;
+  P.vocab = vocab;
+  P.scale = 1.f;
+  P.tokens64 = tokens_64 != 0;
+  P.negate = 1;
+  return logprobs_impl(P, dtype, batch, false, stream);
+}

@@ -187,6 +187,7 @@ size_t sekv_workspace_size(const sekv_config* cfg, int32_t which, int64_t ctx_le
   const int sms = device_sm_count();
   if (sms <= 0) return 0;
   if (which == SEKV_CALL_BUILD) return build_workspace_size(cfg, ctx_len);
+  if (which == SEKV_CALL_KV4) return kv4_workspace_size(cfg, ctx_len);
   return ws_layout(cfg, sms).total;
 }
 

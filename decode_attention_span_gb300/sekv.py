@@ -21,7 +21,7 @@ from . import build as _build
 _c_i32, _c_f32, _c_vp, _c_sz, _c_i64 = (ctypes.c_int32, ctypes.c_float, ctypes.c_void_p,
                                         ctypes.c_size_t, ctypes.c_int64)
 
-SEKV_CALL_ROUTE, SEKV_CALL_FETCH, SEKV_CALL_DECODE, SEKV_CALL_BUILD = 0, 1, 2, 3
+SEKV_CALL_ROUTE, SEKV_CALL_FETCH, SEKV_CALL_DECODE, SEKV_CALL_BUILD, SEKV_CALL_KV4 = 0, 1, 2, 3, 4
 FLAG_OVERLAP_PREVIOUS = 1
 FLAG_SHORT_WAITS = 2
 STATUS = {0: "SEKV_OK", -1: "SEKV_ERR_INVALID", -2: "SEKV_ERR_CAPACITY", -3: "SEKV_ERR_CUDA",
@@ -37,7 +37,11 @@ EXPORTS = ("sekv_record_size", "sekv_workspace_size", "sekv_workspace_init",
            "sekv_fetch_bases_copy", "sekv_basis_cache_bytes", "sekv_basis_cache_init",
            "sekv_fetch_bases_cached", "sekv_build_flops", "sekv_maint_state_size",
            "sekv_maint_init", "sekv_append_token", "sekv_maint_flush",
+           "sekv_token_logprobs", "sekv_surprisal", "sekv_rope_freqs", "sekv_rope",
+           "sekv_kv4_append", "sekv_kv4_read", "sekv_kv4_attention",
            "sekv_status_string", "sekv_last_launch_count")
+# sekv_dtype
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class SekvError(RuntimeError):
@@ -153,6 +157,27 @@ def lib() -> ctypes.CDLL:
         L.sekv_build_spans.argtypes = [ctypes.POINTER(SekvConfig), _c_i64, _c_vp, _c_vp, _c_vp,
                                        _c_vp, _c_vp, ctypes.POINTER(SekvCacheOut), _c_vp, _c_sz,
                                        _c_vp]
+        L.sekv_token_logprobs.restype = _c_i32
+        L.sekv_token_logprobs.argtypes = [_c_vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                                          _c_vp, _c_i32, _c_i64, _c_f32, _c_i32, _c_vp, _c_vp,
+                                          _c_vp, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]
+        L.sekv_surprisal.restype = _c_i32
+        L.sekv_surprisal.argtypes = [_c_vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp,
+                                     _c_i32, _c_i64, _c_vp, _c_vp, _c_sz, _c_vp]
+        L.sekv_rope_freqs.restype = _c_i32
+        L.sekv_rope_freqs.argtypes = [_c_vp, _c_vp, ctypes.POINTER(_c_f32)]
+        L.sekv_rope.restype = _c_i32
+        L.sekv_rope.argtypes = [_c_vp, _c_vp, _c_f32, _c_i32, _c_i32, _c_i64, _c_i64, _c_vp,
+                                _c_i32, _c_i64, _c_vp, _c_vp, _c_i32, _c_vp]
+        L.sekv_kv4_append.restype = _c_i32
+        L.sekv_kv4_append.argtypes = [_c_vp, _c_vp, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp, _c_i32,
+                                      _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]
+        L.sekv_kv4_read.restype = _c_i32
+        L.sekv_kv4_read.argtypes = [_c_vp, _c_vp, _c_i32, _c_vp, _c_vp, _c_i32, _c_vp, _c_vp,
+                                    _c_vp, _c_sz, _c_vp]
+        L.sekv_kv4_attention.restype = _c_i32
+        L.sekv_kv4_attention.argtypes = [_c_vp, _c_vp, _c_i32, _c_vp, _c_i32, _c_vp, _c_f32,
+                                         _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]
         L.sekv_status_string.restype = ctypes.c_char_p
         L.sekv_status_string.argtypes = [_c_i32]
         L.sekv_last_launch_count.restype = _c_i32
@@ -182,6 +207,18 @@ def _need(t: torch.Tensor, name: str, dtype, cuda: bool = True):
         raise ValueError(f"{name}: must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
+
+
+def check_tensor(t: torch.Tensor, name: str, dtypes, device):
+    """A CUDA tensor of one of `dtypes` on `device`, which has to be the current one
+    (the library launches on the current device)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor on {device}, is on {t.device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {device}, but the current device is "
+                         f"{torch.cuda.current_device()}")
 
 
 # ----------------------------------------------------------------------------

@@ -165,14 +165,16 @@ typedef enum sekv_call {
   SEKV_CALL_ROUTE = 0,
   SEKV_CALL_FETCH = 1,
   SEKV_CALL_DECODE = 2,   /* sekv_decode_attention and sekv_decode_step */
-  SEKV_CALL_BUILD = 3
+  SEKV_CALL_BUILD = 3,
+  SEKV_CALL_KV4 = 4       /* sekv_kv4_*; ctx_len is the largest n_q that will be used (>= 1) */
 } sekv_call;
 
 /* Bytes of one basis record (0 when body <= 0); see the layout above. */
 int64_t sekv_record_size(int32_t body, int32_t rank_k, int32_t rank_v);
 
 /* Workspace bytes the given call needs for this configuration; ctx_len is
- * used by SEKV_CALL_BUILD only.  Returns 0 for an invalid configuration. */
+ * used by SEKV_CALL_BUILD and SEKV_CALL_KV4 only.  Returns 0 for an invalid
+ * configuration. */
 size_t sekv_workspace_size(const sekv_config* cfg, int32_t which, int64_t ctx_len);
 
 /* Zero a workspace (cudaMemsetAsync on `stream`).  Needed once, before the
@@ -545,6 +547,213 @@ sekv_status sekv_maint_flush(const sekv_config* cfg, const float* W_r, const flo
                              const sekv_cache_out* out, int32_t* n_tail, void* state,
                              size_t state_bytes, void* workspace, size_t workspace_bytes,
                              cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the span cache: what a program computes before it calls the entry
+ * points above (rotated queries and keys, the surprisal of its tokens), and a
+ * second form of the cache that holds every token in 4 bits.  The SeKV pages
+ * take these as given; formulas are stated here.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the calls below. */
+typedef enum sekv_dtype { SEKV_BF16 = 0, SEKV_F16 = 1, SEKV_F32 = 2 } sekv_dtype;
+
+/*
+ * sekv_token_logprobs -- log-probabilities of given tokens, with the entropy
+ * of each distribution and its likeliest alternatives.  For row r = (b, t)
+ * with logits l_v: x_v = scale * l_v, m = max x_v, S = sum_v exp(x_v - m),
+ *   lse     = m + ln S
+ *   logprob = x_tok - m - ln S
+ *   entropy = ln S - sum_v exp(x_v - m) (x_v - m) / S      (natural log)
+ *   top     = the n_top largest logits in descending order, ties to the lowest
+ *             token id: ids and log-probabilities.
+ * One pass over the logits; sums and statistics in fp32.
+ *   logits   dtype; the row of (b, t) starts at element b*stride_b + t*stride_t;
+ *            vocab consecutive elements; any alignment of the element type
+ *   tokens   int32 or int64 (tokens_64): token of (b, t) at b*token_stride_b + t;
+ *            -1: no token (logprob 0); any other id outside [0, vocab) gives NaN
+ *            and sets device code 1 (detail: the row)
+ *   outputs  f32 [batch][n_tokens] (lse, entropy: may be NULL); top_ids int32 and
+ *            top_logprobs f32 [batch][n_tokens][n_top] (NULL iff n_top == 0)
+ * Masked entries (-inf, or the type's lowest value) count as any other value: a
+ * -inf entry has probability 0 and is never listed (id -1, logprob -inf fill the
+ * list).  A row of nothing but -inf has lse -inf, logprob -inf (0 for token -1)
+ * and entropy 0.  A row that holds a NaN or +inf gives NaN in every float
+ * output and ids -1.
+ *   workspace  any workspace of the library: only its status word is used
+ */
+#define SEKV_MAX_TOP 32
+sekv_status sekv_token_logprobs(const void* logits, int32_t dtype, int64_t batch,
+                                int64_t n_tokens, int64_t vocab, int64_t stride_b,
+                                int64_t stride_t, const void* tokens, int32_t tokens_64,
+                                int64_t token_stride_b, float scale, int32_t n_top,
+                                float* logprob, float* lse, float* entropy, int32_t* top_ids,
+                                float* top_logprobs, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/*
+ * sekv_surprisal -- H_t = -log p(x_t | x_<t) of whole sequences, in the layout
+ * sekv_build_spans takes (f32 [batch][ctx_len]): the logits of position t - 1
+ * predict token t.  H[b][0] = 0 (nothing precedes the first token).  Logits of
+ * position ctx_len - 1 are not read.  Arguments and special values as in
+ * sekv_token_logprobs with scale 1; token -1 gives 0.
+ */
+sekv_status sekv_surprisal(const void* logits, int32_t dtype, int64_t batch, int64_t ctx_len,
+                           int64_t vocab, int64_t stride_b, int64_t stride_t, const void* tokens,
+                           int32_t tokens_64, int64_t token_stride_b, float* H, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Rotary positions.  The first rot_dim dimensions of a head form rot_dim / 2
+ * pairs (a_i, b_i): dimensions (2i, 2i+1) if interleaved, else (i, i + rot_dim/2);
+ * the others pass through.  Pair i of a token at position p turns by p * f_i:
+ *   a' = mscale (a cos - b sin),  b' = mscale (b cos + a sin)
+ * With d = rot_dim and u_i = base^(-2i/d), f_i is
+ *   NONE    u_i
+ *   LINEAR  u_i / factor
+ *   NTK     u_i of base * factor^(d/(d-2))           (rot_dim > 2)
+ *   PARTS   (1 - r_i) u_i + r_i u_i / factor; r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *           lo = max(0, floor(pair(beta_fast))), hi = min(d - 1, ceil(pair(beta_slow))),
+ *           pair(n) = d ln(original_context / (2 pi n)) / (2 ln base): the pair that
+ *           turns n times in the original context; mscale 0.1 ln(factor) + 1 (factor > 1)
+ *   BANDED  (1 - s_i) u_i / factor + s_i u_i; s_i = clamp((n_i - low_freq_factor) /
+ *           (high_freq_factor - low_freq_factor), 0, 1), n_i = original_context u_i / (2 pi)
+ * mscale is 1 unless PARTS or attention_factor > 0 (which then replaces it).
+ */
+typedef enum sekv_rope_scaling {
+  SEKV_ROPE_NONE = 0,
+  SEKV_ROPE_LINEAR = 1,
+  SEKV_ROPE_NTK = 2,
+  SEKV_ROPE_PARTS = 3,
+  SEKV_ROPE_BANDED = 4
+} sekv_rope_scaling;
+
+typedef struct sekv_rope_config {
+  int32_t rot_dim;          /* even, 2 .. 512 */
+  int32_t interleaved;      /* 0 half layout, 1 adjacent pairs */
+  int32_t scaling;          /* sekv_rope_scaling */
+  int32_t original_context; /* PARTS, BANDED: tokens the model was trained on */
+  double base;              /* > 1 */
+  double factor;            /* > 0; not used by NONE */
+  double beta_fast, beta_slow;                  /* PARTS */
+  double low_freq_factor, high_freq_factor;     /* BANDED */
+  double attention_factor;  /* 0: the scaling's own mscale */
+} sekv_rope_config;
+
+/* The table of a rotary plan (host only): freqs[i] (host, rot_dim / 2 entries) is
+ * f_i / (2 pi) modulo one turn, as a 64-bit fixed-point fraction of a turn, so that
+ * position * freqs[i] modulo 2^64 is the pair's angle exactly however far the
+ * position; *mscale is the factor on the result.  Copy freqs to the device once. */
+sekv_status sekv_rope_freqs(const sekv_rope_config* rope, uint64_t* freqs, float* mscale);
+
+/* Heads of one tensor: element (b, t, h, d) of the input at x[b*x_stride[0] +
+ * t*x_stride[1] + h*x_stride[2] + d], of the output likewise at y. */
+typedef struct sekv_heads {
+  const void* x;
+  void* y;
+  int32_t n_heads;
+  int32_t reserved;
+  int64_t x_stride[3];
+  int64_t y_stride[3];
+} sekv_heads;
+
+#define SEKV_ROPE_BACKWARD 1
+#define SEKV_ROPE_ZERO_PADDING 2
+
+/*
+ * sekv_rope -- rotates queries and keys of [batch][n_tokens] tokens in one
+ * launch.  y may be x with equal strides (in place; dimensions that pass through
+ * are then not touched); otherwise x and y must not overlap.
+ *   freqs     device, from sekv_rope_freqs; mscale likewise
+ *   positions int32 or int64 (positions_64), of token (b, t) at b*pos_stride_b + t
+ *             (0: shared by the batch).  A token with a negative position is
+ *             padding: neither read nor written (SEKV_ROPE_ZERO_PADDING: its outputs
+ *             are set to 0)
+ *   q, k      either may be NULL
+ *   flags     SEKV_ROPE_BACKWARD: turns by -p f_i (the gradient of the call without
+ *             it, and for mscale 1 its inverse); SEKV_ROPE_ZERO_PADDING
+ *   head_dim  >= rot_dim, at most 1024
+ */
+sekv_status sekv_rope(const sekv_rope_config* rope, const uint64_t* freqs, float mscale,
+                      int32_t dtype, int32_t head_dim, int64_t batch, int64_t n_tokens,
+                      const void* positions, int32_t positions_64, int64_t pos_stride_b,
+                      const sekv_heads* q, const sekv_heads* k, int32_t flags,
+                      cudaStream_t stream);
+
+/*
+ * A cache that holds K and V of every token in 4 bits, in pages of 64 tokens.
+ * Each row of 128 values has two groups of 64 dimensions; a group is stored as
+ *   z = the largest bf16 at or below its smallest value
+ *   s = bf16((max - z) * fp32(1/15)), the product in fp32, rounded to nearest even
+ *   n = clamp(rint((x - z) / s), 0, 15), the quotient in fp32; 0 where s is 0
+ * and stands for x^ = z + s n.  A group that holds a NaN or an infinity has
+ * z = s = NaN and reads as NaN (a group wider than fp32's largest value likewise).
+ *
+ * Page (p, c) of KV head c: SEKV_KV4_PAGE_BYTES bytes at pages +
+ * (p*n_kv_heads + c) * SEKV_KV4_PAGE_BYTES, four tiles of 16 tokens and 2304 bytes
+ * each.  Token j of a tile, e = 8 (j / 8), u = (j % 8) / 2, o = j % 2 (e, u and o
+ * name where the tensor cores want the token):
+ *   K code of dimension d: byte 64 j + 16 ((d % 64) / 16) + 8 (d / 64) + (d % 16) / 2,
+ *                          low nibble for even d
+ *   V code of dimension d: byte 1024 + 64 e + 64 ((d % 64) / 8) + 16 u + 8 (d / 64) +
+ *                          4 ((d % 8) / 4) + 2 o + (d % 4) / 2, low nibble for even d
+ *   K scale and zero of group g: bf16 s, bf16 z at byte 2048 + 32 u + 2 e + 8 o + 4 g
+ *   V scale and zero of group g: 128 bytes further
+ * Token t of sequence b lives in page page_table[b*max_pages + t / 64], at
+ * tile (t % 64) / 16, row t % 16.  Pages are caller-owned and need no
+ * initialisation.
+ */
+#define SEKV_KV4_PAGE_TOKENS 64
+#define SEKV_KV4_PAGE_BYTES 9216
+#define SEKV_KV4_MAX_BATCH 1024
+typedef struct sekv_kv4_cache {
+  void* pages;               /* [n_pages][n_kv_heads][SEKV_KV4_PAGE_BYTES], 16-byte aligned */
+  const int32_t* page_table; /* [batch][max_pages] */
+  int32_t n_pages;
+  int32_t max_pages;
+} sekv_kv4_cache;
+
+/* cfg: batch, n_q_heads, n_kv_heads and head_dim count (the rest only has to be
+ * valid); batch at most SEKV_KV4_MAX_BATCH.  Workspaces: SEKV_CALL_KV4.  Device
+ * code 1: a page id outside [0, n_pages), or a token beyond max_pages * 64
+ * (detail: the sequence); such tokens are not stored, read as they were and
+ * not attended to.
+ *
+ * sekv_kv4_append -- stores K and V of up to n_tokens tokens per sequence, from
+ * position first[b] on.  first: int32 [batch] (device).  n_valid: int32 [batch]
+ * (device) or NULL: only the first n_valid[b] of the n_tokens rows are stored.  k, v:
+ * bf16 or f16, element (b, t, c, d) at b*stride[0] + t*stride[1] + c*stride[2] + d,
+ * rows 16-byte aligned (strides multiples of 8).  Pages named twice must not
+ * receive the same token slot twice. */
+sekv_status sekv_kv4_append(const sekv_config* cfg, const sekv_kv4_cache* cache,
+                            int32_t dtype, const void* k, const int64_t k_stride[3],
+                            const void* v, const int64_t v_stride[3], int32_t n_tokens,
+                            const int32_t* first, const int32_t* n_valid, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+
+/* sekv_kv4_read -- the values that tokens first[b] .. first[b] + n_tokens - 1 stand
+ * for, rounded to dtype (bf16, f16 or f32): k_out, v_out [batch][n_kv_heads][n_tokens][128]
+ * (the layout sekv_build_spans takes; 16-byte aligned).  Rows from n_valid[b] on
+ * are left as they were. */
+sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cache* cache, int32_t dtype,
+                          void* k_out, void* v_out, int32_t n_tokens, const int32_t* first,
+                          const int32_t* n_valid, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* sekv_kv4_attention -- softmax attention of n_q query tokens per sequence over
+ * its cached tokens.  seq_len: int32 [batch] (device), tokens held, those of the
+ * queries among them: query i attends to the first seq_len[b] - (n_q - 1 - i)
+ * tokens.  A query that sees none has out 0 and lse -inf.
+ *   q    bf16 or f16 [batch][n_q][n_q_heads][128], n_q 1 .. SEKV_MAX_QUERY_TOKENS
+ *   out  f32 [batch][n_q][n_q_heads][128];  lse f32 [batch][n_q][n_q_heads] (natural
+ *        log; may be NULL)
+ * The (token, head) pairs of a KV head are taken eight at a time in one pass over
+ * its cache (sekv_query_blocks).  Results do not depend on what else runs:
+ * partial results are merged in a fixed order. */
+sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4_cache* cache,
+                               int32_t dtype, const void* q, int32_t n_q,
+                               const int32_t* seq_len, float scale, float* out, float* lse,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Human-readable name of a status. */
 const char* sekv_status_string(sekv_status status);

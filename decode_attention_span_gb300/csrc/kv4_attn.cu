@@ -1,18 +1,18 @@
 // sekv_kv4_attention: attention of a few query tokens over the 4-bit cache.
 //
 // Bound by memory: 144 bytes per (token, KV head) are read once for all query
-// heads of the group.  The cache's layout is the tensor cores' operand
-// layout, so a lane's codes come from shared memory as 16-byte words and become
-// bf16 operands with one shift and one lop3 per pair (0x4300 | n is 128 + n
-// exactly); no value is rebuilt.  With K^ = z + s n for each group of 64
-// dimensions,
-//   q . K^ = sum over groups of  s (sum_d q_d n_d) + z (sum_d q_d)
-// and the 128 is taken off by starting the product's accumulators at
-// -128 sum_d q_d.  For V, sum_j p_j V^_j = sum_j (p_j s_j) (n_j - 8) + sum_j
-// p_j (z_j + 8 s_j): the weights p_j s_j enter the product as the sum of two bf16
-// numbers (16 significant bits), the upper one in rows 0-7 of the A operand and
-// the lower in rows 8-15, which the eight (token, head) columns leave free; so
-// the result keeps fp32's usefulness at no further matrix instruction.
+// heads of the group.  The cache's layout is the matrix instructions' operand
+// layout: a lane's codes come from shared memory as 16-byte words and become the
+// A operand (tokens or dimensions in its 16 rows, the eight (token, head) columns
+// in B) with one or two instructions per pair; no K or V value is rebuilt.  With
+// K^ = z + s n for each group of 64 dimensions,
+//   q . K^ = sum over groups of  s (sum_d q_d n_d) + z (sum_d q_d).
+// bf16 queries meet 128 + n (0x4300 | n, exact) and the 128 comes off by starting
+// the accumulators at -128 sum_d q_d; f16 queries meet n - 8.  For V,
+//   sum_j p_j V^_j = sum_j (p_j s_j) (n_j - 8) + sum_j p_j (z_j + 8 s_j),
+// where the weight p_j s_j enters as the sum of two f16 numbers (22 significant
+// bits: one alone would cost the fp32 result 13 of its bits), scaled by a power of
+// two that follows the largest s seen, so that scales of any size fit f16.
 //
 // Work: the cache is a line of chunks of 32 tokens (sequence by sequence, in
 // it KV head by KV head), cut into equal pieces, one per CTA.  The warps of a CTA
@@ -22,6 +22,7 @@
 // the partials in order.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -30,11 +31,12 @@ using namespace sekv;
 
 namespace {
 
-constexpr int kAttnWarps = 12;
+constexpr int kAttnWarps = 16;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kChunkTokens = 32;
 constexpr int kChunkBytes = 2 * kKv4TileBytes;
+constexpr int kMaxCtas = 256;                    // of a launch
 constexpr int kCols = 8;                         // (token, head) pairs of a block
 constexpr int kStateFloats = kCols * (kHeadDim + 2);  // o, m, l
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -47,9 +49,17 @@ struct AttnShared {
   float w[kAttnWarps][kCols];
   float mx[kCols], sum[kCols];
   uint64_t bar[kAttnWarps][kStages];
-  int64_t before[SEKV_KV4_MAX_BATCH + 1];  // chunks before each sequence
+  int before[SEKV_KV4_MAX_BATCH + 1];  // chunks before each sequence
+  int len[SEKV_KV4_MAX_BATCH];         // tokens of each sequence
   int last;
 };
+// scratch of the last CTA of a group, over the warps' values
+struct JoinShared {
+  float w[kMaxCtas][kCols];   // maxima, then weights
+  float l[kMaxCtas][kCols];
+  float4 half[kCols * kHeadDim / 4];
+};
+static_assert(sizeof(JoinShared) <= sizeof(AttnShared::o), "the join's scratch lies over the warps' values");
 
 struct AttnParams {
   Kv4Pages pg;
@@ -62,27 +72,65 @@ struct AttnParams {
   float scale_log2;
 };
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+// D = A B + C, 16 x 8 = 16 x 16 * 16 x 8 + 16 x 8
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                    const float (&c)[4], __nv_bfloat16) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                    const float (&c)[4], __half) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
 }
 
-// codes i and i + 4 of a word as a bf16 pair 128 + n
-__device__ __forceinline__ uint32_t codes(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+// (w & MASK) | bits in one instruction: the compiler makes two of the plain form, whose
+// two constants do not fit one; `bits` stays in a register
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(MASK), "r"(bits));
+  return r;
 }
-// the same, n - 8 (exact)
-__device__ __forceinline__ uint32_t centred(uint32_t w, int i) {
-  const uint32_t c = codes(w, i);
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c),
-                                   __nv_bfloat162(__ushort_as_bfloat16(0x4308),
-                                                  __ushort_as_bfloat16(0x4308)));
-  return *reinterpret_cast<const uint32_t*>(&r);
+
+// 8x8 matrix of 16-bit values over the warp, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
+
+// The four pairs of a word's codes (pair i: codes i and i + 4) less 8, as f16: the
+// low nibbles of each byte as 1024 + n, the high ones as 1024 + 16 n, both exact.
+__device__ __forceinline__ void centred(uint32_t w, uint32_t (&r)[4]) {
+  const uint32_t w8 = w >> 8;
+  const uint32_t u[4] = {mask_or<0x000f000fu>(w, 0x64006400u), mask_or<0x00f000f0u>(w, 0x64006400u),
+                         mask_or<0x000f000fu>(w8, 0x64006400u), mask_or<0x00f000f0u>(w8, 0x64006400u)};
+  const __half2 low = __half2half2(__ushort_as_half(0xe408));    // -1032
+  const __half2 high = __half2half2(__ushort_as_half(0xd480));   // -72
+  const __half2 inv16 = __half2half2(__ushort_as_half(0x2c00));  // 1/16
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 x = *reinterpret_cast<const __half2*>(&u[i]);
+    const __half2 y = i & 1 ? __hfma2(x, inv16, high) : __hadd2(x, low);
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+// K's pairs as the queries' type meets them: 128 + n in bf16, n - 8 in f16
+__device__ __forceinline__ void k_codes(uint32_t w, uint32_t (&r)[4], __nv_bfloat16) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = mask_or<0x000f000fu>(w >> (4 * i), 0x43004300u);
+}
+__device__ __forceinline__ void k_codes(uint32_t w, uint32_t (&r)[4], __half) { centred(w, r); }
+
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -93,16 +141,183 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ float q_value(const __nv_bfloat16* q) { return __bfloat162float(*q); }
-__device__ __forceinline__ float q_value(const __half* q) { return __half2float(*q); }
+__device__ __forceinline__ uint32_t pack_pair(__nv_bfloat16 a, __nv_bfloat16 b) {
+  return uint32_t(__bfloat16_as_ushort(a)) | uint32_t(__bfloat16_as_ushort(b)) << 16;
+}
+__device__ __forceinline__ uint32_t pack_pair(__half a, __half b) {
+  return uint32_t(__half_as_ushort(a)) | uint32_t(__half_as_ushort(b)) << 16;
+}
+__device__ __forceinline__ float q_value(__nv_bfloat16 q) { return __bfloat162float(q); }
+__device__ __forceinline__ float q_value(__half q) { return __half2float(q); }
 
-// A warp's softmax state of one group: columns g = lane / 4, and of the values
-// the dimensions that the matrix product's accumulators give this lane.
+// A warp's softmax state of one group.  A lane holds columns 2t and 2t + 1, and of
+// the values dimensions 8g .. 8g + 7 of both groups of dimensions; l and c are sums
+// over its own tokens (rows g and g + 8 of each tile).
 struct WarpState {
-  float o[16][4];
-  float m, l;     // of column g; l over this lane's tokens
-  float c[2];     // sum of p (z + 8 s) over this lane's tokens, per group of dimensions
+  float o[8][4];   // [4 dims apiece: word m, i][rows g, g + 8 x columns], in units of 1 / unit
+  float m[2], l[2];
+  float c[2][2];   // sum of p (z + 8 s): [column][group of dimensions]
+  float unit;      // power of two on the weights of o
 };
+
+// What one chunk needs beside the state.
+template <typename T>
+struct Query {
+  uint32_t b[8][2];     // B operand of the eight 16-dimension steps
+  float sum[2][2];      // [column][group]: sum of q over the group's dimensions
+  float offset[2][4];   // [group]: what the accumulators start at (rows g and g + 8 x columns)
+  float scale_log2;
+};
+
+// EDGE: some token of the chunk is not seen by some column (seen: per column of the
+// lane; held: tokens of the chunk that the sequence has).
+template <typename T, bool EDGE>
+__device__ __forceinline__ void chunk_step(WarpState& S, const Query<T>& Q, const uint8_t* chunk,
+                                           int lane, int held, const int (&seen)[2]) {
+  const int g = lane >> 2;
+  constexpr bool kOffset = std::is_same<T, __nv_bfloat16>::value;
+  float x[2][2][2];  // tile, row half, column
+#pragma unroll
+  for (int ti = 0; ti < 2; ++ti) {
+    const uint8_t* tile = chunk + ti * kKv4TileBytes;
+    float acc[2][4];
+    const uint4 k0 = *reinterpret_cast<const uint4*>(tile + lane * 16);
+    const uint4 k1 = *reinterpret_cast<const uint4*>(tile + 512 + lane * 16);
+    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      uint32_t r0[4], r1[4];
+      k_codes(w0[m], r0, T());
+      k_codes(w1[m], r1, T());
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t a[4] = {r0[2 * s], r1[2 * s], r0[2 * s + 1], r1[2 * s + 1]};
+        if ((m & 1) == 0 && s == 0)
+          mma(acc[m >> 1], a, Q.b[2 * m][0], Q.b[2 * m][1], Q.offset[m >> 1], T());
+        else
+          mma(acc[m >> 1], a, Q.b[2 * m + s][0], Q.b[2 * m + s][1], acc[m >> 1], T());
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint2 sz = *reinterpret_cast<const uint2*>(tile + kKv4Params + 32 * (g >> 1) + 8 * (g & 1) + 16 * e);
+      const float s0 = lo16(sz.x), s1 = lo16(sz.y);
+      const float z0 = kOffset ? hi16(sz.x) : fmaf(8.f, s0, hi16(sz.x));
+      const float z1 = kOffset ? hi16(sz.y) : fmaf(8.f, s1, hi16(sz.y));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float y = s0 * acc[0][2 * e + c];
+        y = fmaf(z0, Q.sum[c][0], y);
+        y = fmaf(s1, acc[1][2 * e + c], y);
+        y = fmaf(z1, Q.sum[c][1], y) * Q.scale_log2;
+        x[ti][e][c] = !EDGE || ti * 16 + e * 8 + g < seen[c] ? y : -INFINITY;
+      }
+    }
+  }
+
+  // the columns' maxima, over the rows of all lanes; and the largest scale of V
+  float mx[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    mx[c] = fmaxf(fmaxf(x[0][0][c], x[0][1][c]), fmaxf(x[1][0][c], x[1][1][c]));
+  uint2 vp[2][2];
+  uint32_t top = 0;  // lower half: bf16 bits of the largest scale (never negative)
+#pragma unroll
+  for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      vp[ti][e] = *reinterpret_cast<const uint2*>(chunk + ti * kKv4TileBytes + kKv4Params + 128 +
+                                                  32 * (g >> 1) + 8 * (g & 1) + 16 * e);
+      if (EDGE && ti * 16 + e * 8 + g >= held) vp[ti][e] = make_uint2(0u, 0u);
+      top = __vimax3_u16x2(top, vp[ti][e].x, vp[ti][e].y);
+    }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    mx[0] = fmaxf(mx[0], __shfl_xor_sync(~0u, mx[0], o));
+    mx[1] = fmaxf(mx[1], __shfl_xor_sync(~0u, mx[1], o));
+  }
+  top = __reduce_max_sync(~0u, top & 0xffffu);
+  if (top >= 0x7f80u) {  // an infinity or NaN does not count: look again without them
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t s = (i & 1 ? vp[i >> 2][i >> 1 & 1].y : vp[i >> 2][i >> 1 & 1].x) & 0xffffu;
+      top = max(top, s < 0x7f80u ? s : 0u);
+    }
+    top = __reduce_max_sync(~0u, top);
+  }
+  // largest unit with top * unit < 2^15 (f16 ends at 65504)
+  const float unit = __uint_as_float(min(254u, 268u - max(14u, top >> 7)) << 23);
+  const bool up = mx[0] > S.m[0] || mx[1] > S.m[1];
+  if (__any_sync(~0u, up) || unit < S.unit) {
+    float f[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float m1 = fmaxf(S.m[c], mx[c]);
+      f[c] = S.m[c] == -INFINITY ? 0.f : ex2(S.m[c] - m1);
+      S.m[c] = m1;
+      S.l[c] *= f[c];
+      S.c[c][0] *= f[c];
+      S.c[c][1] *= f[c];
+    }
+    const float v = fminf(unit, S.unit);
+    f[0] *= v / S.unit;
+    f[1] *= v / S.unit;
+    S.unit = v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S.o[j][i] *= f[i & 1];
+  }
+  const float m0[2] = {S.m[0] == -INFINITY ? 0.f : S.m[0], S.m[1] == -INFINITY ? 0.f : S.m[1]};
+
+#pragma unroll
+  for (int ti = 0; ti < 2; ++ti) {
+    const uint8_t* tile = chunk + ti * kKv4TileBytes;
+    uint32_t bh[2][2], bl[2][2];  // [group of dimensions][row half]: B operands, upper and lower part
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t sz[2] = {vp[ti][e].x, vp[ti][e].y};
+      float p[2], w[2][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        p[c] = ex2(x[ti][e][c] - m0[c]);
+        S.l[c] += p[c];
+      }
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        const float s = lo16(sz[gr]), z = fmaf(8.f, s, hi16(sz[gr])), su = s * S.unit;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // a token that the column does not see has p 0, but may hold NaN
+          const bool ok = !EDGE || ti * 16 + e * 8 + g < seen[c];
+          w[gr][c] = ok ? p[c] * su : 0.f;
+          S.c[c][gr] = ok ? fmaf(p[c], z, S.c[c][gr]) : S.c[c][gr];
+        }
+        const __half2 h = __floats2half2_rn(w[gr][0], w[gr][1]);
+        const float2 hf = __half22float2(h);
+        const __half2 l = __floats2half2_rn(w[gr][0] - hf.x, w[gr][1] - hf.y);
+        bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
+        bl[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&l));
+      }
+    }
+    const uint4 v0 = *reinterpret_cast<const uint4*>(tile + kKv4V + lane * 16);
+    const uint4 v1 = *reinterpret_cast<const uint4*>(tile + kKv4V + 512 + lane * 16);
+    const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      uint32_t r0[4], r1[4];
+      centred(w0[m], r0);
+      centred(w1[m], r1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t a[4] = {r0[i], r0[i + 2], r1[i], r1[i + 2]};
+        mma(S.o[2 * m + i], a, bh[m >> 1][0], bh[m >> 1][1], S.o[2 * m + i], __half());
+        mma(S.o[2 * m + i], a, bl[m >> 1][0], bl[m >> 1][1], S.o[2 * m + i], __half());
+      }
+    }
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnParams P) {
@@ -116,23 +331,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.bar[warp][s], 1);
   fence_mbar_init();
   // chunks of each sequence (at least one, so that every group has a CTA)
-  const int64_t cap = int64_t(P.pg.max_pages) * kKv4Page;
+  const int cap = P.pg.max_pages * kKv4Page;
   if (warp == 0) {
-    int64_t run = 0;
+    int run = 0;
     for (int b0 = 0; b0 < P.batch; b0 += 32) {
       const int b = b0 + lane;
-      int64_t n = 0;
+      int n = 0;
       if (b < P.batch) {
-        int64_t len = P.seq_len[b];
-        if (len < 0 || len > cap) {
-          if (blockIdx.x == 0) set_device_error(P.pg.status, DEV_BAD_LIST, b);
-          len = len < 0 ? 0 : cap;
-        }
-        n = max(int64_t(1), (len + kChunkTokens - 1) / kChunkTokens) * per_seq;
+        const int given = P.seq_len[b];
+        const int len = min(max(given, 0), cap);
+        if (given != len && blockIdx.x == 0) set_device_error(P.pg.status, DEV_BAD_LIST, b);
+        sh.len[b] = len;
+        n = max(1, (len + kChunkTokens - 1) / kChunkTokens) * per_seq;
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(~0u, n, o);
+        const int up = __shfl_up_sync(~0u, n, o);
         if (lane >= o) n += up;
       }
       if (b < P.batch) sh.before[b + 1] = run + n;
@@ -141,240 +355,182 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     if (lane == 0) sh.before[0] = 0;
   }
   __syncthreads();
-  const int64_t total = sh.before[P.batch];
-  const int n_cta = int(min(int64_t(gridDim.x), total));
+  const int total = sh.before[P.batch];
+  const int n_cta = min(int(gridDim.x), total);
   const int cta = blockIdx.x;
   if (cta >= n_cta) return;
-  const int64_t u0 = total * cta / n_cta, u1 = total * (cta + 1) / n_cta;
+  // piece of CTA c: [start(c), start(c + 1)), start(c) = total * c / n_cta
+  const int each = total / n_cta, over = total - each * n_cta;
+  auto start = [&](int c) { return each * c + over * c / n_cta; };
+  const int u0 = start(cta), u1 = start(cta + 1);
 
   uint32_t done = 0;  // chunks this warp has taken off its ring, over all segments
   bool lost = false;  // a copy of this warp did not land in time
-  int64_t u = u0;
+  int u = u0, b = 0;
   while (u < u1) {
-    int b = 0;
-    for (int step = 512; step > 0; step >>= 1)
-      if (b + step < P.batch && sh.before[b + step] <= u) b += step;
-    const int64_t len = max(int64_t(0), min(int64_t(P.seq_len[b]), cap));
-    const int n_chunks = int((sh.before[b + 1] - sh.before[b]) / per_seq);
-    const int64_t rel = u - sh.before[b];
-    const int gi = int(rel / n_chunks);
-    const int c0 = int(rel - int64_t(gi) * n_chunks);
-    const int c1 = int(min(int64_t(n_chunks), c0 + (u1 - u)));
+    for (;;) {  // the sequence of chunk u: the last one that starts at or before it
+      const int i = b + 1 + lane;
+      const int n = __popc(__ballot_sync(~0u, i < P.batch && sh.before[i] <= u));
+      b += n;
+      if (n < 32) break;
+    }
+    const int len = sh.len[b];
+    const int n_chunks = (sh.before[b + 1] - sh.before[b]) / per_seq;
+    const int rel = u - sh.before[b];
+    const int gi = rel / n_chunks;
+    const int c0 = rel - gi * n_chunks;
+    const int c1 = min(n_chunks, c0 + (u1 - u));
     const int blk = gi / P.pg.hkv, head = gi - blk * P.pg.hkv;
     const int cols = min(P.tpb, P.n_q - blk * P.tpb) * P.hpg;
-    const int tok_g = blk * P.tpb + g / P.hpg;  // query token of column g
-    const int64_t see = g < cols ? len - (P.n_q - 1 - tok_g) : 0;  // tokens column g sees
 
-    // ring: this warp's k-th chunk of the segment is c0 + warp + 12 k
+    // This warp's k-th chunk of the segment is c0 + warp + kAttnWarps k.  Lane i
+    // looks up the page of chunk 32 j + i; -1 where there is none to copy.
     const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kAttnWarps - 1) / kAttnWarps : 0;
-    auto issue = [&](int k) {  // lane 0
-      const int ch = c0 + warp + k * kAttnWarps;
-      const uint32_t st = (done + k) % kStages;
-      const int64_t pos = int64_t(ch) * kChunkTokens;
-      const uint8_t* src = pos < len && !lost ? P.pg.tile(b, head, pos) : nullptr;
-      if (src) {
-        mbar_arrive_expect_tx(&sh.bar[warp][st], kChunkBytes);
-        bulk_g2s(sh.ring[warp][st], src, kChunkBytes, &sh.bar[warp][st]);
-      } else {
-        mbar_arrive(&sh.bar[warp][st]);  // nothing to copy: no token of the chunk counts
-      }
-      return src != nullptr;
+    auto lookup = [&](int k) {
+      const int pos = (c0 + warp + k * kAttnWarps) * kChunkTokens;
+      if (k >= mine || pos >= len) return -1;
+      const int id = P.pg.table[int64_t(b) * P.pg.max_pages + pos / kKv4Page];
+      if (id >= 0 && id < P.pg.n_pages) return id;
+      set_device_error(P.pg.status, DEV_BAD_LIST, b);
+      return -1;
     };
-    uint32_t present = 0;  // bit k % 32: chunk k has a page
-    if (lane == 0)
-      for (int k = 0; k < min(mine, kStages); ++k)
-        if (issue(k)) present |= 1u << (k & 31);
+    int ids = lookup(lane), ids_next = lookup(32 + lane);
+    uint32_t present = 0;  // bit k % 32: chunk k is in the ring
+    auto issue = [&](int k) {
+      if (k > 0 && (k & 31) == 0) {
+        ids = ids_next;
+        ids_next = lookup(k + 32 + lane);
+      }
+      const int id = lost ? -1 : __shfl_sync(~0u, ids, k & 31);
+      const uint32_t bit = 1u << (k & 31);
+      present = id >= 0 ? present | bit : present & ~bit;
+      if (lane == 0) {
+        const uint32_t st = (done + k) % kStages;
+        if (id >= 0) {
+          const int ch = c0 + warp + k * kAttnWarps;
+          mbar_arrive_expect_tx(&sh.bar[warp][st], kChunkBytes);
+          bulk_g2s(sh.ring[warp][st],
+                   P.pg.pages + (int64_t(id) * P.pg.hkv + head) * kKv4PageBytes +
+                       (ch & (kKv4Page / kChunkTokens - 1)) * kChunkBytes,
+                   kChunkBytes, &sh.bar[warp][st]);
+        } else {
+          mbar_arrive(&sh.bar[warp][st]);  // nothing to copy: no token of the chunk counts
+        }
+      }
+    };
+    for (int k = 0; k < min(mine, kStages); ++k) issue(k);
 
-    // queries: A operand of the eight 16-dimension steps, upper half (rows 0-7) and,
-    // for f16 input, what bf16 leaves of it (rows 8-15)
-    uint32_t qa[8][2], ql[8][2];
-    float qs[2] = {0.f, 0.f}, qsl[2] = {0.f, 0.f};
-    constexpr bool kSplit = !std::is_same<T, __nv_bfloat16>::value;
+    Query<T> Q;
+    Q.scale_log2 = P.scale_log2;
+    int see[2];  // tokens that columns 2t and 2t + 1 see
     {
-      const int h = head * P.hpg + g % P.hpg;
+      const int tok = blk * P.tpb + g / P.hpg;  // this lane's column of the B operand
       const T* q = static_cast<const T*>(P.q) +
-                   ((int64_t(b) * P.n_q + tok_g) * P.pg.hkv * P.hpg + h) * kHeadDim;
+                   ((int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + g % P.hpg) * kHeadDim;
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
+      for (int gr = 0; gr < 2; ++gr) {
+        // the lane's sixteen dimensions of the group, as two vectors
+        union {
+          uint4 w[2];
+          T e[16];
+        } v;
+        v.w[0] = v.w[1] = make_uint4(0, 0, 0, 0);
+        if (g < cols) {
+          const uint4* src = reinterpret_cast<const uint4*>(q + gr * 64 + t * 16);
+          v.w[0] = __ldg(src);
+          v.w[1] = __ldg(src + 1);
+        }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int d = (ks >> 2) * 64 + t * 16 + ((ks >> 1) & 1) * 8 + (ks & 1) * 2 + e;
-          const float x0 = g < cols ? q_value(q + d) : 0.f;
-          const float x1 = g < cols ? q_value(q + d + 4) : 0.f;
-          const uint32_t w = pack_bf16(x0, x1);
-          qa[ks][e] = w;
-          qs[ks >> 2] += lo16(w) + hi16(w);
-          if (kSplit) {
-            const uint32_t wl = pack_bf16(x0 - lo16(w), x1 - hi16(w));
-            ql[ks][e] = wl;
-            qsl[ks >> 2] += lo16(wl) + hi16(wl);
-          } else {
-            ql[ks][e] = 0;
+        for (int i = 0; i < 16; ++i) sum[gr] += q_value(v.e[i]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = (s >> 1) * 8 + (s & 1) * 2 + e;
+            Q.b[gr * 4 + s][e] = pack_pair(v.e[d], v.e[d + 4]);
           }
-        }
+      }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          qs[i] += __shfl_xor_sync(~0u, qs[i], o);
-          qsl[i] += __shfl_xor_sync(~0u, qsl[i], o);
+        for (int o = 1; o < 4; o <<= 1) sum[i] += __shfl_xor_sync(~0u, sum[i], o);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          Q.sum[c][i] = __shfl_sync(~0u, sum[i], (2 * t + c) * 4);
+          Q.offset[i][c] = Q.offset[i][2 + c] =
+              std::is_same<T, __nv_bfloat16>::value ? -128.f * Q.sum[c][i] : 0.f;
         }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = 2 * t + c;
+        see[c] = col < cols ? len - (P.n_q - 1 - (blk * P.tpb + col / P.hpg)) : 0;
+      }
     }
+    // up to here no token is hidden from any column in use
+    const int open = len - (P.n_q - 1 - blk * P.tpb);
 
     WarpState S;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) S.o[j][i] = 0.f;
-    S.m = -INFINITY;
-    S.l = S.c[0] = S.c[1] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      S.m[c] = -INFINITY;
+      S.l[c] = S.c[c][0] = S.c[c][1] = 0.f;
+    }
+    S.unit = __uint_as_float(254u << 23);
 
     for (int k = 0; k < mine; ++k) {
       const uint32_t st = (done + k) % kStages;
-      bool have = __shfl_sync(~0u, present, 0) >> (k & 31) & 1u;
-      if (have && !lost &&
-          !__all_sync(~0u, mbar_wait_parked(&sh.bar[warp][st], ((done + k) / kStages) & 1, kWaitNs))) {
-        // a copy did not land: nothing more is copied or waited for by this warp, and
-        // what is still in flight gets its time to land before the CTA may end
-        if (lane == 0) set_device_error(P.pg.status, DEV_WAIT_TIMEOUT, 4);
-        for (int j = k; j < min(mine, k + kStages); ++j)
-          mbar_wait_parked(&sh.bar[warp][(done + j) % kStages], ((done + j) / kStages) & 1, kWaitNs);
-        lost = true;
-      }
-      have = have && !lost;
-      const int64_t pos = int64_t(c0 + warp + k * kAttnWarps) * kChunkTokens;
-      const int seen = have ? int(min(int64_t(kChunkTokens), see - pos)) : 0;  // this column's
-      const uint8_t* chunk = sh.ring[warp][st];
-
-      float x[2][4];
-#pragma unroll
-      for (int ti = 0; ti < 2; ++ti) {
-        const uint8_t* tile = chunk + ti * kKv4TileBytes;
-        uint32_t kp[4][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(tile + kKv4Params + 32 * t + 16 * i);
-          kp[2 * i][0] = w.x; kp[2 * i][1] = w.y; kp[2 * i + 1][0] = w.z; kp[2 * i + 1][1] = w.w;
+      if ((present >> (k & 31) & 1u) && !lost) {
+        if (__all_sync(~0u, mbar_wait_parked(&sh.bar[warp][st], ((done + k) / kStages) & 1, kWaitNs))) {
+          const int pos = (c0 + warp + k * kAttnWarps) * kChunkTokens;
+          const int held = len - pos;
+          const int seen[2] = {see[0] - pos, see[1] - pos};
+          if (pos + kChunkTokens <= open)
+            chunk_step<T, false>(S, Q, sh.ring[warp][st], lane, held, seen);
+          else
+            chunk_step<T, true>(S, Q, sh.ring[warp][st], lane, held, seen);
+        } else {
+          // a copy did not land: nothing more is copied or waited for by this warp, and
+          // what is still in flight gets its time to land before the CTA may end
+          if (lane == 0) set_device_error(P.pg.status, DEV_WAIT_TIMEOUT, 4);
+          for (int j = k; j < min(mine, k + kStages); ++j)
+            mbar_wait_parked(&sh.bar[warp][(done + j) % kStages], ((done + j) / kStages) & 1, kWaitNs);
+          lost = true;
         }
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          const uint4 kw = *reinterpret_cast<const uint4*>(tile + sub * 512 + lane * 16);
-          const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
-          float y[2] = {0.f, 0.f};
-#pragma unroll
-          for (int gr = 0; gr < 2; ++gr) {
-            float acc[4] = {-128.f * qs[gr], -128.f * qs[gr], -128.f * qsl[gr], -128.f * qsl[gr]};
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const int ks = gr * 4 + s;
-              mma_bf16(acc, qa[ks][0], ql[ks][0], qa[ks][1], ql[ks][1],
-                       codes(w[ks >> 1], (ks & 1) * 2), codes(w[ks >> 1], (ks & 1) * 2 + 1));
-            }
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const uint32_t sz = kp[sub * 2 + o][gr];
-              const float dot = kSplit ? acc[o] + acc[2 + o] : acc[o];
-              y[o] += lo16(sz) * dot + hi16(sz) * (kSplit ? qs[gr] + qsl[gr] : qs[gr]);
-            }
-          }
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const int row = ti * 16 + sub * 8 + 2 * t + o;
-            x[ti][sub * 2 + o] = row < seen ? y[o] * P.scale_log2 : -INFINITY;
-          }
-        }
-      }
-
-      float mx = -INFINITY;
-#pragma unroll
-      for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, x[ti][i]);
-      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-      if (__any_sync(~0u, mx > S.m)) {
-        const float m1 = fmaxf(S.m, mx);
-        const float f = S.m == -INFINITY ? 0.f : ex2(S.m - m1);
-        S.m = m1;
-        S.l *= f;
-        S.c[0] *= f;
-        S.c[1] *= f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) S.o[j][i] *= f;
-      }
-      const float m0 = S.m == -INFINITY ? 0.f : S.m;
-
-#pragma unroll
-      for (int ti = 0; ti < 2; ++ti) {
-        const uint8_t* tile = chunk + ti * kKv4TileBytes;
-        uint32_t a[2][4];  // per group of dimensions: upper and lower parts of p s
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          const uint4 w = *reinterpret_cast<const uint4*>(tile + kKv4Params + 128 + 32 * t + 16 * sub);
-          const uint32_t vp[2][2] = {{w.x, w.y}, {w.z, w.w}};
-          float ps[2][2];
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const float p = ex2(x[ti][sub * 2 + o] - m0);
-            S.l += p;
-#pragma unroll
-            for (int gr = 0; gr < 2; ++gr) {
-              // a row that the column does not see may hold anything: take it as zero
-              const uint32_t sz = ti * 16 + sub * 8 + 2 * t + o < seen ? vp[o][gr] : 0u;
-              const float s = lo16(sz), z = hi16(sz);
-              ps[gr][o] = p * s;
-              S.c[gr] = fmaf(p, fmaf(8.f, s, z), S.c[gr]);
-            }
-          }
-#pragma unroll
-          for (int gr = 0; gr < 2; ++gr) {
-            const uint32_t h = pack_bf16(ps[gr][0], ps[gr][1]);
-            a[gr][2 * sub] = h;
-            a[gr][2 * sub + 1] = pack_bf16(ps[gr][0] - lo16(h), ps[gr][1] - hi16(h));
-          }
-        }
-        const uint4 v0 = *reinterpret_cast<const uint4*>(tile + kKv4V + lane * 16);
-        const uint4 v1 = *reinterpret_cast<const uint4*>(tile + kKv4V + 512 + lane * 16);
-        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          mma_bf16(S.o[j], a[j >> 3][0], a[j >> 3][1], a[j >> 3][2], a[j >> 3][3],
-                   centred(w0[j >> 2], j & 3), centred(w1[j >> 2], j & 3));
       }
       __syncwarp();
-      if (lane == 0 && k + kStages < mine) {
-        const bool ok = issue(k + kStages);
-        const uint32_t bit = 1u << ((k + kStages) & 31);
-        present = ok ? present | bit : present & ~bit;
-      }
+      if (k + kStages < mine) issue(k + kStages);
     }
     done += mine;
 
     // the warps' states into shared memory
+    const float inv_unit = 1.f / S.unit;
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      S.l += __shfl_xor_sync(~0u, S.l, o);
-      S.c[0] += __shfl_xor_sync(~0u, S.c[0], o);
-      S.c[1] += __shfl_xor_sync(~0u, S.c[1], o);
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        S.l[c] += __shfl_xor_sync(~0u, S.l[c], o);
+        S.c[c][0] += __shfl_xor_sync(~0u, S.c[c][0], o);
+        S.c[c][1] += __shfl_xor_sync(~0u, S.c[c][1], o);
+      }
+      if (g == 0) {
+        sh.m[warp][2 * t + c] = S.m[c];
+        sh.l[warp][2 * t + c] = S.l[c];
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float add = S.c[c][m >> 1];
+        *reinterpret_cast<float4*>(&sh.o[warp][2 * t + c][(m >> 1) * 64 + g * 8 + (m & 1) * 4]) =
+            make_float4(fmaf(S.o[2 * m][c], inv_unit, add), fmaf(S.o[2 * m + 1][c], inv_unit, add),
+                        fmaf(S.o[2 * m][2 + c], inv_unit, add),
+                        fmaf(S.o[2 * m + 1][2 + c], inv_unit, add));
+      }
     }
-    if (t == 0) {
-      sh.m[warp][g] = S.m;
-      sh.l[warp][g] = S.l;
-    }
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const int j = gr * 8 + i;
-          *reinterpret_cast<float4*>(&sh.o[warp][g][gr * 64 + t * 16 + e * 8 + i]) = make_float4(
-              S.o[j][e] + S.o[j][2 + e] + S.c[gr], S.o[j + 1][e] + S.o[j + 1][2 + e] + S.c[gr],
-              S.o[j + 2][e] + S.o[j + 2][2 + e] + S.c[gr],
-              S.o[j + 3][e] + S.o[j + 3][2 + e] + S.c[gr]);
-        }
     __syncthreads();
     if (tid < kCols) {
       float mx = -INFINITY, sum = 0.f;
@@ -389,7 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     }
     __syncthreads();
 
-    const int64_t gs = sh.before[b] + int64_t(gi) * n_chunks, ge = gs + n_chunks;
+    const int gs = sh.before[b] + gi * n_chunks, ge = gs + n_chunks;
     const bool whole = u0 <= gs && ge <= u1;
     const int64_t group = int64_t(b) * per_seq + gi;
     auto write_out = [&](int col, int d, float4 v, float mx, float sum) {
@@ -422,33 +578,62 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     }
     if (!whole) {
       // the CTAs of this group, in order of their pieces
-      const int first = int(((gs + 1) * n_cta - 1) / total), last = int((ge * n_cta - 1) / total);
+      const int first = int((int64_t(gs + 1) * n_cta - 1) / total);
+      const int n = int((int64_t(ge) * n_cta - 1) / total) - first + 1;
       __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const int n = atomicAdd(P.arrived + group, 1) + 1;
-        sh.last = n == last - first + 1;
+        sh.last = atomicAdd(P.arrived + group, 1) == n - 1;
         if (sh.last) P.arrived[group] = 0;  // ready for the next call
       }
       __syncthreads();
-      if (sh.last && tid < kCols * kHeadDim / 4) {
+      if (sh.last) {
         __threadfence();
-        const int col = tid / (kHeadDim / 4), d = tid % (kHeadDim / 4) * 4;
-        auto slot = [&](int c) {
-          return P.partials + (int64_t(c) * 2 + (gs > total * c / n_cta ? 1 : 0)) * kStateFloats;
+        JoinShared& jn = *reinterpret_cast<JoinShared*>(&sh.o[0][0][0]);
+        auto slot = [&](int i) {
+          return P.partials + (int64_t(first + i) * 2 + (gs > start(first + i) ? 1 : 0)) * kStateFloats;
         };
-        float mx = -INFINITY, sum = 0.f;
-        for (int c = first; c <= last; ++c) mx = fmaxf(mx, __ldcg(slot(c) + kCols * kHeadDim + col));
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = first; c <= last; ++c) {
-          const float* p = slot(c);
-          const float m = __ldcg(p + kCols * kHeadDim + col);
-          const float f = m == -INFINITY ? 0.f : ex2(m - mx);
-          sum += f * __ldcg(p + kCols * kHeadDim + kCols + col);
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p + col * kHeadDim + d));
-          v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+        for (int i = tid; i < n * kCols; i += kAttnThreads) {
+          const float* p = slot(i / kCols) + kCols * kHeadDim + i % kCols;
+          jn.w[i / kCols][i % kCols] = __ldcg(p);
+          jn.l[i / kCols][i % kCols] = __ldcg(p + kCols);
         }
-        if (col < cols) write_out(col, d, v, mx, sum);
+        __syncthreads();
+        if (warp < kCols) {
+          float mx = -INFINITY, sum = 0.f;
+          for (int i = lane; i < n; i += 32) mx = fmaxf(mx, jn.w[i][warp]);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+          for (int i = lane; i < n; i += 32) {
+            const float m = jn.w[i][warp], f = m == -INFINITY ? 0.f : ex2(m - mx);
+            jn.w[i][warp] = f;
+            sum += f * jn.l[i][warp];
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+          if (lane == 0) {
+            sh.mx[warp] = mx;
+            sh.sum[warp] = sum;
+          }
+        }
+        __syncthreads();
+        // two halves of the partials side by side, several loads in flight
+        const int f4 = tid % (kCols * kHeadDim / 4), col = f4 / (kHeadDim / 4);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = tid / (kCols * kHeadDim / 4); i < n; i += 2) {
+          const float f = jn.w[i][col];
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(slot(i)) + f4);
+          v.x = fmaf(f, x.x, v.x); v.y = fmaf(f, x.y, v.y);
+          v.z = fmaf(f, x.z, v.z); v.w = fmaf(f, x.w, v.w);
+        }
+        if (tid >= kCols * kHeadDim / 4) jn.half[f4] = v;
+        __syncthreads();
+        if (tid < kCols * kHeadDim / 4 && col < cols) {
+          const float4 x = jn.half[f4];
+          write_out(col, f4 % (kHeadDim / 4) * 4,
+                    make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w), sh.mx[col], sh.sum[col]);
+        }
       }
     }
     __syncthreads();  // the shared states are free again
@@ -460,6 +645,8 @@ int blocks_of(const sekv_config* cfg, int64_t n_q) {
   const int tpb = kCols / (cfg->n_q_heads / cfg->n_kv_heads);
   return int((n_q + tpb - 1) / tpb);
 }
+
+int attn_ctas() { return std::min(device_sm_count(), kMaxCtas); }  // one per SM
 
 struct Kv4Ws {
   size_t arrived, partials, total;
@@ -477,7 +664,7 @@ Kv4Ws kv4_ws(const sekv_config* cfg, int64_t n_q, int sms) {
 namespace sekv {
 
 size_t kv4_workspace_size(const sekv_config* cfg, int64_t n_q) {
-  const int sms = device_sm_count();
+  const int sms = attn_ctas();
   if (sms <= 0 || n_q < 1 || n_q > SEKV_MAX_QUERY_TOKENS || cfg->batch > SEKV_KV4_MAX_BATCH) return 0;
   return kv4_ws(cfg, n_q, sms).total;
 }
@@ -495,7 +682,7 @@ sekv_status kv4_check(const sekv_config* cfg, const sekv_kv4_cache* cache, int n
 }
 
 sekv_status kv4_check_ws(const sekv_config* cfg, int n_q, size_t workspace_bytes) {
-  const int sms = device_sm_count();
+  const int sms = attn_ctas();
   if (sms <= 0) return SEKV_ERR_CUDA;
   if (workspace_bytes < kv4_ws(cfg, n_q, sms).total) return SEKV_ERR_CAPACITY;
   return SEKV_OK;
@@ -516,7 +703,12 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
     return SEKV_ERR_INVALID;
   st = kv4_check_ws(cfg, n_q, workspace_bytes);
   if (st != SEKV_OK) return st;
-  const int sms = device_sm_count();
+  const int sms = attn_ctas();
+  // the kernel numbers chunks in 32 bits
+  if (int64_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * cache->max_pages *
+              (kKv4Page / kChunkTokens) > INT32_MAX / 2 ||
+      int64_t(cache->max_pages) * kKv4Page > INT32_MAX / 2)
+    return SEKV_ERR_UNSUPPORTED;
   const Kv4Ws L = kv4_ws(cfg, n_q, sms);
   uint8_t* w = static_cast<uint8_t*>(workspace);
   AttnParams P{};

@@ -7,8 +7,10 @@
 // in B) with one or two instructions per pair; no K or V value is rebuilt.  With
 // K^ = z + s n for each group of 64 dimensions,
 //   q . K^ = sum over groups of  s (sum_d q_d n_d) + z (sum_d q_d).
-// bf16 queries meet 128 + n (0x4300 | n, exact) and the 128 comes off by starting
-// the accumulators at -128 sum_d q_d; f16 queries meet n - 8.  For V,
+// Queries enter as f16, scaled by a power of two per column (exact for bf16 but for
+// elements below 2^-23 of the column's largest).  A word's low nibbles become
+// 1024 + n, less 1024; its high nibbles stay 1024 + 16 n against q / 16, and the 64 too
+// many come off by starting the accumulators at -64 sum q.  For V,
 //   sum_j p_j V^_j = sum_j (p_j s_j) (n_j - 8) + sum_j p_j (z_j + 8 s_j),
 // where the weight p_j s_j enters as the sum of two f16 numbers (22 significant
 // bits: one alone would cost the fp32 result 13 of its bits), scaled by a power of
@@ -23,7 +25,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -48,6 +49,11 @@ struct AttnShared {
   float l[kAttnWarps][kCols];
   float w[kAttnWarps][kCols];
   float mx[kCols], sum[kCols];
+  // the segment's queries: B operand, two 16-dimension steps a vector; per group of dimensions
+  // the sums of q and -64 times those of the odd dimensions; from a column's units to log2 of
+  // its weights
+  uint4 qb[4][32];
+  float q_sum[2][kCols], q_off[2][kCols], q_scale[kCols];
   uint64_t bar[kAttnWarps][kStages];
   int before[SEKV_KV4_MAX_BATCH + 1];  // chunks before each sequence
   int len[SEKV_KV4_MAX_BATCH];         // tokens of each sequence
@@ -72,26 +78,19 @@ struct AttnParams {
   float scale_log2;
 };
 
-// D = A B + C, 16 x 8 = 16 x 16 * 16 x 8 + 16 x 8
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                    const float (&c)[4], __nv_bfloat16) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+// D = A B + C in f16, 16 x 8 = 16 x 16 * 16 x 8 + 16 x 8
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
-        "f"(c[3]));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+        "f"(c3));
 }
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                    const float (&c)[4], __half) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
-        "f"(c[3]));
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  mma_f16(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
-
 // (w & MASK) | bits in one instruction: the compiler makes two of the plain form, whose
 // two constants do not fit one; `bits` stays in a register
 template <uint32_t MASK>
@@ -104,7 +103,7 @@ __device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t bits) {
 // 8x8 matrix of 16-bit values over the warp, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
@@ -124,12 +123,19 @@ __device__ __forceinline__ void centred(uint32_t w, uint32_t (&r)[4]) {
     r[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
 }
-// K's pairs as the queries' type meets them: 128 + n in bf16, n - 8 in f16
-__device__ __forceinline__ void k_codes(uint32_t w, uint32_t (&r)[4], __nv_bfloat16) {
+// K's pairs: n for the low nibbles (pairs 0 and 2), 1024 + 16 n for the high ones
+__device__ __forceinline__ void k_pairs(uint32_t w, uint32_t (&r)[4]) {
+  const uint32_t w8 = w >> 8;
+  const __half2 off = __half2half2(__ushort_as_half(0xe400));  // -1024
+  const uint32_t u[2] = {mask_or<0x000f000fu>(w, 0x64006400u), mask_or<0x000f000fu>(w8, 0x64006400u)};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = mask_or<0x000f000fu>(w >> (4 * i), 0x43004300u);
+  for (int i = 0; i < 2; ++i) {
+    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&u[i]), off);
+    r[2 * i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  r[1] = mask_or<0x00f000f0u>(w, 0x64006400u);
+  r[3] = mask_or<0x00f000f0u>(w8, 0x64006400u);
 }
-__device__ __forceinline__ void k_codes(uint32_t w, uint32_t (&r)[4], __half) { centred(w, r); }
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -141,12 +147,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t pack_pair(__nv_bfloat16 a, __nv_bfloat16 b) {
-  return uint32_t(__bfloat16_as_ushort(a)) | uint32_t(__bfloat16_as_ushort(b)) << 16;
-}
-__device__ __forceinline__ uint32_t pack_pair(__half a, __half b) {
-  return uint32_t(__half_as_ushort(a)) | uint32_t(__half_as_ushort(b)) << 16;
-}
 __device__ __forceinline__ float q_value(__nv_bfloat16 q) { return __bfloat162float(q); }
 __device__ __forceinline__ float q_value(__half q) { return __half2float(q); }
 
@@ -160,22 +160,68 @@ struct WarpState {
   float unit;      // power of two on the weights of o
 };
 
-// What one chunk needs beside the state.
+// B operand, sums and scale of the segment's columns into shared memory, by one warp; qv:
+// this lane's sixteen dimensions of either group of its column.
 template <typename T>
+__device__ __forceinline__ void put_queries(AttnShared& sh, const T (&qv)[32], int lane,
+                                            float scale_log2) {
+  float big = 0.f, sum[2] = {0.f, 0.f}, odd[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float x = q_value(qv[i]);
+    big = fmaxf(big, fabsf(x));
+    sum[i >> 4] += x;
+    if (i & 1) odd[i >> 4] += x;
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      sum[gr] += __shfl_xor_sync(~0u, sum[gr], o);
+      odd[gr] += __shfl_xor_sync(~0u, odd[gr], o);
+    }
+  }
+  // power of two that brings the largest element to 2^13 .. 2^14
+  const int e = min(max(int(__float_as_uint(big) >> 23) - 127, -110), 110);
+  const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+  if ((lane & 3) == 0) {
+    const int col = lane >> 2;
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      // an infinity among the queries makes the column NaN, as NaN does
+      sh.q_sum[gr][col] = big < INFINITY ? sum[gr] * up : NAN;
+      sh.q_off[gr][col] = odd[gr] * up * -64.f;
+    }
+    sh.q_scale[col] = __uint_as_float(uint32_t(127 - 13 + e) << 23) * scale_log2;
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    uint32_t w[4];  // pair i: dimensions i and i + 4 of the word's eight
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u = i & 1 ? up * 0.0625f : up;
+      const __half2 h = __floats2half2_rn(q_value(qv[8 * m + i]) * u, q_value(qv[8 * m + i + 4]) * u);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    sh.qb[m][lane] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The segment's queries as a lane keeps them: its columns are 2t and 2t + 1.
 struct Query {
-  uint32_t b[8][2];     // B operand of the eight 16-dimension steps
-  float sum[2][2];      // [column][group]: sum of q over the group's dimensions
-  float offset[2][4];   // [group]: what the accumulators start at (rows g and g + 8 x columns)
-  float scale_log2;
+  uint4 b[4];
+  float sum[2][2];     // [column][group]
+  float offset[2][2];
+  float scale_log2[2];
 };
 
 // EDGE: some token of the chunk is not seen by some column (seen: per column of the
 // lane; held: tokens of the chunk that the sequence has).
-template <typename T, bool EDGE>
-__device__ __forceinline__ void chunk_step(WarpState& S, const Query<T>& Q, const uint8_t* chunk,
+template <bool EDGE>
+__device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const uint8_t* chunk,
                                            int lane, int held, const int (&seen)[2]) {
   const int g = lane >> 2;
-  constexpr bool kOffset = std::is_same<T, __nv_bfloat16>::value;
   float x[2][2][2];  // tile, row half, column
 #pragma unroll
   for (int ti = 0; ti < 2; ++ti) {
@@ -184,32 +230,42 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query<T>& Q, cons
     const uint4 k0 = *reinterpret_cast<const uint4*>(tile + lane * 16);
     const uint4 k1 = *reinterpret_cast<const uint4*>(tile + 512 + lane * 16);
     const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+    // the groups' chains of products take turns
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      uint32_t r0[4], r1[4];
-      k_codes(w0[m], r0, T());
-      k_codes(w1[m], r1, T());
+    for (int i = 0; i < 2; ++i) {
+      uint32_t r0[2][4], r1[2][4];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t a[4] = {r0[2 * s], r1[2 * s], r0[2 * s + 1], r1[2 * s + 1]};
-        if ((m & 1) == 0 && s == 0)
-          mma(acc[m >> 1], a, Q.b[2 * m][0], Q.b[2 * m][1], Q.offset[m >> 1], T());
+      for (int gr = 0; gr < 2; ++gr) {
+        k_pairs(w0[2 * gr + i], r0[gr]);
+        k_pairs(w1[2 * gr + i], r1[gr]);
+      }
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        const uint32_t a[4] = {r0[gr][0], r1[gr][0], r0[gr][1], r1[gr][1]};
+        const uint4& q = Q.b[2 * gr + i];
+        if (i == 0)
+          mma_f16(acc[gr], a, q.x, q.y, Q.offset[0][gr], Q.offset[1][gr], Q.offset[0][gr],
+                  Q.offset[1][gr]);
         else
-          mma(acc[m >> 1], a, Q.b[2 * m + s][0], Q.b[2 * m + s][1], acc[m >> 1], T());
+          mma_f16(acc[gr], a, q.x, q.y);
+      }
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        const uint32_t a[4] = {r0[gr][2], r1[gr][2], r0[gr][3], r1[gr][3]};
+        mma_f16(acc[gr], a, Q.b[2 * gr + i].z, Q.b[2 * gr + i].w);
       }
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint2 sz = *reinterpret_cast<const uint2*>(tile + kKv4Params + 32 * (g >> 1) + 8 * (g & 1) + 16 * e);
       const float s0 = lo16(sz.x), s1 = lo16(sz.y);
-      const float z0 = kOffset ? hi16(sz.x) : fmaf(8.f, s0, hi16(sz.x));
-      const float z1 = kOffset ? hi16(sz.y) : fmaf(8.f, s1, hi16(sz.y));
+      const float z0 = hi16(sz.x), z1 = hi16(sz.y);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float y = s0 * acc[0][2 * e + c];
         y = fmaf(z0, Q.sum[c][0], y);
         y = fmaf(s1, acc[1][2 * e + c], y);
-        y = fmaf(z1, Q.sum[c][1], y) * Q.scale_log2;
+        y = fmaf(z1, Q.sum[c][1], y);
         x[ti][e][c] = !EDGE || ti * 16 + e * 8 + g < seen[c] ? y : -INFINITY;
       }
     }
@@ -246,6 +302,8 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query<T>& Q, cons
     }
     top = __reduce_max_sync(~0u, top);
   }
+  mx[0] *= Q.scale_log2[0];
+  mx[1] *= Q.scale_log2[1];
   // largest unit with top * unit < 2^15 (f16 ends at 65504)
   const float unit = __uint_as_float(min(254u, 268u - max(14u, top >> 7)) << 23);
   const bool up = mx[0] > S.m[0] || mx[1] > S.m[1];
@@ -281,7 +339,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query<T>& Q, cons
       float p[2], w[2][2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        p[c] = ex2(x[ti][e][c] - m0[c]);
+        p[c] = ex2(fmaf(x[ti][e][c], Q.scale_log2[c], -m0[c]));
         S.l[c] += p[c];
       }
 #pragma unroll
@@ -309,12 +367,11 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query<T>& Q, cons
       uint32_t r0[4], r1[4];
       centred(w0[m], r0);
       centred(w1[m], r1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t a[4] = {r0[i], r0[i + 2], r1[i], r1[i + 2]};
-        mma(S.o[2 * m + i], a, bh[m >> 1][0], bh[m >> 1][1], S.o[2 * m + i], __half());
-        mma(S.o[2 * m + i], a, bl[m >> 1][0], bl[m >> 1][1], S.o[2 * m + i], __half());
-      }
+      const uint32_t a0[4] = {r0[0], r0[2], r1[0], r1[2]}, a1[4] = {r0[1], r0[3], r1[1], r1[3]};
+      mma_f16(S.o[2 * m], a0, bh[m >> 1][0], bh[m >> 1][1]);
+      mma_f16(S.o[2 * m + 1], a1, bh[m >> 1][0], bh[m >> 1][1]);
+      mma_f16(S.o[2 * m], a0, bl[m >> 1][0], bl[m >> 1][1]);
+      mma_f16(S.o[2 * m + 1], a1, bl[m >> 1][0], bl[m >> 1][1]);
     }
   }
 }
@@ -383,6 +440,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     const int blk = gi / P.pg.hkv, head = gi - blk * P.pg.hkv;
     const int cols = min(P.tpb, P.n_q - blk * P.tpb) * P.hpg;
 
+    // The queries' loads go out first: behind the copies they would wait for them.
+    const int tok = blk * P.tpb + g / P.hpg;  // of this lane's column of the B operand
+    union {
+      uint4 w[4];   // sixteen dimensions of either group
+      T e[32];
+    } qv;
+    {
+      const T* q = static_cast<const T*>(P.q) +
+                   ((int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + g % P.hpg) * kHeadDim;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        qv.w[i] = warp == 0 && g < cols ? __ldg(reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + t * 16) + (i & 1))
+                           : make_uint4(0, 0, 0, 0);
+    }
+
     // This warp's k-th chunk of the segment is c0 + warp + kAttnWarps k.  Lane i
     // looks up the page of chunk 32 j + i; -1 where there is none to copy.
     const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kAttnWarps - 1) / kAttnWarps : 0;
@@ -420,53 +492,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     };
     for (int k = 0; k < min(mine, kStages); ++k) issue(k);
 
-    Query<T> Q;
-    Q.scale_log2 = P.scale_log2;
+    if (warp == 0) put_queries<T>(sh, qv.e, lane, P.scale_log2);
+    __syncthreads();
+    Query Q;
     int see[2];  // tokens that columns 2t and 2t + 1 see
-    {
-      const int tok = blk * P.tpb + g / P.hpg;  // this lane's column of the B operand
-      const T* q = static_cast<const T*>(P.q) +
-                   ((int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + g % P.hpg) * kHeadDim;
-      float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < 4; ++m) Q.b[m] = sh.qb[m][lane];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = 2 * t + c;
 #pragma unroll
       for (int gr = 0; gr < 2; ++gr) {
-        // the lane's sixteen dimensions of the group, as two vectors
-        union {
-          uint4 w[2];
-          T e[16];
-        } v;
-        v.w[0] = v.w[1] = make_uint4(0, 0, 0, 0);
-        if (g < cols) {
-          const uint4* src = reinterpret_cast<const uint4*>(q + gr * 64 + t * 16);
-          v.w[0] = __ldg(src);
-          v.w[1] = __ldg(src + 1);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[gr] += q_value(v.e[i]);
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int d = (s >> 1) * 8 + (s & 1) * 2 + e;
-            Q.b[gr * 4 + s][e] = pack_pair(v.e[d], v.e[d + 4]);
-          }
+        Q.sum[c][gr] = sh.q_sum[gr][col];
+        Q.offset[c][gr] = sh.q_off[gr][col];
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) sum[i] += __shfl_xor_sync(~0u, sum[i], o);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          Q.sum[c][i] = __shfl_sync(~0u, sum[i], (2 * t + c) * 4);
-          Q.offset[i][c] = Q.offset[i][2 + c] =
-              std::is_same<T, __nv_bfloat16>::value ? -128.f * Q.sum[c][i] : 0.f;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = 2 * t + c;
-        see[c] = col < cols ? len - (P.n_q - 1 - (blk * P.tpb + col / P.hpg)) : 0;
-      }
+      Q.scale_log2[c] = sh.q_scale[col];
+      see[c] = col < cols ? len - (P.n_q - 1 - (blk * P.tpb + col / P.hpg)) : 0;
     }
     // up to here no token is hidden from any column in use
     const int open = len - (P.n_q - 1 - blk * P.tpb);
@@ -491,9 +532,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
           const int held = len - pos;
           const int seen[2] = {see[0] - pos, see[1] - pos};
           if (pos + kChunkTokens <= open)
-            chunk_step<T, false>(S, Q, sh.ring[warp][st], lane, held, seen);
+            chunk_step<false>(S, Q, sh.ring[warp][st], lane, held, seen);
           else
-            chunk_step<T, true>(S, Q, sh.ring[warp][st], lane, held, seen);
+            chunk_step<true>(S, Q, sh.ring[warp][st], lane, held, seen);
         } else {
           // a copy did not land: nothing more is copied or waited for by this warp, and
           // what is still in flight gets its time to land before the CTA may end
@@ -699,7 +740,8 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
   sekv_status st = kv4_check(cfg, cache, n_q, workspace);
   if (st != SEKV_OK) return st;
   if (dtype != SEKV_BF16 && dtype != SEKV_F16) return SEKV_ERR_INVALID;
-  if (!q || !seq_len || !out || !aligned16(q) || !aligned16(out) || !isfinite(scale))
+  if (!q || !seq_len || !out || !aligned16(q) || !aligned16(out) || !isfinite(scale) ||
+      !(scale > 0.f))
     return SEKV_ERR_INVALID;
   st = kv4_check_ws(cfg, n_q, workspace_bytes);
   if (st != SEKV_OK) return st;

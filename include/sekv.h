@@ -745,6 +745,7 @@ sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cache* cache, i
  * queries among them: query i attends to the first seq_len[b] - (n_q - 1 - i)
  * tokens.  A query that sees none has out 0 and lse -inf.
  *   q    bf16 or f16 [batch][n_q][n_q_heads][128], n_q 1 .. SEKV_MAX_QUERY_TOKENS
+ *   scale  logit scale, > 0
  *   out  f32 [batch][n_q][n_q_heads][128];  lse f32 [batch][n_q][n_q_heads] (natural
  *        log; may be NULL)
  * The (token, head) pairs of a KV head are taken eight at a time in one pass over

@@ -224,7 +224,8 @@ def test_kv4_refusals(libsekv):
     # what does not depend on the GPU's size is refused before the workspace is looked at
     for f, kw in ((append, dict(dt=2)), (append, dict(k=None)), (append, dict(k=ODD)), (append, dict(n=-1)), (append, dict(first=None)),
                   (append, dict(ks=(ctypes.c_int64 * 3)(4, 8, 8))), (read, dict(dt=3)), (read, dict(k=None)), (read, dict(n=-1)),
-                  (attn, dict(dt=2)), (attn, dict(q=None)), (attn, dict(q=ODD)), (attn, dict(scale=math.nan))):
+                  (attn, dict(dt=2)), (attn, dict(q=None)), (attn, dict(q=ODD)), (attn, dict(scale=math.nan)),
+                  (attn, dict(scale=0.0)), (attn, dict(scale=-0.1)), (attn, dict(scale=math.inf))):
         assert f(**kw) == INVALID, kw
 
 

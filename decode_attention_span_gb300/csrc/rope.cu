@@ -29,7 +29,7 @@ struct RopeHeads {
   const void* x;
   void* y;
   int64_t xs[3], ys[3];
-  int n;
+  int n, zero_padding;
 };
 
 struct RopeParams {
@@ -38,7 +38,7 @@ struct RopeParams {
   const void* pos;
   int64_t pos_stride_b;
   float mscale;
-  int pos64, backward, zero_padding;
+  int pos64, backward;
   int rot, dim;            // rotated dimensions, all dimensions
   int nrot, nvec;          // work items of a token: rotated ones, all
   int tok_per_block;
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) 
   const int64_t pos = P.pos64 ? static_cast<const int64_t*>(P.pos)[pi]
                               : int64_t(static_cast<const int32_t*>(P.pos)[pi]);
   const bool pad = pos < 0;
-  if (pad && !P.zero_padding) return;
+  if (pad && !P.q.zero_padding && !P.k.zero_padding) return;
   const bool rotated = vec < P.nrot;
   const int half = P.rot >> 1;
   float cs[NP], sn[NP];
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) 
         T* y = static_cast<T*>(H.y) + b * H.ys[0] + t * H.ys[1] + hh * H.ys[2] + d0;
         if (pad) {
           a[i].w = c[i].w = typename Word<N * int(sizeof(T))>::type();
-          dst[i] = y;
+          dst[i] = H.zero_padding ? y : nullptr;
         } else if (rotated || x != y) {
           dst[i] = y;
           a[i].w = *reinterpret_cast<const decltype(a[i].w)*>(x);
@@ -211,6 +211,7 @@ RopeHeads kernel_heads(const sekv_heads* h) {
   r.x = h->x;
   r.y = h->y;
   r.n = h->n_heads;
+  r.zero_padding = h->zero_padding != 0;
   for (int i = 0; i < 3; ++i) {
     r.xs[i] = h->x_stride[i];
     r.ys[i] = h->y_stride[i];
@@ -266,7 +267,7 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
   sekv_status why;
   if (!rope_ok(r, &why)) return why;
   if (dtype < SEKV_BF16 || dtype > SEKV_F32 || head_dim < r->rot_dim || batch < 0 || n_tokens < 0 ||
-      !freqs || !positions || (!q && !k) || (flags & ~(SEKV_ROPE_BACKWARD | SEKV_ROPE_ZERO_PADDING)) || !isfinite(mscale))
+      !freqs || !positions || (!q && !k) || (flags & ~SEKV_ROPE_BACKWARD) || !isfinite(mscale))
     return SEKV_ERR_INVALID;
   if (head_dim > 1024 || batch > INT32_MAX || n_tokens > INT32_MAX ||
       batch * n_tokens > INT32_MAX)
@@ -308,7 +309,6 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
   P.mscale = mscale;
   P.pos64 = positions_64 != 0;
   P.backward = (flags & SEKV_ROPE_BACKWARD) != 0;
-  P.zero_padding = (flags & SEKV_ROPE_ZERO_PADDING) != 0;
   P.rot = r->rot_dim;
   P.dim = head_dim;
   const int pairs = r->interleaved ? (n > 1 ? n / 2 : 1) : n;

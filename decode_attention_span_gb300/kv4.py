@@ -7,7 +7,8 @@ import ctypes
 
 import torch
 
-from .sekv import DTYPES, Config, Workspace, _check, _ptr, _stream, check_tensor, lib
+from .sekv import (DTYPES, Config, Workspace, _check, check_tensor, lib, on_current_device,
+                   raw_stream)
 
 PAGE_TOKENS = 64
 PAGE_BYTES = 9216
@@ -32,6 +33,7 @@ class Kv4Cache:
 
     def __init__(self, cfg: Config, pages: torch.Tensor, page_table: torch.Tensor):
         dev = pages.device
+        on_current_device(dev)
         check_tensor(pages, "pages", (torch.uint8,), dev)
         check_tensor(page_table, "page_table", (torch.int32,), dev)
         if (pages.dim() != 3 or pages.shape[1:] != (cfg.n_kv_heads, PAGE_BYTES) or
@@ -44,19 +46,24 @@ class Kv4Cache:
                              f"{tuple(page_table.shape)}")
         self.pages, self.page_table, self.device = pages, page_table, dev
         self.batch, self.n_kv_heads = cfg.batch, cfg.n_kv_heads
-        self._c = SekvKv4Cache(pages.data_ptr(), page_table.data_ptr(), pages.shape[0],
-                               page_table.shape[1])
+        self._struct = SekvKv4Cache(pages.data_ptr(), page_table.data_ptr(), pages.shape[0],
+                                    page_table.shape[1])
+        self._c = ctypes.byref(self._struct)
 
 
-def _common(cfg, cache, ws):
-    if (cfg.batch, cfg.n_kv_heads) != (cache.batch, cache.n_kv_heads):
+def _common(cfg, cache, ws) -> int:
+    if cfg.batch != cache.batch or cfg.n_kv_heads != cache.n_kv_heads:
         raise ValueError("cache: made for another batch or number of KV heads")
     if ws.buf.device != cache.device:
         raise ValueError(f"workspace: on {ws.buf.device}, cache on {cache.device}")
+    return on_current_device(cache.device)
+
+
+_I32 = (torch.int32,)
 
 
 def _per_seq(t, name, cfg, dev):
-    check_tensor(t, name, (torch.int32,), dev)
+    check_tensor(t, name, _I32, dev)
     if t.shape != (cfg.batch,) or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous [{cfg.batch}], got {tuple(t.shape)}")
     return t.data_ptr()
@@ -65,28 +72,32 @@ def _per_seq(t, name, cfg, dev):
 _Stride = ctypes.c_int64 * 3
 
 
+def _rows(x, name, dtypes, cfg, n, dev):
+    check_tensor(x, name, dtypes, dev)
+    s = x.stride()
+    if x.shape != (cfg.batch, n, cfg.n_kv_heads, 128) or s[3] != 1:
+        raise ValueError(f"{name}: expected [{cfg.batch}][T][{cfg.n_kv_heads}][128] with "
+                         f"consecutive elements in a head, got {tuple(x.shape)}")
+    return _Stride(s[0], s[1], s[2])
+
+
 def kv4_append(cfg: Config, cache: Kv4Cache, k, v, first, ws: Workspace, n_valid=None,
                stream=None):
     """Stores k and v [B][T][Hkv][128] (bf16 or f16; any strides that are multiples of
     8 with the last one 1) at token positions first[b] .. first[b] + T - 1 of each
     sequence; with n_valid [B], only its first n_valid[b] rows."""
-    _common(cfg, cache, ws)
+    index = _common(cfg, cache, ws)
     dev = cache.device
-    check_tensor(k, "k", _HALF, dev)
-    check_tensor(v, "v", (k.dtype,), dev)
-    for name, x in (("k", k), ("v", v)):
-        if (x.dim() != 4 or x.shape != (cfg.batch, k.shape[1], cfg.n_kv_heads, 128) or
-                x.stride(3) != 1):
-            raise ValueError(f"{name}: expected [{cfg.batch}][T][{cfg.n_kv_heads}][128], got "
-                             f"{tuple(x.shape)}")
+    T = k.shape[1] if k.dim() == 4 else 0
+    ks = _rows(k, "k", _HALF, cfg, T, dev)
+    vs = _rows(v, "v", (k.dtype,), cfg, T, dev)
     f = _per_seq(first, "first", cfg, dev)
     n = None if n_valid is None else _per_seq(n_valid, "n_valid", cfg, dev)
-    c = cfg.c()
-    _check("sekv_kv4_append",
-           lib().sekv_kv4_append(ctypes.byref(c), ctypes.byref(cache._c), DTYPES[k.dtype],
-                                 k.data_ptr(), _Stride(*k.stride()[:3]), v.data_ptr(),
-                                 _Stride(*v.stride()[:3]), k.shape[1], f, n, ws.ptr(), ws.nbytes,
-                                 _stream(stream)))
+    st = lib().sekv_kv4_append(ctypes.byref(cfg.c()), cache._c, DTYPES[k.dtype], k.data_ptr(), ks,
+                               v.data_ptr(), vs, T, f, n, ws.buf.data_ptr(), ws.nbytes,
+                               raw_stream(stream, index))
+    if st != 0:
+        _check("sekv_kv4_append", st)
 
 
 def kv4_read(cfg: Config, cache: Kv4Cache, first, n_tokens: int, ws: Workspace,
@@ -94,25 +105,29 @@ def kv4_read(cfg: Config, cache: Kv4Cache, first, n_tokens: int, ws: Workspace,
     """K and V [B][Hkv][n_tokens][128] that the tokens first[b] .. first[b] + n_tokens - 1
     stand for, rounded to dtype (bf16, f16 or f32).  With n_valid [B], rows from
     n_valid[b] on stay as they were (zero in outputs made here)."""
-    _common(cfg, cache, ws)
+    index = _common(cfg, cache, ws)
     dev = cache.device
     shape = (cfg.batch, cfg.n_kv_heads, n_tokens, 128)
+    n = None
+    if n_valid is not None:
+        n = _per_seq(n_valid, "n_valid", cfg, dev)
     if out is None:
-        k, v = torch.zeros((2, *shape), dtype=dtype, device=dev).unbind(0)
+        if dtype not in DTYPES:
+            raise TypeError(f"dtype: expected one of {list(DTYPES)}, got {dtype}")
+        make = torch.empty if n is None else torch.zeros
+        k, v = make(shape, dtype=dtype, device=dev), make(shape, dtype=dtype, device=dev)
     else:
         k, v = out
-        check_tensor(k, "out[0]", tuple(DTYPES), dev)
+        check_tensor(k, "out[0]", DTYPES, dev)
         check_tensor(v, "out[1]", (k.dtype,), dev)
         if k.shape != shape or v.shape != shape or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError(f"out: expected contiguous {shape}")
     f = _per_seq(first, "first", cfg, dev)
-    n = None if n_valid is None else _per_seq(n_valid, "n_valid", cfg, dev)
-    c = cfg.c()
-    if n_tokens > 0:
-        _check("sekv_kv4_read",
-               lib().sekv_kv4_read(ctypes.byref(c), ctypes.byref(cache._c), DTYPES[k.dtype],
-                                   k.data_ptr(), v.data_ptr(), n_tokens, f, n, ws.ptr(),
-                                   ws.nbytes, _stream(stream)))
+    st = lib().sekv_kv4_read(ctypes.byref(cfg.c()), cache._c, DTYPES[k.dtype], k.data_ptr(),
+                             v.data_ptr(), n_tokens, f, n, ws.buf.data_ptr(), ws.nbytes,
+                             raw_stream(stream, index))
+    if st != 0:
+        _check("sekv_kv4_read", st)
     return k, v
 
 
@@ -121,27 +136,27 @@ def kv4_attention(cfg: Config, cache: Kv4Cache, q, seq_len, scale: float, ws: Wo
     """Attention of q [B][n_q][Hq][128] (bf16 or f16) over the first seq_len[b] cached
     tokens of each sequence, the query tokens being its last n_q; returns out
     [B][n_q][Hq][128] f32 and lse [B][n_q][Hq] f32."""
-    _common(cfg, cache, ws)
+    index = _common(cfg, cache, ws)
     dev = cache.device
     check_tensor(q, "q", _HALF, dev)
-    if q.dim() != 4 or q.shape[0] != cfg.batch or q.shape[2:] != (cfg.n_q_heads, 128) or \
-            not q.is_contiguous():
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != cfg.batch or shape[2] != cfg.n_q_heads or \
+            shape[3] != 128 or not q.is_contiguous():
         raise ValueError(f"q: expected contiguous [{cfg.batch}][n_q][{cfg.n_q_heads}][128], got "
-                         f"{tuple(q.shape)}")
-    n_q = q.shape[1]
-    for name, t, shape in (("out", out, q.shape), ("lse", lse, q.shape[:3])):
+                         f"{tuple(shape)}")
+    for name, t, want in (("out", out, shape), ("lse", lse, shape[:3])):
         if t is not None:
             check_tensor(t, name, (torch.float32,), dev)
-            if t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"{name}: expected contiguous {tuple(shape)}")
+            if t.shape != want or not t.is_contiguous():
+                raise ValueError(f"{name}: expected contiguous {tuple(want)}")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
     s = _per_seq(seq_len, "seq_len", cfg, dev)
-    c = cfg.c()
-    _check("sekv_kv4_attention",
-           lib().sekv_kv4_attention(ctypes.byref(c), ctypes.byref(cache._c), DTYPES[q.dtype],
-                                    q.data_ptr(), n_q, s, scale, out.data_ptr(), lse.data_ptr(),
-                                    ws.ptr(), ws.nbytes, _stream(stream)))
+    st = lib().sekv_kv4_attention(ctypes.byref(cfg.c()), cache._c, DTYPES[q.dtype], q.data_ptr(),
+                                  shape[1], s, scale, out.data_ptr(), lse.data_ptr(),
+                                  ws.buf.data_ptr(), ws.nbytes, raw_stream(stream, index))
+    if st != 0:
+        _check("sekv_kv4_attention", st)
     return out, lse

@@ -7,7 +7,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .sekv import DTYPES, Workspace, _check, _ptr, _stream, check_tensor, lib
+from .sekv import DTYPES, Workspace, _check, check_tensor, lib, on_current_device, raw_stream
 
 
 class TokenLogprobs(NamedTuple):
@@ -18,25 +18,31 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: Optional[torch.Tensor]   # f32 [...][n_top]
 
 
-def _rows(logits, tokens):
-    """(batch, rows of a sequence, strides of logits and tokens) of [T][V] or [B][T][V] logits."""
-    if logits.dim() not in (2, 3) or logits.stride(-1) != 1:
+_IDS = (torch.int32, torch.int64)
+
+
+def _rows(logits, tokens, ws):
+    """(device, device index, type, batch, rows of a sequence, vocabulary, strides of logits,
+    stride of tokens) of [T][V] or [B][T][V] logits."""
+    dtype = DTYPES.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"logits: expected one of {list(DTYPES)}, got {logits.dtype}")
+    dev = logits.device
+    index = on_current_device(dev)
+    shape, ls = logits.shape, logits.stride()
+    if len(shape) not in (2, 3) or ls[-1] != 1:
         raise ValueError(f"logits: expected [T][V] or [B][T][V] with consecutive entries, got "
-                         f"{tuple(logits.shape)}")
-    check_tensor(logits, "logits", tuple(DTYPES), logits.device)
-    check_tensor(tokens, "tokens", (torch.int32, torch.int64), logits.device)
-    if tokens.shape != logits.shape[:-1] or (tokens.shape[-1] > 1 and tokens.stride(-1) != 1):
-        raise ValueError(f"tokens: expected {tuple(logits.shape[:-1])} with consecutive entries, "
-                         f"got {tuple(tokens.shape)}")
-    if logits.dim() == 2:
-        return 1, logits.shape[0], 0, logits.stride(0), 0
-    return (logits.shape[0], logits.shape[1], logits.stride(0), logits.stride(1),
-            tokens.stride(0))
-
-
-def _check_ws(ws, dev):
+                         f"{tuple(shape)}")
+    check_tensor(tokens, "tokens", _IDS, dev)
+    ts = tokens.stride()
+    if tokens.shape != shape[:-1] or (shape[-2] > 1 and ts[-1] != 1):
+        raise ValueError(f"tokens: expected {tuple(shape[:-1])} with consecutive entries, got "
+                         f"{tuple(tokens.shape)}")
     if ws.buf.device != dev:
         raise ValueError(f"workspace: on {ws.buf.device}, tensors on {dev}")
+    if len(shape) == 2:
+        return dev, index, dtype, 1, shape[0], shape[1], 0, ls[0], 0
+    return dev, index, dtype, shape[0], shape[1], shape[2], ls[0], ls[1], ts[0]
 
 
 def token_logprobs(logits, tokens, ws: Workspace, n_top: int = 0, scale: float = 1.0,
@@ -45,24 +51,26 @@ def token_logprobs(logits, tokens, ws: Workspace, n_top: int = 0, scale: float =
     ([T][V] or [B][T][V]; bf16, f16 or f32) times `scale` (1 / temperature), with
     log-sum-exp and entropy (entropy=False: neither) and the n_top (at most 32)
     likeliest tokens.  `ws` is any workspace: bad token ids go to its status."""
-    B, T, sb, st, tb = _rows(logits, tokens)
-    dev = logits.device
-    _check_ws(ws, dev)
+    dev, index, dtype, B, T, V, sb, st, tb = _rows(logits, tokens, ws)
     shape = tokens.shape
-    lp = torch.empty(shape, dtype=torch.float32, device=dev)
+    f32 = torch.float32
+    lp = torch.empty(shape, dtype=f32, device=dev)
     lse = ent = ids = tlp = None
+    p_lse = p_ent = p_ids = p_tlp = None
     if entropy:
-        lse, ent = torch.empty((2, *shape), dtype=torch.float32, device=dev).unbind(0)
+        lse, ent = torch.empty(shape, dtype=f32, device=dev), torch.empty(shape, dtype=f32, device=dev)
+        p_lse, p_ent = lse.data_ptr(), ent.data_ptr()
     if n_top > 0:
         ids = torch.empty((*shape, n_top), dtype=torch.int32, device=dev)
-        tlp = torch.empty((*shape, n_top), dtype=torch.float32, device=dev)
-    if lp.numel():
-        _check("sekv_token_logprobs",
-               lib().sekv_token_logprobs(logits.data_ptr(), DTYPES[logits.dtype], B, T,
-                                         logits.shape[-1], sb, st, tokens.data_ptr(),
-                                         tokens.dtype == torch.int64, tb, scale, n_top,
-                                         lp.data_ptr(), _ptr(lse), _ptr(ent), _ptr(ids),
-                                         _ptr(tlp), ws.ptr(), ws.nbytes, _stream(stream)))
+        tlp = torch.empty((*shape, n_top), dtype=f32, device=dev)
+        p_ids, p_tlp = ids.data_ptr(), tlp.data_ptr()
+    if B * T > 0:
+        err = lib().sekv_token_logprobs(logits.data_ptr(), dtype, B, T, V, sb, st,
+                                        tokens.data_ptr(), tokens.dtype == torch.int64, tb, scale,
+                                        n_top, lp.data_ptr(), p_lse, p_ent, p_ids, p_tlp,
+                                        ws.buf.data_ptr(), ws.nbytes, raw_stream(stream, index))
+        if err != 0:
+            _check("sekv_token_logprobs", err)
     return TokenLogprobs(lp, lse, ent, ids, tlp)
 
 
@@ -71,19 +79,17 @@ def surprisal(logits, tokens, ws: Workspace, out=None, stream=None):
     each token given those before it, 0 for the first; what build_spans takes."""
     if logits.dim() != 3:
         raise ValueError(f"logits: expected [B][T][V], got {tuple(logits.shape)}")
-    B, T, sb, st, tb = _rows(logits, tokens)
-    dev = logits.device
-    _check_ws(ws, dev)
+    dev, index, dtype, B, T, V, sb, st, tb = _rows(logits, tokens, ws)
     if out is None:
         out = torch.empty(B, T, dtype=torch.float32, device=dev)
     else:
         check_tensor(out, "out", (torch.float32,), dev)
         if out.shape != (B, T) or not out.is_contiguous():
             raise ValueError(f"out: expected contiguous [{B}][{T}], got {tuple(out.shape)}")
-    if out.numel():
-        _check("sekv_surprisal",
-               lib().sekv_surprisal(logits.data_ptr(), DTYPES[logits.dtype], B, T,
-                                    logits.shape[-1], sb, st, tokens.data_ptr(),
-                                    tokens.dtype == torch.int64, tb, out.data_ptr(), ws.ptr(),
-                                    ws.nbytes, _stream(stream)))
+    if B * T > 0:
+        err = lib().sekv_surprisal(logits.data_ptr(), dtype, B, T, V, sb, st, tokens.data_ptr(),
+                                   tokens.dtype == torch.int64, tb, out.data_ptr(),
+                                   ws.buf.data_ptr(), ws.nbytes, raw_stream(stream, index))
+        if err != 0:
+            _check("sekv_surprisal", err)
     return out

@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from .sekv import DTYPES, _check, _ptr, _stream, check_tensor, lib
+from .sekv import DTYPES, _check, _ptr, check_tensor, lib, on_current_device, raw_stream
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "banded": 4}
 
@@ -20,10 +20,8 @@ class SekvRopeConfig(ctypes.Structure):
                 ("attention_factor", ctypes.c_double)]
 
 
-class SekvHeads(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("n_heads", ctypes.c_int32),
-                ("reserved", ctypes.c_int32), ("x_stride", ctypes.c_int64 * 3),
-                ("y_stride", ctypes.c_int64 * 3)]
+# sekv_heads as nine 64-bit words: x, y, n_heads | zero_padding << 32, strides of x and of y
+SekvHeads = ctypes.c_int64 * 9
 
 
 def rope_config(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
@@ -61,17 +59,39 @@ class RopePlan:
                  scaling: str = "none", factor: float = 1.0, original_context: int = 8192,
                  beta_fast: float = 32.0, beta_slow: float = 1.0, low_freq_factor: float = 1.0,
                  high_freq_factor: float = 4.0, attention_factor: float = 0.0, device=None):
-        self._c = rope_config(rot_dim, base, interleaved, scaling, factor, original_context,
-                              beta_fast, beta_slow, low_freq_factor, high_freq_factor,
-                              attention_factor)
-        freqs, self.mscale = rope_freqs(self._c)
+        config = rope_config(rot_dim, base, interleaved, scaling, factor, original_context,
+                             beta_fast, beta_slow, low_freq_factor, high_freq_factor,
+                             attention_factor)
+        freqs, self.mscale = rope_freqs(config)
+        self.config, self._c = config, ctypes.byref(config)
         self.rot_dim = int(rot_dim)
         self.freqs = freqs.to(device or "cuda")
+        self.freqs_ptr = self.freqs.data_ptr()
 
 
-def _heads(x, y):
-    xs, ys = x.stride(), y.stride()
-    return SekvHeads(x.data_ptr(), y.data_ptr(), x.shape[2], 0, xs[:3], ys[:3])
+_POSITIONS = (torch.int32, torch.int64)
+
+
+def _heads(name, x, y, shape, dtype, dev):
+    """(sekv_heads, output) of one tensor; an output made here is zero at padding."""
+    if x.dtype != dtype or x.device != dev:
+        check_tensor(x, name, (dtype,), dev)
+    s, xs = x.shape, x.stride()
+    if len(s) != 4 or s[0] != shape[0] or s[1] != shape[1] or s[3] != shape[2] or xs[3] != 1:
+        raise ValueError(f"{name}: expected [{shape[0]}][{shape[1]}][heads][{shape[2]}] with "
+                         f"consecutive elements in a head, got {tuple(x.shape)}")
+    n = s[2]
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        n += 1 << 32
+        ys = y.stride()
+    else:
+        if y.dtype != dtype or y.device != dev:
+            check_tensor(y, name + "_out", (dtype,), dev)
+        ys = y.stride()
+        if y.shape != s or ys[3] != 1:
+            raise ValueError(f"{name}_out: expected shape {tuple(s)}, got {tuple(y.shape)}")
+    return SekvHeads(x.data_ptr(), y.data_ptr(), n, xs[0], xs[1], xs[2], ys[0], ys[1], ys[2]), y
 
 
 def rope(plan: RopePlan, q, k, positions, q_out=None, k_out=None, backward: bool = False,
@@ -87,37 +107,34 @@ def rope(plan: RopePlan, q, k, positions, q_out=None, k_out=None, backward: bool
     x0 = q if q is not None else k
     if x0 is None:
         raise ValueError("rope: q or k is needed")
-    dev = x0.device
+    dev, dtype = x0.device, x0.dtype
+    index = on_current_device(dev)
+    if dtype not in DTYPES or x0.dim() != 4:
+        raise TypeError(f"rope: expected [B][T][heads][D] of {list(DTYPES)}, got {x0.dtype} "
+                        f"{tuple(x0.shape)}")
     B, T, _, D = x0.shape
     if D < plan.rot_dim:
         raise ValueError(f"rope: heads of {D} dimensions, plan rotates {plan.rot_dim}")
     if plan.freqs.device != dev:
         raise ValueError(f"plan: on {plan.freqs.device}, tensors on {dev}")
-    check_tensor(positions, "positions", (torch.int32, torch.int64), dev)
-    if positions.shape not in ((T,), (B, T)) or (T > 1 and positions.stride(-1) != 1):
+    check_tensor(positions, "positions", _POSITIONS, dev)
+    ps = positions.stride()
+    if positions.shape == (B, T):
+        pos_stride = ps[0]
+    elif positions.shape == (T,):
+        pos_stride = 0
+    else:
         raise ValueError(f"positions: expected [{T}] or [{B}][{T}], got {tuple(positions.shape)}")
-    heads = []
-    outs = []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            heads.append(None)
-            outs.append(None)
-            continue
-        check_tensor(x, name, (x0.dtype,), dev)
-        if x.dim() != 4 or x.shape[0] != B or x.shape[1] != T or x.shape[3] != D or x.stride(3) != 1:
-            raise ValueError(f"{name}: expected [{B}][{T}][heads][{D}], got {tuple(x.shape)}")
-        if y is None:
-            y = torch.zeros_like(x, memory_format=torch.contiguous_format)
-        else:
-            check_tensor(y, name + "_out", (x0.dtype,), dev)
-            if y.shape != x.shape or y.stride(3) != 1:
-                raise ValueError(f"{name}_out: expected shape {tuple(x.shape)}, got {tuple(y.shape)}")
-        heads.append(ctypes.byref(_heads(x, y)))
-        outs.append(y)
-    _check("sekv_rope",
-           lib().sekv_rope(ctypes.byref(plan._c), plan.freqs.data_ptr(), plan.mscale,
-                           DTYPES[x0.dtype], D, B, T, positions.data_ptr(),
-                           positions.dtype == torch.int64,
-                           positions.stride(0) if positions.dim() == 2 else 0, heads[0], heads[1],
-                           1 if backward else 0, _stream(stream)))
-    return outs[0], outs[1]
+    if T > 1 and ps[-1] != 1:
+        raise ValueError("positions: must be consecutive along a sequence")
+    qh = kh = None
+    if q is not None:
+        qh, q_out = _heads("q", q, q_out, (B, T, D), dtype, dev)
+    if k is not None:
+        kh, k_out = _heads("k", k, k_out, (B, T, D), dtype, dev)
+    st = lib().sekv_rope(plan._c, plan.freqs_ptr, plan.mscale, DTYPES[dtype], D, B, T,
+                         positions.data_ptr(), positions.dtype == torch.int64, pos_stride, qh, kh,
+                         1 if backward else 0, raw_stream(stream, index))
+    if st != 0:
+        _check("sekv_rope", st)
+    return q_out, k_out

@@ -652,13 +652,12 @@ typedef struct sekv_heads {
   const void* x;
   void* y;
   int32_t n_heads;
-  int32_t reserved;
+  int32_t zero_padding;  /* 1: outputs of padding tokens are set to 0; 0: left as they were */
   int64_t x_stride[3];
   int64_t y_stride[3];
 } sekv_heads;
 
 #define SEKV_ROPE_BACKWARD 1
-#define SEKV_ROPE_ZERO_PADDING 2
 
 /*
  * sekv_rope -- rotates queries and keys of [batch][n_tokens] tokens in one
@@ -667,11 +666,10 @@ typedef struct sekv_heads {
  *   freqs     device, from sekv_rope_freqs; mscale likewise
  *   positions int32 or int64 (positions_64), of token (b, t) at b*pos_stride_b + t
  *             (0: shared by the batch).  A token with a negative position is
- *             padding: neither read nor written (SEKV_ROPE_ZERO_PADDING: its outputs
- *             are set to 0)
+ *             padding: neither read nor written (but see zero_padding)
  *   q, k      either may be NULL
  *   flags     SEKV_ROPE_BACKWARD: turns by -p f_i (the gradient of the call without
- *             it, and for mscale 1 its inverse); SEKV_ROPE_ZERO_PADDING
+ *             it, and for mscale 1 its inverse), 0 otherwise
  *   head_dim  >= rot_dim, at most 1024
  */
 sekv_status sekv_rope(const sekv_rope_config* rope, const uint64_t* freqs, float mscale,

@@ -219,7 +219,7 @@ def test_rope_far_positions(sk, inter):
     q, k, pos, plan, f, m = rope_case(sk, "f32", 1, 6, 2, 1, 64, 64, inter, "none", 3)
     pos[0] = torch.tensor([0, 1 << 20, (1 << 31) - 1, 1 << 33, (1 << 40) - 7, 12345678901])
     from decode_attention_span_gb300 import rotary
-    freqs = [int(v) % (1 << 64) for v in rotary.rope_freqs(plan._c)[0]]
+    freqs = [int(v) % (1 << 64) for v in rotary.rope_freqs(plan.config)[0]]
     got = sk.rope(plan, q.cuda(), None, pos.cuda())[0].double().cpu().numpy()
     for t in range(6):
         ang = np.array([(int(pos[0, t]) * u % (1 << 64)) / 2.0 ** 64 * 2 * math.pi for u in freqs])

@@ -188,12 +188,12 @@ def test_rope_refusals(libsekv):
         rotary.rope_config(64, scaling="other")
 
     heads = lambda x=1 << 20, y=1 << 21, n=2, xs=(0, 256, 128), ys=(0, 256, 128): ctypes.byref(  # noqa: E731
-        rotary.SekvHeads(x, y, n, 0, (ctypes.c_int64 * 3)(*xs), (ctypes.c_int64 * 3)(*ys)))
+        rotary.SekvHeads(x or 0, y, n % (1 << 32), *xs, *ys))
 
     def call(dtype=0, dim=128, B=1, T=2, pos=P, q=heads(), k=None, flags=0, m=1.0, freqs=P):
         return libsekv.sekv_rope(ctypes.byref(rotary.rope_config(64)), freqs, m, dtype, dim, B, T, pos, 0, 0, q, k, flags, None)
     assert call(T=0) == 0 and call(q=heads(n=0)) == 0
-    for kw in (dict(dtype=5), dict(dim=62), dict(B=-1), dict(pos=None), dict(pos=ODD), dict(q=None), dict(flags=4),
+    for kw in (dict(dtype=5), dict(dim=62), dict(B=-1), dict(pos=None), dict(pos=ODD), dict(q=None), dict(flags=2),
                dict(m=math.nan), dict(freqs=None), dict(q=heads(x=None)), dict(q=heads(x=(1 << 20) + 1)), dict(q=heads(n=-1)),
                dict(q=heads(y=1 << 20, ys=(0, 128, 256)))):
         assert call(**kw) == INVALID, kw

@@ -1,16 +1,26 @@
 // sekv_kv4_append and sekv_kv4_read: tokens into the 4-bit cache and back.
 //
-// Bound by memory: append reads 512 bytes and writes 144 per (token, KV head).
-// One warp takes a (token, KV head): lanes 0-15 its K row, lanes 16-31 its V
-// row, eight dimensions a lane.  Eight lanes hold a group of 64, so its minimum and
-// maximum take three shuffles; the lane's eight codes are one 32-bit word.
+// Bound by memory: append reads 512 bytes and writes 144 per (token, KV head),
+// read the reverse.  One warp takes a tile (16 tokens of one KV head, 2304
+// bytes): lanes 0-15 a token's K row, lanes 16-31 its V row, eight dimensions a
+// lane; eight lanes hold a group of 64.  A tile that is written whole is put
+// together in shared memory and leaves in 16-byte stores (V's codes of a token
+// are 2-byte pieces 64 bytes apart, which one by one cost a memory sector each);
+// of a tile written in part only the tokens' own bytes are touched.
+//
+// Codes: n = rint(fl((x - z) / s)) by definition.  x / s - z / s by one fma and
+// the reciprocal of s is off by less than 2^-12 as long as |z / s| < 2^11, so only a
+// quotient nearer than that to a half needs the division; the lanes that have
+// one divide all eight.
 #include "kv4.cuh"
 
 using namespace sekv;
 
 namespace {
 
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 128;
+constexpr int kStoreWarps = kStoreThreads / 32;
+constexpr int kRowsInFlight = 8;  // token rows a warp has loads out for
 
 struct StoreParams {
   Kv4Pages pg;
@@ -19,134 +29,216 @@ struct StoreParams {
   int64_t ks[3], vs[3];
   const int32_t *first, *n_valid;
   int n_tokens;
-  int64_t items;  // batch * n_tokens * hkv
+  int tiles;         // per sequence and KV head, whatever `first` is
+  int64_t items;     // warps: batch * tiles * hkv
 };
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __nv_bfloat16) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// One warp's tile: tokens t0 .. t1 - 1 of the call (rows from j0 on of the tile) of
+// sequence b and KV head c; false where there is nothing to do.
+struct TileWork {
+  uint8_t* tile;
+  int b, c, t0, t1, j0;
+};
+__device__ __forceinline__ bool tile_work(const StoreParams& P, TileWork& W) {
+  const int64_t item = int64_t(blockIdx.x) * kStoreWarps + (threadIdx.x >> 5);
+  if (item >= P.items) return false;
+  W.c = int(item % P.pg.hkv);
+  const int64_t bt = item / P.pg.hkv;
+  const int k = int(bt % P.tiles);
+  W.b = int(bt / P.tiles);
+  const int n = P.n_valid ? min(P.n_valid[W.b], P.n_tokens) : P.n_tokens;
+  const int64_t first = P.first[W.b];
+  // tile k covers positions base .. base + 15 (rounded down, also below zero)
+  const int64_t base = (first - (first & (kKv4Tile - 1))) + int64_t(k) * kKv4Tile;
+  const int64_t p0 = max(base, first), p1 = min(base + kKv4Tile, first + n);
+  if (p0 >= p1) return false;
+  if (base < 0) {
+    set_device_error(P.pg.status, DEV_BAD_LIST, W.b);
+    return false;
   }
-}
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8], __half) {
-  const __half2* h = reinterpret_cast<const __half2*>(&w);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(h[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+  W.tile = P.pg.tile(W.b, W.c, base);
+  W.t0 = int(p0 - first);
+  W.t1 = int(p1 - first);
+  W.j0 = int(p0 - base);
+  return W.tile != nullptr;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreParams P) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * (kStoreThreads / 32) + (threadIdx.x >> 5);
-  if (item >= P.items) return;  // warp-uniform
-  const int c = int(item % P.pg.hkv);
-  const int64_t bt = item / P.pg.hkv;
-  const int t = int(bt % P.n_tokens), b = int(bt / P.n_tokens);
-  if (P.n_valid && t >= P.n_valid[b]) return;
-  const int64_t pos = int64_t(P.first[b]) + t;
-  uint8_t* tile = pos >= 0 ? P.pg.tile(b, c, pos) : nullptr;
-  if (!tile) {
-    if (pos < 0) set_device_error(P.pg.status, DEV_BAD_LIST, b);
+// Smaller (MAX 0) or larger (MAX 1) of two pairs, NaN if either is NaN.
+__device__ __forceinline__ __nv_bfloat162 min2(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmin2_nan(a, b); }
+__device__ __forceinline__ __half2 min2(__half2 a, __half2 b) { return __hmin2_nan(a, b); }
+__device__ __forceinline__ __nv_bfloat162 max2(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2_nan(a, b); }
+__device__ __forceinline__ __half2 max2(__half2 a, __half2 b) { return __hmax2_nan(a, b); }
+__device__ __forceinline__ float2 floats(uint32_t w, __nv_bfloat162) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 floats(uint32_t w, __half2) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Codes (eight nibbles) and bf16 s | z << 16 of this lane's eight values, whose group is
+// held by eight neighbouring lanes.
+template <typename T2>
+__device__ __forceinline__ void quantise(const uint4& in, uint32_t& word, uint32_t& sz) {
+  const uint32_t u[4] = {in.x, in.y, in.z, in.w};
+  auto pair = [&](int i) { return *reinterpret_cast<const T2*>(&u[i]); };
+  const T2 mn2 = min2(min2(pair(0), pair(1)), min2(pair(2), pair(3)));
+  const T2 mx2 = max2(max2(pair(0), pair(1)), max2(pair(2), pair(3)));
+  // (minimum, -maximum) as one pair, so that one reduction does both
+  const uint32_t a = *reinterpret_cast<const uint32_t*>(&mn2);
+  const uint32_t b = *reinterpret_cast<const uint32_t*>(&mx2) ^ 0x80008000u;
+  const uint32_t lo = __byte_perm(a, b, 0x5410), hi = __byte_perm(a, b, 0x7632);
+  T2 m = min2(*reinterpret_cast<const T2*>(&lo), *reinterpret_cast<const T2*>(&hi));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const uint32_t other = __shfl_xor_sync(~0u, *reinterpret_cast<const uint32_t*>(&m), o);
+    m = min2(m, *reinterpret_cast<const T2*>(&other));
+  }
+  const float2 ends = floats(*reinterpret_cast<const uint32_t*>(&m), T2());
+  const float mn = ends.x, mx = -ends.y;
+  const __nv_bfloat16 zb = __float2bfloat16_rd(mn);
+  const float z = __bfloat162float(zb);
+  const __nv_bfloat16 sb = __float2bfloat16_rn((mx - z) * (1.f / 15.f));
+  const float s = __bfloat162float(sb);
+  word = 0;
+  // a NaN or an infinity in the group, or a range beyond fp32
+  if (!(fabsf(s) <= 3.4028235e38f) || !(fabsf(z) <= 3.4028235e38f)) {
+    sz = 0x7fff7fffu;
     return;
   }
-  const int j = int(pos % kKv4Tile);
-  const bool is_v = lane >= 16;
+  sz = uint32_t(__bfloat16_as_ushort(sb)) | uint32_t(__bfloat16_as_ushort(zb)) << 16;
+  const float r = __frcp_rn(s), zr = -z * r;
+  const float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+  float q[8], off = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = floats(u[i], T2());
+    q[2 * i] = fmaf(x.x, r, zr);
+    q[2 * i + 1] = fmaf(x.y, r, zr);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float n = (q[i] + kRound) - kRound;
+    off = fmaxf(off, fabsf(q[i] - n));
+    q[i] = n;
+  }
+  // s below 2^-100 (or 0): the reciprocal or the range of q may be out of bounds
+  if (!(off < 0.5f - 1.f / 4096.f) || !(fabsf(zr) < 2048.f) || s < 7.9e-31f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = floats(u[i], T2());
+      q[2 * i] = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x.x - z, s)), 0.f), 15.f) : 0.f;
+      q[2 * i + 1] = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x.y - z, s)), 0.f), 15.f) : 0.f;
+    }
+  }
+  // four codes as one whole number below 2^16
+  const float h0 = fmaf(fmaf(fmaf(q[3], 16.f, q[2]), 16.f, q[1]), 16.f, q[0]);
+  const float h1 = fmaf(fmaf(fmaf(q[7], 16.f, q[6]), 16.f, q[5]), 16.f, q[4]);
+  word = __byte_perm(__float_as_uint(h0 + kRound), __float_as_uint(h1 + kRound), 0x5410);
+}
+
+__device__ __forceinline__ void put_row(uint8_t* tile, int j, int lane, uint32_t word, uint32_t sz) {
   const int oct = lane & 15;
-  const T* src = is_v ? static_cast<const T*>(P.v) + b * P.vs[0] + t * P.vs[1] + c * P.vs[2]
-                      : static_cast<const T*>(P.k) + b * P.ks[0] + t * P.ks[1] + c * P.ks[2];
-  float x[8];
-  unpack8(reinterpret_cast<const uint4*>(src)[oct], x, T());
-  float mn = x[0], mx = x[0];
-  bool fin = true;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    mn = fminf(mn, x[i]);
-    mx = fmaxf(mx, x[i]);
-    fin &= fabsf(x[i]) <= 3.4028235e38f;  // false for NaN too
-  }
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
-    mn = fminf(mn, __shfl_xor_sync(~0u, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-  }
-  const uint32_t ok = __ballot_sync(~0u, fin) >> (lane & 24) & 0xffu;
-  __nv_bfloat16 zb = __float2bfloat16_rd(mn);
-  const float z = __bfloat162float(zb);
-  __nv_bfloat16 sb = __float2bfloat16_rn((mx - z) * (1.f / 15.f));
-  const float s = __bfloat162float(sb);
-  if (ok != 0xffu || !(fabsf(s) <= 3.4028235e38f) || !(fabsf(z) <= 3.4028235e38f))
-    sb = zb = __ushort_as_bfloat16(0x7fffu);
-  uint32_t word = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float n = s > 0.f ? rintf(__fdiv_rn(x[i] - z, s)) : 0.f;
-    word |= uint32_t(fminf(fmaxf(n, 0.f), 15.f)) << (4 * i);
-  }
-  if (!is_v) {
+  if (lane < 16) {
     *reinterpret_cast<uint32_t*>(tile + kv4_k_word(j, oct)) = word;
   } else {
     *reinterpret_cast<uint16_t*>(tile + kv4_v_half(j, oct)) = uint16_t(word);
     *reinterpret_cast<uint16_t*>(tile + kv4_v_half(j, oct) + 4) = uint16_t(word >> 16);
   }
-  if ((lane & 7) == 0) {
-    const uint32_t sz = uint32_t(__bfloat16_as_ushort(sb)) | uint32_t(__bfloat16_as_ushort(zb)) << 16;
-    *reinterpret_cast<uint32_t*>(tile + kv4_param(j, oct >> 3, is_v)) = sz;
+  if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(tile + kv4_param(j, oct >> 3, lane >= 16)) = sz;
+}
+
+template <typename T2>
+__global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreParams P) {
+  __shared__ __align__(16) uint8_t staged[kStoreWarps][kKv4TileBytes];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  TileWork W;
+  if (!tile_work(P, W)) return;  // warp-uniform
+  const bool whole = W.t1 - W.t0 == kKv4Tile;
+  uint8_t* dst = whole ? staged[warp] : W.tile;
+  const int64_t step = lane < 16 ? P.ks[1] : P.vs[1];  // elements of 2 bytes
+  const uint16_t* src =
+      (lane < 16 ? static_cast<const uint16_t*>(P.k) + W.b * P.ks[0] + W.c * P.ks[2]
+                 : static_cast<const uint16_t*>(P.v) + W.b * P.vs[0] + W.c * P.vs[2]) +
+      W.t0 * step + (lane & 15) * 8;
+  const int rows = W.t1 - W.t0;
+  for (int i0 = 0; i0 < rows; i0 += kRowsInFlight) {
+    uint4 in[kRowsInFlight];
+#pragma unroll
+    for (int i = 0; i < kRowsInFlight; ++i)
+      if (i0 + i < rows) in[i] = __ldcs(reinterpret_cast<const uint4*>(src + (i0 + i) * step));
+#pragma unroll
+    for (int i = 0; i < kRowsInFlight; ++i)
+      if (i0 + i < rows) {
+        uint32_t word, sz;
+        quantise<T2>(in[i], word, sz);
+        put_row(dst, W.j0 + i0 + i, lane, word, sz);
+      }
+  }
+  if (whole) {
+    __syncwarp();
+    for (int i = lane; i < kKv4TileBytes / 16; i += 32)
+      reinterpret_cast<uint4*>(W.tile)[i] = reinterpret_cast<const uint4*>(staged[warp])[i];
   }
 }
 
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                 pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])));
 }
 __device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
   __half2 h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
+  __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<uint4*>(h));
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StoreParams P) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * (kStoreThreads / 32) + (threadIdx.x >> 5);
-  if (item >= P.items) return;
-  const int t = int(item % P.n_tokens);
-  const int64_t bc = item / P.n_tokens;
-  const int c = int(bc % P.pg.hkv), b = int(bc / P.pg.hkv);
-  if (P.n_valid && t >= P.n_valid[b]) return;
-  const int64_t pos = int64_t(P.first[b]) + t;
-  const uint8_t* tile = pos >= 0 ? P.pg.tile(b, c, pos) : nullptr;
-  if (!tile) {
-    if (pos < 0) set_device_error(P.pg.status, DEV_BAD_LIST, b);
-    return;
-  }
-  const int j = int(pos % kKv4Tile);
-  const bool is_v = lane >= 16;
-  const int oct = lane & 15;
-  uint32_t word;
-  if (!is_v) {
-    word = *reinterpret_cast<const uint32_t*>(tile + kv4_k_word(j, oct));
-  } else {
-    word = *reinterpret_cast<const uint16_t*>(tile + kv4_v_half(j, oct)) |
-           uint32_t(*reinterpret_cast<const uint16_t*>(tile + kv4_v_half(j, oct) + 4)) << 16;
-  }
-  const uint32_t sz = *reinterpret_cast<const uint32_t*>(tile + kv4_param(j, oct >> 3, is_v));
-  const float s = __uint_as_float(sz << 16), z = __uint_as_float(sz & 0xffff0000u);
-  float x[8];
+  __shared__ __align__(16) uint8_t staged[kStoreWarps][kKv4TileBytes];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  TileWork W;
+  if (!tile_work(P, W)) return;  // warp-uniform
+  const uint8_t* tile = W.tile;
+  if (W.t1 - W.t0 > 2) {  // more than a few rows: bring the whole tile
+    uint4 in[5];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(s, float((word >> (4 * i)) & 15u), z);
-  T* dst = static_cast<T*>(is_v ? P.vo : P.ko) + item * kHeadDim + oct * 8;
-  store8(dst, x);
+    for (int i = 0; i < 5; ++i)
+      if (lane + 32 * i < kKv4TileBytes / 16) in[i] = __ldcs(reinterpret_cast<const uint4*>(W.tile) + lane + 32 * i);
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (lane + 32 * i < kKv4TileBytes / 16) reinterpret_cast<uint4*>(staged[warp])[lane + 32 * i] = in[i];
+    __syncwarp();
+    tile = staged[warp];
+  }
+  const int oct = lane & 15;
+  T* dst = static_cast<T*>(lane < 16 ? P.ko : P.vo) +
+           ((int64_t(W.b) * P.pg.hkv + W.c) * P.n_tokens + W.t0) * kHeadDim + oct * 8;
+  const int rows = W.t1 - W.t0;
+#pragma unroll 4
+  for (int i = 0; i < rows; ++i) {
+    const int j = W.j0 + i;
+    uint32_t word;
+    if (lane < 16) {
+      word = *reinterpret_cast<const uint32_t*>(tile + kv4_k_word(j, oct));
+    } else {
+      word = *reinterpret_cast<const uint16_t*>(tile + kv4_v_half(j, oct)) |
+             uint32_t(*reinterpret_cast<const uint16_t*>(tile + kv4_v_half(j, oct) + 4)) << 16;
+    }
+    const uint32_t sz = *reinterpret_cast<const uint32_t*>(tile + kv4_param(j, oct >> 3, lane >= 16));
+    const float s = __uint_as_float(sz << 16), z = __uint_as_float(sz & 0xffff0000u);
+    float x[8];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      // the code's bits at the top of a mantissa are 16 + n
+      const uint32_t bits = (d < 5 ? word << (19 - 4 * d) : word >> (4 * d - 19)) & 0x00780000u;
+      x[d] = fmaf(s, __uint_as_float(bits | 0x41800000u) - 16.f, z);
+    }
+    store8(dst + int64_t(i) * kHeadDim, x);
+  }
 }
 
 StoreParams store_params(const sekv_config* cfg, const sekv_kv4_cache* cache, int32_t n_tokens,
@@ -161,11 +253,12 @@ StoreParams store_params(const sekv_config* cfg, const sekv_kv4_cache* cache, in
   P.first = first;
   P.n_valid = n_valid;
   P.n_tokens = n_tokens;
-  P.items = int64_t(cfg->batch) * n_tokens * cfg->n_kv_heads;
+  P.tiles = (n_tokens + kKv4Tile - 2) / kKv4Tile + 1;  // `first` may stand anywhere in a tile
+  P.items = int64_t(cfg->batch) * P.tiles * cfg->n_kv_heads;
   return P;
 }
 
-constexpr int64_t kStoreItemsMax = int64_t(INT32_MAX) * (kStoreThreads / 32);
+constexpr int64_t kStoreItemsMax = int64_t(INT32_MAX) * kStoreWarps;
 
 }  // namespace
 
@@ -191,14 +284,15 @@ extern "C" sekv_status sekv_kv4_append(const sekv_config* cfg, const sekv_kv4_ca
     P.vs[i] = v_stride[i];
   }
   if (n_tokens == 0) return SEKV_OK;
+  if (n_tokens > (1 << 30)) return SEKV_ERR_UNSUPPORTED;
   if (P.items > kStoreItemsMax) return SEKV_ERR_UNSUPPORTED;
   st = kv4_check_ws(cfg, 1, workspace_bytes);
   if (st != SEKV_OK) return st;
-  const unsigned blocks = unsigned((P.items + kStoreThreads / 32 - 1) / (kStoreThreads / 32));
+  const unsigned blocks = unsigned((P.items + kStoreWarps - 1) / kStoreWarps);
   if (dtype == SEKV_BF16)
-    kv4_append_kernel<__nv_bfloat16><<<blocks, kStoreThreads, 0, stream>>>(P);
+    kv4_append_kernel<__nv_bfloat162><<<blocks, kStoreThreads, 0, stream>>>(P);
   else
-    kv4_append_kernel<__half><<<blocks, kStoreThreads, 0, stream>>>(P);
+    kv4_append_kernel<__half2><<<blocks, kStoreThreads, 0, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return SEKV_ERR_CUDA;
   count_launch(1);
   return SEKV_OK;
@@ -219,10 +313,11 @@ extern "C" sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cach
   P.ko = k_out;
   P.vo = v_out;
   if (n_tokens == 0) return SEKV_OK;
+  if (n_tokens > (1 << 30)) return SEKV_ERR_UNSUPPORTED;
   if (P.items > kStoreItemsMax) return SEKV_ERR_UNSUPPORTED;
   st = kv4_check_ws(cfg, 1, workspace_bytes);
   if (st != SEKV_OK) return st;
-  const unsigned blocks = unsigned((P.items + kStoreThreads / 32 - 1) / (kStoreThreads / 32));
+  const unsigned blocks = unsigned((P.items + kStoreWarps - 1) / kStoreWarps);
   if (dtype == SEKV_BF16)
     kv4_read_kernel<__nv_bfloat16><<<blocks, kStoreThreads, 0, stream>>>(P);
   else if (dtype == SEKV_F16)

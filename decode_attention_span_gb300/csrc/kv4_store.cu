@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kStoreThreads = 128;
 constexpr int kStoreWarps = kStoreThreads / 32;
-constexpr int kRowsInFlight = 8;  // token rows a warp has loads out for
+constexpr int kRowsAhead = 8;  // token rows on their way to a warp
 
 struct StoreParams {
   Kv4Pages pg;
@@ -75,6 +75,12 @@ __device__ __forceinline__ float2 floats(uint32_t w, __half2) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// largest bf16 at or below x (a bf16 input is one itself)
+__device__ __forceinline__ float bf16_at_or_below(float x, __nv_bfloat162) { return x; }
+__device__ __forceinline__ float bf16_at_or_below(float x, __half2) {
+  return __bfloat162float(__float2bfloat16_rd(x));
+}
+
 // Codes (eight nibbles) and bf16 s | z << 16 of this lane's eight values, whose group is
 // held by eight neighbouring lanes.
 template <typename T2>
@@ -94,9 +100,8 @@ __device__ __forceinline__ void quantise(const uint4& in, uint32_t& word, uint32
     m = min2(m, *reinterpret_cast<const T2*>(&other));
   }
   const float2 ends = floats(*reinterpret_cast<const uint32_t*>(&m), T2());
-  const float mn = ends.x, mx = -ends.y;
-  const __nv_bfloat16 zb = __float2bfloat16_rd(mn);
-  const float z = __bfloat162float(zb);
+  const float mx = -ends.y;
+  const float z = bf16_at_or_below(ends.x, T2());
   const __nv_bfloat16 sb = __float2bfloat16_rn((mx - z) * (1.f / 15.f));
   const float s = __bfloat162float(sb);
   word = 0;
@@ -105,10 +110,12 @@ __device__ __forceinline__ void quantise(const uint4& in, uint32_t& word, uint32
     sz = 0x7fff7fffu;
     return;
   }
-  sz = uint32_t(__bfloat16_as_ushort(sb)) | uint32_t(__bfloat16_as_ushort(zb)) << 16;
-  const float r = __frcp_rn(s), zr = -z * r;
+  sz = __byte_perm(__bfloat16_as_ushort(sb), __float_as_uint(z), 0x7610);
+  float r;  // 1 / s to an ulp
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const float zr = -z * r;
   const float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
-  float q[8], off = 0.f;
+  float q[8], n[8], off = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 x = floats(u[i], T2());
@@ -117,68 +124,99 @@ __device__ __forceinline__ void quantise(const uint4& in, uint32_t& word, uint32
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float n = (q[i] + kRound) - kRound;
-    off = fmaxf(off, fabsf(q[i] - n));
-    q[i] = n;
+    n[i] = (q[i] + kRound) - kRound;
+    off = fmaxf(off, fabsf(q[i] - n[i]));
   }
   // s below 2^-100 (or 0): the reciprocal or the range of q may be out of bounds
-  if (!(off < 0.5f - 1.f / 4096.f) || !(fabsf(zr) < 2048.f) || s < 7.9e-31f) {
+  const bool far = !(fabsf(zr) < 2048.f) || s < 7.9e-31f;
+  const float kNear = 0.5f - 1.f / 4096.f;
+  if (off >= kNear || far) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = floats(u[i], T2());
-      q[2 * i] = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x.x - z, s)), 0.f), 15.f) : 0.f;
-      q[2 * i + 1] = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x.y - z, s)), 0.f), 15.f) : 0.f;
-    }
+    for (int i = 0; i < 8; ++i)
+      if (far || fabsf(q[i] - n[i]) >= kNear) {
+        const float2 x = floats(u[i >> 1], T2());
+        n[i] = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn((i & 1 ? x.y : x.x) - z, s)), 0.f), 15.f) : 0.f;
+      }
   }
   // four codes as one whole number below 2^16
-  const float h0 = fmaf(fmaf(fmaf(q[3], 16.f, q[2]), 16.f, q[1]), 16.f, q[0]);
-  const float h1 = fmaf(fmaf(fmaf(q[7], 16.f, q[6]), 16.f, q[5]), 16.f, q[4]);
+  const float h0 = fmaf(fmaf(fmaf(n[3], 16.f, n[2]), 16.f, n[1]), 16.f, n[0]);
+  const float h1 = fmaf(fmaf(fmaf(n[7], 16.f, n[6]), 16.f, n[5]), 16.f, n[4]);
   word = __byte_perm(__float_as_uint(h0 + kRound), __float_as_uint(h1 + kRound), 0x5410);
 }
 
-__device__ __forceinline__ void put_row(uint8_t* tile, int j, int lane, uint32_t word, uint32_t sz) {
-  const int oct = lane & 15;
-  if (lane < 16) {
-    *reinterpret_cast<uint32_t*>(tile + kv4_k_word(j, oct)) = word;
-  } else {
-    *reinterpret_cast<uint16_t*>(tile + kv4_v_half(j, oct)) = uint16_t(word);
-    *reinterpret_cast<uint16_t*>(tile + kv4_v_half(j, oct) + 4) = uint16_t(word >> 16);
+// Where a lane's pieces of a token row go in a tile: the codes' lower and upper half
+// (K's in one word, V's four bytes apart), and the scale and zero point, at offsets linear in
+// the three parts of the row number.
+struct RowPlace {
+  uint32_t codes, upper, odd, pair, params;
+  __device__ explicit RowPlace(int lane) {
+    const bool v = lane >= 16;
+    codes = v ? kv4_v_half(0, lane & 15) : kv4_k_word(0, lane & 15);
+    upper = v ? 4 : 2;
+    odd = v ? 2 : 64;    // j % 2
+    pair = v ? 16 : 128; // (j % 8) / 2
+    params = kv4_param(0, (lane & 15) >> 3, v);
   }
-  if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(tile + kv4_param(j, oct >> 3, lane >= 16)) = sz;
-}
+  __device__ __forceinline__ void put(uint8_t* tile, int j, bool group_lead, uint32_t word,
+                                      uint32_t sz) const {
+    const uint32_t o = j & 1, u = (j >> 1) & 3, e = j >> 3;
+    uint8_t* at = tile + (codes + o * odd + u * pair + e * 512);
+    *reinterpret_cast<uint16_t*>(at) = uint16_t(word);
+    *reinterpret_cast<uint16_t*>(at + upper) = uint16_t(word >> 16);
+    if (group_lead) *reinterpret_cast<uint32_t*>(tile + (params + 8 * o + 32 * u + 16 * e)) = sz;
+  }
+};
 
 template <typename T2>
 __global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreParams P) {
   __shared__ __align__(16) uint8_t staged[kStoreWarps][kKv4TileBytes];
+  __shared__ uint4 in[kStoreWarps][kRowsAhead][32];  // each lane copies and reads its own
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   TileWork W;
   if (!tile_work(P, W)) return;  // warp-uniform
   const bool whole = W.t1 - W.t0 == kKv4Tile;
-  uint8_t* dst = whole ? staged[warp] : W.tile;
   const int64_t step = lane < 16 ? P.ks[1] : P.vs[1];  // elements of 2 bytes
   const uint16_t* src =
       (lane < 16 ? static_cast<const uint16_t*>(P.k) + W.b * P.ks[0] + W.c * P.ks[2]
                  : static_cast<const uint16_t*>(P.v) + W.b * P.vs[0] + W.c * P.vs[2]) +
       W.t0 * step + (lane & 15) * 8;
   const int rows = W.t1 - W.t0;
-  for (int i0 = 0; i0 < rows; i0 += kRowsInFlight) {
-    uint4 in[kRowsInFlight];
-#pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i)
-      if (i0 + i < rows) in[i] = __ldcs(reinterpret_cast<const uint4*>(src + (i0 + i) * step));
-#pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i)
-      if (i0 + i < rows) {
-        uint32_t word, sz;
-        quantise<T2>(in[i], word, sz);
-        put_row(dst, W.j0 + i0 + i, lane, word, sz);
-      }
+  // Rows come through a ring in shared memory: kRowsAhead of them on their way without
+  // holding registers.  One group of copies per row, empty past the last row.
+  auto fetch = [&](int i) {
+    if (i < rows)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       smem_u32(&in[warp][i % kRowsAhead][lane])),
+                   "l"(src + i * step)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto row = [&](int i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRowsAhead - 1) : "memory");
+    return in[warp][i % kRowsAhead][lane];
+  };  // the slot is filled again once the row has been used
+  for (int i = 0; i < kRowsAhead; ++i) fetch(i);
+  const RowPlace place(lane);
+  const bool lead = (lane & 7) == 0;
+  if (!whole) {
+    for (int i = 0; i < rows; ++i) {
+      uint32_t word, sz;
+      quantise<T2>(row(i), word, sz);
+      place.put(W.tile, W.j0 + i, lead, word, sz);
+      fetch(i + kRowsAhead);
+    }
+    return;
   }
-  if (whole) {
-    __syncwarp();
-    for (int i = lane; i < kKv4TileBytes / 16; i += 32)
-      reinterpret_cast<uint4*>(W.tile)[i] = reinterpret_cast<const uint4*>(staged[warp])[i];
+#pragma unroll 2
+  for (int j = 0; j < kKv4Tile; ++j) {
+    uint32_t word, sz;
+    quantise<T2>(row(j), word, sz);
+    place.put(staged[warp], j, lead, word, sz);
+    fetch(j + kRowsAhead);
   }
+  __syncwarp();
+  for (int i = lane; i < kKv4TileBytes / 16; i += 32)
+    reinterpret_cast<uint4*>(W.tile)[i] = reinterpret_cast<const uint4*>(staged[warp])[i];
 }
 
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {

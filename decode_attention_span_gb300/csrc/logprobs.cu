@@ -18,6 +18,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "decode_host.h"
 #include "host_common.h"
 
@@ -49,21 +51,33 @@ struct Stat {
   float m, s, a;  // maximum; sums in units of e^(scale (x - m)); a in log2 units
 };
 
+// 2^x, to 2^-22 of its value; 0 for -infinity
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // exponent scale (x - m) in log2 units, finite differences first: with x and m
 // at the type's lowest value the product would overflow, the difference is 0
 __device__ __forceinline__ float exp_arg(float x, float m, float c) {
   return (x - (m == -INFINITY ? 0.f : m)) * c;
 }
 
-__device__ __forceinline__ Stat join(const Stat& p, const Stat& q, float c) {
-  Stat r;
-  r.m = fmaxf(p.m, q.m);
-  const float dp = fmaxf(exp_arg(p.m, r.m, c), -1e30f), dq = fmaxf(exp_arg(q.m, r.m, c), -1e30f);
-  const float fp = exp2f(dp), fq = exp2f(dq);
+// (s, a) of the smaller maximum p.m in units of the larger one, m
+__device__ __forceinline__ void rescale(Stat& p, float m, float c) {
   // a term without weight has no share (0 * finite), whatever its distance
-  r.s = p.s * fp + q.s * fq;
-  r.a = fp * (p.a + p.s * dp) + fq * (q.a + q.s * dq);
-  return r;
+  const float d = fmaxf(exp_arg(p.m, m, c), -1e30f), f = ex2(d);
+  p.a = f * (p.a + p.s * d);
+  p.s *= f;
+  p.m = m;
+}
+
+__device__ __forceinline__ Stat join(Stat p, Stat q, float c) {
+  const float m = fmaxf(p.m, q.m);
+  rescale(p, m, c);
+  rescale(q, m, c);
+  return {m, p.s + q.s, p.a + q.a};
 }
 
 __device__ __forceinline__ Stat shfl_xor(const Stat& v, int o) {
@@ -143,6 +157,19 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f(float v) { return v; }
 
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b, __nv_bfloat16) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b, __half) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b, float) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+
 // A row as 16-byte vectors: vector i holds elements i*VE - off .. + VE - 1; the
 // first and the last may be partial (elements outside the row read as -inf).
 template <typename T>
@@ -150,24 +177,96 @@ struct Row {
   static constexpr int VE = 16 / int(sizeof(T));
   const T* base;   // 16-byte aligned; element 0 of the row is base[off]
   int off;
-  int64_t vocab;
-  __device__ __forceinline__ void load(int64_t i, uint4& w) const {
-    const int64_t e0 = i * VE - off;
-    if (e0 >= 0 && e0 + VE <= vocab) {
-      w = __ldcs(reinterpret_cast<const uint4*>(base) + i);
-    } else {
-      T* e = reinterpret_cast<T*>(&w);
+  int vocab;
+  int full0, full1;  // vectors that lie in the row entirely
+  __device__ __forceinline__ uint4 load(int i) const {
+    if (i >= full0 && i < full1) return __ldcs(reinterpret_cast<const uint4*>(base) + i);
+    uint4 w;
+    T* e = reinterpret_cast<T*>(&w);
+    const int e0 = i * VE - off;
 #pragma unroll
-      for (int j = 0; j < VE; ++j)
-        e[j] = e0 + j >= 0 && e0 + j < vocab ? base[i * VE + j] : T(-INFINITY);
-    }
+    for (int j = 0; j < VE; ++j)
+      e[j] = e0 + j >= 0 && e0 + j < vocab ? base[int64_t(i) * VE + j] : T(-INFINITY);
+    return w;
   }
-  __device__ __forceinline__ void unpack(const uint4& w, float (&x)[VE]) const {
+  __device__ static __forceinline__ void unpack(const uint4& w, float (&x)[VE]) {
     const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
     for (int j = 0; j < VE; ++j) x[j] = to_f(e[j]);
   }
+  // largest element (NaN does not count)
+  __device__ static __forceinline__ float largest(uint32_t m) {
+    if (sizeof(T) == 4) return __uint_as_float(m);
+    const T* e = reinterpret_cast<const T*>(&m);
+    return fmaxf(to_f(e[0]), to_f(e[sizeof(T) == 4 ? 0 : 1]));
+  }
+  // at least about -5e4 (NaN stays): what is smaller has no weight beside a maximum above
+  // -4e4, and its product with that weight, 0, stays finite
+  __device__ static __forceinline__ uint32_t raised(uint32_t w) {
+    uint32_t r;
+    if constexpr (sizeof(T) == 4) {
+      float f;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(w)), "f"(-5e4f));
+      r = __float_as_uint(f);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xfa1afa1au));
+    } else {
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xc744c744u));
+    }
+    return r;
+  }
+  __device__ static __forceinline__ uint4 raised(const uint4& w) {
+    return make_uint4(raised(w.x), raised(w.y), raised(w.z), raised(w.w));
+  }
 };
+
+// Adds a thread's N vectors to its state; true if they hold a new maximum.
+template <typename T, bool FULL, int N>
+__device__ __forceinline__ bool add_vectors(Stat& st, const uint4 (&w)[N], float c) {
+  constexpr int VE = Row<T>::VE;
+  uint32_t top = max_pair(max_pair(w[0].x, w[0].y, T()), max_pair(w[0].z, w[0].w, T()), T());
+#pragma unroll
+  for (int u = 1; u < N; ++u)
+    top = max_pair(top, max_pair(max_pair(w[u].x, w[u].y, T()), max_pair(w[u].z, w[u].w, T()), T()), T());
+  const float gm = Row<T>::largest(top);
+  const bool up = gm > st.m;
+  if (up) rescale(st, gm, c);
+  if (fabsf(st.m) < 4e4f && c < 1e3f && c > 0.05f) {
+    // Exponents by one fma, x c - fl(m c); what rounding m c took, r, is the same for all
+    // of them: 2^-r is multiplied out of the sums, so that a common offset of the
+    // logits costs nothing.
+    const float mc = st.m * c, r = fmaf(st.m, c, -mc);
+    float s[2] = {0.f, 0.f}, a[2] = {0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      float x[VE];
+      Row<T>::unpack(FULL ? Row<T>::raised(w[u]) : w[u], x);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float d = fmaf(x[j], c, -mc), e = ex2(d);
+        s[j & 1] += e;
+        if (FULL) a[j & 1] = fmaf(e, d, a[j & 1]);
+      }
+    }
+    const float sum = s[0] + s[1], k = ex2(-r);
+    st.s = fmaf(sum, k, st.s);
+    if (FULL) st.a = fmaf(fmaf(-r, sum, a[0] + a[1]), k, st.a);
+  } else {
+    const float m0 = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      float x[VE];
+      Row<T>::unpack(w[u], x);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float d = (x[j] - m0) * c, e = ex2(d);
+        st.s += e;
+        if (FULL) st.a = fmaf(e, fmaxf(d, -1e30f), st.a);
+      }
+    }
+  }
+  return up;
+}
 
 template <typename T, bool FULL>  // FULL: entropy and alternatives may be asked for
 __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
@@ -183,9 +282,11 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
   Row<T> row;
   row.off = int((reinterpret_cast<uintptr_t>(first) & 15) / sizeof(T));
   row.base = first - row.off;
-  row.vocab = P.vocab;
-  const int64_t nv = (row.off + P.vocab + VE - 1) / VE;
-  const int64_t lo = nv * rank / nc, hi = nv * (rank + 1) / nc;
+  row.vocab = int(P.vocab);
+  row.full0 = row.off > 0 ? 1 : 0;
+  row.full1 = (row.off + row.vocab) / VE;
+  const int nv = (row.off + row.vocab + VE - 1) / VE;
+  const int lo = int(int64_t(nv) * rank / nc), hi = int(int64_t(nv) * (rank + 1) / nc);
   const float c = P.scale * kLog2e;
 
   int64_t tok = -1;
@@ -200,45 +301,27 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
   // one pass: m, s, a of this thread's vectors lo + tid + kLpThreads * i
   Stat st{-INFINITY, 0.f, 0.f};
   int best_group = 0;
-  int g = 0;
-  for (int64_t i0 = lo + tid; i0 < hi; i0 += int64_t(kLpThreads) * kLpUnroll, ++g) {
+  constexpr int kStep = kLpThreads * kLpUnroll;
+  const int n_groups = (hi - lo + kStep - 1) / kStep;
+  for (int g = 0; g < n_groups; ++g) {
+    const int g0 = lo + g * kStep;
     uint4 w[kLpUnroll];
+    if (g0 >= row.full0 && g0 + kStep <= min(hi, row.full1)) {
+      const uint4* src = reinterpret_cast<const uint4*>(row.base) + g0 + tid;
 #pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      const int64_t i = i0 + int64_t(u) * kLpThreads;
-      if (i < hi) row.load(i, w[u]);
-    }
-    float gm = -INFINITY;
+      for (int u = 0; u < kLpUnroll; ++u) w[u] = __ldcs(src + u * kLpThreads);
+      if (add_vectors<T, FULL>(st, w, c)) best_group = g;
+    } else {
+      const T none = T(-INFINITY);
+      uint4 blank;
 #pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      if (i0 + int64_t(u) * kLpThreads < hi) {
-        float x[VE];
-        row.unpack(w[u], x);
+      for (int j = 0; j < VE; ++j) reinterpret_cast<T*>(&blank)[j] = none;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) gm = fmaxf(gm, x[j]);
+      for (int u = 0; u < kLpUnroll; ++u) {
+        const int i = g0 + tid + u * kLpThreads;
+        w[u] = i < hi ? row.load(i) : blank;
       }
-    }
-    if (gm > st.m) {
-      const float d = fmaxf(exp_arg(st.m, gm, c), -1e30f), f = exp2f(d);
-      if (FULL) st.a = f * (st.a + st.s * d);
-      st.s *= f;
-      st.m = gm;
-      best_group = g;
-    }
-    const float m0 = st.m == -INFINITY ? 0.f : st.m;
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      if (i0 + int64_t(u) * kLpThreads < hi) {
-        float x[VE];
-        row.unpack(w[u], x);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const float d = (x[j] - m0) * c;
-          const float e = exp2f(d);
-          st.s += e;
-          if (FULL) st.a = fmaf(e, fmaxf(d, -1e30f), st.a);
-        }
-      }
+      if (add_vectors<T, FULL>(st, w, c)) best_group = g;
     }
   }
   const float thread_max = st.m;
@@ -261,12 +344,10 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
     uint64_t key = 0;
     if (thread_max > -INFINITY) {
       for (int u = kLpUnroll - 1; u >= 0; --u) {
-        const int64_t i = lo + tid + (int64_t(best_group) * kLpUnroll + u) * kLpThreads;
+        const int i = lo + tid + (best_group * kLpUnroll + u) * kLpThreads;
         if (i < hi) {
-          uint4 w;
           float x[VE];
-          row.load(i, w);
-          row.unpack(w, x);
+          row.unpack(row.load(i), x);
 #pragma unroll
           for (int j = VE - 1; j >= 0; --j)
             if (x[j] == thread_max) key = key_of(x[j], uint32_t(i * VE + j - row.off));
@@ -280,13 +361,10 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
     for (int k = warp; k < P.n_top; k += kLpWarps) {
       const uint64_t ok = __shfl_sync(~0u, owner_key, k);
       if (ok == 0) break;
-      const int64_t vec = (int64_t(key_index(ok)) + row.off) / VE;
-      const int owner = int((vec - lo) % kLpThreads);
-      for (int64_t i = lo + owner + int64_t(lane) * kLpThreads; i < hi; i += 32 * kLpThreads) {
-        uint4 w;
+      const int owner = (int(key_index(ok) + row.off) / VE - lo) % kLpThreads;
+      for (int i = lo + owner + lane * kLpThreads; i < hi; i += 32 * kLpThreads) {
         float x[VE];
-        row.load(i, w);
-        row.unpack(w, x);
+        row.unpack(row.load(i), x);
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
           const uint64_t kk = key_of(x[j], uint32_t(i * VE + j - row.off));
@@ -307,11 +385,9 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
       uint64_t last = ~uint64_t(0);
       for (int k = 0; k < P.n_top; ++k) {
         uint64_t best = 0;
-        for (int64_t i = lo + tid; i < hi; i += kLpThreads) {
-          uint4 w;
+        for (int i = lo + tid; i < hi; i += kLpThreads) {
           float x[VE];
-          row.load(i, w);
-          row.unpack(w, x);
+          row.unpack(row.load(i), x);
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
             const uint64_t kk = key_of(x[j], uint32_t(i * VE + j - row.off));

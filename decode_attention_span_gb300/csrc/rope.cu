@@ -23,7 +23,7 @@ using namespace sekv;
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kHeadsInFlight = 4;  // heads whose loads a thread issues together
+constexpr int kHeadsInFlight = 2;  // heads whose loads a thread issues together
 
 struct RopeHeads {
   const void* x;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) 
     for (int i = 0; i < kHeadsInFlight; ++i) {
       if (!dst[i]) continue;
       if (!rotated) {
-        *reinterpret_cast<decltype(a[i].w)*>(dst[i]) = a[i].w;
+        __stcs(reinterpret_cast<decltype(a[i].w)*>(dst[i]), a[i].w);
         continue;
       }
       if (INTER && N > 1) {
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) 
           a[i].e[2 * j] = from_f<T>(u * cs[j] - v * sn[j]);
           a[i].e[(2 * j + 1) % N] = from_f<T>(v * cs[j] + u * sn[j]);
         }
-        *reinterpret_cast<decltype(a[i].w)*>(dst[i]) = a[i].w;
+        __stcs(reinterpret_cast<decltype(a[i].w)*>(dst[i]), a[i].w);
       } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) 
           a[i].e[j] = from_f<T>(u * cs[j % NP] - v * sn[j % NP]);
           c[i].e[j] = from_f<T>(v * cs[j % NP] + u * sn[j % NP]);
         }
-        *reinterpret_cast<decltype(a[i].w)*>(dst[i]) = a[i].w;
-        *reinterpret_cast<decltype(a[i].w)*>(dst[i] + (INTER ? 1 : half)) = c[i].w;
+        __stcs(reinterpret_cast<decltype(a[i].w)*>(dst[i]), a[i].w);
+        __stcs(reinterpret_cast<decltype(a[i].w)*>(dst[i] + (INTER ? 1 : half)), c[i].w);
       }
     }
   }
@@ -323,7 +323,7 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
   // Heads of one thread: all of them once the tokens alone fill the GPU, else
   // fewer, so that a step of a few tokens spreads its heads over blocks.
   int hpt = heads;
-  while (hpt > kHeadsInFlight && uint64_t(blocks) * ((heads + hpt - 1) / hpt) < uint64_t(sms) * 8)
+  while (hpt > kHeadsInFlight && uint64_t(blocks) * ((heads + hpt - 1) / hpt) < uint64_t(sms) * 32)
     hpt = (hpt + 1) / 2;
   if (uint64_t(blocks) < uint64_t(sms)) hpt = 1;
   P.heads_per_thread = hpt;

@@ -8,12 +8,12 @@
 // over the CTA by shuffles and over the cluster through distributed shared
 // memory.  entropy = ln S - A/S has no cancellation (both terms are >= 0).
 //
-// The alternatives need no second pass over the row.  Each thread remembers
-// the group of vectors its maximum came from, and after the pass looks up the
-// maximum's exact key (value, lowest index first) in that group.  The n-th
-// largest of the threads' keys is a bound below which no alternative lies, and
-// exactly n threads have keys at or above it; only those threads' vectors are
-// read again, one warp per thread.  What reaches the bound is sorted.
+// The alternatives need no second pass over the row.  The n-th largest of the
+// maxima of every four threads is a bound that at least n elements reach; only the
+// vectors of threads whose own maximum reaches it are read again (out of L2), a warp
+// per thread, and what reaches the bound -- little more than n elements as a rule --
+// is sorted by (value, lowest index first).  Where ties make them too many, the
+// bound is found again among exact keys of value and index, which no two elements share.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -28,10 +28,8 @@ using namespace sekv;
 
 namespace {
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpUnroll = 4;      // vectors of a thread in flight
-constexpr int kLpMaxCluster = 16;
+constexpr int kLpMaxCluster = 8;
 
 struct LpParams {
   const void* logits;
@@ -90,10 +88,12 @@ __device__ __forceinline__ Stat shfl_xor(const Stat& v, int o) {
 
 // Order-preserving key of (value, index): larger value first, then the lower
 // index; -0 counts as 0.  Every key is above 0.
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
+__device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
-  const uint32_t o = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  return (uint64_t(o) << 32) | uint32_t(~index);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
+  return (uint64_t(order_of(x)) << 32) | uint32_t(~index);
 }
 __device__ __forceinline__ float key_value(uint64_t k) {
   const uint32_t o = uint32_t(k >> 32);
@@ -101,55 +101,75 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 }
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return ~uint32_t(k); }
 
-__device__ __forceinline__ uint64_t cmp_swap(uint64_t k, int mask, bool keep_max) {
-  const uint64_t o = __shfl_xor_sync(~0u, k, mask);
+template <typename K>
+__device__ __forceinline__ K cmp_swap(K k, int mask, bool keep_max) {
+  const K o = __shfl_xor_sync(~0u, k, mask);
   return keep_max ? (k > o ? k : o) : (k < o ? k : o);
 }
 
-// Lane i of the warp gets the i-th largest of its 32 keys.
-__device__ __forceinline__ uint64_t warp_sort(uint64_t k, int lane) {
+// Lane i of the warp gets the i-th largest of its 32 keys; N sets side by side.
+template <int N, typename K>
+__device__ __forceinline__ void warp_sort(K (&k)[N], int lane) {
 #pragma unroll
   for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
     for (int m = size >> 1; m > 0; m >>= 1)
-      k = cmp_swap(k, m, ((lane & size) == 0) == ((lane & m) == 0));
-  return k;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        k[i] = cmp_swap(k[i], m, ((lane & size) == 0) == ((lane & m) == 0));
 }
 
 // The 32 largest of two descending lists of 32 (q: lane i holds the other
 // list's entry 31 - i): the larger of each pair is a bitonic sequence.
-__device__ __forceinline__ uint64_t warp_merge(uint64_t p, uint64_t q, int lane) {
-  uint64_t k = p > q ? p : q;
+template <typename K>
+__device__ __forceinline__ K warp_merge(K p, K q, int lane) {
+  K k = p > q ? p : q;
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) k = cmp_swap(k, m, (lane & m) == 0);
   return k;
 }
 
+// The 32 largest of N descending lists, descending.
+template <int N, typename K>
+__device__ __forceinline__ K warp_merge_all(K (&k)[N], int lane) {
+#pragma unroll
+  for (int n = 1; n < N; n *= 2)
+#pragma unroll
+    for (int i = 0; i + n < N; i += 2 * n)
+      k[i] = warp_merge(k[i], __shfl_sync(~0u, k[i + n], 31 - lane), lane);
+  return k[0];
+}
+
+template <int NT>
 struct LpShared {
-  Stat stat[kLpWarps];
+  Stat stat[NT / 32];
   Stat cta[kLpMaxCluster];             // rank 0: the cluster's parts
-  uint64_t lists[kLpWarps][32];
-  uint64_t tops[kLpMaxCluster * 32];   // rank 0: the cluster's lists
-  uint64_t cand[kLpThreads];
+  uint64_t tops[kLpMaxCluster][32];    // rank 0: the cluster's lists
+  uint64_t lists[NT / 32][32];
+  uint64_t cand[NT];
   uint64_t sorted[32];
+  uint32_t maxima[NT / 4];
+  uint32_t bound;
   int n_cand;
 };
 
 // The 32 largest of one key per thread, descending, in sh.sorted.
-__device__ __forceinline__ void block_top32(LpShared& sh, uint64_t key) {
+template <int NT>
+__device__ __forceinline__ void block_top32(LpShared<NT>& sh, uint64_t key) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t k = warp_sort(key, lane);
-  sh.lists[warp][lane] = k;
+  uint64_t k[1] = {key};
+  warp_sort(k, lane);
+  sh.lists[warp][lane] = k[0];
   __syncthreads();
 #pragma unroll
-  for (int w = kLpWarps / 2; w > 0; w >>= 1) {
+  for (int w = NT / 64; w > 0; w >>= 1) {
     if (warp < w) {
-      k = warp_merge(k, sh.lists[warp + w][31 - lane], lane);
-      sh.lists[warp][lane] = k;
+      k[0] = warp_merge(k[0], sh.lists[warp + w][31 - lane], lane);
+      sh.lists[warp][lane] = k[0];
     }
     __syncthreads();
   }
-  if (warp == 0) sh.sorted[lane] = k;
+  if (warp == 0) sh.sorted[lane] = k[0];
   __syncthreads();
 }
 
@@ -220,17 +240,16 @@ struct Row {
   }
 };
 
-// Adds a thread's N vectors to its state; true if they hold a new maximum.
+// Adds a thread's N vectors to its state.
 template <typename T, bool FULL, int N>
-__device__ __forceinline__ bool add_vectors(Stat& st, const uint4 (&w)[N], float c) {
+__device__ __forceinline__ void add_vectors(Stat& st, const uint4 (&w)[N], float c) {
   constexpr int VE = Row<T>::VE;
   uint32_t top = max_pair(max_pair(w[0].x, w[0].y, T()), max_pair(w[0].z, w[0].w, T()), T());
 #pragma unroll
   for (int u = 1; u < N; ++u)
     top = max_pair(top, max_pair(max_pair(w[u].x, w[u].y, T()), max_pair(w[u].z, w[u].w, T()), T()), T());
   const float gm = Row<T>::largest(top);
-  const bool up = gm > st.m;
-  if (up) rescale(st, gm, c);
+  if (gm > st.m) rescale(st, gm, c);
   if (fabsf(st.m) < 4e4f && c < 1e3f && c > 0.05f) {
     // Exponents by one fma, x c - fl(m c); what rounding m c took, r, is the same for all
     // of them: 2^-r is multiplied out of the sums, so that a common offset of the
@@ -265,13 +284,98 @@ __device__ __forceinline__ bool add_vectors(Stat& st, const uint4 (&w)[N], float
       }
     }
   }
-  return up;
 }
 
-template <typename T, bool FULL>  // FULL: entropy and alternatives may be asked for
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
+// The vectors of the lanes of this warp that `mine` names, read again, a vector per
+// lane: elements whose key reaches `bound` go to sh.cand.
+template <typename T, int NT>
+__device__ __forceinline__ void collect(LpShared<NT>& sh, const Row<T>& row, int lo, int hi,
+                                        bool mine, uint64_t bound) {
   constexpr int VE = Row<T>::VE;
-  __shared__ LpShared sh;
+  const int lane = threadIdx.x & 31;
+  for (uint32_t left = __ballot_sync(~0u, mine); left != 0; left &= left - 1) {
+    const int owner = (threadIdx.x & ~31) + __ffs(left) - 1;
+    // too many already: the rest would be in vain (the lanes leave together)
+    if (__any_sync(~0u, *const_cast<volatile int*>(&sh.n_cand) > NT)) return;
+    for (int i = lo + owner + lane * NT; i < hi; i += 32 * NT) {
+      float x[VE];
+      row.unpack(row.load(i), x);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const uint64_t k = key_of(x[j], uint32_t(i * VE + j - row.off));
+        if (x[j] > -INFINITY && k >= bound) {
+          const int at = atomicAdd(&sh.n_cand, 1);
+          if (at < NT) sh.cand[at] = k;
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// The alternatives of a slice when many elements share the value of the bound: the bound
+// among exact keys, and if the largest logits all lie in a few threads' vectors so
+// that even those are too many, one alternative per round.
+template <typename T, int NT>
+__device__ __noinline__ void top_of_ties(LpShared<NT>& sh, const Row<T>& row, int lo, int hi,
+                                         float thread_max, int n_top) {
+  constexpr int VE = Row<T>::VE;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t key = 0;  // the first place of this thread's maximum
+  if (thread_max > -INFINITY)
+    for (int i = lo + tid; i < hi && key == 0; i += NT) {
+      float x[VE];
+      row.unpack(row.load(i), x);
+#pragma unroll
+      for (int j = VE - 1; j >= 0; --j)
+        if (x[j] == thread_max) key = key_of(x[j], uint32_t(i * VE + j - row.off));
+    }
+  if (tid == 0) sh.n_cand = 0;
+  block_top32(sh, key);
+  const uint64_t bound = max(sh.sorted[n_top - 1], uint64_t(1));
+  collect(sh, row, lo, hi, key >= bound, bound);
+  __syncthreads();
+  const int n = sh.n_cand;
+  if (n <= NT) {
+    block_top32(sh, tid < n ? sh.cand[tid] : 0);
+    return;
+  }
+  uint64_t last = ~uint64_t(0);
+  for (int k = 0; k < n_top; ++k) {
+    uint64_t best = 0;
+    for (int i = lo + tid; i < hi; i += NT) {
+      float x[VE];
+      row.unpack(row.load(i), x);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const uint64_t kk = key_of(x[j], uint32_t(i * VE + j - row.off));
+        if (x[j] > -INFINITY && kk < last && kk > best) best = kk;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(~0u, best, o);
+      best = best > other ? best : other;
+    }
+    if (lane == 0) sh.lists[warp][0] = best;
+    __syncthreads();
+    for (int w = 0; w < NT / 32; ++w) best = max(best, sh.lists[w][0]);
+    last = best;
+    if (tid == 0) sh.sorted[k] = best;
+    __syncthreads();
+    if (best == 0) {
+      if (tid > k && tid < 32) sh.sorted[tid] = 0;
+      break;
+    }
+  }
+  __syncthreads();
+}
+
+// FULL: entropy, log-sum-exp or alternatives are asked for
+template <typename T, bool FULL, int NT>
+__global__ void __launch_bounds__(NT) logprob_kernel(const LpParams P) {
+  constexpr int VE = Row<T>::VE;
+  __shared__ LpShared<NT> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = cluster.num_blocks(), rank = cluster.block_rank();
   cluster.barrier_arrive();  // waited for before the first remote store: every CTA has started
@@ -298,10 +402,9 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
     if (tok >= 0 && tok < P.vocab) tok_x = to_f(first[tok]);
   }
 
-  // one pass: m, s, a of this thread's vectors lo + tid + kLpThreads * i
+  // one pass: m, s, a of this thread's vectors lo + tid + NT * i
   Stat st{-INFINITY, 0.f, 0.f};
-  int best_group = 0;
-  constexpr int kStep = kLpThreads * kLpUnroll;
+  constexpr int kStep = NT * kLpUnroll;
   const int n_groups = (hi - lo + kStep - 1) / kStep;
   for (int g = 0; g < n_groups; ++g) {
     const int g0 = lo + g * kStep;
@@ -309,8 +412,8 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
     if (g0 >= row.full0 && g0 + kStep <= min(hi, row.full1)) {
       const uint4* src = reinterpret_cast<const uint4*>(row.base) + g0 + tid;
 #pragma unroll
-      for (int u = 0; u < kLpUnroll; ++u) w[u] = __ldcs(src + u * kLpThreads);
-      if (add_vectors<T, FULL>(st, w, c)) best_group = g;
+      for (int u = 0; u < kLpUnroll; ++u) w[u] = __ldcs(src + u * NT);
+      add_vectors<T, FULL>(st, w, c);
     } else {
       const T none = T(-INFINITY);
       uint4 blank;
@@ -318,10 +421,10 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
       for (int j = 0; j < VE; ++j) reinterpret_cast<T*>(&blank)[j] = none;
 #pragma unroll
       for (int u = 0; u < kLpUnroll; ++u) {
-        const int i = g0 + tid + u * kLpThreads;
+        const int i = g0 + tid + u * NT;
         w[u] = i < hi ? row.load(i) : blank;
       }
-      if (add_vectors<T, FULL>(st, w, c)) best_group = g;
+      add_vectors<T, FULL>(st, w, c);
     }
   }
   const float thread_max = st.m;
@@ -329,93 +432,57 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) st = join(st, shfl_xor(st, o), c);
   if (lane == 0) sh.stat[warp] = st;
-  if (tid == 0) sh.n_cand = 0;
+  const bool tops = FULL && P.n_top > 0;
+  const uint32_t order = thread_max > -INFINITY ? order_of(thread_max) : 0u;
+  if (tops) {
+    if (tid == 0) sh.n_cand = 0;
+    uint32_t m = max(order, __shfl_xor_sync(~0u, order, 1));
+    m = max(m, __shfl_xor_sync(~0u, m, 2));
+    if ((lane & 3) == 0) sh.maxima[tid / 4] = m;
+  }
   __syncthreads();
   cluster.barrier_wait();
-  if (warp == 0) {
-    st = lane < kLpWarps ? sh.stat[lane] : Stat{-INFINITY, 0.f, 0.f};
+  if (warp == 1) {  // beside warp 0, which looks for the bound
+    st = lane < NT / 32 ? sh.stat[lane] : Stat{-INFINITY, 0.f, 0.f};
 #pragma unroll
-    for (int o = kLpWarps / 2; o > 0; o >>= 1) st = join(st, shfl_xor(st, o), c);
+    for (int o = NT / 64; o > 0; o >>= 1) st = join(st, shfl_xor(st, o), c);
     if (lane == 0) cluster.map_shared_rank(&sh, 0)->cta[rank] = st;
   }
-
-  if (FULL && P.n_top > 0) {
-    // this thread's largest key: the first place of its maximum in its group
-    uint64_t key = 0;
-    if (thread_max > -INFINITY) {
-      for (int u = kLpUnroll - 1; u >= 0; --u) {
-        const int i = lo + tid + (best_group * kLpUnroll + u) * kLpThreads;
-        if (i < hi) {
-          float x[VE];
-          row.unpack(row.load(i), x);
+  if (tops) {
+    if (warp == 0) {
+      uint32_t k[NT / 128];
 #pragma unroll
-          for (int j = VE - 1; j >= 0; --j)
-            if (x[j] == thread_max) key = key_of(x[j], uint32_t(i * VE + j - row.off));
-        }
-      }
-    }
-    block_top32(sh, key);
-    const uint64_t bound = max(sh.sorted[P.n_top - 1], uint64_t(1));
-    uint64_t owner_key = lane < P.n_top ? sh.sorted[lane] : 0;
-    // the threads at or above the bound: warp w takes every kLpWarps-th of them
-    for (int k = warp; k < P.n_top; k += kLpWarps) {
-      const uint64_t ok = __shfl_sync(~0u, owner_key, k);
-      if (ok == 0) break;
-      const int owner = (int(key_index(ok) + row.off) / VE - lo) % kLpThreads;
-      for (int i = lo + owner + lane * kLpThreads; i < hi; i += 32 * kLpThreads) {
-        float x[VE];
-        row.unpack(row.load(i), x);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const uint64_t kk = key_of(x[j], uint32_t(i * VE + j - row.off));
-          if (x[j] > -INFINITY && kk >= bound) {
-            const int at = atomicAdd(&sh.n_cand, 1);
-            if (at < kLpThreads) sh.cand[at] = kk;
-          }
-        }
-      }
+      for (int i = 0; i < NT / 128; ++i) k[i] = sh.maxima[32 * i + lane];
+      warp_sort(k, lane);
+      const uint32_t m = warp_merge_all(k, lane);
+      if (lane == P.n_top - 1) sh.bound = max(m, 1u);
     }
     __syncthreads();
-    const int n = sh.n_cand;
-    if (n <= kLpThreads) {
-      block_top32(sh, tid < n ? sh.cand[tid] : 0);
-    } else {
-      // more candidates than places (the largest logits of a row all in a few
-      // threads' vectors): one alternative per round, the largest key below the last
-      uint64_t last = ~uint64_t(0);
-      for (int k = 0; k < P.n_top; ++k) {
-        uint64_t best = 0;
-        for (int i = lo + tid; i < hi; i += kLpThreads) {
-          float x[VE];
-          row.unpack(row.load(i), x);
-#pragma unroll
-          for (int j = 0; j < VE; ++j) {
-            const uint64_t kk = key_of(x[j], uint32_t(i * VE + j - row.off));
-            if (x[j] > -INFINITY && kk < last && kk > best) best = kk;
-          }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const uint64_t other = __shfl_xor_sync(~0u, best, o);
-          best = best > other ? best : other;
-        }
-        if (lane == 0) sh.lists[warp][0] = best;
-        __syncthreads();
-        for (int w = 0; w < kLpWarps; ++w) best = max(best, sh.lists[w][0]);
-        last = best;
-        if (tid == 0) sh.sorted[k] = best;
-        __syncthreads();
-        if (best == 0) {
-          if (tid > k && tid < 32) sh.sorted[tid] = 0;
-          break;
-        }
-      }
+    const bool mine = order >= sh.bound;
+    // as a rule n_top threads or little more
+    if (__syncthreads_count(mine) <= 2 * P.n_top + 32) {
+      collect(sh, row, lo, hi, mine, uint64_t(sh.bound) << 32);
       __syncthreads();
+      const int n = sh.n_cand;
+      if (n <= 32) {
+        if (warp == 0) {
+          uint64_t k[1] = {lane < n ? sh.cand[lane] : 0};
+          warp_sort(k, lane);
+          sh.sorted[lane] = k[0];
+        }
+      } else if (n <= NT) {
+        block_top32(sh, tid < n ? sh.cand[tid] : 0);
+      } else {
+        top_of_ties(sh, row, lo, hi, thread_max, P.n_top);
+      }
+    } else {
+      top_of_ties(sh, row, lo, hi, thread_max, P.n_top);
     }
-    if (tid < 32) cluster.map_shared_rank(&sh, 0)->tops[rank * 32 + tid] = tid < P.n_top ? sh.sorted[tid] : 0;
+    if (warp == 0)
+      cluster.map_shared_rank(&sh, 0)->tops[rank][lane] = lane < P.n_top ? sh.sorted[lane] : 0;
   }
   cluster.sync();  // the parts of every CTA are in rank 0's shared memory
-  if (rank != 0) return;
+  if (rank != 0 || warp != 0) return;
 
   Stat all = sh.cta[0];
   for (int k = 1; k < nc; ++k) all = join(all, sh.cta[k], c);
@@ -443,23 +510,28 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
     if (FULL && P.entropy)
       P.entropy[o] = bad ? NAN : all.s > 0.f ? ln_s - all.a / all.s * kLn2 : 0.f;
   }
-  if (FULL && P.n_top > 0) {
-    if (nc > 1) block_top32(sh, tid < nc * 32 ? sh.tops[tid] : 0);
-    if (tid < P.n_top) {
-      const uint64_t k = sh.sorted[tid];
+  if (tops) {
+    uint64_t k = sh.tops[0][lane];
+    if (nc > 1) {
+      uint64_t list[kLpMaxCluster];
+#pragma unroll
+      for (int i = 0; i < kLpMaxCluster; ++i) list[i] = i < nc ? sh.tops[i][lane] : 0;
+      k = warp_merge_all(list, lane);
+    }
+    if (lane < P.n_top) {
       const bool none = k == 0 || bad;
-      P.top_ids[o * P.n_top + tid] = none ? -1 : int32_t(key_index(k));
-      P.top_lp[o * P.n_top + tid] =
+      P.top_ids[o * P.n_top + lane] = none ? -1 : int32_t(key_index(k));
+      P.top_lp[o * P.n_top + lane] =
           bad ? NAN : k == 0 ? -INFINITY : (key_value(k) - all.m) * P.scale - ln_s;
     }
   }
 }
 
-template <typename T, bool FULL>
+template <typename T, bool FULL, int NT>
 sekv_status launch_logprobs(const LpParams& P, int64_t rows, int nc, cudaStream_t stream) {
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3(unsigned(rows * nc));
-  lc.blockDim = dim3(kLpThreads);
+  lc.blockDim = dim3(NT);
   lc.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -468,7 +540,7 @@ sekv_status launch_logprobs(const LpParams& P, int64_t rows, int nc, cudaStream_
   at[0].val.clusterDim.z = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, logprob_kernel<T, FULL>, P) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&lc, logprob_kernel<T, FULL, NT>, P) != cudaSuccess) {
     cudaGetLastError();
     return SEKV_ERR_CUDA;
   }
@@ -476,25 +548,29 @@ sekv_status launch_logprobs(const LpParams& P, int64_t rows, int nc, cudaStream_
   return SEKV_OK;
 }
 
-sekv_status logprobs_impl(LpParams& P, int32_t dtype, int64_t batch, bool full,
-                          cudaStream_t stream) {
-  const int64_t rows = batch * P.n_tokens;
+template <typename T>
+sekv_status logprobs_of(const LpParams& P, int64_t rows, bool full, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return SEKV_ERR_CUDA;
   // CTAs per row: doubled while the rows alone leave SMs without a CTA and a
   // CTA's share is more than one vector per thread
-  const int64_t vecs = P.vocab * (dtype == SEKV_F32 ? 4 : 2) / 16 + 1;
+  const int64_t vecs = P.vocab / Row<T>::VE + 1;
   int nc = 1;
-  while (nc < 8 && rows * nc < 2 * sms && vecs > int64_t(nc) * kLpThreads) nc *= 2;
+  while (nc < kLpMaxCluster && rows * nc < sms && vecs > int64_t(nc) * 512) nc *= 2;
   if (rows * nc > INT32_MAX) return SEKV_ERR_UNSUPPORTED;
-  if (dtype == SEKV_F32)
-    return full ? launch_logprobs<float, true>(P, rows, nc, stream)
-                : launch_logprobs<float, false>(P, rows, nc, stream);
-  if (dtype == SEKV_F16)
-    return full ? launch_logprobs<__half, true>(P, rows, nc, stream)
-                : launch_logprobs<__half, false>(P, rows, nc, stream);
-  return full ? launch_logprobs<__nv_bfloat16, true>(P, rows, nc, stream)
-              : launch_logprobs<__nv_bfloat16, false>(P, rows, nc, stream);
+  if (vecs / nc <= 1024)
+    return full ? launch_logprobs<T, true, 256>(P, rows, nc, stream)
+                : launch_logprobs<T, false, 256>(P, rows, nc, stream);
+  return full ? launch_logprobs<T, true, 512>(P, rows, nc, stream)
+              : launch_logprobs<T, false, 512>(P, rows, nc, stream);
+}
+
+sekv_status logprobs_impl(const LpParams& P, int32_t dtype, int64_t batch, bool full,
+                          cudaStream_t stream) {
+  const int64_t rows = batch * P.n_tokens;
+  if (dtype == SEKV_F32) return logprobs_of<float>(P, rows, full, stream);
+  if (dtype == SEKV_F16) return logprobs_of<__half>(P, rows, full, stream);
+  return logprobs_of<__nv_bfloat16>(P, rows, full, stream);
 }
 
 sekv_status check_logits(const void* logits, int32_t dtype, int64_t batch, int64_t n_tokens,

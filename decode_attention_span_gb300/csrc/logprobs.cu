@@ -373,7 +373,7 @@ __device__ __noinline__ void top_of_ties(LpShared<NT>& sh, const Row<T>& row, in
 
 // FULL: entropy, log-sum-exp or alternatives are asked for
 template <typename T, bool FULL, int NT>
-__global__ void __launch_bounds__(NT) logprob_kernel(const LpParams P) {
+__global__ void __launch_bounds__(NT, NT == 512 ? 3 : 1) logprob_kernel(const LpParams P) {
   constexpr int VE = Row<T>::VE;
   __shared__ LpShared<NT> sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -558,6 +558,9 @@ sekv_status logprobs_of(const LpParams& P, int64_t rows, bool full, cudaStream_t
   int nc = 1;
   while (nc < kLpMaxCluster && rows * nc < sms && vecs > int64_t(nc) * 512) nc *= 2;
   if (rows * nc > INT32_MAX) return SEKV_ERR_UNSUPPORTED;
+  if (vecs / nc <= 256)
+    return full ? launch_logprobs<T, true, 128>(P, rows, nc, stream)
+                : launch_logprobs<T, false, 128>(P, rows, nc, stream);
   if (vecs / nc <= 1024)
     return full ? launch_logprobs<T, true, 256>(P, rows, nc, stream)
                 : launch_logprobs<T, false, 256>(P, rows, nc, stream);

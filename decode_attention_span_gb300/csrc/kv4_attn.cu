@@ -32,14 +32,16 @@ using namespace sekv;
 
 namespace {
 
-constexpr int kAttnWarps = 16;
+constexpr int kAttnWarps = 12;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 constexpr int kChunkTokens = 32;
 constexpr int kChunkBytes = 2 * kKv4TileBytes;
 constexpr int kMaxCtas = 256;                    // of a launch
 constexpr int kCols = 8;                         // (token, head) pairs of a block
 constexpr int kStateFloats = kCols * (kHeadDim + 2);  // o, m, l
+// What a second group costs a CTA (its plan, queries, first copies and join, about 6 us), in chunks
+constexpr int kGroupCost = 40;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct AttnShared {
@@ -55,15 +57,19 @@ struct AttnShared {
   uint4 qb[4][32];
   float q_sum[2][kCols], q_off[2][kCols], q_scale[kCols];
   uint64_t bar[kAttnWarps][kStages];
-  int before[SEKV_KV4_MAX_BATCH + 1];  // chunks before each sequence
+  int before[SEKV_KV4_MAX_BATCH + 1];  // chunks (or pieces) before each sequence
   int len[SEKV_KV4_MAX_BATCH];         // tokens of each sequence
+  int piece;                           // chunks of a piece, 0: pieces cross groups
   int last;
 };
+// The join of partials: kJoinParts sets of threads take every kJoinParts-th partial each.
+constexpr int kJoinThreads = kCols * kHeadDim / 4 / 2;  // two float4 a thread
+constexpr int kJoinParts = kAttnThreads / kJoinThreads;
 // scratch of the last CTA of a group, over the warps' values
 struct JoinShared {
   float w[kMaxCtas][kCols];   // maxima, then weights
   float l[kMaxCtas][kCols];
-  float4 half[kCols * kHeadDim / 4];
+  float4 part[kJoinParts - 1][2][kJoinThreads];
 };
 static_assert(sizeof(JoinShared) <= sizeof(AttnShared::o), "the join's scratch lies over the warps' values");
 
@@ -150,6 +156,10 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float q_value(__nv_bfloat16 q) { return __bfloat162float(q); }
 __device__ __forceinline__ float q_value(__half q) { return __half2float(q); }
 
+__device__ __forceinline__ int chunks_of(int len) {
+  return max(1, (len + kChunkTokens - 1) / kChunkTokens);
+}
+
 // A warp's softmax state of one group.  A lane holds columns 2t and 2t + 1, and of
 // the values dimensions 8g .. 8g + 7 of both groups of dimensions; l and c are sums
 // over its own tokens (rows g and g + 8 of each tile).
@@ -217,8 +227,10 @@ struct Query {
 };
 
 // EDGE: some token of the chunk is not seen by some column (seen: per column of the
-// lane; held: tokens of the chunk that the sequence has).
-template <bool EDGE>
+// lane; held: tokens of the chunk that the sequence has).  PACK: only four columns are in
+// use; columns 4-7 hold the same queries again, and their lanes put the weights' lower
+// parts in, so that one product does for both.
+template <bool EDGE, bool PACK>
 __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const uint8_t* chunk,
                                            int lane, int held, const int (&seen)[2]) {
   const int g = lane >> 2;
@@ -333,6 +345,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
   for (int ti = 0; ti < 2; ++ti) {
     const uint8_t* tile = chunk + ti * kKv4TileBytes;
     uint32_t bh[2][2], bl[2][2];  // [group of dimensions][row half]: B operands, upper and lower part
+    const float low = lane & 2 ? -1.f : 0.f;  // PACK: this lane's columns take the lower parts
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint32_t sz[2] = {vp[ti][e].x, vp[ti][e].y};
@@ -354,9 +367,14 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
         }
         const __half2 h = __floats2half2_rn(w[gr][0], w[gr][1]);
         const float2 hf = __half22float2(h);
-        const __half2 l = __floats2half2_rn(w[gr][0] - hf.x, w[gr][1] - hf.y);
-        bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
-        bl[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&l));
+        if (PACK) {
+          const __half2 v = __floats2half2_rn(fmaf(low, hf.x, w[gr][0]), fmaf(low, hf.y, w[gr][1]));
+          bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&v));
+        } else {
+          const __half2 l = __floats2half2_rn(w[gr][0] - hf.x, w[gr][1] - hf.y);
+          bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
+          bl[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&l));
+        }
       }
     }
     const uint4 v0 = *reinterpret_cast<const uint4*>(tile + kKv4V + lane * 16);
@@ -370,13 +388,15 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
       const uint32_t a0[4] = {r0[0], r0[2], r1[0], r1[2]}, a1[4] = {r0[1], r0[3], r1[1], r1[3]};
       mma_f16(S.o[2 * m], a0, bh[m >> 1][0], bh[m >> 1][1]);
       mma_f16(S.o[2 * m + 1], a1, bh[m >> 1][0], bh[m >> 1][1]);
-      mma_f16(S.o[2 * m], a0, bl[m >> 1][0], bl[m >> 1][1]);
-      mma_f16(S.o[2 * m + 1], a1, bl[m >> 1][0], bl[m >> 1][1]);
+      if (!PACK) {
+        mma_f16(S.o[2 * m], a0, bl[m >> 1][0], bl[m >> 1][1]);
+        mma_f16(S.o[2 * m + 1], a1, bl[m >> 1][0], bl[m >> 1][1]);
+      }
     }
   }
 }
 
-template <typename T>
+template <typename T, bool PACK>
 __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnParams P) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   AttnShared& sh = *reinterpret_cast<AttnShared*>(smem_raw);
@@ -387,19 +407,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
   if (lane == 0)
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.bar[warp][s], 1);
   fence_mbar_init();
-  // chunks of each sequence (at least one, so that every group has a CTA)
+  // The plan, by one warp.  Chunks of each sequence (at least one, so that every group
+  // has a CTA), then either every group cut into pieces of at most `piece` chunks, a CTA
+  // each, or the line of all groups' chunks cut into equal pieces.
   const int cap = P.pg.max_pages * kKv4Page;
   if (warp == 0) {
+    int sum = 0, longest = 1;
+    for (int b = lane; b < P.batch; b += 32) {
+      const int given = P.seq_len[b];
+      const int len = min(max(given, 0), cap);
+      if (given != len && blockIdx.x == 0) set_device_error(P.pg.status, DEV_BAD_LIST, b);
+      sh.len[b] = len;
+      sum += chunks_of(len);
+      longest = max(longest, chunks_of(len));
+    }
+    sum = __reduce_add_sync(~0u, sum);
+    longest = __reduce_max_sync(~0u, longest);
+    __syncwarp();
+    // smallest piece for which the groups' pieces fit the grid: the line's share, or
+    // more; taken if it costs less than the second group of a CTA would
+    const int n_cta = int(gridDim.x), share = (sum * per_seq + n_cta - 1) / n_cta;
+    int piece = 0;
+    if (P.batch * per_seq <= n_cta) {
+      int lo = max(share, 1), hi = longest;  // hi always fits
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        int n = 0;
+        for (int b = lane; b < P.batch; b += 32) n += (chunks_of(sh.len[b]) + mid - 1) / mid;
+        if (__reduce_add_sync(~0u, n) * per_seq <= n_cta) hi = mid; else lo = mid + 1;
+      }
+      if (lo <= share + kGroupCost) piece = lo;
+    }
     int run = 0;
     for (int b0 = 0; b0 < P.batch; b0 += 32) {
       const int b = b0 + lane;
       int n = 0;
       if (b < P.batch) {
-        const int given = P.seq_len[b];
-        const int len = min(max(given, 0), cap);
-        if (given != len && blockIdx.x == 0) set_device_error(P.pg.status, DEV_BAD_LIST, b);
-        sh.len[b] = len;
-        n = max(1, (len + kChunkTokens - 1) / kChunkTokens) * per_seq;
+        n = chunks_of(sh.len[b]);
+        if (piece > 0) n = (n + piece - 1) / piece;
+        n *= per_seq;
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -409,14 +455,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       if (b < P.batch) sh.before[b + 1] = run + n;
       run += __shfl_sync(~0u, n, 31);
     }
-    if (lane == 0) sh.before[0] = 0;
+    if (lane == 0) {
+      sh.before[0] = 0;
+      sh.piece = piece;
+    }
   }
   __syncthreads();
+  const bool by_piece = sh.piece > 0;
   const int total = sh.before[P.batch];
   const int n_cta = min(int(gridDim.x), total);
   const int cta = blockIdx.x;
   if (cta >= n_cta) return;
-  // piece of CTA c: [start(c), start(c + 1)), start(c) = total * c / n_cta
+  // CTA c's share of the line: [start(c), start(c + 1)), start(c) = total * c / n_cta (by
+  // piece: total == n_cta, and the units of the line are the pieces)
   const int each = total / n_cta, over = total - each * n_cta;
   auto start = [&](int c) { return each * c + over * c / n_cta; };
   const int u0 = start(cta), u1 = start(cta + 1);
@@ -432,26 +483,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       if (n < 32) break;
     }
     const int len = sh.len[b];
-    const int n_chunks = (sh.before[b + 1] - sh.before[b]) / per_seq;
+    const int n_units = (sh.before[b + 1] - sh.before[b]) / per_seq;  // of a group
     const int rel = u - sh.before[b];
-    const int gi = rel / n_chunks;
-    const int c0 = rel - gi * n_chunks;
-    const int c1 = min(n_chunks, c0 + (u1 - u));
+    const int gi = rel / n_units;
+    const int i0 = rel - gi * n_units, i1 = min(n_units, i0 + (u1 - u));
+    // this segment's chunks of the group
+    const int c0 = by_piece ? int(int64_t(chunks_of(len)) * i0 / n_units) : i0;
+    const int c1 = by_piece ? int(int64_t(chunks_of(len)) * i1 / n_units) : i1;
     const int blk = gi / P.pg.hkv, head = gi - blk * P.pg.hkv;
     const int cols = min(P.tpb, P.n_q - blk * P.tpb) * P.hpg;
 
     // The queries' loads go out first: behind the copies they would wait for them.
-    const int tok = blk * P.tpb + g / P.hpg;  // of this lane's column of the B operand
+    const int qcol = PACK ? g & 3 : g;            // this lane's column of the B operand
+    const int tok = blk * P.tpb + qcol / P.hpg;   // its query token
     union {
       uint4 w[4];   // sixteen dimensions of either group
       T e[32];
     } qv;
     {
       const T* q = static_cast<const T*>(P.q) +
-                   ((int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + g % P.hpg) * kHeadDim;
+                   ((int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + qcol % P.hpg) * kHeadDim;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        qv.w[i] = warp == 0 && g < cols ? __ldg(reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + t * 16) + (i & 1))
+        qv.w[i] = warp == 0 && qcol < cols ? __ldg(reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + t * 16) + (i & 1))
                            : make_uint4(0, 0, 0, 0);
     }
 
@@ -507,7 +561,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
         Q.offset[c][gr] = sh.q_off[gr][col];
       }
       Q.scale_log2[c] = sh.q_scale[col];
-      see[c] = col < cols ? len - (P.n_q - 1 - (blk * P.tpb + col / P.hpg)) : 0;
+      const int real = PACK ? col & 3 : col;
+      see[c] = real < cols ? len - (P.n_q - 1 - (blk * P.tpb + real / P.hpg)) : 0;
     }
     // up to here no token is hidden from any column in use
     const int open = len - (P.n_q - 1 - blk * P.tpb);
@@ -532,9 +587,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
           const int held = len - pos;
           const int seen[2] = {see[0] - pos, see[1] - pos};
           if (pos + kChunkTokens <= open)
-            chunk_step<false>(S, Q, sh.ring[warp][st], lane, held, seen);
+            chunk_step<false, PACK>(S, Q, sh.ring[warp][st], lane, held, seen);
           else
-            chunk_step<true>(S, Q, sh.ring[warp][st], lane, held, seen);
+            chunk_step<true, PACK>(S, Q, sh.ring[warp][st], lane, held, seen);
         } else {
           // a copy did not land: nothing more is copied or waited for by this warp, and
           // what is still in flight gets its time to land before the CTA may end
@@ -551,6 +606,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
 
     // the warps' states into shared memory
     const float inv_unit = 1.f / S.unit;
+    if (PACK) {  // the lower parts' sums to the upper ones'
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S.o[j][i] += __shfl_xor_sync(~0u, S.o[j][i], 2);
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -586,7 +647,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     }
     __syncthreads();
 
-    const int gs = sh.before[b] + gi * n_chunks, ge = gs + n_chunks;
+    const int gs = sh.before[b] + gi * n_units, ge = gs + n_units;
     const bool whole = u0 <= gs && ge <= u1;
     const int64_t group = int64_t(b) * per_seq + gi;
     auto write_out = [&](int col, int d, float4 v, float mx, float sum) {
@@ -640,6 +701,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
           jn.l[i / kCols][i % kCols] = __ldcg(p + kCols);
         }
         __syncthreads();
+        static_assert(kAttnWarps >= kCols, "a warp per column");
         if (warp < kCols) {
           float mx = -INFINITY, sum = 0.f;
           for (int i = lane; i < n; i += 32) mx = fmaxf(mx, jn.w[i][warp]);
@@ -658,27 +720,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
           }
         }
         __syncthreads();
-        // two halves of the partials side by side, several loads in flight
-        const int f4 = tid % (kCols * kHeadDim / 4), col = f4 / (kHeadDim / 4);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int i = tid / (kCols * kHeadDim / 4); i < n; i += 2) {
-          const float f = jn.w[i][col];
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(slot(i)) + f4);
-          v.x = fmaf(f, x.x, v.x); v.y = fmaf(f, x.y, v.y);
-          v.z = fmaf(f, x.z, v.z); v.w = fmaf(f, x.w, v.w);
+        const int at = tid % kJoinThreads, set = tid / kJoinThreads;
+        float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+        for (int i = set; i < n; i += kJoinParts) {
+          const float4* p = reinterpret_cast<const float4*>(slot(i));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = jn.w[i][(at + h * kJoinThreads) / (kHeadDim / 4)];
+            const float4 x = __ldcg(p + at + h * kJoinThreads);
+            v[h].x = fmaf(f, x.x, v[h].x); v[h].y = fmaf(f, x.y, v[h].y);
+            v[h].z = fmaf(f, x.z, v[h].z); v[h].w = fmaf(f, x.w, v[h].w);
+          }
         }
-        if (tid >= kCols * kHeadDim / 4) jn.half[f4] = v;
+        if (set > 0)
+          for (int h = 0; h < 2; ++h) jn.part[set - 1][h][at] = v[h];
         __syncthreads();
-        if (tid < kCols * kHeadDim / 4 && col < cols) {
-          const float4 x = jn.half[f4];
-          write_out(col, f4 % (kHeadDim / 4) * 4,
-                    make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w), sh.mx[col], sh.sum[col]);
+        if (set == 0) {
+          for (int h = 0; h < 2; ++h) {
+            for (int k = 0; k < kJoinParts - 1; ++k) {
+              const float4 x = jn.part[k][h][at];
+              v[h].x += x.x; v[h].y += x.y; v[h].z += x.z; v[h].w += x.w;
+            }
+            const int f4 = at + h * kJoinThreads, col = f4 / (kHeadDim / 4);
+            if (col < cols) write_out(col, f4 % (kHeadDim / 4) * 4, v[h], sh.mx[col], sh.sum[col]);
+          }
         }
       }
     }
     __syncthreads();  // the shared states are free again
-    u += c1 - c0;
+    u += i1 - i0;
   }
 }
 
@@ -772,8 +843,12 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
   P.tpb = kCols / P.hpg;
   P.n_blk = blocks_of(cfg, n_q);
   P.scale_log2 = scale * kLog2e;
-  const void* fn = dtype == SEKV_BF16 ? reinterpret_cast<const void*>(kv4_attn_kernel<__nv_bfloat16>)
-                                      : reinterpret_cast<const void*>(kv4_attn_kernel<__half>);
+  const bool pack = n_q * P.hpg <= kCols / 2;
+  const void* const fns[4] = {reinterpret_cast<const void*>(kv4_attn_kernel<__nv_bfloat16, false>),
+                              reinterpret_cast<const void*>(kv4_attn_kernel<__half, false>),
+                              reinterpret_cast<const void*>(kv4_attn_kernel<__nv_bfloat16, true>),
+                              reinterpret_cast<const void*>(kv4_attn_kernel<__half, true>)};
+  const void* fn = fns[(dtype == SEKV_BF16 ? 0 : 1) + (pack ? 2 : 0)];
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AttnShared)) !=
       cudaSuccess) {
     cudaGetLastError();

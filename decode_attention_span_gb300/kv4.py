@@ -7,7 +7,7 @@ import ctypes
 
 import torch
 
-from .sekv import (DTYPES, Config, Workspace, _check, check_tensor, lib, on_current_device,
+from .sekv import (DTYPES, Config, Workspace, _check, check_tensor, current_index, lib,
                    raw_stream)
 
 PAGE_TOKENS = 64
@@ -32,10 +32,9 @@ class Kv4Cache:
     tensors are the caller's; the table may be rewritten between calls."""
 
     def __init__(self, cfg: Config, pages: torch.Tensor, page_table: torch.Tensor):
-        dev = pages.device
-        on_current_device(dev)
-        check_tensor(pages, "pages", (torch.uint8,), dev)
-        check_tensor(page_table, "page_table", (torch.int32,), dev)
+        index = current_index(pages, "pages")
+        check_tensor(pages, "pages", (torch.uint8,), index)
+        check_tensor(page_table, "page_table", (torch.int32,), index)
         if (pages.dim() != 3 or pages.shape[1:] != (cfg.n_kv_heads, PAGE_BYTES) or
                 not pages.is_contiguous()):
             raise ValueError(f"pages: expected contiguous [n][{cfg.n_kv_heads}][{PAGE_BYTES}], got "
@@ -44,7 +43,7 @@ class Kv4Cache:
                 not page_table.is_contiguous()):
             raise ValueError(f"page_table: expected contiguous [{cfg.batch}][max_pages], got "
                              f"{tuple(page_table.shape)}")
-        self.pages, self.page_table, self.device = pages, page_table, dev
+        self.pages, self.page_table, self.device = pages, page_table, pages.device
         self.batch, self.n_kv_heads = cfg.batch, cfg.n_kv_heads
         self._struct = SekvKv4Cache(pages.data_ptr(), page_table.data_ptr(), pages.shape[0],
                                     page_table.shape[1])
@@ -54,17 +53,20 @@ class Kv4Cache:
 def _common(cfg, cache, ws) -> int:
     if cfg.batch != cache.batch or cfg.n_kv_heads != cache.n_kv_heads:
         raise ValueError("cache: made for another batch or number of KV heads")
-    if ws.buf.device != cache.device:
+    index = current_index(cache.pages, "pages")
+    if ws.buf.get_device() != index:
         raise ValueError(f"workspace: on {ws.buf.device}, cache on {cache.device}")
-    return on_current_device(cache.device)
+    return index
 
 
 _I32 = (torch.int32,)
+_F32 = (torch.float32,)
 
 
-def _per_seq(t, name, cfg, dev):
-    check_tensor(t, name, _I32, dev)
-    if t.shape != (cfg.batch,) or not t.is_contiguous():
+def _per_seq(t, name, cfg, index):
+    check_tensor(t, name, _I32, index)
+    s = t.shape
+    if len(s) != 1 or s[0] != cfg.batch or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous [{cfg.batch}], got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -72,8 +74,8 @@ def _per_seq(t, name, cfg, dev):
 _Stride = ctypes.c_int64 * 3
 
 
-def _rows(x, name, dtypes, cfg, n, dev):
-    check_tensor(x, name, dtypes, dev)
+def _rows(x, name, dtypes, cfg, n, index):
+    check_tensor(x, name, dtypes, index)
     s = x.stride()
     if x.shape != (cfg.batch, n, cfg.n_kv_heads, 128) or s[3] != 1:
         raise ValueError(f"{name}: expected [{cfg.batch}][T][{cfg.n_kv_heads}][128] with "
@@ -87,12 +89,11 @@ def kv4_append(cfg: Config, cache: Kv4Cache, k, v, first, ws: Workspace, n_valid
     8 with the last one 1) at token positions first[b] .. first[b] + T - 1 of each
     sequence; with n_valid [B], only its first n_valid[b] rows."""
     index = _common(cfg, cache, ws)
-    dev = cache.device
     T = k.shape[1] if k.dim() == 4 else 0
-    ks = _rows(k, "k", _HALF, cfg, T, dev)
-    vs = _rows(v, "v", (k.dtype,), cfg, T, dev)
-    f = _per_seq(first, "first", cfg, dev)
-    n = None if n_valid is None else _per_seq(n_valid, "n_valid", cfg, dev)
+    ks = _rows(k, "k", _HALF, cfg, T, index)
+    vs = _rows(v, "v", (k.dtype,), cfg, T, index)
+    f = _per_seq(first, "first", cfg, index)
+    n = None if n_valid is None else _per_seq(n_valid, "n_valid", cfg, index)
     st = lib().sekv_kv4_append(ctypes.byref(cfg.c()), cache._c, DTYPES[k.dtype], k.data_ptr(), ks,
                                v.data_ptr(), vs, T, f, n, ws.buf.data_ptr(), ws.nbytes,
                                raw_stream(stream, index))
@@ -110,7 +111,7 @@ def kv4_read(cfg: Config, cache: Kv4Cache, first, n_tokens: int, ws: Workspace,
     shape = (cfg.batch, cfg.n_kv_heads, n_tokens, 128)
     n = None
     if n_valid is not None:
-        n = _per_seq(n_valid, "n_valid", cfg, dev)
+        n = _per_seq(n_valid, "n_valid", cfg, index)
     if out is None:
         if dtype not in DTYPES:
             raise TypeError(f"dtype: expected one of {list(DTYPES)}, got {dtype}")
@@ -118,11 +119,11 @@ def kv4_read(cfg: Config, cache: Kv4Cache, first, n_tokens: int, ws: Workspace,
         k, v = make(shape, dtype=dtype, device=dev), make(shape, dtype=dtype, device=dev)
     else:
         k, v = out
-        check_tensor(k, "out[0]", DTYPES, dev)
-        check_tensor(v, "out[1]", (k.dtype,), dev)
+        check_tensor(k, "out[0]", DTYPES, index)
+        check_tensor(v, "out[1]", (k.dtype,), index)
         if k.shape != shape or v.shape != shape or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError(f"out: expected contiguous {shape}")
-    f = _per_seq(first, "first", cfg, dev)
+    f = _per_seq(first, "first", cfg, index)
     st = lib().sekv_kv4_read(ctypes.byref(cfg.c()), cache._c, DTYPES[k.dtype], k.data_ptr(),
                              v.data_ptr(), n_tokens, f, n, ws.buf.data_ptr(), ws.nbytes,
                              raw_stream(stream, index))
@@ -137,23 +138,25 @@ def kv4_attention(cfg: Config, cache: Kv4Cache, q, seq_len, scale: float, ws: Wo
     tokens of each sequence, the query tokens being its last n_q; returns out
     [B][n_q][Hq][128] f32 and lse [B][n_q][Hq] f32."""
     index = _common(cfg, cache, ws)
-    dev = cache.device
-    check_tensor(q, "q", _HALF, dev)
+    check_tensor(q, "q", _HALF, index)
     shape = q.shape
     if len(shape) != 4 or shape[0] != cfg.batch or shape[2] != cfg.n_q_heads or \
             shape[3] != 128 or not q.is_contiguous():
         raise ValueError(f"q: expected contiguous [{cfg.batch}][n_q][{cfg.n_q_heads}][128], got "
                          f"{tuple(shape)}")
-    for name, t, want in (("out", out, shape), ("lse", lse, shape[:3])):
-        if t is not None:
-            check_tensor(t, name, (torch.float32,), dev)
-            if t.shape != want or not t.is_contiguous():
-                raise ValueError(f"{name}: expected contiguous {tuple(want)}")
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = torch.empty(shape, dtype=torch.float32, device=cache.device)
+    else:
+        check_tensor(out, "out", _F32, index)
+        if out.shape != shape or not out.is_contiguous():
+            raise ValueError(f"out: expected contiguous {tuple(shape)}")
     if lse is None:
-        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
-    s = _per_seq(seq_len, "seq_len", cfg, dev)
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=cache.device)
+    else:
+        check_tensor(lse, "lse", _F32, index)
+        if lse.shape != shape[:3] or not lse.is_contiguous():
+            raise ValueError(f"lse: expected contiguous {tuple(shape[:3])}")
+    s = _per_seq(seq_len, "seq_len", cfg, index)
     st = lib().sekv_kv4_attention(ctypes.byref(cfg.c()), cache._c, DTYPES[q.dtype], q.data_ptr(),
                                   shape[1], s, scale, out.data_ptr(), lse.data_ptr(),
                                   ws.buf.data_ptr(), ws.nbytes, raw_stream(stream, index))

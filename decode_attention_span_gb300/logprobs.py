@@ -7,7 +7,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .sekv import DTYPES, Workspace, _check, check_tensor, lib, on_current_device, raw_stream
+from .sekv import DTYPES, Workspace, _check, check_tensor, current_index, lib, raw_stream
 
 
 class TokenLogprobs(NamedTuple):
@@ -22,27 +22,27 @@ _IDS = (torch.int32, torch.int64)
 
 
 def _rows(logits, tokens, ws):
-    """(device, device index, type, batch, rows of a sequence, vocabulary, strides of logits,
-    stride of tokens) of [T][V] or [B][T][V] logits."""
+    """(device index, type, batch, rows of a sequence, vocabulary, strides of logits, stride of
+    tokens) of [T][V] or [B][T][V] logits."""
     dtype = DTYPES.get(logits.dtype)
     if dtype is None:
         raise TypeError(f"logits: expected one of {list(DTYPES)}, got {logits.dtype}")
-    dev = logits.device
-    index = on_current_device(dev)
-    shape, ls = logits.shape, logits.stride()
-    if len(shape) not in (2, 3) or ls[-1] != 1:
+    index = current_index(logits, "logits")
+    s, ls = logits.shape, logits.stride()
+    n = len(s)
+    if n not in (2, 3) or ls[-1] != 1:
         raise ValueError(f"logits: expected [T][V] or [B][T][V] with consecutive entries, got "
-                         f"{tuple(shape)}")
-    check_tensor(tokens, "tokens", _IDS, dev)
+                         f"{tuple(s)}")
+    check_tensor(tokens, "tokens", _IDS, index)
     ts = tokens.stride()
-    if tokens.shape != shape[:-1] or (shape[-2] > 1 and ts[-1] != 1):
-        raise ValueError(f"tokens: expected {tuple(shape[:-1])} with consecutive entries, got "
+    if tokens.shape != s[:-1] or (s[-2] > 1 and ts[-1] != 1):
+        raise ValueError(f"tokens: expected {tuple(s[:-1])} with consecutive entries, got "
                          f"{tuple(tokens.shape)}")
-    if ws.buf.device != dev:
-        raise ValueError(f"workspace: on {ws.buf.device}, tensors on {dev}")
-    if len(shape) == 2:
-        return dev, index, dtype, 1, shape[0], shape[1], 0, ls[0], 0
-    return dev, index, dtype, shape[0], shape[1], shape[2], ls[0], ls[1], ts[0]
+    if ws.buf.get_device() != index:
+        raise ValueError(f"workspace: on {ws.buf.device}, tensors on {logits.device}")
+    if n == 2:
+        return index, dtype, 1, s[0], s[1], 0, ls[0], 0
+    return index, dtype, s[0], s[1], s[2], ls[0], ls[1], ts[0]
 
 
 def token_logprobs(logits, tokens, ws: Workspace, n_top: int = 0, scale: float = 1.0,
@@ -51,18 +51,18 @@ def token_logprobs(logits, tokens, ws: Workspace, n_top: int = 0, scale: float =
     ([T][V] or [B][T][V]; bf16, f16 or f32) times `scale` (1 / temperature), with
     log-sum-exp and entropy (entropy=False: neither) and the n_top (at most 32)
     likeliest tokens.  `ws` is any workspace: bad token ids go to its status."""
-    dev, index, dtype, B, T, V, sb, st, tb = _rows(logits, tokens, ws)
+    index, dtype, B, T, V, sb, st, tb = _rows(logits, tokens, ws)
     shape = tokens.shape
-    f32 = torch.float32
-    lp = torch.empty(shape, dtype=f32, device=dev)
+    empty, f32, dev = torch.empty, torch.float32, logits.device
+    lp = empty(shape, dtype=f32, device=dev)
     lse = ent = ids = tlp = None
     p_lse = p_ent = p_ids = p_tlp = None
     if entropy:
-        lse, ent = torch.empty(shape, dtype=f32, device=dev), torch.empty(shape, dtype=f32, device=dev)
+        lse, ent = empty(shape, dtype=f32, device=dev), empty(shape, dtype=f32, device=dev)
         p_lse, p_ent = lse.data_ptr(), ent.data_ptr()
     if n_top > 0:
-        ids = torch.empty((*shape, n_top), dtype=torch.int32, device=dev)
-        tlp = torch.empty((*shape, n_top), dtype=f32, device=dev)
+        ids = empty((*shape, n_top), dtype=torch.int32, device=dev)
+        tlp = empty((*shape, n_top), dtype=f32, device=dev)
         p_ids, p_tlp = ids.data_ptr(), tlp.data_ptr()
     if B * T > 0:
         err = lib().sekv_token_logprobs(logits.data_ptr(), dtype, B, T, V, sb, st,
@@ -79,11 +79,11 @@ def surprisal(logits, tokens, ws: Workspace, out=None, stream=None):
     each token given those before it, 0 for the first; what build_spans takes."""
     if logits.dim() != 3:
         raise ValueError(f"logits: expected [B][T][V], got {tuple(logits.shape)}")
-    dev, index, dtype, B, T, V, sb, st, tb = _rows(logits, tokens, ws)
+    index, dtype, B, T, V, sb, st, tb = _rows(logits, tokens, ws)
     if out is None:
-        out = torch.empty(B, T, dtype=torch.float32, device=dev)
+        out = torch.empty(B, T, dtype=torch.float32, device=logits.device)
     else:
-        check_tensor(out, "out", (torch.float32,), dev)
+        check_tensor(out, "out", (torch.float32,), index)
         if out.shape != (B, T) or not out.is_contiguous():
             raise ValueError(f"out: expected contiguous [{B}][{T}], got {tuple(out.shape)}")
     if B * T > 0:

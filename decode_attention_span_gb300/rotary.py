@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from .sekv import DTYPES, _check, _ptr, check_tensor, lib, on_current_device, raw_stream
+from .sekv import DTYPES, _check, _ptr, check_tensor, current_index, lib, raw_stream
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "banded": 4}
 
@@ -66,31 +66,30 @@ class RopePlan:
         self.config, self._c = config, ctypes.byref(config)
         self.rot_dim = int(rot_dim)
         self.freqs = freqs.to(device or "cuda")
-        self.freqs_ptr = self.freqs.data_ptr()
+        self.freqs_ptr, self.device_index = self.freqs.data_ptr(), self.freqs.get_device()
 
 
 _POSITIONS = (torch.int32, torch.int64)
 
 
-def _heads(name, x, y, shape, dtype, dev):
+def _heads(name, x, y, B, T, D, dtype, index):
     """(sekv_heads, output) of one tensor; an output made here is zero at padding."""
-    if x.dtype != dtype or x.device != dev:
-        check_tensor(x, name, (dtype,), dev)
+    if x.dtype != dtype or x.get_device() != index:
+        check_tensor(x, name, (dtype,), index)
     s, xs = x.shape, x.stride()
-    if len(s) != 4 or s[0] != shape[0] or s[1] != shape[1] or s[3] != shape[2] or xs[3] != 1:
-        raise ValueError(f"{name}: expected [{shape[0]}][{shape[1]}][heads][{shape[2]}] with "
-                         f"consecutive elements in a head, got {tuple(x.shape)}")
+    if len(s) != 4 or s[0] != B or s[1] != T or s[3] != D or xs[3] != 1:
+        raise ValueError(f"{name}: expected [{B}][{T}][heads][{D}] with consecutive elements in a "
+                         f"head, got {tuple(s)}")
     n = s[2]
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
-        n += 1 << 32
-        ys = y.stride()
-    else:
-        if y.dtype != dtype or y.device != dev:
-            check_tensor(y, name + "_out", (dtype,), dev)
-        ys = y.stride()
-        if y.shape != s or ys[3] != 1:
-            raise ValueError(f"{name}_out: expected shape {tuple(s)}, got {tuple(y.shape)}")
+        return SekvHeads(x.data_ptr(), y.data_ptr(), n + (1 << 32), xs[0], xs[1], xs[2],
+                         T * n * D, n * D, D), y
+    if y.dtype != dtype or y.get_device() != index:
+        check_tensor(y, name + "_out", (dtype,), index)
+    ys = y.stride()
+    if y.shape != s or ys[3] != 1:
+        raise ValueError(f"{name}_out: expected shape {tuple(s)}, got {tuple(y.shape)}")
     return SekvHeads(x.data_ptr(), y.data_ptr(), n, xs[0], xs[1], xs[2], ys[0], ys[1], ys[2]), y
 
 
@@ -107,32 +106,33 @@ def rope(plan: RopePlan, q, k, positions, q_out=None, k_out=None, backward: bool
     x0 = q if q is not None else k
     if x0 is None:
         raise ValueError("rope: q or k is needed")
-    dev, dtype = x0.device, x0.dtype
-    index = on_current_device(dev)
-    if dtype not in DTYPES or x0.dim() != 4:
-        raise TypeError(f"rope: expected [B][T][heads][D] of {list(DTYPES)}, got {x0.dtype} "
+    dtype = x0.dtype
+    code = DTYPES.get(dtype)
+    if code is None or x0.dim() != 4:
+        raise TypeError(f"rope: expected [B][T][heads][D] of {list(DTYPES)}, got {dtype} "
                         f"{tuple(x0.shape)}")
+    index = current_index(x0, "rope")
     B, T, _, D = x0.shape
     if D < plan.rot_dim:
         raise ValueError(f"rope: heads of {D} dimensions, plan rotates {plan.rot_dim}")
-    if plan.freqs.device != dev:
-        raise ValueError(f"plan: on {plan.freqs.device}, tensors on {dev}")
-    check_tensor(positions, "positions", _POSITIONS, dev)
-    ps = positions.stride()
-    if positions.shape == (B, T):
+    if plan.device_index != index:
+        raise ValueError(f"plan: on {plan.freqs.device}, tensors on {x0.device}")
+    check_tensor(positions, "positions", _POSITIONS, index)
+    s, ps = positions.shape, positions.stride()
+    if len(s) == 2 and s[0] == B and s[1] == T:
         pos_stride = ps[0]
-    elif positions.shape == (T,):
+    elif len(s) == 1 and s[0] == T:
         pos_stride = 0
     else:
-        raise ValueError(f"positions: expected [{T}] or [{B}][{T}], got {tuple(positions.shape)}")
+        raise ValueError(f"positions: expected [{T}] or [{B}][{T}], got {tuple(s)}")
     if T > 1 and ps[-1] != 1:
         raise ValueError("positions: must be consecutive along a sequence")
     qh = kh = None
     if q is not None:
-        qh, q_out = _heads("q", q, q_out, (B, T, D), dtype, dev)
+        qh, q_out = _heads("q", q, q_out, B, T, D, dtype, index)
     if k is not None:
-        kh, k_out = _heads("k", k, k_out, (B, T, D), dtype, dev)
-    st = lib().sekv_rope(plan._c, plan.freqs_ptr, plan.mscale, DTYPES[dtype], D, B, T,
+        kh, k_out = _heads("k", k, k_out, B, T, D, dtype, index)
+    st = lib().sekv_rope(plan._c, plan.freqs_ptr, plan.mscale, code, D, B, T,
                          positions.data_ptr(), positions.dtype == torch.int64, pos_stride, qh, kh,
                          1 if backward else 0, raw_stream(stream, index))
     if st != 0:

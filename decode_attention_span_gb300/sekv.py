@@ -209,22 +209,23 @@ def _need(t: torch.Tensor, name: str, dtype, cuda: bool = True):
         raise ValueError(f"{name}: must be contiguous")
 
 
-def on_current_device(device) -> int:
-    """Index of `device`, which has to be the current CUDA device (the library launches there)."""
-    index = device.index
-    # a CUDA tensor exists, so CUDA is initialised and torch.cuda.current_device()'s own
-    # check of that (1 us) can be left out
-    if device.type != "cuda" or index != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {device}: they must be on the current CUDA device")
+def current_index(t: torch.Tensor, name: str) -> int:
+    """Index of the CUDA device that `t` is on, which has to be the current one (the
+    library launches there)."""
+    index = t.get_device()
+    # for a CUDA tensor CUDA is initialised, so torch.cuda.current_device()'s own check of
+    # that (1 us) can be left out
+    if index < 0 or index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: on {t.device}, must be on the current CUDA device")
     return index
 
 
-def check_tensor(t: torch.Tensor, name: str, dtypes, device):
-    """`t` is of one of `dtypes` and on `device`."""
+def check_tensor(t: torch.Tensor, name: str, dtypes, index: int):
+    """`t` is of one of `dtypes` and on CUDA device `index`."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, the other tensors on cuda:{index}")
 
 
 def raw_stream(stream, index: int) -> int:

@@ -65,6 +65,7 @@ struct AttnShared {
 // The join of partials: kJoinParts sets of threads take every kJoinParts-th partial each.
 constexpr int kJoinThreads = kCols * kHeadDim / 4 / 2;  // two float4 a thread
 constexpr int kJoinParts = kAttnThreads / kJoinThreads;
+constexpr int kFewPartials = 4;  // joined without shared memory
 // scratch of the last CTA of a group, over the warps' values
 struct JoinShared {
   float w[kMaxCtas][kCols];   // maxima, then weights
@@ -170,52 +171,41 @@ struct WarpState {
   float unit;      // power of two on the weights of o
 };
 
-// B operand, sums and scale of the segment's columns into shared memory, by one warp; qv:
-// this lane's sixteen dimensions of either group of its column.
+// B operand, sums and scale of column `col` into shared memory, by one warp: q is this
+// lane's four dimensions, 4 lane .. 4 lane + 3.
 template <typename T>
-__device__ __forceinline__ void put_queries(AttnShared& sh, const T (&qv)[32], int lane,
+__device__ __forceinline__ void put_queries(AttnShared& sh, const T (&q)[4], int col, int lane,
                                             float scale_log2) {
-  float big = 0.f, sum[2] = {0.f, 0.f}, odd[2] = {0.f, 0.f};
+  float x[4], big = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float x = q_value(qv[i]);
-    big = fmaxf(big, fabsf(x));
-    sum[i >> 4] += x;
-    if (i & 1) odd[i >> 4] += x;
+  for (int i = 0; i < 4; ++i) {
+    x[i] = q_value(q[i]);
+    big = fmaxf(big, fabsf(x[i]));
   }
+  float odd = x[1] + x[3], sum = odd + x[0] + x[2];
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
+  for (int o = 1; o < 32; o <<= 1) {
     big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
-      sum[gr] += __shfl_xor_sync(~0u, sum[gr], o);
-      odd[gr] += __shfl_xor_sync(~0u, odd[gr], o);
+    if (o < 16) {  // the lower lanes have the first group of dimensions
+      sum += __shfl_xor_sync(~0u, sum, o);
+      odd += __shfl_xor_sync(~0u, odd, o);
     }
   }
   // power of two that brings the largest element to 2^13 .. 2^14
   const int e = min(max(int(__float_as_uint(big) >> 23) - 127, -110), 110);
   const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
-  if ((lane & 3) == 0) {
-    const int col = lane >> 2;
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
-      // an infinity among the queries makes the column NaN, as NaN does
-      sh.q_sum[gr][col] = big < INFINITY ? sum[gr] * up : NAN;
-      sh.q_off[gr][col] = odd[gr] * up * -64.f;
-    }
+  if ((lane & 15) == 0) {
+    // an infinity among the queries makes the column NaN, as NaN does
+    sh.q_sum[lane >> 4][col] = big < INFINITY ? sum * up : NAN;
+    sh.q_off[lane >> 4][col] = odd * up * -64.f;
     sh.q_scale[col] = __uint_as_float(uint32_t(127 - 13 + e) << 23) * scale_log2;
   }
+  // dimension d = 64 gr + 16 t + 8 w + i is in vector 2 gr + w of lane 4 col + t, half i / 4
+  // of word i % 4; odd dimensions meet high nibbles
+  __half* dst = reinterpret_cast<__half*>(&sh.qb[(lane >> 4) * 2 + (lane >> 1 & 1)][col * 4 + (lane >> 2 & 3)]);
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    uint32_t w[4];  // pair i: dimensions i and i + 4 of the word's eight
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float u = i & 1 ? up * 0.0625f : up;
-      const __half2 h = __floats2half2_rn(q_value(qv[8 * m + i]) * u, q_value(qv[8 * m + i + 4]) * u);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    sh.qb[m][lane] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  for (int i = 0; i < 4; ++i)
+    dst[2 * i + (lane & 1)] = __float2half_rn(x[i] * (i & 1 ? up * 0.0625f : up));
 }
 
 // The segment's queries as a lane keeps them: its columns are 2t and 2t + 1.
@@ -424,19 +414,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     sum = __reduce_add_sync(~0u, sum);
     longest = __reduce_max_sync(~0u, longest);
     __syncwarp();
-    // smallest piece for which the groups' pieces fit the grid: the line's share, or
-    // more; taken if it costs less than the second group of a CTA would
-    const int n_cta = int(gridDim.x), share = (sum * per_seq + n_cta - 1) / n_cta;
+    // as many CTAs for each group, if there are enough and its longest piece is not much
+    // more than the line's share
+    const int n_cta = int(gridDim.x), groups = P.batch * per_seq;
     int piece = 0;
-    if (P.batch * per_seq <= n_cta) {
-      int lo = max(share, 1), hi = longest;  // hi always fits
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        int n = 0;
-        for (int b = lane; b < P.batch; b += 32) n += (chunks_of(sh.len[b]) + mid - 1) / mid;
-        if (__reduce_add_sync(~0u, n) * per_seq <= n_cta) hi = mid; else lo = mid + 1;
-      }
-      if (lo <= share + kGroupCost) piece = lo;
+    if (groups <= n_cta) {
+      const int k = n_cta / groups, share = (sum * per_seq + n_cta - 1) / n_cta;
+      piece = (longest + k - 1) / k;
+      if (piece > share + kGroupCost) piece = 0;
     }
     int run = 0;
     for (int b0 = 0; b0 < P.batch; b0 += 32) {
@@ -493,20 +478,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     const int blk = gi / P.pg.hkv, head = gi - blk * P.pg.hkv;
     const int cols = min(P.tpb, P.n_q - blk * P.tpb) * P.hpg;
 
-    // The queries' loads go out first: behind the copies they would wait for them.
-    const int qcol = PACK ? g & 3 : g;            // this lane's column of the B operand
-    const int tok = blk * P.tpb + qcol / P.hpg;   // its query token
+    // The queries: warp w brings column w.
     union {
-      uint4 w[4];   // sixteen dimensions of either group
-      T e[32];
+      uint2 w;
+      T e[4];
     } qv;
-    {
+    qv.w = make_uint2(0, 0);
+    const int qcol = PACK ? warp & 3 : warp;
+    if (warp < kCols && qcol < cols) {
+      const int tok = blk * P.tpb + qcol / P.hpg;
       const T* q = static_cast<const T*>(P.q) +
-                   ((int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + qcol % P.hpg) * kHeadDim;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        qv.w[i] = warp == 0 && qcol < cols ? __ldg(reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + t * 16) + (i & 1))
-                           : make_uint4(0, 0, 0, 0);
+                   ((int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + qcol % P.hpg) *
+                       kHeadDim;
+      // volatile: the compiler would move a plain load down to its use, behind the copies
+      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(qv.w.x), "=r"(qv.w.y) : "l"(q + 4 * lane));
     }
 
     // This warp's k-th chunk of the segment is c0 + warp + kAttnWarps k.  Lane i
@@ -544,9 +529,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
         }
       }
     };
-    for (int k = 0; k < min(mine, kStages); ++k) issue(k);
 
-    if (warp == 0) put_queries<T>(sh, qv.e, lane, P.scale_log2);
+    if (warp < kCols) put_queries<T>(sh, qv.e, warp, lane, P.scale_log2);
     __syncthreads();
     Query Q;
     int see[2];  // tokens that columns 2t and 2t + 1 see
@@ -566,6 +550,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     }
     // up to here no token is hidden from any column in use
     const int open = len - (P.n_q - 1 - blk * P.tpb);
+
+    // Only now the first copies: with the copy engine's queue full, shuffles and loads from
+    // shared memory behind them take 600 clocks a step (the queries above: 3000).
+    for (int k = 0; k < min(mine, kStages); ++k) issue(k);
 
     WarpState S;
 #pragma unroll
@@ -682,19 +670,49 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       // the CTAs of this group, in order of their pieces
       const int first = int((int64_t(gs + 1) * n_cta - 1) / total);
       const int n = int((int64_t(ge) * n_cta - 1) / total) - first + 1;
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
+        __threadfence();
         sh.last = atomicAdd(P.arrived + group, 1) == n - 1;
         if (sh.last) P.arrived[group] = 0;  // ready for the next call
+        __threadfence();
       }
       __syncthreads();
-      if (sh.last) {
-        __threadfence();
+      auto slot = [&](int i) {
+        return P.partials + (int64_t(first + i) * 2 + (gs > start(first + i) ? 1 : 0)) * kStateFloats;
+      };
+      if (sh.last && n <= kFewPartials) {
+        // each thread on its own: two loads deep and no barrier
+        if (tid < kCols * kHeadDim / 4) {
+          const int col = tid / (kHeadDim / 4);
+          float m[kFewPartials], l[kFewPartials];
+          float4 x[kFewPartials];
+#pragma unroll
+          for (int i = 0; i < kFewPartials; ++i) {
+            m[i] = -INFINITY;
+            if (i < n) {
+              const float* p = slot(i);
+              m[i] = __ldcg(p + kCols * kHeadDim + col);
+              l[i] = __ldcg(p + kCols * kHeadDim + kCols + col);
+              x[i] = __ldcg(reinterpret_cast<const float4*>(p) + tid);
+            }
+          }
+          float mx = m[0], sum = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 1; i < kFewPartials; ++i) mx = fmaxf(mx, m[i]);
+#pragma unroll
+          for (int i = 0; i < kFewPartials; ++i)
+            if (i < n) {
+              const float f = m[i] == -INFINITY ? 0.f : ex2(m[i] - mx);
+              sum = fmaf(f, l[i], sum);
+              v.x = fmaf(f, x[i].x, v.x); v.y = fmaf(f, x[i].y, v.y);
+              v.z = fmaf(f, x[i].z, v.z); v.w = fmaf(f, x[i].w, v.w);
+            }
+          if (col < cols) write_out(col, tid % (kHeadDim / 4) * 4, v, mx, sum);
+        }
+      } else if (sh.last) {
         JoinShared& jn = *reinterpret_cast<JoinShared*>(&sh.o[0][0][0]);
-        auto slot = [&](int i) {
-          return P.partials + (int64_t(first + i) * 2 + (gs > start(first + i) ? 1 : 0)) * kStateFloats;
-        };
         for (int i = tid; i < n * kCols; i += kAttnThreads) {
           const float* p = slot(i / kCols) + kCols * kHeadDim + i % kCols;
           jn.w[i / kCols][i % kCols] = __ldcg(p);

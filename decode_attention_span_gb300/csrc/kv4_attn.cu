@@ -779,13 +779,15 @@ int blocks_of(const sekv_config* cfg, int64_t n_q) {
 int attn_ctas() { return std::min(device_sm_count(), kMaxCtas); }  // one per SM
 
 struct Kv4Ws {
-  size_t arrived, partials, total;
+  size_t partials, arrived, total;
 };
 Kv4Ws kv4_ws(const sekv_config* cfg, int64_t n_q, int sms) {
+  // the counters last: where they begin is the same whatever batch and n_q a call has, so
+  // that calls of different sizes can take turns on a workspace
   Kv4Ws L{};
-  L.arrived = 256;
-  L.partials = L.arrived + align256(size_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * 4);
-  L.total = L.partials + align256(size_t(sms) * 2 * kStateFloats * 4);
+  L.partials = 256;
+  L.arrived = L.partials + align256(size_t(sms) * 2 * kStateFloats * 4);
+  L.total = L.arrived + align256(size_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * 4);
   return L;
 }
 
@@ -832,14 +834,13 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
   if (!q || !seq_len || !out || !aligned16(q) || !aligned16(out) || !isfinite(scale) ||
       !(scale > 0.f))
     return SEKV_ERR_INVALID;
+  // the kernel numbers tokens and chunks in 32 bits
+  if (cache->max_pages >= 1 << 24 ||
+      int64_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * cache->max_pages >= 1 << 29)
+    return SEKV_ERR_UNSUPPORTED;
   st = kv4_check_ws(cfg, n_q, workspace_bytes);
   if (st != SEKV_OK) return st;
   const int sms = attn_ctas();
-  // the kernel numbers chunks in 32 bits
-  if (int64_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * cache->max_pages *
-              (kKv4Page / kChunkTokens) > INT32_MAX / 2 ||
-      int64_t(cache->max_pages) * kKv4Page > INT32_MAX / 2)
-    return SEKV_ERR_UNSUPPORTED;
   const Kv4Ws L = kv4_ws(cfg, n_q, sms);
   uint8_t* w = static_cast<uint8_t*>(workspace);
   AttnParams P{};

@@ -316,7 +316,9 @@ extern "C" sekv_status sekv_kv4_append(const sekv_config* cfg, const sekv_kv4_ca
   StoreParams P = store_params(cfg, cache, n_tokens, first, n_valid, workspace);
   P.k = k;
   P.v = v;
+  const int64_t size[3] = {cfg->batch, n_tokens, cfg->n_kv_heads};
   for (int i = 0; i < 3; ++i) {
+    if (size[i] <= 1) continue;  // the stride of a single row means nothing
     if (k_stride[i] % 8 != 0 || v_stride[i] % 8 != 0) return SEKV_ERR_INVALID;
     P.ks[i] = k_stride[i];
     P.vs[i] = v_stride[i];

@@ -7,7 +7,7 @@ import ctypes
 
 import torch
 
-from .sekv import (DTYPES, Config, Workspace, _check, check_tensor, current_index, lib,
+from .sekv import (DTYPES, SEKV_CALL_KV4, Config, Workspace, _check, check_tensor, current_index, lib,
                    raw_stream)
 
 PAGE_TOKENS = 64
@@ -54,6 +54,8 @@ def _common(cfg, cache, ws) -> int:
     if cfg.batch != cache.batch or cfg.n_kv_heads != cache.n_kv_heads:
         raise ValueError("cache: made for another batch or number of KV heads")
     index = current_index(cache.pages, "pages")
+    if ws.which != SEKV_CALL_KV4:
+        raise ValueError("workspace: made for another call, expected which=SEKV_CALL_KV4")
     if ws.buf.get_device() != index:
         raise ValueError(f"workspace: on {ws.buf.device}, cache on {cache.device}")
     return index
@@ -105,7 +107,8 @@ def kv4_read(cfg: Config, cache: Kv4Cache, first, n_tokens: int, ws: Workspace,
              dtype=torch.bfloat16, n_valid=None, out=None, stream=None):
     """K and V [B][Hkv][n_tokens][128] that the tokens first[b] .. first[b] + n_tokens - 1
     stand for, rounded to dtype (bf16, f16 or f32).  With n_valid [B], rows from
-    n_valid[b] on stay as they were (zero in outputs made here)."""
+    n_valid[b] on stay as they were (zero in outputs made here); tokens that the workspace's
+    status flags are not written."""
     index = _common(cfg, cache, ws)
     dev = cache.device
     shape = (cfg.batch, cfg.n_kv_heads, n_tokens, 128)

@@ -301,7 +301,7 @@ class Workspace:
         n = int(lib().sekv_workspace_size(ctypes.byref(c), which, ctx_len))
         if n == 0:
             raise SekvError("sekv_workspace_size", -1)
-        self.nbytes = n
+        self.nbytes, self.which = n, which
         self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
         _check("sekv_workspace_init", lib().sekv_workspace_init(_ptr(self.buf), n, _stream()))
 

@@ -712,7 +712,10 @@ typedef struct sekv_kv4_cache {
 } sekv_kv4_cache;
 
 /* cfg: batch, n_q_heads, n_kv_heads and head_dim count (the rest only has to be
- * valid); batch at most SEKV_KV4_MAX_BATCH.  Workspaces: SEKV_CALL_KV4.  Device
+ * valid); batch at most SEKV_KV4_MAX_BATCH.  Workspaces: SEKV_CALL_KV4, not shared with
+ * other kinds of call; calls of any batch and n_q that it is large enough for may take turns
+ * on one.  sekv_kv4_attention: batch * n_kv_heads * sekv_query_blocks * max_pages below 2^29
+ * and max_pages below 2^24 (else SEKV_ERR_UNSUPPORTED).  Device
  * code 1: a page id outside [0, n_pages), or a token beyond max_pages * 64
  * (detail: the sequence); such tokens are not stored, read as they were and
  * not attended to.
@@ -721,7 +724,7 @@ typedef struct sekv_kv4_cache {
  * position first[b] on.  first: int32 [batch] (device).  n_valid: int32 [batch]
  * (device) or NULL: only the first n_valid[b] of the n_tokens rows are stored.  k, v:
  * bf16 or f16, element (b, t, c, d) at b*stride[0] + t*stride[1] + c*stride[2] + d,
- * rows 16-byte aligned (strides multiples of 8).  Pages named twice must not
+ * rows 16-byte aligned (strides of more than one row multiples of 8).  Pages named twice must not
  * receive the same token slot twice. */
 sekv_status sekv_kv4_append(const sekv_config* cfg, const sekv_kv4_cache* cache,
                             int32_t dtype, const void* k, const int64_t k_stride[3],

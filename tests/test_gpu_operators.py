@@ -118,6 +118,23 @@ def test_logprobs_masked_and_special_rows(sk, ws, dtype):
     assert ws.status() == (0, 0)
 
 
+@pytest.mark.parametrize("scale,offset", [(1e-3, 0.0), (0.02, 0.0), (30.0, 0.0), (2000.0, 0.0), (1.0, 3000.0), (1.0, 60000.0), (1.0, -1e6)])
+def test_logprobs_scales_and_offsets(sk, ws, scale, offset):
+    """Very flat and very sharp distributions; logits with a large common offset, whose
+    log-probabilities are those without it (the logits of f32 being rounded first)."""
+    x = torch.randn(5, 9001, generator=gen(1)) * 3 + offset
+    tok = x.argmax(1)
+    r = sk.token_logprobs(x.cuda(), tok.cuda(), ws, n_top=6, scale=scale)
+    ref = tokens.token_logprobs(x.double().numpy(), tok.numpy(), float(np.float32(scale)), 6)
+    assert np.array_equal(r.top_ids.cpu().numpy(), ref["top_ids"])
+    # exponents err by 3 * 2^-24 of what still counts (100) and 2^-22, sums by 2^-24 an addition
+    d = 300 * 2.0 ** -24 + 2.0 ** -22 + 2.0 ** -24 * (9001 / 256 + 40)
+    for name in ("logprob", "top_logprobs", "entropy"):
+        want = ref[name]
+        compare(getattr(r, name).double().cpu().numpy(), want, 3 * d * (1 + np.abs(want)), name)
+    compare(r.lse.double().cpu().numpy(), ref["lse"], 3 * d + 2.0 ** -22 * np.abs(ref["lse"]), "lse")
+
+
 def test_logprobs_bad_token_is_flagged(sk, ws):
     x = torch.zeros(3, 50, device="cuda")
     r = sk.token_logprobs(x, torch.tensor([1, 50, -1]).cuda(), ws)
@@ -415,6 +432,83 @@ def test_kv4_attention(sk, dtype, hq, hkv, n_q, lens):
     assert torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+def fill_cache(sk, cfg, cache, ws, lens, seed, dtype="bf16"):
+    k, v = kv_rows(dtype, len(lens), max(1, max(lens)), cfg.n_kv_heads, seed)
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    sk.kv4_append(cfg, cache, k.cuda(), v.cuda(), torch.zeros_like(n), ws, n_valid=n)
+    return n
+
+
+@pytest.mark.parametrize("hq,hkv,n_q,lens", [
+    # more groups than CTAs: a CTA's share crosses groups, and there are more than 32 sequences
+    (8, 4, 1, [(37 * i) % 190 for i in range(70)]),
+    # groups for every CTA, one of them far longer than the rest
+    (8, 8, 1, [20000] + [5, 0, 64] * 5), (4, 2, 4, [9000, 1, 700, 33]),
+    # one group over all CTAs
+    (3, 1, 1, [30000])])
+def test_kv4_attention_shares(sk, hq, hkv, n_q, lens):
+    B = len(lens)
+    cfg, cache, ws = kv_cache(sk, B, hkv, max(1, -(-max(lens) // 64)), n_q, hq, seed=3)
+    n = fill_cache(sk, cfg, cache, ws, lens, 5)
+    q = torch.randn(B, n_q, hq, 128, generator=gen(9)).bfloat16()
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), n, 0.0884, ws)
+    assert ws.status() == (0, 0)
+    check_attention(out, lse, kv4.attention(q.double().numpy(), cache.pages.cpu().numpy(), cache.page_table.cpu().numpy(), lens, 0.0884))
+
+
+def test_kv4_calls_of_different_sizes_take_turns_on_a_workspace(sk):
+    """A workspace for 64 query tokens and four sequences serves calls of other batches and
+    numbers of query tokens in between."""
+    cfg4, c4, ws = kv_cache(sk, 4, 2, 12, 64, 16)
+    n4 = fill_cache(sk, cfg4, c4, ws, [700, 64, 1, 300], 1)
+    cfg1, c1, _ = kv_cache(sk, 1, 2, 12, 1, 16, seed=1)
+    n1 = fill_cache(sk, cfg1, c1, ws, [750], 2)
+    calls = []
+    for cfg, c, n, n_q in ((cfg4, c4, n4, 64), (cfg1, c1, n1, 1), (cfg4, c4, n4, 2), (cfg1, c1, n1, 7)):
+        q = torch.randn(cfg.batch, n_q, 16, 128, generator=gen(n_q)).bfloat16().cuda()
+        own = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=n_q)
+        calls.append((cfg, c, q, n, sk.kv4_attention(cfg, c, q, n, 0.1, own)))
+    for _ in range(2):
+        for cfg, c, q, n, want in calls:
+            got = sk.kv4_attention(cfg, c, q, n, 0.1, ws)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert ws.status() == (0, 0)
+
+
+def test_kv4_two_streams_at_once(sk):
+    """Two calls side by side on streams of their own, each with its own workspace."""
+    cfg, cache, ws = kv_cache(sk, 2, 2, 80, 1, 8)
+    n = fill_cache(sk, cfg, cache, ws, [5000, 3000], 1)
+    q = [torch.randn(2, 1, 8, 128, generator=gen(i)).bfloat16().cuda() for i in range(2)]
+    want = [sk.kv4_attention(cfg, cache, x, n, 0.1, ws) for x in q]
+    wss = [sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(sk.kv4_attention(cfg, cache, q[i], n, 0.1, wss[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_kv4_attention_non_finite_queries(sk):
+    """A NaN or an infinity in one head's query makes that head NaN and no other."""
+    cfg, cache, ws = kv_cache(sk, 1, 1, 2, 2, 4)
+    n = fill_cache(sk, cfg, cache, ws, [100], 3)
+    q = torch.randn(1, 2, 4, 128, generator=gen(2)).bfloat16()
+    clean = sk.kv4_attention(cfg, cache, q.cuda(), n, 0.1, ws)
+    q[0, 0, 1, 77], q[0, 1, 2, 3], q[0, 1, 3, 64] = math.nan, INF, -INF
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), n, 0.1, ws)
+    bad = torch.zeros(1, 2, 4, dtype=torch.bool, device="cuda")
+    bad[0, 0, 1] = bad[0, 1, 2] = bad[0, 1, 3] = True
+    assert torch.equal(torch.isnan(lse), bad) and torch.isnan(out[bad]).all()
+    assert torch.equal(out[~bad], clean[0][~bad])
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e4, 1e30])
 def test_kv4_attention_values_of_any_size(sk, size):
     """Values far outside fp16's range, keys with a large common offset."""
@@ -483,6 +577,8 @@ def test_kv4_workspace_and_shape_refusals(sk):
         sk.Kv4Cache(cfg, cache.pages, cache.page_table[:, ::2])
     with pytest.raises(sk.SekvError):
         sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=65)
+    with pytest.raises(ValueError):   # a workspace of another kind of call
+        sk.kv4_attention(cfg, cache, q, lens, 1.0, sk.Workspace(cfg))
     k = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
         sk.kv4_append(cfg, cache, k, k[:, :, :1], lens, ws)

@@ -221,9 +221,11 @@ def test_kv4_refusals(libsekv):
         assert f(a=(None, args()[1])) == INVALID
     for nq in (0, -1, 65):
         assert attn(nq=nq) == UNSUPPORTED
+    assert attn(args(cache=(1 << 20, 1 << 20, 4, 1 << 24))) == UNSUPPORTED
+    assert attn(args(cfg=(1024, 512, 512), cache=(1 << 20, 1 << 20, 4, 1 << 10))) == UNSUPPORTED
     # what does not depend on the GPU's size is refused before the workspace is looked at
     for f, kw in ((append, dict(dt=2)), (append, dict(k=None)), (append, dict(k=ODD)), (append, dict(n=-1)), (append, dict(first=None)),
-                  (append, dict(ks=(ctypes.c_int64 * 3)(4, 8, 8))), (read, dict(dt=3)), (read, dict(k=None)), (read, dict(n=-1)),
+                  (append, dict(ks=(ctypes.c_int64 * 3)(8, 8, 4))), (append, dict(n=2, ks=(ctypes.c_int64 * 3)(8, 4, 8))), (read, dict(dt=3)), (read, dict(k=None)), (read, dict(n=-1)),
                   (attn, dict(dt=2)), (attn, dict(q=None)), (attn, dict(q=ODD)), (attn, dict(scale=math.nan)),
                   (attn, dict(scale=0.0)), (attn, dict(scale=-0.1)), (attn, dict(scale=math.inf))):
         assert f(**kw) == INVALID, kw

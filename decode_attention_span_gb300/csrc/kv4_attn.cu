@@ -42,6 +42,7 @@ constexpr int kCols = 8;                         // (token, head) pairs of a blo
 constexpr int kStateFloats = kCols * (kHeadDim + 2);  // o, m, l
 // What a second group costs a CTA (its plan, queries, first copies and join, about 6 us), in chunks
 constexpr int kGroupCost = 40;
+constexpr int kFlush = 16;                       // chunks between two flushes
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct AttnShared {
@@ -216,13 +217,38 @@ struct Query {
   float scale_log2[2];
 };
 
+// The matrix instructions cut their sums off towards zero, which over hundreds of them adds
+// up to more than fp32's rounding.  So every kFlush chunks a warp adds its values to
+// a second set in shared memory, rounded properly; eight 16-byte words a lane.
+__device__ __forceinline__ void flush(WarpState& S, float4* kept, int lane, bool first) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float4 v = make_float4(S.o[j][0], S.o[j][1], S.o[j][2], S.o[j][3]);
+    if (!first) {
+      const float4 x = kept[j * 32 + lane];
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    kept[j * 32 + lane] = v;
+    S.o[j][0] = S.o[j][1] = S.o[j][2] = S.o[j][3] = 0.f;
+  }
+}
+// f0 and f1: on the values of the lane's columns
+__device__ __noinline__ void rescale_kept(float4* kept, int lane, float f0, float f1) {
+  for (int j = 0; j < 8; ++j) {
+    float4 v = kept[j * 32 + lane];
+    v.x *= f0; v.y *= f1; v.z *= f0; v.w *= f1;
+    kept[j * 32 + lane] = v;
+  }
+}
+
 // EDGE: some token of the chunk is not seen by some column (seen: per column of the
 // lane; held: tokens of the chunk that the sequence has).  PACK: only four columns are in
 // use; columns 4-7 hold the same queries again, and their lanes put the weights' lower
 // parts in, so that one product does for both.
 template <bool EDGE, bool PACK>
 __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const uint8_t* chunk,
-                                           int lane, int held, const int (&seen)[2]) {
+                                           float4* kept, bool any_kept, int lane, int held,
+                                           const int (&seen)[2]) {
   const int g = lane >> 2;
   float x[2][2][2];  // tile, row half, column
 #pragma unroll
@@ -328,6 +354,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) S.o[j][i] *= f[i & 1];
+    if (any_kept) rescale_kept(kept, lane, f[0], f[1]);
   }
   const float m0[2] = {S.m[0] == -INFINITY ? 0.f : S.m[0], S.m[1] == -INFINITY ? 0.f : S.m[1]};
 
@@ -567,6 +594,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     }
     S.unit = __uint_as_float(254u << 23);
 
+    float4* kept = reinterpret_cast<float4*>(&sh.o[warp][0][0]);
     for (int k = 0; k < mine; ++k) {
       const uint32_t st = (done + k) % kStages;
       if ((present >> (k & 31) & 1u) && !lost) {
@@ -575,9 +603,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
           const int held = len - pos;
           const int seen[2] = {see[0] - pos, see[1] - pos};
           if (pos + kChunkTokens <= open)
-            chunk_step<false, PACK>(S, Q, sh.ring[warp][st], lane, held, seen);
+            chunk_step<false, PACK>(S, Q, sh.ring[warp][st], kept, k >= kFlush, lane, held, seen);
           else
-            chunk_step<true, PACK>(S, Q, sh.ring[warp][st], lane, held, seen);
+            chunk_step<true, PACK>(S, Q, sh.ring[warp][st], kept, k >= kFlush, lane, held, seen);
         } else {
           // a copy did not land: nothing more is copied or waited for by this warp, and
           // what is still in flight gets its time to land before the CTA may end
@@ -589,8 +617,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       }
       __syncwarp();
       if (k + kStages < mine) issue(k + kStages);
+      if (k % kFlush == kFlush - 1) flush(S, kept, lane, k < kFlush);
     }
     done += mine;
+    if (mine >= kFlush) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 x = kept[j * 32 + lane];
+        S.o[j][0] += x.x; S.o[j][1] += x.y; S.o[j][2] += x.z; S.o[j][3] += x.w;
+      }
+      __syncwarp();  // the state goes where the kept values were
+    }
 
     // the warps' states into shared memory
     const float inv_unit = 1.f / S.unit;

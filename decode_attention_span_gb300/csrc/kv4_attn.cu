@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kAttnWarps = 12;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kChunkTokens = 32;
 constexpr int kChunkBytes = 2 * kKv4TileBytes;
 constexpr int kMaxCtas = 256;                    // of a launch
@@ -42,12 +42,16 @@ constexpr int kCols = 8;                         // (token, head) pairs of a blo
 constexpr int kStateFloats = kCols * (kHeadDim + 2);  // o, m, l
 // What a second group costs a CTA (its plan, queries, first copies and join, about 6 us), in chunks
 constexpr int kGroupCost = 40;
+constexpr float kNone = -3e38f;
+constexpr float kGrowth = 8.f;                   // log2 by which a weight may outgrow the reference
+constexpr float kMaxScale = 128.f;               // of V with the unit: 2^8 times it fits f16
 constexpr int kFlush = 16;                       // chunks between two flushes
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct AttnShared {
   uint8_t ring[kAttnWarps][kStages][kChunkBytes];
   float o[kAttnWarps][kCols][kHeadDim];
+  float4 par[kAttnWarps][2][kChunkTokens];  // a chunk's scales and zeros, K's and V's, as floats
   float m[kAttnWarps][kCols];
   float l[kAttnWarps][kCols];
   float w[kAttnWarps][kCols];
@@ -167,7 +171,7 @@ __device__ __forceinline__ int chunks_of(int len) {
 // over its own tokens (rows g and g + 8 of each tile).
 struct WarpState {
   float o[8][4];   // [4 dims apiece: word m, i][rows g, g + 8 x columns], in units of 1 / unit
-  float m[2], l[2];
+  float m[2], l[2];  // the weights' reference, log2: within 2^8 of the largest; kNone: no token yet
   float c[2][2];   // sum of p (z + 8 s): [column][group of dimensions]
   float unit;      // power of two on the weights of o
 };
@@ -247,9 +251,17 @@ __device__ __noinline__ void rescale_kept(float4* kept, int lane, float f0, floa
 // parts in, so that one product does for both.
 template <bool EDGE, bool PACK>
 __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const uint8_t* chunk,
-                                           float4* kept, bool any_kept, int lane, int held,
+                                           float4 (&par)[2][kChunkTokens], float4* kept,
+                                           bool any_kept, int lane, int held,
                                            const int (&seen)[2]) {
   const int g = lane >> 2;
+  // a lane turns one token's scales and zeros into floats for all
+  const uint8_t* sz = chunk + (lane >> 4) * kKv4TileBytes + kv4_param(lane & 15, 0, false);
+  const uint2 kp = *reinterpret_cast<const uint2*>(sz);
+  uint2 vp = *reinterpret_cast<const uint2*>(sz + 128);
+  if (EDGE && lane >= held) vp = make_uint2(0u, 0u);  // behind the end: may hold anything
+  par[0][lane] = make_float4(lo16(kp.x), hi16(kp.x), lo16(kp.y), hi16(kp.y));
+  __syncwarp();
   float x[2][2][2];  // tile, row half, column
 #pragma unroll
   for (int ti = 0; ti < 2; ++ti) {
@@ -285,78 +297,54 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint2 sz = *reinterpret_cast<const uint2*>(tile + kKv4Params + 32 * (g >> 1) + 8 * (g & 1) + 16 * e);
-      const float s0 = lo16(sz.x), s1 = lo16(sz.y);
-      const float z0 = hi16(sz.x), z1 = hi16(sz.y);
+      const float4 k = par[0][ti * 16 + e * 8 + g];  // s, z of both groups
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float y = s0 * acc[0][2 * e + c];
-        y = fmaf(z0, Q.sum[c][0], y);
-        y = fmaf(s1, acc[1][2 * e + c], y);
-        y = fmaf(z1, Q.sum[c][1], y);
+        float y = k.x * acc[0][2 * e + c];
+        y = fmaf(k.y, Q.sum[c][0], y);
+        y = fmaf(k.z, acc[1][2 * e + c], y);
+        y = fmaf(k.w, Q.sum[c][1], y);
         x[ti][e][c] = !EDGE || ti * 16 + e * 8 + g < seen[c] ? y : -INFINITY;
       }
     }
   }
 
-  // the columns' maxima, over the rows of all lanes; and the largest scale of V
+  // A new reference, or a new unit for V's scales, only where the old one no longer does.
+  const float s0 = lo16(vp.x), s1 = lo16(vp.y);
   float mx[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
-    mx[c] = fmaxf(fmaxf(x[0][0][c], x[0][1][c]), fmaxf(x[1][0][c], x[1][1][c]));
-  uint2 vp[2][2];
-  uint32_t top = 0;  // lower half: bf16 bits of the largest scale (never negative)
-#pragma unroll
-  for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      vp[ti][e] = *reinterpret_cast<const uint2*>(chunk + ti * kKv4TileBytes + kKv4Params + 128 +
-                                                  32 * (g >> 1) + 8 * (g & 1) + 16 * e);
-      if (EDGE && ti * 16 + e * 8 + g >= held) vp[ti][e] = make_uint2(0u, 0u);
-      top = __vimax3_u16x2(top, vp[ti][e].x, vp[ti][e].y);
-    }
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    mx[0] = fmaxf(mx[0], __shfl_xor_sync(~0u, mx[0], o));
-    mx[1] = fmaxf(mx[1], __shfl_xor_sync(~0u, mx[1], o));
-  }
-  top = __reduce_max_sync(~0u, top & 0xffffu);
-  if (top >= 0x7f80u) {  // an infinity or NaN does not count: look again without them
-    top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t s = (i & 1 ? vp[i >> 2][i >> 1 & 1].y : vp[i >> 2][i >> 1 & 1].x) & 0xffffu;
-      top = max(top, s < 0x7f80u ? s : 0u);
-    }
-    top = __reduce_max_sync(~0u, top);
-  }
-  mx[0] *= Q.scale_log2[0];
-  mx[1] *= Q.scale_log2[1];
-  // largest unit with top * unit < 2^15 (f16 ends at 65504)
-  const float unit = __uint_as_float(min(254u, 268u - max(14u, top >> 7)) << 23);
-  const bool up = mx[0] > S.m[0] || mx[1] > S.m[1];
-  if (__any_sync(~0u, up) || unit < S.unit) {
+    mx[c] = Q.scale_log2[c] * fmaxf(fmaxf(x[0][0][c], x[0][1][c]), fmaxf(x[1][0][c], x[1][1][c]));
+  const bool over = mx[0] > S.m[0] + kGrowth || mx[1] > S.m[1] + kGrowth ||
+                    fmaxf(s0, s1) * S.unit >= kMaxScale;
+  if (__any_sync(~0u, over)) {
+    // the largest finite scale, as bf16 bits (never negative), and the unit that brings it
+    // to 64 .. 128
+    const uint32_t t0 = vp.x & 0xffffu, t1 = vp.y & 0xffffu;
+    const uint32_t top = __reduce_max_sync(~0u, max(t0 < 0x7f80u ? t0 : 0u, t1 < 0x7f80u ? t1 : 0u));
+    const float unit = fminf(S.unit, __uint_as_float(min(254u, 260u - max(6u, top >> 7)) << 23));
     float f[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(~0u, mx[c], o));
       const float m1 = fmaxf(S.m[c], mx[c]);
-      f[c] = S.m[c] == -INFINITY ? 0.f : ex2(S.m[c] - m1);
+      f[c] = ex2(S.m[c] - m1);
       S.m[c] = m1;
       S.l[c] *= f[c];
       S.c[c][0] *= f[c];
       S.c[c][1] *= f[c];
+      f[c] *= unit / S.unit;
     }
-    const float v = fminf(unit, S.unit);
-    f[0] *= v / S.unit;
-    f[1] *= v / S.unit;
-    S.unit = v;
+    S.unit = unit;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) S.o[j][i] *= f[i & 1];
     if (any_kept) rescale_kept(kept, lane, f[0], f[1]);
   }
-  const float m0[2] = {S.m[0] == -INFINITY ? 0.f : S.m[0], S.m[1] == -INFINITY ? 0.f : S.m[1]};
+  par[1][lane] = make_float4(s0 * S.unit, fmaf(8.f, s0, hi16(vp.x)), s1 * S.unit, fmaf(8.f, s1, hi16(vp.y)));
+  __syncwarp();
 
 #pragma unroll
   for (int ti = 0; ti < 2; ++ti) {
@@ -365,16 +353,16 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
     const float low = lane & 2 ? -1.f : 0.f;  // PACK: this lane's columns take the lower parts
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t sz[2] = {vp[ti][e].x, vp[ti][e].y};
+      const float4 v = par[1][ti * 16 + e * 8 + g];  // s in units and z + 8 s, of both groups
       float p[2], w[2][2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        p[c] = ex2(fmaf(x[ti][e][c], Q.scale_log2[c], -m0[c]));
+        p[c] = ex2(fmaf(x[ti][e][c], Q.scale_log2[c], -S.m[c]));
         S.l[c] += p[c];
       }
 #pragma unroll
       for (int gr = 0; gr < 2; ++gr) {
-        const float s = lo16(sz[gr]), z = fmaf(8.f, s, hi16(sz[gr])), su = s * S.unit;
+        const float su = gr ? v.z : v.x, z = gr ? v.w : v.y;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           // a token that the column does not see has p 0, but may hold NaN
@@ -385,8 +373,8 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
         const __half2 h = __floats2half2_rn(w[gr][0], w[gr][1]);
         const float2 hf = __half22float2(h);
         if (PACK) {
-          const __half2 v = __floats2half2_rn(fmaf(low, hf.x, w[gr][0]), fmaf(low, hf.y, w[gr][1]));
-          bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&v));
+          const __half2 part = __floats2half2_rn(fmaf(low, hf.x, w[gr][0]), fmaf(low, hf.y, w[gr][1]));
+          bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&part));
         } else {
           const __half2 l = __floats2half2_rn(w[gr][0] - hf.x, w[gr][1] - hf.y);
           bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
@@ -589,7 +577,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       for (int i = 0; i < 4; ++i) S.o[j][i] = 0.f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      S.m[c] = -INFINITY;
+      S.m[c] = kNone;
       S.l[c] = S.c[c][0] = S.c[c][1] = 0.f;
     }
     S.unit = __uint_as_float(254u << 23);
@@ -603,9 +591,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
           const int held = len - pos;
           const int seen[2] = {see[0] - pos, see[1] - pos};
           if (pos + kChunkTokens <= open)
-            chunk_step<false, PACK>(S, Q, sh.ring[warp][st], kept, k >= kFlush, lane, held, seen);
+            chunk_step<false, PACK>(S, Q, sh.ring[warp][st], sh.par[warp], kept, k >= kFlush, lane, held, seen);
           else
-            chunk_step<true, PACK>(S, Q, sh.ring[warp][st], kept, k >= kFlush, lane, held, seen);
+            chunk_step<true, PACK>(S, Q, sh.ring[warp][st], sh.par[warp], kept, k >= kFlush, lane, held, seen);
         } else {
           // a copy did not land: nothing more is copied or waited for by this warp, and
           // what is still in flight gets its time to land before the CTA may end
@@ -660,10 +648,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     }
     __syncthreads();
     if (tid < kCols) {
-      float mx = -INFINITY, sum = 0.f;
+      float mx = kNone, sum = 0.f;
       for (int w = 0; w < kAttnWarps; ++w) mx = fmaxf(mx, sh.m[w][tid]);
       for (int w = 0; w < kAttnWarps; ++w) {
-        const float f = sh.m[w][tid] == -INFINITY ? 0.f : ex2(sh.m[w][tid] - mx);
+        const float f = ex2(sh.m[w][tid] - mx);
         sh.w[w][tid] = f;
         sum += f * sh.l[w][tid];
       }
@@ -726,7 +714,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
           float4 x[kFewPartials];
 #pragma unroll
           for (int i = 0; i < kFewPartials; ++i) {
-            m[i] = -INFINITY;
+            m[i] = kNone;
             if (i < n) {
               const float* p = slot(i);
               m[i] = __ldcg(p + kCols * kHeadDim + col);
@@ -741,7 +729,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
 #pragma unroll
           for (int i = 0; i < kFewPartials; ++i)
             if (i < n) {
-              const float f = m[i] == -INFINITY ? 0.f : ex2(m[i] - mx);
+              const float f = ex2(m[i] - mx);
               sum = fmaf(f, l[i], sum);
               v.x = fmaf(f, x[i].x, v.x); v.y = fmaf(f, x[i].y, v.y);
               v.z = fmaf(f, x[i].z, v.z); v.w = fmaf(f, x[i].w, v.w);
@@ -758,12 +746,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
         __syncthreads();
         static_assert(kAttnWarps >= kCols, "a warp per column");
         if (warp < kCols) {
-          float mx = -INFINITY, sum = 0.f;
+          float mx = kNone, sum = 0.f;
           for (int i = lane; i < n; i += 32) mx = fmaxf(mx, jn.w[i][warp]);
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
           for (int i = lane; i < n; i += 32) {
-            const float m = jn.w[i][warp], f = m == -INFINITY ? 0.f : ex2(m - mx);
+            const float f = ex2(jn.w[i][warp] - mx);
             jn.w[i][warp] = f;
             sum += f * jn.l[i][warp];
           }

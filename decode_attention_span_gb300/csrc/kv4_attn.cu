@@ -86,6 +86,7 @@ struct AttnParams {
   float *out, *lse;
   float* partials;   // [CTA][2][kStateFloats]
   int32_t* arrived;  // per group; zero between calls
+  uint64_t wait_ns;  // of a warp for its next chunk
   int batch, hpg, n_q, tpb, n_blk;
   float scale_log2;
 };
@@ -93,7 +94,7 @@ struct AttnParams {
 // D = A B + C in f16, 16 x 8 = 16 x 16 * 16 x 8 + 16 x 8
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
@@ -115,7 +116,7 @@ __device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t bits) {
 // 8x8 matrix of 16-bit values over the warp, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     for (int k = 0; k < mine; ++k) {
       const uint32_t st = (done + k) % kStages;
       if ((present >> (k & 31) & 1u) && !lost) {
-        if (__all_sync(~0u, mbar_wait_parked(&sh.bar[warp][st], ((done + k) / kStages) & 1, kWaitNs))) {
+        if (__all_sync(~0u, mbar_wait_parked(&sh.bar[warp][st], ((done + k) / kStages) & 1, P.wait_ns))) {
           const int pos = (c0 + warp + k * kAttnWarps) * kChunkTokens;
           const int held = len - pos;
           const int seen[2] = {see[0] - pos, see[1] - pos};
@@ -883,6 +884,7 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
   P.lse = lse;
   P.arrived = reinterpret_cast<int32_t*>(w + L.arrived);
   P.partials = reinterpret_cast<float*>(w + L.partials);
+  P.wait_ns = (cfg->flags & SEKV_FLAG_SHORT_WAITS) ? 0 : kWaitNs;
   P.batch = cfg->batch;
   P.hpg = cfg->n_q_heads / cfg->n_kv_heads;
   P.n_q = n_q;

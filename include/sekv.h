@@ -82,7 +82,8 @@ typedef struct sekv_config {
  * launch gaps between layers. */
 #define SEKV_FLAG_OVERLAP_PREVIOUS 1
 
-/* Fault-path testing only: every wait of a decode kernel for a copy to land
+/* Fault-path testing only: every wait of a decode kernel (sekv_kv4_attention's
+ * among them) for a copy to land
  * gives up at once if the copy has not landed when it is first tested
  * (normally it waits up to about two seconds).  Some wait then runs out, the
  * call's results are unreliable and sekv_workspace_status reports

@@ -495,6 +495,23 @@ def test_kv4_two_streams_at_once(sk):
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+def test_kv4_short_waits_time_out_and_leave_the_gpu_usable(sk):
+    """With waits that give up at once the call reports the time-out (or is right, if every
+    copy had landed), and the next call is right."""
+    cfg, cache, ws = kv_cache(sk, 1, 2, 200, 1, 8)
+    n = fill_cache(sk, cfg, cache, ws, [12000], 1)
+    q = torch.randn(1, 1, 8, 128, generator=gen(1)).bfloat16().cuda()
+    want = sk.kv4_attention(cfg, cache, q, n, 0.1, ws)
+    assert ws.status() == (0, 0)
+    short = sk.Config(1, 8, 2, 0, 0, 64, flags=sk.sekv.FLAG_SHORT_WAITS)
+    got = sk.kv4_attention(short, cache, q, n, 0.1, ws)
+    code, detail = ws.status()
+    assert (code, detail) == (2, 4) or (code == 0 and torch.equal(got[0], want[0]))
+    again = sk.kv4_attention(cfg, cache, q, n, 0.1, ws)
+    assert ws.status() == (0, 0)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
 def test_kv4_attention_non_finite_queries(sk):
     """A NaN or an infinity in one head's query makes that head NaN and no other."""
     cfg, cache, ws = kv_cache(sk, 1, 1, 2, 2, 4)

@@ -54,7 +54,6 @@ struct AttnShared {
   float4 par[kAttnWarps][2][kChunkTokens];  // a chunk's scales and zeros, K's and V's, as floats
   float m[kAttnWarps][kCols];
   float l[kAttnWarps][kCols];
-  float w[kAttnWarps][kCols];
   float mx[kCols], sum[kCols];
   // the segment's queries: B operand, two 16-dimension steps a vector; per group of dimensions
   // the sums of q and -64 times those of the odd dimensions; from a column's units to log2 of
@@ -475,6 +474,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
   const int each = total / n_cta, over = total - each * n_cta;
   auto start = [&](int c) { return each * c + over * c / n_cta; };
   const int u0 = start(cta), u1 = start(cta + 1);
+  auto cta_of = [&](int u) {  // whose share unit u is in: an estimate, and its correction
+    int c = max(0, min(n_cta - 1, int(float(u) * (float(n_cta) / float(total)))));
+    while (start(c) > u) --c;
+    while (start(c + 1) <= u) ++c;
+    return c;
+  };
 
   uint32_t done = 0;  // chunks this warp has taken off its ring, over all segments
   bool lost = false;  // a copy of this warp did not land in time
@@ -492,8 +497,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     const int gi = rel / n_units;
     const int i0 = rel - gi * n_units, i1 = min(n_units, i0 + (u1 - u));
     // this segment's chunks of the group
-    const int c0 = by_piece ? int(int64_t(chunks_of(len)) * i0 / n_units) : i0;
-    const int c1 = by_piece ? int(int64_t(chunks_of(len)) * i1 / n_units) : i1;
+    int c0 = i0, c1 = i1;
+    if (by_piece) {  // n_units is at most the number of CTAs: no product overflows
+      const int n = chunks_of(len), q = n / n_units, r = n - q * n_units;
+      c0 = q * i0 + r * i0 / n_units;
+      c1 = q * i1 + r * i1 / n_units;
+    }
     const int blk = gi / P.pg.hkv, head = gi - blk * P.pg.hkv;
     const int cols = min(P.tpb, P.n_q - blk * P.tpb) * P.hpg;
 
@@ -620,46 +629,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       __syncwarp();  // the state goes where the kept values were
     }
 
-    // the warps' states into shared memory
+    // the warps' states into shared memory (PACK: the lower parts' sums as columns 4-7)
     const float inv_unit = 1.f / S.unit;
-    if (PACK) {  // the lower parts' sums to the upper ones'
+#pragma unroll 1
+    for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S.o[j][i] += __shfl_xor_sync(~0u, S.o[j][i], 2);
-    }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
+      for (int c = 0; c < 2; ++c) {
         S.l[c] += __shfl_xor_sync(~0u, S.l[c], o);
         S.c[c][0] += __shfl_xor_sync(~0u, S.c[c][0], o);
         S.c[c][1] += __shfl_xor_sync(~0u, S.c[c][1], o);
       }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
       if (g == 0) {
         sh.m[warp][2 * t + c] = S.m[c];
         sh.l[warp][2 * t + c] = S.l[c];
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float add = S.c[c][m >> 1];
+        const float add = PACK && t >= 2 ? 0.f : S.c[c][m >> 1];
         *reinterpret_cast<float4*>(&sh.o[warp][2 * t + c][(m >> 1) * 64 + g * 8 + (m & 1) * 4]) =
             make_float4(fmaf(S.o[2 * m][c], inv_unit, add), fmaf(S.o[2 * m + 1][c], inv_unit, add),
                         fmaf(S.o[2 * m][2 + c], inv_unit, add),
                         fmaf(S.o[2 * m + 1][2 + c], inv_unit, add));
       }
-    }
-    __syncthreads();
-    if (tid < kCols) {
-      float mx = kNone, sum = 0.f;
-      for (int w = 0; w < kAttnWarps; ++w) mx = fmaxf(mx, sh.m[w][tid]);
-      for (int w = 0; w < kAttnWarps; ++w) {
-        const float f = ex2(sh.m[w][tid] - mx);
-        sh.w[w][tid] = f;
-        sum += f * sh.l[w][tid];
-      }
-      sh.mx[tid] = mx;
-      sh.sum[tid] = sum;
     }
     __syncthreads();
 
@@ -676,34 +669,55 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       if (d == 0 && P.lse) P.lse[row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
     };
     float* part = P.partials + (int64_t(cta) * 2 + (gs > u0 ? 1 : 0)) * kStateFloats;
-    if (tid < kCols * kHeadDim / 4) {
-      const int col = tid / (kHeadDim / 4), d = tid % (kHeadDim / 4) * 4;
+    if (warp < (PACK ? kCols / 2 : kCols)) {  // warp: a column, lane: four of its dimensions
+      const int col = warp, d = 4 * lane;
+      const float m = lane < kAttnWarps ? sh.m[lane][col] : kNone;
+      float mx = m;
+#pragma unroll 1
+      for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+      mx = __shfl_sync(~0u, mx, 0);
+      const float f = ex2(m - mx);
+      float sum = lane < kAttnWarps ? f * sh.l[lane][col] : 0.f;
+#pragma unroll 1
+      for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      sum = __shfl_sync(~0u, sum, 0);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int w = 0; w < kAttnWarps; ++w) {
-        const float f = sh.w[w][col];
-        const float4 x = *reinterpret_cast<const float4*>(&sh.o[w][col][d]);
-        v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+        const float fw = __shfl_sync(~0u, f, w);
+        float4 x = *reinterpret_cast<const float4*>(&sh.o[w][col][d]);
+        if (PACK) {
+          const float4 y = *reinterpret_cast<const float4*>(&sh.o[w][col + kCols / 2][d]);
+          x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        }
+        v.x = fmaf(fw, x.x, v.x); v.y = fmaf(fw, x.y, v.y);
+        v.z = fmaf(fw, x.z, v.z); v.w = fmaf(fw, x.w, v.w);
       }
-      if (whole) {
-        if (col < cols) write_out(col, d, v, sh.mx[col], sh.sum[col]);
-      } else {
-        *reinterpret_cast<float4*>(part + col * kHeadDim + d) = v;
-        if (d == 0) {
-          part[kCols * kHeadDim + col] = sh.mx[col];
-          part[kCols * kHeadDim + kCols + col] = sh.sum[col];
+      if (col < cols) {
+        if (whole) {
+          write_out(col, d, v, mx, sum);
+        } else {
+          *reinterpret_cast<float4*>(part + col * kHeadDim + d) = v;
+          if (lane == 0) {
+            part[kCols * kHeadDim + col] = mx;
+            part[kCols * kHeadDim + kCols + col] = sum;
+          }
         }
       }
     }
     if (!whole) {
       // the CTAs of this group, in order of their pieces
-      const int first = int((int64_t(gs + 1) * n_cta - 1) / total);
-      const int n = int((int64_t(ge) * n_cta - 1) / total) - first + 1;
+      const int first = cta_of(gs), n = cta_of(ge - 1) - first + 1;
       __syncthreads();
       if (tid == 0) {
-        __threadfence();
-        sh.last = atomicAdd(P.arrived + group, 1) == n - 1;
+        // releases the CTA's partial (ordered before by the barrier), acquires the others'
+        int before;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(P.arrived + group)
+                     : "memory");
+        sh.last = before == n - 1;
         if (sh.last) P.arrived[group] = 0;  // ready for the next call
-        __threadfence();
       }
       __syncthreads();
       auto slot = [&](int i) {
@@ -711,7 +725,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       };
       if (sh.last && n <= kFewPartials) {
         // each thread on its own: two loads deep and no barrier
-        if (tid < kCols * kHeadDim / 4) {
+        if (tid < cols * kHeadDim / 4) {
           const int col = tid / (kHeadDim / 4);
           float m[kFewPartials], l[kFewPartials];
           float4 x[kFewPartials];
@@ -737,7 +751,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
               v.x = fmaf(f, x[i].x, v.x); v.y = fmaf(f, x[i].y, v.y);
               v.z = fmaf(f, x[i].z, v.z); v.w = fmaf(f, x[i].w, v.w);
             }
-          if (col < cols) write_out(col, tid % (kHeadDim / 4) * 4, v, mx, sum);
+          write_out(col, tid % (kHeadDim / 4) * 4, v, mx, sum);
         }
       } else if (sh.last) {
         JoinShared& jn = *reinterpret_cast<JoinShared*>(&sh.o[0][0][0]);

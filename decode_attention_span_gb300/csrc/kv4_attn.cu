@@ -1,8 +1,7 @@
 // sekv_kv4_attention: attention of a few query tokens over the 4-bit cache.
 //
-// Bound by memory: 144 bytes per (token, KV head) are read once for all query
-// heads of the group.  The cache's layout is the matrix instructions' operand
-// layout: a lane's codes come from shared memory as 16-byte words and become the
+// 144 bytes per (token, KV head) are read once for all query heads of the group.
+// The cache's layout is the matrix instructions' operand layout: a lane's codes come from shared memory as 16-byte words and become the
 // A operand (tokens or dimensions in its 16 rows, the eight (token, head) columns
 // in B) with one or two instructions per pair; no K or V value is rebuilt.  With
 // K^ = z + s n for each group of 64 dimensions,
@@ -22,6 +21,17 @@
 // joins its warps' softmax states per (sequence, KV head) and, where that
 // group spans several CTAs, leaves a partial; the last of them to finish joins
 // the partials in order.
+//
+// What bounds it is instruction issue, not memory: a chunk takes a warp about 660
+// instructions (256 of them turn codes into operands), issued at 55% of the rate
+// because most are two-clock ones (logic, f16 pairs) and a matrix instruction takes two to
+// four slots.  Measured, 16 sequences of up to 65536 tokens, 28 query and 4 KV heads (463 MB):
+// 111 us, copies alone 76 us, arithmetic alone 107 us; one sequence of 131072, 32 and 8
+// heads (151 MB): 41 us, copies alone 31 us, of which about 9 us move no data.  128-row
+// tcgen05 tiles would want the operands in shared memory as f16: 16 KB a chunk written and
+// read again at 128 bytes a clock, 256 clocks where a chunk now takes 280 in all.
+// e4m3 operands (a code's four bits in a byte are n 2^-9) need no arithmetic to make, but
+// mma.sync converts them to f16 again: 53 us where f16 took 44.
 #include <math.h>
 
 #include <algorithm>
@@ -32,9 +42,9 @@ using namespace sekv;
 
 namespace {
 
-constexpr int kAttnWarps = 12;
+constexpr int kAttnWarps = 12;  // 168 registers; 8: 124 us where 12 take 112 and 16 (128 registers) 114
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kStages = 2;
+constexpr int kStages = 2;       // 3 are no faster: the copies are not what is waited for
 constexpr int kChunkTokens = 32;
 constexpr int kChunkBytes = 2 * kKv4TileBytes;
 constexpr int kMaxCtas = 256;                    // of a launch
@@ -45,7 +55,7 @@ constexpr int kGroupCost = 40;
 constexpr float kNone = -3e38f;
 constexpr float kGrowth = 8.f;                   // log2 by which a weight may outgrow the reference
 constexpr float kMaxScale = 128.f;               // of V with the unit: 2^8 times it fits f16
-constexpr int kFlush = 16;                       // chunks between two flushes
+constexpr int kFlush = 16;                       // chunks between two flushes: 1% of the time
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct AttnShared {
@@ -224,7 +234,7 @@ struct Query {
 };
 
 // The matrix instructions cut their sums off towards zero, which over hundreds of them adds
-// up to more than fp32's rounding.  So every kFlush chunks a warp adds its values to
+// up to more than fp32's rounding (16 x 65536: 1.3e-6 of the result, with flushes 4e-7).  So every kFlush chunks a warp adds its values to
 // a second set in shared memory, rounded properly; eight 16-byte words a lane.
 __device__ __forceinline__ void flush(WarpState& S, float4* kept, int lane, bool first) {
 #pragma unroll
@@ -578,8 +588,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     // up to here no token is hidden from any column in use
     const int open = len - (P.n_q - 1 - blk * P.tpb);
 
-    // Only now the first copies: with the copy engine's queue full, shuffles and loads from
-    // shared memory behind them take 600 clocks a step (the queries above: 3000).
+    // the first copies; the queries' shuffles above do not wait behind them
     for (int k = 0; k < min(mine, kStages); ++k) issue(k);
 
     WarpState S;

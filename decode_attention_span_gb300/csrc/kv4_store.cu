@@ -10,8 +10,11 @@
 //
 // Codes: n = rint(fl((x - z) / s)) by definition.  x / s - z / s by one fma and
 // the reciprocal of s is off by less than 2^-12 as long as |z / s| < 2^11, so only a
-// quotient nearer than that to a half needs the division; the lanes that have
-// one divide all eight.
+// quotient nearer than that to a half needs the division.
+//
+// Measured, 32768 tokens of 8 KV heads: append 48 us (172 MB, 25 us at the copy rate; 170
+// instructions a row issue at 78% of the rate: the codes' arithmetic bounds it), read 30 us
+// (the same bytes).  A warp per token with direct stores took 226 us for both.
 #include "kv4.cuh"
 
 using namespace sekv;

@@ -1,7 +1,9 @@
 // sekv_token_logprobs and sekv_surprisal: log-probabilities of given tokens,
 // entropies and the likeliest alternatives, in one pass over the logits.
 //
-// Bound by memory: rows * vocab elements are read once.  A row is cut into
+// Bound by memory: rows * vocab elements are read once (surprisal of 4096 rows of 128000
+// in bf16: 163 us, 95% of the copy rate; few rows: launch and joins, 6 us for one row of
+// 32000 with five alternatives).  A row is cut into
 // 16-byte vectors; a cluster of 1 to 16 CTAs takes one row (as many as it takes
 // to fill the GPU when there are few rows), and each thread keeps a running
 // maximum m, S = sum e^(x-m) and A = sum e^(x-m) (x-m) of its own vectors, joined
@@ -552,12 +554,15 @@ template <typename T>
 sekv_status logprobs_of(const LpParams& P, int64_t rows, bool full, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return SEKV_ERR_CUDA;
-  // CTAs per row: doubled while the rows alone leave SMs without a CTA and a
-  // CTA's share is more than one vector per thread
+  // CTAs per row: doubled while the rows alone leave SMs without a CTA and a CTA's share is
+  // more than one vector per thread.  More only multiplies the joins: 257 rows of 50021
+  // in f32 take 13 us with one CTA, 18 with two, 22 with four.
   const int64_t vecs = P.vocab / Row<T>::VE + 1;
   int nc = 1;
   while (nc < kLpMaxCluster && rows * nc < sms && vecs > int64_t(nc) * 512) nc *= 2;
   if (rows * nc > INT32_MAX) return SEKV_ERR_UNSUPPORTED;
+  // threads by the CTA's share: 2000 rows of 500 take 10 us with 128 threads, 15 with 256 and
+  // 26 with 512, 1000 rows of 128000 53 us with 256 and 49 with 512
   if (vecs / nc <= 256)
     return full ? launch_logprobs<T, true, 128>(P, rows, nc, stream)
                 : launch_logprobs<T, false, 128>(P, rows, nc, stream);

@@ -8,13 +8,14 @@
 // are 2-byte pieces 64 bytes apart, which one by one cost a memory sector each);
 // of a tile written in part only the tokens' own bytes are touched.
 //
-// Codes: n = rint(fl((x - z) / s)) by definition.  x / s - z / s by one fma and
-// the reciprocal of s is off by less than 2^-12 as long as |z / s| < 2^11, so only a
-// quotient nearer than that to a half needs the division.
+// Codes: n = rint(fl((x - z) / s)) by definition.  The quotient is taken with the
+// group's reciprocal and Markstein's correction (q + (a - q s) r, the residual exact in
+// an fma), which rounds as a division does.
 //
-// Measured, 32768 tokens of 8 KV heads: append 48 us (172 MB, 25 us at the copy rate; 170
-// instructions a row issue at 78% of the rate: the codes' arithmetic bounds it), read 30 us
-// (the same bytes).  A warp per token with direct stores took 226 us for both.
+// Measured, 32768 tokens of 8 KV heads: append 36 us (172 MB, 25 us at the copy rate; the
+// codes' arithmetic bounds it), read 30 us (the same bytes).  With an approximate quotient and
+// a division wherever it came near a half (39% of bf16 rows have such a value) append took
+// 48 us; a warp per token with direct stores took 226 us for both.
 #include "kv4.cuh"
 
 using namespace sekv;
@@ -23,7 +24,7 @@ namespace {
 
 constexpr int kStoreThreads = 128;
 constexpr int kStoreWarps = kStoreThreads / 32;
-constexpr int kRowsAhead = 8;  // token rows on their way to a warp
+constexpr int kRowsAhead = 4;  // token rows on their way to a warp (8: 67 us for 65, fewer warps fit)
 
 struct StoreParams {
   Kv4Pages pg;
@@ -84,6 +85,19 @@ __device__ __forceinline__ float bf16_at_or_below(float x, __half2) {
   return __bfloat162float(__float2bfloat16_rd(x));
 }
 
+// The codes where s is below 2^-100, and a reciprocal or a quotient may be out of range.
+template <typename T2>
+__device__ __noinline__ uint32_t small_codes(uint4 in, float z, float s) {
+  const uint32_t u[4] = {in.x, in.y, in.z, in.w};
+  uint32_t word = 0;
+  for (int i = 7; i >= 0; --i) {
+    const float2 x = floats(u[i >> 1], T2());
+    const float n = rintf(__fdiv_rn((i & 1 ? x.y : x.x) - z, s));
+    word = word * 16 + uint32_t(fminf(fmaxf(n, 0.f), 15.f));
+  }
+  return word;
+}
+
 // Codes (eight nibbles) and bf16 s | z << 16 of this lane's eight values, whose group is
 // held by eight neighbouring lanes.
 template <typename T2>
@@ -114,37 +128,23 @@ __device__ __forceinline__ void quantise(const uint4& in, uint32_t& word, uint32
     return;
   }
   sz = __byte_perm(__bfloat16_as_ushort(sb), __float_as_uint(z), 0x7610);
-  float r;  // 1 / s to an ulp
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  const float zr = -z * r;
-  const float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
-  float q[8], n[8], off = 0.f;
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+  if (s >= 7.9e-31f) {
+    float r;  // 1 / s to an ulp, then by Newton's step
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = fmaf(fmaf(-s, r, 1.f), r, r);
+    uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = floats(u[i], T2());
-    q[2 * i] = fmaf(x.x, r, zr);
-    q[2 * i + 1] = fmaf(x.y, r, zr);
+    for (int i = 7; i >= 0; --i) {
+      const float2 x = floats(u[i >> 1], T2());
+      const float d = (i & 1 ? x.y : x.x) - z;
+      const float q0 = d * r, q = fmaf(fmaf(-q0, s, d), r, q0);
+      w = w * 16 + __float_as_uint(q + kRound);  // the bits of kRound come off below
+    }
+    word = w - __float_as_uint(kRound) * 0x11111111u;
+  } else {
+    word = s > 0.f ? small_codes<T2>(in, z, s) : 0u;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    n[i] = (q[i] + kRound) - kRound;
-    off = fmaxf(off, fabsf(q[i] - n[i]));
-  }
-  // s below 2^-100 (or 0): the reciprocal or the range of q may be out of bounds
-  const bool far = !(fabsf(zr) < 2048.f) || s < 7.9e-31f;
-  const float kNear = 0.5f - 1.f / 4096.f;
-  if (off >= kNear || far) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (far || fabsf(q[i] - n[i]) >= kNear) {
-        const float2 x = floats(u[i >> 1], T2());
-        n[i] = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn((i & 1 ? x.y : x.x) - z, s)), 0.f), 15.f) : 0.f;
-      }
-  }
-  // four codes as one whole number below 2^16
-  const float h0 = fmaf(fmaf(fmaf(n[3], 16.f, n[2]), 16.f, n[1]), 16.f, n[0]);
-  const float h1 = fmaf(fmaf(fmaf(n[7], 16.f, n[6]), 16.f, n[5]), 16.f, n[4]);
-  word = __byte_perm(__float_as_uint(h0 + kRound), __float_as_uint(h1 + kRound), 0x5410);
 }
 
 // Where a lane's pieces of a token row go in a tile: the codes' lower and upper half

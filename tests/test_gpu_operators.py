@@ -340,6 +340,30 @@ def test_kv4_append_writes_the_documented_bytes(sk, dtype, B, H, T, first, valid
     assert kd.dtype == torch.bfloat16 and kd.shape == (B, H, T, 128) and ws.status() == (0, 0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_kv4_append_ties_and_tiny_steps(sk, dtype):
+    """Whole numbers whose quotients fall on halves (to the even code), for every step from 2
+    to 16 and for steps of powers of two down to where they vanish, and steps below 2^-100."""
+    cfg, cache, ws = kv_cache(sk, 1, 1, 2)
+    x = torch.zeros(60, 128)
+    for r in range(15):                      # s = r + 2: values 0, s / 2, s, ... 15 s
+        x[r, :64] = (torch.arange(64) % 31) * (r + 2) / 2
+        x[r, 64:] = -x[r, :64]
+    for r in range(15, 60):
+        x[r, :64] = (torch.arange(64) % 31) * 2.0 ** -(r * 2.9 // 1 + (0 if dtype == "bf16" else -40))
+        x[r, 64:] = x[r, :64] * (1 + 2.0 ** -5)
+    x = x.to(DT[dtype])[None, :, None]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sk.kv4_append(cfg, cache, x.cuda(), -x.cuda(), zero, ws)
+    want = cache.pages.cpu().numpy().copy()
+    table = cache.page_table.cpu().numpy()
+    for is_v, y in ((0, x), (1, -x)):
+        n, sb, zb = kv4.quantise(y.float().numpy())
+        for t in range(60):
+            kv4.put(want, table, 0, 0, t, n[0, t, 0], sb[0, t, 0], zb[0, t, 0], is_v)
+    assert np.array_equal(cache.pages.cpu().numpy(), want)
+
+
 def test_kv4_append_strides_and_non_finite(sk):
     cfg, cache, ws = kv_cache(sk, 2, 2, 2)
     g = gen(3)

@@ -64,9 +64,11 @@ def parse():
     ap.add_argument("--traffic-scale", type=float, default=1.0)
     ap.add_argument("--traffic-command", default="")
     ap.add_argument("--path", default="decode",
-                    choices=["decode", "build", "fullkv", "append", "multi", "e2e"],
+                    choices=["decode", "build", "fullkv", "kv4", "append", "multi", "e2e"],
                     help="decode: the headline decode step; build: the prefill cache build; "
                          "fullkv: the same decode step over a full-KV cache (comparator); "
+                         "kv4: a decode step over a cache of every token in 4 bits (rotate, "
+                         "append, attend); "
                          "append: decode-time cache maintenance, one token per step; "
                          "multi: several query tokens per sequence over one cache; "
                          "e2e: the tiered end-to-end leg of the decode line alone")
@@ -1219,6 +1221,79 @@ def run_fullkv_bench(args, ws_n, rank, local):
     print(json.dumps(line), flush=True)
 
 
+def run_kv4_bench(args, ws_n, rank, local):
+    """A decode step over the 4-bit cache at the headline shape: per layer the new
+    token's query and key are rotated, its key and value appended, and the query
+    attends to all T tokens.  Layers hold distinct caches, so every step streams
+    from HBM; each replay appends at the same position, T - 1."""
+    import decode_attention_span_gb300 as sk
+    if not torch.cuda.is_available():
+        raise SystemExit("bench.py (kv4) needs a CUDA device")
+    dev = torch.device("cuda", local)
+    torch.cuda.set_device(dev)
+    w = synth.get_config(args.config)
+    if args.layers:
+        w = synth.get_config(args.config, layers=args.layers)
+    T, B = w.ctx, w.batch
+    cfg = sk.Config(B, w.n_q_heads, w.n_kv_heads, 0, 0, 64)
+    ws = sk.Workspace(cfg, dev, which=sk.SEKV_CALL_KV4, ctx_len=1)
+    plan = sk.RopePlan(128, base=500000.0, device=dev)
+    pages = -(-T // 64)
+    i32 = dict(dtype=torch.int32, device=dev)
+    table = torch.arange(B * pages, **i32).view(B, pages)
+    zero, last, lens = (torch.full((B,), n, **i32) for n in (0, T - 1, T))
+    pos = last.view(B, 1)
+    layers = []
+    for l in range(w.layers):
+        d = gen.full_kv_cache(w, l, T, device=dev)
+        g = gen._gen(w.seed * 7919 + 101 * l + 1, dev)
+        cache = sk.Kv4Cache(cfg, sk.alloc_kv4_pages(cfg, B * pages, dev), table)
+        k, v = (d[n][:, :, :T].transpose(1, 2) for n in ("k_full", "v_full"))
+        sk.kv4_append(cfg, cache, k, v, zero, ws)
+        q = gen.query(g, B, w.n_q_heads, dev).view(B, 1, w.n_q_heads, 128)
+        layers.append(dict(cache=cache, q=q, q_rot=torch.empty_like(q),
+                           k=k[:, -1:].clone(), v=v[:, -1:].clone(),
+                           k_rot=torch.empty(B, 1, w.n_kv_heads, 128, dtype=q.dtype, device=dev),
+                           out=torch.empty(B, 1, w.n_q_heads, 128, device=dev),
+                           lse=torch.empty(B, 1, w.n_q_heads, device=dev)))
+    scale = sk.default_scale()
+
+    def step():
+        for L in layers:
+            sk.rope(plan, L["q"], L["k"], pos, q_out=L["q_rot"], k_out=L["k_rot"])
+            sk.kv4_append(cfg, L["cache"], L["k_rot"], L["v"], last, ws)
+            sk.kv4_attention(cfg, L["cache"], L["q_rot"], lens, scale, ws, out=L["out"],
+                             lse=L["lse"])
+
+    torch.cuda.synchronize()
+    clocks = ClockSampler(dev.index if dev.index is not None else 0)
+    ms_total, ck = time_graph(step, args.steps, args.warmup, torch.cuda.Stream(), ws_n, clocks)
+    ws.raise_on_error()
+    ms_total = max_over_ranks(ms_total, ws_n)
+    layer_s = ms_total / 1e3 / args.steps / w.layers
+    per_layer = float(B * w.n_kv_heads * T * 2 * 72)  # 72 bytes a row of 128 values
+    peak, peak_kind = measured_peaks()
+    achieved = per_layer / layer_s / 1e9
+    if rank != 0:
+        return
+    line = {"metric": f"decode steps/s over a 4-bit cache of every token at {T // 1024}K ctx "
+                      "(rotate, append, attend)",
+            "value": whole_job_rate(args.steps, ms_total, ws_n), "unit": "steps/s",
+            "n_gpus": ws_n, "steps": args.steps, "warmup": args.warmup,
+            "ms_per_step": ms_total / args.steps, "higher_is_better": True, "scaling": "weak",
+            "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+            "config": {"workload": w.name + "_kv4", "layers": w.layers, "batch": B, "ctx": T,
+                       "q_heads": w.n_q_heads, "kv_heads": w.n_kv_heads,
+                       "l2": "inputs larger than L2 (distinct caches per layer)",
+                       "graph": "one CUDA graph per step, three launches a layer"},
+            "roofline": {"bound": "hbm", "achieved": achieved, "peak": peak, "unit": "GB/s",
+                         "frac": achieved / peak, "traffic": None, "peak_kind": peak_kind,
+                         "kernel": "kv4_attn_kernel and the layer's rotation and append",
+                         "bytes_per_layer": per_layer, "avg_layer_us": layer_s * 1e6},
+            "clocks": ck, "gpu_launches": args.steps * w.layers * 3}
+    print(json.dumps(line), flush=True)
+
+
 def main():
     args = parse()
     if args.traffic_from:
@@ -1241,6 +1316,8 @@ def main():
     if args.path == "fullkv":
         run_fullkv_bench(args, ws_n, rank, local)
         return
+    if args.path == "kv4":
+        return run_kv4_bench(args, ws_n, rank, local)
     if args.path == "e2e":
         return run_e2e_bench(args, ws_n, rank, local)
     w = synth.get_config(args.config)

@@ -1,19 +1,29 @@
 // sekv_kv4_attention: attention of a few query tokens over the 4-bit cache.
 //
 // 144 bytes per (token, KV head) are read once for all query heads of the group.
-// The cache's layout is the matrix instructions' operand layout: a lane's codes come from shared memory as 16-byte words and become the
-// A operand (tokens or dimensions in its 16 rows, the eight (token, head) columns
-// in B) with one or two instructions per pair; no K or V value is rebuilt.  With
+// The cache's layout is the matrix instructions' operand layout: a lane's codes come from
+// shared memory as 16-byte words and become the A operand (tokens or dimensions in its 16 rows,
+// the eight (token, head) columns in B) with one or two instructions per pair; no K or V value
+// is rebuilt.  With
 // K^ = z + s n for each group of 64 dimensions,
 //   q . K^ = sum over groups of  s (sum_d q_d n_d) + z (sum_d q_d).
 // Queries enter as f16, scaled by a power of two per column (exact for bf16 but for
-// elements below 2^-23 of the column's largest).  A word's low nibbles become
-// 1024 + n, less 1024; its high nibbles stay 1024 + 16 n against q / 16, and the 64 too
-// many come off by starting the accumulators at -64 sum q.  For V,
-//   sum_j p_j V^_j = sum_j (p_j s_j) (n_j - 8) + sum_j p_j (z_j + 8 s_j),
-// where the weight p_j s_j enters as the sum of two f16 numbers (22 significant
-// bits: one alone would cost the fp32 result 13 of its bits), scaled by a power of
-// two that follows the largest s seen, so that scales of any size fit f16.
+// elements below 2^-23 of the column's largest).  Codes masked out of a word are f16 numbers
+// below the normal ones as they stand: n 2^-24 from the low nibbles, n 2^-20 from the high ones
+// (K's low ones are multiplied up to n 2^-14, for queries 2^-6 of the high ones').  For V,
+//   sum_j p_j V^_j = sum_j +-(p_j s_j) n'_j + sum_j p_j z'_j,
+// an even token with n' = n, z' = z and +, an odd one with n' = 15 - n, z' = z + 15 s and -:
+// the mask's instruction inverts the odd tokens' codes too, and the sum of many tokens stays
+// as small as it would with codes around zero.  The weight p_j s_j enters as the sum of two f16
+// numbers (22 significant bits: one alone would cost the fp32 result 13 of its bits), scaled by
+// a power of two that follows the largest s seen, so that scales of any size fit f16.
+//
+// The matrix instructions take a number below the normal ones as if it were as large as those
+// when they line their addends up, and cut off 25 bits under the largest.  So the place of
+// a code in its f16 costs bits: shifted up by two, V's give an error of 2.6e-7 where n 2^-24
+// gives 1.1e-6 (4 x 2000), and a query element counts in steps of 2^-19 of the column's largest
+// (n 2^-24 for all of K: 2^-15, and 100 us at 16 x 65536 instead of 103; K's high nibbles as
+// normal numbers too: 107 us).
 //
 // Work: the cache is a line of chunks of 32 tokens (sequence by sequence, in
 // it KV head by KV head), cut into equal pieces, one per CTA.  The warps of a CTA
@@ -22,14 +32,15 @@
 // group spans several CTAs, leaves a partial; the last of them to finish joins
 // the partials in order.
 //
-// What bounds it is instruction issue, not memory: a chunk takes a warp about 660
-// instructions (256 of them turn codes into operands), issued at 55% of the rate
-// because most are two-clock ones (logic, f16 pairs) and a matrix instruction takes two to
-// four slots.  Measured, 16 sequences of up to 65536 tokens, 28 query and 4 KV heads (463 MB):
-// 111 us, copies alone 76 us, arithmetic alone 107 us; one sequence of 131072, 32 and 8
-// heads (151 MB): 41 us, copies alone 31 us, of which about 9 us move no data.  128-row
+// What bounds it is instruction issue, not memory: a chunk takes a warp about 600
+// instructions (208 of them turn codes into operands), issued at 53% of the rate
+// because many are two-clock ones (logic, conversions), a matrix instruction takes two to
+// four slots, and registers allow three warps per SM quarter, too few to hide every wait for a
+// result.  Measured, 16 sequences of up to 65536 tokens, 28 query and 4 KV heads (463 MB):
+// 103 us, copies alone 76 us, arithmetic alone 97 us; one sequence of 131072, 32 and 8
+// heads (151 MB): 39.5 us, copies alone 31 us, of which about 9 us move no data.  128-row
 // tcgen05 tiles would want the operands in shared memory as f16: 16 KB a chunk written and
-// read again at 128 bytes a clock, 256 clocks where a chunk now takes 280 in all.
+// read again at 128 bytes a clock, 256 clocks where a chunk now takes 265 in all.
 // e4m3 operands (a code's four bits in a byte are n 2^-9) need no arithmetic to make, but
 // mma.sync converts them to f16 again: 53 us where f16 took 44.
 #include <math.h>
@@ -42,7 +53,7 @@ using namespace sekv;
 
 namespace {
 
-constexpr int kAttnWarps = 12;  // 168 registers; 8: 124 us where 12 take 112 and 16 (128 registers) 114
+constexpr int kAttnWarps = 12;  // 168 registers; 8: 118 us where 12 take 102 and 15 (128 registers) 109
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kStages = 2;       // 3 are no faster: the copies are not what is waited for
 constexpr int kChunkTokens = 32;
@@ -56,6 +67,7 @@ constexpr float kNone = -3e38f;
 constexpr float kGrowth = 8.f;                   // log2 by which a weight may outgrow the reference
 constexpr float kMaxScale = 128.f;               // of V with the unit: 2^8 times it fits f16
 constexpr int kFlush = 16;                       // chunks between two flushes: 1% of the time
+constexpr int kCodeBits = 20;                    // K's sums of q n are in units of 2^-20
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct AttnShared {
@@ -66,10 +78,9 @@ struct AttnShared {
   float l[kAttnWarps][kCols];
   float mx[kCols], sum[kCols];
   // the segment's queries: B operand, two 16-dimension steps a vector; per group of dimensions
-  // the sums of q and -64 times those of the odd dimensions; from a column's units to log2 of
-  // its weights
+  // the sums of q; from a column's units to log2 of its weights
   uint4 qb[4][32];
-  float q_sum[2][kCols], q_off[2][kCols], q_scale[kCols];
+  float q_sum[2][kCols], q_scale[kCols];
   uint64_t bar[kAttnWarps][kStages];
   int before[SEKV_KV4_MAX_BATCH + 1];  // chunks (or pieces) before each sequence
   int len[SEKV_KV4_MAX_BATCH];         // tokens of each sequence
@@ -103,7 +114,7 @@ struct AttnParams {
 // D = A B + C in f16, 16 x 8 = 16 x 16 * 16 x 8 + 16 x 8
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
@@ -113,50 +124,68 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
                                         uint32_t b1) {
   mma_f16(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
-// (w & MASK) | bits in one instruction: the compiler makes two of the plain form, whose
+// (w & MASK) ^ bits in one instruction: the compiler makes two of the plain form, whose
 // two constants do not fit one; `bits` stays in a register
 template <uint32_t MASK>
-__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t bits) {
+__device__ __forceinline__ uint32_t mask_xor(uint32_t w, uint32_t bits) {
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(MASK), "r"(bits));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "n"(MASK), "r"(bits));
   return r;
+}
+
+// Two floats in one register pair, and a product and sum of two at once
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(c.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return c;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+  return a;
+}
+
+// What h, a rounded pair, lacks of (w0, w1)
+__device__ __forceinline__ __half2 rest(__half2 h, float w0, float w1) {
+  float d0, d1;
+  asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; sub.rn.f32.f16 %0, a, %3; sub.rn.f32.f16 %1, b, %4;}"
+      : "=f"(d0), "=f"(d1)
+      : "r"(*reinterpret_cast<const uint32_t*>(&h)), "f"(w0), "f"(w1));
+  return __floats2half2_rn(-d0, -d1);
 }
 
 // 8x8 matrix of 16-bit values over the warp, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
-// The four pairs of a word's codes (pair i: codes i and i + 4) less 8, as f16: the
-// low nibbles of each byte as 1024 + n, the high ones as 1024 + 16 n, both exact.
-__device__ __forceinline__ void centred(uint32_t w, uint32_t (&r)[4]) {
+// The four pairs of a word of K's codes (pair i: codes i and i + 4) as f16 numbers: n 2^-14
+// from the low nibbles of each byte (pairs 0 and 2), n 2^-20 from the high ones.
+__device__ __forceinline__ void k_pairs(uint32_t w, uint32_t (&r)[4]) {
   const uint32_t w8 = w >> 8;
-  const uint32_t u[4] = {mask_or<0x000f000fu>(w, 0x64006400u), mask_or<0x00f000f0u>(w, 0x64006400u),
-                         mask_or<0x000f000fu>(w8, 0x64006400u), mask_or<0x00f000f0u>(w8, 0x64006400u)};
-  const __half2 low = __half2half2(__ushort_as_half(0xe408));    // -1032
-  const __half2 high = __half2half2(__ushort_as_half(0xd480));   // -72
-  const __half2 inv16 = __half2half2(__ushort_as_half(0x2c00));  // 1/16
+  r[0] = w & 0x000f000fu;
+  r[1] = w & 0x00f000f0u;
+  r[2] = w8 & 0x000f000fu;
+  r[3] = w8 & 0x00f000f0u;
+  const __half2 up = __half2half2(__ushort_as_half(0x6400));  // 2^10
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 x = *reinterpret_cast<const __half2*>(&u[i]);
-    const __half2 y = i & 1 ? __hfma2(x, inv16, high) : __hadd2(x, low);
+  for (int i = 0; i < 4; i += 2) {
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r[i]), up);
     r[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
 }
-// K's pairs: n for the low nibbles (pairs 0 and 2), 1024 + 16 n for the high ones
-__device__ __forceinline__ void k_pairs(uint32_t w, uint32_t (&r)[4]) {
-  const uint32_t w8 = w >> 8;
-  const __half2 off = __half2half2(__ushort_as_half(0xe400));  // -1024
-  const uint32_t u[2] = {mask_or<0x000f000fu>(w, 0x64006400u), mask_or<0x000f000fu>(w8, 0x64006400u)};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&u[i]), off);
-    r[2 * i] = *reinterpret_cast<const uint32_t*>(&y);
-  }
-  r[1] = mask_or<0x00f000f0u>(w, 0x64006400u);
-  r[3] = mask_or<0x00f000f0u>(w8, 0x64006400u);
+// V's: n 2^-22 and n 2^-18, the upper code of each pair, an odd token's, as 15 - n.
+__device__ __forceinline__ void v_pairs(uint32_t w, uint32_t (&r)[4]) {
+  const uint32_t w2 = w << 2, w6 = w >> 6;
+  r[0] = mask_xor<0x003c003cu>(w2, 0x003c0000u);
+  r[1] = mask_xor<0x03c003c0u>(w2, 0x03c00000u);
+  r[2] = mask_xor<0x003c003cu>(w6, 0x003c0000u);
+  r[3] = mask_xor<0x03c003c0u>(w6, 0x03c00000u);
 }
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
@@ -182,7 +211,7 @@ __device__ __forceinline__ int chunks_of(int len) {
 struct WarpState {
   float o[8][4];   // [4 dims apiece: word m, i][rows g, g + 8 x columns], in units of 1 / unit
   float m[2], l[2];  // the weights' reference, log2: within 2^8 of the largest; kNone: no token yet
-  float c[2][2];   // sum of p (z + 8 s): [column][group of dimensions]
+  float c[2][2];   // sum of p z': [column][group of dimensions]
   float unit;      // power of two on the weights of o
 };
 
@@ -197,45 +226,42 @@ __device__ __forceinline__ void put_queries(AttnShared& sh, const T (&q)[4], int
     x[i] = q_value(q[i]);
     big = fmaxf(big, fabsf(x[i]));
   }
-  float odd = x[1] + x[3], sum = odd + x[0] + x[2];
+  float sum = (x[0] + x[2]) + (x[1] + x[3]);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
-    if (o < 16) {  // the lower lanes have the first group of dimensions
-      sum += __shfl_xor_sync(~0u, sum, o);
-      odd += __shfl_xor_sync(~0u, odd, o);
-    }
+    if (o < 16) sum += __shfl_xor_sync(~0u, sum, o);  // the lower lanes: the first group
   }
   // power of two that brings the largest element to 2^13 .. 2^14
   const int e = min(max(int(__float_as_uint(big) >> 23) - 127, -110), 110);
   const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
   if ((lane & 15) == 0) {
     // an infinity among the queries makes the column NaN, as NaN does
-    sh.q_sum[lane >> 4][col] = big < INFINITY ? sum * up : NAN;
-    sh.q_off[lane >> 4][col] = odd * up * -64.f;
-    sh.q_scale[col] = __uint_as_float(uint32_t(127 - 13 + e) << 23) * scale_log2;
+    sh.q_sum[lane >> 4][col] = big < INFINITY ? sum * up / (1 << kCodeBits) : NAN;
+    sh.q_scale[col] = __uint_as_float(uint32_t(127 - 13 + kCodeBits + e) << 23) * scale_log2;
   }
   // dimension d = 64 gr + 16 t + 8 w + i is in vector 2 gr + w of lane 4 col + t, half i / 4
-  // of word i % 4; odd dimensions meet high nibbles
+  // of word i % 4; even dimensions meet low nibbles
   __half* dst = reinterpret_cast<__half*>(&sh.qb[(lane >> 4) * 2 + (lane >> 1 & 1)][col * 4 + (lane >> 2 & 3)]);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    dst[2 * i + (lane & 1)] = __float2half_rn(x[i] * (i & 1 ? up * 0.0625f : up));
+    dst[2 * i + (lane & 1)] = __float2half_rn(x[i] * (i & 1 ? up : up * 0.015625f));
 }
 
 // The segment's queries as a lane uses them: its columns are 2t and 2t + 1.  The B operand
-// stays in shared memory: its sixteen registers are worth more to the rest (108 against
-// 111 us at 16 sequences of 65536).
+// stays in shared memory: its sixteen registers are worth more to the rest (3% at 16 sequences of
+// 65536).
 struct Query {
   const uint4* b;      // [4][32], this lane's element of each
   float sum[2][2];     // [column][group]
-  float offset[2][2];
   float scale_log2[2];
 };
 
 // The matrix instructions cut their sums off towards zero, which over hundreds of them adds
-// up to more than fp32's rounding (16 x 65536: 1.3e-6 of the result, with flushes 4e-7).  So every kFlush chunks a warp adds its values to
-// a second set in shared memory, rounded properly; eight 16-byte words a lane.
+// up to more than fp32's rounding (16 x 65536: 3.5e-7 of
+// the result, with flushes 1.8e-7; more where odd tokens weigh more than even ones or less).  So
+// every kFlush chunks a warp adds its values to a second set in shared memory, rounded
+// properly; eight 16-byte words a lane.
 __device__ __forceinline__ void flush(WarpState& S, float4* kept, int lane, bool first) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -296,8 +322,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
         const uint32_t a[4] = {r0[gr][0], r1[gr][0], r0[gr][1], r1[gr][1]};
         const uint4 q = Q.b[(2 * gr + i) * 32];
         if (i == 0)
-          mma_f16(acc[gr], a, q.x, q.y, Q.offset[0][gr], Q.offset[1][gr], Q.offset[0][gr],
-                  Q.offset[1][gr]);
+          mma_f16(acc[gr], a, q.x, q.y, 0.f, 0.f, 0.f, 0.f);
         else
           mma_f16(acc[gr], a, q.x, q.y);
       }
@@ -311,14 +336,16 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float4 k = par[0][ti * 16 + e * 8 + g];  // s, z of both groups
+      // both columns at once (2% at 16 sequences of 65536)
+      Pair y = mul2(Pair(k.x, k.x), Pair(acc[0][2 * e], acc[0][2 * e + 1]));
+      y = fma2(Pair(k.y, k.y), Pair(Q.sum[0][0], Q.sum[1][0]), y);
+      y = fma2(Pair(k.z, k.z), Pair(acc[1][2 * e], acc[1][2 * e + 1]), y);
+      y = fma2(Pair(k.w, k.w), Pair(Q.sum[0][1], Q.sum[1][1]), y);
+      y.get(x[ti][e][0], x[ti][e][1]);
+      if (EDGE)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float y = k.x * acc[0][2 * e + c];
-        y = fmaf(k.y, Q.sum[c][0], y);
-        y = fmaf(k.z, acc[1][2 * e + c], y);
-        y = fmaf(k.w, Q.sum[c][1], y);
-        x[ti][e][c] = !EDGE || ti * 16 + e * 8 + g < seen[c] ? y : -INFINITY;
-      }
+        for (int c = 0; c < 2; ++c)
+          if (ti * 16 + e * 8 + g >= seen[c]) x[ti][e][c] = -INFINITY;
     }
   }
 
@@ -356,7 +383,9 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
       for (int i = 0; i < 4; ++i) S.o[j][i] *= f[i & 1];
     if (any_kept) rescale_kept(kept, lane, f[0], f[1]);
   }
-  par[1][lane] = make_float4(s0 * S.unit, fmaf(8.f, s0, hi16(vp.x)), s1 * S.unit, fmaf(8.f, s1, hi16(vp.y)));
+  // s in units, signed, and z'
+  const float odd = lane & 1 ? 15.f : 0.f, su = lane & 1 ? -S.unit : S.unit;
+  par[1][lane] = make_float4(s0 * su, fmaf(odd, s0, hi16(vp.x)), s1 * su, fmaf(odd, s1, hi16(vp.y)));
   __syncwarp();
 
 #pragma unroll
@@ -366,7 +395,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
     const float low = lane & 2 ? -1.f : 0.f;  // PACK: this lane's columns take the lower parts
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float4 v = par[1][ti * 16 + e * 8 + g];  // s in units and z + 8 s, of both groups
+      const float4 v = par[1][ti * 16 + e * 8 + g];  // of both groups
       float p[2], w[2][2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -384,12 +413,12 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
           S.c[c][gr] = ok ? fmaf(p[c], z, S.c[c][gr]) : S.c[c][gr];
         }
         const __half2 h = __floats2half2_rn(w[gr][0], w[gr][1]);
-        const float2 hf = __half22float2(h);
         if (PACK) {
+          const float2 hf = __half22float2(h);
           const __half2 part = __floats2half2_rn(fmaf(low, hf.x, w[gr][0]), fmaf(low, hf.y, w[gr][1]));
           bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&part));
         } else {
-          const __half2 l = __floats2half2_rn(w[gr][0] - hf.x, w[gr][1] - hf.y);
+          const __half2 l = rest(h, w[gr][0], w[gr][1]);
           bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
           bl[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&l));
         }
@@ -401,8 +430,8 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       uint32_t r0[4], r1[4];
-      centred(w0[m], r0);
-      centred(w1[m], r1);
+      v_pairs(w0[m], r0);
+      v_pairs(w1[m], r1);
       const uint32_t a0[4] = {r0[0], r0[2], r1[0], r1[2]}, a1[4] = {r0[1], r0[3], r1[1], r1[3]};
       mma_f16(S.o[2 * m], a0, bh[m >> 1][0], bh[m >> 1][1]);
       mma_f16(S.o[2 * m + 1], a1, bh[m >> 1][0], bh[m >> 1][1]);
@@ -579,7 +608,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
 #pragma unroll
       for (int gr = 0; gr < 2; ++gr) {
         Q.sum[c][gr] = sh.q_sum[gr][col];
-        Q.offset[c][gr] = sh.q_off[gr][col];
       }
       Q.scale_log2[c] = sh.q_scale[col];
       const int real = PACK ? col & 3 : col;
@@ -639,7 +667,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     }
 
     // the warps' states into shared memory (PACK: the lower parts' sums as columns 4-7)
-    const float inv_unit = 1.f / S.unit;
+    const float inv_unit = 1.f / S.unit, low = float(1 << 22), high = float(1 << 18);
 #pragma unroll 1
     for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
@@ -658,9 +686,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       for (int m = 0; m < 4; ++m) {
         const float add = PACK && t >= 2 ? 0.f : S.c[c][m >> 1];
         *reinterpret_cast<float4*>(&sh.o[warp][2 * t + c][(m >> 1) * 64 + g * 8 + (m & 1) * 4]) =
-            make_float4(fmaf(S.o[2 * m][c], inv_unit, add), fmaf(S.o[2 * m + 1][c], inv_unit, add),
-                        fmaf(S.o[2 * m][2 + c], inv_unit, add),
-                        fmaf(S.o[2 * m + 1][2 + c], inv_unit, add));
+            make_float4(fmaf(S.o[2 * m][c] * low, inv_unit, add), fmaf(S.o[2 * m + 1][c] * high, inv_unit, add),
+                        fmaf(S.o[2 * m][2 + c] * low, inv_unit, add),
+                        fmaf(S.o[2 * m + 1][2 + c] * high, inv_unit, add));
       }
     }
     __syncthreads();

@@ -414,9 +414,9 @@ def test_kv4_bad_pages_and_positions_are_flagged(sk):
 
 
 def check_attention(out, lse, ref, what=""):
-    """A weight enters the product to 2^-16 of itself and an exponential errs by 2^-22; a logit by a few
-    2^-22 of the products it is summed from (codes up to 143 where the exact form has 15).  An
-    output moves by at most twice that times the weighted mean of |z| + 15 |s|."""
+    """A weight enters the product to 2^-16 of itself and an exponential errs by 2^-22; a logit by a
+    few 2^-22 of the products it is summed from.  An output moves by at most twice that times the
+    weighted mean of |z| + 15 |s|."""
     o, l, bound, logit = ref
     dx = 2.0 ** -19 * logit + 2.0 ** -21
     compare(out.double().cpu().numpy(), o, (2.0 ** -16 + 2 * dx[..., None]) * bound + 1e-37, what + "out")
@@ -561,6 +561,38 @@ def test_kv4_attention_values_of_any_size(sk, size):
     q = torch.randn(1, 1, 4, 128, generator=gen(2)).bfloat16()
     out, lse = sk.kv4_attention(cfg, cache, q.cuda(), zero + 150, 0.088, ws)
     check_attention(out, lse, kv4.attention(q.double().numpy(), cache.pages.cpu().numpy(), cache.page_table.cpu().numpy(), [150], 0.088))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("at", [6, 71])
+def test_kv4_attention_query_outlier(sk, dtype, at):
+    """One dimension (of an even and of an odd place) far larger than the others, where the keys
+    are small: the other dimensions still count."""
+    cfg, cache, ws = kv_cache(sk, 1, 1, 3, 1, 4)
+    k = torch.randint(0, 16, (1, 150, 1, 128), generator=gen(1)).float()
+    k[..., 0], k[..., 1], k[..., 64], k[..., 65], k[..., at] = 0, 15, 0, 15, 1
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sk.kv4_append(cfg, cache, k.to(DT[dtype]).cuda(), kv_rows(dtype, 1, 150, 1, 5)[1].cuda(), zero, ws)
+    q = torch.randn(1, 1, 4, 128, generator=gen(2))
+    q[..., at] = 64
+    q = q.to(DT[dtype])
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), zero + 150, 0.088, ws)
+    check_attention(out, lse, kv4.attention(q.double().numpy(), cache.pages.cpu().numpy(), cache.page_table.cpu().numpy(), [150], 0.088))
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("T", [31, 700, 9000])
+def test_kv4_attention_every_other_token(sk, odd, T):
+    """Only the even or only the odd tokens have weight."""
+    cfg, cache, ws = kv_cache(sk, 1, 1, -(-T // 64), 1, 2)
+    k, v = kv_rows("bf16", 1, T, 1, 5)
+    q = torch.randn(1, 1, 2, 128, generator=gen(2)).bfloat16()
+    u = q[0, 0].float().sum(0)
+    k = (0.1 * k.float() + torch.where(torch.arange(T) % 2 == odd, 1.0, -1.0).view(1, T, 1, 1) * u).bfloat16()
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sk.kv4_append(cfg, cache, k.cuda(), v.cuda(), zero, ws)
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), zero + T, 0.088, ws)
+    check_attention(out, lse, kv4.attention(q.double().numpy(), cache.pages.cpu().numpy(), cache.page_table.cpu().numpy(), [T], 0.088))
 
 
 def test_kv4_masked_row_with_nan_does_not_show(sk):

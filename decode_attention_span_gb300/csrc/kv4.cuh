@@ -30,6 +30,25 @@ __host__ __device__ inline int kv4_param(int j, int g, bool v) {
   return kKv4Params + (v ? 128 : 0) + 32 * ((j & 7) >> 1) + 16 * (j >> 3) + 8 * (j & 1) + 4 * g;
 }
 
+// Two floats in one register pair, and arithmetic on both at once: half the instructions
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(c.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return c;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+  return a;
+}
+
 struct Kv4Pages {
   uint8_t* pages;
   const int32_t* table;

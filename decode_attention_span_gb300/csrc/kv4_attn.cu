@@ -133,21 +133,6 @@ __device__ __forceinline__ uint32_t mask_xor(uint32_t w, uint32_t bits) {
   return r;
 }
 
-// Two floats in one register pair, and a product and sum of two at once
-struct Pair {
-  uint64_t v;
-  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(c.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return c;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
-  return a;
-}
-
 // What h, a rounded pair, lacks of (w0, w1)
 __device__ __forceinline__ __half2 rest(__half2 h, float w0, float w1) {
   float d0, d1;

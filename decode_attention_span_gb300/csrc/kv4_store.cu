@@ -12,8 +12,9 @@
 // group's reciprocal and Markstein's correction (q + (a - q s) r, the residual exact in
 // an fma), which rounds as a division does.
 //
-// Measured, 32768 tokens of 8 KV heads: append 36 us (172 MB, 25 us at the copy rate; the
-// codes' arithmetic bounds it), read 30 us (the same bytes).  With an approximate quotient and
+// Measured, 32768 tokens of 8 KV heads: append 35 us (172 MB, 25 us at the copy rate; the
+// codes' arithmetic bounds it), read 28 us (the same bytes), one after the other 59 us.
+// Arithmetic on two floats at a time took 5 us off both.  With an approximate quotient and
 // a division wherever it came near a half (39% of bf16 rows have such a value) append took
 // 48 us; a warp per token with direct stores took 226 us for both.
 #include "kv4.cuh"
@@ -22,9 +23,9 @@ using namespace sekv;
 
 namespace {
 
-constexpr int kStoreThreads = 128;
+constexpr int kStoreThreads = 64;  // 128: 60.2 us for 59 of both, 256: 63
 constexpr int kStoreWarps = kStoreThreads / 32;
-constexpr int kRowsAhead = 4;  // token rows on their way to a warp (8: 67 us for 65, fewer warps fit)
+constexpr int kRowsAhead = 4;  // token rows on their way to a warp (8: 2% slower, fewer warps fit)
 
 struct StoreParams {
   Kv4Pages pg;
@@ -121,29 +122,33 @@ __device__ __forceinline__ void quantise(const uint4& in, uint32_t& word, uint32
   const float z = bf16_at_or_below(ends.x, T2());
   const __nv_bfloat16 sb = __float2bfloat16_rn((mx - z) * (1.f / 15.f));
   const float s = __bfloat162float(sb);
-  word = 0;
-  // a NaN or an infinity in the group, or a range beyond fp32
-  if (!(fabsf(s) <= 3.4028235e38f) || !(fabsf(z) <= 3.4028235e38f)) {
-    sz = 0x7fff7fffu;
-    return;
-  }
   sz = __byte_perm(__bfloat16_as_ushort(sb), __float_as_uint(z), 0x7610);
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
-  if (s >= 7.9e-31f) {
+  // one comparison of bits for kSmall <= s <= the largest number
+  constexpr uint32_t kSmall = 0x0d800000u, kLargest = 0x7f7fffffu;  // 2^-100
+  if (__float_as_uint(s) - kSmall <= kLargest - kSmall) {
     float r;  // 1 / s to an ulp, then by Newton's step
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     r = fmaf(fmaf(-s, r, 1.f), r, r);
     uint32_t w = 0;
+    const Pair r2(r, r), s2(-s, -s);
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-      const float2 x = floats(u[i >> 1], T2());
-      const float d = (i & 1 ? x.y : x.x) - z;
-      const float q0 = d * r, q = fmaf(fmaf(-q0, s, d), r, q0);
-      w = w * 16 + __float_as_uint(q + kRound);  // the bits of kRound come off below
+    for (int i = 3; i >= 0; --i) {
+      const float2 x = floats(u[i], T2());
+      const Pair d = add2(Pair(x.x, x.y), Pair(-z, -z)), q0 = mul2(d, r2);
+      float even, odd;
+      add2(fma2(fma2(q0, s2, d), r2, q0), Pair(kRound, kRound)).get(even, odd);
+      w = w * 16 + __float_as_uint(odd);  // the bits of kRound come off below
+      w = w * 16 + __float_as_uint(even);
     }
     word = w - __float_as_uint(kRound) * 0x11111111u;
+  } else if (s > 0.f && s < 1.f) {
+    word = small_codes<T2>(in, z, s);
   } else {
-    word = s > 0.f ? small_codes<T2>(in, z, s) : 0u;
+    // one value in the whole group (s 0); or a NaN or an infinity in it, or a range beyond
+    // fp32, which leave s no number
+    word = 0;
+    if (s != 0.f) sz = 0x7fff7fffu;
   }
 }
 
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StorePara
   T* dst = static_cast<T*>(lane < 16 ? P.ko : P.vo) +
            ((int64_t(W.b) * P.pg.hkv + W.c) * P.n_tokens + W.t0) * kHeadDim + oct * 8;
   const int rows = W.t1 - W.t0;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < rows; ++i) {
     const int j = W.j0 + i;
     uint32_t word;
@@ -272,11 +277,14 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StorePara
     const uint32_t sz = *reinterpret_cast<const uint32_t*>(tile + kv4_param(j, oct >> 3, lane >= 16));
     const float s = __uint_as_float(sz << 16), z = __uint_as_float(sz & 0xffff0000u);
     float x[8];
+    // a byte under the exponent of 2^23 is 2^23 + n
+    const uint32_t even = word & 0x0f0f0f0fu, odd = word >> 4 & 0x0f0f0f0fu;
 #pragma unroll
-    for (int d = 0; d < 8; ++d) {
-      // the code's bits at the top of a mantissa are 16 + n
-      const uint32_t bits = (d < 5 ? word << (19 - 4 * d) : word >> (4 * d - 19)) & 0x00780000u;
-      x[d] = fmaf(s, __uint_as_float(bits | 0x41800000u) - 16.f, z);
+    for (int d = 0; d < 8; d += 2) {
+      const Pair n = add2(Pair(__uint_as_float(__byte_perm(even, 0x4b000000u, 0x7440 + d / 2)),
+                               __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7440 + d / 2))),
+                          Pair(-8388608.f, -8388608.f));
+      fma2(Pair(s, s), n, Pair(z, z)).get(x[d], x[d + 1]);
     }
     store8(dst + int64_t(i) * kHeadDim, x);
   }

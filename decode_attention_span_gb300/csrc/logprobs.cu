@@ -4,7 +4,7 @@
 // Bound by memory: rows * vocab elements are read once (surprisal of 4096 rows of 128000
 // in bf16: 163 us, 95% of the copy rate; few rows: launch and joins, 6 us for one row of
 // 32000 with five alternatives).  A row is cut into
-// 16-byte vectors; a cluster of 1 to 16 CTAs takes one row (as many as it takes
+// 16-byte vectors; a cluster of 1 to 8 CTAs takes one row (as many as it takes
 // to fill the GPU when there are few rows), and each thread keeps a running
 // maximum m, S = sum e^(x-m) and A = sum e^(x-m) (x-m) of its own vectors, joined
 // over the CTA by shuffles and over the cluster through distributed shared
@@ -556,7 +556,7 @@ sekv_status logprobs_of(const LpParams& P, int64_t rows, bool full, cudaStream_t
   if (sms <= 0) return SEKV_ERR_CUDA;
   // CTAs per row: doubled while the rows alone leave SMs without a CTA and a CTA's share is
   // more than one vector per thread.  More only multiplies the joins: 257 rows of 50021
-  // in f32 take 13 us with one CTA, 18 with two, 22 with four.
+  // in f32 with three alternatives take 16 us with one CTA, 23 with two, 29 with four.
   const int64_t vecs = P.vocab / Row<T>::VE + 1;
   int nc = 1;
   while (nc < kLpMaxCluster && rows * nc < sms && vecs > int64_t(nc) * 512) nc *= 2;

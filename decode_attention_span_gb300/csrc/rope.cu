@@ -281,6 +281,10 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
     if (!h->x || !h->y || h->n_heads < 0 || h->n_heads > 65535 ||
         reinterpret_cast<uintptr_t>(h->x) % elem || reinterpret_cast<uintptr_t>(h->y) % elem)
       return SEKV_ERR_INVALID;
+    // rows of the output that lie on one another
+    if ((batch > 1 && h->y_stride[0] == 0) || (n_tokens > 1 && h->y_stride[1] == 0) ||
+        (h->n_heads > 1 && h->y_stride[2] == 0))
+      return SEKV_ERR_INVALID;
     if (h->x == h->y && memcmp(h->x_stride, h->y_stride, sizeof(h->x_stride)) != 0)
       return SEKV_ERR_INVALID;
   }

@@ -663,7 +663,8 @@ typedef struct sekv_heads {
 /*
  * sekv_rope -- rotates queries and keys of [batch][n_tokens] tokens in one
  * launch.  y may be x with equal strides (in place; dimensions that pass through
- * are then not touched); otherwise x and y must not overlap.
+ * are then not touched); otherwise x and y must not overlap.  Rows of x may lie on one
+ * another (strides of 0: broadcast), rows of y must not.
  *   freqs     device, from sekv_rope_freqs; mscale likewise
  *   positions int32 or int64 (positions_64), of token (b, t) at b*pos_stride_b + t
  *             (0: shared by the batch).  A token with a negative position is

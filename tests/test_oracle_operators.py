@@ -197,6 +197,10 @@ def test_rope_refusals(libsekv):
                dict(m=math.nan), dict(freqs=None), dict(q=heads(x=None)), dict(q=heads(x=(1 << 20) + 1)), dict(q=heads(n=-1)),
                dict(q=heads(y=1 << 20, ys=(0, 128, 256)))):
         assert call(**kw) == INVALID, kw
+    # output rows on one another, which a broadcast tensor given for the output has
+    for kw in (dict(q=heads(ys=(0, 256, 0))), dict(q=heads(ys=(0, 0, 128))), dict(B=2), dict(k=heads(ys=(512, 0, 128))),
+               dict(q=heads(y=1 << 20, xs=(0, 0, 128), ys=(0, 0, 128)))):
+        assert call(**kw) == INVALID, kw
     assert call(dim=1026) == UNSUPPORTED and call(T=1 << 31) == UNSUPPORTED and call(q=heads(n=65535), k=heads(n=1)) == UNSUPPORTED
 
 

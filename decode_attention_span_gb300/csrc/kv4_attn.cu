@@ -439,6 +439,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
   if (lane == 0)
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.bar[warp][s], 1);
   fence_mbar_init();
+  follow_previous();
   // The plan, by one warp.  Chunks of each sequence (at least one, so that every group
   // has a CTA), then either every group cut into pieces of at most `piece` chunks, a CTA
   // each, or the line of all groups' chunks cut into equal pieces.
@@ -928,22 +929,14 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
   P.n_blk = blocks_of(cfg, n_q);
   P.scale_log2 = scale * kLog2e;
   const bool pack = n_q * P.hpg <= kCols / 2;
-  const void* const fns[4] = {reinterpret_cast<const void*>(kv4_attn_kernel<__nv_bfloat16, false>),
-                              reinterpret_cast<const void*>(kv4_attn_kernel<__half, false>),
-                              reinterpret_cast<const void*>(kv4_attn_kernel<__nv_bfloat16, true>),
-                              reinterpret_cast<const void*>(kv4_attn_kernel<__half, true>)};
-  const void* fn = fns[(dtype == SEKV_BF16 ? 0 : 1) + (pack ? 2 : 0)];
+  void (*const fns[4])(AttnParams) = {
+      kv4_attn_kernel<__nv_bfloat16, false>, kv4_attn_kernel<__half, false>,
+      kv4_attn_kernel<__nv_bfloat16, true>, kv4_attn_kernel<__half, true>};
+  void (*const fn)(AttnParams) = fns[(dtype == SEKV_BF16 ? 0 : 1) + (pack ? 2 : 0)];
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AttnShared)) !=
       cudaSuccess) {
     cudaGetLastError();
     return SEKV_ERR_CUDA;
   }
-  void* args[] = {&P};
-  if (cudaLaunchKernel(fn, dim3(sms), dim3(kAttnThreads), args, sizeof(AttnShared), stream) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return SEKV_ERR_CUDA;
-  }
-  count_launch(1);
-  return SEKV_OK;
+  return launch_following(fn, dim3(sms), kAttnThreads, sizeof(AttnShared), stream, P);
 }

@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StorePa
   __shared__ __align__(16) uint8_t staged[kStoreWarps][kKv4TileBytes];
   __shared__ uint4 in[kStoreWarps][kRowsAhead][32];  // each lane copies and reads its own
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  follow_previous();
   TileWork W;
   if (!tile_work(P, W)) return;  // warp-uniform
   const bool whole = W.t1 - W.t0 == kKv4Tile;
@@ -246,6 +247,7 @@ template <typename T>
 __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StoreParams P) {
   __shared__ __align__(16) uint8_t staged[kStoreWarps][kKv4TileBytes];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  follow_previous();
   TileWork W;
   if (!tile_work(P, W)) return;  // warp-uniform
   const uint8_t* tile = W.tile;
@@ -340,13 +342,8 @@ extern "C" sekv_status sekv_kv4_append(const sekv_config* cfg, const sekv_kv4_ca
   st = kv4_check_ws(cfg, 1, workspace_bytes);
   if (st != SEKV_OK) return st;
   const unsigned blocks = unsigned((P.items + kStoreWarps - 1) / kStoreWarps);
-  if (dtype == SEKV_BF16)
-    kv4_append_kernel<__nv_bfloat162><<<blocks, kStoreThreads, 0, stream>>>(P);
-  else
-    kv4_append_kernel<__half2><<<blocks, kStoreThreads, 0, stream>>>(P);
-  if (cudaGetLastError() != cudaSuccess) return SEKV_ERR_CUDA;
-  count_launch(1);
-  return SEKV_OK;
+  return launch_following(dtype == SEKV_BF16 ? kv4_append_kernel<__nv_bfloat162> : kv4_append_kernel<__half2>,
+                          dim3(blocks), kStoreThreads, 0, stream, P);
 }
 
 extern "C" sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cache* cache,
@@ -369,13 +366,8 @@ extern "C" sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cach
   st = kv4_check_ws(cfg, 1, workspace_bytes);
   if (st != SEKV_OK) return st;
   const unsigned blocks = unsigned((P.items + kStoreWarps - 1) / kStoreWarps);
-  if (dtype == SEKV_BF16)
-    kv4_read_kernel<__nv_bfloat16><<<blocks, kStoreThreads, 0, stream>>>(P);
-  else if (dtype == SEKV_F16)
-    kv4_read_kernel<__half><<<blocks, kStoreThreads, 0, stream>>>(P);
-  else
-    kv4_read_kernel<float><<<blocks, kStoreThreads, 0, stream>>>(P);
-  if (cudaGetLastError() != cudaSuccess) return SEKV_ERR_CUDA;
-  count_launch(1);
-  return SEKV_OK;
+  return launch_following(dtype == SEKV_BF16  ? kv4_read_kernel<__nv_bfloat16>
+                          : dtype == SEKV_F16 ? kv4_read_kernel<__half>
+                                              : kv4_read_kernel<float>,
+                          dim3(blocks), kStoreThreads, 0, stream, P);
 }

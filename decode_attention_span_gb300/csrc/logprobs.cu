@@ -2,7 +2,7 @@
 // entropies and the likeliest alternatives, in one pass over the logits.
 //
 // Bound by memory: rows * vocab elements are read once (surprisal of 4096 rows of 128000
-// in bf16: 163 us, 95% of the copy rate; few rows: launch and joins, 6 us for one row of
+// in bf16: 163 us, 95% of the copy rate; few rows: launch and joins, 5.7 us for one row of
 // 32000 with five alternatives).  A row is cut into
 // 16-byte vectors; a cluster of 1 to 8 CTAs takes one row (as many as it takes
 // to fill the GPU when there are few rows), and each thread keeps a running
@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : 1) logprob_kernel(const Lp
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = cluster.num_blocks(), rank = cluster.block_rank();
   cluster.barrier_arrive();  // waited for before the first remote store: every CTA has started
+  follow_previous();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r = blockIdx.x / nc;
   const int64_t b = r / P.n_tokens, t = r - b * P.n_tokens;
@@ -535,13 +536,18 @@ sekv_status launch_logprobs(const LpParams& P, int64_t rows, int nc, cudaStream_
   lc.gridDim = dim3(unsigned(rows * nc));
   lc.blockDim = dim3(NT);
   lc.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = nc;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
-  lc.numAttrs = 1;
+  // Blocks on their way while the kernel before still runs: 5.6 us for 6.2 with one row of
+  // 32000.  Where there is more than one for each SM they would gather on the SMs that are
+  // free first (257 rows of 50021: 18.6 us for 16.1).
+  lc.numAttrs = rows * nc <= device_sm_count() ? 2 : 1;
   if (cudaLaunchKernelEx(&lc, logprob_kernel<T, FULL, NT>, P) != cudaSuccess) {
     cudaGetLastError();
     return SEKV_ERR_CUDA;

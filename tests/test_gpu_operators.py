@@ -708,6 +708,45 @@ def test_operators_on_a_side_stream_and_in_a_graph(sk, ws):
     assert wsk.status() == (0, 0) and wsg.status() == (0, 0) and ws.status() == (0, 0)
 
 
+def test_operators_follow_each_other_without_a_wait(sk, ws):
+    """Blocks of a call may be on their way while the call before it runs: each still sees all
+    that came before, and overwrites nothing that is still read."""
+    B, hq, hkv, T = 2, 8, 2, 5000
+    cfg = sk.Config(B, hq, hkv, 0, 0, 64)
+    kws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1)
+    mp = -(-T // 64)
+    x = torch.randn(B, T, hq + 2 * hkv, 128, generator=gen(1)).bfloat16().cuda()
+    logits = torch.randn(B, 4000, generator=gen(2)).cuda()
+    plan, zero = sk.RopePlan(128), torch.zeros(B, dtype=torch.int32, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+
+    def chain(wait):
+        cache = sk.Kv4Cache(cfg, torch.zeros(B * mp, hkv, 9216, dtype=torch.uint8, device="cuda"),
+                            torch.arange(B * mp, dtype=torch.int32, device="cuda").view(B, mp))
+        qkv, got = x.clone(), []
+        q, k, v = qkv[:, :, :hq], qkv[:, :, hq:hq + hkv], qkv[:, :, hq + hkv:]
+        calls = [lambda: sk.rope(plan, q, k, pos, q_out=q, k_out=k),
+                 lambda: sk.kv4_append(cfg, cache, k, v, zero, kws),
+                 lambda: got.extend(sk.kv4_attention(cfg, cache, q[:, -1:].contiguous(), zero + T, 0.0884, kws)),
+                 lambda: got.extend(sk.kv4_read(cfg, cache, zero, T, kws)),
+                 lambda: k.copy_(got[-2].transpose(1, 2)),
+                 lambda: sk.kv4_append(cfg, cache, v, k, zero, kws),
+                 lambda: got.extend(sk.kv4_attention(cfg, cache, q[:, -1:].contiguous(), zero + T, 0.0884, kws)),
+                 lambda: got.append(sk.token_logprobs(logits, zero.long(), ws, n_top=4).top_logprobs)]
+        for _ in range(3):
+            for f in calls:
+                f()
+                if wait:
+                    torch.cuda.synchronize()
+        return got
+
+    want = chain(True)
+    for _ in range(5):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
+    assert kws.status() == (0, 0) and ws.status() == (0, 0)
+
+
 def test_prefill_through_the_operators_into_the_span_cache(sk):
     """Logits to surprisal, projection to rotated keys, both into the 4-bit cache and
     the span build: the calls a program makes in order, each on the other's outputs."""

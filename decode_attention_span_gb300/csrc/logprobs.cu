@@ -323,6 +323,9 @@ __device__ __noinline__ void top_of_ties(LpShared<NT>& sh, const Row<T>& row, in
                                          float thread_max, int n_top) {
   constexpr int VE = Row<T>::VE;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // The caller's threads chose this path by n_cand: all have read it before it is set to 0, or
+  // one that comes late would choose another path and wait at another barrier.
+  __syncthreads();
   uint64_t key = 0;  // the first place of this thread's maximum
   if (thread_max > -INFINITY)
     for (int i = lo + tid; i < hi && key == 0; i += NT) {

@@ -8,7 +8,7 @@ import ctypes
 import torch
 
 from .sekv import (DTYPES, SEKV_CALL_KV4, Config, Workspace, _check, check_tensor, current_index, lib,
-                   raw_stream)
+                   made_on, raw_stream)
 
 PAGE_TOKENS = 64
 PAGE_BYTES = 9216
@@ -119,7 +119,8 @@ def kv4_read(cfg: Config, cache: Kv4Cache, first, n_tokens: int, ws: Workspace,
         if dtype not in DTYPES:
             raise TypeError(f"dtype: expected one of {list(DTYPES)}, got {dtype}")
         make = torch.empty if n is None else torch.zeros
-        k, v = make(shape, dtype=dtype, device=dev), make(shape, dtype=dtype, device=dev)
+        with made_on(stream, index):
+            k, v = make(shape, dtype=dtype, device=dev), make(shape, dtype=dtype, device=dev)
     else:
         k, v = out
         check_tensor(k, "out[0]", DTYPES, index)
@@ -148,13 +149,15 @@ def kv4_attention(cfg: Config, cache: Kv4Cache, q, seq_len, scale: float, ws: Wo
         raise ValueError(f"q: expected contiguous [{cfg.batch}][n_q][{cfg.n_q_heads}][128], got "
                          f"{tuple(shape)}")
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=cache.device)
+        with made_on(stream, index):
+            out = torch.empty(shape, dtype=torch.float32, device=cache.device)
     else:
         check_tensor(out, "out", _F32, index)
         if out.shape != shape or not out.is_contiguous():
             raise ValueError(f"out: expected contiguous {tuple(shape)}")
     if lse is None:
-        lse = torch.empty(shape[:3], dtype=torch.float32, device=cache.device)
+        with made_on(stream, index):
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=cache.device)
     else:
         check_tensor(lse, "lse", _F32, index)
         if lse.shape != shape[:3] or not lse.is_contiguous():

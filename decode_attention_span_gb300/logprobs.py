@@ -7,7 +7,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .sekv import DTYPES, Workspace, _check, check_tensor, current_index, lib, raw_stream
+from .sekv import DTYPES, Workspace, _check, check_tensor, current_index, lib, made_on, raw_stream
 
 
 class TokenLogprobs(NamedTuple):
@@ -54,16 +54,17 @@ def token_logprobs(logits, tokens, ws: Workspace, n_top: int = 0, scale: float =
     index, dtype, B, T, V, sb, st, tb = _rows(logits, tokens, ws)
     shape = tokens.shape
     empty, f32, dev = torch.empty, torch.float32, logits.device
-    lp = empty(shape, dtype=f32, device=dev)
     lse = ent = ids = tlp = None
     p_lse = p_ent = p_ids = p_tlp = None
-    if entropy:
-        lse, ent = empty(shape, dtype=f32, device=dev), empty(shape, dtype=f32, device=dev)
-        p_lse, p_ent = lse.data_ptr(), ent.data_ptr()
-    if n_top > 0:
-        ids = empty((*shape, n_top), dtype=torch.int32, device=dev)
-        tlp = empty((*shape, n_top), dtype=f32, device=dev)
-        p_ids, p_tlp = ids.data_ptr(), tlp.data_ptr()
+    with made_on(stream, index):
+        lp = empty(shape, dtype=f32, device=dev)
+        if entropy:
+            lse, ent = empty(shape, dtype=f32, device=dev), empty(shape, dtype=f32, device=dev)
+            p_lse, p_ent = lse.data_ptr(), ent.data_ptr()
+        if n_top > 0:
+            ids = empty((*shape, n_top), dtype=torch.int32, device=dev)
+            tlp = empty((*shape, n_top), dtype=f32, device=dev)
+            p_ids, p_tlp = ids.data_ptr(), tlp.data_ptr()
     if B * T > 0:
         err = lib().sekv_token_logprobs(logits.data_ptr(), dtype, B, T, V, sb, st,
                                         tokens.data_ptr(), tokens.dtype == torch.int64, tb, scale,
@@ -81,7 +82,8 @@ def surprisal(logits, tokens, ws: Workspace, out=None, stream=None):
         raise ValueError(f"logits: expected [B][T][V], got {tuple(logits.shape)}")
     index, dtype, B, T, V, sb, st, tb = _rows(logits, tokens, ws)
     if out is None:
-        out = torch.empty(B, T, dtype=torch.float32, device=logits.device)
+        with made_on(stream, index):
+            out = torch.empty(B, T, dtype=torch.float32, device=logits.device)
     else:
         check_tensor(out, "out", (torch.float32,), index)
         if out.shape != (B, T) or not out.is_contiguous():

@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from .sekv import DTYPES, _check, _ptr, check_tensor, current_index, lib, raw_stream
+from .sekv import DTYPES, _check, _ptr, check_tensor, current_index, lib, made_on, raw_stream
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "banded": 4}
 
@@ -72,7 +72,7 @@ class RopePlan:
 _POSITIONS = (torch.int32, torch.int64)
 
 
-def _heads(name, x, y, B, T, D, dtype, index):
+def _heads(name, x, y, B, T, D, dtype, index, stream):
     """(sekv_heads, output) of one tensor; an output made here is zero at padding."""
     if x.dtype != dtype or x.get_device() != index:
         check_tensor(x, name, (dtype,), index)
@@ -82,7 +82,8 @@ def _heads(name, x, y, B, T, D, dtype, index):
                          f"head, got {tuple(s)}")
     n = s[2]
     if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        with made_on(stream, index):
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
         return SekvHeads(x.data_ptr(), y.data_ptr(), n + (1 << 32), xs[0], xs[1], xs[2],
                          T * n * D, n * D, D), y
     if y.dtype != dtype or y.get_device() != index:
@@ -129,9 +130,9 @@ def rope(plan: RopePlan, q, k, positions, q_out=None, k_out=None, backward: bool
         raise ValueError("positions: must be consecutive along a sequence")
     qh = kh = None
     if q is not None:
-        qh, q_out = _heads("q", q, q_out, B, T, D, dtype, index)
+        qh, q_out = _heads("q", q, q_out, B, T, D, dtype, index, stream)
     if k is not None:
-        kh, k_out = _heads("k", k, k_out, B, T, D, dtype, index)
+        kh, k_out = _heads("k", k, k_out, B, T, D, dtype, index, stream)
     st = lib().sekv_rope(plan._c, plan.freqs_ptr, plan.mscale, code, D, B, T,
                          positions.data_ptr(), positions.dtype == torch.int64, pos_stride, qh, kh,
                          1 if backward else 0, raw_stream(stream, index))

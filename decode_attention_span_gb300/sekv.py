@@ -8,6 +8,7 @@ no CPU fallback: if the library is missing, every call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import math
@@ -232,6 +233,17 @@ def raw_stream(stream, index: int) -> int:
     """Handle of `stream`, or of the current stream of CUDA device `index`."""
     # torch.cuda.current_stream() builds a Stream object (3 us, a third of a small call)
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+_NULL = contextlib.nullcontext()
+
+
+def made_on(stream, index: int):
+    """Context in which a call on `stream` makes its outputs: a tensor filled, or taken from
+    another stream's freed memory, on any but the stream that writes it would race with it."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(index):
+        return _NULL
+    return torch.cuda.stream(stream)
 
 
 # ----------------------------------------------------------------------------

@@ -52,3 +52,48 @@ def test_alternatives_of_short_rows_with_masked_first_ids(sk, ws, dtype, vocab, 
         err = np.abs(r.logprob.double().cpu().numpy() - want["logprob"])
         assert (err <= 3 * (120 * 2.0 ** -24 + 2.0 ** -22 + 56 * 2.0 ** -24) + 2.0 ** -22 * 60).all()
     assert ws.status() == (0, 0)
+
+
+# ------------------------------------------------------------------ outputs and streams
+def small_cache(sk, B, Hkv, hq, T, seed=0, n_q=1):
+    """A 4-bit cache that holds T random tokens of each sequence."""
+    cfg = sk.Config(B, hq, Hkv, 0, 0, 64)
+    mp = -(-T // 64)
+    cache = sk.Kv4Cache(cfg, sk.alloc_kv4_pages(cfg, B * mp),
+                        torch.arange(B * mp, dtype=torch.int32, device="cuda").view(B, mp))
+    kws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=n_q)
+    k, v = (torch.randn(B, T, Hkv, 128, generator=gen(seed + i)).bfloat16().cuda() for i in range(2))
+    sk.kv4_append(cfg, cache, k, v, torch.zeros(B, dtype=torch.int32, device="cuda"), kws)
+    return cfg, cache, kws
+
+
+def test_outputs_made_for_another_stream(sk, ws):
+    """Outputs of a call with stream= are neither filled on the current stream nor taken from its
+    freed memory: here the current stream is busy, and has writes to such memory ahead of it."""
+    B, T = 2, 40
+    cfg, cache, kws = small_cache(sk, B, 2, 4, T)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    zero, n = torch.zeros(B, **i32), torch.full((B,), 30, **i32)
+    q = torch.randn(B, 1, 4, 128, generator=gen(3)).bfloat16().cuda()
+    logits, tok = torch.randn(B, T, 300, generator=gen(4)).cuda(), torch.zeros(B, T, dtype=torch.int64, device="cuda")
+    plan, pos = sk.RopePlan(128), torch.arange(T, **i32)
+    x = torch.randn(B, T, 3, 128, generator=gen(5)).cuda()
+    side = torch.cuda.Stream()
+    calls = [lambda s: sk.kv4_read(cfg, cache, zero, T, kws, n_valid=n, stream=s),
+             lambda s: sk.kv4_read(cfg, cache, zero, T, kws, stream=s),
+             lambda s: sk.kv4_attention(cfg, cache, q, n, 0.1, kws, stream=s),
+             lambda s: sk.token_logprobs(logits, tok, ws, n_top=3, stream=s),
+             lambda s: [sk.surprisal(logits, tok, ws, stream=s)],
+             lambda s: sk.rope(plan, x, x[:, :, :1], pos, stream=s)]
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        old = [torch.empty_like(t) for t in want for _ in range(2)]
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+        for t in old:
+            t.fill_(7)
+        del old, t
+        got = call(side)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

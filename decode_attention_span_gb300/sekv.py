@@ -350,12 +350,15 @@ def route(cfg: Config, cache: LayerCache, q, W_r, theta, ws: Workspace, want_z: 
     _need(theta, "theta", torch.float32)
     dev = q.device
     NG = cfg.batch * cfg.n_kv_heads
-    if expanded is None:
-        expanded = torch.empty(NG * cfg.max_spans, dtype=torch.int32, device=dev)
-    if n_expanded is None:
-        n_expanded = torch.empty(NG, dtype=torch.int32, device=dev)
-    z = (torch.zeros(cfg.batch * cfg.n_q_heads * cfg.max_spans, dtype=torch.float32, device=dev)
-         if want_z else None)
+    z = None
+    with made_on(stream, dev.index):
+        if expanded is None:
+            expanded = torch.empty(NG * cfg.max_spans, dtype=torch.int32, device=dev)
+        if n_expanded is None:
+            n_expanded = torch.empty(NG, dtype=torch.int32, device=dev)
+        if want_z:
+            z = torch.zeros(cfg.batch * cfg.n_q_heads * cfg.max_spans, dtype=torch.float32,
+                            device=dev)
     c = cfg.c()
     _check("sekv_route", lib().sekv_route(ctypes.byref(c), ctypes.byref(cache.c), _ptr(q),
                                           _ptr(W_r), _ptr(theta), _ptr(expanded),
@@ -370,10 +373,11 @@ def decode_attention(cfg: Config, cache: LayerCache, q, expanded, n_expanded, sc
     _need(q, "q", torch.bfloat16); _need(expanded, "expanded", torch.int32)
     _need(n_expanded, "n_expanded", torch.int32)
     dev = q.device
-    if out is None:
-        out = torch.empty(cfg.batch, cfg.n_q_heads, 128, dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty(cfg.batch, cfg.n_q_heads, dtype=torch.float32, device=dev)
+    with made_on(stream, dev.index):
+        if out is None:
+            out = torch.empty(cfg.batch, cfg.n_q_heads, 128, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(cfg.batch, cfg.n_q_heads, dtype=torch.float32, device=dev)
     c = cfg.c()
     _check("sekv_decode_attention",
            lib().sekv_decode_attention(ctypes.byref(c), ctypes.byref(cache.c), _ptr(q),
@@ -388,15 +392,16 @@ def decode_step(cfg: Config, cache: LayerCache, q, W_r, theta, scale: float, ws:
     _need(q, "q", torch.bfloat16); _need(W_r, "W_r", torch.float32)
     _need(theta, "theta", torch.float32)
     dev = q.device
-    if out is None:
-        out = torch.empty(cfg.batch, cfg.n_q_heads, 128, dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty(cfg.batch, cfg.n_q_heads, dtype=torch.float32, device=dev)
     NG = cfg.batch * cfg.n_kv_heads
     expanded = n_expanded = None
-    if want_list:
-        expanded = torch.zeros(NG * cfg.max_spans, dtype=torch.int32, device=dev)
-        n_expanded = torch.zeros(NG, dtype=torch.int32, device=dev)
+    with made_on(stream, dev.index):
+        if out is None:
+            out = torch.empty(cfg.batch, cfg.n_q_heads, 128, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(cfg.batch, cfg.n_q_heads, dtype=torch.float32, device=dev)
+        if want_list:
+            expanded = torch.zeros(NG * cfg.max_spans, dtype=torch.int32, device=dev)
+            n_expanded = torch.zeros(NG, dtype=torch.int32, device=dev)
     c = cfg.c()
     _check("sekv_decode_step",
            lib().sekv_decode_step(ctypes.byref(c), ctypes.byref(cache.c), _ptr(q), _ptr(W_r),
@@ -422,16 +427,17 @@ def decode_step_multi(cfg: Config, cache: LayerCache, q, W_r, theta, scale: floa
     _need(theta, "theta", torch.float32)
     B, n_q = q.shape[0], q.shape[1]
     dev = q.device
-    if out is None:
-        out = torch.empty(B, n_q, cfg.n_q_heads, 128, dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty(B, n_q, cfg.n_q_heads, dtype=torch.float32, device=dev)
     NG = cfg.batch * cfg.n_kv_heads
     expanded = n_expanded = None
-    if want_list:
-        nb = max(query_blocks(cfg, n_q), 1)
-        expanded = torch.zeros(nb * NG * cfg.max_spans, dtype=torch.int32, device=dev)
-        n_expanded = torch.zeros(nb * NG, dtype=torch.int32, device=dev)
+    with made_on(stream, dev.index):
+        if out is None:
+            out = torch.empty(B, n_q, cfg.n_q_heads, 128, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(B, n_q, cfg.n_q_heads, dtype=torch.float32, device=dev)
+        if want_list:
+            nb = max(query_blocks(cfg, n_q), 1)
+            expanded = torch.zeros(nb * NG * cfg.max_spans, dtype=torch.int32, device=dev)
+            n_expanded = torch.zeros(nb * NG, dtype=torch.int32, device=dev)
     c = cfg.c()
     _check("sekv_decode_step_multi",
            lib().sekv_decode_step_multi(ctypes.byref(c), ctypes.byref(cache.c), _ptr(q), n_q,
@@ -454,15 +460,16 @@ def decode_step_noalloc(cfg: Config, cache: LayerCache, q, W_r, theta, scale: fl
     _need(q, "q", torch.bfloat16); _need(W_r, "W_r", torch.float32)
     _need(theta, "theta", torch.float32)
     dev = q.device
-    if out is None:
-        out = torch.empty(cfg.batch, cfg.n_q_heads, 128, dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty(cfg.batch, cfg.n_q_heads, dtype=torch.float32, device=dev)
     NG = cfg.batch * cfg.n_kv_heads
     expanded = n_expanded = None
-    if want_list:
-        expanded = torch.zeros(NG * cfg.max_spans, dtype=torch.int32, device=dev)
-        n_expanded = torch.zeros(NG, dtype=torch.int32, device=dev)
+    with made_on(stream, dev.index):
+        if out is None:
+            out = torch.empty(cfg.batch, cfg.n_q_heads, 128, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(cfg.batch, cfg.n_q_heads, dtype=torch.float32, device=dev)
+        if want_list:
+            expanded = torch.zeros(NG * cfg.max_spans, dtype=torch.int32, device=dev)
+            n_expanded = torch.zeros(NG, dtype=torch.int32, device=dev)
     c = cfg.c()
     _check("sekv_decode_step_noalloc",
            lib().sekv_decode_step_noalloc(ctypes.byref(c), ctypes.byref(cache.c), _ptr(q),
@@ -604,8 +611,9 @@ class Maintainer:
         dev = out["k_full"].device
         c = cfg.c()
         n = int(lib().sekv_maint_state_size(ctypes.byref(c)))
-        self.state = torch.zeros(n, dtype=torch.uint8, device=dev)
-        self.n_tail = torch.zeros(cfg.batch, dtype=torch.int32, device=dev)
+        with made_on(stream, dev.index):
+            self.state = torch.zeros(n, dtype=torch.uint8, device=dev)
+            self.n_tail = torch.zeros(cfg.batch, dtype=torch.int32, device=dev)
         self._o = SekvCacheOut(*[_ptr(out[k]) for k in CACHE_FIELDS], out["store"].numel())
         _need(K, "K", torch.bfloat16); _need(V, "V", torch.bfloat16); _need(H, "H", torch.float32)
         _check("sekv_maint_init",

@@ -8,6 +8,8 @@ import torch
 
 from oracle import tokens
 
+from cases import SCALE, TOL_ABS, decode_case
+
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "f32": torch.float32}
@@ -97,3 +99,37 @@ def test_outputs_made_for_another_stream(sk, ws):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_outputs_of_the_span_cache_calls_made_for_another_stream(sk):
+    """The same of the calls over the span cache, whose lists and logits start at zero."""
+    case = decode_case("llama3_8b_32k", ctx=4096, run_oracle=False)
+    w = case.wcfg
+    cfg = sk.Config(w.batch, w.n_q_heads, w.n_kv_heads, w.n_sink, w.n_recent, case.tensors["max_spans"],
+                    w.rank_cap, w.len_min, w.len_max, w.tau)
+    cache = sk.LayerCache({k: v.cuda() for k, v in case.tensors.items() if isinstance(v, torch.Tensor)})
+    wsd, side = sk.Workspace(cfg), torch.cuda.Stream()
+    q, W, theta = case.q.cuda(), case.W.cuda(), torch.from_numpy(case.theta).cuda()
+    q2 = q[:, None].repeat(1, 2, 1, 1)
+    lst, cnt, _ = sk.route(cfg, cache, q, W, theta, wsd)
+    # no outputs that the kernels leave unwritten: `expanded` of route holds counts entries only
+    calls = [lambda s: sk.route(cfg, cache, q, W, theta, wsd, want_z=True, stream=s)[1:],
+             lambda s: sk.decode_attention(cfg, cache, q, lst, cnt, SCALE, wsd, stream=s),
+             lambda s: sk.decode_step(cfg, cache, q, W, theta, SCALE, wsd, want_list=True, stream=s),
+             lambda s: sk.decode_step_noalloc(cfg, cache, q, W, theta, SCALE, want_list=True, stream=s),
+             lambda s: sk.decode_step_multi(cfg, cache, q2, W, theta, SCALE, wsd, want_list=True, stream=s)]
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        old = [torch.empty_like(t) for t in want for _ in range(2)]
+        torch.cuda._sleep(50_000_000)
+        for t in old:
+            t.fill_(7)
+        del old, t
+        got = call(side)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            # the decode kernel's CTAs share the work in the order they come: each result is within
+            # TOL_ABS of the exact one, so two are within twice that (a lost one is off by far more)
+            assert torch.equal(a, b) if a.dtype == torch.int32 else (a - b).abs().max().item() <= 2 * TOL_ABS
+    assert wsd.status() == (0, 0)

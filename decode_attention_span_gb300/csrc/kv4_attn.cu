@@ -543,8 +543,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       const T* q = static_cast<const T*>(P.q) +
                    ((int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + qcol % P.hpg) *
                        kHeadDim;
-      // volatile: the compiler would move a plain load down to its use, behind the copies
-      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(qv.w.x), "=r"(qv.w.y) : "l"(q + 4 * lane));
+      // volatile: the compiler would move a plain load down to its use, behind the copies; not
+      // .nc: this grid may be resident while the kernel before it still writes the queries
+      asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(qv.w.x), "=r"(qv.w.y) : "l"(q + 4 * lane));
     }
 
     // This warp's k-th chunk of the segment is c0 + warp + kAttnWarps k.  Lane i

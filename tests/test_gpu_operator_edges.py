@@ -133,3 +133,31 @@ def test_outputs_of_the_span_cache_calls_made_for_another_stream(sk):
             # TOL_ABS of the exact one, so two are within twice that (a lost one is off by far more)
             assert torch.equal(a, b) if a.dtype == torch.int32 else (a - b).abs().max().item() <= 2 * TOL_ABS
     assert wsd.status() == (0, 0)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rotation_directly_before_the_attention(sk, in_place):
+    """The attention's blocks may be resident while the rotation still writes their queries; step
+    after step the same buffers hold other queries, with nothing launched in between."""
+    B, T, hq, n_q = 3, 300, 8, 4
+    cfg, cache, kws = small_cache(sk, B, 2, hq, T, n_q=n_q)
+    plan = sk.RopePlan(128)
+    lens = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    x = [torch.randn(B, n_q, hq, 128, generator=gen(i)).bfloat16().cuda() for i in range(30)]
+    pos = [torch.full((n_q,), 10 * i, dtype=torch.int32, device="cuda") for i in range(30)]
+    want = []
+    for q, p in zip(x, pos):
+        q = sk.rope(plan, q, None, p)[0]
+        torch.cuda.synchronize()
+        want.append(sk.kv4_attention(cfg, cache, q, lens, 0.1, kws))
+        torch.cuda.synchronize()
+    buf = torch.empty_like(x[0])
+    src = [q.clone() for q in x]
+    got = [(torch.empty_like(o), torch.empty_like(l)) for o, l in want]
+    for q, p, (o, l) in zip(src, pos, got):
+        r = q if in_place else buf
+        sk.rope(plan, q, None, p, q_out=r)
+        sk.kv4_attention(cfg, cache, r, lens, 0.1, kws, out=o, lse=l)
+    for (o, l), (ow, lw) in zip(got, want):
+        assert torch.equal(o, ow) and torch.equal(l, lw)
+    assert kws.status() == (0, 0)

@@ -16,7 +16,9 @@
 // the mask's instruction inverts the odd tokens' codes too, and the sum of many tokens stays
 // as small as it would with codes around zero.  The weight p_j s_j enters as the sum of two f16
 // numbers (22 significant bits: one alone would cost the fp32 result 13 of its bits), scaled by
-// a power of two that follows the largest s seen, so that scales of any size fit f16.
+// a power of two, the unit of a column and a group of dimensions.  It follows the largest weight
+// p_j s_j of that column and group, not the largest s: a token of large scale and no weight, or with
+// weight in another column, takes no bits from the others.
 //
 // The matrix instructions take a number below the normal ones as if it were as large as those
 // when they line their addends up, and cut off 25 bits under the largest.  So the place of
@@ -66,6 +68,11 @@ constexpr int kGroupCost = 40;
 constexpr float kNone = -3e38f;
 constexpr float kGrowth = 8.f;                   // log2 by which a weight may outgrow the reference
 constexpr float kMaxScale = 128.f;               // of V with the unit: 2^8 times it fits f16
+// A unit brings V's largest scale to 2^5 .. 2^6 unless the column's largest weight is then below
+// kLeast, of which f16 takes 2^-25; it brings that weight to 2^5 .. 2^6 then.
+constexpr float kLeast = 1.f, kMost = 4096.f;
+constexpr int kUnitTop = 5;
+constexpr uint32_t kUnitMax = 127 + 118;         // exponent: a weight of 2^8 fits fp32 with it
 constexpr int kFlush = 16;                       // chunks between two flushes: 1% of the time
 constexpr int kCodeBits = 20;                    // K's sums of q n are in units of 2^-20
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -76,6 +83,8 @@ struct AttnShared {
   float4 par[kAttnWarps][2][kChunkTokens];  // a chunk's scales and zeros, K's and V's, as floats
   float m[kAttnWarps][kCols];
   float l[kAttnWarps][kCols];
+  float4 units[kAttnWarps][32];    // powers of two on the weights: group 0 of a lane's columns, group 1
+  float4 weights[kAttnWarps][32];  // the columns' largest weights, once they have units of their own
   float mx[kCols], sum[kCols];
   // the segment's queries: B operand, two 16-dimension steps a vector; per group of dimensions
   // the sums of q; from a column's units to log2 of its weights
@@ -197,8 +206,15 @@ struct WarpState {
   float o[8][4];   // [4 dims apiece: word m, i][rows g, g + 8 x columns], in units of 1 / unit
   float m[2], l[2];  // the weights' reference, log2: within 2^8 of the largest; kNone: no token yet
   float c[2][2];   // sum of p z': [column][group of dimensions]
-  float unit;      // power of two on the weights of o
+  float most;      // the largest unit of any column and group of dimensions
+  float least;     // what every column's largest weight with its unit is at least
+  bool split;      // the columns and groups have units of their own
 };
+
+// The power of two that brings the number with these exponent bits to 2^kUnitTop .. twice that
+__device__ __forceinline__ float unit_of(uint32_t exponent) {
+  return __uint_as_float(uint32_t(min(max(2 * 127 + kUnitTop - int(exponent), 1), int(kUnitMax))) << 23);
+}
 
 // B operand, sums and scale of column `col` into shared memory, by one warp: q is this
 // lane's four dimensions, 4 lane .. 4 lane + 3.
@@ -259,13 +275,55 @@ __device__ __forceinline__ void flush(WarpState& S, float4* kept, int lane, bool
     S.o[j][0] = S.o[j][1] = S.o[j][2] = S.o[j][3] = 0.f;
   }
 }
-// f0 and f1: on the values of the lane's columns
-__device__ __noinline__ void rescale_kept(float4* kept, int lane, float f0, float f1) {
+// k: on the values, of group 0 of the lane's columns, then of group 1
+__device__ __noinline__ void rescale_kept(float4* kept, int lane, float4 k) {
   for (int j = 0; j < 8; ++j) {
+    if (j == 4) k.x = k.z, k.y = k.w;
     float4 v = kept[j * 32 + lane];
-    v.x *= f0; v.y *= f1; v.z *= f0; v.w *= f1;
+    v.x *= k.x; v.y *= k.y; v.z *= k.x; v.w *= k.y;
     kept[j * 32 + lane] = v;
   }
+}
+
+// Units of their own for the columns and groups of dimensions, where scales lie far apart: by the
+// chunk's largest scale as long as the column's largest weight is kLeast or more with that, and
+// by that weight otherwise.  f: on the sums, as the reference moves; k: on the values.
+__device__ __forceinline__ void split_units(WarpState& S, const Query& Q, const float (&x)[2][2][2],
+                                            const float4* par, float by_scale,
+                                            const float (&f)[2], float (&k)[2][2], float4& units,
+                                            float4& weights, int g) {
+  float* un = reinterpret_cast<float*>(&units);
+  float* largest = reinterpret_cast<float*>(&weights);
+  float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, most = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = par[i * 8 + g];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float p = ex2(fmaf(x[i >> 1][i & 1][c], Q.scale_log2[c], -S.m[c]));
+      w[0][c] = fmaxf(w[0][c], p * fabsf(v.x));  // NaN does not count
+      w[1][c] = fmaxf(w[1][c], p * fabsf(v.z));
+    }
+  }
+#pragma unroll
+  for (int gr = 0; gr < 2; ++gr) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float old = un[2 * gr + c];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) w[gr][c] = fmaxf(w[gr][c], __shfl_xor_sync(~0u, w[gr][c], o));
+      const float all = fmaxf(w[gr][c], f[c] * (S.split ? largest[2 * gr + c] : kLeast / old));
+      float unit = fminf(old, by_scale);
+      if (!(all * unit >= kLeast && all * unit < kMost)) unit = unit_of(__float_as_uint(all) >> 23);
+      un[2 * gr + c] = unit;
+      largest[2 * gr + c] = all;
+      k[gr][c] = unit >= 1.f ? f[c] * unit / old : f[c] * (unit / old);  // in range in between, too
+      most = fmaxf(most, unit);
+    }
+  }
+  most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+  S.most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+  S.split = true;
 }
 
 // EDGE: some token of the chunk is not seen by some column (seen: per column of the
@@ -275,8 +333,8 @@ __device__ __noinline__ void rescale_kept(float4* kept, int lane, float f0, floa
 template <bool EDGE, bool PACK>
 __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const uint8_t* chunk,
                                            float4 (&par)[2][kChunkTokens], float4* kept,
-                                           bool any_kept, int lane, int held,
-                                           const int (&seen)[2]) {
+                                           float4* units, float4* weights, bool any_kept, int lane,
+                                           int held, const int (&seen)[2]) {
   const int g = lane >> 2;
   // a lane turns one token's scales and zeros into floats for all
   const uint8_t* sz = chunk + (lane >> 4) * kKv4TileBytes + kv4_param(lane & 15, 0, false);
@@ -284,6 +342,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
   uint2 vp = *reinterpret_cast<const uint2*>(sz + 128);
   if (EDGE && lane >= held) vp = make_uint2(0u, 0u);  // behind the end: may hold anything
   par[0][lane] = make_float4(lo16(kp.x), hi16(kp.x), lo16(kp.y), hi16(kp.y));
+  const float s0 = lo16(vp.x), s1 = lo16(vp.y);
   __syncwarp();
   float x[2][2][2];  // tile, row half, column
 #pragma unroll
@@ -334,21 +393,20 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
     }
   }
 
-  // A new reference, or a new unit for V's scales, only where the old one no longer does.
-  const float s0 = lo16(vp.x), s1 = lo16(vp.y);
+  {  // s, signed, and z'
+    const float odd = lane & 1 ? 15.f : 0.f, sign = lane & 1 ? -1.f : 1.f;
+    par[1][lane] = make_float4(s0 * sign, fmaf(odd, s0, hi16(vp.x)), s1 * sign, fmaf(odd, s1, hi16(vp.y)));
+  }
+  __syncwarp();
+  // A new reference, or new units, only where the old ones may no longer do.
   float mx[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
     mx[c] = Q.scale_log2[c] * fmaxf(fmaxf(x[0][0][c], x[0][1][c]), fmaxf(x[1][0][c], x[1][1][c]));
   const bool over = mx[0] > S.m[0] + kGrowth || mx[1] > S.m[1] + kGrowth ||
-                    fmaxf(s0, s1) * S.unit >= kMaxScale;
+                    fmaxf(s0, s1) * S.most >= kMaxScale;
   if (__any_sync(~0u, over)) {
-    // the largest finite scale, as bf16 bits (never negative), and the unit that brings it
-    // to 64 .. 128
-    const uint32_t t0 = vp.x & 0xffffu, t1 = vp.y & 0xffffu;
-    const uint32_t top = __reduce_max_sync(~0u, max(t0 < 0x7f80u ? t0 : 0u, t1 < 0x7f80u ? t1 : 0u));
-    const float unit = fminf(S.unit, __uint_as_float(min(254u, 260u - max(6u, top >> 7)) << 23));
-    float f[2];
+    float f[2], k[2][2];  // k: on the values, [group][column]
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -359,20 +417,30 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
       S.l[c] *= f[c];
       S.c[c][0] *= f[c];
       S.c[c][1] *= f[c];
-      f[c] *= unit / S.unit;
     }
-    S.unit = unit;
+    // One unit for all while that serves them: where a column's reference moves, a token of this
+    // chunk has weight 1 in it, and so at least the chunk's smallest scale.
+    const uint32_t t0 = vp.x & 0x7fffu, t1 = vp.y & 0x7fffu;
+    const uint32_t top = __reduce_max_sync(~0u, max(t0 < 0x7f80u ? t0 : 0u, t1 < 0x7f80u ? t1 : 0u));
+    const uint32_t low = __reduce_min_sync(~0u, EDGE && lane >= held ? 0x7f80u : min(t0, t1));
+    const float by_scale = unit_of(top >> 7), unit = fminf(S.most, by_scale), ratio = unit / S.most;
+    S.least = fminf(S.least * ratio, __uint_as_float(low << 16) * unit);
+    if (!S.split && S.least >= kLeast) {
+      S.most = unit;
+      *units = make_float4(unit, unit, unit, unit);
+      k[0][0] = k[1][0] = f[0] * ratio;
+      k[0][1] = k[1][1] = f[1] * ratio;
+    } else {
+      split_units(S, Q, x, par[1], by_scale, f, k, *units, *weights, g);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S.o[j][i] *= f[i & 1];
-    if (any_kept) rescale_kept(kept, lane, f[0], f[1]);
+      for (int i = 0; i < 4; ++i) S.o[j][i] *= k[j >> 2][i & 1];
+    if (any_kept) rescale_kept(kept, lane, make_float4(k[0][0], k[0][1], k[1][0], k[1][1]));
   }
-  // s in units, signed, and z'
-  const float odd = lane & 1 ? 15.f : 0.f, su = lane & 1 ? -S.unit : S.unit;
-  par[1][lane] = make_float4(s0 * su, fmaf(odd, s0, hi16(vp.x)), s1 * su, fmaf(odd, s1, hi16(vp.y)));
-  __syncwarp();
 
+  const float4 un = *units;
 #pragma unroll
   for (int ti = 0; ti < 2; ++ti) {
     const uint8_t* tile = chunk + ti * kKv4TileBytes;
@@ -381,7 +449,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float4 v = par[1][ti * 16 + e * 8 + g];  // of both groups
-      float p[2], w[2][2];
+      float p[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         p[c] = ex2(fmaf(x[ti][e][c], Q.scale_log2[c], -S.m[c]));
@@ -389,21 +457,25 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
       }
 #pragma unroll
       for (int gr = 0; gr < 2; ++gr) {
-        const float su = gr ? v.z : v.x, z = gr ? v.w : v.y;
+        const float sv = gr ? v.z : v.x, z = gr ? v.w : v.y;
+        float w[2];
+        // in this order: a large s with the unit of a column without weight on it may overflow
+        const Pair u(gr ? un.z : un.x, gr ? un.w : un.y);
+        mul2(mul2(Pair(p[0], p[1]), u), Pair(sv, sv)).get(w[0], w[1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           // a token that the column does not see has p 0, but may hold NaN
           const bool ok = !EDGE || ti * 16 + e * 8 + g < seen[c];
-          w[gr][c] = ok ? p[c] * su : 0.f;
+          if (!ok) w[c] = 0.f;
           S.c[c][gr] = ok ? fmaf(p[c], z, S.c[c][gr]) : S.c[c][gr];
         }
-        const __half2 h = __floats2half2_rn(w[gr][0], w[gr][1]);
+        const __half2 h = __floats2half2_rn(w[0], w[1]);
         if (PACK) {
           const float2 hf = __half22float2(h);
-          const __half2 part = __floats2half2_rn(fmaf(low, hf.x, w[gr][0]), fmaf(low, hf.y, w[gr][1]));
+          const __half2 part = __floats2half2_rn(fmaf(low, hf.x, w[0]), fmaf(low, hf.y, w[1]));
           bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&part));
         } else {
-          const __half2 l = rest(h, w[gr][0], w[gr][1]);
+          const __half2 l = rest(h, w[0], w[1]);
           bh[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
           bl[gr][e] = transpose8(*reinterpret_cast<const uint32_t*>(&l));
         }
@@ -616,7 +688,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       S.m[c] = kNone;
       S.l[c] = S.c[c][0] = S.c[c][1] = 0.f;
     }
-    S.unit = __uint_as_float(254u << 23);
+    S.most = __uint_as_float(kUnitMax << 23);
+    S.least = INFINITY;
+    S.split = false;
+    sh.units[warp][lane] = make_float4(S.most, S.most, S.most, S.most);
 
     float4* kept = reinterpret_cast<float4*>(&sh.o[warp][0][0]);
     for (int k = 0; k < mine; ++k) {
@@ -626,10 +701,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
           const int pos = (c0 + warp + k * kAttnWarps) * kChunkTokens;
           const int held = len - pos;
           const int seen[2] = {see[0] - pos, see[1] - pos};
+          float4 *un = &sh.units[warp][lane], *wt = &sh.weights[warp][lane];
           if (pos + kChunkTokens <= open)
-            chunk_step<false, PACK>(S, Q, sh.ring[warp][st], sh.par[warp], kept, k >= kFlush, lane, held, seen);
+            chunk_step<false, PACK>(S, Q, sh.ring[warp][st], sh.par[warp], kept, un, wt, k >= kFlush, lane, held, seen);
           else
-            chunk_step<true, PACK>(S, Q, sh.ring[warp][st], sh.par[warp], kept, k >= kFlush, lane, held, seen);
+            chunk_step<true, PACK>(S, Q, sh.ring[warp][st], sh.par[warp], kept, un, wt, k >= kFlush, lane, held, seen);
         } else {
           // a copy did not land: nothing more is copied or waited for by this warp, and
           // what is still in flight gets its time to land before the CTA may end
@@ -654,7 +730,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     }
 
     // the warps' states into shared memory (PACK: the lower parts' sums as columns 4-7)
-    const float inv_unit = 1.f / S.unit, low = float(1 << 22), high = float(1 << 18);
+    const float* un = reinterpret_cast<const float*>(&sh.units[warp][lane]);
+    const float low = float(1 << 22), high = float(1 << 18);
 #pragma unroll 1
     for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
@@ -671,7 +748,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float add = PACK && t >= 2 ? 0.f : S.c[c][m >> 1];
+        const float add = PACK && t >= 2 ? 0.f : S.c[c][m >> 1], inv_unit = 1.f / un[(m >> 1) * 2 + c];
         *reinterpret_cast<float4*>(&sh.o[warp][2 * t + c][(m >> 1) * 64 + g * 8 + (m & 1) * 4]) =
             make_float4(fmaf(S.o[2 * m][c] * low, inv_unit, add), fmaf(S.o[2 * m + 1][c] * high, inv_unit, add),
                         fmaf(S.o[2 * m][2 + c] * low, inv_unit, add),

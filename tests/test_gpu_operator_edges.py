@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import tokens
+from oracle import kv4, tokens
 
 from cases import SCALE, TOL_ABS, decode_case
 
@@ -161,3 +161,194 @@ def test_rotation_directly_before_the_attention(sk, in_place):
     for (o, l), (ow, lw) in zip(got, want):
         assert torch.equal(o, ow) and torch.equal(l, lw)
     assert kws.status() == (0, 0)
+
+
+# ------------------------------------------------------------------ the 4-bit attention's precision
+# What a call may be off by, of the softmax-weighted mean of |z| + 15 |s| (per group of dimensions;
+# `bound` of the oracle):
+#   2^-22   a weight p s as two f16 numbers, each rounded by half a step, 2^-11 of 2^-11 of it, and
+#           2^-25 of the largest weight with it where that is more (n tokens of it add like n^0.5)
+#   2^-22   the exponential, twice: above and below the fraction line
+#   cuts    the matrix instructions cut less than a step, 2^-23, off their running sum; two for each
+#           tile of 16 tokens, and the sum grows evenly over the 64 of 16 chunks, after which it is
+#           put by: 64 / 2 steps at most
+#   2^-24   each of the fp32 additions in a row: four a chunk and lane, the joins of lanes, warps, CTAs
+# and by the logits' error in log2 units `arg` (of p, above and below).
+def step_bound(T, arg=0.0, ctas=152):
+    chunks = -(-T // 32 // 12) + 1               # of a warp, if one CTA has them all
+    cuts = min(4 * chunks, 64) / 2 + 2
+    adds = 4 * chunks + 3 + 12 + min(ctas, chunks)
+    return 4 * 2.0 ** -22 + cuts * 2.0 ** -23 + adds * 2.0 ** -24 + 2 * arg
+
+
+def put_all(pages, table, b, c, codes, s, z, is_v):
+    """Codes [T][128], scales and zero points [T][2] of a sequence's KV head into pages."""
+    sb, zb = kv4.bf16_bits(s), kv4.bf16_bits(z)
+    for t in range(codes.shape[0]):
+        kv4.put(pages, table, b, c, t, codes[t], sb[t], zb[t], is_v)
+
+
+def cache_of(sk, K, V, hq, n_q=1):
+    """A cache of one sequence and KV head holding K = (codes, s, z) and V likewise."""
+    T = K[0].shape[0]
+    mp = -(-T // 64)
+    pages = np.zeros((mp, 1, kv4.PAGE_BYTES), np.uint8)
+    table = np.arange(mp, dtype=np.int32)[None]
+    put_all(pages, table, 0, 0, *K, False)
+    put_all(pages, table, 0, 0, *V, True)
+    cfg = sk.Config(1, hq, 1, 0, 0, 64)
+    cache = sk.Kv4Cache(cfg, torch.from_numpy(pages).cuda(), torch.from_numpy(table).cuda())
+    return cfg, cache, sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=n_q), pages, table
+
+
+def check_bound(out, lse, ref, tol, lse_tol):
+    o, l, bound, _ = ref
+    err = np.abs(out.double().cpu().numpy() - o)
+    assert np.isfinite(err).all()
+    worst = (err / np.maximum(bound, 1e-300)).max()
+    assert worst <= tol, f"out: {worst:.3g} of the bound, allowed {tol:.3g}"
+    e = np.abs(lse.double().cpu().numpy() - l).max()
+    assert e <= lse_tol, f"lse: {e:.3g}, allowed {lse_tol:.3g}"
+
+
+@pytest.mark.parametrize("hq", [1, 4, 8])
+@pytest.mark.parametrize("T", [1, 2, 5, 33, 700, 6000])
+def test_attention_of_equal_weights(sk, hq, T):
+    """A query of zeros: every weight is the same, exactly, and what is left is the products' error."""
+    r = np.random.default_rng(T)
+    kv = [(r.integers(0, 16, (T, 128)).astype(np.uint8), r.uniform(0.1, 0.4, (T, 2)).astype(np.float32),
+           r.normal(-1, 1, (T, 2)).astype(np.float32)) for _ in range(2)]
+    cfg, cache, kws, pages, table = cache_of(sk, *kv, hq)
+    q = torch.zeros(1, 1, hq, 128, dtype=torch.bfloat16)
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), 0.1, kws)
+    check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], 0.1), step_bound(T), 2.0 ** -22 * (1 + math.log(T)))
+
+
+@pytest.mark.parametrize("hq", [4, 8])
+def test_attention_of_equal_weights_over_many_chunks(sk, hq):
+    """Some 170 chunks a warp of one page, whose even tokens hold the largest codes and odd ones the
+    smallest, so that the running sums only grow: without putting them by every 16 chunks the cuts
+    alone would come to about 2e-5."""
+    B, H, T = 30, 8, 65536
+    codes = np.where(np.arange(64)[:, None] % 2 == 0, 15, 0).repeat(128, 1).astype(np.uint8)
+    s, z = np.full((64, 2), 0.3125, np.float32), np.full((64, 2), -2.0, np.float32)
+    page = np.zeros((1, H, kv4.PAGE_BYTES), np.uint8)
+    for c in range(H):
+        put_all(page, [[0]], 0, c, codes, s, z, False)
+        put_all(page, [[0]], 0, c, codes, s, z, True)
+    cfg = sk.Config(B, H * hq, H, 0, 0, 64)
+    cache = sk.Kv4Cache(cfg, torch.from_numpy(page).cuda(), torch.zeros(B, T // 64, dtype=torch.int32, device="cuda"))
+    kws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1)
+    q = torch.zeros(B, 1, H * hq, 128, dtype=torch.bfloat16, device="cuda")
+    out, lse = sk.kv4_attention(cfg, cache, q, torch.full((B,), T, dtype=torch.int32, device="cuda"), 0.1, kws)
+    bound = 2.0 + 15 * 0.3125
+    worst = (out.double() - (-2.0 + 7.5 * 0.3125)).abs().max().item() / bound
+    # per warp: 64 / 2 cuts, and 11 times putting by; four additions of zero points a chunk and lane
+    tol = 4 * 2.0 ** -22 + 34 * 2.0 ** -23 + (11 + 15 + 152) * 2.0 ** -24 + 4 * 171 / 2 * 2.0 ** -24 * 2.0 / bound
+    assert worst <= tol, f"{worst:.3g}, allowed {tol:.3g}"
+    assert (lse.double() - math.log(T)).abs().max().item() <= 2.0 ** -20 * math.log(T)
+
+
+@pytest.mark.parametrize("hq", [3, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_attention_of_whole_number_logits(sk, hq, dtype):
+    """Queries and keys whose products are whole numbers: the logits are exact, up to 2^-24 of them in
+    the scale, and as much in the exponent."""
+    T = 900
+    r = np.random.default_rng(3)
+    K = (r.integers(0, 16, (T, 128)).astype(np.uint8), np.ones((T, 2), np.float32), np.full((T, 2), -7.0, np.float32))
+    V = (r.integers(0, 16, (T, 128)).astype(np.uint8), r.uniform(0.1, 0.4, (T, 2)).astype(np.float32), r.normal(-1, 1, (T, 2)).astype(np.float32))
+    cfg, cache, kws, pages, table = cache_of(sk, K, V, hq, 2)
+    q = torch.from_numpy(r.integers(-4, 5, (1, 2, hq, 128))).to(DT[dtype])
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), 2.0 ** -6, kws)
+    top = 4 * 8 * 128 / 64 * 1.4427            # the largest logit there can be, log2
+    arg = 3 * 2.0 ** -24 * top
+    check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], 2.0 ** -6), step_bound(T, arg), arg + 2.0 ** -20)
+
+
+def scales_case(T, seed, v_scale, k_code=None, k_scale=4.0):
+    """K whose first group holds k_code [T][2] in its first two dimensions (times k_scale) and zeros
+    elsewhere, the second group random; V of the given scales [T][2], with zero points of its own size."""
+    r = np.random.default_rng(seed)
+    kc = r.integers(0, 16, (T, 128)).astype(np.uint8)
+    kc[:, :64] = 0
+    if k_code is not None:
+        kc[:, :2] = k_code
+    ks, kz = np.tile(np.float32([k_scale, 0.125]), (T, 1)), np.tile(np.float32([0, -1]), (T, 1))
+    vz = kv4.bf16_value(kv4.bf16_bits((-8 * v_scale * r.uniform(0.9, 1.1, v_scale.shape)).astype(np.float32)))
+    return (kc, ks, kz), (r.integers(0, 16, (T, 128)).astype(np.uint8), v_scale.astype(np.float32), vz)
+
+
+@pytest.mark.parametrize("hq", [2, 8])
+@pytest.mark.parametrize("at", [0, 40, 399])
+@pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** 40, 2.0 ** 100])
+def test_attention_beside_a_token_of_large_scale(sk, hq, at, big):
+    """A token of very large V, which half of the heads attend to and the others give no weight at
+    all (their logit for it is 1200 below): it takes nothing from the others' precision."""
+    T = 400
+    r = np.random.default_rng(at)
+    s = r.uniform(0.1, 0.4, (T, 2))
+    s[at] *= big
+    code = np.zeros((T, 2), np.uint8)
+    code[at, 0] = 15
+    K, V = scales_case(T, at + 1, s, code)
+    cfg, cache, kws, pages, table = cache_of(sk, K, V, hq)
+    q = torch.from_numpy(r.normal(0, 1, (1, 1, hq, 128)) * 0.5).bfloat16()
+    q[..., :64] = 0
+    q[:, :, :, 0] = torch.where(torch.arange(hq) % 2 == 0, -20.0, 20.0)
+    ref = kv4.attention(q.double().numpy(), pages, table, [T], 1.0)
+    assert ref[2][0, 0, 0].max() < 100 and ref[2][0, 0, 1].min() > 0.1 * big
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), 1.0, kws)
+    # the second group's logits: 64 products of up to 2 and 1, in steps of 2^-19 of 20 (the column's
+    # largest) times s for each of four matrix instructions; rounded in fp32 at up to 1200
+    arg = 1.4427 * (4 * 2.0 ** -19 * 20 * 0.125 + 3 * 2.0 ** -24 * 1300)
+    check_bound(out, lse, ref, step_bound(T, arg), arg + 2.0 ** -20 + 1300 * 2.0 ** -23)
+
+
+@pytest.mark.parametrize("hq", [1, 8])
+def test_attention_groups_and_tokens_of_any_scale(sk, hq):
+    """Scales of every size from 2^-60 to 2^60, unrelated in the two groups of dimensions."""
+    T = 500
+    r = np.random.default_rng(5)
+    K, V = scales_case(T, 6, 2.0 ** r.uniform(-60, 60, (T, 2)) * np.float32([1.0, 2.0 ** -50]))
+    cfg, cache, kws, pages, table = cache_of(sk, K, V, hq)
+    q = torch.zeros(1, 1, hq, 128, dtype=torch.bfloat16)
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), 1.0, kws)
+    check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], 1.0), step_bound(T), 2.0 ** -20 * math.log(T))
+
+
+@pytest.mark.parametrize("hq", [1, 8])
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+def test_attention_weights_against_scales(sk, hq, order):
+    """Tokens whose weights fall as their scales rise, from 2^-56 to 2^56: all count alike."""
+    T = 480
+    r = np.random.default_rng(7)
+    e = np.sort(r.integers(0, 15, T))
+    e = {"up": e, "down": e[::-1], "mixed": r.permutation(e)}[order]
+    code = np.stack([e, np.zeros_like(e)], -1).astype(np.uint8)
+    K, V = scales_case(T, 8, r.uniform(1, 2, (T, 2)) * 2.0 ** (8.0 * e[:, None] - 56), code, 8.0)
+    cfg, cache, kws, pages, table = cache_of(sk, K, V, hq)
+    q = torch.zeros(1, 1, hq, 128, dtype=torch.bfloat16)
+    q[..., 0] = -1.0
+    scale = math.log(2.0)                       # log2 of the weight: -8 e
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), scale, kws)
+    arg = 3 * 2.0 ** -24 * 120
+    check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], float(np.float32(scale))), step_bound(T, arg), arg + 2.0 ** -20 + 2.0 ** -22 * 10)
+
+
+def test_attention_after_a_token_of_scale_zero_outweighs_all(sk):
+    """The reference of the weights moves far up with a token whose scale is 0 (a vector of one value):
+    what was summed before it still counts by its own size, here that of all that is in the group."""
+    T = 300
+    r = np.random.default_rng(9)
+    s = r.uniform(0.1, 0.4, (T, 2)) * 2.0 ** 60
+    code = np.zeros((T, 2), np.uint8)
+    s[150], code[150, 0] = 0.0, 6
+    K, V = scales_case(T, 10, s, code, 8.0)
+    V[2][150] = 2.0 ** 10
+    cfg, cache, kws, pages, table = cache_of(sk, K, V, 2)
+    q = torch.zeros(1, 1, 2, 128, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), 1.0, kws)
+    arg = 3 * 2.0 ** -24 * 70
+    check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], 1.0), step_bound(T, arg), arg + 2.0 ** -18)

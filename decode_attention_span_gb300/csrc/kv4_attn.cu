@@ -227,19 +227,21 @@ __device__ __forceinline__ void put_queries(AttnShared& sh, const T (&q)[4], int
     x[i] = q_value(q[i]);
     big = fmaxf(big, fabsf(x[i]));
   }
-  float sum = (x[0] + x[2]) + (x[1] + x[3]);
+  // 2^-7 of the sum, which large queries do not take past fp32 (exact for every bf16 and f16 number)
+  float sum = (x[0] * 0.0078125f + x[2] * 0.0078125f) + (x[1] * 0.0078125f + x[3] * 0.0078125f);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
     if (o < 16) sum += __shfl_xor_sync(~0u, sum, o);  // the lower lanes: the first group
   }
-  // power of two that brings the largest element to 2^13 .. 2^14
-  const int e = min(max(int(__float_as_uint(big) >> 23) - 127, -110), 110);
+  // power of two that brings the largest element to 2^13 .. 2^14 (less where it is below 2^-114)
+  const int e = min(max(int(__float_as_uint(big) >> 23) - 127, -114), 127);
   const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
   if ((lane & 15) == 0) {
     // an infinity among the queries makes the column NaN, as NaN does
-    sh.q_sum[lane >> 4][col] = big < INFINITY ? sum * up / (1 << kCodeBits) : NAN;
-    sh.q_scale[col] = __uint_as_float(uint32_t(127 - 13 + kCodeBits + e) << 23) * scale_log2;
+    sh.q_sum[lane >> 4][col] = big < INFINITY ? sum * up / (1 << (kCodeBits - 7)) : NAN;
+    const int f = 127 - 13 + kCodeBits + e, over = max(f - 254, 0);
+    sh.q_scale[col] = scale_log2 * float(1 << over) * __uint_as_float(uint32_t(f - over) << 23);
   }
   // dimension d = 64 gr + 16 t + 8 w + i is in vector 2 gr + w of lane 4 col + t, half i / 4
   // of word i % 4; even dimensions meet low nibbles

@@ -352,3 +352,24 @@ def test_attention_after_a_token_of_scale_zero_outweighs_all(sk):
     out, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), 1.0, kws)
     arg = 3 * 2.0 ** -24 * 70
     check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], 1.0), step_bound(T, arg), arg + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("hq", [2, 8])
+@pytest.mark.parametrize("top,scale", [(119, 2.0 ** -6), (127, 2.0 ** -9), (-113, 2.0 ** -6), (-126, 2.0 ** -6)])
+def test_attention_of_queries_of_any_size(sk, hq, top, scale):
+    """Finite queries far outside f16's range, with keys that make their logits ordinary: whole
+    numbers up to 8, times powers of two."""
+    T = 300
+    r = np.random.default_rng(11)
+    unit = 2.0 ** (-top - 2)                     # |q| up to 2^top, |K| up to 8 units, logits up to 2^7 of the scale
+    ks = np.tile(np.float32([unit, 1.0]), (T, 1)) if top > 0 else np.full((T, 2), unit, np.float32)
+    K = (r.integers(0, 16, (T, 128)).astype(np.uint8), ks, -7 * ks)
+    V = (r.integers(0, 16, (T, 128)).astype(np.uint8), r.uniform(0.1, 0.4, (T, 2)).astype(np.float32), r.normal(-1, 1, (T, 2)).astype(np.float32))
+    cfg, cache, kws, pages, table = cache_of(sk, K, V, hq)
+    q = np.ldexp(r.integers(-8, 9, (1, 1, hq, 128)).astype(np.float64), top - 3)
+    q[..., 0], q[..., 64:] = np.ldexp(1.0, top), 0.0
+    q = torch.from_numpy(q).bfloat16()
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), scale, kws)
+    assert kws.status() == (0, 0)
+    arg = 3 * 2.0 ** -24 * 1.4427 * 64 * 2 * scale   # of the largest logit there can be
+    check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], scale), step_bound(T, arg), arg + 2.0 ** -20)

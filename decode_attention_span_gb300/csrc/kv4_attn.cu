@@ -976,8 +976,8 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
   sekv_status st = kv4_check(cfg, cache, n_q, workspace);
   if (st != SEKV_OK) return st;
   if (dtype != SEKV_BF16 && dtype != SEKV_F16) return SEKV_ERR_INVALID;
-  if (!q || !seq_len || !out || !aligned16(q) || !aligned16(out) || !isfinite(scale) ||
-      !(scale > 0.f))
+  if (!q || !seq_len || !out || !aligned16(q) || !aligned16(out) ||
+      !isfinite(scale * kLog2e) || !(scale > 0.f))
     return SEKV_ERR_INVALID;
   // the kernel numbers tokens and chunks in 32 bits
   if (cache->max_pages >= 1 << 24 ||

@@ -622,7 +622,7 @@ extern "C" sekv_status sekv_token_logprobs(const void* logits, int32_t dtype, in
   const sekv_status st = check_logits(logits, dtype, batch, n_tokens, vocab, tokens, tokens_64,
                                       workspace, workspace_bytes);
   if (st != SEKV_OK) return st;
-  if (!(scale > 0.f) || !isfinite(scale) || n_top < 0 || !logprob ||
+  if (!(scale > 0.f) || !isfinite(scale * kLog2e) || n_top < 0 || !logprob ||
       (n_top > 0) != (top_ids != nullptr) || (n_top > 0) != (top_logprobs != nullptr))
     return SEKV_ERR_INVALID;
   if (n_top > SEKV_MAX_TOP) return SEKV_ERR_UNSUPPORTED;

@@ -569,6 +569,7 @@ typedef enum sekv_dtype { SEKV_BF16 = 0, SEKV_F16 = 1, SEKV_F32 = 2 } sekv_dtype
  *   top     = the n_top largest logits in descending order, ties to the lowest
  *             token id: ids and log-probabilities.
  * One pass over the logits; sums and statistics in fp32.
+ *   scale    > 0, at most 2^127 (as a factor on logits to the base 2 it has to be an fp32 number)
  *   logits   dtype; the row of (b, t) starts at element b*stride_b + t*stride_t;
  *            vocab consecutive elements; any alignment of the element type
  *   tokens   int32 or int64 (tokens_64): token of (b, t) at b*token_stride_b + t;
@@ -748,7 +749,7 @@ sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cache* cache, i
  * queries among them: query i attends to the first seq_len[b] - (n_q - 1 - i)
  * tokens.  A query that sees none has out 0 and lse -inf.
  *   q    bf16 or f16 [batch][n_q][n_q_heads][128], n_q 1 .. SEKV_MAX_QUERY_TOKENS
- *   scale  logit scale, > 0
+ *   scale  logit scale, > 0, at most 2^127
  *   out  f32 [batch][n_q][n_q_heads][128];  lse f32 [batch][n_q][n_q_heads] (natural
  *        log; may be NULL)
  * The (token, head) pairs of a KV head are taken eight at a time in one pass over

@@ -58,10 +58,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// exponent scale (x - m) in log2 units, finite differences first: with x and m
-// at the type's lowest value the product would overflow, the difference is 0
+// c (x - m), finite differences first: with x and m at the type's lowest value the product would
+// overflow, the difference is 0; of halves, because with x and m at its two ends the difference would
+__device__ __forceinline__ float scaled(float x, float m, float c) {
+  return (x * 0.5f - m * 0.5f) * c * 2.f;
+}
+// exponent scale (x - m) in log2 units
 __device__ __forceinline__ float exp_arg(float x, float m, float c) {
-  return (x - (m == -INFINITY ? 0.f : m)) * c;
+  return scaled(x, m == -INFINITY ? 0.f : m, c);
 }
 
 // (s, a) of the smaller maximum p.m in units of the larger one, m
@@ -280,7 +284,7 @@ __device__ __forceinline__ void add_vectors(Stat& st, const uint4 (&w)[N], float
       Row<T>::unpack(w[u], x);
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
-        const float d = (x[j] - m0) * c, e = ex2(d);
+        const float d = scaled(x[j], m0, c), e = ex2(d);
         st.s += e;
         if (FULL) st.a = fmaf(e, fmaxf(d, -1e30f), st.a);
       }
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : 1) logprob_kernel(const Lp
     } else if (tok_x == -INFINITY) {
       lp = -INFINITY;
     } else {
-      lp = (tok_x - all.m) * P.scale - ln_s;
+      lp = scaled(tok_x, all.m, P.scale) - ln_s;
     }
     P.logprob[o] = P.negate && !isnan(lp) ? 0.f - lp : lp;
     if (P.negate && t == 0) P.logprob[o - 1] = 0.f;
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : 1) logprob_kernel(const Lp
       const bool none = k == 0 || bad;
       P.top_ids[o * P.n_top + lane] = none ? -1 : int32_t(key_index(k));
       P.top_lp[o * P.n_top + lane] =
-          bad ? NAN : k == 0 ? -INFINITY : (key_value(k) - all.m) * P.scale - ln_s;
+          bad ? NAN : k == 0 ? -INFINITY : scaled(key_value(k), all.m, P.scale) - ln_s;
     }
   }
 }

@@ -56,6 +56,33 @@ def test_alternatives_of_short_rows_with_masked_first_ids(sk, ws, dtype, vocab, 
     assert ws.status() == (0, 0)
 
 
+@pytest.mark.parametrize("scale", [0.25, 2e-38])
+def test_logits_further_apart_than_fp32_reaches(sk, ws, scale):
+    """Differences of f32 logits of both signs next to the type's ends are past fp32 before the scale
+    brings them back."""
+    V = 3000
+    x = (torch.rand(6, V, generator=gen(2)) * 2 - 1) * 3.3e38
+    x[0, :] = -3.4e38
+    x[0, 5] = 3.4e38
+    x[1, 2999] = 3.4e38
+    x[2, ::2] = torch.randn(V // 2, generator=gen(3))
+    tok = torch.tensor([5, 0, 1, 7, 8, 9])
+    tok[0] = 17
+    r = sk.token_logprobs(x.cuda(), tok.cuda(), ws, n_top=4, scale=scale)
+    want = tokens.token_logprobs(x.double().numpy(), tok.numpy(), float(np.float32(scale)), 4)
+    assert np.array_equal(r.top_ids.cpu().numpy(), want["top_ids"])
+    # three roundings of what an exponent comes from (those below -100 do not count), 2^-22 of the
+    # exponential, the sums; a value past fp32 would be an infinity of its sign
+    d = 300 * 2.0 ** -24 + 2.0 ** -22 + 2.0 ** -24 * (V / 128 + 40)
+    for name in ("logprob", "top_logprobs", "lse", "entropy"):
+        w = want[name]
+        g = getattr(r, name).double().cpu().numpy()
+        big = np.abs(w) > 3.4e38
+        assert np.array_equal(g[big], np.sign(w[big]) * INF), name
+        err = np.abs(g - w)[~big]
+        assert (err <= 3 * d * (1 + (name == "entropy") * np.abs(w[~big])) + 2.0 ** -22 * np.abs(w[~big])).all(), (name, err.max())
+
+
 # ------------------------------------------------------------------ outputs and streams
 def small_cache(sk, B, Hkv, hq, T, seed=0, n_q=1):
     """A 4-bit cache that holds T random tokens of each sequence."""

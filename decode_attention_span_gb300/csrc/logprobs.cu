@@ -32,6 +32,8 @@ namespace {
 
 constexpr int kLpUnroll = 4;      // vectors of a thread in flight
 constexpr int kLpMaxCluster = 8;
+// exponents below this count as this, without weight; times 2^30 elements it is an fp32 number
+constexpr float kFar = -1e28f;
 
 struct LpParams {
   const void* logits;
@@ -71,7 +73,7 @@ __device__ __forceinline__ float exp_arg(float x, float m, float c) {
 // (s, a) of the smaller maximum p.m in units of the larger one, m
 __device__ __forceinline__ void rescale(Stat& p, float m, float c) {
   // a term without weight has no share (0 * finite), whatever its distance
-  const float d = fmaxf(exp_arg(p.m, m, c), -1e30f), f = ex2(d);
+  const float d = fmaxf(exp_arg(p.m, m, c), kFar), f = ex2(d);
   p.a = f * (p.a + p.s * d);
   p.s *= f;
   p.m = m;
@@ -286,7 +288,7 @@ __device__ __forceinline__ void add_vectors(Stat& st, const uint4 (&w)[N], float
       for (int j = 0; j < VE; ++j) {
         const float d = scaled(x[j], m0, c), e = ex2(d);
         st.s += e;
-        if (FULL) st.a = fmaf(e, fmaxf(d, -1e30f), st.a);
+        if (FULL) st.a = fmaf(e, fmaxf(d, kFar), st.a);
       }
     }
   }

@@ -83,6 +83,17 @@ def test_logits_further_apart_than_fp32_reaches(sk, ws, scale):
         assert (err <= 3 * d * (1 + (name == "entropy") * np.abs(w[~big])) + 2.0 ** -22 * np.abs(w[~big])).all(), (name, err.max())
 
 
+def test_one_likely_token_among_450_million_masked_ones(sk, ws):
+    """So many logits at the type's lowest value that their number times their distance, in which
+    the entropy's sum is rescaled, comes near fp32's end; all of the weight is on the last."""
+    V = 450_000_000
+    x = torch.full((1, V), torch.finfo(torch.bfloat16).min, dtype=torch.bfloat16, device="cuda")
+    x[0, -1] = 1.0
+    r = sk.token_logprobs(x, torch.tensor([V - 1], device="cuda"), ws, n_top=1)
+    assert (r.logprob.item(), r.lse.item(), r.entropy.item()) == (0.0, 1.0, 0.0)
+    assert (r.top_ids.item(), r.top_logprobs.item()) == (V - 1, 0.0)
+
+
 # ------------------------------------------------------------------ outputs and streams
 def small_cache(sk, B, Hkv, hq, T, seed=0, n_q=1):
     """A 4-bit cache that holds T random tokens of each sequence."""

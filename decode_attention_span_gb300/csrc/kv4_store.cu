@@ -323,8 +323,8 @@ extern "C" sekv_status sekv_kv4_append(const sekv_config* cfg, const sekv_kv4_ca
   sekv_status st = kv4_check(cfg, cache, 1, workspace);
   if (st != SEKV_OK) return st;
   if (dtype != SEKV_BF16 && dtype != SEKV_F16) return SEKV_ERR_INVALID;
-  if (!k || !v || !k_stride || !v_stride || !first || n_tokens < 0 || !aligned16(k) ||
-      !aligned16(v))
+  if (((!k || !v) && n_tokens != 0) || !k_stride || !v_stride || !first || n_tokens < 0 ||
+      !aligned16(k) || !aligned16(v))
     return SEKV_ERR_INVALID;
   StoreParams P = store_params(cfg, cache, n_tokens, first, n_valid, workspace);
   P.k = k;
@@ -355,7 +355,7 @@ extern "C" sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cach
   sekv_status st = kv4_check(cfg, cache, 1, workspace);
   if (st != SEKV_OK) return st;
   if (dtype < SEKV_BF16 || dtype > SEKV_F32) return SEKV_ERR_INVALID;
-  if (!k_out || !v_out || !first || n_tokens < 0 || !aligned16(k_out) || !aligned16(v_out))
+  if (((!k_out || !v_out) && n_tokens != 0) || !first || n_tokens < 0 || !aligned16(k_out) || !aligned16(v_out))
     return SEKV_ERR_INVALID;
   StoreParams P = store_params(cfg, cache, n_tokens, first, n_valid, workspace);
   P.ko = k_out;

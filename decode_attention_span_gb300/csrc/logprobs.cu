@@ -599,8 +599,8 @@ sekv_status logprobs_impl(const LpParams& P, int32_t dtype, int64_t batch, bool 
 sekv_status check_logits(const void* logits, int32_t dtype, int64_t batch, int64_t n_tokens,
                          int64_t vocab, const void* tokens, int32_t tokens_64, void* workspace,
                          size_t workspace_bytes) {
-  if (dtype < SEKV_BF16 || dtype > SEKV_F32 || batch < 0 || n_tokens < 0 || vocab < 1 || !logits ||
-      !tokens || !workspace)
+  if (dtype < SEKV_BF16 || dtype > SEKV_F32 || batch < 0 || n_tokens < 0 || vocab < 1 ||
+      ((!logits || !tokens) && batch > 0 && n_tokens > 0) || !workspace)
     return SEKV_ERR_INVALID;
   const int elem = dtype == SEKV_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) % elem ||
@@ -628,8 +628,9 @@ extern "C" sekv_status sekv_token_logprobs(const void* logits, int32_t dtype, in
   const sekv_status st = check_logits(logits, dtype, batch, n_tokens, vocab, tokens, tokens_64,
                                       workspace, workspace_bytes);
   if (st != SEKV_OK) return st;
-  if (!(scale > 0.f) || !isfinite(scale * kLog2e) || n_top < 0 || !logprob ||
-      (n_top > 0) != (top_ids != nullptr) || (n_top > 0) != (top_logprobs != nullptr))
+  if (!(scale > 0.f) || !isfinite(scale * kLog2e) || n_top < 0) return SEKV_ERR_INVALID;
+  if (batch > 0 && n_tokens > 0 &&
+      (!logprob || (n_top > 0) != (top_ids != nullptr) || (n_top > 0) != (top_logprobs != nullptr)))
     return SEKV_ERR_INVALID;
   if (n_top > SEKV_MAX_TOP) return SEKV_ERR_UNSUPPORTED;
   if (batch == 0 || n_tokens == 0) return SEKV_OK;
@@ -662,8 +663,8 @@ extern "C" sekv_status sekv_surprisal(const void* logits, int32_t dtype, int64_t
   const sekv_status st = check_logits(logits, dtype, batch, ctx_len, vocab, tokens, tokens_64,
                                       workspace, workspace_bytes);
   if (st != SEKV_OK) return st;
-  if (!H) return SEKV_ERR_INVALID;
   if (batch == 0 || ctx_len == 0) return SEKV_OK;
+  if (!H) return SEKV_ERR_INVALID;
   if (ctx_len == 1)  // nothing is predicted: H is all zeros
     return cudaMemsetAsync(H, 0, size_t(batch) * 4, stream) == cudaSuccess ? SEKV_OK : SEKV_ERR_CUDA;
   LpParams P{};

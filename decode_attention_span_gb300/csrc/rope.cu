@@ -269,7 +269,7 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
   sekv_status why;
   if (!rope_ok(r, &why)) return why;
   if (dtype < SEKV_BF16 || dtype > SEKV_F32 || head_dim < r->rot_dim || batch < 0 || n_tokens < 0 ||
-      !freqs || !positions || (!q && !k) || (flags & ~SEKV_ROPE_BACKWARD) || !isfinite(mscale))
+      !freqs || (!positions && batch > 0 && n_tokens > 0) || (!q && !k) || (flags & ~SEKV_ROPE_BACKWARD) || !isfinite(mscale))
     return SEKV_ERR_INVALID;
   if (head_dim > 1024 || batch > INT32_MAX || n_tokens > INT32_MAX ||
       batch * n_tokens > INT32_MAX)
@@ -277,8 +277,10 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
   const int elem = dtype == SEKV_F32 ? 4 : 2;
   for (const sekv_heads* h : {q, k}) {
     if (!h) continue;
-    if (!h->x || !h->y || h->n_heads < 0 || h->n_heads > 65535 ||
-        reinterpret_cast<uintptr_t>(h->x) % elem || reinterpret_cast<uintptr_t>(h->y) % elem)
+    if (h->n_heads < 0 || h->n_heads > 65535) return SEKV_ERR_INVALID;
+    // what has no elements may have no address, and any strides
+    if (batch == 0 || n_tokens == 0 || h->n_heads == 0) continue;
+    if (!h->x || !h->y || reinterpret_cast<uintptr_t>(h->x) % elem || reinterpret_cast<uintptr_t>(h->y) % elem)
       return SEKV_ERR_INVALID;
     // rows of the output that lie on one another
     if ((batch > 1 && h->y_stride[0] == 0) || (n_tokens > 1 && h->y_stride[1] == 0) ||

@@ -556,7 +556,8 @@ sekv_status sekv_maint_flush(const sekv_config* cfg, const float* W_r, const flo
  * take these as given; formulas are stated here.
  * ------------------------------------------------------------------------ */
 
-/* Element types of the calls below. */
+/* Sizes may be 0 (no tokens, no sequences of logits, no heads): the call does nothing then, and
+ * tensors without elements may be NULL.  Element types of the calls below: */
 typedef enum sekv_dtype { SEKV_BF16 = 0, SEKV_F16 = 1, SEKV_F32 = 2 } sekv_dtype;
 
 /*

@@ -201,6 +201,28 @@ def test_rotation_directly_before_the_attention(sk, in_place):
     assert kws.status() == (0, 0)
 
 
+def test_calls_on_nothing(sk, ws):
+    """No tokens, no sequences, no heads: empty outputs, nothing written, nothing flagged."""
+    cfg, cache, kws = small_cache(sk, 2, 2, 4, 70)
+    pages = cache.pages.clone()
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    k = torch.empty(2, 0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    sk.kv4_append(cfg, cache, k, k, zero, kws)
+    r = sk.kv4_read(cfg, cache, zero, 0, kws, n_valid=zero)
+    assert r[0].shape == (2, 2, 0, 128) and torch.equal(cache.pages, pages)
+    plan = sk.RopePlan(128)
+    for B, T, h in ((2, 0, 3), (0, 4, 3), (2, 4, 0)):
+        x = torch.empty(B, T, h, 128, device="cuda")
+        q, kk = sk.rope(plan, x, x, torch.zeros(B, T, dtype=torch.int64, device="cuda"))
+        assert q.shape == kk.shape == x.shape
+    for B, T in ((0, 3), (2, 0)):
+        t = torch.zeros(B, T, dtype=torch.int64, device="cuda")
+        x = torch.empty(B, T, 50, device="cuda")
+        assert sk.token_logprobs(x, t, ws, n_top=2).top_ids.shape == (B, T, 2)
+        assert sk.surprisal(x, t, ws).shape == (B, T)
+    assert kws.status() == (0, 0) and ws.status() == (0, 0)
+
+
 # ------------------------------------------------------------------ the 4-bit attention's precision
 # What a call may be off by, of the softmax-weighted mean of |z| + 15 |s| (per group of dimensions;
 # `bound` of the oracle):

@@ -28,3 +28,32 @@ def test_scales_beyond_fp32_to_the_base_two_are_refused(libsekv):
         for scale in (3.4e38, 2.5e38):
             assert call(scale) == INVALID
         assert call(2.0 ** 127) != INVALID
+
+
+def test_tensors_without_elements_may_have_no_address(libsekv):
+    """What torch gives for an empty tensor is address 0."""
+    import decode_attention_span_gb300 as sk
+    from decode_attention_span_gb300 import rotary
+    from decode_attention_span_gb300.kv4 import SekvKv4Cache
+    cfg = ctypes.byref(sk.Config(1, 8, 2, 0, 0, 64).c())
+    cache = ctypes.byref(SekvKv4Cache(1 << 20, 1 << 20, 4, 4))
+    S = (ctypes.c_int64 * 3)(8, 8, 8)
+    append = lambda n: libsekv.sekv_kv4_append(cfg, cache, 0, None, S, None, S, n, P, None, P, 0, None)  # noqa: E731
+    read = lambda n: libsekv.sekv_kv4_read(cfg, cache, 0, None, None, n, P, None, P, 0, None)  # noqa: E731
+    heads = lambda n, s=256: ctypes.byref(rotary.SekvHeads(0, 0, n, 0, s, 128, 0, s, 128))  # noqa: E731
+
+    def rope(B, T, n, pos=None):
+        return libsekv.sekv_rope(ctypes.byref(rotary.rope_config(64)), P, 1.0, 0, 128, B, T, pos, 0, 0, heads(n), None, 0, None)
+
+    def logprobs(B, T):
+        return libsekv.sekv_token_logprobs(None, 0, B, T, 9, 0, 9, None, 0, 0, 1.0, 0, None, None, None, None, None, P, 4096, None)
+
+    def surprisal(B, T):
+        return libsekv.sekv_surprisal(None, 0, B, T, 9, 0, 9, None, 0, 0, None, P, 4096, None)
+    assert append(0) == 0 and read(0) == 0
+    assert append(1) == INVALID and read(1) == INVALID
+    assert rope(1, 0, 2) == 0 and rope(0, 3, 2) == 0 and rope(1, 3, 0, P) == 0 and rope(2, 0, 2) == 0
+    assert rope(2, 3, 0, P) == 0                 # its strides as torch has them are 0 too
+    assert rope(1, 3, 2, P) == INVALID and rope(1, 3, 2) == INVALID
+    for call in (logprobs, surprisal):
+        assert call(0, 3) == 0 and call(2, 0) == 0 and call(1, 2) == INVALID

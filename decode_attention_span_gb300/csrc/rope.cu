@@ -14,7 +14,6 @@
 // copy rate; one token 2.0 us.
 #include <cuda_fp16.h>
 #include <math.h>
-#include <string.h>
 
 #include "decode_host.h"
 #include "host_common.h"
@@ -280,14 +279,16 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
     if (h->n_heads < 0 || h->n_heads > 65535) return SEKV_ERR_INVALID;
     // what has no elements may have no address, and any strides
     if (batch == 0 || n_tokens == 0 || h->n_heads == 0) continue;
-    if (!h->x || !h->y || reinterpret_cast<uintptr_t>(h->x) % elem || reinterpret_cast<uintptr_t>(h->y) % elem)
+    if (!h->x || !h->y || reinterpret_cast<uintptr_t>(h->x) % elem ||
+        reinterpret_cast<uintptr_t>(h->y) % elem)
       return SEKV_ERR_INVALID;
-    // rows of the output that lie on one another
-    if ((batch > 1 && h->y_stride[0] == 0) || (n_tokens > 1 && h->y_stride[1] == 0) ||
-        (h->n_heads > 1 && h->y_stride[2] == 0))
-      return SEKV_ERR_INVALID;
-    if (h->x == h->y && memcmp(h->x_stride, h->y_stride, sizeof(h->x_stride)) != 0)
-      return SEKV_ERR_INVALID;
+    const int64_t size[3] = {batch, n_tokens, h->n_heads};
+    for (int i = 0; i < 3; ++i) {
+      if (size[i] <= 1) continue;  // the stride of a single row means nothing
+      // rows of the output that lie on one another, or on other rows of the input
+      if (h->y_stride[i] == 0 || (h->x == h->y && h->x_stride[i] != h->y_stride[i]))
+        return SEKV_ERR_INVALID;
+    }
   }
   if (reinterpret_cast<uintptr_t>(freqs) % 8 ||
       reinterpret_cast<uintptr_t>(positions) % (positions_64 ? 8 : 4))

@@ -201,6 +201,18 @@ def test_rotation_directly_before_the_attention(sk, in_place):
     assert kws.status() == (0, 0)
 
 
+def test_rotation_in_place_of_a_single_sequence(sk):
+    """The same rows seen through another view, whose stride of the single sequence is another:
+    still in place."""
+    plan, pos = sk.RopePlan(128), torch.arange(5, dtype=torch.int32, device="cuda")
+    big = torch.randn(3, 5, 4, 128, generator=gen(1)).bfloat16().cuda()
+    want = sk.rope(plan, big[1:2].clone(), None, pos)[0]
+    x, y = big[1:2], big[1].unsqueeze(0).as_strided((1, 5, 4, 128), (8, 512, 128, 1), 5 * 4 * 128)
+    assert x.data_ptr() == y.data_ptr() and x.stride(0) != y.stride(0)
+    sk.rope(plan, x, None, pos, q_out=y)
+    assert torch.equal(x, want)
+
+
 def test_calls_on_nothing(sk, ws):
     """No tokens, no sequences, no heads: empty outputs, nothing written, nothing flagged."""
     cfg, cache, kws = small_cache(sk, 2, 2, 4, 70)

@@ -3,9 +3,11 @@
 //
 // Pair i of a token at position p turns by p f_i.  The table holds f_i / (2 pi)
 // as a 64-bit fixed-point fraction of a turn, so p * table[i] modulo 2^64 (one
-// integer product) is the angle's fraction of a turn without any rounding that
-// grows with p; its upper 32 bits go to sincospi.  An fp32 product p * f_i
-// would lose the angle from positions of about 10^5 on.
+// integer product) is the angle's fraction of a turn, and only the entry's own
+// error grows with p: the entries are computed in fp64, which puts an angle off
+// by at most p 2^-49 (below fp32's step up to p of 2^25).  The upper 32 bits go to
+// sincospi.  An fp32 product p * f_i would lose the angle from positions of
+// about 10^5 on.
 //
 // Bound by memory: every value is read and written once.  One thread owns a
 // few neighbouring pairs of one token, takes their sines once and applies them

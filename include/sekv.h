@@ -645,8 +645,10 @@ typedef struct sekv_rope_config {
 
 /* The table of a rotary plan (host only): freqs[i] (host, rot_dim / 2 entries) is
  * f_i / (2 pi) modulo one turn, as a 64-bit fixed-point fraction of a turn, so that
- * position * freqs[i] modulo 2^64 is the pair's angle exactly however far the
- * position; *mscale is the factor on the result.  Copy freqs to the device once. */
+ * position * freqs[i] modulo 2^64 is the pair's angle with no rounding of its own.
+ * The entries come from fp64 arithmetic: an angle is off by at most position * 2^-49
+ * (and by fp32's step in the sine and cosine).  *mscale is the factor on the result.
+ * Copy freqs to the device once. */
 sekv_status sekv_rope_freqs(const sekv_rope_config* rope, uint64_t* freqs, float* mscale);
 
 /* Heads of one tensor: element (b, t, h, d) of the input at x[b*x_stride[0] +

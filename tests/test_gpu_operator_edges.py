@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from oracle import kv4, tokens
+from turns import turns
 
 from cases import SCALE, TOL_ABS, decode_case
 
@@ -211,6 +212,20 @@ def test_rotation_in_place_of_a_single_sequence(sk):
     assert x.data_ptr() == y.data_ptr() and x.stride(0) != y.stride(0)
     sk.rope(plan, x, None, pos, q_out=y)
     assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_at_far_positions_by_fifty_digits(sk, inter):
+    """Positions up to 2^40 against angles that do not come from the table."""
+    pos = [1, 1 << 20, (1 << 24) + 1, (1 << 31) - 1, 12345678901, (1 << 40) - 7]
+    plan, w = sk.RopePlan(128, 500000.0, inter), turns(128, 500000.0)
+    x = torch.randn(1, len(pos), 2, 128, generator=gen(3)).cuda()
+    got = sk.rope(plan, x, None, torch.tensor([pos], device="cuda"))[0].double().cpu().numpy()
+    for t, p in enumerate(pos):
+        angle = np.array([float(p * v % 1) * 2 * math.pi for v in w])
+        want = tokens.rope(x[:, t:t + 1].double().cpu().numpy(), [[1]], angle, 1.0, inter)
+        # the table's error, and fp32's: the fraction of a half turn, the sine, three operations
+        assert np.abs(got[:, t:t + 1] - want).max() <= 2 * 5 * (p * 2.0 ** -49 + 2.0 ** -22), p
 
 
 def test_calls_on_nothing(sk, ws):

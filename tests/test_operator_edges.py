@@ -1,7 +1,10 @@
 """Host-side refusals and tables of the operators around the cache (CPU)."""
 import ctypes
 
+import numpy as np
 import pytest
+
+from turns import turns
 
 
 @pytest.fixture(scope="module")
@@ -57,3 +60,23 @@ def test_tensors_without_elements_may_have_no_address(libsekv):
     assert rope(1, 3, 2, P) == INVALID and rope(1, 3, 2) == INVALID
     for call in (logprobs, surprisal):
         assert call(0, 3) == 0 and call(2, 0) == 0 and call(1, 2) == INVALID
+
+
+@pytest.mark.parametrize("rot,base,scaling,factor", [
+    (128, 500000.0, "none", 1.0), (64, 10000.0, "linear", 3.0), (128, 10000.0, "ntk", 8.0), (96, 1e6, "parts", 40.0),
+    (128, 500000.0, "banded", 8.0), (512, 1e6, "none", 1.0), (2, 10000.0, "none", 1.0)])
+def test_rope_table_against_fifty_digits(libsekv, rot, base, scaling, factor):
+    """The table's entries against the formulas in decimals, not through fp64.  With t = ln of
+    the unscaled pace, an exponent's rounding moves it by t 2^-53 of itself; the power, 2 pi, its
+    quotient and the scalings' six operations by 2^-53 each; the entry is cut at 2^-63.  As
+    (t + 12) e^-t is at most 12, an angle is off by 12 * 2^-53 of a radian a position, below
+    2^-49."""
+    from decode_attention_span_gb300 import rotary
+    freqs, _ = rotary.rope_freqs(rotary.rope_config(rot, base, scaling=scaling, factor=factor))
+    want = turns(rot, base, scaling, factor)
+    for i, (got, w) in enumerate(zip(freqs.numpy().view(np.uint64), want)):
+        off = abs(int(got) - int(w % 1 * 2 ** 64))
+        off = min(off, 2 ** 64 - off) / 2.0 ** 64
+        t = 2 * i / rot * np.log(base * (factor ** (rot / (rot - 2)) if scaling == "ntk" else 1))
+        assert off <= (t + 12) * 2.0 ** -53 * float(w) + 2.0 ** -63, i
+        assert off * 2 * np.pi <= 2.0 ** -49

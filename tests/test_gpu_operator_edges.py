@@ -460,3 +460,45 @@ def test_attention_of_queries_of_any_size(sk, hq, top, scale):
     assert kws.status() == (0, 0)
     arg = 3 * 2.0 ** -24 * 1.4427 * 64 * 2 * scale   # of the largest logit there can be
     check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], scale), step_bound(T, arg), arg + 2.0 ** -20)
+
+
+# ------------------------------------------------------------------ the 4-bit cache's codes
+def rows_at_halves(dtype):
+    """Groups of 64 for every significand of a scale s and every half n + 1/2: the dividend x - z is
+    that half times s, exactly, and next to it by one step of fp32 and by more; and the ends of
+    the range.  (z takes all of the half's bits that bf16 holds, x the rest and the step.)"""
+    groups = []
+    to = lambda v: torch.tensor(v, dtype=torch.float32).to(DT[dtype]).float().tolist()  # noqa: E731
+    for m in range(128, 256):
+        s = m / 64.0
+        for n in range(15):
+            half = (n + 0.5) * s
+            z = kv4.bf16_value(kv4.bf16_floor_bits(np.float32(-half))).item()
+            step = 2.0 ** (math.floor(math.log2(half)) - 23)
+            rest = half + z
+            xs = [rest + k * step / 2 for k in range(-8, 9)] + [rest * (1 + k / 256) for k in range(-10, 11)]
+            xs += [z + (n + h) * s for h in (0.4, 0.499, 0.5, 0.501, 0.6)] + [z + i * s for i in range(16)]
+            xs = [min(max(x, z), z + 15 * s) for x in to(xs)]
+            groups.append((to([z, z + 15 * s]) + xs + [z] * 64)[:64])
+    return torch.tensor(groups).view(-1, 128)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_codes_of_dividends_at_every_half(sk, dtype):
+    """The codes come from a corrected reciprocal; they are those of a division."""
+    x = rows_at_halves(dtype).to(DT[dtype])[None, :, None]
+    T = x.shape[1]
+    mp = -(-T // 64)
+    cfg = sk.Config(1, 1, 1, 0, 0, 64)
+    table = np.arange(mp, dtype=np.int32)[None]
+    cache = sk.Kv4Cache(cfg, torch.zeros(mp, 1, 9216, dtype=torch.uint8, device="cuda"), torch.from_numpy(table).cuda())
+    kws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1)
+    sk.kv4_append(cfg, cache, x.cuda(), (-x).cuda(), torch.zeros(1, dtype=torch.int32, device="cuda"), kws)
+    want = np.zeros((mp, 1, kv4.PAGE_BYTES), np.uint8)
+    for is_v, y in ((0, x), (1, -x)):
+        n, sb, zb = kv4.quantise(y.float().numpy())
+        if not is_v:
+            assert len(set((sb & 127).reshape(-1).tolist())) == 128   # every significand of a scale
+        for t in range(T):
+            kv4.put(want, table, 0, 0, t, n[0, t, 0], sb[0, t, 0], zb[0, t, 0], is_v)
+    assert np.array_equal(cache.pages.cpu().numpy(), want)

@@ -757,7 +757,14 @@ sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cache* cache, i
  *        log; may be NULL)
  * The (token, head) pairs of a KV head are taken eight at a time in one pass over
  * its cache (sekv_query_blocks).  Results do not depend on what else runs:
- * partial results are merged in a fixed order. */
+ * partial results are merged in a fixed order.
+ * Accuracy: sums are fp32.  A query element counts in steps of some 2^-18 of the largest
+ * of its (token, head), which takes up to 2^-16 max|q| (s_0 + s_1) scale off a logit (s_g:
+ * the key's scales); fp32 roundings are 2^-22 of scale sum_d |q_d| (|z| + 15 |s|).  A
+ * weight enters with 22 bits: an output is off by up to 2^-18 of the softmax-weighted mean
+ * of |z| + 15 |s| over the values' group (2^-22 as a rule), and by twice the logits' error times
+ * that.  No token takes bits from another by the size of its values alone.  Finite queries
+ * with max|q| scale below 2^119 give finite results where the logits are. */
 sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4_cache* cache,
                                int32_t dtype, const void* q, int32_t n_q,
                                const int32_t* seq_len, float scale, float* out, float* lse,

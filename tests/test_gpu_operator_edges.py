@@ -462,6 +462,37 @@ def test_attention_of_queries_of_any_size(sk, hq, top, scale):
     check_bound(out, lse, kv4.attention(q.double().numpy(), pages, table, [T], scale), step_bound(T, arg), arg + 2.0 ** -20)
 
 
+@pytest.mark.parametrize("hq", [1, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("outlier", [0.0, 50.0, 3000.0])
+def test_logits_one_by_one(sk, hq, dtype, outlier):
+    """Sequences of one token: the log-sum-exp is the logit, held to the header's bound."""
+    B, scale = 200, 0.0884
+    r = np.random.default_rng(13)
+    cfg = sk.Config(B, hq, 1, 0, 0, 64)
+    pages, table = np.zeros((B, 1, kv4.PAGE_BYTES), np.uint8), np.arange(B, dtype=np.int32)[:, None]
+    for b in range(B):
+        s, z = r.uniform(0.05, 2, (1, 2)), r.normal(-3, 3, (1, 2))
+        put_all(pages, table, b, 0, r.integers(0, 16, (1, 128)).astype(np.uint8), s.astype(np.float32), z.astype(np.float32), False)
+    cache = sk.Kv4Cache(cfg, torch.from_numpy(pages).cuda(), torch.from_numpy(table).cuda())
+    kws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1)
+    q = r.normal(0, 1, (B, 1, hq, 128))
+    for i in range(B):
+        q[i, 0, :, r.integers(0, 128)] += outlier
+    q = torch.from_numpy(q).to(DT[dtype])
+    _, lse = sk.kv4_attention(cfg, cache, q.cuda(), torch.ones(B, dtype=torch.int32, device="cuda"), scale, kws)
+    scale = float(np.float32(scale))
+    want = kv4.attention(q.double().numpy(), pages, table, [1] * B, scale)
+    q = np.abs(q.double().numpy())[:, 0]
+    s = np.stack([kv4.bf16_value(pages[:, 0, 2048 + 4 * g:2050 + 4 * g].copy().view(np.uint16)[:, 0]) for g in range(2)], 1).astype(np.float64)
+    z = np.stack([kv4.bf16_value(pages[:, 0, 2050 + 4 * g:2052 + 4 * g].copy().view(np.uint16)[:, 0]) for g in range(2)], 1).astype(np.float64)
+    size = np.einsum("bhgd,bg->bh", q.reshape(B, hq, 2, 64), np.abs(z) + 15 * s)
+    bound = scale * (2.0 ** -16 * q.max(-1) * s.sum(1)[:, None] + 2.0 ** -22 * size)
+    # the way to log2 and back: 2^-22 of the logit
+    err = np.abs(lse.double().cpu().numpy() - want[1])[:, 0]
+    assert (err <= bound + 2.0 ** -22 * np.abs(want[1][:, 0])).all(), (err / bound).max()
+
+
 # ------------------------------------------------------------------ the 4-bit cache's codes
 def rows_at_halves(dtype):
     """Groups of 64 for every significand of a scale s and every half n + 1/2: the dividend x - z is

@@ -533,3 +533,132 @@ def test_codes_of_dividends_at_every_half(sk, dtype):
         for t in range(T):
             kv4.put(want, table, 0, 0, t, n[0, t, 0], sb[0, t, 0], zb[0, t, 0], is_v)
     assert np.array_equal(cache.pages.cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ together
+def step_inputs(sk, B=2, hq=8, hkv=2, V=3000):
+    cfg = sk.Config(B, hq, hkv, 0, 0, 64)
+    mp = 4
+    pages = torch.zeros(B * mp, hkv, 9216, dtype=torch.uint8, device="cuda")
+    cache = sk.Kv4Cache(cfg, pages, torch.arange(B * mp, dtype=torch.int32, device="cuda").view(B, mp))
+    g = gen(21)
+    x = {n: torch.randn(B, 1, h, 128, generator=g).bfloat16().cuda() for n, h in (("q", hq), ("k", hkv), ("v", hkv))}
+    x["logits"], x["tok"] = torch.randn(B, V, generator=g).cuda(), torch.tensor([3, V - 1]).cuda()
+    return cfg, cache, x, sk.RopePlan(128)
+
+
+def test_a_step_captured_over_two_streams(sk, ws):
+    """Calls that fork and join inside one captured graph: launches that may start early only do so
+    behind the kernel before them on their own stream, and all wait for what they need."""
+    cfg, cache, x, plan = step_inputs(sk)
+    B = cfg.batch
+    kws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1)
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first, lens = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    one, H = torch.zeros(B, 1, dtype=torch.int64, device="cuda"), torch.full((B, 1), 9.0, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step(fork):
+        s = side if fork else None
+        here = torch.cuda.current_stream()
+        qr, kr = sk.rope(plan, x["q"], x["k"], pos)
+        if fork:
+            side.wait_stream(here)
+        sk.kv4_append(cfg, cache, kr, x["v"], first, kws, stream=s)
+        r = sk.token_logprobs(x["logits"], x["tok"], ws, n_top=3)
+        H.fill_(9)
+        sk.surprisal(x["logits"][:, None], one, ws, out=H)      # a fill, no kernel of its own
+        if fork:
+            here.wait_stream(side)
+        o, lse = sk.kv4_attention(cfg, cache, qr, lens, 0.0884, kws)
+        return [o, lse, r.logprob, r.top_ids, H.clone()]
+
+    def set_step(t):
+        pos.fill_(t); first.fill_(t); lens.fill_(t + 1)
+        for i, n in enumerate(("q", "k", "v", "logits")):
+            x[n].copy_(torch.randn(x[n].shape, generator=gen(100 * t + i)))
+    set_step(0)
+    step(True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(True)
+    want = []
+    cache.pages.zero_()
+    for t in range(60):
+        set_step(t)
+        want.append([a.clone() for a in step(False)])
+        torch.cuda.synchronize()
+    cache.pages.zero_()
+    for t in range(60):
+        set_step(t)
+        graph.replay()
+        for a, b in zip(got, want[t]):
+            assert torch.equal(a, b), t
+    assert kws.status() == (0, 0) and ws.status() == (0, 0)
+
+
+def test_calls_from_two_threads(sk):
+    """Two host threads, each with its own stream, workspaces and cache."""
+    import threading
+    results = [None, None]
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            cfg, cache, x, plan = step_inputs(sk)
+            w, kws = sk.Workspace(cfg), sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1)
+            out = []
+            for t in range(100):
+                i32 = dict(dtype=torch.int32, device="cuda")
+                qr, kr = sk.rope(plan, x["q"], x["k"], torch.full((1,), t, **i32))
+                sk.kv4_append(cfg, cache, kr, x["v"], torch.full((2,), t, **i32), kws)
+                o, _ = sk.kv4_attention(cfg, cache, qr, torch.full((2,), t + 1, **i32), 0.1, kws)
+                out += [o, sk.token_logprobs(x["logits"], x["tok"], w, n_top=2).top_logprobs]
+            results[i] = [a.cpu() for a in out] + [kws.status(), w.status()]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert results[0][-2:] == results[1][-2:] == [(0, 0), (0, 0)]
+    for a, b in zip(results[0][:-2], results[1][:-2]):
+        assert torch.equal(a, b)
+
+
+def test_rows_further_apart_than_32_bits(sk, ws):
+    """Sequences 2^32 and more elements apart, in and out."""
+    far = (1 << 32) + 1024
+    big = torch.empty(far + 65536, dtype=torch.bfloat16, device="cuda")
+    T, H = 20, 3
+    x = big.as_strided((2, T, H, 128), (far, H * 128, 128, 1))
+    x.copy_(torch.randn(2, T, H, 128, generator=gen(1)))
+    near = x.clone()
+    plan, pos = sk.RopePlan(128), torch.arange(T, dtype=torch.int32, device="cuda")
+    want = sk.rope(plan, near, None, pos)[0]
+    assert torch.equal(sk.rope(plan, x, None, pos)[0], want)
+    cfg = sk.Config(2, H, H, 0, 0, 64)
+    caches = [sk.Kv4Cache(cfg, torch.zeros(2, H, 9216, dtype=torch.uint8, device="cuda"),
+                          torch.arange(2, dtype=torch.int32, device="cuda").view(2, 1)) for _ in range(2)]
+    kws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1)
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for c, y in zip(caches, (near, x)):
+        sk.kv4_append(cfg, c, y, y, zero, kws)
+    assert torch.equal(caches[0].pages, caches[1].pages)
+    logits = big.as_strided((2, 4, 1999), (far, 2048, 1))
+    logits.copy_(torch.randn(2, 4, 1999, generator=gen(2)))
+    tok = torch.randint(0, 1999, (2, 4), generator=gen(3)).cuda()
+    r = sk.token_logprobs(logits, tok, ws, n_top=5)
+    want_lp = tokens.token_logprobs(logits.double().cpu().numpy().reshape(8, 1999), tok.cpu().numpy().reshape(-1), 1.0, 5)
+    assert np.array_equal(r.top_ids.cpu().numpy().reshape(8, 5), want_lp["top_ids"])
+    # not bit for bit a call on rows of 1999 side by side: those start at other offsets in their
+    # 16-byte vectors, and so group their sums otherwise.  Exponents of up to 10, 2000 / 128 + 40 additions,
+    # the result's own size (up to 13)
+    d = 30 * 2.0 ** -24 + 2.0 ** -22 + 56 * 2.0 ** -24
+    for name in ("logprob", "lse", "entropy", "top_logprobs"):
+        got = getattr(r, name).double().cpu().numpy().reshape(want_lp[name].shape)
+        assert np.abs(got - want_lp[name]).max() <= 3 * d * (14 if name == "entropy" else 1) + 2.0 ** -22 * 13, name
+    x.copy_(near)
+    sk.rope(plan, x, None, pos, q_out=x)
+    assert torch.equal(x, want)
+    assert kws.status() == (0, 0) and ws.status() == (0, 0)

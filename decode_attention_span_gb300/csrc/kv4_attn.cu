@@ -22,10 +22,10 @@
 //
 // The matrix instructions take a number below the normal ones as if it were as large as those
 // when they line their addends up, and cut off 25 bits under the largest.  So the place of
-// a code in its f16 costs bits: shifted up by two, V's give an error of 2.6e-7 where n 2^-24
+// a code in its f16 costs bits: shifted up by two, V's give an error of 2.4e-7 where n 2^-24
 // gives 1.1e-6 (4 x 2000), and a query element counts in steps of 2^-19 of the column's largest
-// (n 2^-24 for all of K: 2^-15, and 100 us at 16 x 65536 instead of 103; K's high nibbles as
-// normal numbers too: 107 us).
+// (n 2^-24 for all of K: 2^-15, for 3% less time at 16 x 65536; K's high nibbles as normal
+// numbers too: 3% more).
 //
 // Work: the cache is a line of chunks of 32 tokens (sequence by sequence, in
 // it KV head by KV head), cut into equal pieces, one per CTA.  The warps of a CTA
@@ -34,15 +34,15 @@
 // group spans several CTAs, leaves a partial; the last of them to finish joins
 // the partials in order.
 //
-// What bounds it is instruction issue, not memory: a chunk takes a warp about 600
-// instructions (208 of them turn codes into operands), issued at 53% of the rate
-// because many are two-clock ones (logic, conversions), a matrix instruction takes two to
-// four slots, and registers allow three warps per SM quarter, too few to hide every wait for a
-// result.  Measured, 16 sequences of up to 65536 tokens, 28 query and 4 KV heads (463 MB):
-// 103 us, copies alone 76 us, arithmetic alone 97 us; one sequence of 131072, 32 and 8
+// What bounds it is waits for results, not memory and no single unit: a chunk takes a warp
+// about 600 instructions (208 of them turn codes into operands), most of them in chains of fixed
+// latency, and registers allow three warps per SM quarter, too few to hide those (issue 55%, ALU
+// 46%, tensor 34%, DRAM 55% busy).  Measured, 16 sequences of up to 65536 tokens, 28 query
+// and 4 KV heads (463 MB): 102.5 us, copies alone 76 us; one sequence of 131072, 32 and 8
 // heads (151 MB): 39.5 us, copies alone 31 us, of which about 9 us move no data.  128-row
-// tcgen05 tiles would want the operands in shared memory as f16: 16 KB a chunk written and
-// read again at 128 bytes a clock, 256 clocks where a chunk now takes 265 in all.
+// tcgen05 tiles with these eight columns alone, and f16 operands by way of shared memory,
+// would write and read 16 KB a chunk again at 128 bytes a clock: 256 clocks where a chunk now
+// takes about 265 in all.
 // e4m3 operands (a code's four bits in a byte are n 2^-9) need no arithmetic to make, but
 // mma.sync converts them to f16 again: 53 us where f16 took 44.
 #include <math.h>

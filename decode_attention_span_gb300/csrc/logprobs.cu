@@ -14,8 +14,9 @@
 // maxima of every four threads is a bound that at least n elements reach; only the
 // vectors of threads whose own maximum reaches it are read again (out of L2), a warp
 // per thread, and what reaches the bound -- little more than n elements as a rule --
-// is sorted by (value, lowest index first).  Where ties make them too many, the
-// bound is found again among exact keys of value and index, which no two elements share.
+// is sorted by (value, lowest index first).  Where that is too many -- ties, or rows
+// so short that the n-th of the maxima is one of the lowest of them -- the bound is found
+// again among exact keys of value and index, which no two elements share.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -321,9 +322,10 @@ __device__ __forceinline__ void collect(LpShared<NT>& sh, const Row<T>& row, int
   }
 }
 
-// The alternatives of a slice when many elements share the value of the bound: the bound
-// among exact keys, and if the largest logits all lie in a few threads' vectors so
-// that even those are too many, one alternative per round.
+// The alternatives of a slice when many elements reach the bound (ties; or short rows with
+// many alternatives, such as 500 in bf16 with 20): the bound among exact keys, and if even
+// those are too many -- the largest logits lie in a few threads' vectors, or there are fewer
+// threads with a vector than alternatives -- one alternative per round.
 template <typename T, int NT>
 __device__ __noinline__ void top_of_ties(LpShared<NT>& sh, const Row<T>& row, int lo, int hi,
                                          float thread_max, int n_top) {

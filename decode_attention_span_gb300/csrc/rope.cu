@@ -25,8 +25,8 @@ using namespace sekv;
 namespace {
 
 constexpr int kRopeThreads = 128;
-// heads whose loads a thread issues together: 32768 tokens take 116 us with 2, 140 with 4
-// (fewer warps fit), 124 with 1
+// heads whose loads a thread issues together: 32768 tokens take 112 us with 2, 144 with 4
+// (fewer warps fit), 108 with 1 (which was behind, 124 to 116, before the streaming stores)
 constexpr int kHeadsInFlight = 2;
 
 struct RopeHeads {
@@ -43,7 +43,7 @@ struct RopeParams {
   int64_t pos_stride_b;
   float mscale;
   int pos64, backward;
-  int rot, dim;            // rotated dimensions, all dimensions
+  int rot;                 // rotated dimensions
   int nrot, nvec;          // work items of a token: rotated ones, all
   int tok_per_block;
   uint32_t n_tokens;       // per sequence
@@ -321,7 +321,6 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
   P.pos64 = positions_64 != 0;
   P.backward = (flags & SEKV_ROPE_BACKWARD) != 0;
   P.rot = r->rot_dim;
-  P.dim = head_dim;
   const int pairs = r->interleaved ? (n > 1 ? n / 2 : 1) : n;
   P.nrot = r->rot_dim / 2 / pairs;
   P.nvec = P.nrot + (head_dim - r->rot_dim) / n;
@@ -332,7 +331,7 @@ extern "C" sekv_status sekv_rope(const sekv_rope_config* r, const uint64_t* freq
   if (sms <= 0) return SEKV_ERR_CUDA;
   const uint32_t blocks = (P.total + P.tok_per_block - 1) / P.tok_per_block;
   // Heads of one thread: halved until the blocks make some four waves (32768 tokens: 112 us;
-  // with one wave of longer threads 116, with eight 122, the sines being taken more often);
+  // with one wave of longer threads 116, with eight 117, the sines being taken more often);
   // a step of a few tokens spreads its heads over blocks one by one.
   int hpt = heads;
   while (hpt > kHeadsInFlight && uint64_t(blocks) * ((heads + hpt - 1) / hpt) < uint64_t(sms) * 32)

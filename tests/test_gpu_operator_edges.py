@@ -662,3 +662,49 @@ def test_rows_further_apart_than_32_bits(sk, ws):
     sk.rope(plan, x, None, pos, q_out=x)
     assert torch.equal(x, want)
     assert kws.status() == (0, 0) and ws.status() == (0, 0)
+
+
+def test_most_sequences_a_cache_may_have(sk):
+    """1024 sequences, half of them empty, over pages that they share."""
+    B, H, hq, T = 1024, 2, 6, 150
+    cfg1, one, ws1 = small_cache(sk, 1, H, hq, T, seed=4)
+    cfg = sk.Config(B, hq, H, 0, 0, 64)
+    cache = sk.Kv4Cache(cfg, one.pages, one.page_table.repeat(B, 1))
+    kws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=2)
+    lens = torch.randint(0, T + 1, (B,), generator=gen(2)).int()
+    lens[::2] = 0
+    q = torch.randn(B, 2, hq, 128, generator=gen(3)).bfloat16()
+    out, lse = sk.kv4_attention(cfg, cache, q.cuda(), lens.cuda(), 0.0884, kws)
+    assert kws.status() == (0, 0)
+    assert not out[::2].any() and (lse[::2] == -INF).all()
+    pages, table = one.pages.cpu().numpy(), one.page_table.cpu().numpy()
+    scale = float(np.float32(0.0884))
+    for b in (1, 37, 511, 1023):
+        ref = kv4.attention(q[b:b + 1].double().numpy(), pages, table, [int(lens[b])], scale)
+        # scales below 0.5, |q| below 5, |K| below 5: what the header allows a logit
+        arg = 1.4427 * scale * (2.0 ** -16 * 5 * 1 + 2.0 ** -22 * 128 * 5 * 10)
+        check_bound(out[b:b + 1], lse[b:b + 1], ref, step_bound(T, arg), arg + 2.0 ** -20)
+
+
+def test_append_of_one_row_for_all_tokens_and_more_valid_than_there_are(sk):
+    """Rows of k and v may lie on one another; n_valid beyond the rows counts as all of them."""
+    cfg, cache, kws = small_cache(sk, 2, 2, 2, 128)
+    _, other, _ = small_cache(sk, 2, 2, 2, 128)
+    k, v = (torch.randn(2, 1, 2, 128, generator=gen(i)).half().cuda() for i in range(2))
+    first = torch.tensor([3, 60], dtype=torch.int32).cuda()
+    sk.kv4_append(cfg, cache, k.expand(2, 40, 2, 128), v.expand(2, 40, 2, 128), first, kws, n_valid=first * 0 + 1000)
+    sk.kv4_append(cfg, other, k.repeat(1, 40, 1, 1), v.repeat(1, 40, 1, 1), first, kws)
+    assert torch.equal(cache.pages, other.pages)
+    a, b = sk.kv4_read(cfg, cache, first, 40, kws, n_valid=first * 0 + 41), sk.kv4_read(cfg, cache, first, 40, kws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and kws.status() == (0, 0)
+
+
+def test_a_million_short_rows(sk, ws):
+    x = torch.randn(1 << 20, 50, generator=gen(1)).bfloat16()
+    tok = torch.randint(0, 50, (1 << 20,), generator=gen(2))
+    r = sk.token_logprobs(x.cuda(), tok.cuda(), ws, n_top=2)
+    want = torch.log_softmax(x.double(), -1)
+    # exponents of up to 13 with three roundings, 2^-22 of the exponential, 8 + 7 additions: 58 * 2^-24
+    assert (r.logprob.cpu().double() - want.gather(1, tok[:, None])[:, 0]).abs().max().item() <= 2.0 ** -18
+    ids = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :2]
+    assert torch.equal(r.top_ids.cpu().long(), ids)

@@ -38,3 +38,10 @@ from .kv4 import (  # noqa: F401
 )
 from .logprobs import TokenLogprobs, surprisal, token_logprobs  # noqa: F401
 from .rotary import RopePlan, rope  # noqa: F401
+from .states import (  # noqa: F401
+    StatesLogprobs,
+    StatesWorkspace,
+    states_logprobs,
+    states_logprobs_backward,
+    states_surprisal,
+)

@@ -25,6 +25,11 @@ bool encode_rows4d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
                    uint64_t row_elems, uint64_t rows, uint64_t groups, int elem_bytes,
                    uint32_t box_rows);
 
+// Rows of `inner` 16-bit elements, `stride` bytes apart, in boxes of box_inner elements by
+// box_rows rows, 128-byte swizzle, zeros beyond the ends.
+bool encode_rows2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
+                   uint64_t rows, uint64_t stride, uint32_t box_inner, uint32_t box_rows);
+
 // Launches a kernel that begins with follow_previous(): its blocks may be on their way
 // while the kernel before it on the stream still runs.
 template <typename Params>

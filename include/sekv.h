@@ -770,6 +770,73 @@ sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4_cache* cac
                                const int32_t* seq_len, float scale, float* out, float* lse,
                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Log-probabilities of tokens from a model's last states, without the logits.  Row r has the state
+ * h_r and the logits x_v = scale * h_r . w_v against the vocabulary matrix:
+ *   lse     = ln sum_v exp(x_v)
+ *   logprob = x_tok - lse              (minus the softmax cross entropy of the token)
+ * The products' operands are as given, their sums and all statistics fp32; no logit is stored.
+ *   dtype    bf16 or f16, of states and weight
+ *   states   row r at element r*state_stride, dim consecutive elements; weight likewise: row v
+ *            at v*weight_stride.  Both 16-byte aligned; dim and the strides multiples of 8, strides
+ *            at least dim (of a single row they mean nothing)
+ *   tokens   int32 or int64 (tokens_64), one a row, consecutive; -1: no token (logprob 0); any other
+ *            id outside [0, vocab) gives NaN and sets device code 1 (detail: the row)
+ *   scale    > 0, at most 2^127
+ *   logprob, lse   f32 [n_rows]; lse may be NULL
+ *   flags    SEKV_FLAG_SHORT_WAITS or 0
+ * A row with a NaN or +inf among its logits (times scale, as fp32 numbers to the base 2) gives
+ * NaN; a logit of -inf has probability 0; a row of nothing else has lse and logprob -inf.
+ *   workspace  of its own kind: sekv_states_workspace_size bytes, zeroed once (sekv_workspace_init),
+ *            256-byte aligned; calls of smaller sizes may use it too.  One stream at a time.
+ * n_rows 0 does nothing.  Rows are taken 8192 at a time.
+ */
+size_t sekv_states_workspace_size(int64_t n_rows, int64_t vocab, int64_t dim, int32_t backward);
+sekv_status sekv_states_logprobs(const void* states, int32_t dtype, int64_t n_rows, int64_t dim,
+                                 int64_t state_stride, const void* weight, int64_t vocab,
+                                 int64_t weight_stride, const void* tokens, int32_t tokens_64,
+                                 float scale, float* logprob, float* lse, int32_t flags,
+                                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * sekv_states_surprisal -- sekv_surprisal from last states: H f32 [batch][ctx_len], H_t = -log p of
+ * token t under the state of position t - 1, H[b][0] = 0.  Row b*ctx_len + t of states and tokens
+ * is position t of sequence b.  The last position's state is read and counts for nothing; token
+ * -1 gives 0.  Other arguments as above, scale 1.
+ */
+sekv_status sekv_states_surprisal(const void* states, int32_t dtype, int64_t batch,
+                                  int64_t ctx_len, int64_t dim, int64_t state_stride,
+                                  const void* weight, int64_t vocab, int64_t weight_stride,
+                                  const void* tokens, int32_t tokens_64, float* H, int32_t flags,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * sekv_states_logprobs_backward -- gradient of
+ *   sum_r grad_logprob[r] * logprob_r + grad_lse[r] * lse_r
+ * by the states and the weight, from the same states, weight, tokens and scale, and the lse that
+ * sekv_states_logprobs gave:
+ *   G_rv = scale ((grad_lse_r - grad_logprob_r) exp(x_rv - lse_r) + grad_logprob_r [v = tok_r])
+ *   d_states = G weight,  d_weight = G^T states
+ * The logits are made again, for one piece of the vocabulary at a time; G is held for that piece
+ * as numbers of dtype (f16: times a power of two that brings the largest factor on a row to
+ * 2^13 .. 2^14, so that an element below 2^-38 of that counts as 0), the sums are fp32 and rounded
+ * once.
+ *   grad_logprob, grad_lse   f32 [n_rows], either may be NULL (0)
+ *   d_states [n_rows][dim], d_weight [vocab][dim], dtype, dense, 16-byte aligned; either may be
+ *            NULL.  They must not overlap the inputs
+ * A row of token -1 has no logprob; a row whose two factors are 0 adds nothing to d_weight and has
+ * gradient 0, provided that its state is finite.  A token outside [0, vocab) makes its row's
+ * gradient, and what it adds to d_weight, NaN.  n_rows 0 sets d_weight to 0.  Deterministic.
+ */
+sekv_status sekv_states_logprobs_backward(const void* states, int32_t dtype, int64_t n_rows,
+                                          int64_t dim, int64_t state_stride, const void* weight,
+                                          int64_t vocab, int64_t weight_stride,
+                                          const void* tokens, int32_t tokens_64, float scale,
+                                          const float* lse, const float* grad_logprob,
+                                          const float* grad_lse, void* d_states, void* d_weight,
+                                          int32_t flags, void* workspace, size_t workspace_bytes,
+                                          cudaStream_t stream);
+
 /* Human-readable name of a status. */
 const char* sekv_status_string(sekv_status status);
 

@@ -538,6 +538,14 @@ sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t str
   return SEKV_OK;
 }
 
+// A pair of CTAs shares a tile of 256 rows where there are that many
+int ctas_of(int m) { return m > kRowsOfCta ? 2 : 1; }
+template <typename T, Mode MODE, bool AX, bool BX>
+sekv_status launch_for(TileParams& P, int32_t dtype, int sms, cudaStream_t stream) {
+  return ctas_of(P.m) == 2 ? launch_tiles<T, 2, MODE, AX, BX>(P, dtype, sms, stream)
+                           : launch_tiles<T, 1, MODE, AX, BX>(P, dtype, sms, stream);
+}
+
 // What the calls share: sizes, tensors and tokens.
 struct Call {
   const void* states;
@@ -599,11 +607,12 @@ sekv_status forward(const Call& c, float* logprob, float* lse, bool negate) {
     P.sums = reinterpret_cast<float2*>(c.ws + L.sums);
     P.ld = P.m;
     P.width = kColumns;
+    const int cg = ctas_of(P.m);
     const void* states = static_cast<const T*>(c.states) + r0 * c.state_stride;
     if (!map_rows(&P.a, c.dtype, states, c.dim, P.m, c.state_stride, kRowsOfCta) ||
-        !map_rows(&P.b, c.dtype, c.weight, c.dim, c.vocab, c.weight_stride, P.width))
+        !map_rows(&P.b, c.dtype, c.weight, c.dim, c.vocab, c.weight_stride, P.width / cg))
       return SEKV_ERR_UNSUPPORTED;
-    sekv_status st = launch_tiles<T, 1, kSums, false, false>(P, c.dtype, sms, c.stream);
+    sekv_status st = launch_for<T, kSums, false, false>(P, c.dtype, sms, c.stream);
     if (st != SEKV_OK) return st;
     JoinParams J{};
     J.sums = P.sums;
@@ -657,9 +666,9 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
     P.ld = piece;
     P.width = kColumns;
     if (!map_rows(&P.a, c.dtype, c.states, c.dim, c.rows, c.state_stride, kRowsOfCta) ||
-        !map_rows(&P.b, c.dtype, weight, c.dim, nv, c.weight_stride, P.width))
+        !map_rows(&P.b, c.dtype, weight, c.dim, nv, c.weight_stride, P.width / ctas_of(P.m)))
       return SEKV_ERR_UNSUPPORTED;
-    st = launch_tiles<T, 1, kGradient, false, false>(P, c.dtype, sms, c.stream);
+    st = launch_for<T, kGradient, false, false>(P, c.dtype, sms, c.stream);
     if (st == SEKV_OK && d_states) {  // G W, summed over the pieces
       TileParams Q = tile_params(c);
       Q.m = int(c.rows);
@@ -673,7 +682,7 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
       if (!map_rows(&Q.a, c.dtype, g, nv, c.rows, piece, kRowsOfCta) ||
           !map_rows(&Q.b, c.dtype, weight, c.dim, nv, c.weight_stride, kBlockK))
         return SEKV_ERR_UNSUPPORTED;
-      st = launch_tiles<T, 1, kProduct, false, true>(Q, c.dtype, sms, c.stream);
+      st = launch_for<T, kProduct, false, true>(Q, c.dtype, sms, c.stream);
     }
     if (st == SEKV_OK && d_weight) {  // G^T H
       TileParams Q = tile_params(c);
@@ -688,7 +697,7 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
       if (!map_rows(&Q.a, c.dtype, g, nv, c.rows, piece, kBlockK) ||
           !map_rows(&Q.b, c.dtype, c.states, c.dim, c.rows, c.state_stride, kBlockK))
         return SEKV_ERR_UNSUPPORTED;
-      st = launch_tiles<T, 1, kProduct, true, true>(Q, c.dtype, sms, c.stream);
+      st = launch_for<T, kProduct, true, true>(Q, c.dtype, sms, c.stream);
     }
   }
   return st;

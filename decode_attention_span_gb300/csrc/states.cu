@@ -31,6 +31,8 @@ constexpr int kEpilogueWarps = 4;
 constexpr int kThreads = (kEpilogueWarps + 2) * 32;
 constexpr uint64_t kStatesWaitNs = 2000000000ull;
 constexpr int64_t kRowsAtOnce = 8192;  // rows whose tiles' sums are kept at a time
+constexpr int kSplitCtas = 160;        // of a product whose sum over k is split, at most
+constexpr int kSplitBlocks = 8;        // of 64 in a share of k, at least
 constexpr int64_t kPiece = 8192;       // tokens of the vocabulary in a piece, at least
 
 template <int CG>
@@ -51,6 +53,7 @@ enum Mode { kSums, kGradient, kProduct };
 
 struct TileParams {
   CUtensorMap a, b;
+  CUtensorMap a_edge, b_edge;  // boxes of what is left at the ends (map_operand)
   int m, n, k;              // of the product
   int m_tiles, n_tiles, width;  // width: columns of a tile
   int n_first;              // neighbouring tiles share rows of A (1) or of B (0)
@@ -77,6 +80,7 @@ struct TileParams {
   float* acc;               // [m][n] sums of earlier pieces
   void* out;                // [m][n], or null: sums stay in acc
   int first;                // nothing in acc yet
+  int splits;               // shares of k; each has an acc of its own
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -162,7 +166,8 @@ __device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, 
   const bool none = on_p == 0.f && on_tok == 0.f;  // nothing of the row counts, whatever it holds
   const int hit = row < P.m && tok >= 0 && tok < held ? int(tok) : -1;
   T* g = static_cast<T*>(P.g) + int64_t(row) * P.ld + n0;
-  for (int c = 0; c < P.width; c += 32) {
+  // whole groups of 32, which a row of g has room for; beyond `held` it is not read
+  for (int c = 0; c < held; c += 32) {
     uint32_t r[32];
     tmem_load32(r, at + c);
     tmem_wait(r);
@@ -174,11 +179,6 @@ __device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, 
       for (int i = 0; i < 32; ++i)
         if (hit == c + i) x[i] += on_tok;
     }
-    if (c + 32 > held) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (c + i >= held) x[i] = 0.f;
-    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) r[i] = pack2(x[2 * i], x[2 * i + 1], T());
     if (row < P.m) {
@@ -189,10 +189,10 @@ __device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, 
 }
 
 template <typename T>
-__device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, int row, int n0) {
+__device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, int row, int n0, int split) {
   const int held = min(P.width, P.n - n0);  // a multiple of 8
-  const float down = P.unit ? 1.f / *P.unit : 1.f;
-  float* acc = P.acc + int64_t(row) * P.n + n0;
+  const float down = 1.f / *P.unit;
+  float* acc = P.acc + (int64_t(split) * P.m + row) * P.n + n0;
   T* out = static_cast<T*>(P.out) + int64_t(row) * P.n + n0;
   for (int c = 0; c < held; c += 32) {
     uint32_t r[32];
@@ -222,6 +222,68 @@ __device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, i
     }
   }
 }
+
+// What one block of k of an operand's tile brings into shared memory: `there` rows (ACROSS: columns, 64
+// to a box) by `k_held` of K.  The parts of a box that lie beyond a tensor's ends are slow to come
+// (128 rows of which one exists: 0.9 us, all of them: 0.2), so the ends have boxes of their own.  What is
+// left as it was in shared memory reaches rows and columns of the product that nothing reads; along
+// K, products stop at the last 16 that hold something, and what is left of those is zero.
+template <bool ACROSS>
+__device__ __forceinline__ uint32_t operand_bytes(int there, int k_held) {
+  return ACROSS ? uint32_t((there + 63) / 64 * ((k_held + 15) / 16)) * 2048u : uint32_t(there) * 128u;
+}
+template <bool ACROSS, bool PAIR, int MOST>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int x0, int there, int k0, uint32_t bar) {
+  if (ACROSS) {
+#pragma unroll
+    for (int i = 0; i < MOST; i += 64)
+      if (i < there) tma_g2s_2d<PAIR>(dst + i * 128, map, x0 + i, k0, bar);
+  } else if (there > 0) {
+    tma_g2s_2d<PAIR>(dst, map, k0, x0, bar);
+  }
+}
+// The tiles of a CTA (or pair) in turn: t, t + step, ..., without divisions on the way, which the
+// ring would run empty for (together 5% at 4096 x 128000 x 4096).  `inner` tiles are neighbours.
+struct Walk {
+  int t, step, inner, outer, split;
+  int d_inner, d_outer, d_split, n_inner, n_outer, each, more;
+  bool n_first;
+  __device__ __forceinline__ Walk(const TileParams& P, int first, int step_) : t(first), step(step_), n_first(P.n_first) {
+    n_inner = n_first ? P.n_tiles : P.m_tiles;
+    n_outer = n_first ? P.m_tiles : P.n_tiles;
+    inner = t % n_inner;
+    outer = t / n_inner % n_outer;
+    split = t / n_inner / n_outer;
+    d_inner = step % n_inner;
+    d_outer = step / n_inner % n_outer;
+    d_split = step / n_inner / n_outer;
+    const int blocks = (P.k + kBlockK - 1) / kBlockK;
+    each = blocks / P.splits;
+    more = blocks - each * P.splits;
+  }
+  __device__ __forceinline__ void next() {
+    t += step;
+    inner += d_inner;
+    outer += d_outer;
+    split += d_split;
+    if (inner >= n_inner) inner -= n_inner, ++outer;
+    if (outer >= n_outer) outer -= n_outer, ++split;
+  }
+  __device__ __forceinline__ int mt() const { return n_first ? outer : inner; }
+  __device__ __forceinline__ int nt() const { return n_first ? inner : outer; }
+  __device__ __forceinline__ int block(int s) const { return s * each + min(s, more); }  // first of share s of K
+};
+// A place in the ring and the parity of its barriers' phases
+template <int STAGES>
+struct Place {
+  uint32_t s = 0, odd = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == STAGES) {
+      s = 0;
+      odd ^= 1;
+    }
+  }
+};
 
 // A persistent kernel: one CTA an SM, or a pair of CTAs on two (CG 2), takes tiles of 128 CG rows and
 // `width` columns in turn.  One warp copies operands, one issues the products, four turn the finished
@@ -253,49 +315,53 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   const uint32_t tmem = sh.tmem;
   follow_previous();
 
-  const int tiles = P.m_tiles * P.n_tiles, step = gridDim.x / CG;
-  const int k_blocks = (P.k + kBlockK - 1) / kBlockK;
-  auto place = [&](int t, int& mt, int& nt) {
-    if (P.n_first) {
-      mt = t / P.n_tiles;
-      nt = t - mt * P.n_tiles;
-    } else {
-      nt = t / P.m_tiles;
-      mt = t - nt * P.m_tiles;
-    }
-  };
+  const int tiles = P.m_tiles * P.n_tiles * P.splits, step = gridDim.x / CG;
 
   if (warp == kEpilogueWarps) {
     if (lane == 0) {
       const int width = P.width / CG;  // of B's columns that this CTA brings
-      const uint32_t bytes = uint32_t(CG) * (kBytesA + width * kBlockK * 2);
+      const int k_rest = P.k % kBlockK;
+      const uint32_t whole_bytes = CG * (operand_bytes<AX>(kRowsOfCta, kBlockK) + operand_bytes<BX>(width, kBlockK));
+      const uint32_t whole_end = CG * (operand_bytes<AX>(kRowsOfCta, k_rest) + operand_bytes<BX>(width, k_rest));
+      const uint32_t full0 = CG == 2 ? peer_u32(&sh.full[0], 0) : smem_u32(&sh.full[0]), ring0 = smem_u32(sh.ring[0]);
+      Place<kStages> at;
       uint32_t done = 0;
       bool lost = false;
-      for (int t = blockIdx.x / CG; t < tiles && !lost; t += step) {
-        int mt, nt;
-        place(t, mt, nt);
-        const int m0 = mt * kRowsOfCta * CG + int(rank) * kRowsOfCta, n0 = nt * P.width + int(rank) * width;
-        for (int kb = 0; kb < k_blocks; ++kb, ++done) {
-          const uint32_t s = done % kStages;
-          if (!mbar_wait_parked(&sh.empty[s], (done / kStages & 1) ^ 1, P.wait_ns)) {
-            set_device_error(P.status, DEV_WAIT_TIMEOUT, 4);
-            lost = true;
-            break;
-          }
-          const uint32_t bar = CG == 2 ? peer_u32(&sh.full[s], 0) : smem_u32(&sh.full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], bytes);
-          const uint32_t a = smem_u32(sh.ring[s]), b = a + kBytesA;
-          if (AX) {
-            for (int i = 0; i < kRowsOfCta; i += 64) tma_g2s_2d<CG == 2>(a + i * 128, &P.a, m0 + i, kb * kBlockK, bar);
-          } else {
-            tma_g2s_2d<CG == 2>(a, &P.a, kb * kBlockK, m0, bar);
-          }
-          if (BX) {
-            for (int i = 0; i < width; i += 64) tma_g2s_2d<CG == 2>(b + i * 128, &P.b, n0 + i, kb * kBlockK, bar);
-          } else {
-            tma_g2s_2d<CG == 2>(b, &P.b, kb * kBlockK, n0, bar);
+      for (Walk w(P, blockIdx.x / CG, step); w.t < tiles && !lost; w.next()) {
+        const int k_end = w.block(w.split + 1);
+        const int m0 = w.mt() * kRowsOfCta * CG, n0 = w.nt() * P.width;
+        auto there = [](int x0, int extent, int limit) { return min(max(limit - x0, 0), extent); };
+        const int a0 = m0 + int(rank) * kRowsOfCta, b0 = n0 + int(rank) * width;
+        const int a_there = there(a0, kRowsOfCta, P.m), b_there = there(b0, width, P.n);
+        uint32_t bytes = whole_bytes, bytes_end = whole_end;  // of both CTAs
+        if (m0 + CG * kRowsOfCta > P.m || n0 + P.width > P.n) {
+          bytes = bytes_end = 0;
+#pragma unroll
+          for (int r = 0; r < CG; ++r) {
+            const int ta = there(m0 + r * kRowsOfCta, kRowsOfCta, P.m), tb = there(n0 + r * width, width, P.n);
+            bytes += operand_bytes<AX>(ta, kBlockK) + operand_bytes<BX>(tb, kBlockK);
+            bytes_end += operand_bytes<AX>(ta, k_rest) + operand_bytes<BX>(tb, k_rest);
           }
         }
+        auto bring = [&](int kb, const CUtensorMap* ma, const CUtensorMap* mb, uint32_t n) {
+          if (!mbar_wait_parked(&sh.empty[at.s], at.odd ^ 1, P.wait_ns)) {
+            set_device_error(P.status, DEV_WAIT_TIMEOUT, 4);
+            return false;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[at.s], n);
+          const uint32_t bar = full0 + at.s * 8, a = ring0 + at.s * Ring<CG>::kBytes;
+          load_operand<AX, CG == 2, kRowsOfCta>(a, ma, a0, a_there, kb * kBlockK, bar);
+          load_operand<BX, CG == 2, kColumns / CG>(a + kBytesA, mb, b0, b_there, kb * kBlockK, bar);
+          at.next();
+          ++done;
+          return true;
+        };
+        // across, the end of K has boxes of its own; along K, the last rows
+        const CUtensorMap *ma = AX || a_there == kRowsOfCta ? &P.a : &P.a_edge, *mb = BX || b_there == width ? &P.b : &P.b_edge;
+        int kb = w.block(w.split);
+        const int whole = min(k_end, P.k / kBlockK);
+        for (; kb < whole && !lost; ++kb) lost = !bring(kb, ma, mb, bytes);
+        if (kb < k_end && !lost) lost = !bring(kb, AX ? &P.a_edge : ma, BX ? &P.b_edge : mb, bytes_end);
       }
       // no copy may be in flight when the CTA ends
       if (rank == 0)
@@ -304,30 +370,40 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
   } else if (warp == kEpilogueWarps + 1) {
     if (rank == 0 && lane == 0) {
-      uint32_t done = 0, i = 0;
+      Place<kStages> at;
+      uint32_t i = 0;
       bool lost = false;
-      for (int t = blockIdx.x / CG; t < tiles && !lost; t += step, ++i) {
+      const uint64_t desc_a = tc_operand(smem_u32(sh.ring[0]), AX, 64 * 128), desc_b = tc_operand(smem_u32(sh.ring[0]) + kBytesA, BX, 64 * 128);
+      for (Walk w(P, blockIdx.x / CG, step); w.t < tiles && !lost; w.next(), ++i) {
         const uint32_t buf = i & 1;
         if (!mbar_wait_parked(&sh.acc_empty[buf], (i >> 1 & 1) ^ 1, P.wait_ns)) {
           set_device_error(P.status, DEV_WAIT_TIMEOUT, 5);
           break;
         }
         tc_fence_after();
-        for (int kb = 0; kb < k_blocks; ++kb, ++done) {
-          const uint32_t s = done % kStages;
-          if (!mbar_wait_parked(&sh.full[s], done / kStages & 1, P.wait_ns)) {
+        const int k_end = w.block(w.split + 1);
+        bool add = false;
+        auto multiply = [&](int steps) {
+          if (!mbar_wait_parked(&sh.full[at.s], at.odd, P.wait_ns)) {
             set_device_error(P.status, DEV_WAIT_TIMEOUT, 4);
-            lost = true;
-            break;
+            return false;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(sh.ring[s]), b = a + kBytesA;
+          const uint64_t a = desc_a + at.s * (Ring<CG>::kBytes / 16), b = desc_b + at.s * (Ring<CG>::kBytes / 16);
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k)
-            tc_mma<CG>(tmem + buf * kColumns, tc_operand(a + k * (AX ? 2048 : 32), AX, 64 * 128),
-                       tc_operand(b + k * (BX ? 2048 : 32), BX, 64 * 128), P.shape, kb + k > 0);
-          tc_commit<CG>(&sh.empty[s]);
-        }
+            if (k < steps) {
+              tc_mma<CG>(tmem + buf * kColumns, a + k * (AX ? 128 : 2), b + k * (BX ? 128 : 2), P.shape, add);
+              add = true;
+            }
+          tc_commit<CG>(&sh.empty[at.s]);
+          at.next();
+          return true;
+        };
+        int kb = w.block(w.split);
+        const int whole = min(k_end, P.k / kBlockK);
+        for (; kb < whole && !lost; ++kb) lost = !multiply(kBlockK / 16);
+        if (kb < k_end && !lost) lost = !multiply((P.k % kBlockK + 15) / 16);
         if (!lost) tc_commit<CG>(&sh.acc_full[buf]);
       }
       // nor may a product
@@ -336,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
   } else {
     uint32_t i = 0;
-    for (int t = blockIdx.x / CG; t < tiles; t += step, ++i) {
+    for (Walk w(P, blockIdx.x / CG, step); w.t < tiles; w.next(), ++i) {
       const uint32_t buf = i & 1;
       const bool there = mbar_wait_parked(&sh.acc_full[buf], i >> 1 & 1, P.wait_ns);
       if (!__all_sync(~0u, there)) {
@@ -344,16 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         break;
       }
       tc_fence_after();
-      int mt, nt;
-      place(t, mt, nt);
-      const int row = (mt * CG + int(rank)) * kRowsOfCta + warp * 32 + lane, n0 = nt * P.width;
+      const int row = (w.mt() * CG + int(rank)) * kRowsOfCta + warp * 32 + lane, n0 = w.nt() * P.width;
       const uint32_t at = tmem + buf * kColumns + (uint32_t(warp * 32) << 16);
       if constexpr (MODE == kSums)
-        tile_sums(P, at, row, nt, n0, min(P.width, P.n - n0));
+        tile_sums(P, at, row, w.nt(), n0, min(P.width, P.n - n0));
       else if constexpr (MODE == kGradient)
         tile_gradient<T>(P, at, row, n0);
       else
-        tile_product<T>(P, at, row, n0);
+        tile_product<T>(P, at, row, n0, w.split);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -468,6 +542,35 @@ __global__ void __launch_bounds__(1024) unit_kernel(const UnitParams P) {
   }
 }
 
+// Adds the shares of k in order, eight numbers a thread.
+struct AddParams {
+  const float* acc;
+  const float* unit;
+  void* out;
+  int64_t n;  // numbers of a share
+  int splits;
+};
+constexpr int kAddThreads = 128;
+template <typename T>
+__global__ void __launch_bounds__(kAddThreads) add_kernel(const AddParams P) {
+  follow_previous();
+  const int64_t i = (int64_t(blockIdx.x) * kAddThreads + threadIdx.x) * 8;
+  if (i >= P.n) return;
+  float x[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < P.splits; ++s) {
+    const float4 u = *reinterpret_cast<const float4*>(P.acc + s * P.n + i);
+    const float4 v = *reinterpret_cast<const float4*>(P.acc + s * P.n + i + 4);
+    x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+    x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+  }
+  const float down = 1.f / *P.unit;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] *= down;
+  *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + i) =
+      make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
+}
+
 // ---------------------------------------------------------------------- host
 struct StatesWs {
   size_t unit, at_token, sums, acc, g, total;
@@ -485,23 +588,30 @@ StatesWs states_ws(int64_t rows, int64_t vocab, int64_t dim, bool backward) {
   L.unit = 256;
   L.at_token = 512;
   L.sums = L.at_token + align256(size_t(at_once) * 4);
-  const size_t few = size_t((vocab + 127) / 128) * std::min<int64_t>(rows, kRowsOfCta) * 8;
+  const size_t few = size_t((vocab + 31) / 32) * std::min<int64_t>(rows, kRowsOfCta) * 8;
   const size_t many = size_t((vocab + kColumns - 1) / kColumns) * at_once * 8;
   const size_t forward = L.sums + align256(std::max(few, many));
   L.total = forward;
   if (backward) {
     L.acc = 512;
-    L.g = L.acc + align256(size_t(rows) * dim * 4);
+    L.g = L.acc + align256(std::max(size_t(rows) * dim, size_t(kSplitCtas) * kRowsOfCta * kColumns) * 4);
     const int64_t all = rows * round_up(vocab, kColumns);
     L.total = std::max(forward, L.g + align256(size_t(std::min(all, std::max(rows * kPiece, int64_t(1) << 27))) * 2));
   }
   return L;
 }
 
-// Rows of `inner` consecutive elements, `stride` elements apart, in boxes of 64 elements and `box` rows
-bool map_rows(CUtensorMap* map, int32_t dtype, const void* base, int64_t inner, int64_t rows, int64_t stride, int box) {
-  return encode_rows2d(map, dtype == SEKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base,
-                       uint64_t(inner), uint64_t(rows), uint64_t(rows > 1 ? stride : round_up(inner, 8)) * 2, kBlockK, uint32_t(box));
+// An operand: rows of `inner` consecutive elements, `stride` elements apart.  Along K (inner is K, rows are
+// the product's): boxes of `extent` rows, and of as many as are left at the end.  Across (rows are K): boxes
+// of 64 by 64, and at the end of K of what is left, in sixteens.
+bool map_operand(CUtensorMap* map, CUtensorMap* edge, int32_t dtype, bool across, const void* base, int64_t inner, int64_t rows,
+                 int64_t stride, int extent) {
+  const CUtensorMapDataType type = dtype == SEKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const uint64_t bytes = uint64_t(rows > 1 ? stride : round_up(inner, 8)) * 2;
+  const int whole = across ? kBlockK : extent, left = int(rows % whole);
+  const int rest = left == 0 ? whole : across ? int(round_up(left, 16)) : left;
+  return encode_rows2d(map, type, base, uint64_t(inner), uint64_t(rows), bytes, kBlockK, uint32_t(whole)) &&
+         encode_rows2d(edge, type, base, uint64_t(inner), uint64_t(rows), bytes, kBlockK, uint32_t(rest));
 }
 
 template <typename T, int CG, Mode MODE, bool AX, bool BX>
@@ -510,6 +620,7 @@ sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t str
   P.m_tiles = int((int64_t(P.m) + kRowsOfCta * CG - 1) / (kRowsOfCta * CG));
   P.n_tiles = (P.n + P.width - 1) / P.width;
   if (int64_t(P.m_tiles) * P.n_tiles > (1 << 30)) return SEKV_ERR_UNSUPPORTED;
+  P.splits = std::max(P.splits, 1);
   auto fn = tile_kernel<T, CG, MODE, AX, BX>;
   const size_t shared = sizeof(TileShared<CG>) + 1024;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared)) != cudaSuccess) {
@@ -517,7 +628,7 @@ sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t str
     return SEKV_ERR_CUDA;
   }
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(unsigned(std::min(P.m_tiles * P.n_tiles, sms / CG) * CG));
+  lc.gridDim = dim3(unsigned(std::min(P.m_tiles * P.n_tiles * P.splits, sms / CG) * CG));
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = shared;
   lc.stream = stream;
@@ -544,6 +655,15 @@ template <typename T, Mode MODE, bool AX, bool BX>
 sekv_status launch_for(TileParams& P, int32_t dtype, int sms, cudaStream_t stream) {
   return ctas_of(P.m) == 2 ? launch_tiles<T, 2, MODE, AX, BX>(P, dtype, sms, stream)
                            : launch_tiles<T, 1, MODE, AX, BX>(P, dtype, sms, stream);
+}
+
+// Columns of a tile of the logits.  Up to 128 rows the weight's bytes bound the product, and 224
+// columns are better where the tiles then fill their waves: 1 x 32000 x 4096 47.4 us for 47.9, 1 x
+// 128000 160 for 167; 128 columns 55 and 180.
+int width_of(int m, int64_t vocab, int sms) {
+  if (ctas_of(m) == 2) return kColumns;
+  auto time = [&](int w) { return ((vocab + w - 1) / w + sms - 1) / sms * w; };
+  return time(224) < time(kColumns) ? 224 : kColumns;
 }
 
 // What the calls share: sizes, tensors and tokens.
@@ -593,6 +713,27 @@ TileParams tile_params(const Call& c) {
   return P;
 }
 
+// The product of a gradient, rounded to `out` (or left in acc, where `out` is null: more pieces follow)
+template <typename T, bool AX, bool BX>
+sekv_status product(TileParams& P, const Call& c, int sms, bool may_split, bool last, void* out) {
+  const int cg = ctas_of(P.m);
+  // too few tiles for the GPU and a long sum: shares of it side by side
+  const int64_t tiles = int64_t((P.m - 1) / (kRowsOfCta * cg) + 1) * ((P.n - 1) / kColumns + 1);
+  P.splits = 1;
+  if (may_split && tiles * 2 * cg <= sms)
+    P.splits = std::max(1, std::min(std::min(sms, kSplitCtas) / int(tiles * cg), (P.k + kBlockK - 1) / kBlockK / kSplitBlocks));
+  P.out = last && P.splits == 1 ? out : nullptr;
+  sekv_status st = launch_for<T, kProduct, AX, BX>(P, c.dtype, sms, c.stream);
+  if (st != SEKV_OK || !last || P.splits == 1) return st;
+  AddParams A{};
+  A.acc = P.acc;
+  A.unit = P.unit;
+  A.out = out;
+  A.n = int64_t(P.m) * P.n;
+  A.splits = P.splits;
+  return launch_following(add_kernel<T>, dim3(unsigned((A.n / 8 + kAddThreads - 1) / kAddThreads)), kAddThreads, 0, c.stream, A);
+}
+
 template <typename T>
 sekv_status forward(const Call& c, float* logprob, float* lse, bool negate) {
   const int sms = device_sm_count();
@@ -606,11 +747,11 @@ sekv_status forward(const Call& c, float* logprob, float* lse, bool negate) {
     P.at_token = reinterpret_cast<float*>(c.ws + L.at_token);
     P.sums = reinterpret_cast<float2*>(c.ws + L.sums);
     P.ld = P.m;
-    P.width = kColumns;
+    P.width = width_of(P.m, c.vocab, sms);
     const int cg = ctas_of(P.m);
     const void* states = static_cast<const T*>(c.states) + r0 * c.state_stride;
-    if (!map_rows(&P.a, c.dtype, states, c.dim, P.m, c.state_stride, kRowsOfCta) ||
-        !map_rows(&P.b, c.dtype, c.weight, c.dim, c.vocab, c.weight_stride, P.width / cg))
+    if (!map_operand(&P.a, &P.a_edge, c.dtype, false, states, c.dim, P.m, c.state_stride, kRowsOfCta) ||
+        !map_operand(&P.b, &P.b_edge, c.dtype, false, c.weight, c.dim, c.vocab, c.weight_stride, P.width / cg))
       return SEKV_ERR_UNSUPPORTED;
     sekv_status st = launch_for<T, kSums, false, false>(P, c.dtype, sms, c.stream);
     if (st != SEKV_OK) return st;
@@ -664,9 +805,9 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
     P.unit = U.unit;
     P.g = g;
     P.ld = piece;
-    P.width = kColumns;
-    if (!map_rows(&P.a, c.dtype, c.states, c.dim, c.rows, c.state_stride, kRowsOfCta) ||
-        !map_rows(&P.b, c.dtype, weight, c.dim, nv, c.weight_stride, P.width / ctas_of(P.m)))
+    P.width = width_of(P.m, nv, sms);
+    if (!map_operand(&P.a, &P.a_edge, c.dtype, false, c.states, c.dim, c.rows, c.state_stride, kRowsOfCta) ||
+        !map_operand(&P.b, &P.b_edge, c.dtype, false, weight, c.dim, nv, c.weight_stride, P.width / ctas_of(P.m)))
       return SEKV_ERR_UNSUPPORTED;
     st = launch_for<T, kGradient, false, false>(P, c.dtype, sms, c.stream);
     if (st == SEKV_OK && d_states) {  // G W, summed over the pieces
@@ -678,11 +819,11 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
       Q.unit = U.unit;
       Q.acc = reinterpret_cast<float*>(c.ws + L.acc);
       Q.first = v0 == 0;
-      Q.out = v0 + piece >= c.vocab ? d_states : nullptr;
-      if (!map_rows(&Q.a, c.dtype, g, nv, c.rows, piece, kRowsOfCta) ||
-          !map_rows(&Q.b, c.dtype, weight, c.dim, nv, c.weight_stride, kBlockK))
+      if (!map_operand(&Q.a, &Q.a_edge, c.dtype, false, g, nv, c.rows, piece, kRowsOfCta) ||
+          !map_operand(&Q.b, &Q.b_edge, c.dtype, true, weight, c.dim, nv, c.weight_stride, kBlockK))
         return SEKV_ERR_UNSUPPORTED;
-      st = launch_for<T, kProduct, false, true>(Q, c.dtype, sms, c.stream);
+      // the shares of every piece have to be the same: the last, smaller one would have other
+      st = product<T, false, true>(Q, c, sms, piece >= c.vocab, v0 + piece >= c.vocab, d_states);
     }
     if (st == SEKV_OK && d_weight) {  // G^T H
       TileParams Q = tile_params(c);
@@ -693,11 +834,12 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
       Q.n_first = 1;
       Q.unit = U.unit;
       Q.first = 1;
-      Q.out = static_cast<T*>(d_weight) + v0 * c.dim;
-      if (!map_rows(&Q.a, c.dtype, g, nv, c.rows, piece, kBlockK) ||
-          !map_rows(&Q.b, c.dtype, c.states, c.dim, c.rows, c.state_stride, kBlockK))
+      Q.acc = reinterpret_cast<float*>(c.ws + L.acc);
+      if (!map_operand(&Q.a, &Q.a_edge, c.dtype, true, g, nv, c.rows, piece, kBlockK) ||
+          !map_operand(&Q.b, &Q.b_edge, c.dtype, true, c.states, c.dim, c.rows, c.state_stride, kBlockK))
         return SEKV_ERR_UNSUPPORTED;
-      st = launch_for<T, kProduct, true, true>(Q, c.dtype, sms, c.stream);
+      // with one piece acc is free again: d_states is done
+      st = product<T, true, true>(Q, c, sms, piece >= c.vocab, true, static_cast<T*>(d_weight) + v0 * c.dim);
     }
   }
   return st;

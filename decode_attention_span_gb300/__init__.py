@@ -34,7 +34,9 @@ from .kv4 import (  # noqa: F401
     alloc_kv4_pages,
     kv4_append,
     kv4_attention,
+    kv4_keep,
     kv4_read,
+    kv4_tree_attention,
 )
 from .logprobs import TokenLogprobs, surprisal, token_logprobs  # noqa: F401
 from .rotary import RopePlan, rope  # noqa: F401

@@ -111,7 +111,9 @@ static_assert(sizeof(JoinShared) <= sizeof(AttnShared::o), "the join's scratch l
 struct AttnParams {
   Kv4Pages pg;
   const void* q;
-  const int32_t* seq_len;
+  const int32_t* seq_len;  // of a tree: tokens before the drafted ones
+  const int64_t* tree;     // bit j of (b, i): drafted token i sees drafted token j
+  int64_t tree_stride;     // of a sequence
   float *out, *lse;
   float* partials;   // [CTA][2][kStateFloats]
   int32_t* arrived;  // per group; zero between calls
@@ -329,10 +331,15 @@ __device__ __forceinline__ void split_units(WarpState& S, const Query& Q, const 
 }
 
 // EDGE: some token of the chunk is not seen by some column (seen: per column of the
-// lane; held: tokens of the chunk that the sequence has).  PACK: only four columns are in
+// lane, the first tokens of the chunk, of a TREE a bit for each; held: tokens of the chunk that the
+// sequence has).  PACK: only four columns are in
 // use; columns 4-7 hold the same queries again, and their lanes put the weights' lower
 // parts in, so that one product does for both.
-template <bool EDGE, bool PACK>
+template <bool TREE>
+__device__ __forceinline__ bool sees(int seen, int i) {
+  return TREE ? uint32_t(seen) >> i & 1u : i < seen;
+}
+template <bool EDGE, bool PACK, bool TREE>
 __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const uint8_t* chunk,
                                            float4 (&par)[2][kChunkTokens], float4* kept,
                                            float4* units, float4* weights, bool any_kept, int lane,
@@ -391,7 +398,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
       if (EDGE)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if (ti * 16 + e * 8 + g >= seen[c]) x[ti][e][c] = -INFINITY;
+          if (!sees<TREE>(seen[c], ti * 16 + e * 8 + g)) x[ti][e][c] = -INFINITY;
     }
   }
 
@@ -467,7 +474,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           // a token that the column does not see has p 0, but may hold NaN
-          const bool ok = !EDGE || ti * 16 + e * 8 + g < seen[c];
+          const bool ok = !EDGE || sees<TREE>(seen[c], ti * 16 + e * 8 + g);
           if (!ok) w[c] = 0.f;
           S.c[c][gr] = ok ? fmaf(p[c], z, S.c[c][gr]) : S.c[c][gr];
         }
@@ -502,7 +509,7 @@ __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const u
   }
 }
 
-template <typename T, bool PACK>
+template <typename T, bool PACK, bool TREE>
 __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnParams P) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   AttnShared& sh = *reinterpret_cast<AttnShared*>(smem_raw);
@@ -521,7 +528,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
   if (warp == 0) {
     int sum = 0, longest = 1;
     for (int b = lane; b < P.batch; b += 32) {
-      const int given = P.seq_len[b];
+      int given = P.seq_len[b];
+      // drafted tokens without a place in the table are not attended to, nor any where the first has none
+      if (TREE && given >= 0) given = given < INT32_MAX - P.n_q ? given + P.n_q : INT32_MAX;
       const int len = min(max(given, 0), cap);
       if (given != len && blockIdx.x == 0) set_device_error(P.pg.status, DEV_BAD_LIST, b);
       sh.len[b] = len;
@@ -662,6 +671,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
     __syncthreads();
     Query Q;
     int see[2];  // tokens that columns 2t and 2t + 1 see
+    uint64_t tree[2];  // drafted ones among them
     Q.b = &sh.qb[0][lane];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -673,9 +683,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
       Q.scale_log2[c] = sh.q_scale[col];
       const int real = PACK ? col & 3 : col;
       see[c] = real < cols ? len - (P.n_q - 1 - (blk * P.tpb + real / P.hpg)) : 0;
+      if (TREE) tree[c] = real < cols ? uint64_t(P.tree[b * P.tree_stride + blk * P.tpb + real / P.hpg]) : 0;
     }
     // up to here no token is hidden from any column in use
-    const int open = len - (P.n_q - 1 - blk * P.tpb);
+    const int prefix = TREE ? min(max(P.seq_len[b], 0), cap) : 0;
+    const int open = TREE ? prefix : len - (P.n_q - 1 - blk * P.tpb);
 
     // the first copies; the queries' shuffles above do not wait behind them
     for (int k = 0; k < min(mine, kStages); ++k) issue(k);
@@ -702,12 +714,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) kv4_attn_kernel(const AttnPar
         if (__all_sync(~0u, mbar_wait_parked(&sh.bar[warp][st], ((done + k) / kStages) & 1, P.wait_ns))) {
           const int pos = (c0 + warp + k * kAttnWarps) * kChunkTokens;
           const int held = len - pos;
-          const int seen[2] = {see[0] - pos, see[1] - pos};
+          int seen[2] = {see[0] - pos, see[1] - pos};
+          if (TREE) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // tokens before the drafted ones, then those of the mask, of what the sequence has
+              const int ahead = prefix - pos;
+              const uint64_t bits = ahead > 0 ? (ahead < 32 ? tree[c] << ahead | ((1ull << ahead) - 1) : ~0ull)
+                                              : -ahead < 64 ? tree[c] >> -ahead : 0ull;
+              const int real = PACK ? (2 * t + c) & 3 : 2 * t + c;
+              seen[c] = real < cols ? int(uint32_t(bits) & (held < 32 ? (1u << max(held, 0)) - 1u : ~0u)) : 0;
+            }
+          }
           float4 *un = &sh.units[warp][lane], *wt = &sh.weights[warp][lane];
           if (pos + kChunkTokens <= open)
-            chunk_step<false, PACK>(S, Q, sh.ring[warp][st], sh.par[warp], kept, un, wt, k >= kFlush, lane, held, seen);
+            chunk_step<false, PACK, TREE>(S, Q, sh.ring[warp][st], sh.par[warp], kept, un, wt, k >= kFlush, lane, held, seen);
           else
-            chunk_step<true, PACK>(S, Q, sh.ring[warp][st], sh.par[warp], kept, un, wt, k >= kFlush, lane, held, seen);
+            chunk_step<true, PACK, TREE>(S, Q, sh.ring[warp][st], sh.par[warp], kept, un, wt, k >= kFlush, lane, held, seen);
         } else {
           // a copy did not land: nothing more is copied or waited for by this warp, and
           // what is still in flight gets its time to land before the CTA may end
@@ -967,11 +990,11 @@ sekv_status kv4_check_ws(const sekv_config* cfg, int n_q, size_t workspace_bytes
 
 }  // namespace sekv
 
-extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4_cache* cache,
-                                          int32_t dtype, const void* q, int32_t n_q,
-                                          const int32_t* seq_len, float scale, float* out,
-                                          float* lse, void* workspace, size_t workspace_bytes,
-                                          cudaStream_t stream) {
+namespace {
+
+sekv_status attention(const sekv_config* cfg, const sekv_kv4_cache* cache, int32_t dtype, const void* q, int32_t n_q,
+                      const int32_t* seq_len, const int64_t* tree, int64_t tree_stride, float scale, float* out, float* lse,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   reset_launches();
   sekv_status st = kv4_check(cfg, cache, n_q, workspace);
   if (st != SEKV_OK) return st;
@@ -997,6 +1020,8 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
   P.pg.hkv = cfg->n_kv_heads;
   P.q = q;
   P.seq_len = seq_len;
+  P.tree = tree;
+  P.tree_stride = tree_stride;
   P.out = out;
   P.lse = lse;
   P.arrived = reinterpret_cast<int32_t*>(w + L.arrived);
@@ -1009,14 +1034,37 @@ extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4
   P.n_blk = blocks_of(cfg, n_q);
   P.scale_log2 = scale * kLog2e;
   const bool pack = n_q * P.hpg <= kCols / 2;
-  void (*const fns[4])(AttnParams) = {
-      kv4_attn_kernel<__nv_bfloat16, false>, kv4_attn_kernel<__half, false>,
-      kv4_attn_kernel<__nv_bfloat16, true>, kv4_attn_kernel<__half, true>};
-  void (*const fn)(AttnParams) = fns[(dtype == SEKV_BF16 ? 0 : 1) + (pack ? 2 : 0)];
+  void (*const fns[8])(AttnParams) = {
+      kv4_attn_kernel<__nv_bfloat16, false, false>, kv4_attn_kernel<__half, false, false>,
+      kv4_attn_kernel<__nv_bfloat16, true, false>,  kv4_attn_kernel<__half, true, false>,
+      kv4_attn_kernel<__nv_bfloat16, false, true>,  kv4_attn_kernel<__half, false, true>,
+      kv4_attn_kernel<__nv_bfloat16, true, true>,   kv4_attn_kernel<__half, true, true>};
+  void (*const fn)(AttnParams) = fns[(dtype == SEKV_BF16 ? 0 : 1) + (pack ? 2 : 0) + (tree ? 4 : 0)];
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AttnShared)) !=
       cudaSuccess) {
     cudaGetLastError();
     return SEKV_ERR_CUDA;
   }
   return launch_following(fn, dim3(sms), kAttnThreads, sizeof(AttnShared), stream, P);
+}
+
+}  // namespace
+
+extern "C" sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4_cache* cache,
+                                          int32_t dtype, const void* q, int32_t n_q,
+                                          const int32_t* seq_len, float scale, float* out,
+                                          float* lse, void* workspace, size_t workspace_bytes,
+                                          cudaStream_t stream) {
+  return attention(cfg, cache, dtype, q, n_q, seq_len, nullptr, 0, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" sekv_status sekv_kv4_tree_attention(const sekv_config* cfg, const sekv_kv4_cache* cache,
+                                               int32_t dtype, const void* q, int32_t n_q,
+                                               const int32_t* first, const int64_t* tree,
+                                               int64_t tree_stride_b, float scale, float* out,
+                                               float* lse, void* workspace,
+                                               size_t workspace_bytes, cudaStream_t stream) {
+  reset_launches();
+  if (!tree || reinterpret_cast<uintptr_t>(tree) % 8 || tree_stride_b < 0) return SEKV_ERR_INVALID;
+  return attention(cfg, cache, dtype, q, n_q, first, tree, tree_stride_b, scale, out, lse, workspace, workspace_bytes, stream);
 }

@@ -294,6 +294,63 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StorePara
   }
 }
 
+// sekv_kv4_keep: a block moves the kept tokens of one (sequence, KV head).  A warp takes every
+// kKeepWarps-th of them; all are read before any is written, because a place may be filled whose token
+// moves too.  A few hundred bytes a block: its time is that of a chain of four loads (list, table,
+// codes) and a launch.
+constexpr int kKeepWarps = 8;
+struct KeepParams {
+  Kv4Pages pg;
+  const int32_t *first, *keep, *n_keep;
+  int most;
+};
+__global__ void __launch_bounds__(kKeepWarps * 32) kv4_keep_kernel(const KeepParams P) {
+  constexpr int kEach = SEKV_MAX_QUERY_TOKENS / kKeepWarps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  follow_previous();
+  const int b = blockIdx.x / P.pg.hkv, c = blockIdx.x % P.pg.hkv;
+  const int n = min(P.n_keep ? P.n_keep[b] : P.most, P.most);
+  const int32_t* keep = P.keep + int64_t(b) * P.most;
+  bool bad = false;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) bad |= keep[i] <= (i > 0 ? keep[i - 1] : -1);
+  const int64_t first = P.first[b];
+  if (__syncthreads_or(bad || (n > 0 && first < 0))) {
+    if (threadIdx.x == 0) set_device_error(P.pg.status, DEV_BAD_LIST, b);
+    return;
+  }
+  // lane: a word of K's codes (0 - 15), two bytes of V's, a scale and zero (0 - 3: K's, V's)
+  const int k_at = lane * 4, v_at = kKv4V + 64 * (lane >> 2) + 8 * (lane >> 1 & 1) + 4 * (lane & 1);
+  uint8_t* to[kEach];
+  uint32_t k[kEach], sz[kEach];
+  uint16_t v[kEach];
+  auto v_of = [&](int j) { return v_at + 512 * (j >> 3) + 16 * ((j & 7) >> 1) + 2 * (j & 1); };
+  auto sz_of = [&](int j) { return kv4_param(j, lane & 1, lane >> 1); };
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int at = i * warps + warp;
+    to[i] = nullptr;
+    if (i * warps >= n) continue;  // for all warps, whichever have tokens
+    if (at >= n || keep[at] == at) continue;
+    const int64_t src = first + keep[at];
+    const uint8_t* from = P.pg.tile(b, c, src);
+    to[i] = from ? P.pg.tile(b, c, first + at) : nullptr;
+    if (!to[i]) continue;
+    const int j = int(src % kKv4Tile);
+    if (lane < 16) k[i] = *reinterpret_cast<const uint32_t*>(from + 64 * j + k_at);
+    v[i] = *reinterpret_cast<const uint16_t*>(from + v_of(j));
+    if (lane < 4) sz[i] = *reinterpret_cast<const uint32_t*>(from + sz_of(j));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (!to[i]) continue;
+    const int j = int((first + i * warps + warp) % kKv4Tile);
+    if (lane < 16) *reinterpret_cast<uint32_t*>(to[i] + 64 * j + k_at) = k[i];
+    *reinterpret_cast<uint16_t*>(to[i] + v_of(j)) = v[i];
+    if (lane < 4) *reinterpret_cast<uint32_t*>(to[i] + sz_of(j)) = sz[i];
+  }
+}
+
 StoreParams store_params(const sekv_config* cfg, const sekv_kv4_cache* cache, int32_t n_tokens,
                          const int32_t* first, const int32_t* n_valid, void* workspace) {
   StoreParams P{};
@@ -372,4 +429,26 @@ extern "C" sekv_status sekv_kv4_read(const sekv_config* cfg, const sekv_kv4_cach
                           : dtype == SEKV_F16 ? kv4_read_kernel<__half>
                                               : kv4_read_kernel<float>,
                           dim3(blocks), kStoreThreads, 0, stream, P);
+}
+
+extern "C" sekv_status sekv_kv4_keep(const sekv_config* cfg, const sekv_kv4_cache* cache,
+                                     const int32_t* first, const int32_t* keep, int32_t n_tokens,
+                                     const int32_t* n_keep, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream) {
+  reset_launches();
+  sekv_status st = kv4_check(cfg, cache, 1, workspace);
+  if (st != SEKV_OK) return st;
+  if (!first || (!keep && n_tokens != 0) || n_tokens < 0) return SEKV_ERR_INVALID;
+  if (n_tokens > SEKV_MAX_QUERY_TOKENS) return SEKV_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return SEKV_OK;
+  st = kv4_check_ws(cfg, 1, workspace_bytes);
+  if (st != SEKV_OK) return st;
+  KeepParams P{};
+  P.pg = store_params(cfg, cache, n_tokens, first, nullptr, workspace).pg;
+  P.first = first;
+  P.keep = keep;
+  P.n_keep = n_keep;
+  P.most = n_tokens;
+  const int threads = 32 * (n_tokens < kKeepWarps ? n_tokens : kKeepWarps);
+  return launch_following(kv4_keep_kernel, dim3(unsigned(cfg->batch * cfg->n_kv_heads)), threads, 0, stream, P);
 }

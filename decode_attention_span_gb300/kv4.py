@@ -136,12 +136,8 @@ def kv4_read(cfg: Config, cache: Kv4Cache, first, n_tokens: int, ws: Workspace,
     return k, v
 
 
-def kv4_attention(cfg: Config, cache: Kv4Cache, q, seq_len, scale: float, ws: Workspace,
-                  out=None, lse=None, stream=None):
-    """Attention of q [B][n_q][Hq][128] (bf16 or f16) over the first seq_len[b] cached
-    tokens of each sequence, the query tokens being its last n_q; returns out
-    [B][n_q][Hq][128] f32 and lse [B][n_q][Hq] f32."""
-    index = _common(cfg, cache, ws)
+def _queries(cfg, cache, q, out, lse, index, stream):
+    """(out, lse) of queries [B][n_q][Hq][128], made here where not given."""
     check_tensor(q, "q", _HALF, index)
     shape = q.shape
     if len(shape) != 4 or shape[0] != cfg.batch or shape[2] != cfg.n_q_heads or \
@@ -162,10 +158,62 @@ def kv4_attention(cfg: Config, cache: Kv4Cache, q, seq_len, scale: float, ws: Wo
         check_tensor(lse, "lse", _F32, index)
         if lse.shape != shape[:3] or not lse.is_contiguous():
             raise ValueError(f"lse: expected contiguous {tuple(shape[:3])}")
+    return out, lse
+
+
+def kv4_attention(cfg: Config, cache: Kv4Cache, q, seq_len, scale: float, ws: Workspace,
+                  out=None, lse=None, stream=None):
+    """Attention of q [B][n_q][Hq][128] (bf16 or f16) over the first seq_len[b] cached
+    tokens of each sequence, the query tokens being its last n_q; returns out
+    [B][n_q][Hq][128] f32 and lse [B][n_q][Hq] f32."""
+    index = _common(cfg, cache, ws)
+    out, lse = _queries(cfg, cache, q, out, lse, index, stream)
     s = _per_seq(seq_len, "seq_len", cfg, index)
     st = lib().sekv_kv4_attention(ctypes.byref(cfg.c()), cache._c, DTYPES[q.dtype], q.data_ptr(),
-                                  shape[1], s, scale, out.data_ptr(), lse.data_ptr(),
+                                  q.shape[1], s, scale, out.data_ptr(), lse.data_ptr(),
                                   ws.buf.data_ptr(), ws.nbytes, raw_stream(stream, index))
     if st != 0:
         _check("sekv_kv4_attention", st)
     return out, lse
+
+
+_I64 = (torch.int64,)
+
+
+def kv4_tree_attention(cfg: Config, cache: Kv4Cache, q, first, tree, scale: float, ws: Workspace,
+                       out=None, lse=None, stream=None):
+    """Attention of a tree of drafted tokens: q [B][n_q][Hq][128] (bf16 or f16), stored at positions
+    first[b] .. first[b] + n_q - 1, over the first[b] tokens before them and, of the drafted ones, over
+    those of the bits of `tree` (int64 [B][n_q], or [n_q] for all sequences: bit j of entry i lets
+    token i see token j).  Returns out and lse as kv4_attention does."""
+    index = _common(cfg, cache, ws)
+    out, lse = _queries(cfg, cache, q, out, lse, index, stream)
+    n = q.shape[1]
+    check_tensor(tree, "tree", _I64, index)
+    if tree.shape not in ((cfg.batch, n), (n,)) or not tree.is_contiguous():
+        raise ValueError(f"tree: expected contiguous [{cfg.batch}][{n}] or [{n}], got "
+                         f"{tuple(tree.shape)}")
+    f = _per_seq(first, "first", cfg, index)
+    st = lib().sekv_kv4_tree_attention(ctypes.byref(cfg.c()), cache._c, DTYPES[q.dtype],
+                                       q.data_ptr(), n, f, tree.data_ptr(),
+                                       n if tree.dim() == 2 else 0, scale, out.data_ptr(),
+                                       lse.data_ptr(), ws.buf.data_ptr(), ws.nbytes,
+                                       raw_stream(stream, index))
+    if st != 0:
+        _check("sekv_kv4_tree_attention", st)
+    return out, lse
+
+
+def kv4_keep(cfg: Config, cache: Kv4Cache, first, keep, n_keep, ws: Workspace, stream=None):
+    """Keeps a branch of the drafted tokens: token first[b] + keep[b][i] moves to first[b] + i, for
+    i < n_keep[b] (None: all); keep int32 [B][n] (n at most 64), ascending."""
+    index = _common(cfg, cache, ws)
+    check_tensor(keep, "keep", _I32, index)
+    if keep.dim() != 2 or keep.shape[0] != cfg.batch or not keep.is_contiguous():
+        raise ValueError(f"keep: expected contiguous [{cfg.batch}][n], got {tuple(keep.shape)}")
+    f = _per_seq(first, "first", cfg, index)
+    n = None if n_keep is None else _per_seq(n_keep, "n_keep", cfg, index)
+    st = lib().sekv_kv4_keep(ctypes.byref(cfg.c()), cache._c, f, keep.data_ptr(), keep.shape[1], n,
+                             ws.buf.data_ptr(), ws.nbytes, raw_stream(stream, index))
+    if st != 0:
+        _check("sekv_kv4_keep", st)

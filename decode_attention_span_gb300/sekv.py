@@ -40,6 +40,7 @@ EXPORTS = ("sekv_record_size", "sekv_workspace_size", "sekv_workspace_init",
            "sekv_maint_init", "sekv_append_token", "sekv_maint_flush",
            "sekv_token_logprobs", "sekv_surprisal", "sekv_rope_freqs", "sekv_rope",
            "sekv_kv4_append", "sekv_kv4_read", "sekv_kv4_attention",
+           "sekv_kv4_tree_attention", "sekv_kv4_keep",
            "sekv_states_workspace_size", "sekv_states_logprobs", "sekv_states_surprisal",
            "sekv_states_logprobs_backward",
            "sekv_status_string", "sekv_last_launch_count")
@@ -181,6 +182,11 @@ def lib() -> ctypes.CDLL:
         L.sekv_kv4_attention.restype = _c_i32
         L.sekv_kv4_attention.argtypes = [_c_vp, _c_vp, _c_i32, _c_vp, _c_i32, _c_vp, _c_f32,
                                          _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]
+        L.sekv_kv4_tree_attention.restype = _c_i32
+        L.sekv_kv4_tree_attention.argtypes = [_c_vp, _c_vp, _c_i32, _c_vp, _c_i32, _c_vp, _c_vp,
+                                              _c_i64, _c_f32, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]
+        L.sekv_kv4_keep.restype = _c_i32
+        L.sekv_kv4_keep.argtypes = [_c_vp, _c_vp, _c_vp, _c_vp, _c_i32, _c_vp, _c_vp, _c_sz, _c_vp]
         L.sekv_states_workspace_size.restype = _c_sz
         L.sekv_states_workspace_size.argtypes = [_c_i64, _c_i64, _c_i64, _c_i32]
         L.sekv_states_logprobs.restype = _c_i32

@@ -770,6 +770,33 @@ sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4_cache* cac
                                const int32_t* seq_len, float scale, float* out, float* lse,
                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* sekv_kv4_tree_attention -- sekv_kv4_attention of a tree of drafted tokens.  Drafted token i of
+ * sequence b is stored at position first[b] + i (sekv_kv4_append with the same first) and attends to
+ * all tokens before first[b] and to the drafted tokens j of bit j of tree[b*tree_stride_b + i]:
+ * its ancestors and itself, as a rule; any set may be given, bits from n_q on count for nothing.
+ *   first  int32 [batch] (device);  tree  int64 (device), n_q entries a sequence; stride 0: one tree
+ *          for all.  A negative first sets device code 1 (detail: the sequence) and its tokens see
+ *          nothing
+ * The other arguments, the workspace (ctx_len: n_q), limits and accuracy are sekv_kv4_attention's; a
+ * token that sees nothing has out 0 and lse -inf. */
+sekv_status sekv_kv4_tree_attention(const sekv_config* cfg, const sekv_kv4_cache* cache,
+                                    int32_t dtype, const void* q, int32_t n_q,
+                                    const int32_t* first, const int64_t* tree,
+                                    int64_t tree_stride_b, float scale, float* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* sekv_kv4_keep -- keeps a branch of the drafted tokens: what position first[b] + keep[b][i] holds
+ * (codes, scales and zeros as they are) moves to first[b] + i, for i < n_keep[b].
+ *   keep    int32 [batch][n_tokens] (device): strictly ascending from 0 on; entries from n_keep[b]
+ *           on are not read.  n_tokens at most SEKV_MAX_QUERY_TOKENS
+ *   n_keep  int32 [batch] (device) or NULL: n_tokens for all
+ * A list that does not ascend, or a negative first, sets device code 1 (detail: the sequence) and
+ * moves nothing of the sequence; a token whose page is not in the pool is not moved. */
+sekv_status sekv_kv4_keep(const sekv_config* cfg, const sekv_kv4_cache* cache,
+                          const int32_t* first, const int32_t* keep, int32_t n_tokens,
+                          const int32_t* n_keep, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
 /*
  * Log-probabilities of tokens from a model's last states, without the logits.  Row r has the state
  * h_r and the logits x_v = scale * h_r . w_v against the vocabulary matrix:

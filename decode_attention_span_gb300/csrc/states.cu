@@ -27,7 +27,9 @@ constexpr int kRowsOfCta = 128;  // lanes of tensor memory
 constexpr int kBlockK = 64;      // 128 bytes of an operand's row
 constexpr int kColumns = 256;    // of an accumulator; two of them fill tensor memory
 constexpr int kBytesA = kRowsOfCta * kBlockK * 2;
-constexpr int kEpilogueWarps = 4;
+constexpr int kEpilogueWarps = 8;  // two for each 32 lanes, half of the columns each
+constexpr int kHalf = kColumns / 2;
+constexpr int kSegment = 16;       // blocks of K that one accumulator of the loss sums
 constexpr int kThreads = (kEpilogueWarps + 2) * 32;
 constexpr uint64_t kStatesWaitNs = 2000000000ull;
 constexpr int64_t kRowsAtOnce = 8192;  // rows whose tiles' sums are kept at a time
@@ -67,7 +69,7 @@ struct TileParams {
   int64_t token_period;     // sequences' lengths where the last row of each has no token; 0: all do
   int64_t row0;             // of the call
   float factor;             // on products, logits to the base 2
-  float2* sums;             // [n_tiles][ld]: reference (log2), sum
+  float2* sums;             // [n_tiles][ld][2]: reference (log2), sum of a tile's halves
   float* at_token;          // [rows]: the token's logit, base 2
   int64_t ld;
   // kGradient
@@ -106,49 +108,45 @@ __device__ __forceinline__ int64_t token_of(const void* tokens, int wide, int64_
   return wide ? static_cast<const int64_t*>(tokens)[r + skip] : static_cast<const int32_t*>(tokens)[r + skip];
 }
 
-// One tile of kSums: this thread's row.
-__device__ __forceinline__ void tile_sums(const TileParams& P, uint32_t at, int row, int tile, int n0, int held) {
-  float ref = -INFINITY, sum = 0.f;
+// One tile of kSums: this thread's row and half of the columns, `x` their products.
+__device__ __forceinline__ void tile_sums(const TileParams& P, float (&x)[kHalf], int row, int tile, int half, int n0, int held) {
   int64_t tok = -1;
   if (row < P.m) tok = token_of(P.tokens, P.tokens_64, P.token_skip, P.token_period, P.row0 + row) - n0;
   const int hit = tok >= 0 && tok < held ? int(tok) : -1;
-  for (int c = 0; c < held; c += 32) {
-    uint32_t r[32];
-    tmem_load32(r, at + c);
-    tmem_wait(r);
-    if (c + 32 > held) {
+  if (__any_sync(~0u, hit >= 0)) {
+    float at = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (c + i >= held) r[i] = 0xff800000u;  // -infinity
-    }
-    float mx = __uint_as_float(r[0]);
-#pragma unroll
-    for (int i = 1; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
-    const float up = fmaxf(ref, mx * P.factor);
-    const float from = up == -INFINITY ? 0.f : up;
-    sum *= ex2(ref - from);
-    ref = up;
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      s0 += ex2(fmaf(__uint_as_float(r[i]), P.factor, -from));
-      s1 += ex2(fmaf(__uint_as_float(r[i + 1]), P.factor, -from));
-    }
-    sum += s0 + s1;
-    if (__any_sync(~0u, hit >= c && hit < c + 32)) {
-      float x = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (hit == c + i) x = __uint_as_float(r[i]);
-      if (hit >= c && hit < c + 32) P.at_token[row] = x * P.factor;
-    }
+    for (int i = 0; i < kHalf; ++i)
+      if (hit == i) at = x[i];
+    if (hit >= 0) P.at_token[row] = at * P.factor;
   }
-  if (row < P.m) P.sums[int64_t(tile) * P.ld + row] = make_float2(ref, sum);
+  if (held < kHalf) {
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i)
+      if (i >= held) x[i] = -INFINITY;
+  }
+  float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int i = 4; i < kHalf; ++i) mx[i % 4] = fmaxf(mx[i % 4], x[i]);
+  const float ref = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.factor;
+  const float from = ref == -INFINITY ? 0.f : ref;
+  Pair s0(0.f, 0.f), s1(0.f, 0.f);
+  const Pair by(P.factor, P.factor), less(-from, -from);
+#pragma unroll
+  for (int i = 0; i < kHalf; i += 4) {
+    float e[4];
+    fma2(Pair(x[i], x[i + 1]), by, less).get(e[0], e[1]);
+    fma2(Pair(x[i + 2], x[i + 3]), by, less).get(e[2], e[3]);
+    s0 = add2(s0, Pair(ex2(e[0]), ex2(e[1])));
+    s1 = add2(s1, Pair(ex2(e[2]), ex2(e[3])));
+  }
+  float a, b;
+  add2(s0, s1).get(a, b);
+  if (row < P.m) P.sums[(int64_t(tile) * P.ld + row) * 2 + half] = make_float2(ref, a + b);
 }
 
 template <typename T>
-__device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, int row, int n0) {
-  const int held = min(P.width, P.n - n0);
+__device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, int row, int n0, int held) {
   float on_p = 0.f, on_tok = 0.f, lse = 0.f;
   int64_t tok = -1;
   if (row < P.m) {
@@ -189,12 +187,11 @@ __device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, 
 }
 
 template <typename T>
-__device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, int row, int n0, int split) {
-  const int held = min(P.width, P.n - n0);  // a multiple of 8
+__device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, int row, int n0, int held, int split) {
   const float down = 1.f / *P.unit;
   float* acc = P.acc + (int64_t(split) * P.m + row) * P.n + n0;
   T* out = static_cast<T*>(P.out) + int64_t(row) * P.n + n0;
-  for (int c = 0; c < held; c += 32) {
+  for (int c = 0; c < held; c += 32) {  // held: a multiple of 8
     uint32_t r[32];
     tmem_load32(r, at + c);
     tmem_wait(r);
@@ -375,14 +372,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       bool lost = false;
       const uint64_t desc_a = tc_operand(smem_u32(sh.ring[0]), AX, 64 * 128), desc_b = tc_operand(smem_u32(sh.ring[0]) + kBytesA, BX, 64 * 128);
       for (Walk w(P, blockIdx.x / CG, step); w.t < tiles && !lost; w.next(), ++i) {
-        const uint32_t buf = i & 1;
-        if (!mbar_wait_parked(&sh.acc_empty[buf], (i >> 1 & 1) ^ 1, P.wait_ns)) {
-          set_device_error(P.status, DEV_WAIT_TIMEOUT, 5);
-          break;
-        }
-        tc_fence_after();
         const int k_end = w.block(w.split + 1);
+        uint32_t buf = 0;
         bool add = false;
+        auto open = [&]() {  // the next accumulator
+          buf = i & 1;
+          add = false;
+          if (!mbar_wait_parked(&sh.acc_empty[buf], (i >> 1 & 1) ^ 1, P.wait_ns)) {
+            set_device_error(P.status, DEV_WAIT_TIMEOUT, 5);
+            return false;
+          }
+          tc_fence_after();
+          return true;
+        };
         auto multiply = [&](int steps) {
           if (!mbar_wait_parked(&sh.full[at.s], at.odd, P.wait_ns)) {
             set_device_error(P.status, DEV_WAIT_TIMEOUT, 4);
@@ -402,9 +404,22 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         };
         int kb = w.block(w.split);
         const int whole = min(k_end, P.k / kBlockK);
-        for (; kb < whole && !lost; ++kb) lost = !multiply(kBlockK / 16);
-        if (kb < k_end && !lost) lost = !multiply((P.k % kBlockK + 15) / 16);
-        if (!lost) tc_commit<CG>(&sh.acc_full[buf]);
+        if (MODE == kSums) {
+          // an accumulator for each kSegment blocks
+          while (kb < k_end && !lost) {
+            const int end = min(kb + kSegment, k_end), end_whole = min(end, whole);
+            lost = !open();
+            for (; kb < end_whole && !lost; ++kb) lost = !multiply(kBlockK / 16);
+            for (; kb < end && !lost; ++kb) lost = !multiply((P.k % kBlockK + 15) / 16);
+            if (!lost) tc_commit<CG>(&sh.acc_full[buf]);
+            if (kb < k_end) ++i;
+          }
+        } else {
+          lost = !open();
+          for (; kb < whole && !lost; ++kb) lost = !multiply(kBlockK / 16);
+          if (kb < k_end && !lost) lost = !multiply((P.k % kBlockK + 15) / 16);
+          if (!lost) tc_commit<CG>(&sh.acc_full[buf]);
+        }
       }
       // nor may a product
       tc_commit<CG>(&sh.drained);
@@ -412,29 +427,69 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
   } else {
     uint32_t i = 0;
-    for (Walk w(P, blockIdx.x / CG, step); w.t < tiles; w.next(), ++i) {
-      const uint32_t buf = i & 1;
-      const bool there = mbar_wait_parked(&sh.acc_full[buf], i >> 1 & 1, P.wait_ns);
-      if (!__all_sync(~0u, there)) {
+    bool lost = false;
+    const int half = warp / 4 * kHalf;
+    const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
+    auto take = [&]() {  // the next accumulator, when it is full
+      if (!__all_sync(~0u, mbar_wait_parked(&sh.acc_full[i & 1], i >> 1 & 1, P.wait_ns))) {
         if (lane == 0) set_device_error(P.status, DEV_WAIT_TIMEOUT, 7);
-        break;
+        lost = true;
       }
       tc_fence_after();
-      const int row = (w.mt() * CG + int(rank)) * kRowsOfCta + warp * 32 + lane, n0 = w.nt() * P.width;
-      const uint32_t at = tmem + buf * kColumns + (uint32_t(warp * 32) << 16);
-      if constexpr (MODE == kSums)
-        tile_sums(P, at, row, w.nt(), n0, min(P.width, P.n - n0));
-      else if constexpr (MODE == kGradient)
-        tile_gradient<T>(P, at, row, n0);
-      else
-        tile_product<T>(P, at, row, n0, w.split);
+      return tmem + (i & 1) * kColumns + lanes + half;
+    };
+    auto give = [&]() {  // it is free again
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if constexpr (CG == 2)
-          mbar_arrive_cluster(peer_u32(&sh.acc_empty[buf], 0));
+          mbar_arrive_cluster(peer_u32(&sh.acc_empty[i & 1], 0));
         else
-          mbar_arrive(&sh.acc_empty[buf]);
+          mbar_arrive(&sh.acc_empty[i & 1]);
+      }
+      ++i;
+    };
+    for (Walk w(P, blockIdx.x / CG, step); w.t < tiles && !lost; w.next()) {
+      const int row = (w.mt() * CG + int(rank)) * kRowsOfCta + warp % 4 * 32 + lane, n0 = w.nt() * P.width + half;
+      const int held = min(kHalf, min(P.width - half, P.n - n0));  // of this half; may be none
+      if constexpr (MODE == kSums) {
+        // The tensor cores cut their sums off towards zero, and 256 times (K 4096) that is 1.8e-6 of
+        // lse; summed here after each 1024 of K, properly rounded, 4e-7.
+        float x[kHalf];
+        uint32_t at = take();
+        if (lost) break;
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 32) {
+          uint32_t r[32];
+          tmem_load32(r, at + c);
+          tmem_wait(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[c + j] = __uint_as_float(r[j]);
+        }
+        give();
+        for (int kb = kSegment * kBlockK; kb < P.k; kb += kSegment * kBlockK) {
+          at = take();
+          if (lost) break;
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32) {
+            uint32_t r[32];
+            tmem_load32(r, at + c);
+            tmem_wait(r);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              add2(Pair(x[c + j], x[c + j + 1]), Pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1]))).get(x[c + j], x[c + j + 1]);
+          }
+          give();
+        }
+        if (!lost) tile_sums(P, x, row, w.nt(), warp / 4, n0, held);
+      } else {
+        const uint32_t at = take();
+        if (lost) break;
+        if constexpr (MODE == kGradient)
+          tile_gradient<T>(P, at, row, n0, held);
+        else
+          tile_product<T>(P, at, row, n0, held, w.split);
+        give();
       }
     }
   }
@@ -448,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 
 // Joins the tiles' sums of each row: 16 rows a block, the tiles in 32 shares.
 struct JoinParams {
-  const float2* sums;
+  const float4* sums;
   const float* at_token;
   const void* tokens;
   float *logprob, *lse;
@@ -471,7 +526,11 @@ __global__ void __launch_bounds__(kJoinRows * kJoinShares) join_kernel(const Joi
   float2 s = make_float2(-INFINITY, 0.f);
   if (row < P.rows) {
 #pragma unroll 4
-    for (int t = share; t < P.n_tiles; t += kJoinShares) join_sums(s, P.sums[int64_t(t) * P.ld + row]);
+    for (int t = share; t < P.n_tiles; t += kJoinShares) {
+      const float4 v = P.sums[int64_t(t) * P.ld + row];
+      join_sums(s, make_float2(v.x, v.y));
+      join_sums(s, make_float2(v.z, v.w));
+    }
   }
   part[share][i] = s;
   __syncthreads();
@@ -588,8 +647,8 @@ StatesWs states_ws(int64_t rows, int64_t vocab, int64_t dim, bool backward) {
   L.unit = 256;
   L.at_token = 512;
   L.sums = L.at_token + align256(size_t(at_once) * 4);
-  const size_t few = size_t((vocab + 31) / 32) * std::min<int64_t>(rows, kRowsOfCta) * 8;
-  const size_t many = size_t((vocab + kColumns - 1) / kColumns) * at_once * 8;
+  const size_t few = size_t((vocab + 223) / 224) * 2 * std::min<int64_t>(rows, kRowsOfCta) * 8;
+  const size_t many = size_t((vocab + kColumns - 1) / kColumns) * 2 * at_once * 8;
   const size_t forward = L.sums + align256(std::max(few, many));
   L.total = forward;
   if (backward) {
@@ -756,7 +815,7 @@ sekv_status forward(const Call& c, float* logprob, float* lse, bool negate) {
     sekv_status st = launch_for<T, kSums, false, false>(P, c.dtype, sms, c.stream);
     if (st != SEKV_OK) return st;
     JoinParams J{};
-    J.sums = P.sums;
+    J.sums = reinterpret_cast<const float4*>(P.sums);
     J.at_token = P.at_token;
     J.tokens = c.tokens;
     J.logprob = logprob;

@@ -50,6 +50,7 @@
 #include <algorithm>
 
 #include "kv4.cuh"
+#include "kv4_tree.h"
 
 using namespace sekv;
 
@@ -62,6 +63,7 @@ constexpr int kChunkTokens = 32;
 constexpr int kChunkBytes = 2 * kKv4TileBytes;
 constexpr int kMaxCtas = 256;                    // of a launch
 constexpr int kCols = 8;                         // (token, head) pairs of a block
+constexpr int kWideColumns = 24;                 // of a tree, from which on kv4_tree.cu is faster
 constexpr int kStateFloats = kCols * (kHeadDim + 2);  // o, m, l
 // What a second group costs a CTA (its plan, queries, first copies and join, about 6 us), in chunks
 constexpr int kGroupCost = 40;
@@ -947,14 +949,15 @@ int blocks_of(const sekv_config* cfg, int64_t n_q) {
 int attn_ctas() { return std::min(device_sm_count(), kMaxCtas); }  // one per SM
 
 struct Kv4Ws {
-  size_t partials, arrived, total;
+  size_t partials, wide, arrived, total;
 };
 Kv4Ws kv4_ws(const sekv_config* cfg, int64_t n_q, int sms) {
   // the counters last: where they begin is the same whatever batch and n_q a call has, so
   // that calls of different sizes can take turns on a workspace
   Kv4Ws L{};
   L.partials = 256;
-  L.arrived = L.partials + align256(size_t(sms) * 2 * kStateFloats * 4);
+  L.wide = L.partials + align256(size_t(sms) * 2 * kStateFloats * 4);
+  L.arrived = L.wide + align256(kTreeBytes);
   L.total = L.arrived + align256(size_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * 4);
   return L;
 }
@@ -1011,6 +1014,30 @@ sekv_status attention(const sekv_config* cfg, const sekv_kv4_cache* cache, int32
   const int sms = attn_ctas();
   const Kv4Ws L = kv4_ws(cfg, n_q, sms);
   uint8_t* w = static_cast<uint8_t*>(workspace);
+  if (tree && n_q * (cfg->n_q_heads / cfg->n_kv_heads) >= kWideColumns) {
+    TreeCall c{};
+    c.pg.pages = static_cast<uint8_t*>(cache->pages);
+    c.pg.table = cache->page_table;
+    c.pg.status = reinterpret_cast<int32_t*>(w);
+    c.pg.n_pages = cache->n_pages;
+    c.pg.max_pages = cache->max_pages;
+    c.pg.hkv = cfg->n_kv_heads;
+    c.q = q;
+    c.first = seq_len;
+    c.tree = tree;
+    c.tree_stride = tree_stride;
+    c.out = out;
+    c.lse = lse;
+    c.partials = reinterpret_cast<float*>(w + L.wide);
+    c.wait_ns = (cfg->flags & SEKV_FLAG_SHORT_WAITS) ? 0 : kWaitNs;
+    c.batch = cfg->batch;
+    c.hpg = cfg->n_q_heads / cfg->n_kv_heads;
+    c.n_q = n_q;
+    c.n_blk = (n_q * c.hpg + kTreeRows - 1) / kTreeRows;
+    c.bf16 = dtype == SEKV_BF16;
+    c.scale_log2 = scale * kLog2e;
+    return tree_attention(c, sms, stream);
+  }
   AttnParams P{};
   P.pg.pages = static_cast<uint8_t*>(cache->pages);
   P.pg.table = cache->page_table;

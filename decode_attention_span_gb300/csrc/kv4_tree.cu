@@ -1,0 +1,854 @@
+// sekv_kv4_tree_attention for many (token, head) columns: 128 of them side by side on the fifth
+// generation's tensor cores, one pass over the cache for all.
+//
+// Mathematics: as in kv4_attn.cu, no K or V value is rebuilt.  With codes n and n' = n - 8,
+//   K^ = (z + 8 s) + s n',   q . K^ = sum over groups g of  s_g (sum_d q_d n'_d) + (z_g + 8 s_g) (sum_d q_d)
+//   sum_j p_j V^_j = sum_j (p_j s_j) n'_j + sum_j p_j (z_j + 8 s_j)
+// The codes become f16 numbers (exact) in shared memory, once for the 128 columns; the two groups
+// of dimensions have accumulators of their own, because a token's scales differ between them.  The
+// weights p_j s_j u enter as the sum of two f16 numbers (22 bits); u is a power of two for each column
+// and group, moved where the column's largest weight so far would leave [kLeast, kMost]: no token takes
+// bits from the others by the size of its values alone.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kv4.cuh"
+#include "kv4_tree.h"
+#include "tc.cuh"
+
+using namespace sekv;
+
+namespace {
+
+constexpr int kRaw = 4;         // pages on their way
+constexpr int kOps = 4;         // pages as operands
+constexpr int kSoftWarps = 8;   // two streams of four
+constexpr int kCodeWarps = 2;
+constexpr int kTreeThreads = (kSoftWarps + kCodeWarps + 2) * 32;
+constexpr int kGroupBytes = kKv4Page * 128;      // an operand of one group: 64 tokens x 64 dimensions f16
+constexpr int kOpBytes = 4 * kGroupBytes;        // K's two groups, V's two
+constexpr int kStreamColumns = 256;              // tensor memory of a stream: logits or weights 128, values 128
+constexpr int kValues = 128;                     // from here on
+constexpr int kItemCost = 6;                     // what an item costs beyond its pages, in pages
+constexpr float kNone = -3e38f;
+constexpr float kGrowth = 8.f;
+constexpr float kLeast = 1.f, kMost = 32768.f;
+constexpr uint64_t kTreeWaitNs = 2000000000ull;
+
+struct PageParams {
+  float4 k[kKv4Page / 2][2];  // tokens 2 i, 2 i + 1: (s0, s0', s1, s1'), (z0, z0', z1, z1'), z with 8 s
+  float4 v[kKv4Page / 2][2];
+  float top[2][2];            // V's largest scale: of 32 tokens, group
+  int held;                   // tokens of the page that the sequence has
+};
+
+struct __align__(1024) TreeShared {
+  uint8_t q[2][kTreeRows * 128];  // the columns' queries: a group of dimensions each
+  uint8_t op[kOps][kOpBytes];
+  uint8_t raw[kRaw][kKv4PageBytes];
+  PageParams par[kOps];
+  float q_sum[2][kTreeRows], q_scale[kTreeRows];
+  float other_m[kTreeRows], other_l[kTreeRows];  // the second stream's
+  uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], s_full[2], p_full[2], o_full, drained;
+  uint32_t tmem;
+  int raw_held[kRaw];
+  TreePlan plan;
+};
+static_assert(sizeof(TreeShared) + 1024 <= 227 * 1024, "shared memory of a CTA");
+static_assert(kOps * kOpBytes >= kTreeRows * kHeadDim * 4, "the second stream's values lie over the operands");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float q_value(__nv_bfloat16 q) { return __bfloat162float(q); }
+__device__ __forceinline__ float q_value(__half q) { return __half2float(q); }
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// What h, a rounded pair, lacks of (w0, w1)
+__device__ __forceinline__ uint32_t rest(__half2 h, float w0, float w1) {
+  float d0, d1;
+  asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; sub.rn.f32.f16 %0, a, %3; sub.rn.f32.f16 %1, b, %4;}"
+      : "=f"(d0), "=f"(d1)
+      : "r"(bits(h)), "f"(w0), "f"(w1));
+  return bits(__floats2half2_rn(-d0, -d1));
+}
+
+// Eight codes of a word as f16 numbers n - 8, in the order 0, 4, 1, 5, 2, 6, 3, 7
+__device__ __forceinline__ uint4 codes(uint32_t w) {
+  constexpr uint32_t kMagic = 0x64006400u;  // 1024: a code in the lowest bits adds itself, one above 16 times
+  const uint32_t w8 = w >> 8;
+  const uint32_t a = (w & 0x000f000fu) | kMagic, b = (w & 0x00f000f0u) | kMagic;
+  const uint32_t c = (w8 & 0x000f000fu) | kMagic, d = (w8 & 0x00f000f0u) | kMagic;
+  const __half2 less = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f), less16 = __float2half2_rn(-72.f);
+  auto h = [](const uint32_t& x) { return *reinterpret_cast<const __half2*>(&x); };
+  return make_uint4(bits(__hadd2(h(a), less)), bits(__hfma2(h(b), sixteenth, less16)), bits(__hadd2(h(c), less)),
+                    bits(__hfma2(h(d), sixteenth, less16)));
+}
+// Byte of 16-byte piece c of row r in an operand
+__device__ __forceinline__ uint32_t piece_at(int r, int c) { return uint32_t(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// One page's codes and scales as operands and floats, by the kCodeWarps
+__device__ __forceinline__ void expand_page(const uint8_t* raw, uint8_t* op, PageParams& par, int held, int tid) {
+#pragma unroll
+  for (int i = 0; i < 256 / (kCodeWarps * 32); ++i) {
+    const int at = tid + i * kCodeWarps * 32;  // 16 bytes: four words
+    const uint8_t* tile = raw + at / 64 * kKv4TileBytes;
+    {  // K: dimensions 16 q .. 16 q + 15 of both groups
+      const uint4 w = *reinterpret_cast<const uint4*>(tile + at % 64 * 16);
+      const int r = at / 4, q = at % 4;
+      *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q)) = codes(w.x);
+      *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q + 1)) = codes(w.y);
+      *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q)) = codes(w.z);
+      *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q + 1)) = codes(w.w);
+    }
+    {  // V: eight dimensions of two neighbouring tokens and both groups
+      const uint4 w = *reinterpret_cast<const uint4*>(tile + kKv4V + at % 64 * 16);
+      const int r = at / 64 * 16 + at % 64 / 32 * 8 + at % 4 * 2, oct = at % 32 / 4;
+      uint8_t* v = op + 2 * kGroupBytes;
+      *reinterpret_cast<uint4*>(v + piece_at(r, oct)) = codes(__byte_perm(w.x, w.y, 0x5410));
+      *reinterpret_cast<uint4*>(v + piece_at(r + 1, oct)) = codes(__byte_perm(w.x, w.y, 0x7632));
+      *reinterpret_cast<uint4*>(v + kGroupBytes + piece_at(r, oct)) = codes(__byte_perm(w.z, w.w, 0x5410));
+      *reinterpret_cast<uint4*>(v + kGroupBytes + piece_at(r + 1, oct)) = codes(__byte_perm(w.z, w.w, 0x7632));
+    }
+  }
+  static_assert(kCodeWarps * 32 == kKv4Page, "a thread for each token's scales");
+  {
+    const uint8_t* sz = raw + tid / 16 * kKv4TileBytes + kv4_param(tid % 16, 0, false);
+    uint2 k = *reinterpret_cast<const uint2*>(sz), v = *reinterpret_cast<const uint2*>(sz + 128);
+    if (tid >= held) k = v = make_uint2(0u, 0u);  // behind the end: may hold anything
+    auto put = [&](float4 (&p)[2], uint2 w) {
+      float *s = reinterpret_cast<float*>(&p[0]) + tid % 2, *z = reinterpret_cast<float*>(&p[1]) + tid % 2;
+      const float s0 = lo16(w.x), s1 = lo16(w.y);
+      s[0] = s0;
+      s[2] = s1;
+      z[0] = fmaf(8.f, s0, hi16(w.x));
+      z[2] = fmaf(8.f, s1, hi16(w.y));
+    };
+    put(par.k[tid / 2], k);
+    put(par.v[tid / 2], v);
+    // bits of numbers that are not negative compare as they do; NaN does not count
+    const uint32_t t0 = v.x & 0x7fffu, t1 = v.y & 0x7fffu;
+    const uint32_t m0 = __reduce_max_sync(~0u, t0 < 0x7f80u ? t0 : 0u), m1 = __reduce_max_sync(~0u, t1 < 0x7f80u ? t1 : 0u);
+    if (tid % 32 == 0) {
+      par.top[tid / 32][0] = __uint_as_float(m0 << 16);
+      par.top[tid / 32][1] = __uint_as_float(m1 << 16);
+    }
+    if (tid == 0) par.held = held;
+  }
+}
+
+// The power of two that brings x 2^9 to 2^5 .. 2^6
+__device__ __forceinline__ float unit_for(float x) {
+  return __uint_as_float(uint32_t(min(max(2 * 127 - 4 - int(__float_as_uint(x) >> 23), 1), 127 + 118)) << 23);
+}
+__device__ __forceinline__ int pages_of(int len) { return max(1, (len + kKv4Page - 1) / kKv4Page); }
+
+// The plan, by one warp: the number of pieces that the longest group is cut into, for which the waves
+// of items take least.
+__device__ __forceinline__ void make_plan(TreePlan& plan, const TreeCall& P, int ctas, bool report, int lane) {
+  const int cap = P.pg.max_pages * kKv4Page, per_seq = P.pg.hkv * P.n_blk;
+  int longest = 1;
+  for (int b = lane; b < P.batch; b += 32) {
+    int given = P.first[b];
+    if (given >= 0) given = given < INT32_MAX - P.n_q ? given + P.n_q : INT32_MAX;
+    const int len = min(max(given, 0), cap);
+    if (report && given != len) set_device_error(P.pg.status, DEV_BAD_LIST, b);
+    plan.len[b] = len;
+    longest = max(longest, pages_of(len));
+  }
+  longest = __reduce_max_sync(~0u, longest);
+  __syncwarp();
+  const int groups = P.batch * per_seq;
+  int piece = longest;
+  if (groups * 2 <= kTreeItems) {  // lane: lane + 1 pieces
+    const int each = (longest + lane) / (lane + 1);
+    int items = 0;
+    for (int b = 0; b < P.batch; ++b) items += (pages_of(plan.len[b]) + each - 1) / each;
+    items *= per_seq;
+    uint32_t cost = ~0u;
+    if (items <= kTreeItems || lane == 0) cost = min(uint32_t((items + ctas - 1) / ctas) * uint32_t(each + kItemCost), 0x03ffffffu);
+    const uint32_t best = __reduce_min_sync(~0u, cost == ~0u ? ~0u : cost << 5 | uint32_t(lane));
+    piece = __shfl_sync(~0u, each, best & 31u);
+  }
+  int run = 0;
+  for (int b0 = 0; b0 < P.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int n = b < P.batch ? (pages_of(plan.len[b]) + piece - 1) / piece * per_seq : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(~0u, n, o);
+      if (lane >= o) n += up;
+    }
+    if (b < P.batch) plan.before[b + 1] = run + n;
+    run += __shfl_sync(~0u, n, 31);
+  }
+  if (lane == 0) {
+    plan.before[0] = 0;
+    plan.piece = piece;
+  }
+}
+
+// An item: pages [page0, page1) of group `group` of sequence b; all of them where `pieces` is 1.
+struct Item {
+  int b, group, pieces, page0, page1, len;
+  __device__ __forceinline__ Item(const TreePlan& plan, const TreeCall& P, int item, int lane) {
+    b = 0;
+    for (;;) {  // the last sequence whose items start at or before it
+      const int i = b + 1 + lane;
+      const int n = __popc(__ballot_sync(~0u, i < P.batch && plan.before[i] <= item));
+      b += n;
+      if (n < 32) break;
+    }
+    const int per_seq = P.pg.hkv * P.n_blk;
+    pieces = (plan.before[b + 1] - plan.before[b]) / per_seq;
+    const int rel = item - plan.before[b];
+    group = rel / pieces;
+    const int i = rel - group * pieces;
+    len = plan.len[b];
+    const int n = pages_of(len), q = n / pieces, r = n - q * pieces;
+    page0 = q * i + r * i / pieces;
+    page1 = q * (i + 1) + r * (i + 1) / pieces;
+  }
+};
+
+// The 64 tokens of the page at `pos` that a drafted token sees: those before the first drafted one, then
+// those of its mask, of what the sequence has.
+__device__ __forceinline__ uint64_t seen_of(uint64_t tree, int prefix, int pos, int held) {
+  const int ahead = prefix - pos;
+  const uint64_t b = ahead >= 64 ? ~0ull : ahead > 0 ? tree << ahead | ((1ull << ahead) - 1) : -ahead < 64 ? tree >> -ahead : 0ull;
+  return held >= 64 ? b : b & ((1ull << max(held, 0)) - 1);
+}
+
+// A softmax thread's part: rows lane / 4 + 8 i (i 0 .. 3) of its warp's 32, and of a page the tokens
+// 8 b + 2 (lane % 4) and the next (b 0 .. 7).
+struct Soft {
+  float m[4];        // reference of the weights, log2
+  float l[4];        // sums over this thread's tokens
+  float c[4][2];     // of p z: [group]
+  float u[4][2];     // units
+  float most[4][2];  // largest weight so far, in units, of the row
+  float qs[4], q_sum[4][2];
+};
+
+// Values of this warp's rows times f[row][group]
+__device__ __forceinline__ void rescale_values(uint32_t at, const float (&f)[4][2]) {
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[8];
+      const uint32_t a = at + kValues + c * 16 + (uint32_t(h * 16) << 16);
+      tmem_load_16x16(r, a);
+      tmem_wait_loads();
+      tie(r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (c < 4 ? f[2 * h + (i >> 1 & 1)][0] : f[2 * h + (i >> 1 & 1)][1]));
+      tmem_store_16x16(a, r);
+    }
+  tmem_wait_stores();
+}
+
+// Maximum over the four threads of a row
+__device__ __forceinline__ float row_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+  return fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+}
+__device__ __forceinline__ float row_sum(float x) {
+  x += __shfl_xor_sync(~0u, x, 1);
+  return x + __shfl_xor_sync(~0u, x, 2);
+}
+
+// One page of a stream: its sums of q n' in tensor memory at `at` become weights there.
+template <bool EDGE>
+__device__ __forceinline__ void soft_page(Soft& S, const PageParams& par, uint32_t at, bool values, const uint64_t (&seen)[4], int t) {
+  float x[2][8][4];  // [row half][block of 8 tokens][row, token]
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t s[2][2][8];  // [row half][group]
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) tmem_load_16x16(s[h][g], at + g * 64 + ch * 16 + (uint32_t(h * 16) << 16));
+    tmem_wait_loads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) tie(s[h][g]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int b = ch * 2 + j;
+      const float4 ks = par.k[4 * b + t][0], kz = par.k[4 * b + t][1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 2 * h + e, i = 4 * j + 2 * e;
+          Pair y = mul2(Pair(ks.x, ks.y), Pair(__uint_as_float(s[h][0][i]), __uint_as_float(s[h][0][i + 1])));
+          y = fma2(Pair(ks.z, ks.w), Pair(__uint_as_float(s[h][1][i]), __uint_as_float(s[h][1][i + 1])), y);
+          y = fma2(Pair(kz.x, kz.y), Pair(S.q_sum[row][0], S.q_sum[row][0]), y);
+          y = fma2(Pair(kz.z, kz.w), Pair(S.q_sum[row][1], S.q_sum[row][1]), y);
+          y.get(x[h][b][2 * e], x[h][b][2 * e + 1]);
+          if (EDGE)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (!(seen[row] >> (8 * b + 2 * t + k) & 1)) x[h][b][2 * e + k] = -INFINITY;
+        }
+    }
+  }
+  // A new reference only where the old one may no longer do
+  float mx[4];
+  bool over = false;
+#pragma unroll
+  for (int row = 0; row < 4; ++row) {
+    const int h = row >> 1, e = row & 1;
+    float v = fmaxf(x[h][0][2 * e], x[h][0][2 * e + 1]);
+#pragma unroll
+    for (int b = 1; b < 8; ++b) v = fmaxf(v, fmaxf(x[h][b][2 * e], x[h][b][2 * e + 1]));
+    mx[row] = v * S.qs[row];
+    over |= mx[row] > S.m[row] + kGrowth;
+  }
+  if (__any_sync(~0u, over)) {
+    float f[4][2];
+#pragma unroll
+    for (int row = 0; row < 4; ++row) {
+      const float m1 = fmaxf(S.m[row], row_max(mx[row]));
+      f[row][0] = f[row][1] = ex2(S.m[row] - m1);
+      S.m[row] = m1;
+      S.l[row] *= f[row][0];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        S.c[row][g] *= f[row][0];
+        S.most[row][g] *= f[row][0];
+      }
+    }
+    if (values) rescale_values(at, f);
+  }
+#pragma unroll 1
+  for (bool again = false;; again = true) {
+    __half2 top[4][2];
+#pragma unroll
+    for (int row = 0; row < 4; ++row) top[row][0] = top[row][1] = __float2half2_rn(0.f);
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+      uint32_t hi[2][2][4], lo[2][2][4];  // [row half][group]
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int b = ch * 2 + j;
+        const float4 vs = par.v[4 * b + t][0], vz = par.v[4 * b + t][1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = 2 * h + e;
+            float p[2];
+            fma2(Pair(x[h][b][2 * e], x[h][b][2 * e + 1]), Pair(S.qs[row], S.qs[row]), Pair(-S.m[row], -S.m[row])).get(p[0], p[1]);
+            bool ok[2] = {true, true};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              p[k] = ex2(p[k]);
+              if (EDGE) {
+                ok[k] = seen[row] >> (8 * b + 2 * t + k) & 1;
+                if (!ok[k]) p[k] = 0.f;
+              }
+            }
+            if (!again) {
+              S.l[row] += p[0] + p[1];
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const float z0 = g ? vz.z : vz.x, z1 = g ? vz.w : vz.y;
+                if (!EDGE || ok[0]) S.c[row][g] = fmaf(p[0], z0, S.c[row][g]);
+                if (!EDGE || ok[1]) S.c[row][g] = fmaf(p[1], z1, S.c[row][g]);
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float w[2];
+              // in this order: a large s with the unit of a row without weight on it may overflow
+              mul2(mul2(Pair(p[0], p[1]), Pair(S.u[row][g], S.u[row][g])), g ? Pair(vs.z, vs.w) : Pair(vs.x, vs.y)).get(w[0], w[1]);
+              if (EDGE)  // what is not seen may hold NaN
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  if (!ok[k]) w[k] = 0.f;
+              const __half2 part = __floats2half2_rn(w[0], w[1]);
+              top[row][g] = __hmax2(top[row][g], part);
+              hi[h][g][2 * j + e] = bits(part);
+              lo[h][g][2 * j + e] = rest(part, w[0], w[1]);
+            }
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t a = at + g * 64 + ch * 8 + (uint32_t(h * 16) << 16);
+          tmem_store_16x8(a, hi[h][g][0], hi[h][g][1], hi[h][g][2], hi[h][g][3]);
+          tmem_store_16x8(a + 32, lo[h][g][0], lo[h][g][1], lo[h][g][2], lo[h][g][3]);
+        }
+    }
+    // the largest weights, of the rows' four threads: two rows a word
+    bool bad = false;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        __half2 w = __hmax2(__lows2half2(top[2 * h][g], top[2 * h + 1][g]), __highs2half2(top[2 * h][g], top[2 * h + 1][g]));
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          const uint32_t other = __shfl_xor_sync(~0u, bits(w), o);
+          w = __hmax2(w, *reinterpret_cast<const __half2*>(&other));
+        }
+        const float2 f = __half22float2(w);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 2 * h + e;
+          const float now = e ? f.y : f.x, all = fmaxf(S.most[row][g], now);
+          bad |= now >= kMost || (all < kLeast && S.m[row] > kNone);
+          if (now < kMost) S.most[row][g] = all;
+        }
+      }
+    if (again || !__any_sync(~0u, bad)) break;
+    // units by the rows' largest weights, in 32 bits; the page's weights are made again
+    float f[4][2];
+#pragma unroll
+    for (int row = 0; row < 4; ++row)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int h = row >> 1, e = row & 1;
+        float w = 0.f;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const float4 vs = par.v[4 * b + t][0];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (EDGE && !(seen[row] >> (8 * b + 2 * t + k) & 1)) continue;
+            const float p = ex2(fmaf(x[h][b][2 * e + k], S.qs[row], -S.m[row])) * 0.001953125f;  // 2^-9: finite with any s
+            w = fmaxf(w, p * (g ? (k ? vs.w : vs.z) : (k ? vs.y : vs.x)));
+          }
+        }
+        w = fmaxf(row_max(w), S.most[row][g] * (0.001953125f / S.u[row][g]));
+        const float unit = w > 0.f && w < INFINITY ? unit_for(w) : S.u[row][g];
+        f[row][g] = fminf(unit / S.u[row][g], 3e38f);  // where that is cut, the values so far are 0
+        S.u[row][g] = unit;
+        S.most[row][g] *= f[row][g];
+      }
+    tmem_wait_stores();
+    if (values) rescale_values(at, f);
+  }
+  tmem_wait_stores();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_constant__ TreeCall P) {
+  extern __shared__ uint8_t smem_raw[];
+  TreeShared& sh = *reinterpret_cast<TreeShared*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kCopy = kSoftWarps + kCodeWarps, kMma = kCopy + 1;
+  if (tid == 0) {
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], kCodeWarps);
+    }
+    for (int i = 0; i < kOps; ++i) {
+      mbar_init(&sh.op_full[i], kCodeWarps);
+      mbar_init(&sh.op_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+    }
+    mbar_init(&sh.o_full, 1);
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMma) tmem_alloc<1>(&sh.tmem, 512);
+  follow_previous();
+  if (warp == kCopy) make_plan(sh.plan, P, gridDim.x, blockIdx.x == 0, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int items = sh.plan.before[P.batch], cap = P.pg.max_pages * kKv4Page;
+  bool lost = false;       // a wait of this warp ran out: it waits and works no more
+  uint32_t pages = 0;      // all roles: pages before this item
+  uint32_t of_stream = 0;  // softmax: pages of the stream before it; products: of stream 0, and 1 below
+  uint32_t of_stream1 = 0;
+  uint32_t n_items = 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity, int which) {
+    if (!lost && !mbar_wait_parked(bar, parity, P.wait_ns)) {
+      set_device_error(P.pg.status, DEV_WAIT_TIMEOUT, which);
+      lost = true;
+    }
+    return !lost;
+  };
+
+  for (int item = blockIdx.x; item < items; item += gridDim.x, ++n_items) {
+    const Item I(sh.plan, P, item, lane);
+    const int blk = I.group / P.pg.hkv, head = I.group - blk * P.pg.hkv;
+    const int col0 = blk * kTreeRows, cols = min(kTreeRows, P.n_q * P.hpg - col0);
+    const int n = I.page1 - I.page0;
+    const int prefix = min(max(P.first[I.b], 0), cap);
+
+    if (warp < kSoftWarps) {  // the queries, a row at a time
+      for (int r = warp; r < kTreeRows; r += kSoftWarps) {
+        union {
+          uint2 w;
+          T e[4];
+        } qv;
+        qv.w = make_uint2(0, 0);
+        if (r < cols) {
+          const int col = col0 + r, tok = col / P.hpg;
+          const T* q = static_cast<const T*>(P.q) +
+                       ((int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg) * kHeadDim;
+          asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(qv.w.x), "=r"(qv.w.y) : "l"(q + 4 * lane));
+        }
+        float x[4], big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = q_value(qv.e[i]);
+          big = fmaxf(big, fabsf(x[i]));
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+        // power of two that brings the largest element to 2^13 .. 2^14
+        const int e = min(max(int(__float_as_uint(big) >> 23) - 127, -113), 127);
+        const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+        float sum = 0.f;
+        // dimension d of a group: piece d / 8, at 2 (d % 4) + d / 4 % 2 of its eight (codes())
+        const uint32_t at = (lane >> 4) * (kTreeRows * 128) + piece_at(r, lane >> 1 & 7) + (lane & 1) * 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half v = __float2half_rn(x[i] * up);
+          sum += __half2float(v);
+          *reinterpret_cast<__half*>(&sh.q[0][0] + at + i * 4) = v;
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if ((lane & 15) == 0) sh.q_sum[lane >> 4][r] = big < INFINITY ? sum : NAN;
+        if (lane == 0) sh.q_scale[r] = P.scale_log2 * __uint_as_float(uint32_t(127 - 13 + e) << 23);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp < kSoftWarps) {
+      const int stream = warp >> 2, g4 = lane >> 2, t = lane & 3, row0 = warp % 4 * 32 + g4;
+      const uint32_t at = tmem + stream * kStreamColumns + (uint32_t(warp % 4 * 32) << 16);
+      Soft S;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        S.m[i] = kNone;
+        S.l[i] = 0.f;
+        S.qs[i] = sh.q_scale[row0 + 8 * i];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          S.c[i][g] = S.most[i][g] = 0.f;
+          S.u[i][g] = 1.f;
+          S.q_sum[i][g] = sh.q_sum[g][row0 + 8 * i];
+        }
+      }
+      bool any = false;
+      for (int k = stream; k < n; k += 2, ++of_stream) {
+        const uint32_t buf = (pages + k) % kOps;
+        wait(&sh.op_full[buf], (pages + k) / kOps & 1, 4);
+        wait(&sh.s_full[stream], of_stream & 1, 5);
+        if (__any_sync(~0u, lost)) {
+          lost = true;
+          break;
+        }
+        tc_fence_after();
+        const PageParams& par = sh.par[buf];
+        const int pos = (I.page0 + k) * kKv4Page;
+        if (!any) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float u = unit_for(fmaxf(par.top[0][g], par.top[1][g]) * 0.001953125f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S.u[i][g] = u;
+          }
+        }
+        uint64_t seen[4] = {};
+        if (pos + kKv4Page > prefix || par.held < kKv4Page) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = row0 + 8 * i;
+            const uint64_t tree = r < cols ? uint64_t(P.tree[I.b * P.tree_stride + (col0 + r) / P.hpg]) : 0;
+            seen[i] = seen_of(tree, prefix, pos, par.held);
+          }
+          soft_page<true>(S, par, at, any, seen, t);
+        } else {
+          soft_page<false>(S, par, at, any, seen, t);
+        }
+        any = true;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[stream]);
+      }
+      wait(&sh.o_full, n_items & 1, 6);
+      lost = __any_sync(~0u, lost);
+      tc_fence_after();
+      float inv[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        S.l[i] = row_sum(S.l[i]);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          S.c[i][g] = row_sum(S.c[i][g]);
+          inv[i][g] = 1.f / S.u[i][g];
+        }
+      }
+      // the second stream's state and values to shared memory, over the operands: their products are done
+      float* other = reinterpret_cast<float*>(&sh.op[0][0]) + tid % 128;
+      float f0[4], f1[4], m[4], l[4];
+      if (stream == 1) {
+        if (t == 0)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sh.other_m[row0 + 8 * i] = S.m[i];
+            sh.other_l[row0 + 8 * i] = S.l[i];
+          }
+      }
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass == 1) {
+          named_bar(1, kSoftWarps * 32);
+          if (stream == 1) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float om = sh.other_m[row0 + 8 * i];
+            m[i] = fmaxf(S.m[i], om);
+            f0[i] = ex2(S.m[i] - m[i]);
+            f1[i] = ex2(om - m[i]);
+            l[i] = f0[i] * S.l[i] + f1[i] * sh.other_l[row0 + 8 * i];
+          }
+        }
+        if (pass != 1 - stream) continue;
+        const bool whole = I.pieces == 1;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t r[2][8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) tmem_load_16x16(r[h], at + kValues + c * 16 + (uint32_t(h * 16) << 16));
+          tmem_wait_loads();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tie(r[h]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = 2 * h + (i >> 1 & 1);
+              float v = any ? fmaf(__uint_as_float(r[h][i]), c < 4 ? inv[row][0] : inv[row][1], c < 4 ? S.c[row][0] : S.c[row][1]) : 0.f;
+              float* mine = other + (c * 16 + h * 8 + i) * 128;
+              if (stream == 1) {
+                *mine = v;
+                continue;
+              }
+              v = f0[row] * v + f1[row] * *mine;
+              const int rr = row0 + 8 * row;
+              // position 2 t + i % 2 of a piece of eight: dimension t or t + 4
+              const int d = c / 4 * 64 + (c % 4 * 2 + (i >> 2)) * 8 + t + (i & 1) * 4;
+              if (rr < cols) {
+                if (whole) {
+                  const int col = col0 + rr, tok = col / P.hpg;
+                  const int64_t o = (int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg;
+                  P.out[o * kHeadDim + d] = l[row] != 0.f ? v / l[row] : 0.f;
+                } else {
+                  P.partials[int64_t(item) * kTreePartialFloats + rr * kHeadDim + d] = v;
+                }
+              }
+            }
+          }
+        }
+        if (stream == 0 && t == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = row0 + 8 * i;
+            if (rr >= cols) continue;
+            if (whole) {
+              const int col = col0 + rr, tok = col / P.hpg;
+              const int64_t o = (int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg;
+              if (P.lse) P.lse[o] = l[i] != 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
+            } else {
+              float* ml = P.partials + int64_t(item) * kTreePartialFloats + kTreeRows * kHeadDim;
+              ml[rr] = m[i];
+              ml[kTreeRows + rr] = l[i];
+            }
+          }
+        }
+      }
+    } else if (warp < kCopy) {
+      for (int k = 0; k < n; ++k) {
+        const uint32_t at = pages + k, raw = at % kRaw, buf = at % kOps;
+        wait(&sh.raw_full[raw], at / kRaw & 1, 4);
+        wait(&sh.op_empty[buf], (at / kOps & 1) ^ 1, 5);
+        if (__any_sync(~0u, lost)) {
+          lost = true;
+          break;
+        }
+        expand_page(sh.raw[raw], sh.op[buf], sh.par[buf], sh.raw_held[raw], tid - kSoftWarps * 32);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.raw_empty[raw]);
+          mbar_arrive(&sh.op_full[buf]);
+        }
+      }
+    } else if (warp == kCopy) {
+      for (int k0 = 0; k0 < n && !lost; k0 += 32) {
+        int id = -1;
+        if (k0 + lane < n && (I.page0 + k0 + lane) * kKv4Page < I.len) {
+          id = P.pg.table[int64_t(I.b) * P.pg.max_pages + I.page0 + k0 + lane];
+          if (id < 0 || id >= P.pg.n_pages) {
+            set_device_error(P.pg.status, DEV_BAD_LIST, I.b);
+            id = -1;
+          }
+        }
+        for (int k = k0; k < min(n, k0 + 32); ++k) {
+          const uint32_t at = pages + k, raw = at % kRaw;
+          wait(&sh.raw_empty[raw], (at / kRaw & 1) ^ 1, 4);
+          lost = __any_sync(~0u, lost);
+          if (lost) break;
+          const int page = __shfl_sync(~0u, id, k - k0);
+          if (lane == 0) {
+            // a page that is not there has no tokens; what lies in its place is finite whatever it is
+            sh.raw_held[raw] = page >= 0 ? min(kKv4Page, I.len - (I.page0 + k) * kKv4Page) : 0;
+            if (page >= 0) {
+              mbar_arrive_expect_tx(&sh.raw_full[raw], kKv4PageBytes);
+              bulk_g2s(sh.raw[raw], P.pg.pages + (int64_t(page) * P.pg.hkv + head) * kKv4PageBytes, kKv4PageBytes, &sh.raw_full[raw]);
+            } else {
+              mbar_arrive(&sh.raw_full[raw]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    } else if (lane == 0) {
+      const uint32_t by_key = tc_shape(kTreeRows, kKv4Page, false, false, false), by_value = tc_shape(kTreeRows, 64, false, false, true);
+      uint32_t of[2] = {of_stream, of_stream1};
+      auto logits = [&](int k) {
+        const uint32_t at = pages + k, buf = at % kOps;
+        if (!wait(&sh.op_full[buf], at / kOps & 1, 4)) return;
+        tc_fence_after();
+        const uint32_t d = tmem + (k & 1) * kStreamColumns;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint64_t a = tc_operand(smem_u32(sh.q[g]), false, 0), b = tc_operand(smem_u32(sh.op[buf] + g * kGroupBytes), false, 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc_mma<1>(d + g * 64, a + j * 2, b + j * 2, by_key, j > 0);
+        }
+        tc_commit<1>(&sh.s_full[k & 1]);
+      };
+      for (int k = 0; k < min(n, 2) && !lost; ++k) logits(k);
+      for (int k = 0; k < n && !lost; ++k) {
+        const uint32_t buf = (pages + k) % kOps;
+        if (!wait(&sh.p_full[k & 1], of[k & 1] & 1, 7)) break;
+        ++of[k & 1];
+        tc_fence_after();
+        const uint32_t s = tmem + (k & 1) * kStreamColumns;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint64_t b = tc_operand(smem_u32(sh.op[buf] + (2 + g) * kGroupBytes), true, kGroupBytes);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tc_mma_tmem(s + kValues + g * 64, s + g * 64 + part * 32 + j * 8, b + j * 128, by_value, k > 1 || part + j > 0);
+        }
+        tc_commit<1>(&sh.op_empty[buf]);
+        if (k + 2 < n) logits(k + 2);
+      }
+      of_stream = of[0];
+      of_stream1 = of[1];
+      tc_commit<1>(&sh.o_full);
+    }
+    pages += n;
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();  // queries, operands and values are free again
+    tc_fence_after();
+  }
+
+  // no copy or product may be in flight when the CTA ends
+  if (warp == kCopy && lane == 0) {
+    for (uint32_t i = pages < kRaw ? 0 : pages - kRaw; i < pages; ++i)
+      if (!mbar_wait_parked(&sh.raw_full[i % kRaw], i / kRaw & 1, kTreeWaitNs)) break;
+  }
+  if (warp == kMma && lane == 0) {
+    tc_commit<1>(&sh.drained);
+    mbar_wait_parked(&sh.drained, 0, kTreeWaitNs);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMma) tmem_free<1>(tmem, 512);
+}
+
+// Joins the pieces of the groups that were cut: eight rows a block, a warp each.
+constexpr int kTreeJoinRows = 8;
+struct TreeJoin {
+  TreeCall call;
+  int ctas;  // of the kernel before
+};
+__global__ void __launch_bounds__(kTreeJoinRows * 32) kv4_tree_join_kernel(const __grid_constant__ TreeJoin J) {
+  __shared__ TreePlan plan;
+  const TreeCall& P = J.call;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  follow_previous();
+  if (warp == 0) make_plan(plan, P, J.ctas, false, lane);
+  __syncthreads();
+  const int per_seq = P.pg.hkv * P.n_blk, b = blockIdx.x / per_seq, group = blockIdx.x % per_seq;
+  const int pieces = (plan.before[b + 1] - plan.before[b]) / per_seq;
+  if (pieces == 1) return;
+  const int blk = group / P.pg.hkv, head = group - blk * P.pg.hkv, r = blockIdx.y * kTreeJoinRows + warp, col = blk * kTreeRows + r;
+  if (col >= P.n_q * P.hpg) return;
+  const float* part = P.partials + int64_t(plan.before[b] + group * pieces) * kTreePartialFloats;
+  float mx = kNone;
+  for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, part[i * kTreePartialFloats + kTreeRows * kHeadDim + r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+  float sum = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const float* p = part + i * kTreePartialFloats;
+    const float f = ex2(p[kTreeRows * kHeadDim + r] - mx);
+    const float4 x = *reinterpret_cast<const float4*>(p + r * kHeadDim + lane * 4);
+    sum = fmaf(f, p[kTreeRows * kHeadDim + kTreeRows + r], sum);
+    v.x = fmaf(f, x.x, v.x);
+    v.y = fmaf(f, x.y, v.y);
+    v.z = fmaf(f, x.z, v.z);
+    v.w = fmaf(f, x.w, v.w);
+  }
+  const int tok = col / P.hpg;
+  const int64_t o = (int64_t(b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<float4*>(P.out + o * kHeadDim + lane * 4) =
+      sum != 0.f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+  if (lane == 0 && P.lse) P.lse[o] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+}  // namespace
+
+namespace sekv {
+
+sekv_status tree_attention(const TreeCall& call, int sms, cudaStream_t stream) {
+  void (*const fn)(TreeCall) = call.bf16 ? kv4_tree_kernel<__nv_bfloat16> : kv4_tree_kernel<__half>;
+  const size_t shared = sizeof(TreeShared) + 1024;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared)) != cudaSuccess) {
+    cudaGetLastError();
+    return SEKV_ERR_CUDA;
+  }
+  const sekv_status st = launch_following(fn, dim3(unsigned(sms)), kTreeThreads, shared, stream, call);
+  const int64_t groups = int64_t(call.batch) * call.pg.hkv * call.n_blk;
+  if (st != SEKV_OK || groups * 2 > kTreeItems) return st;  // no group is cut
+  const TreeJoin J{call, sms};
+  return launch_following(kv4_tree_join_kernel, dim3(unsigned(groups), kTreeRows / kTreeJoinRows), kTreeJoinRows * 32, 0, stream, J);
+}
+
+}  // namespace sekv

@@ -30,7 +30,7 @@ constexpr int kBytesA = kRowsOfCta * kBlockK * 2;
 constexpr int kEpilogueWarps = 8;  // two for each 32 lanes, half of the columns each
 constexpr int kHalf = kColumns / 2;
 constexpr int kSegment = 16;       // blocks of K that one accumulator of the loss sums
-constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+constexpr int kTileThreads = (kEpilogueWarps + 2) * 32;
 constexpr uint64_t kStatesWaitNs = 2000000000ull;
 constexpr int64_t kRowsAtOnce = 8192;  // rows whose tiles' sums are kept at a time
 constexpr int kSplitCtas = 160;        // of a product whose sum over k is split, at most
@@ -286,7 +286,7 @@ struct Place {
 // `width` columns in turn.  One warp copies operands, one issues the products, four turn the finished
 // accumulator into results while the next one fills.
 template <typename T, int CG, Mode MODE, bool AX, bool BX>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ TileParams P) {
+__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ TileParams P) {
   extern __shared__ uint8_t smem_raw[];
   TileShared<CG>& sh = *reinterpret_cast<TileShared<CG>*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   constexpr int kStages = Ring<CG>::kStages;
@@ -688,7 +688,7 @@ sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t str
   }
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3(unsigned(std::min(P.m_tiles * P.n_tiles * P.splits, sms / CG) * CG));
-  lc.blockDim = dim3(kThreads);
+  lc.blockDim = dim3(kTileThreads);
   lc.dynamicSmemBytes = shared;
   lc.stream = stream;
   cudaLaunchAttribute at[2];

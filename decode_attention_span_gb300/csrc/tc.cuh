@@ -90,6 +90,30 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// 16 columns of 16 lanes as the matrix fragment of a warp: r[4 i + 2 h + c] is lane (row) lane / 4 + 8 h,
+// column 8 i + 2 (lane % 4) + c.  The values are there after tmem_wait_loads().
+__device__ __forceinline__ void tmem_load_16x16(uint32_t (&r)[8], uint32_t at) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
+}
+__device__ __forceinline__ void tmem_store_16x16(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// The same fragment as pairs of 16-bit numbers: r[2 i + h] is row lane / 4 + 8 h, column 4 i + lane % 4
+__device__ __forceinline__ void tmem_store_16x8(uint32_t at, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+// Ties a fragment to the wait before it, so that no use of it moves up
+__device__ __forceinline__ void tie(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+}
+__device__ __forceinline__ void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ---------------------------------------------------------------------- products
 // Operand tiles lie in shared memory as 128-byte rows, 128-byte swizzle, 1024-byte aligned.
 //   along K: rows of 64 elements of K, eight rows 1024 bytes
@@ -120,6 +144,14 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(shape), "r"(uint32_t(add))
         : "memory");
+}
+// The same with A in tensor memory: lanes are its rows, a column two numbers of K
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(shape), "r"(uint32_t(add))
+      : "memory");
 }
 // Arrives at `bar` (of both CTAs of a pair) when the products issued so far are done
 template <int CG>

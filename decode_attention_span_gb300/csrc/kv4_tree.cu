@@ -33,13 +33,16 @@ constexpr int kValues = 128;                     // from here on
 constexpr int kItemCost = 6;                     // what an item costs beyond its pages, in pages
 constexpr float kNone = -3e38f;
 constexpr float kGrowth = 8.f;
-constexpr float kLeast = 1.f, kMost = 32768.f;
+constexpr float kMaxScale = 128.f;      // of V with the unit: 2^8 times it fits f16
+constexpr float kLeast = 1.f, kMost = 4096.f;
+constexpr int kUnitTop = 5;             // a unit brings what it is made for to 2^5 .. 2^6
+constexpr uint32_t kUnitMax = 127 + 118;
 constexpr uint64_t kTreeWaitNs = 2000000000ull;
 
 struct PageParams {
   float4 k[kKv4Page / 2][2];  // tokens 2 i, 2 i + 1: (s0, s0', s1, s1'), (z0, z0', z1, z1'), z with 8 s
   float4 v[kKv4Page / 2][2];
-  float top[2][2];            // V's largest scale: of 32 tokens, group
+  uint32_t top[2], low[2];    // V's largest scale and smallest, of 32 tokens: bf16
   int held;                   // tokens of the page that the sequence has
 };
 
@@ -133,18 +136,19 @@ __device__ __forceinline__ void expand_page(const uint8_t* raw, uint8_t* op, Pag
     put(par.v[tid / 2], v);
     // bits of numbers that are not negative compare as they do; NaN does not count
     const uint32_t t0 = v.x & 0x7fffu, t1 = v.y & 0x7fffu;
-    const uint32_t m0 = __reduce_max_sync(~0u, t0 < 0x7f80u ? t0 : 0u), m1 = __reduce_max_sync(~0u, t1 < 0x7f80u ? t1 : 0u);
+    const uint32_t top = __reduce_max_sync(~0u, max(t0 < 0x7f80u ? t0 : 0u, t1 < 0x7f80u ? t1 : 0u));
+    const uint32_t low = __reduce_min_sync(~0u, tid < held ? min(t0, t1) : 0x7f80u);
     if (tid % 32 == 0) {
-      par.top[tid / 32][0] = __uint_as_float(m0 << 16);
-      par.top[tid / 32][1] = __uint_as_float(m1 << 16);
+      par.top[tid / 32] = top;
+      par.low[tid / 32] = low;
     }
     if (tid == 0) par.held = held;
   }
 }
 
-// The power of two that brings x 2^9 to 2^5 .. 2^6
-__device__ __forceinline__ float unit_for(float x) {
-  return __uint_as_float(uint32_t(min(max(2 * 127 - 4 - int(__float_as_uint(x) >> 23), 1), 127 + 118)) << 23);
+// The power of two that brings the number with these exponent bits to 2^kUnitTop .. twice that
+__device__ __forceinline__ float unit_of(int exponent) {
+  return __uint_as_float(uint32_t(min(max(2 * 127 + kUnitTop - exponent, 1), int(kUnitMax))) << 23);
 }
 __device__ __forceinline__ int pages_of(int len) { return max(1, (len + kKv4Page - 1) / kKv4Page); }
 
@@ -227,33 +231,40 @@ __device__ __forceinline__ uint64_t seen_of(uint64_t tree, int prefix, int pos, 
 // A softmax thread's part: rows lane / 4 + 8 i (i 0 .. 3) of its warp's 32, and of a page the tokens
 // 8 b + 2 (lane % 4) and the next (b 0 .. 7).
 struct Soft {
-  float m[4];        // reference of the weights, log2
-  float l[4];        // sums over this thread's tokens
-  float c[4][2];     // of p z: [group]
-  float u[4][2];     // units
-  float most[4][2];  // largest weight so far, in units, of the row
-  float qs[4], q_sum[4][2];
+  float m[4];        // reference of the weights, log2: within 2^8 of the largest; kNone: no token yet
+  float u[4][2];     // units: [group]
+  float largest[4][2];  // the rows' largest weights, once they have units of their own
+  float qs[4];
+  float most;        // the largest unit of the warp's rows
+  float least;       // what every row's largest weight with its unit is at least
+  bool split;        // the rows and groups have units of their own
 };
 
 // Values of this warp's rows times f[row][group]
 __device__ __forceinline__ void rescale_values(uint32_t at, const float (&f)[4][2]) {
 #pragma unroll 1
-  for (int c = 0; c < 8; ++c)
+  for (int g = 0; g < 2; ++g) {
+    float by[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t r[8];
-      const uint32_t a = at + kValues + c * 16 + (uint32_t(h * 16) << 16);
-      tmem_load_16x16(r, a);
-      tmem_wait_loads();
-      tie(r);
+    for (int i = 0; i < 4; ++i) by[i] = g ? f[i][1] : f[i][0];
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (c < 4 ? f[2 * h + (i >> 1 & 1)][0] : f[2 * h + (i >> 1 & 1)][1]));
-      tmem_store_16x16(a, r);
-    }
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[16];
+        const uint32_t a = at + kValues + g * 64 + c * 32 + (uint32_t(h * 16) << 16);
+        tmem_load_16x32(r, a);
+        tmem_wait_loads();
+        tie(r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * by[2 * h + (i >> 1 & 1)]);
+        tmem_store_16x32(a, r);
+      }
+  }
   tmem_wait_stores();
 }
 
-// Maximum over the four threads of a row
+// Maximum and sum over the four threads of a row
 __device__ __forceinline__ float row_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
   return fmaxf(x, __shfl_xor_sync(~0u, x, 2));
@@ -263,181 +274,225 @@ __device__ __forceinline__ float row_sum(float x) {
   return x + __shfl_xor_sync(~0u, x, 2);
 }
 
-// One page of a stream: its sums of q n' in tensor memory at `at` become weights there.
+// Tensor memory of a stream: the logits' two accumulators, 64 columns each.  The logits take the place
+// of the second; the weights' parts of tokens 0 .. 31, [group][part] 16 columns, that of the first,
+// those of tokens 32 .. 63 the logits' own.
+constexpr int kLogits = 64;
+
+// Units of their own for the rows and groups of dimensions, where scales lie far apart: by the page's largest
+// scale as long as the row's largest weight is kLeast or more with that, and by that weight otherwise.
+// f: on the sums, as the reference moves; k: on the values.
 template <bool EDGE>
-__device__ __forceinline__ void soft_page(Soft& S, const PageParams& par, uint32_t at, bool values, const uint64_t (&seen)[4], int t) {
-  float x[2][8][4];  // [row half][block of 8 tokens][row, token]
+__device__ __forceinline__ void split_units(Soft& S, const PageParams& par, uint32_t at, float by_scale, const float (&f)[4],
+                                         float (&k)[4][2], const uint64_t (&seen)[4], int t) {
+  float w[4][2] = {};
+#pragma unroll 1
+  for (int it = 0; it < 2; ++it)
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t x[16];
+      tmem_load_16x32(x, at + kLogits + it * 32 + (uint32_t(h * 16) << 16));
+      tmem_wait_loads();
+      tie(x);
 #pragma unroll
-  for (int ch = 0; ch < 4; ++ch) {
-    uint32_t s[2][2][8];  // [row half][group]
+      for (int b = 0; b < 4; ++b) {
+        const int b8 = it * 4 + b;
+        const float4 vs = par.v[4 * b8 + t][0];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+        for (int e = 0; e < 2; ++e) {
+          const float m = h ? S.m[2 + e] : S.m[e], qs = h ? S.qs[2 + e] : S.qs[e];
+          const uint64_t bits = h ? seen[2 + e] : seen[e];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) tmem_load_16x16(s[h][g], at + g * 64 + ch * 16 + (uint32_t(h * 16) << 16));
-    tmem_wait_loads();
+          for (int j = 0; j < 2; ++j) {
+            const bool ok = !EDGE || (bits >> (8 * b8 + 2 * t + j) & 1);
+            const float p = ok ? ex2(fmaf(__uint_as_float(x[4 * b + 2 * e + j]), qs, -m)) : 0.f;
+            // NaN does not count; 2^-9: finite with any s
+            const float w0 = ok ? p * 0.001953125f * (j ? vs.y : vs.x) : 0.f, w1 = ok ? p * 0.001953125f * (j ? vs.w : vs.z) : 0.f;
+            if (h) {
+              w[2 + e][0] = fmaxf(w[2 + e][0], w0);
+              w[2 + e][1] = fmaxf(w[2 + e][1], w1);
+            } else {
+              w[e][0] = fmaxf(w[e][0], w0);
+              w[e][1] = fmaxf(w[e][1], w1);
+            }
+          }
+        }
+      }
+    }
+  float most = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int row = 0; row < 4; ++row)
 #pragma unroll
-      for (int g = 0; g < 2; ++g) tie(s[h][g]);
+    for (int g = 0; g < 2; ++g) {
+      const float old = S.u[row][g];
+      // largest weights, here and in `largest`, times 2^-9
+      const float all = fmaxf(row_max(w[row][g]), f[row] * (S.split ? S.largest[row][g] : kLeast * 0.001953125f / old));
+      float unit = fminf(old, by_scale);
+      if (!(all * unit >= kLeast * 0.001953125f && all * unit < kMost * 0.001953125f)) unit = unit_of(int(__float_as_uint(all) >> 23) + 9);
+      S.u[row][g] = unit;
+      S.largest[row][g] = all;
+      k[row][g] = unit >= 1.f ? f[row] * unit / old : f[row] * (unit / old);  // in range in between, too
+      most = fmaxf(most, unit);
+    }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int b = ch * 2 + j;
-      const float4 ks = par.k[4 * b + t][0], kz = par.k[4 * b + t][1];
+  for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+  S.most = most;
+  S.split = true;
+}
+
+// One page of a stream: its sums of q n' in tensor memory at `at` become weights there.  l, c: sums of
+// the weights and of their products with z, over this thread's even and odd tokens.
+template <bool EDGE>
+__device__ __forceinline__ void soft_page(Soft& S, Pair (&l)[4], Pair (&c)[4][2], const PageParams& par, uint32_t at, bool values,
+                                          const uint64_t (&seen)[4], int t, const float* q_sum) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  {
+    float sum[4][2];  // of the queries
+#pragma unroll
+    for (int row = 0; row < 4; ++row) {
+      sum[row][0] = q_sum[8 * row];
+      sum[row][1] = q_sum[kTreeRows + 8 * row];
+    }
+#pragma unroll 1
+    for (int it = 0; it < 2; ++it) {
+      uint32_t s[2][2][16];  // [row half][group]
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 2 * h + e, i = 4 * j + 2 * e;
-          Pair y = mul2(Pair(ks.x, ks.y), Pair(__uint_as_float(s[h][0][i]), __uint_as_float(s[h][0][i + 1])));
-          y = fma2(Pair(ks.z, ks.w), Pair(__uint_as_float(s[h][1][i]), __uint_as_float(s[h][1][i + 1])), y);
-          y = fma2(Pair(kz.x, kz.y), Pair(S.q_sum[row][0], S.q_sum[row][0]), y);
-          y = fma2(Pair(kz.z, kz.w), Pair(S.q_sum[row][1], S.q_sum[row][1]), y);
-          y.get(x[h][b][2 * e], x[h][b][2 * e + 1]);
-          if (EDGE)
+        for (int g = 0; g < 2; ++g) tmem_load_16x32(s[h][g], at + g * 64 + it * 32 + (uint32_t(h * 16) << 16));
+      tmem_wait_loads();
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (!(seen[row] >> (8 * b + 2 * t + k) & 1)) x[h][b][2 * e + k] = -INFINITY;
-        }
-    }
-  }
-  // A new reference only where the old one may no longer do
-  float mx[4];
-  bool over = false;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-  for (int row = 0; row < 4; ++row) {
-    const int h = row >> 1, e = row & 1;
-    float v = fmaxf(x[h][0][2 * e], x[h][0][2 * e + 1]);
+        for (int g = 0; g < 2; ++g) tie(s[h][g]);
 #pragma unroll
-    for (int b = 1; b < 8; ++b) v = fmaxf(v, fmaxf(x[h][b][2 * e], x[h][b][2 * e + 1]));
-    mx[row] = v * S.qs[row];
-    over |= mx[row] > S.m[row] + kGrowth;
-  }
-  if (__any_sync(~0u, over)) {
-    float f[4][2];
-#pragma unroll
-    for (int row = 0; row < 4; ++row) {
-      const float m1 = fmaxf(S.m[row], row_max(mx[row]));
-      f[row][0] = f[row][1] = ex2(S.m[row] - m1);
-      S.m[row] = m1;
-      S.l[row] *= f[row][0];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        S.c[row][g] *= f[row][0];
-        S.most[row][g] *= f[row][0];
-      }
-    }
-    if (values) rescale_values(at, f);
-  }
-#pragma unroll 1
-  for (bool again = false;; again = true) {
-    __half2 top[4][2];
-#pragma unroll
-    for (int row = 0; row < 4; ++row) top[row][0] = top[row][1] = __float2half2_rn(0.f);
-#pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
-      uint32_t hi[2][2][4], lo[2][2][4];  // [row half][group]
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int b = ch * 2 + j;
-        const float4 vs = par.v[4 * b + t][0], vz = par.v[4 * b + t][1];
+      for (int b = 0; b < 4; ++b) {
+        const int b8 = it * 4 + b;
+        const float4 ks = par.k[4 * b8 + t][0], kz = par.k[4 * b8 + t][1];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int row = 2 * h + e;
+            const int row = 2 * h + e, i = 4 * b + 2 * e;
+            Pair y = mul2(Pair(ks.x, ks.y), Pair(__uint_as_float(s[h][0][i]), __uint_as_float(s[h][0][i + 1])));
+            y = fma2(Pair(ks.z, ks.w), Pair(__uint_as_float(s[h][1][i]), __uint_as_float(s[h][1][i + 1])), y);
+            y = fma2(Pair(kz.x, kz.y), Pair(sum[row][0], sum[row][0]), y);
+            y = fma2(Pair(kz.z, kz.w), Pair(sum[row][1], sum[row][1]), y);
+            float x[2];
+            y.get(x[0], x[1]);
+            if (EDGE)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (!(seen[row] >> (8 * b8 + 2 * t + j) & 1)) x[j] = -INFINITY;
+            mx[row] = fmaxf(mx[row], fmaxf(x[0], x[1]));
+            s[h][1][i] = __float_as_uint(x[0]);
+            s[h][1][i + 1] = __float_as_uint(x[1]);
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_store_16x32(at + kLogits + it * 32 + (uint32_t(h * 16) << 16), s[h][1]);
+    }
+    tmem_wait_stores();
+  }
+  // A new reference, or new units, only where the old ones may no longer do.
+  const uint32_t top = max(par.top[0], par.top[1]);
+  bool over = __uint_as_float(top << 16) * S.most >= kMaxScale;
+#pragma unroll
+  for (int row = 0; row < 4; ++row) {
+    mx[row] *= S.qs[row];
+    over |= mx[row] > S.m[row] + kGrowth;
+  }
+  if (__any_sync(~0u, over)) {
+    float f[4], k[4][2];
+#pragma unroll
+    for (int row = 0; row < 4; ++row) {
+      const float m1 = fmaxf(S.m[row], row_max(mx[row]));
+      f[row] = ex2(S.m[row] - m1);
+      S.m[row] = m1;
+      const Pair f2(f[row], f[row]);
+      l[row] = mul2(l[row], f2);
+      c[row][0] = mul2(c[row][0], f2);
+      c[row][1] = mul2(c[row][1], f2);
+    }
+    // One unit for all while that serves them: where a row's reference moves, a token of this page
+    // has weight 1 in it, and so at least the page's smallest scale.
+    const float low = __uint_as_float(min(par.low[0], par.low[1]) << 16);
+    const float by_scale = unit_of(int(top >> 7)), unit = fminf(S.most, by_scale), ratio = unit / S.most;
+    S.least = fminf(S.least * ratio, low * unit);
+    if (!S.split && S.least >= kLeast) {
+      S.most = unit;
+#pragma unroll
+      for (int row = 0; row < 4; ++row) {
+        S.u[row][0] = S.u[row][1] = unit;
+        k[row][0] = k[row][1] = f[row] * ratio;
+      }
+    } else {
+      split_units<EDGE>(S, par, at, by_scale, f, k, seen, t);
+    }
+    if (values) rescale_values(at, k);
+  }
+#pragma unroll 1
+  for (int it = 0; it < 2; ++it) {
+    uint32_t x[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) tmem_load_16x32(x[h], at + kLogits + it * 32 + (uint32_t(h * 16) << 16));
+    tmem_wait_loads();
+    tie(x[0]);
+    tie(x[1]);
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+      uint32_t part[2][2][2][4];  // [row half][group][part]
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int b = ch * 2 + j, b8 = it * 4 + b;
+        const float4 vs = par.v[4 * b8 + t][0], vz = par.v[4 * b8 + t][1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = 2 * h + e, i = 4 * b + 2 * e;
             float p[2];
-            fma2(Pair(x[h][b][2 * e], x[h][b][2 * e + 1]), Pair(S.qs[row], S.qs[row]), Pair(-S.m[row], -S.m[row])).get(p[0], p[1]);
+            fma2(Pair(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1])), Pair(S.qs[row], S.qs[row]), Pair(-S.m[row], -S.m[row]))
+                .get(p[0], p[1]);
             bool ok[2] = {true, true};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              p[k] = ex2(p[k]);
+            for (int n = 0; n < 2; ++n) {
+              p[n] = ex2(p[n]);
               if (EDGE) {
-                ok[k] = seen[row] >> (8 * b + 2 * t + k) & 1;
-                if (!ok[k]) p[k] = 0.f;
+                ok[n] = seen[row] >> (8 * b8 + 2 * t + n) & 1;
+                if (!ok[n]) p[n] = 0.f;
               }
             }
-            if (!again) {
-              S.l[row] += p[0] + p[1];
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const float z0 = g ? vz.z : vz.x, z1 = g ? vz.w : vz.y;
-                if (!EDGE || ok[0]) S.c[row][g] = fmaf(p[0], z0, S.c[row][g]);
-                if (!EDGE || ok[1]) S.c[row][g] = fmaf(p[1], z1, S.c[row][g]);
-              }
-            }
+            const Pair pp(p[0], p[1]);
+            l[row] = add2(l[row], pp);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
+              float z0 = g ? vz.z : vz.x, z1 = g ? vz.w : vz.y;
+              if (EDGE) {  // what is not seen may hold NaN
+                if (!ok[0]) z0 = 0.f;
+                if (!ok[1]) z1 = 0.f;
+              }
+              c[row][g] = fma2(pp, Pair(z0, z1), c[row][g]);
               float w[2];
               // in this order: a large s with the unit of a row without weight on it may overflow
-              mul2(mul2(Pair(p[0], p[1]), Pair(S.u[row][g], S.u[row][g])), g ? Pair(vs.z, vs.w) : Pair(vs.x, vs.y)).get(w[0], w[1]);
-              if (EDGE)  // what is not seen may hold NaN
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  if (!ok[k]) w[k] = 0.f;
-              const __half2 part = __floats2half2_rn(w[0], w[1]);
-              top[row][g] = __hmax2(top[row][g], part);
-              hi[h][g][2 * j + e] = bits(part);
-              lo[h][g][2 * j + e] = rest(part, w[0], w[1]);
+              mul2(mul2(pp, Pair(S.u[row][g], S.u[row][g])), g ? Pair(vs.z, vs.w) : Pair(vs.x, vs.y)).get(w[0], w[1]);
+              if (EDGE) {
+                if (!ok[0]) w[0] = 0.f;
+                if (!ok[1]) w[1] = 0.f;
+              }
+              const __half2 hi = __floats2half2_rn(w[0], w[1]);
+              part[h][g][0][2 * j + e] = bits(hi);
+              part[h][g][1][2 * j + e] = rest(hi, w[0], w[1]);
             }
           }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t a = at + g * 64 + ch * 8 + (uint32_t(h * 16) << 16);
-          tmem_store_16x8(a, hi[h][g][0], hi[h][g][1], hi[h][g][2], hi[h][g][3]);
-          tmem_store_16x8(a + 32, lo[h][g][0], lo[h][g][1], lo[h][g][2], lo[h][g][3]);
-        }
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) tmem_store_16x8(at + it * 64 + (2 * g + n) * 16 + ch * 8 + (uint32_t(h * 16) << 16), part[h][g][n]);
     }
-    // the largest weights, of the rows' four threads: two rows a word
-    bool bad = false;
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        __half2 w = __hmax2(__lows2half2(top[2 * h][g], top[2 * h + 1][g]), __highs2half2(top[2 * h][g], top[2 * h + 1][g]));
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          const uint32_t other = __shfl_xor_sync(~0u, bits(w), o);
-          w = __hmax2(w, *reinterpret_cast<const __half2*>(&other));
-        }
-        const float2 f = __half22float2(w);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 2 * h + e;
-          const float now = e ? f.y : f.x, all = fmaxf(S.most[row][g], now);
-          bad |= now >= kMost || (all < kLeast && S.m[row] > kNone);
-          if (now < kMost) S.most[row][g] = all;
-        }
-      }
-    if (again || !__any_sync(~0u, bad)) break;
-    // units by the rows' largest weights, in 32 bits; the page's weights are made again
-    float f[4][2];
-#pragma unroll
-    for (int row = 0; row < 4; ++row)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int h = row >> 1, e = row & 1;
-        float w = 0.f;
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const float4 vs = par.v[4 * b + t][0];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (EDGE && !(seen[row] >> (8 * b + 2 * t + k) & 1)) continue;
-            const float p = ex2(fmaf(x[h][b][2 * e + k], S.qs[row], -S.m[row])) * 0.001953125f;  // 2^-9: finite with any s
-            w = fmaxf(w, p * (g ? (k ? vs.w : vs.z) : (k ? vs.y : vs.x)));
-          }
-        }
-        w = fmaxf(row_max(w), S.most[row][g] * (0.001953125f / S.u[row][g]));
-        const float unit = w > 0.f && w < INFINITY ? unit_for(w) : S.u[row][g];
-        f[row][g] = fminf(unit / S.u[row][g], 3e38f);  // where that is cut, the values so far are 0
-        S.u[row][g] = unit;
-        S.most[row][g] *= f[row][g];
-      }
-    tmem_wait_stores();
-    if (values) rescale_values(at, f);
   }
   tmem_wait_stores();
 }
@@ -474,10 +529,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
   const uint32_t tmem = sh.tmem;
   const int items = sh.plan.before[P.batch], cap = P.pg.max_pages * kKv4Page;
   bool lost = false;       // a wait of this warp ran out: it waits and works no more
-  uint32_t pages = 0;      // all roles: pages before this item
-  uint32_t of_stream = 0;  // softmax: pages of the stream before it; products: of stream 0, and 1 below
-  uint32_t of_stream1 = 0;
-  uint32_t n_items = 0;
+  uint32_t pages = 0;      // before this item
   auto wait = [&](uint64_t* bar, uint32_t parity, int which) {
     if (!lost && !mbar_wait_parked(bar, parity, P.wait_ns)) {
       set_device_error(P.pg.status, DEV_WAIT_TIMEOUT, which);
@@ -485,32 +537,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
     }
     return !lost;
   };
+  // Between items, and between the queries and their products, all warps meet
+  auto meet = [&]() {
+    __syncwarp();
+    tc_fence_before();
+    named_bar(2, kTreeThreads);
+    tc_fence_after();
+  };
 
-  for (int item = blockIdx.x; item < items; item += gridDim.x, ++n_items) {
-    const Item I(sh.plan, P, item, lane);
-    const int blk = I.group / P.pg.hkv, head = I.group - blk * P.pg.hkv;
-    const int col0 = blk * kTreeRows, cols = min(kTreeRows, P.n_q * P.hpg - col0);
-    const int n = I.page1 - I.page0;
-    const int prefix = min(max(P.first[I.b], 0), cap);
-
-    if (warp < kSoftWarps) {  // the queries, a row at a time
-      for (int r = warp; r < kTreeRows; r += kSoftWarps) {
-        union {
-          uint2 w;
-          T e[4];
-        } qv;
-        qv.w = make_uint2(0, 0);
+  // Each role goes through the items on its own: the softmax threads have 216 registers, the others 72
+  // (256 x 216 + 128 x 72 = 384 x 168, what the CTA was launched with).
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    uint32_t of_stream = 0, n_items = 0;  // pages of the stream, items
+    for (int item = blockIdx.x; item < items; item += gridDim.x, ++n_items) {
+      const Item I(sh.plan, P, item, lane);
+      const int blk = I.group / P.pg.hkv, head = I.group - blk * P.pg.hkv;
+      const int col0 = blk * kTreeRows, cols = min(kTreeRows, P.n_q * P.hpg - col0);
+      const int n = I.page1 - I.page0;
+      const int prefix = min(max(P.first[I.b], 0), cap);
+      // the queries, a row at a time
+      constexpr int kEach = kTreeRows / kSoftWarps;
+      uint2 in[kEach];  // all on their way at once
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = warp * kEach + i;
+        in[i] = make_uint2(0, 0);
         if (r < cols) {
           const int col = col0 + r, tok = col / P.hpg;
           const T* q = static_cast<const T*>(P.q) +
                        ((int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg) * kHeadDim;
-          asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(qv.w.x), "=r"(qv.w.y) : "l"(q + 4 * lane));
+          asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(in[i].x), "=r"(in[i].y) : "l"(q + 4 * lane));
         }
+      }
+#pragma unroll 4
+      for (int i = 0; i < kEach; ++i) {
+        const int r = warp * kEach + i;
         float x[4], big = 0.f;
+        const T* e4 = reinterpret_cast<const T*>(&in[i]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = q_value(qv.e[i]);
-          big = fmaxf(big, fabsf(x[i]));
+        for (int j = 0; j < 4; ++j) {
+          x[j] = q_value(e4[j]);
+          big = fmaxf(big, fabsf(x[j]));
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
@@ -519,12 +587,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
         float sum = 0.f;
         // dimension d of a group: piece d / 8, at 2 (d % 4) + d / 4 % 2 of its eight (codes())
-        const uint32_t at = (lane >> 4) * (kTreeRows * 128) + piece_at(r, lane >> 1 & 7) + (lane & 1) * 2;
+        const uint32_t to = (lane >> 4) * (kTreeRows * 128) + piece_at(r, lane >> 1 & 7) + (lane & 1) * 2;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half v = __float2half_rn(x[i] * up);
+        for (int j = 0; j < 4; ++j) {
+          const __half v = __float2half_rn(x[j] * up);
           sum += __half2float(v);
-          *reinterpret_cast<__half*>(&sh.q[0][0] + at + i * 4) = v;
+          *reinterpret_cast<__half*>(&sh.q[0][0] + to + j * 4) = v;
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -532,26 +600,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         if (lane == 0) sh.q_scale[r] = P.scale_log2 * __uint_as_float(uint32_t(127 - 13 + e) << 23);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-
-    if (warp < kSoftWarps) {
+      meet();
       const int stream = warp >> 2, g4 = lane >> 2, t = lane & 3, row0 = warp % 4 * 32 + g4;
       const uint32_t at = tmem + stream * kStreamColumns + (uint32_t(warp % 4 * 32) << 16);
       Soft S;
+      const Pair none(0.f, 0.f);
+      Pair l2[4] = {none, none, none, none}, c2[4][2] = {{none, none}, {none, none}, {none, none}, {none, none}};
+      S.most = __uint_as_float(kUnitMax << 23);
+      S.least = INFINITY;
+      S.split = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         S.m[i] = kNone;
-        S.l[i] = 0.f;
         S.qs[i] = sh.q_scale[row0 + 8 * i];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          S.c[i][g] = S.most[i][g] = 0.f;
-          S.u[i][g] = 1.f;
-          S.q_sum[i][g] = sh.q_sum[g][row0 + 8 * i];
-        }
+        S.u[i][0] = S.u[i][1] = S.most;
+        S.largest[i][0] = S.largest[i][1] = 0.f;
       }
       bool any = false;
       for (int k = stream; k < n; k += 2, ++of_stream) {
@@ -565,14 +628,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         tc_fence_after();
         const PageParams& par = sh.par[buf];
         const int pos = (I.page0 + k) * kKv4Page;
-        if (!any) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float u = unit_for(fmaxf(par.top[0][g], par.top[1][g]) * 0.001953125f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S.u[i][g] = u;
-          }
-        }
         uint64_t seen[4] = {};
         if (pos + kKv4Page > prefix || par.held < kKv4Page) {
 #pragma unroll
@@ -581,9 +636,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
             const uint64_t tree = r < cols ? uint64_t(P.tree[I.b * P.tree_stride + (col0 + r) / P.hpg]) : 0;
             seen[i] = seen_of(tree, prefix, pos, par.held);
           }
-          soft_page<true>(S, par, at, any, seen, t);
+          soft_page<true>(S, l2, c2, par, at, any, seen, t, &sh.q_sum[0][row0]);
         } else {
-          soft_page<false>(S, par, at, any, seen, t);
+          soft_page<false>(S, l2, c2, par, at, any, seen, t, &sh.q_sum[0][row0]);
         }
         any = true;
         tc_fence_before();
@@ -593,184 +648,210 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       wait(&sh.o_full, n_items & 1, 6);
       lost = __any_sync(~0u, lost);
       tc_fence_after();
-      float inv[4][2];
+      float l[4], m[4], c[4][2], inv[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        S.l[i] = row_sum(S.l[i]);
+        float x, y;
+        l2[i].get(x, y);
+        l[i] = row_sum(x + y);
+        m[i] = S.m[i];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          S.c[i][g] = row_sum(S.c[i][g]);
+          c2[i][g].get(x, y);
+          c[i][g] = row_sum(x + y);
           inv[i][g] = 1.f / S.u[i][g];
         }
       }
-      // the second stream's state and values to shared memory, over the operands: their products are done
+      // a stream's values, four rows and 32 columns at a time
+      auto values = [&](int c32, float (&v)[2][16]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_load_16x32(reinterpret_cast<uint32_t(&)[16]>(v[h]), at + kValues + c32 * 32 + (uint32_t(h * 16) << 16));
+        tmem_wait_loads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tie(reinterpret_cast<uint32_t(&)[16]>(v[h]));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int row = 2 * h + (i >> 1 & 1);
+            v[h][i] = any ? fmaf(v[h][i], c32 < 2 ? inv[row][0] : inv[row][1], c32 < 2 ? c[row][0] : c[row][1]) : 0.f;
+          }
+        }
+      };
+      // the second stream's state and values through shared memory, over the operands: their products are done
       float* other = reinterpret_cast<float*>(&sh.op[0][0]) + tid % 128;
-      float f0[4], f1[4], m[4], l[4];
       if (stream == 1) {
+#pragma unroll 1
+        for (int c32 = 0; c32 < 4; ++c32) {
+          float v[2][16];
+          values(c32, v);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) other[(c32 * 32 + h * 16 + i) * 128] = v[h][i];
+        }
         if (t == 0)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            sh.other_m[row0 + 8 * i] = S.m[i];
-            sh.other_l[row0 + 8 * i] = S.l[i];
+            sh.other_m[row0 + 8 * i] = m[i];
+            sh.other_l[row0 + 8 * i] = l[i];
           }
       }
-#pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
-        if (pass == 1) {
-          named_bar(1, kSoftWarps * 32);
-          if (stream == 1) break;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float om = sh.other_m[row0 + 8 * i];
-            m[i] = fmaxf(S.m[i], om);
-            f0[i] = ex2(S.m[i] - m[i]);
-            f1[i] = ex2(om - m[i]);
-            l[i] = f0[i] * S.l[i] + f1[i] * sh.other_l[row0 + 8 * i];
-          }
-        }
-        if (pass != 1 - stream) continue;
+      named_bar(1, kSoftWarps * 32);
+      if (stream == 0) {
         const bool whole = I.pieces == 1;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t r[2][8];
+        float f0[4], f1[4];
+        float* to[4];  // dimension t of the rows
 #pragma unroll
-          for (int h = 0; h < 2; ++h) tmem_load_16x16(r[h], at + kValues + c * 16 + (uint32_t(h * 16) << 16));
-          tmem_wait_loads();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tie(r[h]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = 2 * h + (i >> 1 & 1);
-              float v = any ? fmaf(__uint_as_float(r[h][i]), c < 4 ? inv[row][0] : inv[row][1], c < 4 ? S.c[row][0] : S.c[row][1]) : 0.f;
-              float* mine = other + (c * 16 + h * 8 + i) * 128;
-              if (stream == 1) {
-                *mine = v;
-                continue;
-              }
-              v = f0[row] * v + f1[row] * *mine;
-              const int rr = row0 + 8 * row;
-              // position 2 t + i % 2 of a piece of eight: dimension t or t + 4
-              const int d = c / 4 * 64 + (c % 4 * 2 + (i >> 2)) * 8 + t + (i & 1) * 4;
-              if (rr < cols) {
-                if (whole) {
-                  const int col = col0 + rr, tok = col / P.hpg;
-                  const int64_t o = (int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg;
-                  P.out[o * kHeadDim + d] = l[row] != 0.f ? v / l[row] : 0.f;
-                } else {
-                  P.partials[int64_t(item) * kTreePartialFloats + rr * kHeadDim + d] = v;
-                }
-              }
-            }
-          }
-        }
-        if (stream == 0 && t == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = row0 + 8 * i;
-            if (rr >= cols) continue;
-            if (whole) {
-              const int col = col0 + rr, tok = col / P.hpg;
-              const int64_t o = (int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg;
-              if (P.lse) P.lse[o] = l[i] != 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
-            } else {
+        for (int i = 0; i < 4; ++i) {
+          const int r = row0 + 8 * i, col = col0 + r, tok = col / P.hpg;
+          const int64_t o = (int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg;
+          const float om = sh.other_m[r], all = fmaxf(m[i], om);
+          f0[i] = ex2(m[i] - all);
+          f1[i] = ex2(om - all);
+          l[i] = f0[i] * l[i] + f1[i] * sh.other_l[r];
+          to[i] = whole ? P.out + o * kHeadDim : P.partials + int64_t(item) * kTreePartialFloats + r * kHeadDim;
+          if (t == 0 && r < cols) {
+            if (!whole) {
               float* ml = P.partials + int64_t(item) * kTreePartialFloats + kTreeRows * kHeadDim;
-              ml[rr] = m[i];
-              ml[kTreeRows + rr] = l[i];
+              ml[r] = all;
+              ml[kTreeRows + r] = l[i];
+            } else if (P.lse) {
+              P.lse[o] = l[i] != 0.f ? (all + log2f(l[i])) * kLn2 : -INFINITY;
             }
           }
+          if (whole) {  // a row without a token is 0
+            const float by = l[i] != 0.f ? 1.f / l[i] : 0.f;
+            f0[i] *= by;
+            f1[i] *= by;
+          }
+          to[i] = r < cols ? to[i] + t : nullptr;
+        }
+#pragma unroll 1
+        for (int c32 = 0; c32 < 4; ++c32) {
+          float v[2][16];
+          values(c32, v);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int row = 2 * h + (i >> 1 & 1);
+              // position 2 t + i % 2 of a piece of eight: dimension t or t + 4
+              if (to[row]) to[row][c32 * 32 + (i >> 2) * 8 + (i & 1) * 4] = f0[row] * v[h][i] + f1[row] * other[(c32 * 32 + h * 16 + i) * 128];
+            }
         }
       }
-    } else if (warp < kCopy) {
-      for (int k = 0; k < n; ++k) {
-        const uint32_t at = pages + k, raw = at % kRaw, buf = at % kOps;
-        wait(&sh.raw_full[raw], at / kRaw & 1, 4);
-        wait(&sh.op_empty[buf], (at / kOps & 1) ^ 1, 5);
-        if (__any_sync(~0u, lost)) {
-          lost = true;
-          break;
+      pages += n;
+      meet();  // queries, operands and values are free again
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp < kCopy) {
+      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const Item I(sh.plan, P, item, lane);
+        const int n = I.page1 - I.page0;
+        meet();
+        for (int k = 0; k < n; ++k) {
+          const uint32_t at = pages + k, raw = at % kRaw, buf = at % kOps;
+          wait(&sh.raw_full[raw], at / kRaw & 1, 4);
+          wait(&sh.op_empty[buf], (at / kOps & 1) ^ 1, 5);
+          if (__any_sync(~0u, lost)) {
+            lost = true;
+            break;
+          }
+          expand_page(sh.raw[raw], sh.op[buf], sh.par[buf], sh.raw_held[raw], tid - kSoftWarps * 32);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.raw_empty[raw]);
+            mbar_arrive(&sh.op_full[buf]);
+          }
         }
-        expand_page(sh.raw[raw], sh.op[buf], sh.par[buf], sh.raw_held[raw], tid - kSoftWarps * 32);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh.raw_empty[raw]);
-          mbar_arrive(&sh.op_full[buf]);
-        }
+        pages += n;
+        meet();  // queries, operands and values are free again
       }
     } else if (warp == kCopy) {
-      for (int k0 = 0; k0 < n && !lost; k0 += 32) {
-        int id = -1;
-        if (k0 + lane < n && (I.page0 + k0 + lane) * kKv4Page < I.len) {
-          id = P.pg.table[int64_t(I.b) * P.pg.max_pages + I.page0 + k0 + lane];
-          if (id < 0 || id >= P.pg.n_pages) {
-            set_device_error(P.pg.status, DEV_BAD_LIST, I.b);
-            id = -1;
-          }
-        }
-        for (int k = k0; k < min(n, k0 + 32); ++k) {
-          const uint32_t at = pages + k, raw = at % kRaw;
-          wait(&sh.raw_empty[raw], (at / kRaw & 1) ^ 1, 4);
-          lost = __any_sync(~0u, lost);
-          if (lost) break;
-          const int page = __shfl_sync(~0u, id, k - k0);
-          if (lane == 0) {
-            // a page that is not there has no tokens; what lies in its place is finite whatever it is
-            sh.raw_held[raw] = page >= 0 ? min(kKv4Page, I.len - (I.page0 + k) * kKv4Page) : 0;
-            if (page >= 0) {
-              mbar_arrive_expect_tx(&sh.raw_full[raw], kKv4PageBytes);
-              bulk_g2s(sh.raw[raw], P.pg.pages + (int64_t(page) * P.pg.hkv + head) * kKv4PageBytes, kKv4PageBytes, &sh.raw_full[raw]);
-            } else {
-              mbar_arrive(&sh.raw_full[raw]);
+      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const Item I(sh.plan, P, item, lane);
+        const int n = I.page1 - I.page0;
+        const int head = I.group % P.pg.hkv;
+        meet();
+        for (int k0 = 0; k0 < n && !lost; k0 += 32) {
+          int id = -1;
+          if (k0 + lane < n && (I.page0 + k0 + lane) * kKv4Page < I.len) {
+            id = P.pg.table[int64_t(I.b) * P.pg.max_pages + I.page0 + k0 + lane];
+            if (id < 0 || id >= P.pg.n_pages) {
+              set_device_error(P.pg.status, DEV_BAD_LIST, I.b);
+              id = -1;
             }
           }
-          __syncwarp();
+          for (int k = k0; k < min(n, k0 + 32); ++k) {
+            const uint32_t at = pages + k, raw = at % kRaw;
+            wait(&sh.raw_empty[raw], (at / kRaw & 1) ^ 1, 4);
+            lost = __any_sync(~0u, lost);
+            if (lost) break;
+            const int page = __shfl_sync(~0u, id, k - k0);
+            if (lane == 0) {
+              // a page that is not there has no tokens; what lies in its place is finite whatever it is
+              sh.raw_held[raw] = page >= 0 ? min(kKv4Page, I.len - (I.page0 + k) * kKv4Page) : 0;
+              if (page >= 0) {
+                mbar_arrive_expect_tx(&sh.raw_full[raw], kKv4PageBytes);
+                bulk_g2s(sh.raw[raw], P.pg.pages + (int64_t(page) * P.pg.hkv + head) * kKv4PageBytes, kKv4PageBytes, &sh.raw_full[raw]);
+              } else {
+                mbar_arrive(&sh.raw_full[raw]);
+              }
+            }
+            __syncwarp();
+          }
         }
+        pages += n;
+        meet();  // queries, operands and values are free again
       }
-    } else if (lane == 0) {
-      const uint32_t by_key = tc_shape(kTreeRows, kKv4Page, false, false, false), by_value = tc_shape(kTreeRows, 64, false, false, true);
-      uint32_t of[2] = {of_stream, of_stream1};
-      auto logits = [&](int k) {
-        const uint32_t at = pages + k, buf = at % kOps;
-        if (!wait(&sh.op_full[buf], at / kOps & 1, 4)) return;
-        tc_fence_after();
-        const uint32_t d = tmem + (k & 1) * kStreamColumns;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const uint64_t a = tc_operand(smem_u32(sh.q[g]), false, 0), b = tc_operand(smem_u32(sh.op[buf] + g * kGroupBytes), false, 0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tc_mma<1>(d + g * 64, a + j * 2, b + j * 2, by_key, j > 0);
+    } else {
+      uint32_t of[2] = {0, 0};  // pages of the streams
+      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const Item I(sh.plan, P, item, lane);
+        const int n = I.page1 - I.page0;
+        meet();
+        if (lane == 0) {
+          const uint32_t by_key = tc_shape(kTreeRows, kKv4Page, false, false, false), by_value = tc_shape(kTreeRows, 64, false, false, true);
+          auto logits = [&](int k) {
+            const uint32_t at = pages + k, buf = at % kOps;
+            if (!wait(&sh.op_full[buf], at / kOps & 1, 4)) return;
+            tc_fence_after();
+            const uint32_t d = tmem + (k & 1) * kStreamColumns;
+    #pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const uint64_t a = tc_operand(smem_u32(sh.q[g]), false, 0), b = tc_operand(smem_u32(sh.op[buf] + g * kGroupBytes), false, 0);
+    #pragma unroll
+              for (int j = 0; j < 4; ++j) tc_mma<1>(d + g * 64, a + j * 2, b + j * 2, by_key, j > 0);
+            }
+            tc_commit<1>(&sh.s_full[k & 1]);
+          };
+          for (int k = 0; k < min(n, 2) && !lost; ++k) logits(k);
+          for (int k = 0; k < n && !lost; ++k) {
+            const uint32_t buf = (pages + k) % kOps;
+            if (!wait(&sh.p_full[k & 1], of[k & 1] & 1, 7)) break;
+            ++of[k & 1];
+            tc_fence_after();
+            const uint32_t s = tmem + (k & 1) * kStreamColumns;
+    #pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const uint64_t b = tc_operand(smem_u32(sh.op[buf] + (2 + g) * kGroupBytes), true, kGroupBytes);
+    #pragma unroll
+              for (int part = 0; part < 2; ++part)
+    #pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  tc_mma_tmem(s + kValues + g * 64, s + j / 2 * 64 + (2 * g + part) * 16 + j % 2 * 8, b + j * 128, by_value, k > 1 || part + j > 0);
+            }
+            tc_commit<1>(&sh.op_empty[buf]);
+            if (k + 2 < n) logits(k + 2);
+          }
+          tc_commit<1>(&sh.o_full);
         }
-        tc_commit<1>(&sh.s_full[k & 1]);
-      };
-      for (int k = 0; k < min(n, 2) && !lost; ++k) logits(k);
-      for (int k = 0; k < n && !lost; ++k) {
-        const uint32_t buf = (pages + k) % kOps;
-        if (!wait(&sh.p_full[k & 1], of[k & 1] & 1, 7)) break;
-        ++of[k & 1];
-        tc_fence_after();
-        const uint32_t s = tmem + (k & 1) * kStreamColumns;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const uint64_t b = tc_operand(smem_u32(sh.op[buf] + (2 + g) * kGroupBytes), true, kGroupBytes);
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tc_mma_tmem(s + kValues + g * 64, s + g * 64 + part * 32 + j * 8, b + j * 128, by_value, k > 1 || part + j > 0);
-        }
-        tc_commit<1>(&sh.op_empty[buf]);
-        if (k + 2 < n) logits(k + 2);
+        pages += n;
+        meet();  // queries, operands and values are free again
       }
-      of_stream = of[0];
-      of_stream1 = of[1];
-      tc_commit<1>(&sh.o_full);
     }
-    pages += n;
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();  // queries, operands and values are free again
-    tc_fence_after();
   }
 
   // no copy or product may be in flight when the CTA ends

@@ -24,11 +24,12 @@ namespace {
 constexpr int kRaw = 4;         // pages on their way
 constexpr int kOps = 4;         // pages as operands
 constexpr int kSoftWarps = 8;   // two streams of four
-constexpr int kCodeWarps = 2;
-constexpr int kTreeThreads = (kSoftWarps + kCodeWarps + 2) * 32;
+constexpr int kCodeWarps = 4;
+constexpr int kTreeThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // and copies, a stream's products each, one idle
 constexpr int kGroupBytes = kKv4Page * 128;      // an operand of one group: 64 tokens x 64 dimensions f16
 constexpr int kOpBytes = 4 * kGroupBytes;        // K's two groups, V's two
-constexpr int kStreamColumns = 256;              // tensor memory of a stream: logits or weights 128, values 128
+constexpr int kHalfPage = 32;                    // tokens that a stream takes at a time
+constexpr int kStreamColumns = 256;              // tensor memory of a stream: two half pages' logits or weights, values
 constexpr int kValues = 128;                     // from here on
 constexpr int kItemCost = 6;                     // what an item costs beyond its pages, in pages
 constexpr float kNone = -3e38f;
@@ -53,7 +54,7 @@ struct __align__(1024) TreeShared {
   PageParams par[kOps];
   float q_sum[2][kTreeRows], q_scale[kTreeRows];
   float other_m[kTreeRows], other_l[kTreeRows];  // the second stream's
-  uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], s_full[2], p_full[2], o_full, drained;
+  uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], s_full[2][2], p_full[2][2], v_done[2], o_full, drained[2];
   uint32_t tmem;
   int raw_held[kRaw];
   TreePlan plan;
@@ -75,10 +76,10 @@ __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<c
 // What h, a rounded pair, lacks of (w0, w1)
 __device__ __forceinline__ uint32_t rest(__half2 h, float w0, float w1) {
   float d0, d1;
-  asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; sub.rn.f32.f16 %0, a, %3; sub.rn.f32.f16 %1, b, %4;}"
+  asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; add.rn.f32.f16 %0, a, %3; add.rn.f32.f16 %1, b, %4;}"
       : "=f"(d0), "=f"(d1)
-      : "r"(bits(h)), "f"(w0), "f"(w1));
-  return bits(__floats2half2_rn(-d0, -d1));
+      : "r"(bits(h) ^ 0x80008000u), "f"(w0), "f"(w1));
+  return bits(__floats2half2_rn(d0, d1));
 }
 
 // Eight codes of a word as f16 numbers n - 8, in the order 0, 4, 1, 5, 2, 6, 3, 7
@@ -119,8 +120,7 @@ __device__ __forceinline__ void expand_page(const uint8_t* raw, uint8_t* op, Pag
       *reinterpret_cast<uint4*>(v + kGroupBytes + piece_at(r + 1, oct)) = codes(__byte_perm(w.z, w.w, 0x7632));
     }
   }
-  static_assert(kCodeWarps * 32 == kKv4Page, "a thread for each token's scales");
-  {
+  if (tid < kKv4Page) {  // two warps: a thread for each token's scales
     const uint8_t* sz = raw + tid / 16 * kKv4TileBytes + kv4_param(tid % 16, 0, false);
     uint2 k = *reinterpret_cast<const uint2*>(sz), v = *reinterpret_cast<const uint2*>(sz + 128);
     if (tid >= held) k = v = make_uint2(0u, 0u);  // behind the end: may hold anything
@@ -252,7 +252,7 @@ __device__ __forceinline__ void rescale_values(uint32_t at, const float (&f)[4][
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t r[16];
-        const uint32_t a = at + kValues + g * 64 + c * 32 + (uint32_t(h * 16) << 16);
+        const uint32_t a = at + g * 64 + c * 32 + (uint32_t(h * 16) << 16);
         tmem_load_16x32(r, a);
         tmem_wait_loads();
         tie(r);
@@ -274,59 +274,34 @@ __device__ __forceinline__ float row_sum(float x) {
   return x + __shfl_xor_sync(~0u, x, 2);
 }
 
-// Tensor memory of a stream: the logits' two accumulators, 64 columns each.  The logits take the place
-// of the second; the weights' parts of tokens 0 .. 31, [group][part] 16 columns, that of the first,
-// those of tokens 32 .. 63 the logits' own.
-constexpr int kLogits = 64;
-
-// Units of their own for the rows and groups of dimensions, where scales lie far apart: by the page's largest
-// scale as long as the row's largest weight is kLeast or more with that, and by that weight otherwise.
-// f: on the sums, as the reference moves; k: on the values.
+// Units of their own for the rows and groups of dimensions, where scales lie far apart: by the half page's
+// largest scale as long as the row's largest weight is kLeast or more with that, and by that weight otherwise.
+// x: the logits; f: on the sums, as the reference moves; k: on the values.
 template <bool EDGE>
-__device__ __forceinline__ void split_units(Soft& S, const PageParams& par, uint32_t at, float by_scale, const float (&f)[4],
-                                         float (&k)[4][2], const uint64_t (&seen)[4], int t) {
-  float w[4][2] = {};
-#pragma unroll 1
-  for (int it = 0; it < 2; ++it)
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      uint32_t x[16];
-      tmem_load_16x32(x, at + kLogits + it * 32 + (uint32_t(h * 16) << 16));
-      tmem_wait_loads();
-      tie(x);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int b8 = it * 4 + b;
-        const float4 vs = par.v[4 * b8 + t][0];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float m = h ? S.m[2 + e] : S.m[e], qs = h ? S.qs[2 + e] : S.qs[e];
-          const uint64_t bits = h ? seen[2 + e] : seen[e];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const bool ok = !EDGE || (bits >> (8 * b8 + 2 * t + j) & 1);
-            const float p = ok ? ex2(fmaf(__uint_as_float(x[4 * b + 2 * e + j]), qs, -m)) : 0.f;
-            // NaN does not count; 2^-9: finite with any s
-            const float w0 = ok ? p * 0.001953125f * (j ? vs.y : vs.x) : 0.f, w1 = ok ? p * 0.001953125f * (j ? vs.w : vs.z) : 0.f;
-            if (h) {
-              w[2 + e][0] = fmaxf(w[2 + e][0], w0);
-              w[2 + e][1] = fmaxf(w[2 + e][1], w1);
-            } else {
-              w[e][0] = fmaxf(w[e][0], w0);
-              w[e][1] = fmaxf(w[e][1], w1);
-            }
-          }
-        }
-      }
-    }
+__device__ __forceinline__ void split_units(Soft& S, const uint32_t (&x)[2][2][16], const float4 (*v)[2], float by_scale,
+                                            const float (&f)[4], float (&k)[4][2], const uint32_t (&seen)[4], int t) {
   float most = 0.f;
 #pragma unroll
-  for (int row = 0; row < 4; ++row)
+  for (int row = 0; row < 4; ++row) {
+    const int h = row >> 1, e = row & 1;
+    float w[2] = {0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const float4 vs = v[4 * b + t][0];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool ok = !EDGE || (seen[row] >> (8 * b + 2 * t + j) & 1);
+        const float p = ex2(fmaf(__uint_as_float(x[h][1][4 * b + 2 * e + j]), S.qs[row], -S.m[row])) * 0.001953125f;
+        // NaN does not count; 2^-9: finite with any s
+        if (ok) w[0] = fmaxf(w[0], p * (j ? vs.y : vs.x));
+        if (ok) w[1] = fmaxf(w[1], p * (j ? vs.w : vs.z));
+      }
+    }
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const float old = S.u[row][g];
       // largest weights, here and in `largest`, times 2^-9
-      const float all = fmaxf(row_max(w[row][g]), f[row] * (S.split ? S.largest[row][g] : kLeast * 0.001953125f / old));
+      const float all = fmaxf(row_max(w[g]), f[row] * (S.split ? S.largest[row][g] : kLeast * 0.001953125f / old));
       float unit = fminf(old, by_scale);
       if (!(all * unit >= kLeast * 0.001953125f && all * unit < kMost * 0.001953125f)) unit = unit_of(int(__float_as_uint(all) >> 23) + 9);
       S.u[row][g] = unit;
@@ -334,69 +309,62 @@ __device__ __forceinline__ void split_units(Soft& S, const PageParams& par, uint
       k[row][g] = unit >= 1.f ? f[row] * unit / old : f[row] * (unit / old);  // in range in between, too
       most = fmaxf(most, unit);
     }
+  }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
   S.most = most;
   S.split = true;
 }
 
-// One page of a stream: its sums of q n' in tensor memory at `at` become weights there.  l, c: sums of
-// the weights and of their products with z, over this thread's even and odd tokens.
-template <bool EDGE>
-__device__ __forceinline__ void soft_page(Soft& S, Pair (&l)[4], Pair (&c)[4][2], const PageParams& par, uint32_t at, bool values,
-                                          const uint64_t (&seen)[4], int t, const float* q_sum) {
+// Half a page of a stream: its sums of q n' in tensor memory at `at` (32 columns a group) become
+// weights there: [group][part] 16 columns.  l, c: sums of the weights and of their products with z, over this
+// thread's even and odd tokens.  settle(): waits until no product writes the values.
+template <bool EDGE, typename F>
+__device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2], const PageParams& par, int half, uint32_t at,
+                                          uint32_t values, bool any, const uint32_t (&seen)[4], int t, const float* q_sum, F settle) {
+  const float4(*kp)[2] = par.k + half * (kHalfPage / 2);
+  const float4(*vp)[2] = par.v + half * (kHalfPage / 2);
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t s[2][2][16];  // [row half][group]; the second group's place takes the logits
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) tmem_load_16x32(s[h][g], at + g * kHalfPage + (uint32_t(h * 16) << 16));
   {
-    float sum[4][2];  // of the queries
+    Pair sum[4][2] = {{Pair(0.f, 0.f), Pair(0.f, 0.f)}, {Pair(0.f, 0.f), Pair(0.f, 0.f)}, {Pair(0.f, 0.f), Pair(0.f, 0.f)}, {Pair(0.f, 0.f), Pair(0.f, 0.f)}};
 #pragma unroll
-    for (int row = 0; row < 4; ++row) {
-      sum[row][0] = q_sum[8 * row];
-      sum[row][1] = q_sum[kTreeRows + 8 * row];
+    for (int row = 0; row < 4; ++row) {  // of the queries
+      sum[row][0] = Pair(q_sum[8 * row], q_sum[8 * row]);
+      sum[row][1] = Pair(q_sum[kTreeRows + 8 * row], q_sum[kTreeRows + 8 * row]);
     }
-#pragma unroll 1
-    for (int it = 0; it < 2; ++it) {
-      uint32_t s[2][2][16];  // [row half][group]
+    tmem_wait_loads();
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int g = 0; g < 2; ++g) tmem_load_16x32(s[h][g], at + g * 64 + it * 32 + (uint32_t(h * 16) << 16));
-      tmem_wait_loads();
+      for (int g = 0; g < 2; ++g) tie(s[h][g]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int b = 0; b < 4; ++b) {
+      const float4 ks = kp[4 * b + t][0], kz = kp[4 * b + t][1];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) tie(s[h][g]);
+      for (int row = 0; row < 4; ++row) {
+        const int h = row >> 1, i = 4 * b + 2 * (row & 1);
+        Pair y = fma2(Pair(kz.x, kz.y), sum[row][0], mul2(Pair(kz.z, kz.w), sum[row][1]));
+        y = fma2(Pair(ks.x, ks.y), Pair(__uint_as_float(s[h][0][i]), __uint_as_float(s[h][0][i + 1])), y);
+        y = fma2(Pair(ks.z, ks.w), Pair(__uint_as_float(s[h][1][i]), __uint_as_float(s[h][1][i + 1])), y);
+        float x[2];
+        y.get(x[0], x[1]);
+        if (EDGE)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int b8 = it * 4 + b;
-        const float4 ks = par.k[4 * b8 + t][0], kz = par.k[4 * b8 + t][1];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = 2 * h + e, i = 4 * b + 2 * e;
-            Pair y = mul2(Pair(ks.x, ks.y), Pair(__uint_as_float(s[h][0][i]), __uint_as_float(s[h][0][i + 1])));
-            y = fma2(Pair(ks.z, ks.w), Pair(__uint_as_float(s[h][1][i]), __uint_as_float(s[h][1][i + 1])), y);
-            y = fma2(Pair(kz.x, kz.y), Pair(sum[row][0], sum[row][0]), y);
-            y = fma2(Pair(kz.z, kz.w), Pair(sum[row][1], sum[row][1]), y);
-            float x[2];
-            y.get(x[0], x[1]);
-            if (EDGE)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                if (!(seen[row] >> (8 * b8 + 2 * t + j) & 1)) x[j] = -INFINITY;
-            mx[row] = fmaxf(mx[row], fmaxf(x[0], x[1]));
-            s[h][1][i] = __float_as_uint(x[0]);
-            s[h][1][i + 1] = __float_as_uint(x[1]);
-          }
+          for (int j = 0; j < 2; ++j)
+            if (!(seen[row] >> (8 * b + 2 * t + j) & 1)) x[j] = -INFINITY;
+        mx[row] = fmaxf(mx[row], fmaxf(x[0], x[1]));
+        s[h][1][i] = __float_as_uint(x[0]);
+        s[h][1][i + 1] = __float_as_uint(x[1]);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) tmem_store_16x32(at + kLogits + it * 32 + (uint32_t(h * 16) << 16), s[h][1]);
     }
-    tmem_wait_stores();
   }
   // A new reference, or new units, only where the old ones may no longer do.
-  const uint32_t top = max(par.top[0], par.top[1]);
-  bool over = __uint_as_float(top << 16) * S.most >= kMaxScale;
+  bool over = __uint_as_float(par.top[half] << 16) * S.most >= kMaxScale;
 #pragma unroll
   for (int row = 0; row < 4; ++row) {
     mx[row] *= S.qs[row];
@@ -414,10 +382,10 @@ __device__ __forceinline__ void soft_page(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
       c[row][0] = mul2(c[row][0], f2);
       c[row][1] = mul2(c[row][1], f2);
     }
-    // One unit for all while that serves them: where a row's reference moves, a token of this page
-    // has weight 1 in it, and so at least the page's smallest scale.
-    const float low = __uint_as_float(min(par.low[0], par.low[1]) << 16);
-    const float by_scale = unit_of(int(top >> 7)), unit = fminf(S.most, by_scale), ratio = unit / S.most;
+    // One unit for all while that serves them: where a row's reference moves, a token of this half page
+    // has weight 1 in it, and so at least its smallest scale.
+    const float low = __uint_as_float(par.low[half] << 16);
+    const float by_scale = unit_of(int(par.top[half] >> 7)), unit = fminf(S.most, by_scale), ratio = unit / S.most;
     S.least = fminf(S.least * ratio, low * unit);
     if (!S.split && S.least >= kLeast) {
       S.most = unit;
@@ -427,72 +395,64 @@ __device__ __forceinline__ void soft_page(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
         k[row][0] = k[row][1] = f[row] * ratio;
       }
     } else {
-      split_units<EDGE>(S, par, at, by_scale, f, k, seen, t);
+      split_units<EDGE>(S, s, vp, by_scale, f, k, seen, t);
     }
-    if (values) rescale_values(at, k);
+    if (any) {
+      settle();
+      rescale_values(values, k);
+    }
   }
-#pragma unroll 1
-  for (int it = 0; it < 2; ++it) {
-    uint32_t x[2][16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) tmem_load_16x32(x[h], at + kLogits + it * 32 + (uint32_t(h * 16) << 16));
-    tmem_wait_loads();
-    tie(x[0]);
-    tie(x[1]);
+  for (int ch = 0; ch < 2; ++ch) {
+    uint32_t part[2][2][2][4];  // [row half][group][part]
 #pragma unroll
-    for (int ch = 0; ch < 2; ++ch) {
-      uint32_t part[2][2][2][4];  // [row half][group][part]
+    for (int j = 0; j < 2; ++j) {
+      const int b = ch * 2 + j;
+      const float4 vs = vp[4 * b + t][0], vz = vp[4 * b + t][1];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int b = ch * 2 + j, b8 = it * 4 + b;
-        const float4 vs = par.v[4 * b8 + t][0], vz = par.v[4 * b8 + t][1];
+      for (int row = 0; row < 4; ++row) {
+        const int h = row >> 1, e = row & 1, i = 4 * b + 2 * e;
+        float p[2];
+        fma2(Pair(__uint_as_float(s[h][1][i]), __uint_as_float(s[h][1][i + 1])), Pair(S.qs[row], S.qs[row]), Pair(-S.m[row], -S.m[row]))
+            .get(p[0], p[1]);
+        bool ok[2] = {true, true};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = 2 * h + e, i = 4 * b + 2 * e;
-            float p[2];
-            fma2(Pair(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1])), Pair(S.qs[row], S.qs[row]), Pair(-S.m[row], -S.m[row]))
-                .get(p[0], p[1]);
-            bool ok[2] = {true, true};
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              p[n] = ex2(p[n]);
-              if (EDGE) {
-                ok[n] = seen[row] >> (8 * b8 + 2 * t + n) & 1;
-                if (!ok[n]) p[n] = 0.f;
-              }
-            }
-            const Pair pp(p[0], p[1]);
-            l[row] = add2(l[row], pp);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              float z0 = g ? vz.z : vz.x, z1 = g ? vz.w : vz.y;
-              if (EDGE) {  // what is not seen may hold NaN
-                if (!ok[0]) z0 = 0.f;
-                if (!ok[1]) z1 = 0.f;
-              }
-              c[row][g] = fma2(pp, Pair(z0, z1), c[row][g]);
-              float w[2];
-              // in this order: a large s with the unit of a row without weight on it may overflow
-              mul2(mul2(pp, Pair(S.u[row][g], S.u[row][g])), g ? Pair(vs.z, vs.w) : Pair(vs.x, vs.y)).get(w[0], w[1]);
-              if (EDGE) {
-                if (!ok[0]) w[0] = 0.f;
-                if (!ok[1]) w[1] = 0.f;
-              }
-              const __half2 hi = __floats2half2_rn(w[0], w[1]);
-              part[h][g][0][2 * j + e] = bits(hi);
-              part[h][g][1][2 * j + e] = rest(hi, w[0], w[1]);
-            }
+        for (int n = 0; n < 2; ++n) {
+          p[n] = ex2(p[n]);
+          if (EDGE) {
+            ok[n] = seen[row] >> (8 * b + 2 * t + n) & 1;
+            if (!ok[n]) p[n] = 0.f;
           }
+        }
+        const Pair pp(p[0], p[1]);
+        l[row] = add2(l[row], pp);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float z0 = g ? vz.z : vz.x, z1 = g ? vz.w : vz.y;
+          if (EDGE) {  // what is not seen may hold NaN
+            if (!ok[0]) z0 = 0.f;
+            if (!ok[1]) z1 = 0.f;
+          }
+          c[row][g] = fma2(pp, Pair(z0, z1), c[row][g]);
+          float w[2];
+          // in this order: a large s with the unit of a row without weight on it may overflow
+          mul2(mul2(pp, Pair(S.u[row][g], S.u[row][g])), g ? Pair(vs.z, vs.w) : Pair(vs.x, vs.y)).get(w[0], w[1]);
+          if (EDGE) {
+            if (!ok[0]) w[0] = 0.f;
+            if (!ok[1]) w[1] = 0.f;
+          }
+          const __half2 hi = __floats2half2_rn(w[0], w[1]);
+          part[h][g][0][2 * j + e] = bits(hi);
+          part[h][g][1][2 * j + e] = rest(hi, w[0], w[1]);
+        }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) tmem_store_16x8(at + it * 64 + (2 * g + n) * 16 + ch * 8 + (uint32_t(h * 16) << 16), part[h][g][n]);
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) tmem_store_16x8(at + (2 * g + n) * 16 + ch * 8 + (uint32_t(h * 16) << 16), part[h][g][n]);
   }
   tmem_wait_stores();
 }
@@ -502,7 +462,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   TreeShared& sh = *reinterpret_cast<TreeShared*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kCopy = kSoftWarps + kCodeWarps, kMma = kCopy + 1;
+  constexpr int kCopy = kSoftWarps + kCodeWarps, kMma = kCopy + 1;  // and kMma + 1
   if (tid == 0) {
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&sh.raw_full[i], 1);
@@ -513,11 +473,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       mbar_init(&sh.op_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sh.s_full[i][h], 1);
+        mbar_init(&sh.p_full[i][h], 4);
+      }
+      mbar_init(&sh.v_done[i], 1);
     }
-    mbar_init(&sh.o_full, 1);
-    mbar_init(&sh.drained, 1);
+    mbar_init(&sh.o_full, 2);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.drained[i], 1);
     fence_mbar_init();
   }
   if (warp == kMma) tmem_alloc<1>(&sh.tmem, 512);
@@ -545,10 +508,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
     tc_fence_after();
   };
 
-  // Each role goes through the items on its own: the softmax threads have 216 registers, the others 72
-  // (256 x 216 + 128 x 72 = 384 x 168, what the CTA was launched with).
+  // Each role goes through the items on its own: the softmax threads have 184 registers, the others 72
+  // (256 x 184 + 256 x 72 = 512 x 128, what the CTA was launched with).
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     uint32_t of_stream = 0, n_items = 0;  // pages of the stream, items
     for (int item = blockIdx.x; item < items; item += gridDim.x, ++n_items) {
       const Item I(sh.plan, P, item, lane);
@@ -557,47 +520,52 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       const int n = I.page1 - I.page0;
       const int prefix = min(max(P.first[I.b], 0), cap);
       // the queries, a row at a time
+      // two rows at a time: a lane has dimensions 8 (lane % 16) .. + 7 of one, a piece of its operand
       constexpr int kEach = kTreeRows / kSoftWarps;
-      uint2 in[kEach];  // all on their way at once
+#pragma unroll 1
+      for (int i0 = 0; i0 < kEach; i0 += 8) {
+        uint4 in[4];
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int r = warp * kEach + i;
-        in[i] = make_uint2(0, 0);
-        if (r < cols) {
-          const int col = col0 + r, tok = col / P.hpg;
-          const T* q = static_cast<const T*>(P.q) +
-                       ((int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg) * kHeadDim;
-          asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(in[i].x), "=r"(in[i].y) : "l"(q + 4 * lane));
-        }
-      }
-#pragma unroll 4
-      for (int i = 0; i < kEach; ++i) {
-        const int r = warp * kEach + i;
-        float x[4], big = 0.f;
-        const T* e4 = reinterpret_cast<const T*>(&in[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = q_value(e4[j]);
-          big = fmaxf(big, fabsf(x[j]));
+        for (int i = 0; i < 4; ++i) {
+          const int r = warp * kEach + i0 + 2 * i + (lane >> 4), col = col0 + r, tok = col / P.hpg;
+          in[i] = make_uint4(0, 0, 0, 0);
+          if (r < cols) {
+            const T* q = static_cast<const T*>(P.q) +
+                         ((int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg) * kHeadDim + 8 * (lane & 15);
+            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(in[i].x), "=r"(in[i].y), "=r"(in[i].z), "=r"(in[i].w) : "l"(q));
+          }
         }
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
-        // power of two that brings the largest element to 2^13 .. 2^14
-        const int e = min(max(int(__float_as_uint(big) >> 23) - 127, -113), 127);
-        const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
-        float sum = 0.f;
-        // dimension d of a group: piece d / 8, at 2 (d % 4) + d / 4 % 2 of its eight (codes())
-        const uint32_t to = (lane >> 4) * (kTreeRows * 128) + piece_at(r, lane >> 1 & 7) + (lane & 1) * 2;
+        for (int i = 0; i < 4; ++i) {
+          const int r = warp * kEach + i0 + 2 * i + (lane >> 4);
+          const T* e8 = reinterpret_cast<const T*>(&in[i]);
+          float x[8], big = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __half v = __float2half_rn(x[j] * up);
-          sum += __half2float(v);
-          *reinterpret_cast<__half*>(&sh.q[0][0] + to + j * 4) = v;
+          for (int j = 0; j < 8; ++j) {
+            x[j] = q_value(e8[j]);
+            big = fmaxf(big, fabsf(x[j]));
+          }
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+          // power of two that brings the largest element to 2^13 .. 2^14
+          const int e = min(max(int(__float_as_uint(big) >> 23) - 127, -113), 127);
+          const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+          float sum = 0.f;
+          uint32_t w[4];  // in the order of codes(): 0, 4, 1, 5, 2, 6, 3, 7
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __half2 v = __floats2half2_rn(x[j] * up, x[j + 4] * up);
+            const float2 f = __half22float2(v);
+            sum += f.x + f.y;
+            w[j] = bits(v);
+          }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+          const int g = lane >> 3 & 1;
+          *reinterpret_cast<uint4*>(&sh.q[g][piece_at(r, lane & 7)]) = make_uint4(w[0], w[1], w[2], w[3]);
+          if ((lane & 7) == 0) sh.q_sum[g][r] = big < INFINITY ? sum : NAN;
+          if ((lane & 15) == 0) sh.q_scale[r] = P.scale_log2 * __uint_as_float(uint32_t(127 - 13 + e) << 23);
         }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        if ((lane & 15) == 0) sh.q_sum[lane >> 4][r] = big < INFINITY ? sum : NAN;
-        if (lane == 0) sh.q_scale[r] = P.scale_log2 * __uint_as_float(uint32_t(127 - 13 + e) << 23);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       meet();
@@ -620,30 +588,39 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       for (int k = stream; k < n; k += 2, ++of_stream) {
         const uint32_t buf = (pages + k) % kOps;
         wait(&sh.op_full[buf], (pages + k) / kOps & 1, 4);
-        wait(&sh.s_full[stream], of_stream & 1, 5);
-        if (__any_sync(~0u, lost)) {
-          lost = true;
-          break;
-        }
-        tc_fence_after();
         const PageParams& par = sh.par[buf];
         const int pos = (I.page0 + k) * kKv4Page;
-        uint64_t seen[4] = {};
-        if (pos + kKv4Page > prefix || par.held < kKv4Page) {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          wait(&sh.s_full[stream][half], of_stream & 1, 5);
+          if (__any_sync(~0u, lost)) lost = true;
+          if (lost) break;
+          tc_fence_after();
+          // the products with the weights of the half page before
+          auto settle = [&]() {
+            wait(&sh.v_done[stream], (2 * of_stream + half + 1) & 1, 6);
+            tc_fence_after();
+            __syncwarp();
+          };
+          uint32_t seen[4] = {};
+          const uint32_t a = at + half * (2 * kHalfPage);
+          if (pos + (half + 1) * kHalfPage > prefix || par.held < (half + 1) * kHalfPage) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = row0 + 8 * i;
-            const uint64_t tree = r < cols ? uint64_t(P.tree[I.b * P.tree_stride + (col0 + r) / P.hpg]) : 0;
-            seen[i] = seen_of(tree, prefix, pos, par.held);
+            for (int i = 0; i < 4; ++i) {
+              const int r = row0 + 8 * i;
+              const uint64_t tree = r < cols ? uint64_t(P.tree[I.b * P.tree_stride + (col0 + r) / P.hpg]) : 0;
+              seen[i] = uint32_t(seen_of(tree, prefix, pos, par.held) >> (half * kHalfPage));
+            }
+            soft_half<true>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[0][row0], settle);
+          } else {
+            soft_half<false>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[0][row0], settle);
           }
-          soft_page<true>(S, l2, c2, par, at, any, seen, t, &sh.q_sum[0][row0]);
-        } else {
-          soft_page<false>(S, l2, c2, par, at, any, seen, t, &sh.q_sum[0][row0]);
+          any = true;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[stream][half]);
         }
-        any = true;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[stream]);
+        if (lost) break;
       }
       wait(&sh.o_full, n_items & 1, 6);
       lost = __any_sync(~0u, lost);
@@ -807,46 +784,66 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         meet();  // queries, operands and values are free again
       }
     } else {
-      uint32_t of[2] = {0, 0};  // pages of the streams
+      // the whole warp, with operands that are the same in all its threads (tc_mma_warp)
+      auto same = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };
+      auto wait_warp = [&](uint64_t* bar, uint32_t parity, int which) {
+        wait(bar, parity, which);
+        lost = __any_sync(~0u, lost);
+        return !lost;
+      };
+      const uint32_t by_key = tc_shape(kTreeRows, kHalfPage, false, false, false), by_value = tc_shape(kTreeRows, 64, false, false, true);
+      const uint32_t tmem0 = same(tmem), q0 = same(smem_u32(sh.q[0])), op0 = same(smem_u32(sh.op[0]));
+      const uint64_t q_desc = tc_operand(q0, false, 0), k_desc = tc_operand(op0, false, 0),
+                     v_desc = tc_operand(op0 + 2 * kGroupBytes, true, kGroupBytes);
+      const int stream = same(warp - kMma) & 1;
+      const uint32_t d0 = tmem0 + stream * kStreamColumns;
+      uint32_t done = 0;  // pages of the stream
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const Item I(sh.plan, P, item, lane);
-        const int n = I.page1 - I.page0;
+        const int n = same(I.page1 - I.page0);
+        const uint32_t base = same(pages);
         meet();
-        if (lane == 0) {
-          const uint32_t by_key = tc_shape(kTreeRows, kKv4Page, false, false, false), by_value = tc_shape(kTreeRows, 64, false, false, true);
-          auto logits = [&](int k) {
-            const uint32_t at = pages + k, buf = at % kOps;
-            if (!wait(&sh.op_full[buf], at / kOps & 1, 4)) return;
+        if (warp <= kMma + 1) {
+          auto logits = [&](int k, int half) {
+            const uint32_t buf = (base + k) % kOps;
+            if (!wait_warp(&sh.op_full[buf], (base + k) / kOps & 1, 4)) return;
             tc_fence_after();
-            const uint32_t d = tmem + (k & 1) * kStreamColumns;
-    #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const uint64_t a = tc_operand(smem_u32(sh.q[g]), false, 0), b = tc_operand(smem_u32(sh.op[buf] + g * kGroupBytes), false, 0);
-    #pragma unroll
-              for (int j = 0; j < 4; ++j) tc_mma<1>(d + g * 64, a + j * 2, b + j * 2, by_key, j > 0);
-            }
-            tc_commit<1>(&sh.s_full[k & 1]);
+            const uint32_t d = d0 + half * (2 * kHalfPage);
+            const uint64_t b = k_desc + buf * (kOpBytes / 16) + half * (kHalfPage * 128 / 16);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tc_mma_warp(d + g * kHalfPage, q_desc + g * (kTreeRows * 128 / 16) + j * 2, b + g * (kGroupBytes / 16) + j * 2, by_key, j > 0);
+            tc_commit_warp(&sh.s_full[stream][half]);
           };
-          for (int k = 0; k < min(n, 2) && !lost; ++k) logits(k);
-          for (int k = 0; k < n && !lost; ++k) {
-            const uint32_t buf = (pages + k) % kOps;
-            if (!wait(&sh.p_full[k & 1], of[k & 1] & 1, 7)) break;
-            ++of[k & 1];
-            tc_fence_after();
-            const uint32_t s = tmem + (k & 1) * kStreamColumns;
-    #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const uint64_t b = tc_operand(smem_u32(sh.op[buf] + (2 + g) * kGroupBytes), true, kGroupBytes);
-    #pragma unroll
-              for (int part = 0; part < 2; ++part)
-    #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  tc_mma_tmem(s + kValues + g * 64, s + j / 2 * 64 + (2 * g + part) * 16 + j % 2 * 8, b + j * 128, by_value, k > 1 || part + j > 0);
-            }
-            tc_commit<1>(&sh.op_empty[buf]);
-            if (k + 2 < n) logits(k + 2);
+          if (stream < n) {
+            logits(stream, 0);
+            if (!lost) logits(stream, 1);
           }
-          tc_commit<1>(&sh.o_full);
+          for (int k = stream; k < n && !lost; k += 2, ++done) {
+            const uint32_t buf = (base + k) % kOps;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              if (!wait_warp(&sh.p_full[stream][half], done & 1, 7)) break;
+              tc_fence_after();
+              const uint32_t a = d0 + half * (2 * kHalfPage);
+              const uint64_t b = v_desc + buf * (kOpBytes / 16) + half * (kHalfPage * 128 / 16);
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j)
+                    tc_mma_tmem_warp(d0 + kValues + g * 64, a + (2 * g + part) * 16 + j * 8, b + g * (kGroupBytes / 16) + j * 128, by_value,
+                                     k > 1 || half > 0 || part + j > 0);
+              tc_commit_warp(&sh.v_done[stream]);
+              if (half == 1) tc_commit_warp(&sh.op_empty[buf]);
+              if (k + 2 < n) logits(k + 2, half);
+              if (lost) break;
+            }
+          }
+          tc_commit_warp(&sh.o_full);
         }
         pages += n;
         meet();  // queries, operands and values are free again
@@ -859,9 +856,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
     for (uint32_t i = pages < kRaw ? 0 : pages - kRaw; i < pages; ++i)
       if (!mbar_wait_parked(&sh.raw_full[i % kRaw], i / kRaw & 1, kTreeWaitNs)) break;
   }
-  if (warp == kMma && lane == 0) {
-    tc_commit<1>(&sh.drained);
-    mbar_wait_parked(&sh.drained, 0, kTreeWaitNs);
+  if (warp == kMma || warp == kMma + 1) {
+    tc_commit_warp(&sh.drained[warp - kMma]);
+    mbar_wait_parked(&sh.drained[warp - kMma], 0, kTreeWaitNs);
   }
   __syncwarp();
   tc_fence_before();

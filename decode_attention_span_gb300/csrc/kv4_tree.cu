@@ -1,14 +1,14 @@
 // sekv_kv4_tree_attention for many (token, head) columns: 128 of them side by side on the fifth
 // generation's tensor cores, one pass over the cache for all.
 //
-// Mathematics: as in kv4_attn.cu, no K or V value is rebuilt.  With codes n and n' = n - 8,
-//   K^ = (z + 8 s) + s n',   q . K^ = sum over groups g of  s_g (sum_d q_d n'_d) + (z_g + 8 s_g) (sum_d q_d)
-//   sum_j p_j V^_j = sum_j (p_j s_j) n'_j + sum_j p_j (z_j + 8 s_j)
-// The codes become f16 numbers (exact) in shared memory, once for the 128 columns; the two groups
-// of dimensions have accumulators of their own, because a token's scales differ between them.  The
-// weights p_j s_j u enter as the sum of two f16 numbers (22 bits); u is a power of two for each column
-// and group, moved where the column's largest weight so far would leave [kLeast, kMost]: no token takes
-// bits from the others by the size of its values alone.
+// Mathematics.  A group's values z + s n (n 0 .. 15) are z' + s n' with n' = n - 8 and z' = z + 8 s.  s has
+// eight significant bits and n' three (or is -8), so s n' is an f16 number exactly, up to a power of two:
+//   q . K^ = g_t (sum_d q_d k'_d) + sum over groups of z' (sum_d q_d),    k' = s n' / g_t
+//   sum_t p_t V^_t = sum_t (p_t f_t) v'_t + sum_t p_t z'_t,               v' = s n' / f_t
+// with g_t and f_t powers of two that bring a token's larger scale to 2^kTop .. twice that (the smaller one
+// stays exact down to 2^-25 of it).  The weights p_t f_t u enter as the sum of two f16 numbers (22
+// bits); u is a power of two for each column, moved where its largest weight would leave f16's range: no token
+// takes bits from the others by the size of its values alone.
 #include <math.h>
 
 #include <algorithm>
@@ -22,14 +22,16 @@ using namespace sekv;
 namespace {
 
 constexpr int kRaw = 4;         // pages on their way
-constexpr int kOps = 4;         // pages as operands
+constexpr int kKeys = 3;        // pages' keys as operands, and values
+constexpr int kVals = 5;
 constexpr int kSoftWarps = 8;   // two streams of four
-constexpr int kCodeWarps = 4;
+constexpr int kCodeWarps = 8;
 constexpr int kTreeThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // and copies, a stream's products each, one idle
 constexpr int kGroupBytes = kKv4Page * 128;      // an operand of one group: 64 tokens x 64 dimensions f16
-constexpr int kOpBytes = 4 * kGroupBytes;        // K's two groups, V's two
+constexpr int kOpBytes = 2 * kGroupBytes;
+constexpr int kTop = 8;
 constexpr int kHalfPage = 32;                    // tokens that a stream takes at a time
-constexpr int kStreamColumns = 256;              // tensor memory of a stream: two half pages' logits or weights, values
+constexpr int kStreamColumns = 256;              // tensor memory of a stream: two pages' logits or weights, 64 columns each, and the values
 constexpr int kValues = 128;                     // from here on
 constexpr int kItemCost = 6;                     // what an item costs beyond its pages, in pages
 constexpr float kNone = -3e38f;
@@ -40,27 +42,31 @@ constexpr int kUnitTop = 5;             // a unit brings what it is made for to 
 constexpr uint32_t kUnitMax = 127 + 118;
 constexpr uint64_t kTreeWaitNs = 2000000000ull;
 
+// Of tokens 2 i and 2 i + 1, keys (k) and values (v): the powers of two and z' of the first group (a), z' of
+// the second (b)
 struct PageParams {
-  float4 k[kKv4Page / 2][2];  // tokens 2 i, 2 i + 1: (s0, s0', s1, s1'), (z0, z0', z1, z1'), z with 8 s
-  float4 v[kKv4Page / 2][2];
-  uint32_t top[2], low[2];    // V's largest scale and smallest, of 32 tokens: bf16
-  int held;                   // tokens of the page that the sequence has
+  float4 ka[kKv4Page / 2], va[kKv4Page / 2];
+  float2 kb[kKv4Page / 2], vb[kKv4Page / 2];
+  int top[2], low[2];  // exponents of the largest and the smallest f of 32 tokens
+  int held;            // tokens of the page that the sequence has
 };
 
 struct __align__(1024) TreeShared {
   uint8_t q[2][kTreeRows * 128];  // the columns' queries: a group of dimensions each
-  uint8_t op[kOps][kOpBytes];
+  uint8_t key[kKeys][kOpBytes];
+  uint8_t val[kVals][kOpBytes];
   uint8_t raw[kRaw][kKv4PageBytes];
-  PageParams par[kOps];
+  PageParams par[kVals];
   float q_sum[2][kTreeRows], q_scale[kTreeRows];
   float other_m[kTreeRows], other_l[kTreeRows];  // the second stream's
-  uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], s_full[2][2], p_full[2][2], v_done[2], o_full, drained[2];
+  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kKeys], k_empty[kKeys], v_full[kVals], v_empty[kVals];
+  uint64_t s_full[2][2], p_full[2][2][2], v_done[2], o_full, drained[2];
   uint32_t tmem;
   int raw_held[kRaw];
   TreePlan plan;
 };
 static_assert(sizeof(TreeShared) + 1024 <= 227 * 1024, "shared memory of a CTA");
-static_assert(kOps * kOpBytes >= kTreeRows * kHeadDim * 4, "the second stream's values lie over the operands");
+static_assert(kVals * kOpBytes >= kTreeRows * kHeadDim * 4, "the second stream's values lie over the operands");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -82,62 +88,79 @@ __device__ __forceinline__ uint32_t rest(__half2 h, float w0, float w1) {
   return bits(__floats2half2_rn(d0, d1));
 }
 
-// Eight codes of a word as f16 numbers n - 8, in the order 0, 4, 1, 5, 2, 6, 3, 7
-__device__ __forceinline__ uint4 codes(uint32_t w) {
+// Eight codes of a word as f16 numbers (n - 8) s, in the order 0, 4, 1, 5, 2, 6, 3, 7
+__device__ __forceinline__ uint4 codes(uint32_t w, __half2 s) {
   constexpr uint32_t kMagic = 0x64006400u;  // 1024: a code in the lowest bits adds itself, one above 16 times
   const uint32_t w8 = w >> 8;
   const uint32_t a = (w & 0x000f000fu) | kMagic, b = (w & 0x00f000f0u) | kMagic;
   const uint32_t c = (w8 & 0x000f000fu) | kMagic, d = (w8 & 0x00f000f0u) | kMagic;
   const __half2 less = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f), less16 = __float2half2_rn(-72.f);
   auto h = [](const uint32_t& x) { return *reinterpret_cast<const __half2*>(&x); };
-  return make_uint4(bits(__hadd2(h(a), less)), bits(__hfma2(h(b), sixteenth, less16)), bits(__hadd2(h(c), less)),
-                    bits(__hfma2(h(d), sixteenth, less16)));
+  return make_uint4(bits(__hmul2(__hadd2(h(a), less), s)), bits(__hmul2(__hfma2(h(b), sixteenth, less16), s)),
+                    bits(__hmul2(__hadd2(h(c), less), s)), bits(__hmul2(__hfma2(h(d), sixteenth, less16), s)));
+}
+// A token's scales (bf16 s, z of both groups) over a power of two, whose exponent is returned (1 .. 253).  What
+// is not finite, or not there, counts as 0: its z' is not finite either.
+__device__ __forceinline__ int scales(uint2 w, bool there, __half2& s0, __half2& s1) {
+  uint32_t b0 = w.x & 0xffffu, b1 = w.y & 0xffffu;
+  if (!there || (b0 & 0x7fffu) >= 0x7f80u) b0 = 0;
+  if (!there || (b1 & 0x7fffu) >= 0x7f80u) b1 = 0;
+  const int up = min(254 + kTop - int(max(b0 & 0x7fffu, b1 & 0x7fffu) >> 7), 253);
+  const float by = __uint_as_float(uint32_t(up) << 23);
+  s0 = __float2half2_rn(__uint_as_float(b0 << 16) * by);
+  s1 = __float2half2_rn(__uint_as_float(b1 << 16) * by);
+  return 254 - up;
 }
 // Byte of 16-byte piece c of row r in an operand
 __device__ __forceinline__ uint32_t piece_at(int r, int c) { return uint32_t(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// One page's codes and scales as operands and floats, by the kCodeWarps
-__device__ __forceinline__ void expand_page(const uint8_t* raw, uint8_t* op, PageParams& par, int held, int tid) {
+// One page's keys (or values) as an operand, by the kCodeWarps; `held`: its tokens
+__device__ __forceinline__ void expand_keys(const uint8_t* raw, uint8_t* op, int held, int tid) {
 #pragma unroll
   for (int i = 0; i < 256 / (kCodeWarps * 32); ++i) {
-    const int at = tid + i * kCodeWarps * 32;  // 16 bytes: four words
+    // 16 bytes: dimensions 16 q .. 16 q + 15 of both groups of a token
+    const int at = tid + i * kCodeWarps * 32, r = at / 4, q = at % 4;
     const uint8_t* tile = raw + at / 64 * kKv4TileBytes;
-    {  // K: dimensions 16 q .. 16 q + 15 of both groups
-      const uint4 w = *reinterpret_cast<const uint4*>(tile + at % 64 * 16);
-      const int r = at / 4, q = at % 4;
-      *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q)) = codes(w.x);
-      *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q + 1)) = codes(w.y);
-      *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q)) = codes(w.z);
-      *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q + 1)) = codes(w.w);
-    }
-    {  // V: eight dimensions of two neighbouring tokens and both groups
-      const uint4 w = *reinterpret_cast<const uint4*>(tile + kKv4V + at % 64 * 16);
-      const int r = at / 64 * 16 + at % 64 / 32 * 8 + at % 4 * 2, oct = at % 32 / 4;
-      uint8_t* v = op + 2 * kGroupBytes;
-      *reinterpret_cast<uint4*>(v + piece_at(r, oct)) = codes(__byte_perm(w.x, w.y, 0x5410));
-      *reinterpret_cast<uint4*>(v + piece_at(r + 1, oct)) = codes(__byte_perm(w.x, w.y, 0x7632));
-      *reinterpret_cast<uint4*>(v + kGroupBytes + piece_at(r, oct)) = codes(__byte_perm(w.z, w.w, 0x5410));
-      *reinterpret_cast<uint4*>(v + kGroupBytes + piece_at(r + 1, oct)) = codes(__byte_perm(w.z, w.w, 0x7632));
-    }
+    const uint4 w = *reinterpret_cast<const uint4*>(tile + at % 64 * 16);
+    __half2 s0, s1;
+    scales(*reinterpret_cast<const uint2*>(tile + kv4_param(r % 16, 0, false)), r < held, s0, s1);
+    *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q)) = codes(w.x, s0);
+    *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q + 1)) = codes(w.y, s0);
+    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q)) = codes(w.z, s1);
+    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q + 1)) = codes(w.w, s1);
+  }
+}
+__device__ __forceinline__ void expand_values(const uint8_t* raw, uint8_t* op, PageParams& par, int held, int tid) {
+#pragma unroll
+  for (int i = 0; i < 256 / (kCodeWarps * 32); ++i) {
+    // 16 bytes: eight dimensions of two neighbouring tokens and both groups
+    const int at = tid + i * kCodeWarps * 32, r = at / 64 * 16 + at % 64 / 32 * 8 + at % 4 * 2, oct = at % 32 / 4;
+    const uint8_t* tile = raw + at / 64 * kKv4TileBytes;
+    const uint4 w = *reinterpret_cast<const uint4*>(tile + kKv4V + at % 64 * 16);
+    __half2 s0, s1;
+    scales(*reinterpret_cast<const uint2*>(tile + kv4_param(r % 16, 0, true)), r < held, s0, s1);
+    *reinterpret_cast<uint4*>(op + piece_at(r, oct)) = codes(__byte_perm(w.x, w.y, 0x5410), s0);
+    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, oct)) = codes(__byte_perm(w.z, w.w, 0x5410), s1);
+    scales(*reinterpret_cast<const uint2*>(tile + kv4_param(r % 16 + 1, 0, true)), r + 1 < held, s0, s1);
+    *reinterpret_cast<uint4*>(op + piece_at(r + 1, oct)) = codes(__byte_perm(w.x, w.y, 0x7632), s0);
+    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r + 1, oct)) = codes(__byte_perm(w.z, w.w, 0x7632), s1);
   }
   if (tid < kKv4Page) {  // two warps: a thread for each token's scales
     const uint8_t* sz = raw + tid / 16 * kKv4TileBytes + kv4_param(tid % 16, 0, false);
     uint2 k = *reinterpret_cast<const uint2*>(sz), v = *reinterpret_cast<const uint2*>(sz + 128);
     if (tid >= held) k = v = make_uint2(0u, 0u);  // behind the end: may hold anything
-    auto put = [&](float4 (&p)[2], uint2 w) {
-      float *s = reinterpret_cast<float*>(&p[0]) + tid % 2, *z = reinterpret_cast<float*>(&p[1]) + tid % 2;
-      const float s0 = lo16(w.x), s1 = lo16(w.y);
-      s[0] = s0;
-      s[2] = s1;
-      z[0] = fmaf(8.f, s0, hi16(w.x));
-      z[2] = fmaf(8.f, s1, hi16(w.y));
+    auto put = [&](float4* a, float2* b, uint2 w) {
+      __half2 s0, s1;
+      const int e = scales(w, true, s0, s1);
+      float *pa = reinterpret_cast<float*>(a + tid / 2) + tid % 2, *pb = reinterpret_cast<float*>(b + tid / 2) + tid % 2;
+      pa[0] = __uint_as_float(uint32_t(e) << 23);
+      pa[2] = fmaf(8.f, lo16(w.x), hi16(w.x));
+      pb[0] = fmaf(8.f, lo16(w.y), hi16(w.y));
+      return e;
     };
-    put(par.k[tid / 2], k);
-    put(par.v[tid / 2], v);
-    // bits of numbers that are not negative compare as they do; NaN does not count
-    const uint32_t t0 = v.x & 0x7fffu, t1 = v.y & 0x7fffu;
-    const uint32_t top = __reduce_max_sync(~0u, max(t0 < 0x7f80u ? t0 : 0u, t1 < 0x7f80u ? t1 : 0u));
-    const uint32_t low = __reduce_min_sync(~0u, tid < held ? min(t0, t1) : 0x7f80u);
+    put(par.ka, par.kb, k);
+    const int e = put(par.va, par.vb, v);
+    const int top = __reduce_max_sync(~0u, tid < held ? e : 1), low = __reduce_min_sync(~0u, tid < held ? e : 254);
     if (tid % 32 == 0) {
       par.top[tid / 32] = top;
       par.low[tid / 32] = low;
@@ -228,39 +251,33 @@ __device__ __forceinline__ uint64_t seen_of(uint64_t tree, int prefix, int pos, 
   return held >= 64 ? b : b & ((1ull << max(held, 0)) - 1);
 }
 
-// A softmax thread's part: rows lane / 4 + 8 i (i 0 .. 3) of its warp's 32, and of a page the tokens
-// 8 b + 2 (lane % 4) and the next (b 0 .. 7).
+// A softmax thread's part: rows lane / 4 + 8 i (i 0 .. 3) of its warp's 32, and of half a page the tokens
+// 8 b + 2 (lane % 4) and the next (b 0 .. 3).
 struct Soft {
   float m[4];        // reference of the weights, log2: within 2^8 of the largest; kNone: no token yet
-  float u[4][2];     // units: [group]
-  float largest[4][2];  // the rows' largest weights, once they have units of their own
+  float u[4];        // units
+  float largest[4];  // the rows' largest weights p f times 2^-9, once they have units of their own
   float qs[4];
   float most;        // the largest unit of the warp's rows
   float least;       // what every row's largest weight with its unit is at least
-  bool split;        // the rows and groups have units of their own
+  bool split;        // the rows have units of their own
 };
 
-// Values of this warp's rows times f[row][group]
-__device__ __forceinline__ void rescale_values(uint32_t at, const float (&f)[4][2]) {
+// Values of this warp's rows times f[row]
+__device__ __forceinline__ void rescale_values(uint32_t at, const float (&f)[4]) {
 #pragma unroll 1
-  for (int g = 0; g < 2; ++g) {
-    float by[4];
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) by[i] = g ? f[i][1] : f[i][0];
-#pragma unroll 1
-    for (int c = 0; c < 2; ++c)
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[16];
+      const uint32_t a = at + c * 32 + (uint32_t(h * 16) << 16);
+      tmem_load_16x32(r, a);
+      tmem_wait_loads();
+      tie(r);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t r[16];
-        const uint32_t a = at + g * 64 + c * 32 + (uint32_t(h * 16) << 16);
-        tmem_load_16x32(r, a);
-        tmem_wait_loads();
-        tie(r);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * by[2 * h + (i >> 1 & 1)]);
-        tmem_store_16x32(a, r);
-      }
-  }
+      for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f[2 * h + (i >> 1 & 1)]);
+      tmem_store_16x32(a, r);
+    }
   tmem_wait_stores();
 }
 
@@ -274,41 +291,35 @@ __device__ __forceinline__ float row_sum(float x) {
   return x + __shfl_xor_sync(~0u, x, 2);
 }
 
-// Units of their own for the rows and groups of dimensions, where scales lie far apart: by the half page's
-// largest scale as long as the row's largest weight is kLeast or more with that, and by that weight otherwise.
-// x: the logits; f: on the sums, as the reference moves; k: on the values.
+// Units of their own for the rows, where scales lie far apart: by the half page's largest as long as the
+// row's largest weight is kLeast or more with that, and by that weight otherwise.  x: the logits; f: on the
+// sums, as the reference moves; k: on the values.
 template <bool EDGE>
-__device__ __forceinline__ void split_units(Soft& S, const uint32_t (&x)[2][2][16], const float4 (*v)[2], float by_scale,
-                                            const float (&f)[4], float (&k)[4][2], const uint32_t (&seen)[4], int t) {
+__device__ __forceinline__ void split_units(Soft& S, const uint32_t (&x)[2][16], const float4* va, float by_scale, const float (&f)[4],
+                                            float (&k)[4], const uint32_t (&seen)[4], int t) {
   float most = 0.f;
 #pragma unroll
   for (int row = 0; row < 4; ++row) {
     const int h = row >> 1, e = row & 1;
-    float w[2] = {0.f, 0.f};
+    float w = 0.f;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const float4 vs = v[4 * b + t][0];
+      const float4 v = va[4 * b + t];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const bool ok = !EDGE || (seen[row] >> (8 * b + 2 * t + j) & 1);
-        const float p = ex2(fmaf(__uint_as_float(x[h][1][4 * b + 2 * e + j]), S.qs[row], -S.m[row])) * 0.001953125f;
-        // NaN does not count; 2^-9: finite with any s
-        if (ok) w[0] = fmaxf(w[0], p * (j ? vs.y : vs.x));
-        if (ok) w[1] = fmaxf(w[1], p * (j ? vs.w : vs.z));
+        // 2^-9: finite with any f
+        const float p = ex2(fmaf(__uint_as_float(x[h][4 * b + 2 * e + j]), S.qs[row], -S.m[row])) * 0.001953125f;
+        if (!EDGE || (seen[row] >> (8 * b + 2 * t + j) & 1)) w = fmaxf(w, p * (j ? v.y : v.x));
       }
     }
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const float old = S.u[row][g];
-      // largest weights, here and in `largest`, times 2^-9
-      const float all = fmaxf(row_max(w[g]), f[row] * (S.split ? S.largest[row][g] : kLeast * 0.001953125f / old));
-      float unit = fminf(old, by_scale);
-      if (!(all * unit >= kLeast * 0.001953125f && all * unit < kMost * 0.001953125f)) unit = unit_of(int(__float_as_uint(all) >> 23) + 9);
-      S.u[row][g] = unit;
-      S.largest[row][g] = all;
-      k[row][g] = unit >= 1.f ? f[row] * unit / old : f[row] * (unit / old);  // in range in between, too
-      most = fmaxf(most, unit);
-    }
+    const float old = S.u[row];
+    const float all = fmaxf(row_max(w), f[row] * (S.split ? S.largest[row] : kLeast * 0.001953125f / old));
+    float unit = fminf(old, by_scale);
+    if (!(all * unit >= kLeast * 0.001953125f && all * unit < kMost * 0.001953125f)) unit = unit_of(int(__float_as_uint(all) >> 23) + 9);
+    S.u[row] = unit;
+    S.largest[row] = all;
+    k[row] = unit >= 1.f ? f[row] * unit / old : f[row] * (unit / old);  // in range in between, too
+    most = fmaxf(most, unit);
   }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
@@ -316,41 +327,38 @@ __device__ __forceinline__ void split_units(Soft& S, const uint32_t (&x)[2][2][1
   S.split = true;
 }
 
-// Half a page of a stream: its sums of q n' in tensor memory at `at` (32 columns a group) become
-// weights there: [group][part] 16 columns.  l, c: sums of the weights and of their products with z, over this
-// thread's even and odd tokens.  settle(): waits until no product writes the values.
+// Half a page of a stream: its sums of q k' in 32 columns of tensor memory at `at` become the weights'
+// upper and lower parts there, 16 columns each.  l, c: sums of the weights and of their products with z', over
+// this thread's even and odd tokens.  settle(): waits until no product writes the values.
 template <bool EDGE, typename F>
 __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2], const PageParams& par, int half, uint32_t at,
                                           uint32_t values, bool any, const uint32_t (&seen)[4], int t, const float* q_sum, F settle) {
-  const float4(*kp)[2] = par.k + half * (kHalfPage / 2);
-  const float4(*vp)[2] = par.v + half * (kHalfPage / 2);
+  const float4 *ka = par.ka + half * (kHalfPage / 2), *va = par.va + half * (kHalfPage / 2);
+  const float2 *kb = par.kb + half * (kHalfPage / 2), *vb = par.vb + half * (kHalfPage / 2);
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  uint32_t s[2][2][16];  // [row half][group]; the second group's place takes the logits
+  uint32_t s[2][16];  // [row half]: sums, then logits
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int g = 0; g < 2; ++g) tmem_load_16x32(s[h][g], at + g * kHalfPage + (uint32_t(h * 16) << 16));
+  for (int h = 0; h < 2; ++h) tmem_load_16x32(s[h], at + (uint32_t(h * 16) << 16));
   {
-    Pair sum[4][2] = {{Pair(0.f, 0.f), Pair(0.f, 0.f)}, {Pair(0.f, 0.f), Pair(0.f, 0.f)}, {Pair(0.f, 0.f), Pair(0.f, 0.f)}, {Pair(0.f, 0.f), Pair(0.f, 0.f)}};
+    float sum[4][2];  // of the queries
 #pragma unroll
-    for (int row = 0; row < 4; ++row) {  // of the queries
-      sum[row][0] = Pair(q_sum[8 * row], q_sum[8 * row]);
-      sum[row][1] = Pair(q_sum[kTreeRows + 8 * row], q_sum[kTreeRows + 8 * row]);
+    for (int row = 0; row < 4; ++row) {
+      sum[row][0] = q_sum[8 * row];
+      sum[row][1] = q_sum[kTreeRows + 8 * row];
     }
     tmem_wait_loads();
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) tie(s[h][g]);
+    tie(s[0]);
+    tie(s[1]);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const float4 ks = kp[4 * b + t][0], kz = kp[4 * b + t][1];
+      const float4 a4 = ka[4 * b + t];
+      const float2 b2 = kb[4 * b + t];
 #pragma unroll
       for (int row = 0; row < 4; ++row) {
         const int h = row >> 1, i = 4 * b + 2 * (row & 1);
-        Pair y = fma2(Pair(kz.x, kz.y), sum[row][0], mul2(Pair(kz.z, kz.w), sum[row][1]));
-        y = fma2(Pair(ks.x, ks.y), Pair(__uint_as_float(s[h][0][i]), __uint_as_float(s[h][0][i + 1])), y);
-        y = fma2(Pair(ks.z, ks.w), Pair(__uint_as_float(s[h][1][i]), __uint_as_float(s[h][1][i + 1])), y);
+        Pair y = mul2(Pair(b2.x, b2.y), Pair(sum[row][1], sum[row][1]));
+        y = fma2(Pair(a4.z, a4.w), Pair(sum[row][0], sum[row][0]), y);
+        y = fma2(Pair(a4.x, a4.y), Pair(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), y);
         float x[2];
         y.get(x[0], x[1]);
         if (EDGE)
@@ -358,20 +366,20 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
           for (int j = 0; j < 2; ++j)
             if (!(seen[row] >> (8 * b + 2 * t + j) & 1)) x[j] = -INFINITY;
         mx[row] = fmaxf(mx[row], fmaxf(x[0], x[1]));
-        s[h][1][i] = __float_as_uint(x[0]);
-        s[h][1][i + 1] = __float_as_uint(x[1]);
+        s[h][i] = __float_as_uint(x[0]);
+        s[h][i + 1] = __float_as_uint(x[1]);
       }
     }
   }
   // A new reference, or new units, only where the old ones may no longer do.
-  bool over = __uint_as_float(par.top[half] << 16) * S.most >= kMaxScale;
+  bool over = __uint_as_float(uint32_t(par.top[half]) << 23) * S.most >= kMaxScale;
 #pragma unroll
   for (int row = 0; row < 4; ++row) {
     mx[row] *= S.qs[row];
     over |= mx[row] > S.m[row] + kGrowth;
   }
   if (__any_sync(~0u, over)) {
-    float f[4], k[4][2];
+    float f[4], k[4];
 #pragma unroll
     for (int row = 0; row < 4; ++row) {
       const float m1 = fmaxf(S.m[row], row_max(mx[row]));
@@ -383,19 +391,19 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
       c[row][1] = mul2(c[row][1], f2);
     }
     // One unit for all while that serves them: where a row's reference moves, a token of this half page
-    // has weight 1 in it, and so at least its smallest scale.
-    const float low = __uint_as_float(par.low[half] << 16);
-    const float by_scale = unit_of(int(par.top[half] >> 7)), unit = fminf(S.most, by_scale), ratio = unit / S.most;
+    // has p = 1 in it, and so at least its smallest f.
+    const float low = __uint_as_float(uint32_t(par.low[half]) << 23);
+    const float by_scale = unit_of(par.top[half]), unit = fminf(S.most, by_scale), ratio = unit / S.most;
     S.least = fminf(S.least * ratio, low * unit);
     if (!S.split && S.least >= kLeast) {
       S.most = unit;
 #pragma unroll
       for (int row = 0; row < 4; ++row) {
-        S.u[row][0] = S.u[row][1] = unit;
-        k[row][0] = k[row][1] = f[row] * ratio;
+        S.u[row] = unit;
+        k[row] = f[row] * ratio;
       }
     } else {
-      split_units<EDGE>(S, s, vp, by_scale, f, k, seen, t);
+      split_units<EDGE>(S, s, va, by_scale, f, k, seen, t);
     }
     if (any) {
       settle();
@@ -404,55 +412,40 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
   }
 #pragma unroll
   for (int ch = 0; ch < 2; ++ch) {
-    uint32_t part[2][2][2][4];  // [row half][group][part]
+    uint32_t part[2][2][4];  // [row half][part]
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int b = ch * 2 + j;
-      const float4 vs = vp[4 * b + t][0], vz = vp[4 * b + t][1];
+      const float4 a4 = va[4 * b + t];
+      const float2 b2 = vb[4 * b + t];
 #pragma unroll
       for (int row = 0; row < 4; ++row) {
         const int h = row >> 1, e = row & 1, i = 4 * b + 2 * e;
         float p[2];
-        fma2(Pair(__uint_as_float(s[h][1][i]), __uint_as_float(s[h][1][i + 1])), Pair(S.qs[row], S.qs[row]), Pair(-S.m[row], -S.m[row]))
+        fma2(Pair(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), Pair(S.qs[row], S.qs[row]), Pair(-S.m[row], -S.m[row]))
             .get(p[0], p[1]);
-        bool ok[2] = {true, true};
+        float z[4] = {a4.z, a4.w, b2.x, b2.y};
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           p[n] = ex2(p[n]);
-          if (EDGE) {
-            ok[n] = seen[row] >> (8 * b + 2 * t + n) & 1;
-            if (!ok[n]) p[n] = 0.f;
-          }
+          if (EDGE && !(seen[row] >> (8 * b + 2 * t + n) & 1)) p[n] = z[n] = z[2 + n] = 0.f;  // z' may be NaN there
         }
         const Pair pp(p[0], p[1]);
         l[row] = add2(l[row], pp);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float z0 = g ? vz.z : vz.x, z1 = g ? vz.w : vz.y;
-          if (EDGE) {  // what is not seen may hold NaN
-            if (!ok[0]) z0 = 0.f;
-            if (!ok[1]) z1 = 0.f;
-          }
-          c[row][g] = fma2(pp, Pair(z0, z1), c[row][g]);
-          float w[2];
-          // in this order: a large s with the unit of a row without weight on it may overflow
-          mul2(mul2(pp, Pair(S.u[row][g], S.u[row][g])), g ? Pair(vs.z, vs.w) : Pair(vs.x, vs.y)).get(w[0], w[1]);
-          if (EDGE) {
-            if (!ok[0]) w[0] = 0.f;
-            if (!ok[1]) w[1] = 0.f;
-          }
-          const __half2 hi = __floats2half2_rn(w[0], w[1]);
-          part[h][g][0][2 * j + e] = bits(hi);
-          part[h][g][1][2 * j + e] = rest(hi, w[0], w[1]);
-        }
+        c[row][0] = fma2(pp, Pair(z[0], z[1]), c[row][0]);
+        c[row][1] = fma2(pp, Pair(z[2], z[3]), c[row][1]);
+        float w[2];
+        // in this order: a large f with the unit of a row without weight on it may overflow
+        mul2(mul2(pp, Pair(S.u[row], S.u[row])), Pair(a4.x, a4.y)).get(w[0], w[1]);
+        const __half2 hi = __floats2half2_rn(w[0], w[1]);
+        part[h][0][2 * j + e] = bits(hi);
+        part[h][1][2 * j + e] = rest(hi, w[0], w[1]);
       }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) tmem_store_16x8(at + (2 * g + n) * 16 + ch * 8 + (uint32_t(h * 16) << 16), part[h][g][n]);
+      for (int n = 0; n < 2; ++n) tmem_store_16x8(at + n * 16 + ch * 8 + (uint32_t(h * 16) << 16), part[h][n]);
   }
   tmem_wait_stores();
 }
@@ -468,14 +461,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], kCodeWarps);
     }
-    for (int i = 0; i < kOps; ++i) {
-      mbar_init(&sh.op_full[i], kCodeWarps);
-      mbar_init(&sh.op_empty[i], 1);
+    for (int i = 0; i < kKeys; ++i) {
+      mbar_init(&sh.k_full[i], kCodeWarps);
+      mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVals; ++i) {
+      mbar_init(&sh.v_full[i], kCodeWarps);
+      mbar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&sh.s_full[i][h], 1);
-        mbar_init(&sh.p_full[i][h], 4);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&sh.s_full[i][j], 1);
+        for (int h = 0; h < 2; ++h) mbar_init(&sh.p_full[i][j][h], 4);
       }
       mbar_init(&sh.v_done[i], 1);
     }
@@ -508,10 +505,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
     tc_fence_after();
   };
 
-  // Each role goes through the items on its own: the softmax threads have 184 registers, the others 72
-  // (256 x 184 + 256 x 72 = 512 x 128, what the CTA was launched with).
+  // Each role goes through the items on its own: the softmax threads have 168 registers, the others 48
+  // (256 x 168 + 384 x 48 = 640 x 96, what the CTA was launched with).
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     uint32_t of_stream = 0, n_items = 0;  // pages of the stream, items
     for (int item = blockIdx.x; item < items; item += gridDim.x, ++n_items) {
       const Item I(sh.plan, P, item, lane);
@@ -581,21 +578,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       for (int i = 0; i < 4; ++i) {
         S.m[i] = kNone;
         S.qs[i] = sh.q_scale[row0 + 8 * i];
-        S.u[i][0] = S.u[i][1] = S.most;
-        S.largest[i][0] = S.largest[i][1] = 0.f;
+        S.u[i] = S.most;
+        S.largest[i] = 0.f;
       }
       bool any = false;
       for (int k = stream; k < n; k += 2, ++of_stream) {
-        const uint32_t buf = (pages + k) % kOps;
-        wait(&sh.op_full[buf], (pages + k) / kOps & 1, 4);
+        const uint32_t buf = (pages + k) % kVals, place = of_stream & 1;
+        wait(&sh.v_full[buf], (pages + k) / kVals & 1, 4);
+        wait(&sh.s_full[stream][place], of_stream >> 1 & 1, 5);
+        if (__any_sync(~0u, lost)) lost = true;
+        if (lost) break;
+        tc_fence_after();
         const PageParams& par = sh.par[buf];
         const int pos = (I.page0 + k) * kKv4Page;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          wait(&sh.s_full[stream][half], of_stream & 1, 5);
-          if (__any_sync(~0u, lost)) lost = true;
-          if (lost) break;
-          tc_fence_after();
           // the products with the weights of the half page before
           auto settle = [&]() {
             wait(&sh.v_done[stream], (2 * of_stream + half + 1) & 1, 6);
@@ -603,7 +600,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
             __syncwarp();
           };
           uint32_t seen[4] = {};
-          const uint32_t a = at + half * (2 * kHalfPage);
+          const uint32_t a = at + place * kKv4Page + half * kHalfPage;
           if (pos + (half + 1) * kHalfPage > prefix || par.held < (half + 1) * kHalfPage) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -618,14 +615,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
           any = true;
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_full[stream][half]);
+          if (lane == 0) mbar_arrive(&sh.p_full[stream][place][half]);
         }
-        if (lost) break;
       }
       wait(&sh.o_full, n_items & 1, 6);
       lost = __any_sync(~0u, lost);
       tc_fence_after();
-      float l[4], m[4], c[4][2], inv[4][2];
+      float l[4], m[4], c[4][2], inv[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float x, y;
@@ -636,8 +632,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         for (int g = 0; g < 2; ++g) {
           c2[i][g].get(x, y);
           c[i][g] = row_sum(x + y);
-          inv[i][g] = 1.f / S.u[i][g];
         }
+        inv[i] = 1.f / S.u[i];
       }
       // a stream's values, four rows and 32 columns at a time
       auto values = [&](int c32, float (&v)[2][16]) {
@@ -650,12 +646,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int row = 2 * h + (i >> 1 & 1);
-            v[h][i] = any ? fmaf(v[h][i], c32 < 2 ? inv[row][0] : inv[row][1], c32 < 2 ? c[row][0] : c[row][1]) : 0.f;
+            v[h][i] = any ? fmaf(v[h][i], inv[row], c32 < 2 ? c[row][0] : c[row][1]) : 0.f;
           }
         }
       };
       // the second stream's state and values through shared memory, over the operands: their products are done
-      float* other = reinterpret_cast<float*>(&sh.op[0][0]) + tid % 128;
+      float* other = reinterpret_cast<float*>(&sh.val[0][0]) + tid % 128;
       if (stream == 1) {
 #pragma unroll 1
         for (int c32 = 0; c32 < 4; ++c32) {
@@ -721,26 +717,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       meet();  // queries, operands and values are free again
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp < kCopy) {
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const Item I(sh.plan, P, item, lane);
         const int n = I.page1 - I.page0;
         meet();
         for (int k = 0; k < n; ++k) {
-          const uint32_t at = pages + k, raw = at % kRaw, buf = at % kOps;
+          const uint32_t at = pages + k, raw = at % kRaw, key = at % kKeys, val = at % kVals;
           wait(&sh.raw_full[raw], at / kRaw & 1, 4);
-          wait(&sh.op_empty[buf], (at / kOps & 1) ^ 1, 5);
+          wait(&sh.k_empty[key], (at / kKeys & 1) ^ 1, 5);
           if (__any_sync(~0u, lost)) {
             lost = true;
             break;
           }
-          expand_page(sh.raw[raw], sh.op[buf], sh.par[buf], sh.raw_held[raw], tid - kSoftWarps * 32);
+          const int held = sh.raw_held[raw], me = tid - kSoftWarps * 32;
+          expand_keys(sh.raw[raw], sh.key[key], held, me);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.k_full[key]);
+          wait(&sh.v_empty[val], (at / kVals & 1) ^ 1, 5);
+          if (__any_sync(~0u, lost)) {
+            lost = true;
+            break;
+          }
+          expand_values(sh.raw[raw], sh.val[val], sh.par[val], held, me);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&sh.raw_empty[raw]);
-            mbar_arrive(&sh.op_full[buf]);
+            mbar_arrive(&sh.v_full[val]);
           }
         }
         pages += n;
@@ -791,10 +797,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         lost = __any_sync(~0u, lost);
         return !lost;
       };
-      const uint32_t by_key = tc_shape(kTreeRows, kHalfPage, false, false, false), by_value = tc_shape(kTreeRows, 64, false, false, true);
-      const uint32_t tmem0 = same(tmem), q0 = same(smem_u32(sh.q[0])), op0 = same(smem_u32(sh.op[0]));
-      const uint64_t q_desc = tc_operand(q0, false, 0), k_desc = tc_operand(op0, false, 0),
-                     v_desc = tc_operand(op0 + 2 * kGroupBytes, true, kGroupBytes);
+      const uint32_t by_key = tc_shape(kTreeRows, kKv4Page, false, false, false), by_value = tc_shape(kTreeRows, kHeadDim, false, false, true);
+      const uint32_t tmem0 = same(tmem), q0 = same(smem_u32(sh.q[0])), k0 = same(smem_u32(sh.key[0])), v0 = same(smem_u32(sh.val[0]));
+      const uint64_t q_desc = tc_operand(q0, false, 0), k_desc = tc_operand(k0, false, 0), v_desc = tc_operand(v0, true, kGroupBytes);
       const int stream = same(warp - kMma) & 1;
       const uint32_t d0 = tmem0 + stream * kStreamColumns;
       uint32_t done = 0;  // pages of the stream
@@ -804,44 +809,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         const uint32_t base = same(pages);
         meet();
         if (warp <= kMma + 1) {
-          auto logits = [&](int k, int half) {
-            const uint32_t buf = (base + k) % kOps;
-            if (!wait_warp(&sh.op_full[buf], (base + k) / kOps & 1, 4)) return;
+          auto logits = [&](int k, uint32_t count) {  // page k, the stream's count-th
+            const uint32_t key = (base + k) % kKeys, place = count & 1;
+            if (!wait_warp(&sh.k_full[key], (base + k) / kKeys & 1, 4)) return;
             tc_fence_after();
-            const uint32_t d = d0 + half * (2 * kHalfPage);
-            const uint64_t b = k_desc + buf * (kOpBytes / 16) + half * (kHalfPage * 128 / 16);
+            const uint64_t b = k_desc + key * (kOpBytes / 16);
 #pragma unroll
             for (int g = 0; g < 2; ++g)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                tc_mma_warp(d + g * kHalfPage, q_desc + g * (kTreeRows * 128 / 16) + j * 2, b + g * (kGroupBytes / 16) + j * 2, by_key, j > 0);
-            tc_commit_warp(&sh.s_full[stream][half]);
+                tc_mma_warp(d0 + place * kKv4Page, q_desc + g * (kTreeRows * 128 / 16) + j * 2, b + g * (kGroupBytes / 16) + j * 2, by_key,
+                            g + j > 0);
+            tc_commit_warp(&sh.s_full[stream][place]);
+            tc_commit_warp(&sh.k_empty[key]);
           };
-          if (stream < n) {
-            logits(stream, 0);
-            if (!lost) logits(stream, 1);
-          }
+          if (stream < n) logits(stream, done);
+          if (stream + 2 < n && !lost) logits(stream + 2, done + 1);
           for (int k = stream; k < n && !lost; k += 2, ++done) {
-            const uint32_t buf = (base + k) % kOps;
-#pragma unroll 1
+            const uint32_t val = (base + k) % kVals, place = done & 1;
+            if (!wait_warp(&sh.v_full[val], (base + k) / kVals & 1, 4)) break;
+            const uint64_t b = v_desc + val * (kOpBytes / 16);
+#pragma unroll
             for (int half = 0; half < 2; ++half) {
-              if (!wait_warp(&sh.p_full[stream][half], done & 1, 7)) break;
+              if (lost || !wait_warp(&sh.p_full[stream][place][half], done >> 1 & 1, 7)) break;
               tc_fence_after();
-              const uint32_t a = d0 + half * (2 * kHalfPage);
-              const uint64_t b = v_desc + buf * (kOpBytes / 16) + half * (kHalfPage * 128 / 16);
+              const uint32_t a = d0 + place * kKv4Page + half * kHalfPage;
 #pragma unroll
-              for (int g = 0; g < 2; ++g)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                  for (int j = 0; j < 2; ++j)
-                    tc_mma_tmem_warp(d0 + kValues + g * 64, a + (2 * g + part) * 16 + j * 8, b + g * (kGroupBytes / 16) + j * 128, by_value,
-                                     k > 1 || half > 0 || part + j > 0);
+                for (int j = 0; j < 2; ++j)
+                  tc_mma_tmem_warp(d0 + kValues, a + part * 16 + j * 8, b + (2 * half + j) * 128, by_value, k > 1 || half + part + j > 0);
               tc_commit_warp(&sh.v_done[stream]);
-              if (half == 1) tc_commit_warp(&sh.op_empty[buf]);
-              if (k + 2 < n) logits(k + 2, half);
-              if (lost) break;
             }
+            tc_commit_warp(&sh.v_empty[val]);
+            if (k + 4 < n && !lost) logits(k + 4, done + 2);
           }
           tc_commit_warp(&sh.o_full);
         }

@@ -25,8 +25,8 @@ constexpr int kRaw = 4;         // pages on their way
 constexpr int kKeys = 3;        // pages' keys as operands, and values
 constexpr int kVals = 5;
 constexpr int kSoftWarps = 8;   // two streams of four
-constexpr int kCodeWarps = 8;
-constexpr int kTreeThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // and copies, a stream's products each, one idle
+constexpr int kCodeWarps = 4;
+constexpr int kTreeThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // and copies, scales, a stream's products each
 constexpr int kGroupBytes = kKv4Page * 128;      // an operand of one group: 64 tokens x 64 dimensions f16
 constexpr int kOpBytes = 2 * kGroupBytes;
 constexpr int kTop = 8;
@@ -56,10 +56,12 @@ struct __align__(1024) TreeShared {
   uint8_t key[kKeys][kOpBytes];
   uint8_t val[kVals][kOpBytes];
   uint8_t raw[kRaw][kKv4PageBytes];
+  uint4 scale[kRaw][kKv4Page];  // of a token: K's two groups, V's two, each twice as f16
   PageParams par[kVals];
-  float q_sum[2][kTreeRows], q_scale[kTreeRows];
+  float4 q_sum[kTreeRows];  // of the two groups, each twice
+  float q_scale[kTreeRows];
   float other_m[kTreeRows], other_l[kTreeRows];  // the second stream's
-  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kKeys], k_empty[kKeys], v_full[kVals], v_empty[kVals];
+  uint64_t raw_full[kRaw], raw_empty[kRaw], scaled[kRaw], k_full[kKeys], k_empty[kKeys], v_full[kVals], v_empty[kVals];
   uint64_t s_full[2][2], p_full[2][2][2], v_done[2], o_full, drained[2];
   uint32_t tmem;
   int raw_held[kRaw];
@@ -88,90 +90,119 @@ __device__ __forceinline__ uint32_t rest(__half2 h, float w0, float w1) {
   return bits(__floats2half2_rn(d0, d1));
 }
 
+// (w & MASK) | bits in one instruction: the compiler makes two of it, for its two constants
+template <uint32_t MASK>
+__device__ __forceinline__ __half2 mask_or(uint32_t w, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(MASK), "r"(bits));
+  return *reinterpret_cast<const __half2*>(&r);
+}
 // Eight codes of a word as f16 numbers (n - 8) s, in the order 0, 4, 1, 5, 2, 6, 3, 7
-__device__ __forceinline__ uint4 codes(uint32_t w, __half2 s) {
-  constexpr uint32_t kMagic = 0x64006400u;  // 1024: a code in the lowest bits adds itself, one above 16 times
+__device__ __forceinline__ uint4 codes(uint32_t w, uint32_t scale) {
+  const uint32_t magic = 0x64006400u;  // 1024: a code in the lowest bits adds itself, one above 16 times
   const uint32_t w8 = w >> 8;
-  const uint32_t a = (w & 0x000f000fu) | kMagic, b = (w & 0x00f000f0u) | kMagic;
-  const uint32_t c = (w8 & 0x000f000fu) | kMagic, d = (w8 & 0x00f000f0u) | kMagic;
   const __half2 less = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f), less16 = __float2half2_rn(-72.f);
-  auto h = [](const uint32_t& x) { return *reinterpret_cast<const __half2*>(&x); };
-  return make_uint4(bits(__hmul2(__hadd2(h(a), less), s)), bits(__hmul2(__hfma2(h(b), sixteenth, less16), s)),
-                    bits(__hmul2(__hadd2(h(c), less), s)), bits(__hmul2(__hfma2(h(d), sixteenth, less16), s)));
+  const __half2 s = *reinterpret_cast<const __half2*>(&scale);
+  return make_uint4(bits(__hmul2(__hadd2(mask_or<0x000f000fu>(w, magic), less), s)),
+                    bits(__hmul2(__hfma2(mask_or<0x00f000f0u>(w, magic), sixteenth, less16), s)),
+                    bits(__hmul2(__hadd2(mask_or<0x000f000fu>(w8, magic), less), s)),
+                    bits(__hmul2(__hfma2(mask_or<0x00f000f0u>(w8, magic), sixteenth, less16), s)));
 }
 // A token's scales (bf16 s, z of both groups) over a power of two, whose exponent is returned (1 .. 253).  What
 // is not finite, or not there, counts as 0: its z' is not finite either.
-__device__ __forceinline__ int scales(uint2 w, bool there, __half2& s0, __half2& s1) {
+__device__ __forceinline__ int scales(uint2 w, bool there, uint32_t& s0, uint32_t& s1) {
   uint32_t b0 = w.x & 0xffffu, b1 = w.y & 0xffffu;
   if (!there || (b0 & 0x7fffu) >= 0x7f80u) b0 = 0;
   if (!there || (b1 & 0x7fffu) >= 0x7f80u) b1 = 0;
   const int up = min(254 + kTop - int(max(b0 & 0x7fffu, b1 & 0x7fffu) >> 7), 253);
   const float by = __uint_as_float(uint32_t(up) << 23);
-  s0 = __float2half2_rn(__uint_as_float(b0 << 16) * by);
-  s1 = __float2half2_rn(__uint_as_float(b1 << 16) * by);
+  s0 = bits(__float2half2_rn(__uint_as_float(b0 << 16) * by));
+  s1 = bits(__float2half2_rn(__uint_as_float(b1 << 16) * by));
   return 254 - up;
 }
 // Byte of 16-byte piece c of row r in an operand
 __device__ __forceinline__ uint32_t piece_at(int r, int c) { return uint32_t(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// One page's keys (or values) as an operand, by the kCodeWarps; `held`: its tokens
-__device__ __forceinline__ void expand_keys(const uint8_t* raw, uint8_t* op, int held, int tid) {
+// One page's scales, by a warp: `held`, its tokens
+__device__ __forceinline__ void expand_scales(const uint8_t* raw, uint4* scale, PageParams& par, int held, int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = i * 32 + lane;
+    const uint8_t* sz = raw + j / 16 * kKv4TileBytes + kv4_param(j % 16, 0, false);
+    uint2 k = *reinterpret_cast<const uint2*>(sz), v = *reinterpret_cast<const uint2*>(sz + 128);
+    const bool there = j < held;
+    if (!there) k = v = make_uint2(0u, 0u);  // behind the end: may hold anything
+    uint4 s;
+    auto put = [&](float4* a, float2* b, uint2 w, int e) {
+      float *pa = reinterpret_cast<float*>(a + j / 2) + j % 2, *pb = reinterpret_cast<float*>(b + j / 2) + j % 2;
+      pa[0] = __uint_as_float(uint32_t(e) << 23);
+      pa[2] = fmaf(8.f, lo16(w.x), hi16(w.x));
+      pb[0] = fmaf(8.f, lo16(w.y), hi16(w.y));
+    };
+    put(par.ka, par.kb, k, scales(k, there, s.x, s.y));
+    const int e = scales(v, there, s.z, s.w);
+    put(par.va, par.vb, v, e);
+    scale[j] = s;
+    const int top = __reduce_max_sync(~0u, there ? e : 1), low = __reduce_min_sync(~0u, there ? e : 254);
+    if (lane == 0) {
+      par.top[i] = top;
+      par.low[i] = low;
+    }
+  }
+  if (lane == 0) par.held = held;
+}
+// One page's keys (or values) as an operand, by the kCodeWarps
+__device__ __forceinline__ void expand_keys(const uint8_t* raw, const uint4* scale, uint8_t* op, int tid) {
 #pragma unroll
   for (int i = 0; i < 256 / (kCodeWarps * 32); ++i) {
     // 16 bytes: dimensions 16 q .. 16 q + 15 of both groups of a token
     const int at = tid + i * kCodeWarps * 32, r = at / 4, q = at % 4;
-    const uint8_t* tile = raw + at / 64 * kKv4TileBytes;
-    const uint4 w = *reinterpret_cast<const uint4*>(tile + at % 64 * 16);
-    __half2 s0, s1;
-    scales(*reinterpret_cast<const uint2*>(tile + kv4_param(r % 16, 0, false)), r < held, s0, s1);
-    *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q)) = codes(w.x, s0);
-    *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q + 1)) = codes(w.y, s0);
-    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q)) = codes(w.z, s1);
-    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q + 1)) = codes(w.w, s1);
+    const uint4 w = *reinterpret_cast<const uint4*>(raw + at / 64 * kKv4TileBytes + at % 64 * 16);
+    const uint2 s = *reinterpret_cast<const uint2*>(&scale[r].x);
+    *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q)) = codes(w.x, s.x);
+    *reinterpret_cast<uint4*>(op + piece_at(r, 2 * q + 1)) = codes(w.y, s.x);
+    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q)) = codes(w.z, s.y);
+    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, 2 * q + 1)) = codes(w.w, s.y);
   }
 }
-__device__ __forceinline__ void expand_values(const uint8_t* raw, uint8_t* op, PageParams& par, int held, int tid) {
+__device__ __forceinline__ void expand_values(const uint8_t* raw, const uint4* scale, uint8_t* op, int tid) {
 #pragma unroll
   for (int i = 0; i < 256 / (kCodeWarps * 32); ++i) {
     // 16 bytes: eight dimensions of two neighbouring tokens and both groups
     const int at = tid + i * kCodeWarps * 32, r = at / 64 * 16 + at % 64 / 32 * 8 + at % 4 * 2, oct = at % 32 / 4;
-    const uint8_t* tile = raw + at / 64 * kKv4TileBytes;
-    const uint4 w = *reinterpret_cast<const uint4*>(tile + kKv4V + at % 64 * 16);
-    __half2 s0, s1;
-    scales(*reinterpret_cast<const uint2*>(tile + kv4_param(r % 16, 0, true)), r < held, s0, s1);
-    *reinterpret_cast<uint4*>(op + piece_at(r, oct)) = codes(__byte_perm(w.x, w.y, 0x5410), s0);
-    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, oct)) = codes(__byte_perm(w.z, w.w, 0x5410), s1);
-    scales(*reinterpret_cast<const uint2*>(tile + kv4_param(r % 16 + 1, 0, true)), r + 1 < held, s0, s1);
-    *reinterpret_cast<uint4*>(op + piece_at(r + 1, oct)) = codes(__byte_perm(w.x, w.y, 0x7632), s0);
-    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r + 1, oct)) = codes(__byte_perm(w.z, w.w, 0x7632), s1);
-  }
-  if (tid < kKv4Page) {  // two warps: a thread for each token's scales
-    const uint8_t* sz = raw + tid / 16 * kKv4TileBytes + kv4_param(tid % 16, 0, false);
-    uint2 k = *reinterpret_cast<const uint2*>(sz), v = *reinterpret_cast<const uint2*>(sz + 128);
-    if (tid >= held) k = v = make_uint2(0u, 0u);  // behind the end: may hold anything
-    auto put = [&](float4* a, float2* b, uint2 w) {
-      __half2 s0, s1;
-      const int e = scales(w, true, s0, s1);
-      float *pa = reinterpret_cast<float*>(a + tid / 2) + tid % 2, *pb = reinterpret_cast<float*>(b + tid / 2) + tid % 2;
-      pa[0] = __uint_as_float(uint32_t(e) << 23);
-      pa[2] = fmaf(8.f, lo16(w.x), hi16(w.x));
-      pb[0] = fmaf(8.f, lo16(w.y), hi16(w.y));
-      return e;
-    };
-    put(par.ka, par.kb, k);
-    const int e = put(par.va, par.vb, v);
-    const int top = __reduce_max_sync(~0u, tid < held ? e : 1), low = __reduce_min_sync(~0u, tid < held ? e : 254);
-    if (tid % 32 == 0) {
-      par.top[tid / 32] = top;
-      par.low[tid / 32] = low;
-    }
-    if (tid == 0) par.held = held;
+    const uint4 w = *reinterpret_cast<const uint4*>(raw + at / 64 * kKv4TileBytes + kKv4V + at % 64 * 16);
+    const uint2 s = *reinterpret_cast<const uint2*>(&scale[r].z), s1 = *reinterpret_cast<const uint2*>(&scale[r + 1].z);
+    *reinterpret_cast<uint4*>(op + piece_at(r, oct)) = codes(__byte_perm(w.x, w.y, 0x5410), s.x);
+    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r, oct)) = codes(__byte_perm(w.z, w.w, 0x5410), s.y);
+    *reinterpret_cast<uint4*>(op + piece_at(r + 1, oct)) = codes(__byte_perm(w.x, w.y, 0x7632), s1.x);
+    *reinterpret_cast<uint4*>(op + kGroupBytes + piece_at(r + 1, oct)) = codes(__byte_perm(w.z, w.w, 0x7632), s1.y);
   }
 }
 
 // The power of two that brings the number with these exponent bits to 2^kUnitTop .. twice that
 __device__ __forceinline__ float unit_of(int exponent) {
   return __uint_as_float(uint32_t(min(max(2 * 127 + kUnitTop - exponent, 1), int(kUnitMax))) << 23);
+}
+// Bounded wait.  A warp that polls takes the softmax warps' issue slots (2000 of 9000 instructions a page without
+// the sleep), so those that run ahead sleep between two looks.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, uint64_t limit_ns, uint32_t sleep_ns) {
+  auto look = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (limit_ns == 0) return mbar_test_wait(bar, parity);
+  if (look()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (sleep_ns > 0) __nanosleep(sleep_ns);
+    if (look()) return true;
+    if ((i & 63u) == 63u && globaltimer_ns() - t0 > limit_ns) return false;
+  }
 }
 __device__ __forceinline__ int pages_of(int len) { return max(1, (len + kKv4Page - 1) / kKv4Page); }
 
@@ -255,12 +286,34 @@ __device__ __forceinline__ uint64_t seen_of(uint64_t tree, int prefix, int pos, 
 // 8 b + 2 (lane % 4) and the next (b 0 .. 3).
 struct Soft {
   float m[4];        // reference of the weights, log2: within 2^8 of the largest; kNone: no token yet
-  float u[4];        // units
+  Pair u2[4];        // units, twice
   float largest[4];  // the rows' largest weights p f times 2^-9, once they have units of their own
-  float qs[4];
+  Pair qs2[4], less[4];  // the queries' scales, twice; -m, twice
   float most;        // the largest unit of the warp's rows
   float least;       // what every row's largest weight with its unit is at least
   bool split;        // the rows have units of their own
+  __device__ __forceinline__ float u(int row) const { return first(u2[row]); }
+  __device__ __forceinline__ float qs(int row) const { return first(qs2[row]); }
+  static __device__ __forceinline__ float first(const Pair& p) {
+    float a, b;
+    p.get(a, b);
+    return a;
+  }
+  __device__ __forceinline__ Soft(const float* q_scale)
+      : u2{top(), top(), top(), top()},
+        qs2{twice(q_scale[0]), twice(q_scale[8]), twice(q_scale[16]), twice(q_scale[24])},
+        less{twice(-kNone), twice(-kNone), twice(-kNone), twice(-kNone)} {
+    most = __uint_as_float(kUnitMax << 23);
+    least = INFINITY;
+    split = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = kNone;
+      largest[i] = 0.f;
+    }
+  }
+  static __device__ __forceinline__ Pair twice(float x) { return Pair(x, x); }
+  static __device__ __forceinline__ Pair top() { return twice(__uint_as_float(kUnitMax << 23)); }
 };
 
 // Values of this warp's rows times f[row]
@@ -308,15 +361,15 @@ __device__ __forceinline__ void split_units(Soft& S, const uint32_t (&x)[2][16],
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         // 2^-9: finite with any f
-        const float p = ex2(fmaf(__uint_as_float(x[h][4 * b + 2 * e + j]), S.qs[row], -S.m[row])) * 0.001953125f;
+        const float p = ex2(fmaf(__uint_as_float(x[h][4 * b + 2 * e + j]), S.qs(row), -S.m[row])) * 0.001953125f;
         if (!EDGE || (seen[row] >> (8 * b + 2 * t + j) & 1)) w = fmaxf(w, p * (j ? v.y : v.x));
       }
     }
-    const float old = S.u[row];
+    const float old = S.u(row);
     const float all = fmaxf(row_max(w), f[row] * (S.split ? S.largest[row] : kLeast * 0.001953125f / old));
     float unit = fminf(old, by_scale);
     if (!(all * unit >= kLeast * 0.001953125f && all * unit < kMost * 0.001953125f)) unit = unit_of(int(__float_as_uint(all) >> 23) + 9);
-    S.u[row] = unit;
+    S.u2[row] = Soft::twice(unit);
     S.largest[row] = all;
     k[row] = unit >= 1.f ? f[row] * unit / old : f[row] * (unit / old);  // in range in between, too
     most = fmaxf(most, unit);
@@ -332,7 +385,7 @@ __device__ __forceinline__ void split_units(Soft& S, const uint32_t (&x)[2][16],
 // this thread's even and odd tokens.  settle(): waits until no product writes the values.
 template <bool EDGE, typename F>
 __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2], const PageParams& par, int half, uint32_t at,
-                                          uint32_t values, bool any, const uint32_t (&seen)[4], int t, const float* q_sum, F settle) {
+                                          uint32_t values, bool any, const uint32_t (&seen)[4], int t, const float4* q_sum, F settle) {
   const float4 *ka = par.ka + half * (kHalfPage / 2), *va = par.va + half * (kHalfPage / 2);
   const float2 *kb = par.kb + half * (kHalfPage / 2), *vb = par.vb + half * (kHalfPage / 2);
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -340,12 +393,7 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
 #pragma unroll
   for (int h = 0; h < 2; ++h) tmem_load_16x32(s[h], at + (uint32_t(h * 16) << 16));
   {
-    float sum[4][2];  // of the queries
-#pragma unroll
-    for (int row = 0; row < 4; ++row) {
-      sum[row][0] = q_sum[8 * row];
-      sum[row][1] = q_sum[kTreeRows + 8 * row];
-    }
+    const float4 sum[4] = {q_sum[0], q_sum[8], q_sum[16], q_sum[24]};
     tmem_wait_loads();
     tie(s[0]);
     tie(s[1]);
@@ -356,8 +404,8 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
 #pragma unroll
       for (int row = 0; row < 4; ++row) {
         const int h = row >> 1, i = 4 * b + 2 * (row & 1);
-        Pair y = mul2(Pair(b2.x, b2.y), Pair(sum[row][1], sum[row][1]));
-        y = fma2(Pair(a4.z, a4.w), Pair(sum[row][0], sum[row][0]), y);
+        Pair y = mul2(Pair(b2.x, b2.y), Pair(sum[row].z, sum[row].w));
+        y = fma2(Pair(a4.z, a4.w), Pair(sum[row].x, sum[row].y), y);
         y = fma2(Pair(a4.x, a4.y), Pair(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), y);
         float x[2];
         y.get(x[0], x[1]);
@@ -375,7 +423,7 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
   bool over = __uint_as_float(uint32_t(par.top[half]) << 23) * S.most >= kMaxScale;
 #pragma unroll
   for (int row = 0; row < 4; ++row) {
-    mx[row] *= S.qs[row];
+    mx[row] *= S.qs(row);
     over |= mx[row] > S.m[row] + kGrowth;
   }
   if (__any_sync(~0u, over)) {
@@ -385,6 +433,7 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
       const float m1 = fmaxf(S.m[row], row_max(mx[row]));
       f[row] = ex2(S.m[row] - m1);
       S.m[row] = m1;
+      S.less[row] = Soft::twice(-m1);
       const Pair f2(f[row], f[row]);
       l[row] = mul2(l[row], f2);
       c[row][0] = mul2(c[row][0], f2);
@@ -399,7 +448,7 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
       S.most = unit;
 #pragma unroll
       for (int row = 0; row < 4; ++row) {
-        S.u[row] = unit;
+        S.u2[row] = Soft::twice(unit);
         k[row] = f[row] * ratio;
       }
     } else {
@@ -422,7 +471,7 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
       for (int row = 0; row < 4; ++row) {
         const int h = row >> 1, e = row & 1, i = 4 * b + 2 * e;
         float p[2];
-        fma2(Pair(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), Pair(S.qs[row], S.qs[row]), Pair(-S.m[row], -S.m[row]))
+        fma2(Pair(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), S.qs2[row], S.less[row])
             .get(p[0], p[1]);
         float z[4] = {a4.z, a4.w, b2.x, b2.y};
 #pragma unroll
@@ -436,7 +485,7 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
         c[row][1] = fma2(pp, Pair(z[2], z[3]), c[row][1]);
         float w[2];
         // in this order: a large f with the unit of a row without weight on it may overflow
-        mul2(mul2(pp, Pair(S.u[row], S.u[row])), Pair(a4.x, a4.y)).get(w[0], w[1]);
+        mul2(mul2(pp, S.u2[row]), Pair(a4.x, a4.y)).get(w[0], w[1]);
         const __half2 hi = __floats2half2_rn(w[0], w[1]);
         part[h][0][2 * j + e] = bits(hi);
         part[h][1][2 * j + e] = rest(hi, w[0], w[1]);
@@ -455,11 +504,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   TreeShared& sh = *reinterpret_cast<TreeShared*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kCopy = kSoftWarps + kCodeWarps, kMma = kCopy + 1;  // and kMma + 1
+  constexpr int kCopy = kSoftWarps + kCodeWarps, kScale = kCopy + 1, kMma = kScale + 1;  // and kMma + 1
   if (tid == 0) {
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], kCodeWarps);
+      mbar_init(&sh.scaled[i], 1);
     }
     for (int i = 0; i < kKeys; ++i) {
       mbar_init(&sh.k_full[i], kCodeWarps);
@@ -490,8 +540,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
   const int items = sh.plan.before[P.batch], cap = P.pg.max_pages * kKv4Page;
   bool lost = false;       // a wait of this warp ran out: it waits and works no more
   uint32_t pages = 0;      // before this item
-  auto wait = [&](uint64_t* bar, uint32_t parity, int which) {
-    if (!lost && !mbar_wait_parked(bar, parity, P.wait_ns)) {
+  auto wait = [&](uint64_t* bar, uint32_t parity, int which, uint32_t sleep_ns = 0) {
+    if (!lost && !wait_for(bar, parity, P.wait_ns, sleep_ns)) {
       set_device_error(P.pg.status, DEV_WAIT_TIMEOUT, which);
       lost = true;
     }
@@ -505,10 +555,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
     tc_fence_after();
   };
 
-  // Each role goes through the items on its own: the softmax threads have 168 registers, the others 48
-  // (256 x 168 + 384 x 48 = 640 x 96, what the CTA was launched with).
+  // Each role goes through the items on its own: the softmax threads have 184 registers, the others 72
+  // (256 x 184 + 256 x 72 = 512 x 128, what the CTA was launched with).
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     uint32_t of_stream = 0, n_items = 0;  // pages of the stream, items
     for (int item = blockIdx.x; item < items; item += gridDim.x, ++n_items) {
       const Item I(sh.plan, P, item, lane);
@@ -560,7 +610,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
           for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
           const int g = lane >> 3 & 1;
           *reinterpret_cast<uint4*>(&sh.q[g][piece_at(r, lane & 7)]) = make_uint4(w[0], w[1], w[2], w[3]);
-          if ((lane & 7) == 0) sh.q_sum[g][r] = big < INFINITY ? sum : NAN;
+          if ((lane & 7) == 0) {
+            const float v = big < INFINITY ? sum : NAN;
+            reinterpret_cast<float2*>(&sh.q_sum[r])[g] = make_float2(v, v);
+          }
           if ((lane & 15) == 0) sh.q_scale[r] = P.scale_log2 * __uint_as_float(uint32_t(127 - 13 + e) << 23);
         }
       }
@@ -568,19 +621,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       meet();
       const int stream = warp >> 2, g4 = lane >> 2, t = lane & 3, row0 = warp % 4 * 32 + g4;
       const uint32_t at = tmem + stream * kStreamColumns + (uint32_t(warp % 4 * 32) << 16);
-      Soft S;
+      Soft S(&sh.q_scale[row0]);
       const Pair none(0.f, 0.f);
       Pair l2[4] = {none, none, none, none}, c2[4][2] = {{none, none}, {none, none}, {none, none}, {none, none}};
-      S.most = __uint_as_float(kUnitMax << 23);
-      S.least = INFINITY;
-      S.split = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        S.m[i] = kNone;
-        S.qs[i] = sh.q_scale[row0 + 8 * i];
-        S.u[i] = S.most;
-        S.largest[i] = 0.f;
-      }
       bool any = false;
       for (int k = stream; k < n; k += 2, ++of_stream) {
         const uint32_t buf = (pages + k) % kVals, place = of_stream & 1;
@@ -608,9 +651,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
               const uint64_t tree = r < cols ? uint64_t(P.tree[I.b * P.tree_stride + (col0 + r) / P.hpg]) : 0;
               seen[i] = uint32_t(seen_of(tree, prefix, pos, par.held) >> (half * kHalfPage));
             }
-            soft_half<true>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[0][row0], settle);
+            soft_half<true>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[row0], settle);
           } else {
-            soft_half<false>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[0][row0], settle);
+            soft_half<false>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[row0], settle);
           }
           any = true;
           tc_fence_before();
@@ -633,7 +676,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
           c2[i][g].get(x, y);
           c[i][g] = row_sum(x + y);
         }
-        inv[i] = 1.f / S.u[i];
+        inv[i] = 1.f / S.u(i);
       }
       // a stream's values, four rows and 32 columns at a time
       auto values = [&](int c32, float (&v)[2][16]) {
@@ -717,7 +760,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       meet();  // queries, operands and values are free again
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < kCopy) {
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const Item I(sh.plan, P, item, lane);
@@ -725,23 +768,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         meet();
         for (int k = 0; k < n; ++k) {
           const uint32_t at = pages + k, raw = at % kRaw, key = at % kKeys, val = at % kVals;
-          wait(&sh.raw_full[raw], at / kRaw & 1, 4);
-          wait(&sh.k_empty[key], (at / kKeys & 1) ^ 1, 5);
+          wait(&sh.scaled[raw], at / kRaw & 1, 4, 50);
+          wait(&sh.k_empty[key], (at / kKeys & 1) ^ 1, 5, 50);
           if (__any_sync(~0u, lost)) {
             lost = true;
             break;
           }
-          const int held = sh.raw_held[raw], me = tid - kSoftWarps * 32;
-          expand_keys(sh.raw[raw], sh.key[key], held, me);
+          const int me = tid - kSoftWarps * 32;
+          expand_keys(sh.raw[raw], sh.scale[raw], sh.key[key], me);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.k_full[key]);
-          wait(&sh.v_empty[val], (at / kVals & 1) ^ 1, 5);
-          if (__any_sync(~0u, lost)) {
-            lost = true;
-            break;
-          }
-          expand_values(sh.raw[raw], sh.val[val], sh.par[val], held, me);
+          expand_values(sh.raw[raw], sh.scale[raw], sh.val[val], me);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
@@ -769,7 +807,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
           }
           for (int k = k0; k < min(n, k0 + 32); ++k) {
             const uint32_t at = pages + k, raw = at % kRaw;
-            wait(&sh.raw_empty[raw], (at / kRaw & 1) ^ 1, 4);
+            wait(&sh.raw_empty[raw], (at / kRaw & 1) ^ 1, 4, 200);
             lost = __any_sync(~0u, lost);
             if (lost) break;
             const int page = __shfl_sync(~0u, id, k - k0);
@@ -789,11 +827,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         pages += n;
         meet();  // queries, operands and values are free again
       }
+    } else if (warp == kScale) {
+      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const Item I(sh.plan, P, item, lane);
+        const int n = I.page1 - I.page0;
+        meet();
+        for (int k = 0; k < n; ++k) {
+          const uint32_t at = pages + k, raw = at % kRaw, val = at % kVals;
+          wait(&sh.raw_full[raw], at / kRaw & 1, 4, 50);
+          wait(&sh.v_empty[val], (at / kVals & 1) ^ 1, 5, 50);
+          if (__any_sync(~0u, lost)) {
+            lost = true;
+            break;
+          }
+          expand_scales(sh.raw[raw], sh.scale[raw], sh.par[val], sh.raw_held[raw], lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.scaled[raw]);
+        }
+        pages += n;
+        meet();  // queries, operands and values are free again
+      }
     } else {
       // the whole warp, with operands that are the same in all its threads (tc_mma_warp)
       auto same = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };
-      auto wait_warp = [&](uint64_t* bar, uint32_t parity, int which) {
-        wait(bar, parity, which);
+      auto wait_warp = [&](uint64_t* bar, uint32_t parity, int which, uint32_t sleep_ns) {
+        wait(bar, parity, which, sleep_ns);
         lost = __any_sync(~0u, lost);
         return !lost;
       };
@@ -808,10 +866,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         const int n = same(I.page1 - I.page0);
         const uint32_t base = same(pages);
         meet();
-        if (warp <= kMma + 1) {
+        {
           auto logits = [&](int k, uint32_t count) {  // page k, the stream's count-th
             const uint32_t key = (base + k) % kKeys, place = count & 1;
-            if (!wait_warp(&sh.k_full[key], (base + k) / kKeys & 1, 4)) return;
+            if (!wait_warp(&sh.k_full[key], (base + k) / kKeys & 1, 4, 50)) return;
             tc_fence_after();
             const uint64_t b = k_desc + key * (kOpBytes / 16);
 #pragma unroll
@@ -827,11 +885,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
           if (stream + 2 < n && !lost) logits(stream + 2, done + 1);
           for (int k = stream; k < n && !lost; k += 2, ++done) {
             const uint32_t val = (base + k) % kVals, place = done & 1;
-            if (!wait_warp(&sh.v_full[val], (base + k) / kVals & 1, 4)) break;
+            if (!wait_warp(&sh.v_full[val], (base + k) / kVals & 1, 4, 50)) break;
             const uint64_t b = v_desc + val * (kOpBytes / 16);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              if (lost || !wait_warp(&sh.p_full[stream][place][half], done >> 1 & 1, 7)) break;
+              if (lost || !wait_warp(&sh.p_full[stream][place][half], done >> 1 & 1, 7, 20)) break;
               tc_fence_after();
               const uint32_t a = d0 + place * kKv4Page + half * kHalfPage;
 #pragma unroll

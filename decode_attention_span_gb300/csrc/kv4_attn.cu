@@ -63,7 +63,6 @@ constexpr int kChunkTokens = 32;
 constexpr int kChunkBytes = 2 * kKv4TileBytes;
 constexpr int kMaxCtas = 256;                    // of a launch
 constexpr int kCols = 8;                         // (token, head) pairs of a block
-constexpr int kWideColumns = 24;                 // of a tree, from which on kv4_tree.cu is faster
 constexpr int kStateFloats = kCols * (kHeadDim + 2);  // o, m, l
 // What a second group costs a CTA (its plan, queries, first copies and join, about 6 us), in chunks
 constexpr int kGroupCost = 40;
@@ -946,6 +945,13 @@ int blocks_of(const sekv_config* cfg, int64_t n_q) {
   return int((n_q + tpb - 1) / tpb);
 }
 
+// Whether kv4_tree.cu takes less for `tree_blocks` blocks of columns than this file's kernel for `blocks` of its
+// own, over `pages` pages of all sequences and KV heads (the table's: what the sequences hold is not known
+// here).  Measured, that one takes 28 us and 9.1 ns a page and block, this one 10 us and 1.84 ns.
+bool wide_is_faster(int blocks, int tree_blocks, int64_t pages) {
+  return double(pages) * (1.84 * blocks - 9.1 * tree_blocks) > 18000.;
+}
+
 int attn_ctas() { return std::min(device_sm_count(), kMaxCtas); }  // one per SM
 
 struct Kv4Ws {
@@ -1014,7 +1020,8 @@ sekv_status attention(const sekv_config* cfg, const sekv_kv4_cache* cache, int32
   const int sms = attn_ctas();
   const Kv4Ws L = kv4_ws(cfg, n_q, sms);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  if (tree && n_q * (cfg->n_q_heads / cfg->n_kv_heads) >= kWideColumns) {
+  const int tree_blocks = (n_q * (cfg->n_q_heads / cfg->n_kv_heads) + kTreeRows - 1) / kTreeRows;
+  if (tree && wide_is_faster(blocks_of(cfg, n_q), tree_blocks, int64_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages)) {
     TreeCall c{};
     c.pg.pages = static_cast<uint8_t*>(cache->pages);
     c.pg.table = cache->page_table;
@@ -1033,7 +1040,7 @@ sekv_status attention(const sekv_config* cfg, const sekv_kv4_cache* cache, int32
     c.batch = cfg->batch;
     c.hpg = cfg->n_q_heads / cfg->n_kv_heads;
     c.n_q = n_q;
-    c.n_blk = (n_q * c.hpg + kTreeRows - 1) / kTreeRows;
+    c.n_blk = tree_blocks;
     c.bf16 = dtype == SEKV_BF16;
     c.scale_log2 = scale * kLog2e;
     return tree_attention(c, sms, stream);

@@ -33,7 +33,7 @@ constexpr int kTop = 8;
 constexpr int kHalfPage = 32;                    // tokens that a stream takes at a time
 constexpr int kStreamColumns = 256;              // tensor memory of a stream: two pages' logits or weights, 64 columns each, and the values
 constexpr int kValues = 128;                     // from here on
-constexpr int kItemCost = 6;                     // what an item costs beyond its pages, in pages
+constexpr int kItemCost = 8;                     // what an item costs beyond its pages, in pages
 constexpr float kNone = -3e38f;
 constexpr float kGrowth = 8.f;
 constexpr float kMaxScale = 128.f;      // of V with the unit: 2^8 times it fits f16
@@ -60,15 +60,15 @@ struct __align__(1024) TreeShared {
   PageParams par[kVals];
   float4 q_sum[kTreeRows];  // of the two groups, each twice
   float q_scale[kTreeRows];
-  float other_m[kTreeRows], other_l[kTreeRows];  // the second stream's
+  float m[2][kTreeRows], l[2][kTreeRows];  // the streams'
   uint64_t raw_full[kRaw], raw_empty[kRaw], scaled[kRaw], k_full[kKeys], k_empty[kKeys], v_full[kVals], v_empty[kVals];
-  uint64_t s_full[2][2], p_full[2][2][2], v_done[2], o_full, drained[2];
+  uint64_t s_full[2][2], p_full[2][2][2], v_done[2][2][2], o_full, drained[2];
   uint32_t tmem;
   int raw_held[kRaw];
   TreePlan plan;
 };
 static_assert(sizeof(TreeShared) + 1024 <= 227 * 1024, "shared memory of a CTA");
-static_assert(kVals * kOpBytes >= kTreeRows * kHeadDim * 4, "the second stream's values lie over the operands");
+static_assert(kVals * kOpBytes >= kTreeRows * kHeadDim * 4, "the streams' values lie over the operands");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -522,9 +522,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
     for (int i = 0; i < 2; ++i) {
       for (int j = 0; j < 2; ++j) {
         mbar_init(&sh.s_full[i][j], 1);
-        for (int h = 0; h < 2; ++h) mbar_init(&sh.p_full[i][j][h], 4);
+        for (int h = 0; h < 2; ++h) {
+          mbar_init(&sh.p_full[i][j][h], 4);
+          mbar_init(&sh.v_done[i][j][h], 1);
+        }
       }
-      mbar_init(&sh.v_done[i], 1);
     }
     mbar_init(&sh.o_full, 2);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.drained[i], 1);
@@ -547,7 +549,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
     }
     return !lost;
   };
-  // Between items, and between the queries and their products, all warps meet
+  // Between items all warps meet; the softmax warps and those of the products once the queries are there
+  auto ready = [&]() {
+    __syncwarp();
+    tc_fence_before();
+    named_bar(3, (kSoftWarps + 2) * 32);
+    tc_fence_after();
+  };
   auto meet = [&]() {
     __syncwarp();
     tc_fence_before();
@@ -618,7 +626,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      meet();
+      ready();
       const int stream = warp >> 2, g4 = lane >> 2, t = lane & 3, row0 = warp % 4 * 32 + g4;
       const uint32_t at = tmem + stream * kStreamColumns + (uint32_t(warp % 4 * 32) << 16);
       Soft S(&sh.q_scale[row0]);
@@ -636,9 +644,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         const int pos = (I.page0 + k) * kKv4Page;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          // the products with the weights of the half page before
+          // The products with the weights of the half page before.  They may lag behind by three halves, no more
+          // (the logits of this page were multiplied after those of the page before the last), so each place and
+          // half has a barrier of its own, which no two phases can pass unseen.
           auto settle = [&]() {
-            wait(&sh.v_done[stream], (2 * of_stream + half + 1) & 1, 6);
+            const uint32_t of = half ? of_stream : of_stream - 1;
+            wait(&sh.v_done[stream][of & 1][half ^ 1], of >> 1 & 1, 6);
             tc_fence_after();
             __syncwarp();
           };
@@ -693,68 +704,68 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
           }
         }
       };
-      // the second stream's state and values through shared memory, over the operands: their products are done
-      float* other = reinterpret_cast<float*>(&sh.val[0][0]) + tid % 128;
-      if (stream == 1) {
+      // Each stream writes one group of dimensions; the other's values of it come through shared memory, over
+      // the operands, whose products are done.
+      float* shared = reinterpret_cast<float*>(&sh.val[0][0]) + tid % 128;
+      auto slot = [&](int group, int c, int h, int i) { return (group * 64 + c * 32 + h * 16 + i) * 128; };
 #pragma unroll 1
-        for (int c32 = 0; c32 < 4; ++c32) {
-          float v[2][16];
-          values(c32, v);
+      for (int c = 0; c < 2; ++c) {
+        float v[2][16];
+        values(2 * (1 - stream) + c, v);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) other[(c32 * 32 + h * 16 + i) * 128] = v[h][i];
-        }
-        if (t == 0)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sh.other_m[row0 + 8 * i] = m[i];
-            sh.other_l[row0 + 8 * i] = l[i];
-          }
+          for (int i = 0; i < 16; ++i) shared[slot(1 - stream, c, h, i)] = v[h][i];
       }
-      named_bar(1, kSoftWarps * 32);
-      if (stream == 0) {
-        const bool whole = I.pieces == 1;
-        float f0[4], f1[4];
-        float* to[4];  // dimension t of the rows
+      if (t == 0)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = row0 + 8 * i, col = col0 + r, tok = col / P.hpg;
-          const int64_t o = (int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg;
-          const float om = sh.other_m[r], all = fmaxf(m[i], om);
-          f0[i] = ex2(m[i] - all);
-          f1[i] = ex2(om - all);
-          l[i] = f0[i] * l[i] + f1[i] * sh.other_l[r];
-          to[i] = whole ? P.out + o * kHeadDim : P.partials + int64_t(item) * kTreePartialFloats + r * kHeadDim;
-          if (t == 0 && r < cols) {
-            if (!whole) {
-              float* ml = P.partials + int64_t(item) * kTreePartialFloats + kTreeRows * kHeadDim;
-              ml[r] = all;
-              ml[kTreeRows + r] = l[i];
-            } else if (P.lse) {
-              P.lse[o] = l[i] != 0.f ? (all + log2f(l[i])) * kLn2 : -INFINITY;
-            }
-          }
-          if (whole) {  // a row without a token is 0
-            const float by = l[i] != 0.f ? 1.f / l[i] : 0.f;
-            f0[i] *= by;
-            f1[i] *= by;
-          }
-          to[i] = r < cols ? to[i] + t : nullptr;
+          sh.m[stream][row0 + 8 * i] = m[i];
+          sh.l[stream][row0 + 8 * i] = l[i];
         }
+      named_bar(1, kSoftWarps * 32);
+      const bool whole = I.pieces == 1;
+      float f0[4], f1[4];
+      float* to[4];  // dimension t of the rows
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = row0 + 8 * i, col = col0 + r, tok = col / P.hpg;
+        const int64_t o = (int64_t(I.b) * P.n_q + tok) * P.pg.hkv * P.hpg + head * P.hpg + col - tok * P.hpg;
+        const float om = sh.m[1 - stream][r], all = fmaxf(m[i], om);
+        f0[i] = ex2(m[i] - all);
+        f1[i] = ex2(om - all);
+        // in the order of the streams, so that both have the same sum
+        const float own = f0[i] * l[i], else_ = f1[i] * sh.l[1 - stream][r];
+        l[i] = stream == 0 ? own + else_ : else_ + own;
+        to[i] = whole ? P.out + o * kHeadDim : P.partials + int64_t(item) * kTreePartialFloats + r * kHeadDim;
+        if (stream == 0 && t == 0 && r < cols) {
+          if (!whole) {
+            float* ml = P.partials + int64_t(item) * kTreePartialFloats + kTreeRows * kHeadDim;
+            ml[r] = all;
+            ml[kTreeRows + r] = l[i];
+          } else if (P.lse) {
+            P.lse[o] = l[i] != 0.f ? (all + log2f(l[i])) * kLn2 : -INFINITY;
+          }
+        }
+        if (whole) {  // a row without a token is 0
+          const float by = l[i] != 0.f ? 1.f / l[i] : 0.f;
+          f0[i] *= by;
+          f1[i] *= by;
+        }
+        to[i] = r < cols ? to[i] + stream * 64 + t : nullptr;
+      }
 #pragma unroll 1
-        for (int c32 = 0; c32 < 4; ++c32) {
-          float v[2][16];
-          values(c32, v);
+      for (int c = 0; c < 2; ++c) {
+        float v[2][16];
+        values(2 * stream + c, v);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int row = 2 * h + (i >> 1 & 1);
-              // position 2 t + i % 2 of a piece of eight: dimension t or t + 4
-              if (to[row]) to[row][c32 * 32 + (i >> 2) * 8 + (i & 1) * 4] = f0[row] * v[h][i] + f1[row] * other[(c32 * 32 + h * 16 + i) * 128];
-            }
-        }
+          for (int i = 0; i < 16; ++i) {
+            const int row = 2 * h + (i >> 1 & 1);
+            // position 2 t + i % 2 of a piece of eight: dimension t or t + 4
+            if (to[row]) to[row][c * 32 + (i >> 2) * 8 + (i & 1) * 4] = f0[row] * v[h][i] + f1[row] * shared[slot(stream, c, h, i)];
+          }
       }
       pages += n;
       meet();  // queries, operands and values are free again
@@ -765,7 +776,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const Item I(sh.plan, P, item, lane);
         const int n = I.page1 - I.page0;
-        meet();
         for (int k = 0; k < n; ++k) {
           const uint32_t at = pages + k, raw = at % kRaw, key = at % kKeys, val = at % kVals;
           wait(&sh.scaled[raw], at / kRaw & 1, 4, 50);
@@ -795,7 +805,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         const Item I(sh.plan, P, item, lane);
         const int n = I.page1 - I.page0;
         const int head = I.group % P.pg.hkv;
-        meet();
         for (int k0 = 0; k0 < n && !lost; k0 += 32) {
           int id = -1;
           if (k0 + lane < n && (I.page0 + k0 + lane) * kKv4Page < I.len) {
@@ -831,7 +840,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const Item I(sh.plan, P, item, lane);
         const int n = I.page1 - I.page0;
-        meet();
         for (int k = 0; k < n; ++k) {
           const uint32_t at = pages + k, raw = at % kRaw, val = at % kVals;
           wait(&sh.raw_full[raw], at / kRaw & 1, 4, 50);
@@ -865,7 +873,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
         const Item I(sh.plan, P, item, lane);
         const int n = same(I.page1 - I.page0);
         const uint32_t base = same(pages);
-        meet();
+        ready();
         {
           auto logits = [&](int k, uint32_t count) {  // page k, the stream's count-th
             const uint32_t key = (base + k) % kKeys, place = count & 1;
@@ -897,7 +905,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                   tc_mma_tmem_warp(d0 + kValues, a + part * 16 + j * 8, b + (2 * half + j) * 128, by_value, k > 1 || half + part + j > 0);
-              tc_commit_warp(&sh.v_done[stream]);
+              tc_commit_warp(&sh.v_done[stream][place][half]);
             }
             tc_commit_warp(&sh.v_empty[val]);
             if (k + 4 < n && !lost) logits(k + 4, done + 2);

@@ -131,3 +131,50 @@ def attention(q, pages, table, lens, scale):
                     bound[b, i, h] = np.repeat(p @ va[:n], 64)
                     logit[b, i, h] = abs(scale) * np.abs(q[b, i, h]).sum() * ka[:n].max()
     return out, lse, bound, logit
+
+
+def tree_attention(q, pages, table, first, tree, scale):
+    """q [B][n_q][Hq][128] fp64, tree [B][n_q] -> as attention(): query i sees the tokens before
+    first[b] and token first[b] + j for each bit j < n_q of tree[b][i]."""
+    B, nq, Hq, _ = q.shape
+    Hkv = pages.shape[1]
+    G = Hq // Hkv
+    out, lse = np.zeros(q.shape), np.full(q.shape[:3], -math.inf)
+    bound, logit = np.zeros(q.shape), np.zeros(q.shape[:3])
+    for b in range(B):
+        if first[b] < 0:
+            continue
+        for c in range(Hkv):
+            K, V, ka, va = get(pages, table, b, c, int(first[b]) + nq)
+            for i in range(nq):
+                seen = list(range(int(first[b])))
+                seen += [int(first[b]) + j for j in range(nq) if int(tree[b][i]) >> j & 1]
+                if not seen:
+                    continue
+                for h in range(c * G, c * G + G):
+                    x = K[seen] @ q[b, i, h] * scale
+                    e = np.exp(x - x.max())
+                    p = e / e.sum()
+                    out[b, i, h] = p @ V[seen]
+                    lse[b, i, h] = x.max() + math.log(e.sum())
+                    bound[b, i, h] = np.repeat(p @ va[seen], 64)
+                    logit[b, i, h] = abs(scale) * np.abs(q[b, i, h]).sum() * ka[seen].max()
+    return out, lse, bound, logit
+
+
+def keep(pages, table, b, c, first, kept):
+    """Moves the tokens first + kept[i] of sequence b, KV head c to first + i, byte by byte."""
+    d = np.arange(128)
+    rows = []
+    for t in [first + k for k in kept]:
+        tile, j = pages[int(table[b][t // 64]), c][(t % 64) // 16 * 2304:][:2304], t % 16
+        at = [k_byte(j, int(i)) for i in d] + [v_byte(j, int(i)) for i in d]
+        at += [param_byte(j, g, v) + o for g in range(2) for v in range(2) for o in range(4)]
+        rows.append([int(tile[a]) for a in at])
+    for i, row in enumerate(rows):
+        t = first + i
+        tile, j = pages[int(table[b][t // 64]), c][(t % 64) // 16 * 2304:][:2304], t % 16
+        at = [k_byte(j, int(i)) for i in d] + [v_byte(j, int(i)) for i in d]
+        at += [param_byte(j, g, v) + o for g in range(2) for v in range(2) for o in range(4)]
+        for a, x in zip(at, row):
+            tile[a] = x

@@ -54,6 +54,28 @@ def surprisal(logits, tokens):
     return H + 0.0
 
 
+def states_logprobs(states, weight, tokens, scale=1.0):
+    """states [R][D], weight [V][D] -> dict(logprob, lse) of the logits scale * states @ weight.T."""
+    r = token_logprobs(np.asarray(states, np.float64) @ np.asarray(weight, np.float64).T * scale, tokens)
+    return dict(logprob=r["logprob"], lse=r["lse"])
+
+
+def states_gradient(states, weight, tokens, grad, grad_lse, scale=1.0):
+    """(d_states, d_weight, G) of sum(grad * logprob) + sum(grad_lse * lse): logprob of token -1 is
+    0, whatever the states."""
+    h, w = np.asarray(states, np.float64), np.asarray(weight, np.float64)
+    x = h @ w.T * scale
+    p = np.exp(x - x.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    G = grad_lse[:, None] * p
+    for r, t in enumerate(tokens):
+        if t >= 0:
+            G[r] -= grad[r] * p[r]
+            G[r, t] += grad[r]
+    G *= scale
+    return G @ w, G.T @ h, G
+
+
 def rope_frequencies(rot, base, scaling="none", factor=1.0, original=8192, beta_fast=32.0,
                      beta_slow=1.0, low=1.0, high=4.0, attention_factor=0.0):
     """(angle per position of each pair, factor on the result)."""

@@ -33,7 +33,7 @@ constexpr int kSegment = 16;       // blocks of K that one accumulator of the lo
 constexpr int kTileThreads = (kEpilogueWarps + 2) * 32;
 constexpr uint64_t kStatesWaitNs = 2000000000ull;
 constexpr int64_t kRowsAtOnce = 8192;  // rows whose tiles' sums are kept at a time
-constexpr int kSplitCtas = 160;        // of a product whose sum over k is split, at most
+constexpr int kShareCtas = 320;        // tiles of 128 rows, times the shares that their sums over K are cut into, at most
 constexpr int kSplitBlocks = 8;        // of 64 in a share of k, at least
 constexpr int64_t kPiece = 8192;       // tokens of the vocabulary in a piece, at least
 
@@ -82,7 +82,10 @@ struct TileParams {
   float* acc;               // [m][n] sums of earlier pieces
   void* out;                // [m][n], or null: sums stay in acc
   int first;                // nothing in acc yet
-  int splits;               // shares of k; each has an acc of its own
+  int whole;                // tiles that are summed in one go; the sums of the others are cut into
+  int shares;               // shares of K, which meet in
+  float* parts;             // [tile][share][rows of a tile][kColumns]
+  int wide_out;             // rows of out are 32-byte aligned
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -186,35 +189,53 @@ __device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, 
   }
 }
 
+// r (8 numbers), times `down`, as 16 bytes
 template <typename T>
-__device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, int row, int n0, int held, int split) {
+__device__ __forceinline__ uint4 rounded8(const uint32_t* r, float down) {
+  float x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[j]) * down;
+  return make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
+}
+
+// part: where this thread's row of a share goes, or null
+template <typename T>
+__device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, int row, int n0, int held, float* part) {
   const float down = 1.f / *P.unit;
-  float* acc = P.acc + (int64_t(split) * P.m + row) * P.n + n0;
-  T* out = static_cast<T*>(P.out) + int64_t(row) * P.n + n0;
+  float* acc = part ? part : P.acc + int64_t(row) * P.n + n0;
+  const bool add = !part && !P.first;
+  T* out = part ? nullptr : static_cast<T*>(P.out) + int64_t(row) * P.n + n0;
   for (int c = 0; c < held; c += 32) {  // held: a multiple of 8
     uint32_t r[32];
     tmem_load32(r, at + c);
     tmem_wait(r);
     if (row < P.m) {
+      if (add) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        if (c + i < held) {
-          if (!P.first) {
-            const float4 u = *reinterpret_cast<const float4*>(acc + c + i), v = *reinterpret_cast<const float4*>(acc + c + i + 4);
-            const float o[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[i + j] = __float_as_uint(__uint_as_float(r[i + j]) + o[j]);
+        for (int i = 0; i < 32; i += 4)
+          if (c + i < held) {
+            const float4 u = *reinterpret_cast<const float4*>(acc + c + i);
+            r[i] = __float_as_uint(__uint_as_float(r[i]) + u.x);
+            r[i + 1] = __float_as_uint(__uint_as_float(r[i + 1]) + u.y);
+            r[i + 2] = __float_as_uint(__uint_as_float(r[i + 2]) + u.z);
+            r[i + 3] = __float_as_uint(__uint_as_float(r[i + 3]) + u.w);
           }
-          if (P.out) {
-            float x[8];
+      }
+      if (part || !P.out) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[i + j]) * down;
-            *reinterpret_cast<uint4*>(out + c + i) =
-                make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
-          } else {
-            store32(acc + c + i, r + i);
-          }
+        for (int i = 0; i < 32; i += 8)
+          if (c + i < held) store32(acc + c + i, r + i);
+      } else if (P.wide_out && c + 32 <= held) {  // whole sectors (1024 x 32000 x 4096: TODO us, in halves 179)
+#pragma unroll
+        for (int i = 0; i < 32; i += 16) {
+          const uint4 a = rounded8<T>(r + i, down), b = rounded8<T>(r + i + 8, down);
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          store32(out + c + i, w);
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          if (c + i < held) *reinterpret_cast<uint4*>(out + c + i) = rounded8<T>(r + i, down);
       }
     }
   }
@@ -240,35 +261,50 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 // The tiles of a CTA (or pair) in turn: t, t + step, ..., without divisions on the way, which the
-// ring would run empty for (together 5% at 4096 x 128000 x 4096).  `inner` tiles are neighbours.
+// ring would run empty for (together 5% at 4096 x 128000 x 4096).  `inner` tiles are neighbours.  From `whole` on
+// items are shares of a tile's sum over K, a share of all those tiles after the other (CUT).
+template <bool CUT>
 struct Walk {
-  int t, step, inner, outer, split;
-  int d_inner, d_outer, d_split, n_inner, n_outer, each, more;
+  int t, step, inner, outer, share;  // share: -1 of a whole tile
+  int d_inner, d_outer, n_inner, whole, rest, blocks, each, more;
   bool n_first;
   __device__ __forceinline__ Walk(const TileParams& P, int first, int step_) : t(first), step(step_), n_first(P.n_first) {
     n_inner = n_first ? P.n_tiles : P.m_tiles;
-    n_outer = n_first ? P.m_tiles : P.n_tiles;
-    inner = t % n_inner;
-    outer = t / n_inner % n_outer;
-    split = t / n_inner / n_outer;
+    whole = P.whole;
+    rest = P.m_tiles * P.n_tiles - whole;
     d_inner = step % n_inner;
-    d_outer = step / n_inner % n_outer;
-    d_split = step / n_inner / n_outer;
-    const int blocks = (P.k + kBlockK - 1) / kBlockK;
-    each = blocks / P.splits;
-    more = blocks - each * P.splits;
+    d_outer = step / n_inner;
+    blocks = (P.k + kBlockK - 1) / kBlockK;
+    each = CUT ? blocks / P.shares : blocks;
+    more = CUT ? blocks - each * P.shares : 0;
+    place();
+  }
+  __device__ __forceinline__ void place() {
+    int tile = t;
+    share = -1;
+    if (CUT && t >= whole) {
+      share = rest > 0 ? (t - whole) / rest : 0;
+      tile = t - share * rest;
+    }
+    outer = tile / n_inner;
+    inner = tile - outer * n_inner;
   }
   __device__ __forceinline__ void next() {
     t += step;
+    if (CUT && t >= whole) {
+      place();
+      return;
+    }
     inner += d_inner;
     outer += d_outer;
-    split += d_split;
     if (inner >= n_inner) inner -= n_inner, ++outer;
-    if (outer >= n_outer) outer -= n_outer, ++split;
   }
   __device__ __forceinline__ int mt() const { return n_first ? outer : inner; }
   __device__ __forceinline__ int nt() const { return n_first ? inner : outer; }
-  __device__ __forceinline__ int block(int s) const { return s * each + min(s, more); }  // first of share s of K
+  __device__ __forceinline__ int cut() const { return outer * n_inner + inner - whole; }  // of the tiles that are cut
+  // blocks of K
+  __device__ __forceinline__ int from() const { return !CUT || share < 0 ? 0 : share * each + min(share, more); }
+  __device__ __forceinline__ int to() const { return !CUT || share < 0 ? blocks : (share + 1) * each + min(share + 1, more); }
 };
 // A place in the ring and the parity of its barriers' phases
 template <int STAGES>
@@ -312,7 +348,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
   const uint32_t tmem = sh.tmem;
   follow_previous();
 
-  const int tiles = P.m_tiles * P.n_tiles * P.splits, step = gridDim.x / CG;
+  const int items = MODE == kProduct ? P.whole + (P.m_tiles * P.n_tiles - P.whole) * P.shares : P.m_tiles * P.n_tiles;
+  const int step = gridDim.x / CG;
 
   if (warp == kEpilogueWarps) {
     if (lane == 0) {
@@ -324,8 +361,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
       Place<kStages> at;
       uint32_t done = 0;
       bool lost = false;
-      for (Walk w(P, blockIdx.x / CG, step); w.t < tiles && !lost; w.next()) {
-        const int k_end = w.block(w.split + 1);
+      for (Walk<MODE == kProduct> w(P, blockIdx.x / CG, step); w.t < items && !lost; w.next()) {
+        const int k_end = w.to();
         const int m0 = w.mt() * kRowsOfCta * CG, n0 = w.nt() * P.width;
         auto there = [](int x0, int extent, int limit) { return min(max(limit - x0, 0), extent); };
         const int a0 = m0 + int(rank) * kRowsOfCta, b0 = n0 + int(rank) * width;
@@ -355,7 +392,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         };
         // across, the end of K has boxes of its own; along K, the last rows
         const CUtensorMap *ma = AX || a_there == kRowsOfCta ? &P.a : &P.a_edge, *mb = BX || b_there == width ? &P.b : &P.b_edge;
-        int kb = w.block(w.split);
+        int kb = w.from();
         const int whole = min(k_end, P.k / kBlockK);
         for (; kb < whole && !lost; ++kb) lost = !bring(kb, ma, mb, bytes);
         if (kb < k_end && !lost) lost = !bring(kb, AX ? &P.a_edge : ma, BX ? &P.b_edge : mb, bytes_end);
@@ -371,8 +408,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
       uint32_t i = 0;
       bool lost = false;
       const uint64_t desc_a = tc_operand(smem_u32(sh.ring[0]), AX, 64 * 128), desc_b = tc_operand(smem_u32(sh.ring[0]) + kBytesA, BX, 64 * 128);
-      for (Walk w(P, blockIdx.x / CG, step); w.t < tiles && !lost; w.next(), ++i) {
-        const int k_end = w.block(w.split + 1);
+      for (Walk<MODE == kProduct> w(P, blockIdx.x / CG, step); w.t < items && !lost; w.next(), ++i) {
+        const int k_end = w.to();
         uint32_t buf = 0;
         bool add = false;
         auto open = [&]() {  // the next accumulator
@@ -402,7 +439,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
           at.next();
           return true;
         };
-        int kb = w.block(w.split);
+        int kb = w.from();
         const int whole = min(k_end, P.k / kBlockK);
         if (MODE == kSums) {
           // an accumulator for each kSegment blocks
@@ -449,7 +486,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
       }
       ++i;
     };
-    for (Walk w(P, blockIdx.x / CG, step); w.t < tiles && !lost; w.next()) {
+    for (Walk<MODE == kProduct> w(P, blockIdx.x / CG, step); w.t < items && !lost; w.next()) {
       const int row = (w.mt() * CG + int(rank)) * kRowsOfCta + warp % 4 * 32 + lane, n0 = w.nt() * P.width + half;
       const int held = min(kHalf, min(P.width - half, P.n - n0));  // of this half; may be none
       if constexpr (MODE == kSums) {
@@ -488,7 +525,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         if constexpr (MODE == kGradient)
           tile_gradient<T>(P, at, row, n0, held);
         else
-          tile_product<T>(P, at, row, n0, held, w.split);
+          tile_product<T>(P, at, row, n0, held,
+                          w.share < 0 ? nullptr
+                                      : P.parts + ((int64_t(w.cut()) * P.shares + w.share) * CG * kRowsOfCta + row - w.mt() * CG * kRowsOfCta) * kColumns + half);
         give();
       }
     }
@@ -601,38 +640,45 @@ __global__ void __launch_bounds__(1024) unit_kernel(const UnitParams P) {
   }
 }
 
-// Adds the shares of k in order, eight numbers a thread.
+// Adds the shares of the tiles whose sums were cut, in order, eight numbers a thread.
 struct AddParams {
-  const float* acc;
+  const float* parts;
+  float* acc;
   const float* unit;
-  void* out;
-  int64_t n;  // numbers of a share
-  int splits;
+  void* out;  // or null: the sums stay in acc
+  int m, n, m_tiles, n_tiles, n_first, whole, shares, rows, first;
 };
 constexpr int kAddThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kAddThreads) add_kernel(const AddParams P) {
   follow_previous();
-  const int64_t i = (int64_t(blockIdx.x) * kAddThreads + threadIdx.x) * 8;
-  if (i >= P.n) return;
+  const int i = (blockIdx.x * kAddThreads + threadIdx.x) * 8, tile = P.whole + blockIdx.y;
+  const int outer = tile / (P.n_first ? P.n_tiles : P.m_tiles), inner = tile - outer * (P.n_first ? P.n_tiles : P.m_tiles);
+  const int row = (P.n_first ? outer : inner) * P.rows + i / kColumns, col = (P.n_first ? inner : outer) * kColumns + i % kColumns;
+  if (row >= P.m || col >= P.n) return;
+  const float* part = P.parts + int64_t(blockIdx.y) * P.shares * P.rows * kColumns + i;
+  const int64_t at = int64_t(row) * P.n + col;
   float x[8] = {};
-#pragma unroll 4
-  for (int s = 0; s < P.splits; ++s) {
-    const float4 u = *reinterpret_cast<const float4*>(P.acc + s * P.n + i);
-    const float4 v = *reinterpret_cast<const float4*>(P.acc + s * P.n + i + 4);
+  auto add = [&](const float* p) {
+    const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
     x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
     x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
-  }
-  const float down = 1.f / *P.unit;
+  };
+  if (!P.first) add(P.acc + at);
+#pragma unroll 4
+  for (int s = 0; s < P.shares; ++s) add(part + int64_t(s) * P.rows * kColumns);
+  uint32_t r[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] *= down;
-  *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + i) =
-      make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
+  for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(x[j]);
+  if (P.out)
+    *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at) = rounded8<T>(r, 1.f / *P.unit);
+  else
+    store32(P.acc + at, r);
 }
 
 // ---------------------------------------------------------------------- host
 struct StatesWs {
-  size_t unit, at_token, sums, acc, g, total;
+  size_t unit, at_token, sums, parts, acc, g, total;
 };
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 // Tokens of the vocabulary whose part of G is held at a time: at least kPiece, and 2^27 numbers
@@ -652,8 +698,9 @@ StatesWs states_ws(int64_t rows, int64_t vocab, int64_t dim, bool backward) {
   const size_t forward = L.sums + align256(std::max(few, many));
   L.total = forward;
   if (backward) {
-    L.acc = 512;
-    L.g = L.acc + align256(std::max(size_t(rows) * dim, size_t(kSplitCtas) * kRowsOfCta * kColumns) * 4);
+    L.parts = 512;
+    L.acc = L.parts + align256(size_t(kShareCtas) * kRowsOfCta * kColumns * 4);
+    L.g = L.acc + align256(size_t(rows) * dim * 4);
     const int64_t all = rows * round_up(vocab, kColumns);
     L.total = std::max(forward, L.g + align256(size_t(std::min(all, std::max(rows * kPiece, int64_t(1) << 27))) * 2));
   }
@@ -679,7 +726,10 @@ sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t str
   P.m_tiles = int((int64_t(P.m) + kRowsOfCta * CG - 1) / (kRowsOfCta * CG));
   P.n_tiles = (P.n + P.width - 1) / P.width;
   if (int64_t(P.m_tiles) * P.n_tiles > (1 << 30)) return SEKV_ERR_UNSUPPORTED;
-  P.splits = std::max(P.splits, 1);
+  if (P.shares == 0) {  // all tiles whole
+    P.whole = P.m_tiles * P.n_tiles;
+    P.shares = 1;
+  }
   auto fn = tile_kernel<T, CG, MODE, AX, BX>;
   const size_t shared = sizeof(TileShared<CG>) + 1024;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared)) != cudaSuccess) {
@@ -687,7 +737,7 @@ sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t str
     return SEKV_ERR_CUDA;
   }
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(unsigned(std::min(P.m_tiles * P.n_tiles * P.splits, sms / CG) * CG));
+  lc.gridDim = dim3(unsigned(std::min(P.whole + (P.m_tiles * P.n_tiles - P.whole) * P.shares, sms / CG) * CG));
   lc.blockDim = dim3(kTileThreads);
   lc.dynamicSmemBytes = shared;
   lc.stream = stream;
@@ -772,25 +822,40 @@ TileParams tile_params(const Call& c) {
   return P;
 }
 
-// The product of a gradient, rounded to `out` (or left in acc, where `out` is null: more pieces follow)
+// The product of a gradient, rounded to `out` (or left in acc, where `last` is false: more pieces follow).  The
+// tiles that do not fill a wave have their sums over K cut into shares (4096 x 4096 over 32768 on 76 pairs: 256
+// tiles are three waves and 28 tiles, which take a wave of their own or, in shares, TODO of one).
 template <typename T, bool AX, bool BX>
-sekv_status product(TileParams& P, const Call& c, int sms, bool may_split, bool last, void* out) {
-  const int cg = ctas_of(P.m);
-  // too few tiles for the GPU and a long sum: shares of it side by side
-  const int64_t tiles = int64_t((P.m - 1) / (kRowsOfCta * cg) + 1) * ((P.n - 1) / kColumns + 1);
-  P.splits = 1;
-  if (may_split && tiles * 2 * cg <= sms)
-    P.splits = std::max(1, std::min(std::min(sms, kSplitCtas) / int(tiles * cg), (P.k + kBlockK - 1) / kBlockK / kSplitBlocks));
-  P.out = last && P.splits == 1 ? out : nullptr;
+sekv_status product(TileParams& P, const Call& c, int sms, bool last, void* out) {
+  const int cg = ctas_of(P.m), units = sms / cg, blocks = (P.k + kBlockK - 1) / kBlockK;
+  const int64_t m_tiles = (P.m - 1) / (kRowsOfCta * cg) + 1, tiles = m_tiles * ((P.n - 1) / kColumns + 1);
+  const int rest = int(tiles % units);
+  int shares = 1;
+  auto time = [&](int s) { return double((rest * s + units - 1) / units) / s + 0.002 * s; };
+  for (int s = 2; s <= units && rest > 0 && rest * s * cg <= kShareCtas && blocks / s >= kSplitBlocks; ++s)
+    if (time(s) < time(shares)) shares = s;
+  const bool cut = shares > 1 && (time(1) - time(shares)) * blocks >= 16;  // what adding them up costs
+  P.whole = int(cut ? tiles - rest : tiles);
+  P.shares = cut ? shares : 1;
+  P.out = last ? out : nullptr;
+  P.wide_out = P.n % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 32 == 0;
   sekv_status st = launch_for<T, kProduct, AX, BX>(P, c.dtype, sms, c.stream);
-  if (st != SEKV_OK || !last || P.splits == 1) return st;
+  if (st != SEKV_OK || !cut) return st;
   AddParams A{};
+  A.parts = P.parts;
   A.acc = P.acc;
   A.unit = P.unit;
-  A.out = out;
-  A.n = int64_t(P.m) * P.n;
-  A.splits = P.splits;
-  return launch_following(add_kernel<T>, dim3(unsigned((A.n / 8 + kAddThreads - 1) / kAddThreads)), kAddThreads, 0, c.stream, A);
+  A.out = P.out;
+  A.m = P.m;
+  A.n = P.n;
+  A.m_tiles = P.m_tiles;
+  A.n_tiles = P.n_tiles;
+  A.n_first = P.n_first;
+  A.whole = P.whole;
+  A.shares = shares;
+  A.rows = cg * kRowsOfCta;
+  A.first = P.first;
+  return launch_following(add_kernel<T>, dim3(unsigned(A.rows * kColumns / 8 / kAddThreads), unsigned(rest)), kAddThreads, 0, c.stream, A);
 }
 
 template <typename T>
@@ -881,8 +946,8 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
       if (!map_operand(&Q.a, &Q.a_edge, c.dtype, false, g, nv, c.rows, piece, kRowsOfCta) ||
           !map_operand(&Q.b, &Q.b_edge, c.dtype, true, weight, c.dim, nv, c.weight_stride, kBlockK))
         return SEKV_ERR_UNSUPPORTED;
-      // the shares of every piece have to be the same: the last, smaller one would have other
-      st = product<T, false, true>(Q, c, sms, piece >= c.vocab, v0 + piece >= c.vocab, d_states);
+      Q.parts = reinterpret_cast<float*>(c.ws + L.parts);
+      st = product<T, false, true>(Q, c, sms, v0 + piece >= c.vocab, d_states);
     }
     if (st == SEKV_OK && d_weight) {  // G^T H
       TileParams Q = tile_params(c);
@@ -893,12 +958,11 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
       Q.n_first = 1;
       Q.unit = U.unit;
       Q.first = 1;
-      Q.acc = reinterpret_cast<float*>(c.ws + L.acc);
+      Q.parts = reinterpret_cast<float*>(c.ws + L.parts);
       if (!map_operand(&Q.a, &Q.a_edge, c.dtype, true, g, nv, c.rows, piece, kBlockK) ||
           !map_operand(&Q.b, &Q.b_edge, c.dtype, true, c.states, c.dim, c.rows, c.state_stride, kBlockK))
         return SEKV_ERR_UNSUPPORTED;
-      // with one piece acc is free again: d_states is done
-      st = product<T, true, true>(Q, c, sms, piece >= c.vocab, true, static_cast<T*>(d_weight) + v0 * c.dim);
+      st = product<T, true, true>(Q, c, sms, true, static_cast<T*>(d_weight) + v0 * c.dim);
     }
   }
   return st;

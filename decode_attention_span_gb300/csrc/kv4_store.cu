@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StorePara
 // sekv_kv4_keep: a block moves the kept tokens of one (sequence, KV head).  A warp takes every
 // kKeepWarps-th of them; all are read before any is written, because a place may be filled whose token
 // moves too.  A few hundred bytes a block: its time is that of a chain of four loads (list, table,
-// codes) and a launch.
+// codes) and a launch (with the read of what was kept, two launches: 1 x 16 tokens 4.1 us, 256 x 64 17.1 us).
 constexpr int kKeepWarps = 8;
 struct KeepParams {
   Kv4Pages pg;

@@ -166,7 +166,7 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 // The same by a whole warp, one of whose threads issues it: with operands that the compiler sees to be the
-// warp's own, it keeps them in uniform registers (a thread that is alone takes about 120 clocks to move them there)
+// warp's own, it keeps them in uniform registers (64 columns, A in tensor memory: 34 clocks each, by a lone thread 46)
 __device__ __forceinline__ void tc_mma_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
   asm volatile(
       "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n"

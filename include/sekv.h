@@ -778,7 +778,11 @@ sekv_status sekv_kv4_attention(const sekv_config* cfg, const sekv_kv4_cache* cac
  *          for all.  A negative first sets device code 1 (detail: the sequence) and its tokens see
  *          nothing
  * The other arguments, the workspace (ctx_len: n_q), limits and accuracy are sekv_kv4_attention's; a
- * token that sees nothing has out 0 and lse -inf. */
+ * token that sees nothing has out 0 and lse -inf.  Many (token, head) pairs over many pages go
+ * 128 at a time through another kernel; which one, and how the pages are shared out, goes by the
+ * sizes, the lengths and the table's width, and moves results by roundings only.  In that kernel keys and
+ * values are exact but where a token's two scales lie more than 2^25 apart (the smaller one is then
+ * rounded to a multiple of 2^-32 of the larger's power of two). */
 sekv_status sekv_kv4_tree_attention(const sekv_config* cfg, const sekv_kv4_cache* cache,
                                     int32_t dtype, const void* q, int32_t n_q,
                                     const int32_t* first, const int64_t* tree,
@@ -851,6 +855,9 @@ sekv_status sekv_states_surprisal(const void* states, int32_t dtype, int64_t bat
  *   grad_logprob, grad_lse   f32 [n_rows], either may be NULL (0)
  *   d_states [n_rows][dim], d_weight [vocab][dim], dtype, dense, 16-byte aligned; either may be
  *            NULL.  They must not overlap the inputs
+ * The factors of the logits are rounded to the inputs' type before the two products with them, so that an
+ * f16 d_weight is off by 1.3 to 1.4 times what rounding the result alone gives.
+ * A row whose lse is not finite has gradient NaN (and so all of d_weight) unless its factors are 0.
  * A row of token -1 has no logprob; a row whose two factors are 0 adds nothing to d_weight and has
  * gradient 0, provided that its state is finite.  A token outside [0, vocab) makes its row's
  * gradient, and what it adds to d_weight, NaN.  n_rows 0 sets d_weight to 0.  Deterministic.

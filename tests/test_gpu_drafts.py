@@ -82,7 +82,7 @@ def oracle_of(q, cache, first, tree, scale, used):
 
 
 # ------------------------------------------------------------------ trees
-CASES = [(8, 1, 1, [0]), (4, 1, 3, [5, 0]), (32, 8, 6, [33]), (28, 4, 5, [64, 63, 1]), (8, 2, 16, [48, 112]), (7, 1, 64, [300]),
+CASES = [(8, 1, 1, [0]), (1, 1, 1, [64]), (2, 1, 2, [70, 3]), (4, 1, 3, [5, 0]), (32, 8, 6, [33]), (28, 4, 5, [64, 63, 1]), (8, 2, 16, [48, 112]), (7, 1, 64, [300]),
          (8, 1, 64, [0, 1, 700]), (16, 2, 64, [64, 10]), (6, 2, 61, [191]), (8, 8, 33, [77, 5])]
 
 

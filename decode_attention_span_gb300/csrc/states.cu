@@ -60,6 +60,10 @@ struct __align__(1024) TileShared {
   uint8_t ring[Ring<CG>::kStages][Ring<CG>::kBytes];
   uint64_t full[Ring<CG>::kStages], empty[Ring<CG>::kStages], acc_full[2], acc_empty[2], drained;
   uint32_t tmem;
+  // of a pair, for its end: blocks that each CTA's copies were issued for, and whether a warp of the
+  // pair gave up (the copies' of either CTA, the products'); of a place's last block, the bytes of this
+  // CTA's copies and of the other's
+  uint32_t issued[2], gave_up[3], own[Ring<CG>::kStages], others[Ring<CG>::kStages];
 };
 
 enum Mode { kSums, kGradient, kProduct };
@@ -388,12 +392,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             bytes_end += operand_bytes<AX>(ta, k_rest) + operand_bytes<BX>(tb, k_rest);
           }
         }
-        auto bring = [&](int kb, const CUtensorMap* ma, const CUtensorMap* mb, uint32_t n) {
+        auto bring = [&](int kb, const CUtensorMap* ma, const CUtensorMap* mb, uint32_t n, int k_held) {
           if (!mbar_wait_parked(&sh.empty[at.s], at.odd ^ 1, P.wait_ns)) {
             set_device_error(P.status, DEV_WAIT_TIMEOUT, 4);
             return false;
           }
           if (rank == 0) mbar_arrive_expect_tx(&sh.full[at.s], n);
+          if constexpr (CG == 2) {
+            const uint32_t own = operand_bytes<AX>(a_there, k_held) + operand_bytes<BX>(b_there, k_held);
+            sh.own[at.s] = own;
+            sh.others[at.s] = n - own;
+          }
           const uint32_t bar = full0 + at.s * 8, a = ring0 + at.s * Ring<CG>::kBytes;
           load_operand<AX, CG == 2, kRowsOfCta>(a, ma, a0, a_there, kb * kBlockK, bar);
           load_operand<BX, CG == 2, kColumns / CG>(a + kBytesA, mb, b0, b_there, kb * kBlockK, bar);
@@ -405,13 +414,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         const CUtensorMap *ma = AX || a_there == kRowsOfCta ? &P.a : &P.a_edge, *mb = BX || b_there == width ? &P.b : &P.b_edge;
         int kb = w.from();
         const int whole = min(k_end, P.k / kBlockK);
-        for (; kb < whole && !lost; ++kb) lost = !bring(kb, ma, mb, bytes);
-        if (kb < k_end && !lost) lost = !bring(kb, AX ? &P.a_edge : ma, BX ? &P.b_edge : mb, bytes_end);
+        for (; kb < whole && !lost; ++kb) lost = !bring(kb, ma, mb, bytes, kBlockK);
+        if (kb < k_end && !lost) lost = !bring(kb, AX ? &P.a_edge : ma, BX ? &P.b_edge : mb, bytes_end, k_rest);
       }
-      // no copy may be in flight when the CTA ends
-      if (rank == 0)
+      // no copy may be in flight when the CTA ends; a pair sees to that when both know of each other
+      if constexpr (CG == 2) {
+        store_both(&sh.issued[rank], done);
+        store_both(&sh.gave_up[rank], lost);
+      } else {
         for (uint32_t i = done < kStages ? 0 : done - kStages; i < done; ++i)
           if (!mbar_wait_parked(&sh.full[i % kStages], i / kStages & 1, kStatesWaitNs)) break;
+      }
     }
   } else if (warp == kEpilogueWarps + 1) {
     if (rank == 0 && lane == 0) {
@@ -472,6 +485,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
       // nor may a product
       tc_commit<CG>(&sh.drained);
       mbar_wait_parked(&sh.drained, 0, kStatesWaitNs);
+      if constexpr (CG == 2) store_both(&sh.gave_up[2], lost);
     }
   } else {
     uint32_t i = 0;
@@ -546,7 +560,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync_all();
+  if constexpr (CG == 2) {
+    cluster_sync_all();
+    // The products' commits arrive in both CTAs: this CTA's last arrival, before it may end
+    if (rank != 0 && warp == kEpilogueWarps + 1) mbar_wait_parked(&sh.drained, 0, kStatesWaitNs);
+    // Where nobody gave up, the products have waited for every copy.  Otherwise each CTA stopped copying on
+    // its own, and copies of either signal the first one's barriers: a block that only one of them copied is
+    // waited for without the other's bytes.  (One is ahead by kStages blocks at most: a place is free again only
+    // when a product of both CTAs' copies has read it.)
+    if (sh.gave_up[0] || sh.gave_up[1] || sh.gave_up[2]) {  // the same in both
+      if (rank == 0 && threadIdx.x == kEpilogueWarps * 32) {
+        const uint32_t here = sh.issued[0], there = sh.issued[1], most = max(here, there);
+        for (uint32_t i = most < kStages ? 0 : most - kStages; i < most; ++i) {
+          uint64_t* bar = &sh.full[i % kStages];
+          if (i >= here)
+            mbar_arrive_expect_tx(bar, load_peer(&sh.own[i % kStages], 1));
+          else if (i >= there)
+            mbar_complete_tx(bar, sh.others[i % kStages]);
+          if (!mbar_wait_parked(bar, i / kStages & 1, kStatesWaitNs)) break;
+        }
+      }
+      __syncwarp();
+      cluster_sync_all();
+    }
+  }
   tc_fence_after();
   if (warp == kEpilogueWarps) tmem_free<CG>(tmem, 2 * kColumns);
 }

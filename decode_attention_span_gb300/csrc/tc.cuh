@@ -21,6 +21,20 @@ __device__ __forceinline__ uint32_t peer_u32(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+__device__ __forceinline__ uint32_t load_peer(const uint32_t* p, uint32_t rank) {
+  uint32_t x;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(peer_u32(p, rank)) : "memory");
+  return x;
+}
+// In both CTAs of a pair
+__device__ __forceinline__ void store_both(uint32_t* p, uint32_t x) {
+#pragma unroll
+  for (uint32_t r = 0; r < 2; ++r) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_u32(p, r)), "r"(x) : "memory");
+}
+// Takes bytes that will not come off what the barrier's phase waits for
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
   const int items = sh.plan.before[P.batch], cap = P.pg.max_pages * kKv4Page;
   bool lost = false;       // a wait of this warp ran out: it waits and works no more
   uint32_t pages = 0;      // before this item
+  uint32_t issued = 0;     // pages that the copying warp has brought: all of them, unless it is lost
   auto wait = [&](uint64_t* bar, uint32_t parity, int which, uint32_t sleep_ns = 0) {
     if (!lost && !wait_for(bar, parity, P.wait_ns, sleep_ns)) {
       set_device_error(P.pg.status, DEV_WAIT_TIMEOUT, which);
@@ -845,6 +846,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
                 mbar_arrive(&sh.raw_full[raw]);
               }
             }
+            ++issued;
             __syncwarp();
           }
         }
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
 
   // no copy or product may be in flight when the CTA ends
   if (warp == kCopy && lane == 0) {
-    for (uint32_t i = pages < kRaw ? 0 : pages - kRaw; i < pages; ++i)
+    for (uint32_t i = issued < kRaw ? 0 : issued - kRaw; i < issued; ++i)
       if (!mbar_wait_parked(&sh.raw_full[i % kRaw], i / kRaw & 1, kTreeWaitNs)) break;
   }
   if (warp == kMma || warp == kMma + 1) {

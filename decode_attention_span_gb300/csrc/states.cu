@@ -10,8 +10,9 @@
 // tile of logits lives in tensor memory only: the loss keeps a maximum and a sum of each row and
 // half tile, the gradient a tile of G as 16-bit numbers, for one piece of the vocabulary at a time,
 // which the other two products read.  G is written once and read twice, across K in the second product
-// (dW), so that no transposed copy is made.  Its rounding to 16 bits adds to that of the results: in f16 dW's error is
-// 1.3 to 1.4 times that of 32-bit sums rounded once (4.4e-4 for 3.2e-4); two numbers for G would double both products.
+// (dW), so that no transposed copy is made.  Its rounding to 16 bits adds to that of the results
+// (a mean over 96 to 1024 rows: errors 1.02 to 1.04 times those of rounding the results alone in bf16, 1.06 to 1.09 in
+// f16); two numbers for G would remove that and double both products.
 //
 // One kernel does all: a pair of CTAs takes 256 x 256 tiles (each brings half of both operands, so that an
 // operand byte is read from L2 for 256 products, not 128), one CTA 128 x 256 where there are up to 128 rows.
@@ -22,6 +23,7 @@
 // bytes' time).  Rows whose length is no multiple of 128 bytes cross a line of L2
 // more (1003 x 50021 x 1000 in f16: 87 us, 1.15 PFLOP/s).
 #include <cuda_fp16.h>
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -89,8 +91,7 @@ struct TileParams {
   int64_t ld;
   // kGradient
   const float *lse, *grad, *grad_lse;
-  const float* unit;        // of G
-  float scale;
+  const float* unit;        // of G: what brings its rows' factors there, and what takes the sums back
   int col0, vocab;          // this piece's first token
   void* g;                  // [m][ld]
   // kProduct
@@ -166,6 +167,7 @@ __device__ __forceinline__ void tile_sums(const TileParams& P, float (&x)[kHalf]
 template <typename T>
 __device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, int row, int n0, int held) {
   float on_p = 0.f, on_tok = 0.f, lse = 0.f;
+  bool none = true;  // nothing of the row counts, whatever it holds
   int64_t tok = -1;
   if (row < P.m) {
     tok = token_of(P.tokens, P.tokens_64, P.token_skip, P.token_period, P.row0 + row);
@@ -173,13 +175,13 @@ __device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, 
     if (!ok && tok != -1) on_tok = NAN;
     if (ok && P.grad) on_tok = P.grad[row];
     on_p = (P.grad_lse ? P.grad_lse[row] : 0.f) - on_tok;
-    const float up = P.scale * *P.unit;
+    none = on_p == 0.f && on_tok == 0.f;
+    const float up = P.unit[0];
     on_p *= up;
     on_tok *= up;
     lse = P.lse[row] * kLog2e;
     tok -= P.col0 + n0;
   }
-  const bool none = on_p == 0.f && on_tok == 0.f;  // nothing of the row counts, whatever it holds
   const int hit = row < P.m && tok >= 0 && tok < held ? int(tok) : -1;
   T* g = static_cast<T*>(P.g) + int64_t(row) * P.ld + n0;
   // whole groups of 32, which a row of g has room for; beyond `held` it is not read
@@ -216,7 +218,7 @@ __device__ __forceinline__ uint4 rounded8(const uint32_t* r, float down) {
 // part: where this thread's row of a share goes, or null
 template <typename T>
 __device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, int row, int n0, int held, float* part) {
-  const float down = 1.f / *P.unit;
+  const float down = P.unit[1];
   float* acc = part ? part : P.acc + int64_t(row) * P.n + n0;
   const bool add = !part && !P.first;
   T* out = part ? nullptr : static_cast<T*>(P.out) + int64_t(row) * P.n + n0;
@@ -652,25 +654,25 @@ __global__ void __launch_bounds__(kJoinRows * kJoinShares) join_kernel(const Joi
   }
 }
 
-// A power of two that brings the largest factor on a row of G to 2^13 .. 2^14 (f16 has 2^-24 below
-// it), or 1 (bf16).
+// G's unit: G is held as `up` times its rows' factors, with the largest of them at 2^13 (f16 has 2^-24 below 1), and
+// the sums are multiplied by `down` = scale / up.  Where all rows have one factor, as those of a mean have, its
+// rounding in a G is one and the same in all of them, and so an error of the gradient as a whole (of 1000 rows in f16 at
+// a power of two: 2.1 times what rounding the results alone gives, by arithmetic in 64 bits); 2^13 is exact.
 struct UnitParams {
   const float *grad, *grad_lse;
   float* unit;
   float scale;
   int64_t rows;
-  int f16;
 };
 __global__ void __launch_bounds__(1024) unit_kernel(const UnitParams P) {
   __shared__ float part[32];
   follow_previous();
   float big = 0.f;
-  if (P.f16)
-    for (int64_t r = threadIdx.x; r < P.rows; r += 1024) {
-      const float g = P.grad ? P.grad[r] : 0.f, e = P.grad_lse ? P.grad_lse[r] : 0.f;
-      const float x = fmaxf(fabsf(g), fabsf(e - g)) * P.scale;
-      if (x < INFINITY) big = fmaxf(big, x);
-    }
+  for (int64_t r = threadIdx.x; r < P.rows; r += 1024) {
+    const float g = P.grad ? P.grad[r] : 0.f, e = P.grad_lse ? P.grad_lse[r] : 0.f;
+    const float x = fmaxf(fabsf(g), fabsf(e - g));
+    if (x < INFINITY) big = fmaxf(big, x);
+  }
   for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = big;
   __syncthreads();
@@ -678,12 +680,10 @@ __global__ void __launch_bounds__(1024) unit_kernel(const UnitParams P) {
     big = part[threadIdx.x];
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
     if (threadIdx.x == 0) {
-      float unit = 1.f;
-      if (big > 0.f) {
-        const int e = int(__float_as_uint(big) >> 23) - 127;
-        unit = __uint_as_float(uint32_t(min(max(127 + 13 - e, 1), 253)) << 23);
-      }
-      *P.unit = unit;
+      // 2^126: both stay normal numbers, for factors of any size
+      const float up = big > 0.f ? fminf(8192.f / big, 0x1p126f) : 1.f;
+      P.unit[0] = up;
+      P.unit[1] = fminf(P.scale / up, FLT_MAX);
     }
   }
 }
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kAddThreads) add_kernel(const AddParams P) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(x[j]);
   if (P.out)
-    *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at) = rounded8<T>(r, 1.f / *P.unit);
+    *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at) = rounded8<T>(r, P.unit[1]);
   else
     store32(P.acc + at, r);
 }
@@ -863,7 +863,6 @@ TileParams tile_params(const Call& c) {
   P.tokens_64 = c.tokens_64 != 0;
   P.token_skip = c.token_skip;
   P.token_period = c.token_period;
-  P.scale = c.scale;
   P.factor = c.scale * kLog2e;
   P.vocab = int(c.vocab);
   P.k = int(c.dim);
@@ -961,7 +960,6 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
   U.unit = reinterpret_cast<float*>(c.ws + L.unit);
   U.scale = c.scale;
   U.rows = c.rows;
-  U.f16 = c.dtype == SEKV_F16;
   sekv_status st = launch_following(unit_kernel, dim3(1), 1024, 0, c.stream, U);
   const int64_t piece = piece_of(c.rows, c.vocab);
   T* g = reinterpret_cast<T*>(c.ws + L.g);

@@ -849,14 +849,15 @@ sekv_status sekv_states_surprisal(const void* states, int32_t dtype, int64_t bat
  *   G_rv = scale ((grad_lse_r - grad_logprob_r) exp(x_rv - lse_r) + grad_logprob_r [v = tok_r])
  *   d_states = G weight,  d_weight = G^T states
  * The logits are made again, for one piece of the vocabulary at a time; G is held for that piece
- * as numbers of dtype (f16: times a power of two that brings the largest factor on a row to
- * 2^13 .. 2^14, so that an element below 2^-38 of that counts as 0), the sums are fp32 and rounded
- * once.
+ * as numbers of dtype, times a number that brings the largest |grad_logprob_r| or
+ * |grad_lse_r - grad_logprob_r| to 2^13; the sums are fp32 and rounded once.  In f16 an element
+ * below 2^-27 of that largest factor loses bits, and one below 2^-38 counts as 0, so that a row whose
+ * factors are far below another row's is less exact; in bf16 no element loses bits by its size.
  *   grad_logprob, grad_lse   f32 [n_rows], either may be NULL (0)
  *   d_states [n_rows][dim], d_weight [vocab][dim], dtype, dense, 16-byte aligned; either may be
  *            NULL.  They must not overlap the inputs
- * The factors of the logits are rounded to the inputs' type before the two products with them, so that an
- * f16 d_weight is off by 1.3 to 1.4 times what rounding the result alone gives.
+ * The rounding of G adds to that of the results: rows with one factor (of a mean) are off by 1.03 to 1.1
+ * times what rounding the results alone gives, rows with any factors by up to 1.42 times (in the mean square).
  * A row whose lse is not finite has gradient NaN (and so all of d_weight) unless its factors are 0.
  * A row of token -1 has no logprob; a row whose two factors are 0 adds nothing to d_weight and has
  * gradient 0, provided that its state is finite.  A token outside [0, vocab) makes its row's

@@ -40,3 +40,49 @@ def test_pairs_that_give_up_end_at_once(sk, T, D):
     again = sk.states_logprobs_backward(x, w, tok, want.lse, g, ws)
     assert ws.status() == (0, 0) and torch.equal(got.lse, want.lse) and torch.equal(got.logprob, want.logprob)
     assert torch.equal(again[0], grads[0]) and torch.equal(again[1], grads[1])
+
+
+def rounding_ratios(sk, dtype, n, scale=1.0):
+    """Errors of d_states and d_weight of a mean over n rows (times 1024, away from f16's smallest numbers), in units of
+    the error that rounding the exact ones alone has."""
+    V, D = 4000, 64
+    x, w, tok = inputs(dtype, n, V, D, n)
+    ws = sk.StatesWorkspace(n, V, D, backward=True)
+    g = torch.full((n,), -1024.0 / n, device="cuda")
+    lse = sk.states_logprobs(x.cuda(), w.cuda(), tok.cuda(), ws, scale=scale).lse
+    got = sk.states_logprobs_backward(x.cuda(), w.cuda(), tok.cuda(), lse, g, ws, scale=scale)
+    h, m = x.double(), w.double()
+    G = torch.softmax(h @ m.T * scale, 1)
+    G[torch.arange(n), tok] -= 1
+    G *= scale * 1024.0 / n
+    return [float((a.cpu().double() - b).norm() / (b.to(x.dtype).double() - b).norm()) for a, b in zip(got, (G @ m, G.T @ h))]
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 1021), ("bf16", 600), ("bf16", 300), ("bf16", 1024), ("fp16", 1000), ("fp16", 200), ("fp16", 1021)])
+def test_gradient_of_a_mean_for_any_number_of_rows(sk, dtype, n):
+    """G's roundings are independent of each other: their error in the results is at most as large as the results' own
+    roundings', in the mean square, so that both together are at most sqrt(2) of those (2% for the sample).  One and
+    the same rounding of 1 / n in all rows would be more: 1.5 to 2.1 times at these n, at a power of two."""
+    assert max(rounding_ratios(sk, dtype, n)) < 2 ** 0.5 * 1.02
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("scale,size", [(2.0 ** 100, 2.0 ** -104), (2.0 ** -30, 2.0 ** 34), (2.0 ** 120, 2.0 ** -120)])
+def test_gradient_of_scales_and_factors_that_cancel(sk, dtype, scale, size):
+    """Factor times scale is of ordinary size, though neither of the two is.  All logits are 0: states and weight
+    share no dimension."""
+    T, V, D = 40, 300, 64
+    h, m, tok = inputs(dtype, T, V, D, 3)
+    h[:, 32:], m[:, :32] = 0, 0
+    ws = sk.StatesWorkspace(T, V, D, backward=True)
+    g = torch.full((T,), size, device="cuda")
+    lse = sk.states_logprobs(h.cuda(), m.cuda(), tok.cuda(), ws, scale=scale).lse
+    got = sk.states_logprobs_backward(h.cuda(), m.cuda(), tok.cuda(), lse, g, ws, scale=scale)
+    assert ws.status() == (0, 0)
+    G = torch.full((T, V), -1.0 / V, dtype=torch.float64)
+    G[torch.arange(T), tok] += 1
+    G *= size * scale
+    # each element of G and each result is off by half a step, and the probabilities by 2^-20
+    eps = torch.finfo(h.dtype).eps
+    for a, want, size in zip(got, (G @ m.double(), G.T @ h.double()), (G.abs() @ m.double().abs(), G.abs().T @ h.double().abs())):
+        assert ((a.cpu().double() - want).abs() <= 1.05 * eps * size + (2.0 ** -25 if dtype == "fp16" else 0)).all()

@@ -660,16 +660,20 @@ __global__ void __launch_bounds__(kJoinRows * kJoinShares) join_kernel(const Joi
 // a power of two: 2.1 times what rounding the results alone gives, by arithmetic in 64 bits); 2^13 is exact.
 struct UnitParams {
   const float *grad, *grad_lse;
+  const void* tokens;
   float* unit;
   float scale;
-  int64_t rows;
+  int64_t rows, vocab;
+  int tokens_64;
 };
 __global__ void __launch_bounds__(1024) unit_kernel(const UnitParams P) {
   __shared__ float part[32];
   follow_previous();
   float big = 0.f;
   for (int64_t r = threadIdx.x; r < P.rows; r += 1024) {
-    const float g = P.grad ? P.grad[r] : 0.f, e = P.grad_lse ? P.grad_lse[r] : 0.f;
+    const int64_t tok = token_of(P.tokens, P.tokens_64, 0, 0, r);
+    // without a token grad counts for nothing, and may be anything
+    const float g = P.grad && tok >= 0 && tok < P.vocab ? P.grad[r] : 0.f, e = P.grad_lse ? P.grad_lse[r] : 0.f;
     const float x = fmaxf(fabsf(g), fabsf(e - g));
     if (x < INFINITY) big = fmaxf(big, x);
   }
@@ -960,6 +964,9 @@ sekv_status backward(const Call& c, const float* lse, const float* grad, const f
   U.unit = reinterpret_cast<float*>(c.ws + L.unit);
   U.scale = c.scale;
   U.rows = c.rows;
+  U.vocab = c.vocab;
+  U.tokens = c.tokens;
+  U.tokens_64 = c.tokens_64 != 0;
   sekv_status st = launch_following(unit_kernel, dim3(1), 1024, 0, c.stream, U);
   const int64_t piece = piece_of(c.rows, c.vocab);
   T* g = reinterpret_cast<T*>(c.ws + L.g);

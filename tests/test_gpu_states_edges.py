@@ -86,3 +86,24 @@ def test_gradient_of_scales_and_factors_that_cancel(sk, dtype, scale, size):
     eps = torch.finfo(h.dtype).eps
     for a, want, size in zip(got, (G @ m.double(), G.T @ h.double()), (G.abs() @ m.double().abs(), G.abs().T @ h.double().abs())):
         assert ((a.cpu().double() - want).abs() <= 1.05 * eps * size + (2.0 ** -25 if dtype == "fp16" else 0)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("ids", [torch.int32, torch.int64])
+@pytest.mark.parametrize("pad", [1e30, 3e38, float("inf"), float("nan")])
+def test_gradient_beside_padding_with_anything_in_it(sk, dtype, ids, pad):
+    """The factor on a row without a token counts for nothing, whatever it is: the same bits as with 0 there."""
+    T, V, D = 200, 300, 64
+    x, w, tok = (t.cuda() for t in inputs(dtype, T, V, D, 5))
+    tok = tok.to(ids)
+    tok[::3] = -1
+    ws = sk.StatesWorkspace(T, V, D, backward=True)
+    g = torch.randn(T, generator=torch.Generator().manual_seed(1)).cuda()
+    g[::3] = 0
+    lse = sk.states_logprobs(x, w, tok, ws).lse
+    want = sk.states_logprobs_backward(x, w, tok, lse, g, ws)
+    g[::3] = pad
+    got = sk.states_logprobs_backward(x, w, tok, lse, g, ws)
+    assert ws.status() == (0, 0) and not got[0][::3].any()
+    for a, b in zip(got, want):
+        assert a.any() and torch.equal(a, b)

@@ -963,7 +963,7 @@ Kv4Ws kv4_ws(const sekv_config* cfg, int64_t n_q, int sms) {
   Kv4Ws L{};
   L.partials = 256;
   L.wide = L.partials + align256(size_t(sms) * 2 * kStateFloats * 4);
-  L.arrived = L.wide + align256(kTreeBytes);
+  L.arrived = L.wide + align256(tree_bytes(sms));
   L.total = L.arrived + align256(size_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * 4);
   return L;
 }
@@ -1036,6 +1036,7 @@ sekv_status attention(const sekv_config* cfg, const sekv_kv4_cache* cache, int32
     c.out = out;
     c.lse = lse;
     c.partials = reinterpret_cast<float*>(w + L.wide);
+    c.kept = c.partials + kTreeItems * kTreePartialFloats;
     c.wait_ns = (cfg->flags & SEKV_FLAG_SHORT_WAITS) ? 0 : kWaitNs;
     c.batch = cfg->batch;
     c.hpg = cfg->n_q_heads / cfg->n_kv_heads;

@@ -48,6 +48,10 @@ constexpr int kTop = 8;
 constexpr int kHalfPage = 32;                    // tokens that a stream takes at a time
 constexpr int kStreamColumns = 256;              // tensor memory of a stream: two pages' logits or weights, 64 columns each, and the values
 constexpr int kValues = 128;                     // from here on
+// Pages of a stream between two flushes, of 128 additions in tensor memory.  Those cut off towards zero: values that
+// all point one way were off by 2^-17.6 of their size after 32 pages and 2^-13.6 after 500, with flushes 2^-18.7 after
+// any number.  A flush takes some 3 us, its wait for the products among them (131072 tokens 308 -> 332 us).
+constexpr int kFlush = 16;
 constexpr int kItemCost = 8;                     // what an item costs beyond its pages, in pages
 constexpr float kNone = -3e38f;
 constexpr float kGrowth = 8.f;
@@ -514,6 +518,77 @@ __device__ __forceinline__ void soft_half(Soft& S, Pair (&l)[4], Pair (&c)[4][2]
   tmem_wait_stores();
 }
 
+// What a thread has flushed, in memory: it alone writes and reads it
+__device__ __forceinline__ float4 load_kept(const float4* p) {
+  float4 x;
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p) : "memory");
+  return x;
+}
+__device__ __forceinline__ void store_kept(float4* p, float4 x) {
+  asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
+}
+// A thread's place there: values, then for each of its rows the sums of the weights and of those times z', and the
+// reference that all of them are of
+constexpr int kKeptSums = kTreeRows * kHeadDim / 4;
+__device__ __forceinline__ float4* kept_of(const TreeCall& P, int stream) {
+  return reinterpret_cast<float4*>(P.kept + (int64_t(blockIdx.x) * 2 + stream) * kTreeKeptFloats) + threadIdx.x % kTreeRows;
+}
+// A stream's sums since the last flush join those before it (`first`: none), rounded properly, there or, of the
+// `last` pages, in tensor memory.  done(): waits for the products.
+template <typename F>
+__device__ __forceinline__ void flush(const TreeCall& P, const Soft& S, Pair (&l)[4], Pair (&c)[4][2], int stream, uint32_t values, bool first,
+                                      bool last, F done) {
+  float4* kept = kept_of(P, stream);
+  float4 was[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) was[i] = first ? make_float4(0.f, 0.f, 0.f, kNone) : load_kept(kept + kKeptSums + i * kTreeRows);
+  done();
+  float old[4], now[4];  // factors on what was there and on what joins it
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f = ex2(was[i].w - S.m[i]);
+    old[i] = last ? f * S.u(i) : f;
+    now[i] = last ? 1.f : 1.f / S.u(i);
+    float l0, l1, z0, z1, z2, z3;
+    l[i].get(l0, l1);
+    c[i][0].get(z0, z1);
+    c[i][1].get(z2, z3);
+    const float4 x = make_float4(fmaf(was[i].x, f, l0 + l1), fmaf(was[i].y, f, z0 + z1), fmaf(was[i].z, f, z2 + z3), S.m[i]);
+    if (!last) store_kept(kept + kKeptSums + i * kTreeRows, x);
+    l[i] = Pair(last ? x.x : 0.f, 0.f);
+    c[i][0] = Pair(last ? x.y : 0.f, 0.f);
+    c[i][1] = Pair(last ? x.z : 0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int n = 0; n < 4; ++n, kept += 8 * kTreeRows, values += 32) {
+    uint32_t r[2][16];
+    float4 y[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) tmem_load_16x32(r[h], values + (uint32_t(h * 16) << 16));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = first ? make_float4(0.f, 0.f, 0.f, 0.f) : load_kept(kept + j * kTreeRows);
+    tmem_wait_loads();
+    tie(r[0]);
+    tie(r[1]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t* v = &r[j / 4][j % 4 * 4];
+      auto join = [&](float x, uint32_t w, int row) { return fmaf(x, old[row], __uint_as_float(w) * now[row]); };
+      const int row = j / 4 * 2;
+      y[j] = make_float4(join(y[j].x, v[0], row), join(y[j].y, v[1], row), join(y[j].z, v[2], row + 1), join(y[j].w, v[3], row + 1));
+      v[0] = __float_as_uint(y[j].x), v[1] = __float_as_uint(y[j].y), v[2] = __float_as_uint(y[j].z), v[3] = __float_as_uint(y[j].w);
+    }
+    if (last) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_store_16x32(values + (uint32_t(h * 16) << 16), r[h]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) store_kept(kept + j * kTreeRows, y[j]);
+    }
+  }
+  tmem_wait_stores();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_constant__ TreeCall P) {
   extern __shared__ uint8_t smem_raw[];
@@ -649,43 +724,59 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       const Pair none(0.f, 0.f);
       Pair l2[4] = {none, none, none, none}, c2[4][2] = {{none, none}, {none, none}, {none, none}, {none, none}};
       bool any = false;
-      for (int k = stream; k < n; k += 2, ++of_stream) {
-        const uint32_t buf = (pages + k) % kVals, place = of_stream & 1;
-        wait(&sh.v_full[buf], (pages + k) / kVals & 1, 4);
-        wait(&sh.s_full[stream][place], of_stream >> 1 & 1, 5);
-        if (__any_sync(~0u, lost)) lost = true;
-        if (lost) break;
-        tc_fence_after();
-        const PageParams& par = sh.par[buf];
-        const int pos = (I.page0 + k) * kKv4Page;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          // The products with the weights of the half page before.  They may lag behind by three halves, no more
-          // (the logits of this page were multiplied after those of the page before the last), so each place and
-          // half has a barrier of its own, which no two phases can pass unseen.
-          auto settle = [&]() {
-            const uint32_t of = half ? of_stream : of_stream - 1;
-            wait(&sh.v_done[stream][of & 1][half ^ 1], of >> 1 & 1, 6);
+      for (int k0 = stream; k0 < n && !lost; k0 += 2 * kFlush) {
+        const int k1 = k0 + 2 * kFlush;
+#pragma unroll 1
+        for (int k = k0; k < min(n, k1); k += 2, ++of_stream) {
+          const uint32_t buf = (pages + k) % kVals, place = of_stream & 1;
+          wait(&sh.v_full[buf], (pages + k) / kVals & 1, 4);
+          wait(&sh.s_full[stream][place], of_stream >> 1 & 1, 5);
+          if (__any_sync(~0u, lost)) lost = true;
+          if (lost) break;
+          tc_fence_after();
+          const PageParams& par = sh.par[buf];
+          const int pos = (I.page0 + k) * kKv4Page;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            // The products with the weights of the half page before.  They may lag behind by three halves, no more
+            // (the logits of this page were multiplied after those of the page before the last), so each place and
+            // half has a barrier of its own, which no two phases can pass unseen.
+            auto settle = [&]() {
+              const uint32_t of = half ? of_stream : of_stream - 1;
+              wait(&sh.v_done[stream][of & 1][half ^ 1], of >> 1 & 1, 6);
+              tc_fence_after();
+              __syncwarp();
+            };
+            uint32_t seen[4] = {};
+            const uint32_t a = at + place * kKv4Page + half * kHalfPage;
+            if (pos + (half + 1) * kHalfPage > prefix || par.held < (half + 1) * kHalfPage) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = row0 + 8 * i;
+                const uint64_t tree = r < cols ? uint64_t(P.tree[I.b * P.tree_stride + (col0 + r) / P.hpg]) : 0;
+                seen[i] = uint32_t(seen_of(tree, prefix, pos, par.held) >> (half * kHalfPage));
+              }
+              soft_half<true>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[row0], settle);
+            } else {
+              soft_half<false>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[row0], settle);
+            }
+            any = true;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[stream][place][half]);
+          }
+        }
+        const bool first = k0 < 2, last = k1 >= n;
+        lost = __any_sync(~0u, lost);
+        if (!(first && last) && !lost) {  // the products of the pages that follow are a new sum
+          flush(P, S, l2, c2, stream, at + kValues, first, last, [&]() {
+            wait(&sh.v_done[stream][(of_stream - 1) & 1][1], (of_stream - 1) >> 1 & 1, 6);
             tc_fence_after();
             __syncwarp();
-          };
-          uint32_t seen[4] = {};
-          const uint32_t a = at + place * kKv4Page + half * kHalfPage;
-          if (pos + (half + 1) * kHalfPage > prefix || par.held < (half + 1) * kHalfPage) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = row0 + 8 * i;
-              const uint64_t tree = r < cols ? uint64_t(P.tree[I.b * P.tree_stride + (col0 + r) / P.hpg]) : 0;
-              seen[i] = uint32_t(seen_of(tree, prefix, pos, par.held) >> (half * kHalfPage));
-            }
-            soft_half<true>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[row0], settle);
-          } else {
-            soft_half<false>(S, l2, c2, par, half, a, at + kValues, any, seen, t, &sh.q_sum[row0], settle);
-          }
-          any = true;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_full[stream][place][half]);
+          });
+          any = last;
+          lost = __any_sync(~0u, lost);
         }
       }
       wait(&sh.o_full, n_items & 1, 6);
@@ -910,6 +1001,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
           if (stream + 2 < n && !lost) logits(stream + 2, done + 1);
           for (int k = stream; k < n && !lost; k += 2, ++done) {
             const uint32_t val = (base + k) % kVals, place = done & 1;
+            const bool more = (k >> 1) % kFlush > 0;
             if (!wait_warp(&sh.v_full[val], (base + k) / kVals & 1, 4, 50)) break;
             const uint64_t b = v_desc + val * (kOpBytes / 16);
 #pragma unroll
@@ -921,7 +1013,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
               for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                  tc_mma_tmem_warp(d0 + kValues, a + part * 16 + j * 8, b + (2 * half + j) * 128, by_value, k > 1 || half + part + j > 0);
+                  tc_mma_tmem_warp(d0 + kValues, a + part * 16 + j * 8, b + (2 * half + j) * 128, by_value,
+                                   more || half + part + j > 0);
               tc_commit_warp(&sh.v_done[stream][place][half]);
             }
             tc_commit_warp(&sh.v_empty[val]);

@@ -1,11 +1,14 @@
 """GPU: tree attention where it is easy to go wrong: waits that run out, long sums, workspaces."""
+import math
 import time
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_drafts import cache_of, i32, masks, put, trees
-from test_gpu_operators import gen, kv_rows
+from oracle import kv4
+from test_gpu_drafts import cache_of, i32, masks, put, rising, trees
+from test_gpu_operators import check_attention, gen, kv_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +40,99 @@ def test_a_tree_that_gives_up_ends_at_once(sk, pages):
     assert time.monotonic() - t0 < 1.0
     got = sk.kv4_tree_attention(cfg, cache, q, first, t, 0.1, ws)
     assert ws.status() == (0, 0) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def shared_cache(sk, B, hkv, n_q, hq, k, v):
+    """B sequences that all hold the tokens k, v [1][T][hkv][128], in the same pages."""
+    T = k.shape[1]
+    mp = -(-T // 64)
+    one = sk.Config(1, hq, hkv, 0, 0, 64)
+    pages = torch.zeros(mp, hkv, 9216, dtype=torch.uint8, device="cuda")
+    table = torch.randperm(mp, generator=gen(1)).to(torch.int32)[None].cuda()
+    ws = sk.Workspace(one, which=sk.SEKV_CALL_KV4, ctx_len=n_q)
+    cache = sk.Kv4Cache(one, pages, table)
+    sk.kv4_append(one, cache, k, v, i32([0]), ws)
+    values = sk.kv4_read(one, cache, i32([0]), T, ws, out=tuple(torch.empty(1, hkv, T, 128, device="cuda") for _ in "kv"))
+    cfg = sk.Config(B, hq, hkv, 0, 0, 64)
+    many = sk.Kv4Cache(cfg, pages, table.expand(B, mp).contiguous())
+    return cfg, many, sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=n_q), values
+
+
+@pytest.mark.parametrize("kind", ["high", "low", "constant", "any"])
+@pytest.mark.parametrize("B,hq,hkv,T", [
+    (20, 16, 8, 24000),     # 160 groups: more than are ever cut
+    (20, 16, 8, 2100),      # a flush and little more
+    (1, 32, 8, 131072),     # cut into long pieces
+    (3, 7, 1, 50000)])
+def test_values_that_point_one_way_over_a_long_context(sk, kind, B, hq, hkv, T):
+    """Logits near 0: outputs are off by at most 2^-18 of the weighted mean of a group's largest value, and twice the
+    logits' error, however long the sum is."""
+    n_q = 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    v = 1 - 0.05 * torch.rand(1, T, hkv, 128, generator=g, device="cuda")
+    if kind == "low":
+        v = 1 - v
+    v[..., ::64] = 1.0 if kind == "low" else 0.0     # one element of a group spreads its codes
+    v *= 0.5 + 0.5 * torch.rand(1, T, hkv, 1, generator=g, device="cuda")
+    if kind == "constant":
+        v[:] = 0.1
+    if kind == "any":
+        v = torch.randn(1, T, hkv, 128, generator=g, device="cuda")
+    v = v.bfloat16()
+    k = torch.randn(1, T, hkv, 128, generator=g, device="cuda").bfloat16()
+    cfg, cache, ws, (keys, values) = shared_cache(sk, B, hkv, n_q, hq, k, v)
+    q, scale = torch.randn(B, n_q, hq, 128, generator=gen(2)).bfloat16().cuda(), 0.002
+    own = torch.tensor([1 << i if i < 63 else -(1 << 63) for i in range(n_q)], dtype=torch.int64).cuda()
+    out, lse = sk.kv4_tree_attention(cfg, cache, q, i32([T - n_q] * B), own, scale, ws)
+    assert ws.status() == (0, 0) and sk.last_launch_count() == (1 if B * hkv > 152 else 2)
+    G = hq // hkv
+    hidden = torch.cat([torch.zeros(n_q, T - n_q, dtype=torch.bool), ~torch.eye(n_q, dtype=torch.bool)], 1).cuda()
+    for b, c in {(0, 0), (B - 1, hkv - 1)}:
+        x, y, h = keys[0, c].double(), values[0, c].double(), q[b, :, c * G:c * G + G].double()
+        kmax = x.abs().amax().item()  # s is at most 2 kmax / 15 (rounded up by 2^-8), |z| + 15 |s| at most 3 kmax
+        dx = scale * (2.0 ** -16 * h.abs().amax(-1) * 4.1 / 15 * kmax + 2.0 ** -22 * h.abs().sum(-1) * 3 * kmax)
+        p = torch.einsum("igd,td->igt", h, x) * scale
+        p.masked_fill_(hidden[:, None], float("-inf"))
+        want_lse = torch.logsumexp(p, -1)
+        p = torch.softmax(p, -1)
+        bound = p @ y.view(T, 2, 64).abs().amax(2).repeat_interleave(64, 1)
+        err = (out[b, :, c * G:c * G + G].double() - p @ y).abs() / bound
+        assert (err <= 2.0 ** -18 + 2 * dx[..., None]).all(), err.max().item()
+        assert ((lse[b, :, c * G:c * G + G].double() - want_lse).abs() <= 2.0 ** -18 + dx + 2.0 ** -22 * want_lse).all()
+
+
+@pytest.mark.parametrize("what", [3.0, 9.0, 20.0, -9.0, "early", "late", "falling"])
+def test_references_and_units_move_between_flushes(sk, what):
+    """160 groups of 94 pages, none cut: what was flushed follows when logits rise by `what` of log2 each 32 tokens, and
+    when tokens of far larger values come early or late or all become smaller."""
+    B, hq, hkv, n_q, T = 20, 16, 8, 64, 6000
+    if isinstance(what, float):
+        k, v, q1 = rising(T, hkv, n_q, hq // hkv, what, 7)
+        scale = 1.0
+    else:
+        k, v = kv_rows("bf16", 1, T, hkv, 9)
+        q1, scale = torch.randn(1, n_q, hq, 128, generator=gen(3)).bfloat16(), 0.02
+        v = v.float()
+        if what == "falling":
+            v *= 2.0 ** (30 - torch.arange(T) / 100).view(1, T, 1, 1)
+        else:
+            v[0, 40 if what == "early" else 5000] *= 2.0 ** 40
+        v = v.bfloat16()
+    cfg, cache, ws, (keys, values) = shared_cache(sk, B, hkv, n_q, hq, k.cuda(), v.cuda())
+    tree = trees(1, n_q, 5)
+    q = q1.cuda().expand(B, n_q, hq, 128).contiguous()
+    out, lse = sk.kv4_tree_attention(cfg, cache, q, i32([T - n_q] * B), masks(tree)[0].contiguous(), scale, ws)
+    assert ws.status() == (0, 0) and sk.last_launch_count() == 1
+    assert torch.equal(out[0], out[B - 1]) and torch.equal(lse[0], lse[7])
+    pages, table = cache.pages.cpu().numpy(), cache.page_table.cpu().numpy()
+    for c in (0, hkv - 1):
+        K, V, ka, va = kv4.get(pages, table, 0, c, T)
+        for i in (0, 31, 63):
+            seen = list(range(T - n_q)) + [T - n_q + j for j in range(n_q) if tree[0][i] >> j & 1]
+            for h in (2 * c, 2 * c + 1):
+                x = K[seen] @ q1[0, i, h].double().numpy() * scale
+                e = np.exp(x - x.max())
+                p = e / e.sum()
+                ref = (p @ V[seen], x.max() + math.log(e.sum()), np.repeat(p @ va[seen], 64),
+                       scale * np.abs(q1[0, i, h].double().numpy()).sum() * ka[seen].max())
+                check_attention(out[3, i, h][None], lse[3, i, h][None], [np.asarray(r)[None] for r in ref])

@@ -945,26 +945,36 @@ int blocks_of(const sekv_config* cfg, int64_t n_q) {
   return int((n_q + tpb - 1) / tpb);
 }
 
-// Whether kv4_tree.cu takes less for `tree_blocks` blocks of columns than this file's kernel for `blocks` of its
-// own, over `pages` pages of all sequences and KV heads (the table's: what the sequences hold is not known
-// here).  Measured, that one takes 28 us and 9.1 ns a page and block, this one 10 us and 1.84 ns.
-bool wide_is_faster(int blocks, int tree_blocks, int64_t pages) {
-  return double(pages) * (1.84 * blocks - 9.1 * tree_blocks) > 18000.;
+// ns a page that kv4_tree.cu saves over this file's kernel.  Measured, that one takes 28 us and 9.1 ns a page and
+// block of its columns, this one 10 us and 1.84 ns.
+double wide_gain(const sekv_config* cfg, int64_t n_q) {
+  const int64_t tree_blocks = (n_q * (cfg->n_q_heads / cfg->n_kv_heads) + kTreeRows - 1) / kTreeRows;
+  return 1.84 * blocks_of(cfg, n_q) - 9.1 * double(tree_blocks);
 }
+// `pages`: of all sequences and KV heads (the table's: what the sequences hold is not known here)
+bool wide_is_faster(const sekv_config* cfg, int64_t n_q, int64_t pages) { return double(pages) * wide_gain(cfg, n_q) > 18000.; }
 
 int attn_ctas() { return std::min(device_sm_count(), kMaxCtas); }  // one per SM
 
 struct Kv4Ws {
   size_t partials, wide, arrived, total;
 };
-Kv4Ws kv4_ws(const sekv_config* cfg, int64_t n_q, int sms) {
-  // the counters last: where they begin is the same whatever batch and n_q a call has, so
-  // that calls of different sizes can take turns on a workspace
+// Room for the counters of 2^20 groups before what kv4_tree.cu takes
+constexpr size_t kCounterBytes = 4 << 20;
+// `wide`: with what kv4_tree.cu takes
+Kv4Ws kv4_ws(const sekv_config* cfg, int64_t n_q, int sms, bool wide) {
+  // The counters behind the partials, whose size is that of any call, and what kv4_tree.cu takes behind all counters:
+  // nothing that a call writes lies where another one, of whatever batch and n_q, has counters, so that calls of
+  // different sizes can take turns on a workspace.
   Kv4Ws L{};
   L.partials = 256;
-  L.wide = L.partials + align256(size_t(sms) * 2 * kStateFloats * 4);
-  L.arrived = L.wide + align256(tree_bytes(sms));
-  L.total = L.arrived + align256(size_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * 4);
+  L.arrived = L.partials + align256(size_t(sms) * 2 * kStateFloats * 4);
+  L.wide = L.arrived + kCounterBytes;
+  const size_t counters = align256(size_t(cfg->batch) * cfg->n_kv_heads * blocks_of(cfg, n_q) * 4);
+  const size_t end = L.wide + align256(tree_bytes(sms));
+  if (counters > kCounterBytes) L.arrived = end;
+  L.total = L.arrived + counters;
+  if (wide) L.total = std::max(L.total, end);
   return L;
 }
 
@@ -975,7 +985,9 @@ namespace sekv {
 size_t kv4_workspace_size(const sekv_config* cfg, int64_t n_q) {
   const int sms = attn_ctas();
   if (sms <= 0 || n_q < 1 || n_q > SEKV_MAX_QUERY_TOKENS || cfg->batch > SEKV_KV4_MAX_BATCH) return 0;
-  return kv4_ws(cfg, n_q, sms).total;
+  bool wide = false;  // for a tree of n_q tokens, or of fewer
+  for (int64_t n = 1; n <= n_q && !wide; ++n) wide = wide_gain(cfg, n) > 0;
+  return kv4_ws(cfg, n_q, sms, wide).total;
 }
 
 sekv_status kv4_check(const sekv_config* cfg, const sekv_kv4_cache* cache, int n_q,
@@ -993,7 +1005,7 @@ sekv_status kv4_check(const sekv_config* cfg, const sekv_kv4_cache* cache, int n
 sekv_status kv4_check_ws(const sekv_config* cfg, int n_q, size_t workspace_bytes) {
   const int sms = attn_ctas();
   if (sms <= 0) return SEKV_ERR_CUDA;
-  if (workspace_bytes < kv4_ws(cfg, n_q, sms).total) return SEKV_ERR_CAPACITY;
+  if (workspace_bytes < kv4_ws(cfg, n_q, sms, false).total) return SEKV_ERR_CAPACITY;
   return SEKV_OK;
 }
 
@@ -1018,10 +1030,11 @@ sekv_status attention(const sekv_config* cfg, const sekv_kv4_cache* cache, int32
   st = kv4_check_ws(cfg, n_q, workspace_bytes);
   if (st != SEKV_OK) return st;
   const int sms = attn_ctas();
-  const Kv4Ws L = kv4_ws(cfg, n_q, sms);
+  const bool wide = tree && wide_gain(cfg, n_q) > 0;
+  const Kv4Ws L = kv4_ws(cfg, n_q, sms, wide);
+  if (workspace_bytes < L.total) return SEKV_ERR_CAPACITY;
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  const int tree_blocks = (n_q * (cfg->n_q_heads / cfg->n_kv_heads) + kTreeRows - 1) / kTreeRows;
-  if (tree && wide_is_faster(blocks_of(cfg, n_q), tree_blocks, int64_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages)) {
+  if (wide && wide_is_faster(cfg, n_q, int64_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages)) {
     TreeCall c{};
     c.pg.pages = static_cast<uint8_t*>(cache->pages);
     c.pg.table = cache->page_table;
@@ -1041,7 +1054,7 @@ sekv_status attention(const sekv_config* cfg, const sekv_kv4_cache* cache, int32
     c.batch = cfg->batch;
     c.hpg = cfg->n_q_heads / cfg->n_kv_heads;
     c.n_q = n_q;
-    c.n_blk = tree_blocks;
+    c.n_blk = (n_q * c.hpg + kTreeRows - 1) / kTreeRows;
     c.bf16 = dtype == SEKV_BF16;
     c.scale_log2 = scale * kLog2e;
     return tree_attention(c, sms, stream);

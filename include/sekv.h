@@ -167,7 +167,8 @@ typedef enum sekv_call {
   SEKV_CALL_FETCH = 1,
   SEKV_CALL_DECODE = 2,   /* sekv_decode_attention and sekv_decode_step */
   SEKV_CALL_BUILD = 3,
-  SEKV_CALL_KV4 = 4       /* sekv_kv4_*; ctx_len is the largest n_q that will be used (>= 1) */
+  SEKV_CALL_KV4 = 4       /* sekv_kv4_*; ctx_len is the largest n_q that will be used (>= 1): some 1.3 MB, and
+                             45 MB where a tree of that many tokens and heads can go 128 columns at a time */
 } sekv_call;
 
 /* Bytes of one basis record (0 when body <= 0); see the layout above. */

@@ -136,3 +136,67 @@ def test_references_and_units_move_between_flushes(sk, what):
                 ref = (p @ V[seen], x.max() + math.log(e.sum()), np.repeat(p @ va[seen], 64),
                        scale * np.abs(q1[0, i, h].double().numpy()).sum() * ka[seen].max())
                 check_attention(out[3, i, h][None], lse[3, i, h][None], [np.asarray(r)[None] for r in ref])
+
+
+def small_ws(sk, cfg, n_q):
+    """A workspace of what the calls other than a wide tree's need: the partials of eight columns for two groups of each
+    CTA, and a counter for each group."""
+    ctas = min(torch.cuda.get_device_properties(0).multi_processor_count, 256)
+    blocks = -(-n_q // (8 // (cfg.n_q_heads // cfg.n_kv_heads)))
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    ws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=1)
+    ws.nbytes = 256 + up(ctas * 2 * 8 * 130 * 4) + up(cfg.batch * cfg.n_kv_heads * blocks * 4)
+    ws.buf = torch.zeros(ws.nbytes, dtype=torch.uint8, device="cuda")
+    return ws
+
+
+@pytest.mark.parametrize("B,hq,hkv,n_q", [(1, 8, 1, 1), (3, 28, 4, 4), (1, 32, 8, 8), (2, 8, 2, 64), (1000, 8, 8, 1)])
+def test_calls_without_a_wide_tree_need_small_workspaces(sk, B, hq, hkv, n_q):
+    cfg, cache, _ = cache_of(sk, B, hq, hkv, 1, 100, False)
+    ws = small_ws(sk, cfg, n_q)
+    full = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=n_q)
+    assert full.nbytes == ws.nbytes if n_q < 9 else full.nbytes > 40 << 20
+    k, v = kv_rows("bf16", B, 100, hkv, 4)
+    put(sk, cfg, cache, ws, k, v, [100] * B)
+    q = torch.randn(B, n_q, hq, 128, generator=gen(1)).bfloat16().cuda()
+    got = sk.kv4_attention(cfg, cache, q, i32([100] * B), 0.1, ws)
+    want = sk.kv4_attention(cfg, cache, q, i32([100] * B), 0.1, full)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    sk.kv4_keep(cfg, cache, i32([90] * B), i32([[0, 2]] * B), None, ws)
+    sk.kv4_read(cfg, cache, i32([90] * B), 2, ws)
+    tree = masks(trees(B, n_q, 1))
+    if n_q == 64:
+        with pytest.raises(sk.SekvError):
+            sk.kv4_tree_attention(cfg, cache, q, i32([30] * B), tree, 0.1, ws)
+    elif n_q < 8:
+        sk.kv4_tree_attention(cfg, cache, q, i32([30] * B), tree, 0.1, ws)
+    assert ws.status() == (0, 0)
+    ws.nbytes -= 256
+    with pytest.raises(sk.SekvError):
+        sk.kv4_attention(cfg, cache, q, i32([100] * B), 0.1, ws)
+
+
+def test_more_groups_than_counters_before_a_wide_tree(sk):
+    """1024 x 17 x 64 groups, whose counters lie behind what a wide tree takes: both take turns on a workspace."""
+    B, hkv, n_q = 1024, 17, 64
+    cfg = sk.Config(B, 8 * hkv, hkv, 0, 0, 64)
+    ws = sk.Workspace(cfg, which=sk.SEKV_CALL_KV4, ctx_len=n_q)
+    pages = torch.zeros(1, hkv, 9216, dtype=torch.uint8, device="cuda")
+    one = sk.Config(1, 8 * hkv, hkv, 0, 0, 64)
+    cache = sk.Kv4Cache(cfg, pages, torch.zeros(B, 1, dtype=torch.int32, device="cuda"))
+    k, v = kv_rows("bf16", 1, 64, hkv, 4)
+    sk.kv4_append(one, sk.Kv4Cache(one, pages, torch.zeros(1, 1, dtype=torch.int32, device="cuda")), k.cuda(), v.cuda(), i32([0]), ws)
+    q = torch.randn(1, n_q, 8 * hkv, 128, generator=gen(1)).bfloat16().cuda().expand(B, -1, -1, -1).contiguous()
+    cfg1, cache1, _ = cache_of(sk, 1, 8, 1, n_q, 9000, True)
+    k1, v1 = kv_rows("bf16", 1, 9000, 1, 4)
+    put(sk, cfg1, cache1, ws, k1, v1, [9000])
+    q1, t1 = torch.randn(1, n_q, 8, 128, generator=gen(2)).bfloat16().cuda(), masks(trees(1, n_q, 1))
+    first = sk.kv4_tree_attention(cfg1, cache1, q1, i32([8900]), t1, 0.1, ws)
+    assert sk.last_launch_count() == 2
+    for _ in range(2):
+        out, lse = sk.kv4_attention(cfg, cache, q, i32([64] * B), 0.1, ws)
+        assert torch.equal(out[0], out[-1]) and torch.equal(lse[5], lse[-1]) and torch.isfinite(out).all()
+        again = sk.kv4_tree_attention(cfg1, cache1, q1, i32([8900]), t1, 0.1, ws)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    check_attention(out[:1], lse[:1], kv4.attention(q[:1].double().cpu().numpy(), pages.cpu().numpy(), np.zeros((1, 1), np.int32), [64], 0.1))
+    assert ws.status() == (0, 0)

@@ -42,7 +42,11 @@ constexpr int kColumns = 256;    // of an accumulator; two of them fill tensor m
 constexpr int kBytesA = kRowsOfCta * kBlockK * 2;
 constexpr int kEpilogueWarps = 8;  // two for each 32 lanes, half of the columns each
 constexpr int kHalf = kColumns / 2;
-constexpr int kSegment = 16;       // blocks of K that one accumulator of the loss sums
+// Blocks of K that one accumulator sums, of the logits and of the products with G.  The tensor cores cut their sums off
+// towards zero, and what is added outside is rounded properly: in 256 additions (K 4096) 1.8e-6 of lse, after each 1024 of
+// K 4e-7.  The products' results are rounded to 16 bits; terms of one sign were off by 3.9e-4 with K 60000 (f16 rounds
+// by 2.0e-4 in the mean square), after each 4096 of K by 2.4e-5.
+constexpr int kSegmentLogits = 16, kSegmentProduct = 64;
 constexpr int kTileThreads = (kEpilogueWarps + 2) * 32;
 constexpr uint64_t kStatesWaitNs = 2000000000ull;
 constexpr int64_t kRowsAtOnce = 8192;  // rows whose tiles' sums are kept at a time
@@ -206,6 +210,48 @@ __device__ __forceinline__ void tile_gradient(const TileParams& P, uint32_t at, 
   }
 }
 
+// The same of products that are in registers: loops that leave the columns' numbers known
+template <typename T>
+__device__ __forceinline__ void tile_gradient(const TileParams& P, const float (&y)[kHalf], int row, int n0, int held) {
+  float on_p = 0.f, on_tok = 0.f, lse = 0.f;
+  bool none = true;
+  int64_t tok = -1;
+  if (row < P.m) {
+    tok = token_of(P.tokens, P.tokens_64, P.token_skip, P.token_period, P.row0 + row);
+    const bool ok = tok >= 0 && tok < P.vocab;
+    if (!ok && tok != -1) on_tok = NAN;
+    if (ok && P.grad) on_tok = P.grad[row];
+    on_p = (P.grad_lse ? P.grad_lse[row] : 0.f) - on_tok;
+    none = on_p == 0.f && on_tok == 0.f;
+    const float up = P.unit[0];
+    on_p *= up;
+    on_tok *= up;
+    lse = P.lse[row] * kLog2e;
+    tok -= P.col0 + n0;
+  }
+  const int hit = row < P.m && tok >= 0 && tok < held ? int(tok) : -1;
+  T* g = static_cast<T*>(P.g) + int64_t(row) * P.ld + n0;
+#pragma unroll
+  for (int c = 0; c < kHalf; c += 32) {
+    if (c >= held) break;
+    uint32_t r[16];
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = none ? 0.f : on_p * ex2(fmaf(y[c + i], P.factor, -lse));
+    if (__any_sync(~0u, hit >= c && hit < c + 32)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (hit == c + i) x[i] += on_tok;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = pack2(x[2 * i], x[2 * i + 1], T());
+    if (row < P.m) {
+      store32(g + c, r);
+      store32(g + c + 16, r + 8);
+    }
+  }
+}
+
 // r (8 numbers), times `down`, as 16 bytes
 template <typename T>
 __device__ __forceinline__ uint4 rounded8(const uint32_t* r, float down) {
@@ -254,6 +300,49 @@ __device__ __forceinline__ void tile_product(const TileParams& P, uint32_t at, i
         for (int i = 0; i < 32; i += 8)
           if (c + i < held) *reinterpret_cast<uint4*>(out + c + i) = rounded8<T>(r + i, down);
       }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void tile_product(const TileParams& P, float (&x)[kHalf], int row, int n0, int held, float* part) {
+  if (row >= P.m) return;
+  const float down = P.unit[1];
+  float* acc = part ? part : P.acc + int64_t(row) * P.n + n0;
+  const bool add = !part && !P.first;
+  T* out = part ? nullptr : static_cast<T*>(P.out) + int64_t(row) * P.n + n0;
+#pragma unroll
+  for (int c = 0; c < kHalf; c += 32) {
+    if (c >= held) break;
+    if (add) {
+#pragma unroll
+      for (int i = c; i < c + 32; i += 4)
+        if (i < held) {
+          const float4 u = *reinterpret_cast<const float4*>(acc + i);
+          x[i] += u.x;
+          x[i + 1] += u.y;
+          x[i + 2] += u.z;
+          x[i + 3] += u.w;
+        }
+    }
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(x[c + i]);
+    if (part || !P.out) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 8)
+        if (c + i < held) store32(acc + c + i, r + i);
+    } else if (P.wide_out && c + 32 <= held) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 16) {
+        const uint4 a = rounded8<T>(r + i, down), b = rounded8<T>(r + i + 8, down);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        store32(out + c + i, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 8)
+        if (c + i < held) *reinterpret_cast<uint4*>(out + c + i) = rounded8<T>(r + i, down);
     }
   }
 }
@@ -338,11 +427,12 @@ struct Place {
 // A persistent kernel: one CTA an SM, or a pair of CTAs on two (CG 2), takes tiles of 128 CG rows and
 // `width` columns in turn.  One warp copies operands, one issues the products, four turn the finished
 // accumulator into results while the next one fills.
-template <typename T, int CG, Mode MODE, bool AX, bool BX>
+// SEG: sums over K in segments of kSegmentLogits or kSegmentProduct blocks.
+template <typename T, int CG, Mode MODE, bool SEG, bool AX, bool BX>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ TileParams P) {
   extern __shared__ uint8_t smem_raw[];
   TileShared<CG>& sh = *reinterpret_cast<TileShared<CG>*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
-  constexpr int kStages = Ring<CG>::kStages;
+  constexpr int kStages = Ring<CG>::kStages, kSegment = MODE == kProduct ? kSegmentProduct : kSegmentLogits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
@@ -467,7 +557,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         };
         int kb = w.from();
         const int whole = min(k_end, P.k / kBlockK);
-        if (MODE == kSums) {
+        if (SEG) {
           // an accumulator for each kSegment blocks
           while (kb < k_end && !lost) {
             const int end = min(kb + kSegment, k_end), end_whole = min(end, whole);
@@ -513,12 +603,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
       }
       ++i;
     };
+    auto part_of = [&](const Walk<MODE == kProduct>& w, int row) {
+      return w.share < 0 ? nullptr
+                         : P.parts + ((int64_t(w.cut()) * P.shares + w.share) * CG * kRowsOfCta + row - w.mt() * CG * kRowsOfCta) * kColumns + half;
+    };
     for (Walk<MODE == kProduct> w(P, blockIdx.x / CG, step); w.t < items && !lost; w.next()) {
       const int row = (w.mt() * CG + int(rank)) * kRowsOfCta + warp % 4 * 32 + lane, n0 = w.nt() * P.width + half;
       const int held = min(kHalf, min(P.width - half, P.n - n0));  // of this half; may be none
-      if constexpr (MODE == kSums) {
-        // The tensor cores cut their sums off towards zero, and 256 times (K 4096) that is 1.8e-6 of
-        // lse; summed here after each 1024 of K, properly rounded, 4e-7.
+      if constexpr (SEG) {
         float x[kHalf];
         uint32_t at = take();
         if (lost) break;
@@ -531,7 +623,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
           for (int j = 0; j < 32; ++j) x[c + j] = __uint_as_float(r[j]);
         }
         give();
-        for (int kb = kSegment * kBlockK; kb < P.k; kb += kSegment * kBlockK) {
+        for (int kb = w.from() + kSegment; kb < w.to(); kb += kSegment) {
           at = take();
           if (lost) break;
 #pragma unroll
@@ -545,16 +637,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
           }
           give();
         }
-        if (!lost) tile_sums(P, x, row, w.nt(), warp / 4, n0, held);
+        if (lost) break;
+        if constexpr (MODE == kSums)
+          tile_sums(P, x, row, w.nt(), warp / 4, n0, held);
+        else if constexpr (MODE == kGradient)
+          tile_gradient<T>(P, x, row, n0, held);
+        else
+          tile_product<T>(P, x, row, n0, held, part_of(w, row));
       } else {
         const uint32_t at = take();
         if (lost) break;
         if constexpr (MODE == kGradient)
           tile_gradient<T>(P, at, row, n0, held);
         else
-          tile_product<T>(P, at, row, n0, held,
-                          w.share < 0 ? nullptr
-                                      : P.parts + ((int64_t(w.cut()) * P.shares + w.share) * CG * kRowsOfCta + row - w.mt() * CG * kRowsOfCta) * kColumns + half);
+          tile_product<T>(P, at, row, n0, held, part_of(w, row));
         give();
       }
     }
@@ -772,7 +868,7 @@ bool map_operand(CUtensorMap* map, CUtensorMap* edge, int32_t dtype, bool across
          encode_rows2d(edge, type, base, uint64_t(inner), uint64_t(rows), bytes, kBlockK, uint32_t(rest));
 }
 
-template <typename T, int CG, Mode MODE, bool AX, bool BX>
+template <typename T, int CG, Mode MODE, bool SEG, bool AX, bool BX>
 sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t stream) {
   P.shape = tc_shape(kRowsOfCta * CG, P.width, dtype == SEKV_BF16, AX, BX);
   P.m_tiles = int((int64_t(P.m) + kRowsOfCta * CG - 1) / (kRowsOfCta * CG));
@@ -782,7 +878,7 @@ sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t str
     P.whole = P.m_tiles * P.n_tiles;
     P.shares = 1;
   }
-  auto fn = tile_kernel<T, CG, MODE, AX, BX>;
+  auto fn = tile_kernel<T, CG, MODE, SEG, AX, BX>;
   const size_t shared = sizeof(TileShared<CG>) + 1024;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared)) != cudaSuccess) {
     cudaGetLastError();
@@ -812,10 +908,19 @@ sekv_status launch_tiles(TileParams& P, int32_t dtype, int sms, cudaStream_t str
 
 // A pair of CTAs shares a tile of 256 rows where there are that many
 int ctas_of(int m) { return m > kRowsOfCta ? 2 : 1; }
+// SEG only where a sum is longer than a segment: its tiles pass through registers as a whole, by code that is four times
+// as long, which 96 x 32000 x 1024 takes 74 us for and 67 without
+template <typename T, Mode MODE, bool SEG, bool AX, bool BX>
+sekv_status launch_seg(TileParams& P, int32_t dtype, int sms, cudaStream_t stream) {
+  return ctas_of(P.m) == 2 ? launch_tiles<T, 2, MODE, SEG, AX, BX>(P, dtype, sms, stream)
+                           : launch_tiles<T, 1, MODE, SEG, AX, BX>(P, dtype, sms, stream);
+}
 template <typename T, Mode MODE, bool AX, bool BX>
 sekv_status launch_for(TileParams& P, int32_t dtype, int sms, cudaStream_t stream) {
-  return ctas_of(P.m) == 2 ? launch_tiles<T, 2, MODE, AX, BX>(P, dtype, sms, stream)
-                           : launch_tiles<T, 1, MODE, AX, BX>(P, dtype, sms, stream);
+  int blocks = (P.k + kBlockK - 1) / kBlockK;  // of the longest sum
+  if (MODE == kProduct && P.whole == 0) blocks = (blocks + P.shares - 1) / P.shares;
+  if (blocks > (MODE == kProduct ? kSegmentProduct : kSegmentLogits)) return launch_seg<T, MODE, true, AX, BX>(P, dtype, sms, stream);
+  return launch_seg<T, MODE, MODE == kSums, AX, BX>(P, dtype, sms, stream);
 }
 
 // Columns of a tile of the logits.  Up to 128 rows the weight's bytes bound the product, and 224

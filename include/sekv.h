@@ -851,7 +851,8 @@ sekv_status sekv_states_surprisal(const void* states, int32_t dtype, int64_t bat
  *   d_states = G weight,  d_weight = G^T states
  * The logits are made again, for one piece of the vocabulary at a time; G is held for that piece
  * as numbers of dtype, times a number that brings the largest |grad_logprob_r| (of rows with a
- * token) or |grad_lse_r - grad_logprob_r| to 2^13; the sums are fp32 and rounded once.  In f16 an element
+ * token) or |grad_lse_r - grad_logprob_r| to 2^13; the sums are fp32 (off by 2^-14 of their terms' sizes
+ * at most, however long) and rounded once.  In f16 an element
  * below 2^-27 of that largest factor loses bits, and one below 2^-38 counts as 0, so that a row whose
  * factors are far below another row's is less exact; in bf16 no element loses bits by its size.
  *   grad_logprob, grad_lse   f32 [n_rows], either may be NULL (0)

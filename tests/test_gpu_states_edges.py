@@ -107,3 +107,63 @@ def test_gradient_beside_padding_with_anything_in_it(sk, dtype, ids, pad):
     assert ws.status() == (0, 0) and not got[0][::3].any()
     for a, b in zip(got, want):
         assert a.any() and torch.equal(a, b)
+
+
+def exact_gradient(x, w, tok, g, e):
+    """d_states and d_weight in 64 bits, of tensors on the GPU."""
+    m = w.double()
+    dx, dw = torch.empty(x.shape, dtype=torch.float64, device="cuda"), torch.zeros(w.shape, dtype=torch.float64, device="cuda")
+    for i in range(0, x.shape[0], 1024):
+        h, t, gi = x[i:i + 1024].double(), tok[i:i + 1024], g[i:i + 1024].double()
+        gi = torch.where(t >= 0, gi, 0.0)
+        G = torch.softmax(h @ m.T, 1) * (e[i:i + 1024].double() - gi)[:, None]
+        G[torch.arange(len(t)), t.clamp(min=0)] += gi
+        dx[i:i + 1024] = G @ m
+        dw += G.T @ h
+    return dx, dw
+
+
+@pytest.mark.parametrize("T,V,D", [(1024, 32000, 4096), (60000, 8000, 512), (9000, 70000, 256)])
+def test_long_sums_of_one_sign_are_not_cut_off(sk, T, V, D):
+    """Positive factors, states and weights: errors of the sums would all point one way.  4096 of K are 256 additions of 16
+    products to a sum that grows evenly, each cut off by at most 17 * 2^-25 of it, and what comes after is rounded; the mean
+    error beyond the results' own rounding is at most that, however long the sum."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = (torch.rand(n, D, generator=g, device="cuda") * 0.5 + 0.75 for n in (T, V))
+    x[:, D // 2:] = 0
+    w[:, :D // 2] = 0     # logits from the first dimension alone
+    x[:, 0], w[:, 0] = (torch.randn(n, generator=g, device="cuda") for n in (T, V))
+    x, w = x.half(), w.half()
+    tok, zero, one = torch.full((T,), -1, device="cuda"), torch.zeros(T, device="cuda"), torch.ones(T, device="cuda")
+    ws = sk.StatesWorkspace(T, V, D, backward=True)
+    lse = sk.states_logprobs(x, w, tok, ws).lse
+    got = sk.states_logprobs_backward(x, w, tok, lse, None, ws, grad_lse=one)
+    assert ws.status() == (0, 0)
+    for a, want, at in zip(got, exact_gradient(x, w, tok, zero, one), (slice(D // 2, D), slice(1, D // 2))):
+        a, want = a.double()[:, at], want[:, at]
+        bias = ((a - want.half().double()) / want).mean().item()
+        assert abs(bias) <= 17 * 2.0 ** -25 * 128 + 2.0 ** -18, bias
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_gradient_of_pieces_whose_last_tiles_are_cut(sk, dtype):
+    """10000 rows take 13312 tokens at a time, and 4 of the 80 tiles of d_states have their sums cut into shares in each
+    piece: those of earlier pieces join them.  Each tile on its own, against 64 bits: G and the result are rounded by half
+    a step each."""
+    T, V, D = 10000, 30000, 512
+    x, w, tok = (t.cuda() for t in inputs(dtype, T, V, D, 6))
+    tok[::11] = -1
+    ws = sk.StatesWorkspace(T, V, D, backward=True)
+    g, e = (torch.randn(T, generator=torch.Generator().manual_seed(i)).cuda() for i in (1, 2))
+    lse = sk.states_logprobs(x, w, tok, ws).lse
+    dx, dw = sk.states_logprobs_backward(x, w, tok, lse, g, ws, grad_lse=e)
+    assert ws.status() == (0, 0)
+    half = torch.finfo(x.dtype).eps / 2
+    for a, want in zip((dx, dw), exact_gradient(x, w, tok, g, e)):
+        for i in range(0, want.shape[0], 256):
+            for j in range(0, D, 256):
+                u, v = a[i:i + 256, j:j + 256].double(), want[i:i + 256, j:j + 256]
+                assert float((u - v).norm() / v.norm()) <= 2 * half, (i, j)
+    # one without the other
+    only, _ = sk.states_logprobs_backward(x, w, tok, lse, g, ws, grad_lse=e, want_weight=False)
+    assert torch.equal(only, dx)

@@ -7,8 +7,9 @@ import pytest
 import torch
 
 from oracle import kv4
-from test_gpu_drafts import cache_of, i32, masks, put, rising, trees
+from test_gpu_drafts import cache_of, i32, masks, oracle_of, put, rising, trees
 from test_gpu_operators import check_attention, gen, kv_rows
+from test_gpu_states import check_states
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +201,39 @@ def test_more_groups_than_counters_before_a_wide_tree(sk):
         assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
     check_attention(out[:1], lse[:1], kv4.attention(q[:1].double().cpu().numpy(), pages.cpu().numpy(), np.zeros((1, 1), np.int32), [64], 0.1))
     assert ws.status() == (0, 0)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_two_steps_with_drafted_tokens_against_the_oracles(sk, wide):
+    """Append drafted tokens, attend, score them from last states, keep a branch, and the same again behind it: each step's
+    outputs against the oracles, on the pages that the oracle's keep leaves."""
+    B, hq, hkv, n_q, T, V, D = 2, 16, 2, 64, 300, 500, 128
+    cfg, cache, ws = cache_of(sk, B, hq, hkv, n_q, T + 128, wide)
+    states_ws = sk.StatesWorkspace(B * n_q, V, D)
+    k, v = kv_rows("bf16", B, T, hkv, 1)
+    lens = [T, 190]
+    put(sk, cfg, cache, ws, k, v, lens)
+    branches = [([0, 3, 9, 30], [1, 2]), ([5], [0, 1, 2, 3, 40])]
+    used = -(-(T + 128) // 64)
+    for step in range(2):
+        k, v = (x.cuda() for x in kv_rows("bf16", B, n_q, hkv, 2 + step))
+        q = torch.randn(B, n_q, hq, 128, generator=gen(3 + step)).bfloat16()
+        tree = trees(B, n_q, 4 + step)
+        sk.kv4_append(cfg, cache, k, v, i32(lens), ws)
+        out, lse = sk.kv4_tree_attention(cfg, cache, q.cuda(), i32(lens), masks(tree), 0.088, ws)
+        assert sk.last_launch_count() == (2 if wide else 1)
+        check_attention(out, lse, oracle_of(q, cache, lens, tree, 0.088, used))
+        x, w, tok = torch.randn(B, n_q, D, generator=gen(5)).bfloat16(), torch.randn(V, D, generator=gen(6)).bfloat16() / 8, \
+            torch.randint(0, V, (B, n_q), generator=gen(7 + step))
+        r = sk.states_logprobs(x.cuda(), w.cuda(), tok.cuda(), states_ws)
+        check_states(r, x.view(B * n_q, D), w, tok)
+        kept = branches[step]
+        most = max(len(b) for b in kept)
+        want = cache.pages.cpu().numpy().copy()
+        for b in range(B):
+            for c in range(hkv):
+                kv4.keep(want, cache.page_table.cpu().numpy(), b, c, lens[b], kept[b])
+        sk.kv4_keep(cfg, cache, i32(lens), i32([b + [0] * (most - len(b)) for b in kept]), i32([len(b) for b in kept]), ws)
+        assert np.array_equal(cache.pages.cpu().numpy(), want)
+        lens = [n + len(b) for n, b in zip(lens, kept)]
+    assert ws.status() == (0, 0) and states_ws.status() == (0, 0)

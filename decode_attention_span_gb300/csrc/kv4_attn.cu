@@ -336,15 +336,15 @@ __device__ __forceinline__ void split_units(WarpState& S, const Query& Q, const 
   S.split = true;
 }
 
+template <bool TREE>
+__device__ __forceinline__ bool sees(int seen, int i) {
+  return TREE ? uint32_t(seen) >> i & 1u : i < seen;
+}
 // EDGE: some token of the chunk is not seen by some column (seen: per column of the
 // lane, the first tokens of the chunk, of a TREE a bit for each; held: tokens of the chunk that the
 // sequence has).  PACK: only four columns are in
 // use; columns 4-7 hold the same queries again, and their lanes put the weights' lower
 // parts in, so that one product does for both.
-template <bool TREE>
-__device__ __forceinline__ bool sees(int seen, int i) {
-  return TREE ? uint32_t(seen) >> i & 1u : i < seen;
-}
 template <bool EDGE, bool PACK, bool TREE>
 __device__ __forceinline__ void chunk_step(WarpState& S, const Query& Q, const uint8_t* chunk,
                                            float4 (&par)[2][kChunkTokens], float4* kept,

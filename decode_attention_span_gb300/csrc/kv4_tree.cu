@@ -18,12 +18,13 @@
 // serves four weights.
 //
 // What bounds it is taken to be the softmax warps' chains of dependent instructions, two such warps to an SM
-// quarter (issue 47% of active cycles, tensor pipe 23%, DRAM 11%: 65536 tokens, 32 drafted, at the step of 326 us).
-// 131072 tokens, 32 and 8 heads, 64 drafted tokens (two blocks of columns): 315 us; 8 sequences of up to
-// 16384, 28 and 4 heads, 26 drafted: 150 us.  Leaving parts out of copies of it that gave wrong results (when the whole took
+// quarter (issue 49% of active cycles, tensor pipe 23%, DRAM 11%: 65536 tokens, 32 drafted).
+// 131072 tokens, 32 and 8 heads, 64 drafted tokens (two blocks of columns): 331 us; 8 sequences of up to
+// 16384, 28 and 4 heads, 26 drafted: 158 us.  Leaving parts out of copies of it that gave wrong results (when the whole took
 // 326 to 352 us): code expansion 315 us, expansion and scales 306, softmax 271, softmax and expansion 195; none hides the
 // others entirely.  Steps: logits kept in registers 715 us, in tensor memory 426; half pages in turn and
-// products issued by whole warps 352; scales folded into the operands 339; a warp for the scales 326.
+// products issued by whole warps 352; scales folded into the operands 339; a warp for the scales 326.  The
+// flushes cost 308 -> 331.
 #include <math.h>
 
 #include <algorithm>
@@ -665,8 +666,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) kv4_tree_kernel(const __grid_
       const int col0 = blk * kTreeRows, cols = min(kTreeRows, P.n_q * P.hpg - col0);
       const int n = I.page1 - I.page0;
       const int prefix = min(max(P.first[I.b], 0), cap);
-      // the queries, a row at a time
-      // two rows at a time: a lane has dimensions 8 (lane % 16) .. + 7 of one, a piece of its operand
+      // the queries, two rows at a time: a lane has dimensions 8 (lane % 16) .. + 7 of one, a piece of its operand
       constexpr int kEach = kTreeRows / kSoftWarps;
 #pragma unroll 1
       for (int i0 = 0; i0 < kEach; i0 += 8) {

@@ -18,10 +18,10 @@
 // operand byte is read from L2 for 256 products, not 128), one CTA 128 x 256 where there are up to 128 rows.
 // What bounds it: with many rows the tensor cores, or the power that they draw (4096 x 128000 x 4096: loss 2.1 ms,
 // 2.0 PFLOP/s, beside 2.05 ms of a library product of the same sizes that only makes the logits;
-// gradient 7.05 ms, 1.83 PFLOP/s; 1024 x 32000 x 4096, each product 148 us, tensor pipe 78 to 84% busy); with few
-// the weight's bytes (128 x 128000 x 4096: 166 us, 6.3 TB/s; 1 x 32000 x 4096: 47 us, 5.6 TB/s, 8 us above the
-// bytes' time).  Rows whose length is no multiple of 128 bytes cross a line of L2
-// more (1003 x 50021 x 1000 in f16: 87 us, 1.15 PFLOP/s).
+// gradient 7.3 ms, 1.77 PFLOP/s; 1024 x 32000 x 4096, each product 146 to 166 us, tensor pipe 69 to 83% busy); with few
+// the weight's bytes (128 x 128000 x 4096: 170 us, 6.2 TB/s; 1 x 32000 x 4096: 48 us, 5.5 TB/s, 9 us above the
+// bytes' time).  Rows whose length is no multiple of 128 bytes may cost as much again (1003 x 50021 x 1000 in f16: 97 us,
+// with rows 1024 elements apart 69), or nothing (1021 x 50021 x 2000: 131 and 136 us).
 #include <cuda_fp16.h>
 #include <float.h>
 #include <math.h>
@@ -425,7 +425,7 @@ struct Place {
 };
 
 // A persistent kernel: one CTA an SM, or a pair of CTAs on two (CG 2), takes tiles of 128 CG rows and
-// `width` columns in turn.  One warp copies operands, one issues the products, four turn the finished
+// `width` columns in turn.  One warp copies operands, one issues the products, eight turn the finished
 // accumulator into results while the next one fills.
 // SEG: sums over K in segments of kSegmentLogits or kSegmentProduct blocks.
 template <typename T, int CG, Mode MODE, bool SEG, bool AX, bool BX>
@@ -981,7 +981,7 @@ TileParams tile_params(const Call& c) {
 // The product of a gradient, rounded to `out` (or left in acc, where `last` is false: more pieces follow).  The
 // tiles that do not fill a wave have their sums over K cut into shares: of 4096 x 4096 over 32768, 76 pairs of CTAs
 // have 256 tiles, three waves and 28 more, which take a wave or, in five shares each, two fifths of one (the gradient of 4096 x
-// 128000 x 4096 7.05 ms for 7.3; 96 x 32000 x 1024, with four tiles in all, 66 us for 250).
+// 128000 x 4096 7.05 ms for 7.3 when it was made; 96 x 32000 x 1024, with four tiles in all, 66 us for 250).
 template <typename T, bool AX, bool BX>
 sekv_status product(TileParams& P, const Call& c, int sms, bool last, void* out) {
   const int cg = ctas_of(P.m), units = sms / cg, blocks = (P.k + kBlockK - 1) / kBlockK;

@@ -237,3 +237,21 @@ def test_two_steps_with_drafted_tokens_against_the_oracles(sk, wide):
         assert np.array_equal(cache.pages.cpu().numpy(), want)
         lens = [n + len(b) for n, b in zip(lens, kept)]
     assert ws.status() == (0, 0) and states_ws.status() == (0, 0)
+
+
+def test_long_items_that_give_up_end_at_once(sk):
+    """The same with items of 94 pages, whose values would be flushed."""
+    B, hkv, T = 20, 8, 6000
+    k, v = kv_rows("bf16", 1, T, hkv, 9)
+    cfg, cache, ws, _ = shared_cache(sk, B, hkv, 64, 16, k.cuda(), v.cuda())
+    q, t, first = torch.randn(B, 64, 16, 128, generator=gen(1)).bfloat16().cuda(), masks(trees(B, 64, 2)), i32([T - 64] * B)
+    want = sk.kv4_tree_attention(cfg, cache, q, first, t, 0.1, ws)
+    short = sk.Config(B, 16, hkv, 0, 0, 64, flags=2)
+    assert ws.status() == (0, 0)
+    t0 = time.monotonic()
+    for _ in range(5):
+        sk.kv4_tree_attention(short, cache, q, first, t, 0.1, ws)
+    assert ws.status()[0] == 2
+    assert time.monotonic() - t0 < 1.0
+    got = sk.kv4_tree_attention(cfg, cache, q, first, t, 0.1, ws)
+    assert ws.status() == (0, 0) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -5,7 +5,7 @@ import time
 import pytest
 import torch
 
-from test_gpu_states import inputs
+from test_gpu_states import check_states, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +167,15 @@ def test_gradient_of_pieces_whose_last_tiles_are_cut(sk, dtype):
     # one without the other
     only, _ = sk.states_logprobs_backward(x, w, tok, lse, g, ws, grad_lse=e, want_weight=False)
     assert torch.equal(only, dx)
+
+
+@pytest.mark.parametrize("T", [8192, 8193, 8200, 8320, 16390])
+def test_rows_behind_the_last_whole_part(sk, T):
+    """Rows are taken 8192 at a time; a few that are left go through the kernel of one CTA, with tiles of its own width."""
+    V, D = 1100, 72
+    x, w, tok = inputs("bf16", T, V, D, 4)
+    ws = sk.StatesWorkspace(T, V, D)
+    r = sk.states_logprobs(x.cuda(), w.cuda(), tok.cuda(), ws)
+    at = [0, 1, 4096, 8190, 8191] + list(range(8192, T, 97)) + [T - 1]
+    check_states(sk.StatesLogprobs(r.logprob[at], r.lse[at]), x[at], w, tok[at])
+    assert ws.status() == (0, 0)

@@ -851,10 +851,10 @@ sekv_status sekv_states_surprisal(const void* states, int32_t dtype, int64_t bat
  *   d_states = G weight,  d_weight = G^T states
  * The logits are made again, for one piece of the vocabulary at a time; G is held for that piece
  * as numbers of dtype, times a number that brings the largest |grad_logprob_r| (of rows with a
- * token) or |grad_lse_r - grad_logprob_r| to 2^13; the sums are fp32 (off by 2^-14 of their terms' sizes
+ * token) or |grad_lse_r - grad_logprob_r| to 2^13; the sums are fp32 (off by some 2^-14 of their terms' sizes
  * at most, however long) and rounded once.  In f16 an element
  * below 2^-27 of that largest factor loses bits, and one below 2^-38 counts as 0, so that a row whose
- * factors are far below another row's is less exact; in bf16 no element loses bits by its size.
+ * factors are far below another row's is less exact; in bf16 no element within 2^-130 of it loses bits.
  *   grad_logprob, grad_lse   f32 [n_rows], either may be NULL (0)
  *   d_states [n_rows][dim], d_weight [vocab][dim], dtype, dense, 16-byte aligned; either may be
  *            NULL.  They must not overlap the inputs
@@ -862,7 +862,8 @@ sekv_status sekv_states_surprisal(const void* states, int32_t dtype, int64_t bat
  * times what rounding the results alone gives, rows with any factors by up to 1.42 times (in the mean square).
  * A row whose lse is not finite has gradient NaN (and so all of d_weight) unless its factors are 0.
  * A row of token -1 has no logprob; a row whose two factors are 0 adds nothing to d_weight and has
- * gradient 0, provided that its state is finite.  A token outside [0, vocab) makes its row's
+ * gradient 0, provided that its state is finite.  An element of weight that is not finite makes its
+ * dimension of d_states NaN.  A token outside [0, vocab) makes its row's
  * gradient, and what it adds to d_weight, NaN.  n_rows 0 sets d_weight to 0.  Deterministic.
  */
 sekv_status sekv_states_logprobs_backward(const void* states, int32_t dtype, int64_t n_rows,
